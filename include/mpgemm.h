@@ -401,6 +401,69 @@ mpg_status mpg_attention(int64_t lq, int64_t lk, int64_t d, const float* Q, int6
                          const void* V, int64_t ldv, float* O, int64_t ldo, float scale, mpg_attn_mode mode,
                          int32_t key_splits, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- 8-bit operands with a scale for each block of 128 --------------------
+ * Storage of 8-bit matrices: one byte per element, e4m3 (largest value 448,
+ * 3 fraction bits, no infinity) or e5m2 (57344, 2 fraction bits). */
+typedef enum { MPG_E4M3 = 0, MPG_E5M2 = 1 } mpg_fp8_format;
+
+/* A rows x k matrix of 8-bit values, k contiguous (row-major), and its fp32
+ * scales: element (r, j) stands for
+ *     value(data[r*ld + j]) * scale[(r / scale_rows) * scale_row_stride + (j / 128) * scale_k_stride].
+ *   scale_rows  1: a scale for each 1 x 128 block (activations, gradients);
+ *               128: for each 128 x 128 block (weights).  Other values:
+ *               MPG_ERR_UNSUPPORTED.
+ *   Scales are any fp32 values (powers of two are what mpg_fp8_quantize makes).
+ *   Per-row scales are read fastest with scale_row_stride 1. */
+typedef struct {
+  const void* data;
+  int64_t ld;
+  mpg_fp8_format format;
+  int32_t scale_rows;
+  const float* scale;
+  int64_t scale_row_stride;
+  int64_t scale_k_stride;
+} mpg_fp8_operand;
+
+/* Quantise X (rows x cols, row-major, fp32 / fp16 / bf16) to 8 bits with a
+ * power-of-two scale for each block, in one pass over X:
+ *   Q, S    the matrix itself: Q rows x cols (ldq >= cols), S as in
+ *           mpg_fp8_operand with k = cols (s_row_stride, s_k_stride in floats);
+ *   QT, ST  its transpose: QT cols x rows (ldqt >= rows), blocks along the rows
+ *           of X (k = rows).  Either pair may be NULL.
+ * For a block whose largest finite magnitude is a, the scale is the smallest
+ * 2^t >= a / 448 (e5m2: a / 57344), t >= -126, and 1 when a = 0; each element
+ * is x / scale rounded once, to nearest even (the division is exact).
+ * Infinities and NaN do not set the scale and become NaN.  Blocks cut by the
+ * matrix's edge hold what is inside.  scale_rows 128 gives Q and QT the same
+ * scales (transposed). */
+mpg_status mpg_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, mpg_dtype x_dtype,
+                            mpg_fp8_format format, int32_t scale_rows, void* Q, int64_t ldq, float* S,
+                            int64_t s_row_stride, int64_t s_k_stride, void* QT, int64_t ldqt, float* ST,
+                            int64_t st_row_stride, int64_t st_k_stride, void* stream);
+
+/* C = alpha * A * B^T + beta * C for 8-bit A (m x k) and B (n x k):
+ *     C[i, j] = alpha * sum_kb sA[i, kb] sB[j, kb] sum_{l in block kb} A[i, l] B[j, l] + beta * C[i, j].
+ * The tensor cores sum each block of 128 k in fp32; the blocks' sums are
+ * scaled and added in fp32 with round-to-nearest fused multiply-adds, in the
+ * order of k (per range, where k is divided).  A and B may differ in format
+ * and in scale_rows.  C is row-major, ldc >= n, of type opt->c_dtype (fp32 by
+ * default), rounded once when stored; beta == 0: C is not read; k == 0 or
+ * alpha == 0: C = beta*C and the operands are not read.
+ *   opt   NULL = defaults.  Read are c_dtype, wait_timeout_ns, splitk (the
+ *         ranges that k is divided into, each on a CTA of one cluster: 0 =
+ *         the library's choice, else 1 .. 8) and tile_n (0 = the library's
+ *         choice; 128: tiles of 128 x 128; 16, 32, 64: tiles of that many rows
+ *         of A by 128 rows of B, for few rows of A).
+ * Data pointers that are not 16-byte aligned or whose ld is no multiple of 16
+ * are copied to aligned lines in the workspace first
+ * (mpg_gemm_fp8_workspace_size bytes, else 0; MPG_ERR_WORKSPACE without it).
+ * Results do not depend on timing. */
+size_t mpg_gemm_fp8_workspace_size(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* A,
+                                   const mpg_fp8_operand* B);
+mpg_status mpg_gemm_fp8(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* A, const mpg_fp8_operand* B, void* C,
+                        int64_t ldc, float alpha, float beta, void* workspace, size_t workspace_bytes, void* stream,
+                        const mpg_options* opt);
+
 /* Bytes of workspace for this exact call: mpg_gemm_workspace_size() plus
  * room for copies of the operands the TMA path cannot take as given:
  * 16-bit operands (FP16 / BF16 modes) and fp32 operands (TF32) whose base is

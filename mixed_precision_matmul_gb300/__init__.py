@@ -11,6 +11,8 @@ Entry points mirror ``include/mpgemm.h``:
   strides: a 2-D operand with unit column stride is row-major, with unit row
   stride column-major; a leading batch dimension gives the batch stride).
 * :func:`gemm_raw`   the plain-pointer form of ``mpg_gemm_ex``.
+* :func:`fp8_quantize`, :func:`gemm_fp8`   8-bit operands with a scale for
+  each block of 128: the quantiser and the product.
 * :func:`acc_coords`, :func:`acc_offset`, :func:`acc_matrix_offset`,
   :func:`acc_decode`, :func:`tmem_acc_coords`, :func:`tmem_acc_decode`   host decode of accumulator
   fragments.
@@ -70,6 +72,18 @@ class Options(ctypes.Structure):
     ]
 
 
+class Fp8Operand(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("format", ctypes.c_int32),
+        ("scale_rows", ctypes.c_int32),
+        ("scale", ctypes.c_void_p),
+        ("scale_row_stride", ctypes.c_int64),
+        ("scale_k_stride", ctypes.c_int64),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -120,6 +134,14 @@ def lib():
         L.mpg_gemm_host_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, i32, i32, i64, i64, i32, i32,
                                                    i64, i64, f32, f32, i32, ctypes.POINTER(Options)]
         L.mpg_gemm_host_workspace_size.restype = sz
+        pf8 = ctypes.POINTER(Fp8Operand)
+        L.mpg_fp8_quantize.argtypes = [i64, i64, vp, i64, i32, i32, i32, vp, i64, vp, i64, i64, vp, i64, vp, i64, i64,
+                                       vp]
+        L.mpg_fp8_quantize.restype = i32
+        L.mpg_gemm_fp8_workspace_size.argtypes = [i64, i64, i64, pf8, pf8]
+        L.mpg_gemm_fp8_workspace_size.restype = sz
+        L.mpg_gemm_fp8.argtypes = [i64, i64, i64, pf8, pf8, vp, i64, f32, f32, vp, sz, vp, ctypes.POINTER(Options)]
+        L.mpg_gemm_fp8.restype = i32
         L.mpg_options_init.argtypes = [ctypes.POINTER(Options)]
         L.mpg_options_init.restype = None
         L.mpg_device_status.argtypes = [vp]
@@ -594,3 +616,6 @@ def probe_epilogue_staging(blocks_in, scalar=False, stream=None):
 
 def selftest_wait_timeout(timeout_ns: int, stream=None) -> int:
     return lib().mpg_selftest_wait_timeout(timeout_ns, _stream_handle(stream))
+
+
+from .fp8 import E4M3, E5M2, fp8_quantize, fp8_quantize_raw, gemm_fp8, gemm_fp8_raw  # noqa: E402,F401

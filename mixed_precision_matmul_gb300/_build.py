@@ -37,8 +37,12 @@ SOURCES = [
     "tc_pair.cu",
     "attention.cu",
     "tmem_probe.cu",
+    "fp8_api.cu",
+    "fp8_quant.cu",
+    "fp8_gemm.cu",
 ]
-HEADERS = ["ptx.cuh", "internal.h", "tc_gemm.cuh", "outio.cuh", "host.h", "staging.cuh"]
+HEADERS = ["ptx.cuh", "cluster.cuh", "internal.h", "tc_gemm.cuh", "outio.cuh", "host.h", "staging.cuh",
+           "fp8.h", "fp8_tc.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

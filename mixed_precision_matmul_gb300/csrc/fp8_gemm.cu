@@ -1,0 +1,296 @@
+// The block-scaled 8-bit product on single CTAs (sm_103a, cta_group::1): one
+// 128 x BN tile of D per CTA, or per cluster of 2, 4 or 8 CTAs that divide the
+// tile's k-blocks among them.
+//
+// Roles:
+//   warp 0      TMA producer (one line of 128 k per row and stage)
+//   warp 1      TMEM allocation; lane 0 issues the MMAs, one accumulator
+//               buffer per k-block (four buffers in turn)
+//   warps 2..   epilogue: read each k-block's accumulator, add it to the
+//               running sums under its scales (fp8_tc.cuh), and at the end
+//               put the sums into shared memory, where the tile is read back
+//               in the order that C is stored in.  With a cluster, each CTA
+//               reads its share of the rows from all CTAs' shared memory and
+//               adds the partial sums in rank order, so the result does not
+//               depend on timing and needs no workspace.
+//
+// Few tokens (m <= 64): R, the 128-row operand, is the weights and the tokens
+// are the columns (BN = 16, 32 or 64), so that the tensor core's rows are full
+// and each weight byte is read once; the kernel is then bound by the weights'
+// bytes, and the k range is divided so that every SM has some in flight.
+#include "fp8_tc.cuh"
+
+namespace mpg {
+namespace {
+
+template <int BN_, bool kSwapped_, bool kColVec_>
+struct Fp8Traits {
+  static constexpr int BM = 128;
+  static constexpr int BN = BN_;
+  static constexpr bool kSwapped = kSwapped_;
+  static constexpr bool kColVec = kColVec_;
+  static constexpr int kStage = (BM + BN) * kFp8RowBytes;
+  static constexpr int kStages = BN >= 128 ? 6 : BN >= 64 ? 7 : 9;
+  static constexpr int kAccBufs = 4;
+  static constexpr int kAccStride = BN < 32 ? 32 : BN;
+  static constexpr int kTmemCols = kAccBufs * kAccStride;
+  static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
+  static constexpr int kCols = BN / (kEpiWarps / 4);      // columns of one epilogue warp
+  static constexpr int kThreads = (2 + kEpiWarps) * 32;
+  using Ring = ScaleRing<kCols, kColVec>;
+  static constexpr int kPitch = BN + 1;                   // floats per row of the staged tile
+  static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiWarps * Ring::kBytes + kNumBars * 8 + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(BM * kPitch * 4 <= kStages * kStage, "the staged tile reuses the operand stages");
+  static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
+};
+
+// One 32-bit word of the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // the same offset in every CTA of a cluster (the partial sums are read by address)
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring_base = smem + T::kStages * T::kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_base + T::kEpiWarps * T::Ring::kBytes);
+  uint64_t* op_full = bars;
+  uint64_t* op_empty = bars + T::kStages;
+  uint64_t* acc_full = bars + 2 * T::kStages;
+  uint64_t* acc_empty = acc_full + T::kAccBufs;
+  uint64_t* done_bar = acc_empty + T::kAccBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();          // this CTA's share of the k range
+  const int tile = (int)(blockIdx.x / (uint32_t)p.splits);
+  const int cblk = tile / p.num_r_blk, rblk = tile - cblk * p.num_r_blk;
+  const int row0 = rblk * T::BM, col0 = cblk * T::BN;
+  const int kb0 = (int)rank * p.kb_per_split;
+  const int nkb = max(0, min(p.num_k_blk, kb0 + p.kb_per_split) - kb0);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::kStages; ++i) {
+      mbar_init(&op_full[i], 1);
+      mbar_init(&op_empty[i], 1);
+    }
+    for (int i = 0; i < T::kAccBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], T::kEpiWarps);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&p.map_r);
+    tma_prefetch_map(&p.map_c);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, T::kTmemCols);
+    tmem_relinquish();
+    tc_fence_before_sync();
+  }
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  WaitCtl ctl;
+  ctl.abort = abort_flag;
+  ctl.status = p.status;
+  ctl.limit_ns = p.wait_limit_ns;
+  const uint32_t op_smem = smem_addr(smem);
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int i = 0;
+      for (; i < nkb; ++i) {
+        const int st = i % T::kStages;
+        if (!mbar_wait(&op_empty[st], ((i / T::kStages) & 1u) ^ 1u, ctl)) break;
+        mbar_arrive_expect_tx(&op_full[st], T::kStage);
+        uint8_t* dst = smem + st * T::kStage;
+        const int k0 = (kb0 + i) * kFp8Block;
+        tma_load_3d(dst, &p.map_r, &op_full[st], k0, row0, 0);
+        tma_load_3d(dst + T::BM * kFp8RowBytes, &p.map_c, &op_full[st], k0, col0, 0);
+      }
+      // the stages' last releases cover the copies still in flight
+      for (int j = max(0, i - T::kStages); j < i; ++j)
+        drain_wait(&op_empty[j % T::kStages], (j / T::kStages) & 1u, p.wait_limit_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc(0u, false, false, T::BM, T::BN) | p.fmt_bits;
+      for (int i = 0; i < nkb; ++i) {
+        const int st = i % T::kStages, ab = i % T::kAccBufs;
+        if (!mbar_wait(&acc_empty[ab], ((i / T::kAccBufs) & 1u) ^ 1u, ctl)) break;
+        if (!mbar_wait(&op_full[st], (i / T::kStages) & 1u, ctl)) break;
+        tc_fence_after_sync();
+        const uint32_t r_tile = op_smem + st * T::kStage;
+        const uint32_t c_tile = r_tile + T::BM * kFp8RowBytes;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_f8(tmem_base + ab * T::kAccStride, fp8_desc(r_tile, ks), fp8_desc(c_tile, ks), idesc, ks > 0 ? 1u : 0u);
+        mma_commit(&op_empty[st]);
+        mma_commit(&acc_full[ab]);
+      }
+      mma_commit(done_bar);
+      drain_wait(done_bar, 0, p.wait_limit_ns);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ running sums
+    const int q = warp & 3;
+    const int ew = warp - 2;
+    const int wc0 = (ew / 4) * T::kCols;                  // this warp's first column in the tile
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + wc0;
+    typename T::Ring ring;
+    ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row0 + 32 * q, col0 + wc0, kb0);
+#pragma unroll
+    for (int i = 0; i < T::Ring::kDepth - 1; ++i) ring.fetch(i, nkb);
+    float acc[T::kCols];
+#pragma unroll
+    for (int j = 0; j < T::kCols; ++j) acc[j] = 0.0f;
+    constexpr int kChunk = T::kCols >= 32 ? 32 : 16;
+#pragma unroll 1
+    for (int i = 0; i < nkb; ++i) {
+      const int ab = i % T::kAccBufs;
+      if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
+      tc_fence_after_sync();
+      // (the warp has converged here: block i - 1's slot may be refilled)
+      ring.fetch(i + T::Ring::kDepth - 1, nkb);
+      cp_async_wait<T::Ring::kDepth - 1>();
+      __syncwarp();
+      const uint32_t slot = ring.slot(i);
+      const float rs = ld_shared_f32(slot + lane * 4);
+      const float rcs = T::kColVec ? 0.0f : rs * ld_shared_f32(slot + 128 + lane * 4);
+#pragma unroll
+      for (int c = 0; c < T::kCols; c += kChunk) {
+        float v[kChunk];
+        if constexpr (kChunk == 32) tmem_ld_32cols(tacc + ab * T::kAccStride + c, v);
+        else tmem_ld_16cols(tacc + ab * T::kAccStride + c, v);
+        tmem_ld_wait();
+        if (c + kChunk == T::kCols) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[ab]);
+        }
+        scale_add<kChunk, T::kColVec>(acc + c, v, slot, c, rs, rcs);
+      }
+    }
+    cp_async_wait<0>();
+    if (ok) {
+      // every MMA of this CTA is complete: the operand stages are free
+      const uint32_t dst = op_smem + ((uint32_t)(32 * q + lane) * T::kPitch + wc0) * 4u;
+#pragma unroll
+      for (int j = 0; j < T::kCols; ++j) st_shared_f32(dst + j * 4, acc[j]);
+    }
+  }
+
+  // ---------------------------------------------------------------- C
+  tc_fence_before_sync();
+  if (p.splits > 1) cluster_sync_all();
+  else __syncthreads();
+  if (*abort_flag == 0) {
+    const int splits = p.splits;
+    const int rows_per = (T::BM + splits - 1) / splits;
+    const int ra = (int)rank * rows_per;
+    const int rows_here = min(min(T::BM, ra + rows_per), p.rows - row0) - ra;    // rows that this CTA stores
+    const int cols_here = min(T::BN, p.cols - col0);
+    const int warps = T::kThreads / 32;
+    uint32_t peer[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) peer[s] = s < splits ? cluster_smem_addr(op_smem, (uint32_t)s) : 0u;
+    auto sum_at = [&](int r, int c) {
+      const uint32_t off = ((uint32_t)(ra + r) * T::kPitch + c) * 4u;
+      if (splits == 1) return ld_shared_f32(op_smem + off);
+      float x = ld_cluster_f32(peer[0] + off);
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < splits) x += ld_cluster_f32(peer[s] + off);
+      return x;
+    };
+    if constexpr (T::kSwapped) {
+      // C[col, row]: lanes along the rows
+      const int groups = (rows_here + 31) / 32;
+      for (int u = warp; u < groups * cols_here; u += warps) {
+        const int c = u / groups, r = (u - c * groups) * 32 + lane;
+        if (r < rows_here) {
+          const float x = p.alpha * sum_at(r, c);
+          const int64_t idx = (int64_t)(col0 + c) * p.ld_out + row0 + ra + r;
+          out_store(p.out, idx, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx, p.out_dtype), x) : x, p.out_dtype);
+        }
+      }
+    } else {
+      for (int r = warp; r < rows_here; r += warps) {
+        const int64_t line = (int64_t)(row0 + ra + r) * p.ld_out + col0;
+        if (p.out_vec && cols_here == T::BN) {
+#pragma unroll
+          for (int c = lane * 4; c < T::BN; c += 128) {
+            float4 o = make_float4(p.alpha * sum_at(r, c), p.alpha * sum_at(r, c + 1), p.alpha * sum_at(r, c + 2),
+                                   p.alpha * sum_at(r, c + 3));
+            if (p.beta != 0.0f) {
+              const float4 z = out_load4(p.out, line + c, p.out_dtype);
+              o.x = fmaf(p.beta, z.x, o.x);
+              o.y = fmaf(p.beta, z.y, o.y);
+              o.z = fmaf(p.beta, z.z, o.z);
+              o.w = fmaf(p.beta, z.w, o.w);
+            }
+            out_store4(p.out, line + c, o, p.out_dtype);
+          }
+        } else {
+          for (int c = lane; c < cols_here; c += 32) {
+            const float x = p.alpha * sum_at(r, c);
+            out_store(p.out, line + c, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, line + c, p.out_dtype), x) : x,
+                      p.out_dtype);
+          }
+        }
+      }
+    }
+  }
+  // no CTA exits while another may still read its shared memory
+  __syncwarp();
+  if (p.splits > 1) cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, T::kTmemCols);
+  }
+}
+
+template <class T>
+bool fill(Fp8Kernel* out) {
+  out->fn = reinterpret_cast<const void*>(&fp8_gemm_kernel<T>);
+  out->block = T::kThreads;
+  out->smem_bytes = T::kSmemBytes;
+  out->tile_rows = T::BM;
+  out->tile_cols = T::BN;
+  return true;
+}
+
+}  // namespace
+
+bool fp8_lookup(int bn, bool swapped, bool col_vec, Fp8Kernel* out) {
+  if (swapped) {
+    switch (bn) {
+      case 16: return fill<Fp8Traits<16, true, true>>(out);
+      case 32: return fill<Fp8Traits<32, true, true>>(out);
+      case 64: return fill<Fp8Traits<64, true, true>>(out);
+      default: return false;
+    }
+  }
+  if (bn != 128) return false;
+  return col_vec ? fill<Fp8Traits<128, false, true>>(out) : fill<Fp8Traits<128, false, false>>(out);
+}
+
+}  // namespace mpg

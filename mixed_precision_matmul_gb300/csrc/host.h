@@ -79,6 +79,18 @@ void resolve_options(const mpg_options* opt, mpg_options* o);
 mpg_status encode_map(CUtensorMap* map, const Operand& x, int64_t inner, int64_t outer, int64_t batch,
                       int box_inner, int box_outer);
 
+// The same for lines of bytes (8-bit operands): map {inner, outer, 1}, ld in bytes.
+mpg_status encode_map_bytes(CUtensorMap* map, const void* ptr, int64_t ld, int64_t inner, int64_t outer,
+                            int box_inner, int box_outer);
+// Raises the kernel's dynamic shared-memory limit, once per kernel and device.
+mpg_status allow_smem(DeviceInfo* dev, const void* fn, int bytes);
+// Clusters of `size` CTAs of the kernel that can be resident at once (kept per
+// kernel, size and device).
+mpg_status resident_clusters(DeviceInfo* dev, const void* fn, int block, int smem_bytes, int size, int* out);
+// Launch attributes of a kernel on clusters of `cluster` CTAs (1: none) that
+// starts as a programmatic dependent of the kernel before it on the stream.
+int launch_attributes(cudaLaunchAttribute* attr, int cluster);
+
 int choose_splits(int64_t m, int64_t n, int64_t k, int64_t batch, int sm_count, const mpg_options& o);
 size_t splitk_bytes(int splits, int64_t m, int64_t n, int64_t batch);
 // Workspace of the CTA-pair kernel's split tail for `tiles` tiles: two

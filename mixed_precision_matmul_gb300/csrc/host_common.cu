@@ -105,4 +105,98 @@ mpg_status encode_map(CUtensorMap* map, const Operand& x, int64_t inner, int64_t
   return MPG_OK;
 }
 
+mpg_status encode_map_bytes(CUtensorMap* map, const void* ptr, int64_t ld, int64_t inner, int64_t outer,
+                            int box_inner, int box_outer) {
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)(ld * std::max<int64_t>(outer, 1))};
+  cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MPG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return MPG_OK;
+}
+
+namespace {
+struct KernelNote {
+  const void* fn;
+  int size;       // 0: the shared-memory limit was raised; else resident clusters of this size
+  int clusters;
+};
+constexpr int kMaxNotes = 128;
+std::mutex g_note_mu;
+KernelNote g_notes[kMaxDevices][kMaxNotes];
+int g_num_notes[kMaxDevices];
+
+KernelNote* find_note(int devid, const void* fn, int size) {
+  for (int i = 0; i < g_num_notes[devid]; ++i)
+    if (g_notes[devid][i].fn == fn && g_notes[devid][i].size == size) return &g_notes[devid][i];
+  return nullptr;
+}
+void add_note(int devid, const KernelNote& n) {
+  if (g_num_notes[devid] < kMaxNotes) g_notes[devid][g_num_notes[devid]++] = n;
+}
+}  // namespace
+
+mpg_status allow_smem(DeviceInfo* dev, const void* fn, int bytes) {
+  if (bytes > dev->max_smem_optin)
+    return fail(MPG_ERR_UNSUPPORTED, "kernel needs %d bytes of shared memory, device offers %d", bytes,
+                dev->max_smem_optin);
+  const int devid = (int)(dev - g_devices);
+  std::lock_guard<std::mutex> lock(g_note_mu);
+  if (find_note(devid, fn, 0)) return MPG_OK;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  add_note(devid, KernelNote{fn, 0, 0});
+  return MPG_OK;
+}
+
+mpg_status resident_clusters(DeviceInfo* dev, const void* fn, int block, int smem_bytes, int size, int* out) {
+  mpg_status s = allow_smem(dev, fn, smem_bytes);
+  if (s != MPG_OK) return s;
+  const int devid = (int)(dev - g_devices);
+  std::lock_guard<std::mutex> lock(g_note_mu);
+  if (KernelNote* k = find_note(devid, fn, size)) {
+    *out = k->clusters;
+    return MPG_OK;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = (size_t)smem_bytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  cudaError_t e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+  if (e != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return fail(MPG_ERR_UNSUPPORTED, "no resident cluster of %d CTAs: %s", size,
+                e != cudaSuccess ? cudaGetErrorString(e) : "occupancy 0");
+  }
+  add_note(devid, KernelNote{fn, size, n});
+  *out = n;
+  return MPG_OK;
+}
+
+int launch_attributes(cudaLaunchAttribute* attr, int cluster) {
+  int n = 0;
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  return n;
+}
+
 }  // namespace mpg
