@@ -464,6 +464,32 @@ mpg_status mpg_gemm_fp8(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* 
                         int64_t ldc, float alpha, float beta, void* workspace, size_t workspace_bytes, void* stream,
                         const mpg_options* opt);
 
+/* ---- orthogonalised update -------------------------------------------------
+ * O_b = alpha * NS(G_b) + beta * O_b for a batch of m x n matrices, where NS
+ * starts from X = G / (|G|_F + eps) and takes `steps` steps of
+ *     X <- a X + (b S + c S S) X,  S = X X^T   (S on the shorter side),
+ * the Newton-Schulz iteration towards the nearest matrix with orthonormal rows
+ * or columns; coeffs = {a, b, c}, e.g. {3.4445, -4.7750, 2.0315} with 5 steps,
+ * which carry every singular value above about 0.01 of the norm to 0.7 .. 1.2
+ * (the update of the Muon optimiser).  alpha and beta fold the step into a
+ * weight: O = W, alpha = -learning rate, beta = 1 - learning rate * decay.
+ *   G        fp32, fp16 or bf16, row-major, ldg >= n; strideG 0 = m*ldg.
+ *   O        fp32, fp16 or bf16, ldo >= n; strideO 0 = m*ldo; the matrices of O
+ *            must not overlap; beta == 0: O is not read.  O may be G.
+ *   steps    1 .. 100.  eps >= 0.  batch <= 65535.
+ *   workspace  mpg_orthogonalize_workspace_size() bytes, 16-byte aligned.
+ * Products run in fp16 with fp32 accumulation, X scaled by a power of two; the
+ * norm is summed in 64 bits.  Against 64 bits the result is off by about 1e-3
+ * of its norm (before its rounding to O's type); directions whose singular
+ * value is below about 2^-12 of the largest come out as noise of that size
+ * times a^steps.  A NaN or infinity in a matrix makes the whole of its result
+ * NaN; other matrices of the batch are not touched by it. */
+size_t mpg_orthogonalize_workspace_size(int64_t m, int64_t n, int64_t batch);
+mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G, int64_t ldg, int64_t strideG,
+                             mpg_dtype g_dtype, void* O, int64_t ldo, int64_t strideO, mpg_dtype o_dtype,
+                             int32_t steps, const float* coeffs, float eps, float alpha, float beta, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Bytes of workspace for this exact call: mpg_gemm_workspace_size() plus
  * room for copies of the operands the TMA path cannot take as given:
  * 16-bit operands (FP16 / BF16 modes) and fp32 operands (TF32) whose base is

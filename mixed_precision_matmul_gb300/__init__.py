@@ -13,6 +13,7 @@ Entry points mirror ``include/mpgemm.h``:
 * :func:`gemm_raw`   the plain-pointer form of ``mpg_gemm_ex``.
 * :func:`fp8_quantize`, :func:`gemm_fp8`   8-bit operands with a scale for
   each block of 128: the quantiser and the product.
+* :func:`orthogonalize`   Newton-Schulz orthogonalisation of an update.
 * :func:`acc_coords`, :func:`acc_offset`, :func:`acc_matrix_offset`,
   :func:`acc_decode`, :func:`tmem_acc_coords`, :func:`tmem_acc_decode`   host decode of accumulator
   fragments.
@@ -142,6 +143,11 @@ def lib():
         L.mpg_gemm_fp8_workspace_size.restype = sz
         L.mpg_gemm_fp8.argtypes = [i64, i64, i64, pf8, pf8, vp, i64, f32, f32, vp, sz, vp, ctypes.POINTER(Options)]
         L.mpg_gemm_fp8.restype = i32
+        L.mpg_orthogonalize_workspace_size.argtypes = [i64, i64, i64]
+        L.mpg_orthogonalize_workspace_size.restype = sz
+        L.mpg_orthogonalize.argtypes = [i64, i64, i64, vp, i64, i64, i32, vp, i64, i64, i32, i32,
+                                        ctypes.POINTER(ctypes.c_float), f32, f32, f32, vp, sz, vp]
+        L.mpg_orthogonalize.restype = i32
         L.mpg_options_init.argtypes = [ctypes.POINTER(Options)]
         L.mpg_options_init.restype = None
         L.mpg_device_status.argtypes = [vp]
@@ -619,3 +625,4 @@ def selftest_wait_timeout(timeout_ns: int, stream=None) -> int:
 
 
 from .fp8 import E4M3, E5M2, fp8_quantize, fp8_quantize_raw, gemm_fp8, gemm_fp8_raw  # noqa: E402,F401
+from .ortho import NS_COEFFS, orthogonalize, orthogonalize_raw, orthogonalize_workspace_size  # noqa: E402,F401

@@ -40,9 +40,11 @@ SOURCES = [
     "fp8_api.cu",
     "fp8_quant.cu",
     "fp8_gemm.cu",
+    "ortho_api.cu",
+    "ortho.cu",
 ]
 HEADERS = ["ptx.cuh", "cluster.cuh", "internal.h", "tc_gemm.cuh", "outio.cuh", "host.h", "staging.cuh",
-           "fp8.h", "fp8_tc.cuh"]
+           "fp8.h", "fp8_tc.cuh", "ortho.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

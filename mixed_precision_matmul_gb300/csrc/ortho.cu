@@ -1,0 +1,519 @@
+// Kernels of the orthogonalised update (sm_103a): X <- a X + (b S + c S S) X
+// with S = X X^T, from X = G / (|G| + eps).
+//
+// Numbers.  The products run on the tensor cores in fp16 with fp32
+// accumulation.  Every matrix of the iteration has singular values up to
+// about 1.2, so fp16's 11 bits can be used without fear of its range: X is
+// stored times a power of two near the root of its longer side (its entries
+// then have a root mean square near 1 when X is orthogonal), S and b S + c S S
+// as they are.  bf16 storage would lose three bits at every rounding; rounding
+// errors of X grow by up to a = 3.4 a step in the directions of small singular
+// values.  With five steps on a matrix of noise and a few strong directions
+// the result is off by 1.3e-3 of its norm with fp16 storage and by 1.1e-2 with
+// bf16 (the rounding to a bf16 result alone is 1.7e-3).  G itself enters
+// scaled by a power of two, so that 16-bit gradients are stored exactly; the
+// rest of 1 / (|G| + eps) is a factor of the first step's epilogues.
+//
+// Work.  S and b S + c S S are symmetric: only tiles on and above the diagonal
+// are computed, and stored twice.  A step costs m^2 n + m^3 + 2 m^2 n flops
+// (m the shorter side) instead of 2 m^2 n + 2 m^3 + 2 m^2 n.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "cluster.cuh"
+#include "internal.h"
+#include "ortho.h"
+#include "outio.cuh"
+#include "staging.cuh"
+#include "tc_gemm.cuh"
+
+namespace mpg {
+namespace {
+
+// ---------------------------------------------------------------------------
+// norm and scaling
+// ---------------------------------------------------------------------------
+template <class XT>
+__device__ __forceinline__ float as_f32(XT v);
+template <>
+__device__ __forceinline__ float as_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float as_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float as_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Elements 8c .. 8c+7 of a line (zeros beyond its end).
+template <class XT>
+__device__ __forceinline__ void read8(const XT* line, int c, int cols, bool vec, float (&v)[8]) {
+  if (vec && c + 8 <= cols) {
+    if constexpr (sizeof(XT) == 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(line + c));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(line + c) + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(line + c));
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t l = (uint16_t)(w[i] & 0xFFFFu), h = (uint16_t)(w[i] >> 16);
+        XT lo, hi;
+        memcpy(&lo, &l, 2);
+        memcpy(&hi, &h, 2);
+        v[2 * i] = as_f32<XT>(lo);
+        v[2 * i + 1] = as_f32<XT>(hi);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? as_f32<XT>(line[c + j]) : 0.0f;
+  }
+}
+
+constexpr int kScaleThreads = 256;
+
+// partial[b][block] = sum of squares over the block's share of matrix b.  The
+// squares of 8 elements are added in fp32 where that is safe (the sum neither
+// near overflow nor near underflow) and in 64 bits elsewhere; a thread's sum
+// of such groups in fp32, the rest in 64 bits, always in the same order.
+template <class XT>
+__global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_constant__ OrthoScaleParams p) {
+  __shared__ double red[kScaleThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.y;
+  const XT* g = reinterpret_cast<const XT*>(p.g) + (int64_t)b * p.stride_g;
+  const int per = (p.cols + 7) / 8;
+  const int64_t total = (int64_t)p.rows * per;
+  float sum = 0.0f;
+  double wide = 0.0;
+  for (int64_t i = blockIdx.x * (int64_t)kScaleThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kScaleThreads) {
+    const int64_t r = i / per;
+    float v[8];
+    read8<XT>(g + r * p.ldg, (int)(i - r * per) * 8, p.cols, p.g_vec != 0, v);
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+    if (s >= 1e-30f && s <= 1e30f) {
+      sum += s;
+      if (sum > 1e30f) { wide += (double)sum; sum = 0.0f; }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wide += (double)v[j] * (double)v[j];
+    }
+  }
+  wide += (double)sum;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = wide;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kScaleThreads / 32; ++w) s += red[w];
+    p.partial[(int64_t)b * kOrthoNormBlocks + blockIdx.x] = s;
+  }
+}
+
+// x = fp16(g * 2^e) with the power of two that brings the norm to [target,
+// 2 target), and factor = 2^-e / (norm + eps).
+template <class XT>
+__global__ void __launch_bounds__(kScaleThreads) ortho_scale_kernel(const __grid_constant__ OrthoScaleParams p) {
+  __shared__ double red[kScaleThreads / 32];
+  __shared__ float scale_sh;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.y;
+  double s = (int)threadIdx.x < p.blocks ? p.partial[(int64_t)b * kOrthoNormBlocks + threadIdx.x] : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kScaleThreads / 32; ++w) s += red[w];
+    const double norm = sqrt(s);
+    int e = 0;
+    if (norm > 0.0 && norm < 1e300) {
+      e = ilogb((double)p.target) - ilogb(norm);
+      if (scalbn(norm, e) < (double)p.target) ++e;
+    }
+    // fp32 inputs below 2^-126 in norm reach the target only as far as a
+    // single factor of fp32 carries them
+    e = min(max(e, -126), 127);
+    scale_sh = scalbnf(1.0f, e);
+    if (blockIdx.x == 0) p.factor[b] = (float)(scalbn(1.0, -e) / (norm + (double)p.eps));
+  }
+  __syncthreads();
+  const float scale = scale_sh;
+  const XT* g = reinterpret_cast<const XT*>(p.g) + (int64_t)b * p.stride_g;
+  uint16_t* x = p.x + (int64_t)b * p.rows * p.ldx;
+  const int per = (int)(p.ldx / 8);
+  const int64_t total = (int64_t)p.rows * per;
+  for (int64_t i = blockIdx.x * (int64_t)kScaleThreads + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * kScaleThreads) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    float v[8];
+    read8<XT>(g + r * p.ldg, c, p.cols, p.g_vec != 0, v);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 h = __floats2half2_rn(v[2 * j] * scale, v[2 * j + 1] * scale);
+      memcpy(&w[j], &h, 4);
+    }
+    *reinterpret_cast<uint4*>(x + r * p.ldx + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the product
+// ---------------------------------------------------------------------------
+// kPair: tiles of 256 x 256 on a cluster of two CTAs (cta_group::2), each CTA
+// with 128 rows of A and 128 columns of B in shared memory and its 128 rows
+// of the accumulator in TMEM.  Else tiles of 128 x 128 on one CTA.  Roles and
+// hand-overs are the same: a TMA producer warp, an MMA warp (rank 0's issues
+// for the pair), eight epilogue warps; two accumulators, so that the epilogue
+// of a tile runs beside the products of the next.
+template <bool kPair_>
+struct OrthoTraits {
+  static constexpr bool kPair = kPair_;
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int BM = 128;                    // rows of A held by one CTA
+  static constexpr int kTile = kPair ? 256 : 128;
+  static constexpr int kBHeld = 128;                // columns of B held by one CTA
+  static constexpr int BK = 64;
+  static constexpr int kRowBytes = 128;
+  static constexpr uint32_t kSwizzle = kSwizzle128B;
+  static constexpr int kInstrK = 16;
+  static constexpr int kKSteps = BK / kInstrK;
+  static constexpr int kATile = BM * kRowBytes;
+  static constexpr int kStage = kATile + kBHeld * kRowBytes;
+  static constexpr int kStages = 6;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = (2 + kEpiWarps) * 32;
+  static constexpr int kAccBufs = 2;
+  static constexpr int kTmemCols = kAccBufs * kTile;
+  static constexpr int kEpiBytes = kEpiWarps * 32 * 32 * 4;
+  static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiBytes + kNumBars * 8 + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+struct OrthoTile {
+  int b, mb, nb;
+};
+__device__ __forceinline__ OrthoTile ortho_tile(const OrthoGemmParams& p, int t) {
+  OrthoTile c;
+  c.b = t / p.tiles_per_matrix;
+  const int r = t - c.b * p.tiles_per_matrix;
+  if (p.symmetric) {
+    // column nb holds the tiles mb = 0 .. nb
+    int nb = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
+    while ((int64_t)nb * (nb + 1) / 2 > r) --nb;
+    while ((int64_t)(nb + 1) * (nb + 2) / 2 <= r) ++nb;
+    c.nb = nb;
+    c.mb = r - (int)((int64_t)nb * (nb + 1) / 2);
+  } else {
+    const int group = p.group_m * p.num_n_blk;
+    const int g = r / group;
+    const int first = g * p.group_m;
+    const int gm = min(p.group_m, p.num_m_blk - first);
+    const int within = r - g * group;
+    c.mb = first + within % gm;
+    c.nb = within / gm;
+    if (g & 1) c.nb = p.num_n_blk - 1 - c.nb;
+  }
+  return c;
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid_constant__ OrthoGemmParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* epi_base = reinterpret_cast<float*>(smem + T::kStages * T::kStage);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(epi_base) + T::kEpiBytes);
+  uint64_t* op_full = bars;
+  uint64_t* op_empty = bars + T::kStages;
+  uint64_t* acc_full = bars + 2 * T::kStages;
+  uint64_t* acc_empty = acc_full + T::kAccBufs;
+  uint64_t* done_bar = acc_empty + T::kAccBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = T::kPair ? cluster_ctarank() : 0u;
+  const int worker = T::kPair ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int workers = T::kPair ? (int)num_clusters_x() : (int)gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::kStages; ++i) {
+      mbar_init(&op_full[i], 1);
+      mbar_init(&op_empty[i], 1);
+    }
+    for (int i = 0; i < T::kAccBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], T::kCtas * T::kEpiWarps);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&p.map_a);
+    tma_prefetch_map(&p.map_b);
+  }
+  if (warp == 1) {
+    if constexpr (T::kPair) {
+      tmem_alloc_pair(tmem_slot, T::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, T::kTmemCols);
+      tmem_relinquish();
+    }
+    tc_fence_before_sync();
+  }
+  if constexpr (T::kPair) cluster_sync_all();
+  else __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  WaitCtl ctl;
+  ctl.abort = abort_flag;
+  if constexpr (T::kPair) ctl.peer_abort = cluster_generic_ptr(const_cast<int*>(abort_flag), rank ^ 1u);
+  ctl.status = p.status;
+  ctl.limit_ns = p.wait_limit_ns;
+  const uint32_t op_smem = smem_addr(smem);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint32_t full0 = T::kPair ? cluster_smem_addr(smem_addr(op_full), 0) : smem_addr(op_full);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = worker; t < p.num_tiles && ok; t += workers) {
+        const OrthoTile tc = ortho_tile(p, t);
+        const int arow = tc.mb * T::kTile + (int)rank * T::BM;
+        const int bcol = tc.nb * T::kTile + (int)rank * T::kBHeld;
+        for (int kb = 0; kb < p.num_k_blk; ++kb, ++it) {
+          const uint32_t st = it % T::kStages;
+          if (!mbar_wait(&op_empty[st], ((it / T::kStages) & 1u) ^ 1u, ctl)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&op_full[st], T::kCtas * T::kStage);
+          uint8_t* dst = smem + st * T::kStage;
+          const int k0 = kb * T::BK;
+          auto load = [&](const CUtensorMap* map, uint8_t* to, bool mn, int row0) {
+            auto one = [&](uint8_t* d, int c0, int c1) {
+              if constexpr (T::kPair) tma_load_3d_pair(d, map, full0 + st * 8u, c0, c1, tc.b);
+              else tma_load_3d(d, map, &op_full[st], c0, c1, tc.b);
+            };
+            if (!mn) {
+              one(to, k0, row0);
+            } else {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) one(to + g * T::BK * T::kRowBytes, row0 + g * T::BK, k0);
+            }
+          };
+          load(&p.map_a, dst, p.a_mn_major != 0, arow);
+          load(&p.map_b, dst + T::kATile, p.b_mn_major != 0, bcol);
+        }
+      }
+      // a stage is released after its copies landed and were read
+      const uint32_t n_drain = it < (uint32_t)T::kStages ? it : (uint32_t)T::kStages;
+      for (uint32_t i = it - n_drain; i < it; ++i)
+        drain_wait(&op_empty[i % T::kStages], (i / T::kStages) & 1u, p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && rank == 0) {
+      const bool a_mn = p.a_mn_major != 0, b_mn = p.b_mn_major != 0;
+      const uint32_t idesc = make_idesc(0u /* f16 */, a_mn, b_mn, T::kTile, T::kTile);
+      auto commit = [&](uint64_t* bar, uint16_t mask) {
+        if constexpr (T::kPair) mma_commit_multicast(bar, mask);
+        else mma_commit(bar);
+      };
+      uint32_t it = 0, g = 0;
+      bool ok = true;
+      for (int t = worker; t < p.num_tiles && ok; t += workers, ++g) {
+        const uint32_t ab = g % T::kAccBufs;
+        if (!mbar_wait(&acc_empty[ab], ((g / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
+        if constexpr (T::kPair) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        tc_fence_after_sync();
+        const uint32_t d0 = tmem_base + ab * T::kTile;
+        for (int kb = 0; kb < p.num_k_blk; ++kb, ++it) {
+          const uint32_t st = it % T::kStages;
+          if (!mbar_wait(&op_full[st], (it / T::kStages) & 1u, ctl)) { ok = false; break; }
+          tc_fence_after_sync();
+          const uint32_t a_tile = op_smem + st * T::kStage;
+          const uint32_t b_tile = a_tile + T::kATile;
+#pragma unroll
+          for (int ks = 0; ks < T::kKSteps; ++ks) {
+            const uint64_t da = operand_desc<T>(a_tile, a_mn, ks), db = operand_desc<T>(b_tile, b_mn, ks);
+            const uint32_t acc = (kb > 0 || ks > 0) ? 1u : 0u;
+            if constexpr (T::kPair) mma_f16_pair(d0, da, db, idesc, acc);
+            else mma_f16(d0, da, db, idesc, acc);
+          }
+          commit(&op_empty[st], 0x3);
+        }
+        if (!ok) break;
+        commit(&acc_full[ab], 0x3);
+      }
+      // every MMA completes before TMEM is released
+      commit(done_bar, 0x1);
+      drain_wait(done_bar, 0, p.wait_limit_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * q) << 16;
+    const uint32_t stg = smem_addr(epi_base + (warp - 2) * 1024);
+    constexpr int kCcPer = T::kTile / 32 / (T::kEpiWarps / 4);
+    const int cc0 = ((warp - 2) / 4) * kCcPer;
+    const uint32_t acc_empty0 = T::kPair ? cluster_smem_addr(smem_addr(acc_empty), 0) : 0u;
+    const int dt = p.d_dtype;
+    const int es = dt == kOutF32 ? 4 : 2;
+    uint32_t g = 0;
+    for (int t = worker; t < p.num_tiles; t += workers, ++g) {
+      const OrthoTile tc = ortho_tile(p, t);
+      const float f = p.factor ? __ldg(p.factor + tc.b) : 1.0f;
+      const float ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
+      const float cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
+      const float co = p.co;
+      const uint16_t* z = p.z ? p.z + (int64_t)tc.b * p.stride_z : nullptr;
+      uint8_t* d = static_cast<uint8_t*>(p.d) + (int64_t)tc.b * p.stride_d * es;
+      const uint32_t ab = g % T::kAccBufs;
+      if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
+      tc_fence_after_sync();
+      const uint32_t tacc = tmem_base + lane_off + ab * T::kTile;
+      const int row_base = tc.mb * T::kTile + (int)rank * T::BM + 32 * q;
+      const bool mirror = p.symmetric && tc.mb != tc.nb;
+#pragma unroll 1
+      for (int cc = cc0; cc < cc0 + kCcPer; ++cc) {
+        float v[32];
+        tmem_ld_32cols(tacc + cc * 32, v);
+        tmem_ld_wait();
+        if (cc == cc0 + kCcPer - 1) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (T::kPair) mbar_arrive_cluster(acc_empty0 + ab * 8u);
+            else mbar_arrive(&acc_empty[ab]);
+          }
+        }
+        const int col_base = tc.nb * T::kTile + cc * 32;
+        if (row_base >= p.m || col_base >= p.n) continue;
+        stage_write_row(stg, lane, v);
+        __syncwarp();
+        if (p.vec && col_base + 32 <= p.n) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int grow = row_base + i * 4 + (lane >> 3);
+            const float4 x = stage_read_chunk(stg, lane, i);
+            if (grow < p.m) {
+              const int col = col_base + (lane & 7) * 4;
+              float4 o = make_float4(ca * x.x, ca * x.y, ca * x.z, ca * x.w);
+              if (z) {
+                const float4 y = out_load4(z, (int64_t)grow * p.ldz + col, kOutF16);
+                o.x = fmaf(cz, y.x, o.x);
+                o.y = fmaf(cz, y.y, o.y);
+                o.z = fmaf(cz, y.z, o.z);
+                o.w = fmaf(cz, y.w, o.w);
+              }
+              const int64_t idx = (int64_t)grow * p.ldd + col;
+              if (co != 0.0f) {
+                const float4 y = out_load4(d, idx, dt);
+                o.x = fmaf(co, y.x, o.x);
+                o.y = fmaf(co, y.y, o.y);
+                o.z = fmaf(co, y.z, o.z);
+                o.w = fmaf(co, y.w, o.w);
+              }
+              out_store4(d, idx, o, dt);
+            }
+          }
+        } else {
+          const int col = col_base + lane;
+#pragma unroll 4
+          for (int r = 0; r < 32; ++r) {
+            const float x = stage_read_elem(stg, lane, r);
+            const int grow = row_base + r;
+            if (grow < p.m && col < p.n) {
+              float o = ca * x;
+              if (z) o = fmaf(cz, out_load(z, (int64_t)grow * p.ldz + col, kOutF16), o);
+              const int64_t idx = (int64_t)grow * p.ldd + col;
+              if (co != 0.0f) o = fmaf(co, out_load(d, idx, dt), o);
+              out_store(d, idx, o, dt);
+            }
+          }
+        }
+        if (mirror) {
+          // the same values at (column, row): lanes along the row of D^T
+          const int grow = row_base + lane;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int col = col_base + j;
+            if (col < p.n && grow < p.m) {
+              float o = ca * v[j];
+              if (z) o = fmaf(cz, out_load(z, (int64_t)col * p.ldz + grow, kOutF16), o);
+              out_store(d, (int64_t)col * p.ldd + grow, o, dt);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  // neither CTA of a pair leaves while the other may address its shared memory
+  __syncwarp();
+  tc_fence_before_sync();
+  if constexpr (T::kPair) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    if constexpr (T::kPair) tmem_dealloc_pair(tmem_base, T::kTmemCols);
+    else tmem_dealloc(tmem_base, T::kTmemCols);
+  }
+}
+
+template <class T>
+void fill(OrthoKernel* out) {
+  out->fn = reinterpret_cast<const void*>(&ortho_gemm_kernel<T>);
+  out->block = T::kThreads;
+  out->smem_bytes = T::kSmemBytes;
+  out->tile = T::kTile;
+  out->ctas = T::kCtas;
+}
+
+template <class XT>
+cudaError_t launch_scale_type(const OrthoScaleParams& p, cudaLaunchConfig_t& cfg) {
+  cudaError_t e = cudaLaunchKernelEx(&cfg, ortho_norm_kernel<XT>, p);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, ortho_scale_kernel<XT>, p);
+}
+
+}  // namespace
+
+void ortho_lookup(bool pair, OrthoKernel* out) {
+  if (pair) fill<OrthoTraits<true>>(out);
+  else fill<OrthoTraits<false>>(out);
+}
+
+cudaError_t launch_ortho_scale(const OrthoScaleParams& p, int g_dtype, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.blocks, (unsigned)p.batch);
+  cfg.blockDim = dim3(kScaleThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  switch (g_dtype) {
+    case 0: return launch_scale_type<float>(p, cfg);
+    case 1: return launch_scale_type<__half>(p, cfg);
+    default: return launch_scale_type<__nv_bfloat16>(p, cfg);
+  }
+}
+
+}  // namespace mpg

@@ -1,0 +1,58 @@
+// Internal structures of the orthogonalised update: the norm and scaling
+// kernels and the fp16 product with a fused linear epilogue (ortho.cu),
+// launched from ortho_api.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mpg {
+
+// Blocks that sum the squares of one matrix, at most.
+constexpr int kOrthoNormBlocks = 256;
+
+struct OrthoScaleParams {
+  const void* g;
+  int64_t ldg, stride_g;
+  int32_t rows, cols, batch;
+  int32_t g_vec;              // 8-element chunks of a line of g are 16-byte aligned
+  double* partial;            // [batch][kOrthoNormBlocks]
+  int32_t blocks;             // partial sums of one matrix
+  uint16_t* x;                // fp16 [batch][rows][ldx], ldx % 8 == 0
+  int64_t ldx;
+  float* factor;              // [batch]: normalised matrix = factor * x
+  float target;               // x is scaled by a power of two to a norm in [target, 2 target)
+  float eps;
+};
+cudaError_t launch_ortho_scale(const OrthoScaleParams& p, int g_dtype, cudaStream_t stream);
+
+// D = ca * A B + cz * Z + co * D, for each matrix of the batch.
+struct OrthoGemmParams {
+  CUtensorMap map_a, map_b;   // fp16; box 64 x 128 (K-major) or 64 x 64 (MN-major)
+  int32_t a_mn_major, b_mn_major;
+  int32_t m, n, k, batch;
+  int32_t symmetric;          // D and Z are symmetric: tiles above the diagonal are stored twice
+  int32_t num_m_blk, num_n_blk, num_k_blk, tiles_per_matrix, num_tiles, group_m;
+  const uint16_t* z;          // fp16, or null
+  int64_t ldz, stride_z;
+  void* d;
+  int64_t ldd, stride_d;
+  int32_t d_dtype;            // 0 fp32, 1 fp16, 2 bf16
+  int32_t vec;                // 4-element vectors of D and Z are aligned
+  float ca, cz, co;
+  const float* factor;        // per matrix, or null
+  int32_t ca_power, cz_power; // ca and cz are multiplied by factor to these powers (0, 1, 2)
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+struct OrthoKernel {
+  const void* fn;
+  int block, smem_bytes;
+  int tile;                   // tiles are tile x tile
+  int ctas;                   // CTAs that share a tile
+};
+void ortho_lookup(bool pair, OrthoKernel* out);
+
+}  // namespace mpg
