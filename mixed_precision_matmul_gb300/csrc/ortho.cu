@@ -71,6 +71,55 @@ __device__ __forceinline__ void read8(const XT* line, int c, int cols, bool vec,
 }
 
 constexpr int kScaleThreads = 256;
+constexpr int kBatch = 4;   // loads of 16 or 32 bytes that a thread has in flight
+
+// The chunks of 8 elements of a matrix that one thread takes: its index, then
+// every grid's width further, as (row, chunk of the row) without divisions in
+// the loop.
+struct ChunkWalk {
+  int64_t row;
+  int chunk, rows, per, step_rows, step_chunks;
+  __device__ __forceinline__ ChunkWalk(int per_, int rows_) : rows(rows_), per(per_) {
+    const uint32_t i = blockIdx.x * kScaleThreads + threadIdx.x, n = gridDim.x * kScaleThreads;
+    row = i / (uint32_t)per;
+    chunk = (int)(i % (uint32_t)per);
+    step_rows = (int)(n / (uint32_t)per);
+    step_chunks = (int)(n % (uint32_t)per);
+  }
+  __device__ __forceinline__ bool inside() const { return row < rows; }
+  __device__ __forceinline__ void next() {
+    row += step_rows;
+    chunk += step_chunks;
+    if (chunk >= per) {
+      chunk -= per;
+      ++row;
+    }
+  }
+};
+
+// The thread's next kBatch chunks, their loads issued together (zeros beyond
+// the matrix).
+template <class XT>
+__device__ __forceinline__ void read_batch(ChunkWalk& at, const XT* g, int64_t ldg, int cols, bool vec,
+                                           float (&v)[kBatch][8]) {
+  const XT* line[kBatch];
+  int c[kBatch];
+  bool fast = vec;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    line[u] = at.inside() ? g + at.row * ldg : nullptr;
+    c[u] = at.chunk * 8;
+    fast = fast && line[u] && c[u] + 8 <= cols;
+    at.next();
+  }
+  if (fast) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) read8<XT>(line[u], c[u], c[u] + 8, true, v[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) read8<XT>(line[u], c[u], line[u] ? cols : 0, vec, v[u]);
+  }
+}
 
 // partial[b][block] = sum of squares over the block's share of matrix b.  The
 // squares of 8 elements are added in fp32 where that is safe (the sum neither
@@ -78,40 +127,51 @@ constexpr int kScaleThreads = 256;
 // of such groups in fp32, the rest in 64 bits, always in the same order.
 template <class XT>
 __global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_constant__ OrthoScaleParams p) {
-  __shared__ double red[kScaleThreads / 32];
+  __shared__ float red[kScaleThreads / 32];
+  __shared__ double red_wide[kScaleThreads / 32];
+  if (threadIdx.x < kScaleThreads / 32) red_wide[threadIdx.x] = 0.0;
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.y;
   const XT* g = reinterpret_cast<const XT*>(p.g) + (int64_t)b * p.stride_g;
-  const int per = (p.cols + 7) / 8;
-  const int64_t total = (int64_t)p.rows * per;
+  ChunkWalk at((p.cols + 7) / 8, p.rows);
   float sum = 0.0f;
   double wide = 0.0;
-  for (int64_t i = blockIdx.x * (int64_t)kScaleThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kScaleThreads) {
-    const int64_t r = i / per;
-    float v[8];
-    read8<XT>(g + r * p.ldg, (int)(i - r * per) * 8, p.cols, p.g_vec != 0, v);
-    float s = 0.0f;
+  while (at.inside()) {
+    float v[kBatch][8];
+    read_batch<XT>(at, g, p.ldg, p.cols, p.g_vec != 0, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
-    if (s >= 1e-30f && s <= 1e30f) {
-      sum += s;
-      if (sum > 1e30f) { wide += (double)sum; sum = 0.0f; }
-    } else {
+    for (int u = 0; u < kBatch; ++u) {
+      float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wide += (double)v[j] * (double)v[j];
+      for (int j = 0; j < 8; ++j) s = fmaf(v[u][j], v[u][j], s);
+      if (s >= 1e-30f && s <= 1e30f) {
+        sum += s;
+        if (sum > 1e30f) { wide += (double)sum; sum = 0.0f; }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (v[u][j] != 0.0f) wide += (double)v[u][j] * (double)v[u][j];
+      }
     }
   }
-  wide += (double)sum;
+  // 64-bit arithmetic is slow here (reducing every thread's sum in 64 bits
+  // took four times as long as reading a 4096^2 matrix): the safe sums are
+  // reduced in fp32, the others only where there are any
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = wide;
-  __syncthreads();
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[warp] = sum;
+  if (__syncthreads_or(wide != 0.0)) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
+    if ((threadIdx.x & 31) == 0) red_wide[warp] = wide;
+    __syncthreads();
+  }
   if (threadIdx.x == 0) {
     double s = 0.0;
 #pragma unroll
-    for (int w = 0; w < kScaleThreads / 32; ++w) s += red[w];
+    for (int w = 0; w < kScaleThreads / 32; ++w) s += (double)red[w] + red_wide[w];
     p.partial[(int64_t)b * kOrthoNormBlocks + blockIdx.x] = s;
   }
 }
@@ -120,51 +180,45 @@ __global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_
 // 2 target), and factor = 2^-e / (norm + eps).
 template <class XT>
 __global__ void __launch_bounds__(kScaleThreads) ortho_scale_kernel(const __grid_constant__ OrthoScaleParams p) {
-  __shared__ double red[kScaleThreads / 32];
   __shared__ float scale_sh;
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.y;
-  double s = (int)threadIdx.x < p.blocks ? p.partial[(int64_t)b * kOrthoNormBlocks + threadIdx.x] : 0.0;
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < p.blocks; i += 32) s += p.partial[(int64_t)b * kOrthoNormBlocks + i];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.0;
-#pragma unroll
-    for (int w = 0; w < kScaleThreads / 32; ++w) s += red[w];
-    const double norm = sqrt(s);
-    int e = 0;
-    if (norm > 0.0 && norm < 1e300) {
-      e = ilogb((double)p.target) - ilogb(norm);
-      if (scalbn(norm, e) < (double)p.target) ++e;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(s);
+      int e = 0;
+      if (norm > 0.0 && norm < 1e300) {
+        e = ilogb((double)p.target) - ilogb(norm);
+        if (scalbn(norm, e) < (double)p.target) ++e;
+      }
+      // fp32 inputs below 2^-126 in norm reach the target only as far as a
+      // single factor of fp32 carries them
+      e = min(max(e, -126), 127);
+      scale_sh = scalbnf(1.0f, e);
+      if (blockIdx.x == 0) p.factor[b] = (float)(scalbn(1.0, -e) / (norm + (double)p.eps));
     }
-    // fp32 inputs below 2^-126 in norm reach the target only as far as a
-    // single factor of fp32 carries them
-    e = min(max(e, -126), 127);
-    scale_sh = scalbnf(1.0f, e);
-    if (blockIdx.x == 0) p.factor[b] = (float)(scalbn(1.0, -e) / (norm + (double)p.eps));
   }
   __syncthreads();
   const float scale = scale_sh;
   const XT* g = reinterpret_cast<const XT*>(p.g) + (int64_t)b * p.stride_g;
   uint16_t* x = p.x + (int64_t)b * p.rows * p.ldx;
-  const int per = (int)(p.ldx / 8);
-  const int64_t total = (int64_t)p.rows * per;
-  for (int64_t i = blockIdx.x * (int64_t)kScaleThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kScaleThreads) {
-    const int64_t r = i / per;
-    const int c = (int)(i - r * per) * 8;
-    float v[8];
-    read8<XT>(g + r * p.ldg, c, p.cols, p.g_vec != 0, v);
-    uint32_t w[4];
+  ChunkWalk at((int)(p.ldx / 8), p.rows);
+  while (at.inside()) {
+    float v[kBatch][8];
+    ChunkWalk to = at;
+    read_batch<XT>(at, g, p.ldg, p.cols, p.g_vec != 0, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2 h = __floats2half2_rn(v[2 * j] * scale, v[2 * j + 1] * scale);
-      memcpy(&w[j], &h, 4);
+    for (int u = 0; u < kBatch; ++u, to.next()) {
+      if (!to.inside()) continue;
+      *reinterpret_cast<uint4*>(x + to.row * p.ldx + to.chunk * 8) =
+          make_uint4(pack_f16x2(v[u][0] * scale, v[u][1] * scale), pack_f16x2(v[u][2] * scale, v[u][3] * scale),
+                     pack_f16x2(v[u][4] * scale, v[u][5] * scale), pack_f16x2(v[u][6] * scale, v[u][7] * scale));
     }
-    *reinterpret_cast<uint4*>(x + r * p.ldx + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -201,6 +255,18 @@ struct OrthoTraits {
   static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiBytes + kNumBars * 8 + 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 struct OrthoTile {
   int b, mb, nb;
@@ -366,6 +432,10 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
     }
   } else {
     // ------------------------------------------------------------ epilogue
+    // A warp owns 32 rows (one per lane) and half of the tile's columns, in
+    // chunks of 32.  Z's elements of a chunk are fetched a chunk ahead (the
+    // first before the accumulator is complete): loaded where they are used,
+    // their latency was most of the kernel's time at 768^2.
     const int q = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(32 * q) << 16;
     const uint32_t stg = smem_addr(epi_base + (warp - 2) * 1024);
@@ -381,14 +451,23 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
       const float ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
       const float cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
       const float co = p.co;
-      const uint16_t* z = p.z ? p.z + (int64_t)tc.b * p.stride_z : nullptr;
       uint8_t* d = static_cast<uint8_t*>(p.d) + (int64_t)tc.b * p.stride_d * es;
       const uint32_t ab = g % T::kAccBufs;
-      if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
-      tc_fence_after_sync();
       const uint32_t tacc = tmem_base + lane_off + ab * T::kTile;
       const int row_base = tc.mb * T::kTile + (int)rank * T::BM + 32 * q;
+      const int row = row_base + lane;
       const bool mirror = p.symmetric && tc.mb != tc.nb;
+      const uint16_t* zrow = p.z && row < p.m ? p.z + (int64_t)tc.b * p.stride_z + (int64_t)row * p.ldz : nullptr;
+      uint4 z[4];
+      auto fetch_z = [&](int cc) {
+        const int c0 = tc.nb * T::kTile + cc * 32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          z[i] = zrow && c0 + 8 * i < p.n ? __ldg(reinterpret_cast<const uint4*>(zrow + c0) + i) : make_uint4(0, 0, 0, 0);
+      };
+      fetch_z(cc0);
+      if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
+      tc_fence_after_sync();
 #pragma unroll 1
       for (int cc = cc0; cc < cc0 + kCcPer; ++cc) {
         float v[32];
@@ -402,63 +481,115 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
             else mbar_arrive(&acc_empty[ab]);
           }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            __half2 h;
+            memcpy(&h, &w[j], 4);
+            const float2 y = __half22float2(h);
+            v[8 * i + 2 * j] = fmaf(cz, y.x, ca * v[8 * i + 2 * j]);
+            v[8 * i + 2 * j + 1] = fmaf(cz, y.y, ca * v[8 * i + 2 * j + 1]);
+          }
+        }
+        if (cc + 1 < cc0 + kCcPer) fetch_z(cc + 1);
         const int col_base = tc.nb * T::kTile + cc * 32;
         if (row_base >= p.m || col_base >= p.n) continue;
+        const bool whole = col_base + 32 <= p.n;
+        if (dt != kOutF32 && co == 0.0f && p.vec16 && whole) {
+          // 16-bit rows of 64 bytes through shared memory: chunk c of row r at
+          // slot c ^ ((r / 2) & 3), which spreads both the writes (a row per
+          // lane) and the reads (four lanes a row) over all banks
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = dt == kOutF16 ? pack_f16x2(v[2 * j], v[2 * j + 1]) : pack_bf16x2(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            st_shared_v4(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
+                         w[4 * c + 3]);
+          if (mirror) {
+            // and transposed: row j of D^T's chunk is column j here
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int c = 2 * j + h;
+                st_shared_u16(stg + 2048 + c * 64 + (((lane >> 3) ^ ((c >> 1) & 3)) << 4) + (lane & 7) * 2,
+                              (uint16_t)(w[j] >> (16 * h)));
+              }
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), c = lane & 3;
+            const uint32_t at = r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+            if (row_base + r < p.m)
+              *reinterpret_cast<uint4*>(d + ((int64_t)(row_base + r) * p.ldd + col_base + c * 8) * 2) =
+                  ld_shared_u4(stg + at);
+            if (mirror) {
+              // column col_base + r, rows row_base + 8c ..
+              const int row8 = row_base + c * 8;
+              uint16_t* to = reinterpret_cast<uint16_t*>(d) + (int64_t)(col_base + r) * p.ldd + row8;
+              const uint4 x = ld_shared_u4(stg + 2048 + at);
+              if (row8 + 8 <= p.m) {
+                *reinterpret_cast<uint4*>(to) = x;
+              } else {
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (row8 + j < p.m) to[j] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
+              }
+            }
+          }
+          __syncwarp();
+          continue;
+        }
         stage_write_row(stg, lane, v);
         __syncwarp();
-        if (p.vec && col_base + 32 <= p.n) {
+        if (p.vec && whole) {
+          float4 y[8];
+          if (co != 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int grow = row_base + i * 4 + (lane >> 3);
+              if (grow < p.m) y[i] = out_load4(d, (int64_t)grow * p.ldd + col_base + (lane & 7) * 4, dt);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int grow = row_base + i * 4 + (lane >> 3);
-            const float4 x = stage_read_chunk(stg, lane, i);
+            float4 o = stage_read_chunk(stg, lane, i);
             if (grow < p.m) {
-              const int col = col_base + (lane & 7) * 4;
-              float4 o = make_float4(ca * x.x, ca * x.y, ca * x.z, ca * x.w);
-              if (z) {
-                const float4 y = out_load4(z, (int64_t)grow * p.ldz + col, kOutF16);
-                o.x = fmaf(cz, y.x, o.x);
-                o.y = fmaf(cz, y.y, o.y);
-                o.z = fmaf(cz, y.z, o.z);
-                o.w = fmaf(cz, y.w, o.w);
-              }
-              const int64_t idx = (int64_t)grow * p.ldd + col;
               if (co != 0.0f) {
-                const float4 y = out_load4(d, idx, dt);
-                o.x = fmaf(co, y.x, o.x);
-                o.y = fmaf(co, y.y, o.y);
-                o.z = fmaf(co, y.z, o.z);
-                o.w = fmaf(co, y.w, o.w);
+                o.x = fmaf(co, y[i].x, o.x);
+                o.y = fmaf(co, y[i].y, o.y);
+                o.z = fmaf(co, y[i].z, o.z);
+                o.w = fmaf(co, y[i].w, o.w);
               }
-              out_store4(d, idx, o, dt);
+              out_store4(d, (int64_t)grow * p.ldd + col_base + (lane & 7) * 4, o, dt);
             }
           }
         } else {
           const int col = col_base + lane;
 #pragma unroll 4
           for (int r = 0; r < 32; ++r) {
-            const float x = stage_read_elem(stg, lane, r);
+            float o = stage_read_elem(stg, lane, r);
             const int grow = row_base + r;
             if (grow < p.m && col < p.n) {
-              float o = ca * x;
-              if (z) o = fmaf(cz, out_load(z, (int64_t)grow * p.ldz + col, kOutF16), o);
               const int64_t idx = (int64_t)grow * p.ldd + col;
               if (co != 0.0f) o = fmaf(co, out_load(d, idx, dt), o);
               out_store(d, idx, o, dt);
             }
           }
         }
-        if (mirror) {
+        if (mirror && row < p.m) {
           // the same values at (column, row): lanes along the row of D^T
-          const int grow = row_base + lane;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int col = col_base + j;
-            if (col < p.n && grow < p.m) {
-              float o = ca * v[j];
-              if (z) o = fmaf(cz, out_load(z, (int64_t)col * p.ldz + grow, kOutF16), o);
-              out_store(d, (int64_t)col * p.ldd + grow, o, dt);
-            }
-          }
+          for (int j = 0; j < 32; ++j)
+            if (col_base + j < p.n) out_store(d, (int64_t)(col_base + j) * p.ldd + row, v[j], dt);
         }
         __syncwarp();
       }

@@ -39,7 +39,8 @@ struct OrthoGemmParams {
   void* d;
   int64_t ldd, stride_d;
   int32_t d_dtype;            // 0 fp32, 1 fp16, 2 bf16
-  int32_t vec;                // 4-element vectors of D and Z are aligned
+  int32_t vec;                // 4-element vectors of D are aligned
+  int32_t vec16;              // 16-byte chunks of a 16-bit D are aligned
   float ca, cz, co;
   const float* factor;        // per matrix, or null
   int32_t ca_power, cz_power; // ca and cz are multiplied by factor to these powers (0, 1, 2)

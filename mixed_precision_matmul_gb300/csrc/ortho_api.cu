@@ -56,9 +56,10 @@ mpg_status operand_map(CUtensorMap* map, const Matrix& x, bool mn_major, int64_t
 
 mpg_status launch_gemm(DeviceInfo* dev, OrthoGemmParams p, cudaStream_t stream) {
   // Tiles of 256 x 256 on CTA pairs read half the operand bytes per flop, but
-  // leave more of the machine idle when there are few tiles.  The rule takes
-  // the form whose last round ends first, counting a round of pair tiles as
-  // twice a round of 128 x 128 tiles (twice the flops per SM).
+  // leave more of the machine idle when there are few tiles.  A 128 x 128
+  // tile keeps the shared memory of its SM busy for as long as a pair takes
+  // for four times the work on two SMs (k = 4096: 22 us against 25 us), so
+  // single CTAs pay only where they need fewer rounds.
   OrthoKernel one, two;
   ortho_lookup(false, &one);
   ortho_lookup(true, &two);
@@ -72,8 +73,8 @@ mpg_status launch_gemm(DeviceInfo* dev, OrthoGemmParams p, cudaStream_t stream) 
   };
   const int64_t t1 = tiles(one.tile), t2 = tiles(two.tile);
   const int64_t r1 = (t1 * p.batch + dev->sm_count - 1) / dev->sm_count;
-  const int64_t r2 = 2 * ((t2 * p.batch + clusters - 1) / clusters);
-  const bool pair = r2 <= r1;
+  const int64_t r2 = (t2 * p.batch + clusters - 1) / clusters;
+  const bool pair = r2 < r1;
   const OrthoKernel& k = pair ? two : one;
   const int64_t per = pair ? t2 : t1;
   if (per * p.batch > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
@@ -164,8 +165,9 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
   // single entry that holds the whole norm stays within fp16
   sp.target = (float)std::min(std::sqrt((double)m * (double)n), 16384.0);
   sp.eps = eps;
+  // two loads in flight per thread at least, at most enough blocks to fill the machine
   const int64_t chunks = m * (l.ldx / 8);
-  sp.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((chunks + 1023) / 1024, kOrthoNormBlocks));
+  sp.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((chunks + 511) / 512, kOrthoNormBlocks));
   cudaError_t e = launch_ortho_scale(sp, (int)g_dtype, st);
   if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "scaling launch: %s", cudaGetErrorString(e));
 
@@ -191,7 +193,7 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
     p.ldd = S.ld;
     p.stride_d = side * S.ld;
     p.d_dtype = MPG_F16;
-    p.vec = 1;
+    p.vec = p.vec16 = 1;
     p.ca = first ? 1.0f : 1.0f / (sx * sx);
     p.factor = first ? factor : nullptr;
     p.ca_power = first ? 2 : 0;
@@ -210,7 +212,7 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
     p.ldd = B.ld;
     p.stride_d = side * B.ld;
     p.d_dtype = MPG_F16;
-    p.vec = 1;
+    p.vec = p.vec16 = 1;
     p.ca = coeffs[2];
     p.cz = coeffs[1];
     if ((s = launch_gemm(dev, p, st)) != MPG_OK) return s;
@@ -244,12 +246,13 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
       p.co = beta;
       const size_t chunk = o_dtype == MPG_F32 ? 16 : 8;
       p.vec = aligned(O, chunk) && ldo % 4 == 0 && strideO % 4 == 0;
+      p.vec16 = aligned(O, 16) && ldo % 8 == 0 && strideO % 8 == 0;
     } else {
       p.d = Y.ptr;
       p.ldd = Y.ld;
       p.stride_d = m * Y.ld;
       p.d_dtype = MPG_F16;
-      p.vec = 1;
+      p.vec = p.vec16 = 1;
     }
     if ((s = launch_gemm(dev, p, st)) != MPG_OK) return s;
   }

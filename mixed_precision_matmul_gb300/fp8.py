@@ -26,6 +26,15 @@ def _default_options(c_dtype: int):
     return _m.options(c_dtype=c_dtype)
 
 
+@functools.cache
+def _raw_stream():
+    """Handle of the current stream of a device index.  (torch.cuda.current_stream
+    builds a Stream object first: 2 us a call of about 10.)"""
+    torch = _types()[0]
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on_stream(stream, tensors, call):
     """Run ``call()`` with ``stream`` current, so that what it allocates belongs
     to that stream, and keep ``tensors`` alive for the work enqueued there."""
@@ -39,19 +48,21 @@ def _on_stream(stream, tensors, call):
         return call()
 
 
-def _current(device):
-    """Handle of the current stream of a tensor's device."""
-    return _types()[0].cuda.current_stream(device).cuda_stream
-
-
-def _check_device(*tensors):
-    device = tensors[0].device
-    if device.type != "cuda":
+def _device_index(*tensors) -> int:
+    """The CUDA device that all given tensors are on."""
+    index = tensors[0].get_device()
+    if index < 0:
         raise ValueError("CUDA tensors expected")
-    for t in tensors[1:]:
-        if t is not None and t.device != device:
+    for t in tensors:
+        if t is not None and t.get_device() != index:
             raise ValueError("operands are on different devices")
-    return device
+    return index
+
+
+def _on_device(index, call):
+    """``call`` with device ``index`` current."""
+    with _types()[0].cuda.device(index):
+        return call()
 
 
 def fp8_quantize_raw(rows, cols, X, ldx, x_dtype, fmt, scale_rows, Q, ldq, S, s_row, s_k, QT, ldqt, ST, st_row, st_k,
@@ -65,21 +76,20 @@ def fp8_quantize_raw(rows, cols, X, ldx, x_dtype, fmt, scale_rows, Q, ldq, S, s_
 
 
 def _codes(rows, cols, dtype, device):
-    """rows x cols 8-bit tensor whose lines start on 16-byte boundaries."""
-    torch = _types()[0]
-    ld = -(-cols // 16) * 16
-    t = torch.empty((rows, ld), dtype=dtype, device=device)
-    return t if ld == cols else t[:, :cols]
+    """(rows x cols 8-bit tensor whose lines start on 16-byte boundaries, leading dimension)."""
+    ld = (cols + 15) & ~15
+    t = _types()[0].empty((rows, ld), dtype=dtype, device=device)
+    return (t if ld == cols else t[:, :cols]), max(ld, 1)
 
 
 def _scales(rows, cols, scale_rows, device):
-    """Scales of a rows x cols matrix; per-row scales lie block by block, which
-    is how the product reads them fastest."""
+    """(scales of a rows x cols matrix, row stride, k stride).  Per-row scales lie
+    block by block, which is how the product reads them fastest."""
     torch = _types()[0]
     kb = -(-cols // BLOCK)
     if scale_rows == 1:
-        return torch.empty((kb, rows), dtype=torch.float32, device=device).t()
-    return torch.empty((-(-rows // BLOCK), kb), dtype=torch.float32, device=device)
+        return torch.empty_strided((rows, kb), (1, rows), dtype=torch.float32, device=device), 1, rows
+    return torch.empty((-(-rows // BLOCK), kb), dtype=torch.float32, device=device), kb, 1
 
 
 def fp8_quantize(x, fmt="e4m3", block: str = "row", transpose: bool = False, stream=None):
@@ -97,35 +107,40 @@ def fp8_quantize(x, fmt="e4m3", block: str = "row", transpose: bool = False, str
     if stream is not None:
         return _on_stream(stream, [x], lambda: fp8_quantize(x, fmt, block, transpose))
     fmt = FORMAT_NAMES.get(fmt, fmt)
-    if fmt not in dtypes:
+    code = dtypes.get(fmt)
+    if code is None:
         raise ValueError(f"unknown 8-bit format {fmt!r}")
     if block not in ("row", "tile"):
         raise ValueError("block is 'row' or 'tile'")
     if x.dim() != 2:
         raise ValueError("a 2-D tensor is expected")
-    if x.dtype not in codes:
+    x_dtype = codes.get(x.dtype)
+    if x_dtype is None:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    device = _check_device(x)
+    index = _device_index(x)
+    if index != torch.cuda.current_device():
+        return _on_device(index, lambda: fp8_quantize(x, fmt, block, transpose))
     rows, cols = x.shape
-    if rows and cols > 1 and x.stride(1) != 1:
+    ldx, unit = x.stride()
+    if rows and cols > 1 and unit != 1:
         raise ValueError("x must be row-major with unit column stride")
-    ldx = x.stride(0) if rows > 1 else max(cols, 1)
+    if rows < 2:
+        ldx = max(cols, 1)
     if ldx < cols:
         raise ValueError("the rows of x overlap")
+    device = x.device
     scale_rows = 1 if block == "row" else BLOCK
-    q = _codes(rows, cols, dtypes[fmt], device)
-    s = _scales(rows, cols, scale_rows, device)
+    q, ldq = _codes(rows, cols, code, device)
+    s, s_row, s_k = _scales(rows, cols, scale_rows, device)
     qt = st = None
+    t_args = (0, 0, 0, 0, 0)
     if transpose:
-        qt = _codes(cols, rows, dtypes[fmt], device)
-        st = _scales(cols, rows, scale_rows, device)
+        qt, ldqt = _codes(cols, rows, code, device)
+        st, st_row, st_k = _scales(cols, rows, scale_rows, device)
+        t_args = (qt.data_ptr(), ldqt, st.data_ptr(), st_row, st_k)
     if rows and cols:
-        with torch.cuda.device(device):
-            fp8_quantize_raw(rows, cols, x.data_ptr(), ldx, codes[x.dtype], fmt, scale_rows,
-                             q.data_ptr(), q.stride(0), s.data_ptr(), s.stride(0), s.stride(1),
-                             qt.data_ptr() if transpose else 0, qt.stride(0) if transpose else 0,
-                             st.data_ptr() if transpose else 0, st.stride(0) if transpose else 0,
-                             st.stride(1) if transpose else 0, _current(device))
+        fp8_quantize_raw(rows, cols, x.data_ptr(), ldx, x_dtype, fmt, scale_rows, q.data_ptr(), ldq, s.data_ptr(),
+                         s_row, s_k, *t_args, _raw_stream()(index))
     return (q, s, qt, st) if transpose else (q, s)
 
 
@@ -142,31 +157,32 @@ def gemm_fp8_raw(m, n, k, A, B, C, ldc, alpha, beta, workspace=0, workspace_byte
 
 
 def _operand(t, scale, name, formats):
-    """The description of an 8-bit tensor and its scales."""
-    torch = _types()[0]
+    """(description of an 8-bit tensor and its scales, rows, k)."""
     if t.dim() != 2 or scale.dim() != 2:
         raise ValueError(f"{name} and its scales are 2-D tensors")
     fmt = formats.get(t.dtype)
     if fmt is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if scale.dtype != torch.float32:
+    if scale.dtype != _types()[0].float32:
         raise TypeError(f"{name}: scales must be fp32")
     rows, k = t.shape
-    kb = -(-k // BLOCK)
-    if tuple(scale.shape) == (rows, kb):
+    sr, sk = scale.shape
+    if sk == (k + BLOCK - 1) // BLOCK and sr == rows:
         scale_rows = 1
-    elif tuple(scale.shape) == (-(-rows // BLOCK), kb):
+    elif sk == (k + BLOCK - 1) // BLOCK and sr == (rows + BLOCK - 1) // BLOCK:
         scale_rows = BLOCK
     else:
         raise ValueError(f"{name}: scales of shape {tuple(scale.shape)} fit neither 1 x 128 nor 128 x 128 blocks of "
                          f"{tuple(t.shape)}")
-    if rows and k > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if k > 1 and unit != 1 and rows:
         raise ValueError(f"{name} must be row-major with unit column stride")
-    ld = t.stride(0) if rows > 1 else max(k, 1)
-    if rows and ld < k:
+    if rows < 2:
+        ld = k
+    elif ld < k:
         raise ValueError(f"the rows of {name} overlap")
-    return _m.Fp8Operand(t.data_ptr(), max(ld, k, 1), fmt, scale_rows, scale.data_ptr(), scale.stride(0),
-                         scale.stride(1))
+    s_row, s_k = scale.stride()
+    return _m.Fp8Operand(t.data_ptr(), ld or 1, fmt, scale_rows, scale.data_ptr(), s_row, s_k), rows, k
 
 
 def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0.0, out_dtype=None, workspace=None,
@@ -186,29 +202,35 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
     if stream is not None:
         return _on_stream(stream, [A, a_scale, B, b_scale, C, workspace],
                           lambda: gemm_fp8(A, a_scale, B, b_scale, C, alpha, beta, out_dtype, workspace, opts))
-    device = _check_device(A, a_scale, B, b_scale, C, workspace)
-    a = _operand(A, a_scale, "A", formats)
-    b = _operand(B, b_scale, "B", formats)
-    m, k = A.shape
-    n = B.shape[0]
-    if B.shape[1] != k:
+    index = _device_index(A, a_scale, B, b_scale, C, workspace)
+    if index != torch.cuda.current_device():
+        return _on_device(index, lambda: gemm_fp8(A, a_scale, B, b_scale, C, alpha, beta, out_dtype, workspace, opts))
+    a, m, k = _operand(A, a_scale, "A", formats)
+    b, n, kb = _operand(B, b_scale, "B", formats)
+    if kb != k:
         raise ValueError("A and B have different k")
     if C is None:
         if beta != 0.0:
             raise ValueError("beta needs C")
-        C = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=device)
-    elif out_dtype is not None and C.dtype != out_dtype:
-        raise ValueError("C has another dtype than out_dtype")
-    if tuple(C.shape) != (m, n):
-        raise ValueError("shape mismatch")
-    if C.dtype not in codes or (m and n > 1 and C.stride(1) != 1):
-        raise ValueError("C must be fp32, fp16 or bf16 with unit column stride")
-    ldc = C.stride(0) if m > 1 else max(n, 1)
-    if m and ldc < n:
-        raise ValueError("the rows of C overlap")
+        C = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=A.device)
+        ldc = n
+    else:
+        if out_dtype is not None and C.dtype != out_dtype:
+            raise ValueError("C has another dtype than out_dtype")
+        if C.shape != (m, n):
+            raise ValueError("shape mismatch")
+        ldc, unit = C.stride()
+        if m and n > 1 and unit != 1:
+            raise ValueError("C must have unit column stride")
+        if m < 2:
+            ldc = n
+        elif ldc < n:
+            raise ValueError("the rows of C overlap")
+    code = codes.get(C.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {C.dtype}")
     if m == 0 or n == 0:
         return C
-    code = codes[C.dtype]
     if opts is None:
         opts = _default_options(code)
     elif opts.c_dtype != code:
@@ -216,11 +238,13 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
         ctypes.memmove(ctypes.byref(o), ctypes.byref(opts), ctypes.sizeof(_m.Options))
         o.c_dtype = code
         opts = o
-    with torch.cuda.device(device):
+    ws = ws_bytes = 0
+    if workspace is None and (((a.data or 0) | (b.data or 0)) & 15 or (m > 1 and a.ld & 15) or (n > 1 and b.ld & 15)):
+        # lines that TMA cannot describe are copied to aligned ones
         need = _m.lib().mpg_gemm_fp8_workspace_size(m, n, k, ctypes.byref(a), ctypes.byref(b))
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        gemm_fp8_raw(m, n, k, a, b, C.data_ptr(), ldc, alpha, beta,
-                     workspace.data_ptr() if workspace is not None else 0,
-                     workspace.numel() * workspace.element_size() if workspace is not None else 0, _current(device), opts)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    gemm_fp8_raw(m, n, k, a, b, C.data_ptr(), ldc, alpha, beta, ws, ws_bytes, _raw_stream()(index), opts)
     return C

@@ -6,7 +6,7 @@ import ctypes
 
 import mixed_precision_matmul_gb300 as _m
 
-from .fp8 import _check_device, _current, _on_stream, _types
+from .fp8 import _device_index, _on_device, _on_stream, _raw_stream, _types
 
 #: a, b, c of the quintic step whose five applications bring singular values to 0.7 .. 1.2
 NS_COEFFS = (3.4445, -4.7750, 2.0315)
@@ -60,11 +60,14 @@ def orthogonalize(G, O=None, steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7
         raise TypeError(f"unsupported dtype {G.dtype}")
     if len(coeffs) != 3:
         raise ValueError("three coefficients are expected")
-    device = _check_device(G, O, workspace)
+    index = _device_index(G, O, workspace)
+    if index != torch.cuda.current_device():
+        return _on_device(index,
+                          lambda: orthogonalize(G, O, steps, coeffs, eps, alpha, beta, out_dtype, workspace))
     if O is None:
         if beta != 0.0:
             raise ValueError("beta needs O")
-        O = torch.empty(G.shape, dtype=out_dtype or torch.bfloat16, device=device)
+        O = torch.empty(G.shape, dtype=out_dtype or torch.bfloat16, device=G.device)
     elif out_dtype is not None and O.dtype != out_dtype:
         raise ValueError("O has another dtype than out_dtype")
     if O.shape != G.shape:
@@ -83,11 +86,9 @@ def orthogonalize(G, O=None, steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7
         # one matrix shared by the whole batch: the ABI's 0 means packed
         g3 = g3.contiguous()
         ldg, sg = _lines(g3, "G")
-    with torch.cuda.device(device):
-        need = orthogonalize_workspace_size(m, n, batch)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        orthogonalize_raw(m, n, batch, g3.data_ptr(), ldg, sg, codes[G.dtype], o3.data_ptr(), ldo, so, codes[O.dtype],
-                          steps, coeffs, eps, alpha, beta, workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), _current(device))
+    if workspace is None:
+        workspace = torch.empty(orthogonalize_workspace_size(m, n, batch), dtype=torch.uint8, device=G.device)
+    orthogonalize_raw(m, n, batch, g3.data_ptr(), ldg, sg, codes[G.dtype], o3.data_ptr(), ldo, so, codes[O.dtype],
+                      steps, coeffs, eps, alpha, beta, workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size(), _raw_stream()(index))
     return O
