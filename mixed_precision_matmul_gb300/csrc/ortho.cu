@@ -121,63 +121,79 @@ __device__ __forceinline__ void read_batch(ChunkWalk& at, const XT* g, int64_t l
   }
 }
 
+// Squares of 8 elements whose sum fp32 cannot hold safely, in 64 bits.  (Kept
+// out of line: 64-bit arithmetic is very slow here, and inlined it was done for
+// every element and discarded.)
+__device__ __noinline__ void add_wide(double* wide, const float (&v)[8]) {
+  double s = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) s += (double)v[j] * (double)v[j];
+  *wide += s;
+}
+
 // partial[b][block] = sum of squares over the block's share of matrix b.  The
 // squares of 8 elements are added in fp32 where that is safe (the sum neither
-// near overflow nor near underflow) and in 64 bits elsewhere; a thread's sum
-// of such groups in fp32, the rest in 64 bits, always in the same order.
+// near overflow nor near underflow) and in 64 bits elsewhere; so are the
+// threads' sums, always in the same order.
 template <class XT>
 __global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_constant__ OrthoScaleParams p) {
   __shared__ float red[kScaleThreads / 32];
-  __shared__ double red_wide[kScaleThreads / 32];
-  if (threadIdx.x < kScaleThreads / 32) red_wide[threadIdx.x] = 0.0;
+  __shared__ double red_wide[kScaleThreads];
+  red_wide[threadIdx.x] = 0.0;
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.y;
   const XT* g = reinterpret_cast<const XT*>(p.g) + (int64_t)b * p.stride_g;
   ChunkWalk at((p.cols + 7) / 8, p.rows);
   float sum = 0.0f;
-  double wide = 0.0;
+  bool unsafe = false;
   while (at.inside()) {
     float v[kBatch][8];
     read_batch<XT>(at, g, p.ldg, p.cols, p.g_vec != 0, v);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      float s = 0.0f;
+      float s = 0.0f, any = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(v[u][j], v[u][j], s);
-      if (s >= 1e-30f && s <= 1e30f) {
+      for (int j = 0; j < 8; ++j) {
+        s = fmaf(v[u][j], v[u][j], s);
+        any = fmaxf(any, fabsf(v[u][j]));
+      }
+      if ((s >= 1e-30f && s <= 1e30f) || (s == 0.0f && any == 0.0f)) {
         sum += s;
-        if (sum > 1e30f) { wide += (double)sum; sum = 0.0f; }
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (v[u][j] != 0.0f) wide += (double)v[u][j] * (double)v[u][j];
+        unsafe = true;
+        add_wide(&red_wide[threadIdx.x], v[u]);
       }
     }
+    if (sum > 1e30f) {
+      unsafe = true;
+      const float v[8] = {sqrtf(sum)};   // a square root and its square: half a step of fp32 each
+      add_wide(&red_wide[threadIdx.x], v);
+      sum = 0.0f;
+    }
   }
-  // 64-bit arithmetic is slow here (reducing every thread's sum in 64 bits
-  // took four times as long as reading a 4096^2 matrix): the safe sums are
-  // reduced in fp32, the others only where there are any
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) red[warp] = sum;
-  if (__syncthreads_or(wide != 0.0)) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
-    if ((threadIdx.x & 31) == 0) red_wide[warp] = wide;
-    __syncthreads();
-  }
+  const bool wide = __syncthreads_or(unsafe) != 0;
   if (threadIdx.x == 0) {
-    double s = 0.0;
+    float f = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kScaleThreads / 32; ++w) s += (double)red[w] + red_wide[w];
+    for (int w = 0; w < kScaleThreads / 32; ++w) f += red[w];
+    double s = (double)f;
+    if (wide) {
+#pragma unroll 1
+      for (int i = 0; i < kScaleThreads; ++i) s += red_wide[i];
+    }
     p.partial[(int64_t)b * kOrthoNormBlocks + blockIdx.x] = s;
   }
 }
 
-// x = fp16(g * 2^e) with the power of two that brings the norm to [target,
-// 2 target), and factor = 2^-e / (norm + eps).
+// x = fp16(g * 2^e) with the power of two that brings the norm to [2^t, 2^(t+1))
+// (t: target_exp), and factor = 2^-e / (norm + eps).  Every block works them
+// out from the partial sums: a few additions in 64 bits, the rest on the
+// sum's exponent and fraction.
 template <class XT>
 __global__ void __launch_bounds__(kScaleThreads) ortho_scale_kernel(const __grid_constant__ OrthoScaleParams p) {
   __shared__ float scale_sh;
@@ -190,17 +206,24 @@ __global__ void __launch_bounds__(kScaleThreads) ortho_scale_kernel(const __grid
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (threadIdx.x == 0) {
-      const double norm = sqrt(s);
-      int e = 0;
-      if (norm > 0.0 && norm < 1e300) {
-        e = ilogb((double)p.target) - ilogb(norm);
-        if (scalbn(norm, e) < (double)p.target) ++e;
+      const uint32_t hi = (uint32_t)__double2hiint(s);
+      const int exponent = (int)(hi >> 20) - 1023;               // s = fraction * 2^exponent
+      float scale = 1.0f, factor;
+      if (hi == 0u || exponent == 1024) {
+        // zero, infinite or NaN
+        factor = 1.0f / (hi == 0u ? p.eps : __uint_as_float(0x7F800000u | (hi & 0xFFFFFu)));
+      } else {
+        const float fraction = __uint_as_float(0x3F800000u | ((hi & 0xFFFFFu) << 3) | ((uint32_t)__double2loint(s) >> 29));
+        // norm = root * 2^half, root in [1, 2)
+        const int half = exponent >> 1;
+        const float root = sqrtf((exponent & 1) ? 2.0f * fraction : fraction);
+        // one factor of fp32 carries the tiniest norms of fp32 inputs only part of the way
+        const int e = min(max(p.target_exp - half, -126), 127);
+        scale = scalbnf(1.0f, e);
+        factor = 1.0f / (scalbnf(root, half + e) + scalbnf(p.eps, e));
       }
-      // fp32 inputs below 2^-126 in norm reach the target only as far as a
-      // single factor of fp32 carries them
-      e = min(max(e, -126), 127);
-      scale_sh = scalbnf(1.0f, e);
-      if (blockIdx.x == 0) p.factor[b] = (float)(scalbn(1.0, -e) / (norm + (double)p.eps));
+      scale_sh = scale;
+      if (blockIdx.x == 0) p.factor[b] = factor;
     }
   }
   __syncthreads();

@@ -22,7 +22,7 @@ struct OrthoScaleParams {
   uint16_t* x;                // fp16 [batch][rows][ldx], ldx % 8 == 0
   int64_t ldx;
   float* factor;              // [batch]: normalised matrix = factor * x
-  float target;               // x is scaled by a power of two to a norm in [target, 2 target)
+  int32_t target_exp;         // x is scaled by a power of two to a norm in [2^t, 2^(t+1))
   float eps;
 };
 cudaError_t launch_ortho_scale(const OrthoScaleParams& p, int g_dtype, cudaStream_t stream);

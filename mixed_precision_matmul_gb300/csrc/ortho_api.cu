@@ -161,9 +161,9 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
   sp.x = reinterpret_cast<uint16_t*>(ws + l.x[0]);
   sp.ldx = l.ldx;
   sp.factor = factor;
-  // a norm of sqrt(m n) gives entries near 1; at most 2^14, so that even a
+  // a norm near sqrt(m n) gives entries near 1; below 2^15, so that even a
   // single entry that holds the whole norm stays within fp16
-  sp.target = (float)std::min(std::sqrt((double)m * (double)n), 16384.0);
+  sp.target_exp = std::min((int)std::floor(0.5 * std::log2((double)m * (double)n)), 14);
   sp.eps = eps;
   // two loads in flight per thread at least, at most enough blocks to fill the machine
   const int64_t chunks = m * (l.ldx / 8);
