@@ -451,9 +451,10 @@ mpg_status mpg_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t l
  * alpha == 0: C = beta*C and the operands are not read.
  *   opt   NULL = defaults.  Read are c_dtype, wait_timeout_ns, splitk (the
  *         ranges that k is divided into, each on a CTA of one cluster: 0 =
- *         the library's choice, else 1 .. 8) and tile_n (0 = the library's
+ *         the library's choice, else 1 .. 8), tile_n (0 = the library's
  *         choice; 128: tiles of 128 x 128; 16, 32, 64: tiles of that many rows
- *         of A by 128 rows of B, for few rows of A).
+ *         of A by 128 rows of B, for few rows of A) and cta_pair (1: tiles of
+ *         256 x 256 on pairs of CTAs, 0: the library's choice, -1: never).
  * Data pointers that are not 16-byte aligned or whose ld is no multiple of 16
  * are copied to aligned lines in the workspace first
  * (mpg_gemm_fp8_workspace_size bytes, else 0; MPG_ERR_WORKSPACE without it).

@@ -40,6 +40,7 @@ SOURCES = [
     "fp8_api.cu",
     "fp8_quant.cu",
     "fp8_gemm.cu",
+    "fp8_pair.cu",
     "ortho_api.cu",
     "ortho.cu",
 ]

@@ -47,6 +47,41 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same without ordering of ordinary memory accesses, for hand-overs of
+// TMEM alone: tcgen05.fence orders those around it.  (A release or a fence at
+// cluster scope waits for the thread's outstanding accesses, hundreds of
+// cycles; it dominated a loop with one hand-over per 512 cycles of MMAs.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_test_relaxed(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_relaxed(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
+  if (mbar_test_relaxed(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_test_relaxed(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*c.abort) return false;
+      const uint64_t t = global_timer_ns();
+      if (it == 64) t0 = t;
+      if (t - t0 > c.limit_ns || it > (1u << 30)) {
+        raise_abort(c, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // 3-D tiled load into this CTA's shared memory; completion is signalled on
 // the barrier at `bar_cluster_addr`, which may sit in the peer CTA.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster_addr,

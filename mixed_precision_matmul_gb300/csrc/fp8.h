@@ -49,6 +49,7 @@ struct Fp8GemmParams {
   int64_t ld_out;
   int32_t out_dtype;
   int32_t out_vec;                      // 4-element vectors of C are aligned
+  int32_t out_vec16;                    // 16-byte chunks of C are aligned
   int32_t rows, cols;                   // extents of D
   int32_t num_r_blk, num_c_blk, num_k_blk;
   int32_t splits, kb_per_split;

@@ -57,12 +57,13 @@ Copies plan_copies(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand& A, co
 
 // The product's tile and its division along k.
 struct Fp8Plan {
+  bool pair = false;      // 256 x 256 tiles on CTA pairs
   bool swapped = false;
   int bn = 128;
   int splits = 1;
 };
 
-Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, int sm_count) {
+Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, int sm_count, int clusters) {
   Fp8Plan p;
   // Few tokens: the weights' rows fill the tensor core's 128 rows.
   p.swapped = m <= 64;
@@ -83,12 +84,26 @@ Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, int 
   s = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(s, 8), kb));
   const int64_t per = (kb + s - 1) / s;
   p.splits = (int)((kb + per - 1) / per);
+  // A 128 x 128 tile of one CTA keeps its SM's shared memory busy for a block
+  // of k as long as a pair's 256 x 256 tile does (a copy in and a read of 32
+  // KB either way), so the form with fewer rounds of blocks wins.
+  const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  const int64_t pair_rounds = (pair_tiles + clusters - 1) / clusters * kb;
+  const int64_t rounds = (tiles * p.splits + sm_count - 1) / sm_count * per;
+  if (o.cta_pair == 1 || (o.cta_pair == 0 && o.tile_n == 0 && o.splitk == 0 && !p.swapped && pair_rounds < rounds)) {
+    p.pair = true;
+    p.swapped = false;
+    p.splits = 1;
+  }
   return p;
 }
 
 mpg_status check_options(const mpg_options& o) {
   if (o.tile_n != 0 && o.tile_n != 16 && o.tile_n != 32 && o.tile_n != 64 && o.tile_n != 128)
     return fail(MPG_ERR_INVALID_ARG, "tile_n %d: 0, 16, 32, 64 or 128 for 8-bit operands", o.tile_n);
+  if (o.cta_pair < -1 || o.cta_pair > 1) return fail(MPG_ERR_INVALID_ARG, "cta_pair %d outside [-1, 1]", o.cta_pair);
+  if (o.cta_pair == 1 && (o.tile_n != 0 || o.splitk > 1))
+    return fail(MPG_ERR_INVALID_ARG, "cta_pair 1 has 256 x 256 tiles and one range of k");
   if (o.splitk < 0 || o.splitk > 8) return fail(MPG_ERR_INVALID_ARG, "splitk %d outside [0, 8]", o.splitk);
   if (o.c_dtype < 0 || o.c_dtype > 2) return fail(MPG_ERR_INVALID_ARG, "unknown c_dtype %d", o.c_dtype);
   if (o.wait_timeout_ns < 0) return fail(MPG_ERR_INVALID_ARG, "negative wait_timeout_ns");
@@ -98,21 +113,27 @@ mpg_status check_options(const mpg_options& o) {
 mpg_status launch_product(DeviceInfo* dev, int64_t m, int64_t n, int64_t k, const mpg_fp8_operand& A,
                           const mpg_fp8_operand& B, void* C, int64_t ldc, float alpha, float beta,
                           const mpg_options& o, cudaStream_t stream) {
-  const Fp8Plan plan = plan_product(m, n, k, o, dev->sm_count);
+  Fp8Kernel kern;
+  fp8_lookup_pair(B.scale_rows == 1, &kern);
+  int clusters = 0;
+  mpg_status s = resident_clusters(dev, kern.fn, kern.block, kern.smem_bytes, 2, &clusters);
+  if (s != MPG_OK) return s;
+  const Fp8Plan plan = plan_product(m, n, k, o, dev->sm_count, clusters);
   const mpg_fp8_operand& R = plan.swapped ? B : A;
   const mpg_fp8_operand& S = plan.swapped ? A : B;
-  Fp8Kernel kern;
-  if (!fp8_lookup(plan.bn, plan.swapped, plan.swapped || S.scale_rows == 1, &kern))
-    return fail(MPG_ERR_UNSUPPORTED, "no 8-bit kernel for tile_n %d", plan.bn);
-  mpg_status s = allow_smem(dev, kern.fn, kern.smem_bytes);
-  if (s != MPG_OK) return s;
+  if (!plan.pair) {
+    if (!fp8_lookup(plan.bn, plan.swapped, plan.swapped || S.scale_rows == 1, &kern))
+      return fail(MPG_ERR_UNSUPPORTED, "no 8-bit kernel for tile_n %d", plan.bn);
+    if ((s = allow_smem(dev, kern.fn, kern.smem_bytes)) != MPG_OK) return s;
+  }
   Fp8GemmParams p;
   std::memset(&p, 0, sizeof(p));
   p.rows = (int32_t)(plan.swapped ? n : m);
   p.cols = (int32_t)(plan.swapped ? m : n);
-  s = encode_map_bytes(&p.map_r, R.data, R.ld, k, p.rows, kFp8Block, kern.tile_rows);
+  // (each CTA of a pair holds half of the tile's rows and half of its columns)
+  s = encode_map_bytes(&p.map_r, R.data, R.ld, k, p.rows, kFp8Block, kern.tile_rows / (plan.pair ? 2 : 1));
   if (s != MPG_OK) return s;
-  s = encode_map_bytes(&p.map_c, S.data, S.ld, k, p.cols, kFp8Block, kern.tile_cols);
+  s = encode_map_bytes(&p.map_c, S.data, S.ld, k, p.cols, kFp8Block, kern.tile_cols / (plan.pair ? 2 : 1));
   if (s != MPG_OK) return s;
   p.sr = R.scale;
   p.sr_row = R.scale_row_stride;
@@ -126,6 +147,7 @@ mpg_status launch_product(DeviceInfo* dev, int64_t m, int64_t n, int64_t k, cons
   p.ld_out = ldc;
   p.out_dtype = o.c_dtype;
   p.out_vec = aligned(C, o.c_dtype == MPG_F32 ? 16 : 8) && ldc % 4 == 0;
+  p.out_vec16 = aligned(C, 16) && (ldc * elem_bytes((mpg_dtype)o.c_dtype)) % 16 == 0;
   p.num_r_blk = (p.rows + kern.tile_rows - 1) / kern.tile_rows;
   p.num_c_blk = (p.cols + kern.tile_cols - 1) / kern.tile_cols;
   p.num_k_blk = (int32_t)blocks_of(k);
@@ -136,15 +158,18 @@ mpg_status launch_product(DeviceInfo* dev, int64_t m, int64_t n, int64_t k, cons
   p.beta = beta;
   p.status = dev->status;
   p.wait_limit_ns = o.wait_timeout_ns ? (uint64_t)o.wait_timeout_ns : kDefaultWaitNs;
-  const int64_t ctas = (int64_t)p.num_r_blk * p.num_c_blk * p.splits;
-  if (ctas > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
+  const int64_t tiles = (int64_t)p.num_r_blk * p.num_c_blk;
+  if (tiles * p.splits > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
+  p.num_tiles = (int32_t)tiles;
+  p.group = 8;
+  const int64_t ctas = plan.pair ? 2 * std::min<int64_t>(tiles, clusters) : tiles * p.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3((unsigned)kern.block);
   cfg.dynamicSmemBytes = (size_t)kern.smem_bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  cfg.numAttrs = (unsigned)launch_attributes(attr, p.splits);
+  cfg.numAttrs = (unsigned)launch_attributes(attr, plan.pair ? 2 : p.splits);
   cfg.attrs = attr;
   void* args[] = {&p};
   cudaError_t e = cudaLaunchKernelExC(&cfg, kern.fn, args);

@@ -156,45 +156,35 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_gemm_kernel(const __grid_c
     const int wc0 = (ew / 4) * T::kCols;                  // this warp's first column in the tile
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + wc0;
     typename T::Ring ring;
-    ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row0 + 32 * q, col0 + wc0, kb0);
+    ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row0 + 32 * q, col0 + wc0, kb0, nkb);
+    f32x2 acc[T::kCols / 2];
 #pragma unroll
-    for (int i = 0; i < T::Ring::kDepth - 1; ++i) ring.fetch(i, nkb);
-    float acc[T::kCols];
-#pragma unroll
-    for (int j = 0; j < T::kCols; ++j) acc[j] = 0.0f;
-    constexpr int kChunk = T::kCols >= 32 ? 32 : 16;
+    for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
 #pragma unroll 1
     for (int i = 0; i < nkb; ++i) {
       const int ab = i % T::kAccBufs;
+      __syncwarp();                                      // every lane is done with block i - 1's slot
+      ring.fetch(i + T::Ring::kDepth - 1);
+      cp_async_wait<T::Ring::kDepth - 1>();
       if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
       tc_fence_after_sync();
-      // (the warp has converged here: block i - 1's slot may be refilled)
-      ring.fetch(i + T::Ring::kDepth - 1, nkb);
-      cp_async_wait<T::Ring::kDepth - 1>();
-      __syncwarp();
-      const uint32_t slot = ring.slot(i);
-      const float rs = ld_shared_f32(slot + lane * 4);
-      const float rcs = T::kColVec ? 0.0f : rs * ld_shared_f32(slot + 128 + lane * 4);
-#pragma unroll
-      for (int c = 0; c < T::kCols; c += kChunk) {
-        float v[kChunk];
-        if constexpr (kChunk == 32) tmem_ld_32cols(tacc + ab * T::kAccStride + c, v);
-        else tmem_ld_16cols(tacc + ab * T::kAccStride + c, v);
-        tmem_ld_wait();
-        if (c + kChunk == T::kCols) {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[ab]);
-        }
-        scale_add<kChunk, T::kColVec>(acc + c, v, slot, c, rs, rcs);
-      }
+      add_block<T::kCols, T::kColVec>(acc, tacc + ab * T::kAccStride, ring.slot(i), lane, [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      });
     }
     cp_async_wait<0>();
     if (ok) {
       // every MMA of this CTA is complete: the operand stages are free
       const uint32_t dst = op_smem + ((uint32_t)(32 * q + lane) * T::kPitch + wc0) * 4u;
 #pragma unroll
-      for (int j = 0; j < T::kCols; ++j) st_shared_f32(dst + j * 4, acc[j]);
+      for (int j = 0; j < T::kCols; j += 2) {
+        float lo, hi;
+        unpack2(acc[j / 2], lo, hi);
+        st_shared_f32(dst + j * 4, lo);
+        st_shared_f32(dst + j * 4 + 4, hi);
+      }
     }
   }
 

@@ -1,0 +1,413 @@
+// The block-scaled 8-bit product on pairs of CTAs (sm_103a, cta_group::2): a
+// persistent cluster of two CTAs computes 256 x 256 tiles of D.
+//
+// Each CTA holds 128 rows of the tile's R panel and 128 lines of its C panel
+// for a block of 128 k.  Four M = 256, N = 256, K = 32 instructions leave the
+// block's product in one of two TMEM buffers (256 columns each), and eight
+// epilogue warps in each CTA (32 rows x 128 columns a warp, 128 running sums a
+// thread, in registers for the whole k range) add it under its scales while
+// the tensor cores fill the other buffer.  A warp of its own fetches the
+// scales, eight blocks ahead.
+//
+// A block's products take the tensor cores 512 cycles (about 620 here: the
+// operands' way in and out of shared memory).  The epilogue has to keep up:
+// 64 packed multiply-adds a warp (128 and 32 loads with a scale for each
+// column), four reads of TMEM and the hand-overs, two warps to a scheduler.
+// It is bound by latencies, so everything that is not one of these is on other
+// warps, and reads overlap additions.
+#include "fp8_tc.cuh"
+#include "staging.cuh"
+
+namespace mpg {
+namespace {
+
+template <bool kColVec_>
+struct Fp8PairTraits {
+  static constexpr bool kColVec = kColVec_;
+  static constexpr int BM = 128;                    // rows of R and lines of C held by one CTA
+  static constexpr int kTile = 256;
+  static constexpr int kRTile = BM * kFp8RowBytes;
+  static constexpr int kStage = 2 * kRTile;
+  static constexpr int kStages = 6;
+  static constexpr int kAccBufs = 2;
+  static constexpr int kTmemCols = kAccBufs * kTile;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kCols = kTile / (kEpiWarps / 4);
+  static constexpr int kThreads = (4 + kEpiWarps) * 32;
+  // Registers: the block is launched with 168 a thread; the first warpgroup
+  // (producer, MMA, two for column scales) gives up all but 40, the two of the
+  // epilogue take 232: 128 running sums, 64 columns on their way.
+  static constexpr int kLaunchRegs = 168, kIdleRegs = 40, kEpiRegs = 232;
+  static_assert(128 * kIdleRegs + kEpiWarps * 32 * kEpiRegs <= kThreads * kLaunchRegs, "register split");
+  // Scales of the tile's columns, by blocks of k (two warps of their own fetch them).
+  static constexpr int kScaleSlots = kColVec ? 8 : 0;
+  static constexpr int kScaleSlot = kTile;
+  static constexpr int kScaleBytes = (kScaleSlots * kScaleSlot * 4 + 15) / 16 * 16;
+  static constexpr int kEpiBytes = kEpiWarps * 2048;
+  static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 2 * kScaleSlots + 1;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiBytes + kScaleBytes + kNumBars * 8 + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+struct PairTile {
+  int rb, cb;
+};
+__device__ __forceinline__ PairTile pair_tile(const Fp8GemmParams& p, int t) {
+  // groups of tile rows, walked column by column, every other group backwards
+  const int per = p.group * p.num_c_blk;
+  const int g = t / per;
+  const int first = g * p.group;
+  const int gm = min(p.group, p.num_r_blk - first);
+  const int within = t - g * per;
+  PairTile c;
+  c.rb = first + within % gm;
+  c.cb = within / gm;
+  if (g & 1) c.cb = p.num_c_blk - 1 - c.cb;
+  return c;
+}
+
+// alpha x + beta C for 32 rows (one a lane) and 32 columns.  Rows pass through
+// 64-byte lines of shared memory (32 16-bit values, or 16 fp32 values twice),
+// chunk c of row r at slot c ^ ((r / 2) & 3): writes (a row a lane) and reads
+// (four lanes a row) reach all banks.  Each store then covers 8 rows x 64 bytes.
+__device__ __forceinline__ void store_rows32(const Fp8GemmParams& p, uint32_t stg, int lane, const float (&x)[32],
+                                             int row_base, int col_base) {
+  const uint32_t wr = stg + lane * 64, wsw = (lane >> 1) & 3;
+  const int dt = p.out_dtype;
+  if (dt != kOutF32 && p.beta == 0.0f && p.out_vec16 && col_base + 32 <= p.cols) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      w[j] = dt == kOutF16 ? pack_f16x2(p.alpha * x[2 * j], p.alpha * x[2 * j + 1])
+                           : pack_bf16x2(p.alpha * x[2 * j], p.alpha * x[2 * j + 1]);
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c) st_shared_v4(wr + ((c ^ wsw) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), c = lane & 3;
+      const float4 y = stage_ld16(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+      if (row_base + r < p.rows)
+        *reinterpret_cast<float4*>(static_cast<uint16_t*>(p.out) + (int64_t)(row_base + r) * p.ld_out + col_base + c * 8) = y;
+    }
+    __syncwarp();
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      stage_st16(wr + ((c ^ wsw) << 4), x[16 * h + 4 * c], x[16 * h + 4 * c + 1], x[16 * h + 4 * c + 2], x[16 * h + 4 * c + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), c = lane & 3;
+      const float4 y = stage_ld16(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+      const int row = row_base + r, col = col_base + 16 * h + 4 * c;
+      if (row >= p.rows) continue;
+      const int64_t idx = (int64_t)row * p.ld_out + col;
+      if (p.out_vec && col + 4 <= p.cols) {
+        float4 o = make_float4(p.alpha * y.x, p.alpha * y.y, p.alpha * y.z, p.alpha * y.w);
+        if (p.beta != 0.0f) {
+          const float4 z = out_load4(p.out, idx, dt);
+          o.x = fmaf(p.beta, z.x, o.x);
+          o.y = fmaf(p.beta, z.y, o.y);
+          o.z = fmaf(p.beta, z.z, o.z);
+          o.w = fmaf(p.beta, z.w, o.w);
+        }
+        out_store4(p.out, idx, o, dt);
+      } else {
+        const float e[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col + j < p.cols)
+            out_store(p.out, idx + j, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx + j, dt), p.alpha * e[j]) : p.alpha * e[j], dt);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_constant__ Fp8GemmParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* epi_base = smem + T::kStages * T::kStage;
+  uint8_t* scale_base = epi_base + T::kEpiBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scale_base + T::kScaleBytes);
+  uint64_t* op_full = bars;                         // rank 0: both CTAs' halves of a stage landed
+  uint64_t* op_empty = bars + T::kStages;           // each CTA: the pair's MMAs consumed the stage
+  uint64_t* acc_full = bars + 2 * T::kStages;       // each CTA: a block's product is complete
+  uint64_t* acc_empty = acc_full + T::kAccBufs;     // rank 0: both CTAs' epilogues read it
+  uint64_t* scale_full = acc_empty + T::kAccBufs;   // a block's scales are in their slot
+  uint64_t* scale_empty = scale_full + T::kScaleSlots;
+  uint64_t* done_bar = scale_empty + T::kScaleSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int worker = (int)cluster_id_x(), workers = (int)num_clusters_x();
+  const int nkb = p.num_k_blk;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::kStages; ++i) {
+      mbar_init(&op_full[i], 1);
+      mbar_init(&op_empty[i], 1);
+    }
+    for (int i = 0; i < T::kAccBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * T::kEpiWarps);
+    }
+    for (int i = 0; i < T::kScaleSlots; ++i) {
+      mbar_init(&scale_full[i], 64);                // the copies of each lane of the two scale warps
+      mbar_init(&scale_empty[i], T::kEpiWarps);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&p.map_r);
+    tma_prefetch_map(&p.map_c);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, T::kTmemCols);
+    tmem_relinquish_pair();
+    tc_fence_before_sync();
+  }
+  cluster_sync_all();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  WaitCtl ctl;
+  ctl.abort = abort_flag;
+  ctl.peer_abort = cluster_generic_ptr(const_cast<int*>(abort_flag), rank ^ 1u);
+  ctl.status = p.status;
+  ctl.limit_ns = p.wait_limit_ns;
+  const uint32_t op_smem = smem_addr(smem);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T::kIdleRegs));
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint32_t full0 = cluster_smem_addr(smem_addr(op_full), 0);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = worker; t < p.num_tiles && ok; t += workers) {
+        const PairTile tc = pair_tile(p, t);
+        const int rrow = tc.rb * T::kTile + (int)rank * T::BM;
+        const int crow = tc.cb * T::kTile + (int)rank * T::BM;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const uint32_t st = it % T::kStages;
+          if (!mbar_wait(&op_empty[st], ((it / T::kStages) & 1u) ^ 1u, ctl)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&op_full[st], 2 * T::kStage);
+          uint8_t* dst = smem + st * T::kStage;
+          tma_load_3d_pair(dst, &p.map_r, full0 + st * 8u, kb * kFp8Block, rrow, 0);
+          tma_load_3d_pair(dst + T::kRTile, &p.map_c, full0 + st * 8u, kb * kFp8Block, crow, 0);
+        }
+      }
+      // a stage is released after its copies landed and were read
+      const uint32_t n_drain = it < (uint32_t)T::kStages ? it : (uint32_t)T::kStages;
+      for (uint32_t i = it - n_drain; i < it; ++i)
+        drain_wait(&op_empty[i % T::kStages], (i / T::kStages) & 1u, p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (rank 0)
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = make_idesc(0u, false, false, T::kTile, T::kTile) | p.fmt_bits;
+      // the start address sits in the descriptor's low bits, in units of 16 bytes
+      const uint64_t r_desc = fp8_desc(op_smem, 0), c_desc = fp8_desc(op_smem + T::kRTile, 0);
+      uint32_t it = 0, st = 0, st_ph = 0;
+      bool ok = true;
+      for (int t = worker; t < p.num_tiles && ok; t += workers) {
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const uint32_t ab = it % T::kAccBufs;
+          if (!mbar_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
+          if (!mbar_wait_relaxed(&acc_empty[ab], ((it / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
+          tc_fence_after_sync();
+          const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f8_pair(tmem_base + ab * T::kTile, r_desc + at + 2 * ks, c_desc + at + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+          mma_commit_multicast(&acc_full[ab], 0x3);
+          mma_commit_multicast(&op_empty[st], 0x3);
+          if (++st == T::kStages) {
+            st = 0;
+            st_ph ^= 1u;
+          }
+        }
+      }
+      mma_commit_multicast(done_bar, 0x1);
+      drain_wait(done_bar, 0, p.wait_limit_ns);
+    }
+  } else if (T::kColVec) {
+    // ------------------------------------------------------------ column scales
+    uint32_t slot = 0, ph = 0;
+    bool ok = true;
+    for (int t = worker; t < p.num_tiles && ok; t += workers) {
+      const PairTile tc = pair_tile(p, t);
+      // this lane's columns (clamped to the operand's last line)
+      const int c0 = (warp - 2) * T::kCols + lane;
+      const float* src[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        src[i] = p.sc + (int64_t)(min(tc.cb * T::kTile + c0 + 32 * i, p.cols - 1) >> p.sc_shift) * p.sc_row;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!warp_wait(&scale_empty[slot], ph ^ 1u, ctl)) { ok = false; break; }
+        const uint32_t dst = smem_addr(scale_base) + (slot * T::kScaleSlot + c0) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cp_async4(dst + i * 128, src[i]);
+          src[i] += p.sc_k;
+        }
+        cp_async_arrive(&scale_full[slot]);
+        if (++slot == T::kScaleSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    cp_async_wait_all();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T::kEpiRegs));
+    // ------------------------------------------------------------ running sums
+    const int q = warp & 3;
+    const int ew = warp - 4;
+    const uint32_t half = (uint32_t)(ew / 4);
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + half * T::kCols;
+    const uint32_t stg = smem_addr(epi_base) + ew * 2048;
+    const uint32_t scales = smem_addr(scale_base);
+    const uint32_t acc_empty0 = cluster_smem_addr(smem_addr(acc_empty), 0);
+    constexpr int kN = T::kCols / 32;
+    uint32_t it = 0, slot = 0, slot_ph = 0;
+    bool ok = true;
+    for (int t = worker; t < p.num_tiles && ok; t += workers) {
+      const PairTile tc = pair_tile(p, t);
+      const int row_base = tc.rb * T::kTile + (int)rank * T::BM + 32 * q;
+      const int col_first = tc.cb * T::kTile + (int)half * T::kCols;
+      f32x2 acc[T::kCols / 2];
+#pragma unroll
+      for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
+      // This lane's row scale, and the scale of this half's columns, go from
+      // global memory straight into registers, three blocks ahead.
+      const float* row_src =
+          p.sr + (int64_t)(min(row_base + lane, p.rows - 1) >> p.sr_shift) * p.sr_row;
+      const float* col_src = p.sc + (int64_t)(min(col_first, p.cols - 1) >> p.sc_shift) * p.sc_row;
+      float rsc[4], csc[4];
+      int fetched = 0;
+      auto fetch_scales = [&](int i) {
+        if (fetched < nkb) {
+          rsc[i] = __ldg(row_src);
+          row_src += p.sr_k;
+          if (!T::kColVec) {
+            csc[i] = __ldg(col_src);
+            col_src += p.sc_k;
+          }
+          ++fetched;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        rsc[i] = csc[i] = 0.0f;
+        if (i < 3) fetch_scales(i);
+      }
+      // Columns are read 32 at a time, the next 32 on their way while the last
+      // are added, across the blocks of k too: the wait for the next block's
+      // product and its first read go before the last additions of this one.
+      float v[2][32];
+      if (!warp_wait(&acc_full[it % T::kAccBufs], (it / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
+      tc_fence_after_sync();
+      tmem_ld_32cols(tacc + (it % T::kAccBufs) * T::kTile, v[0]);
+#pragma unroll 1
+      for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
+        const uint32_t ab = it % T::kAccBufs, nx = (it + 1) % T::kAccBufs;
+        const uint32_t nx_ph = ((it + 1) / T::kAccBufs) & 1u;
+        fetch_scales(3);
+        const float s = T::kColVec ? rsc[0] : rsc[0] * csc[0];
+        const f32x2 rs = pack2(s, s);
+        uint32_t sl = 0;
+        if constexpr (T::kColVec) {
+          if (!warp_wait(&scale_full[slot], slot_ph, ctl)) { ok = false; break; }
+          sl = scales + slot * (T::kScaleSlot * 4) + half * (T::kCols * 4) - 128;
+        }
+        bool ready = false;
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          tmem_ld_wait();
+          if (c + 1 < kN) {
+            tmem_ld_32cols(tacc + ab * T::kTile + (c + 1) * 32, v[(c + 1) & 1]);
+            // the barrier's answer takes a while (shared memory is busy with
+            // operands), so it is asked for early
+            if (c + 2 == kN && kb + 1 < nkb) ready = mbar_test(&acc_full[nx], nx_ph);
+          } else {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + ab * 8u);
+            if (kb + 1 < nkb) {
+              if (!__all_sync(0xffffffffu, ready) && !warp_wait(&acc_full[nx], nx_ph, ctl)) { ok = false; break; }
+              tc_fence_after_sync();
+              tmem_ld_32cols(tacc + nx * T::kTile, v[(c + 1) & 1]);
+            }
+          }
+          scale_add<32, T::kColVec>(acc + c * 16, v[c & 1], sl, c * 32, rs);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          rsc[i] = rsc[i + 1];
+          csc[i] = csc[i + 1];
+        }
+        if constexpr (T::kColVec) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scale_empty[slot]);
+          if (++slot == T::kScaleSlots) {
+            slot = 0;
+            slot_ph ^= 1u;
+          }
+        }
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- C
+      if (row_base >= p.rows) continue;
+#pragma unroll
+      for (int cc = 0; cc < kN; ++cc) {
+        const int col_base = col_first + cc * 32;
+        if (col_base >= p.cols) continue;
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) unpack2(acc[cc * 16 + j], x[2 * j], x[2 * j + 1]);
+        store_rows32(p, stg, lane, x, row_base, col_base);
+      }
+    }
+  }
+
+  // neither CTA leaves while the other may address its shared memory
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, T::kTmemCols);
+  }
+}
+
+template <class T>
+bool fill(Fp8Kernel* out) {
+  out->fn = reinterpret_cast<const void*>(&fp8_pair_kernel<T>);
+  out->block = T::kThreads;
+  out->smem_bytes = T::kSmemBytes;
+  out->tile_rows = T::kTile;
+  out->tile_cols = T::kTile;
+  return true;
+}
+
+}  // namespace
+
+bool fp8_lookup_pair(bool col_vec, Fp8Kernel* out) {
+  return col_vec ? fill<Fp8PairTraits<true>>(out) : fill<Fp8PairTraits<false>>(out);
+}
+
+}  // namespace mpg

@@ -45,6 +45,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// One arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -59,25 +64,29 @@ __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// acc += x * y on two packed fp32 values (each a round-to-nearest fma).
-__device__ __forceinline__ void fma2(float& a0, float& a1, float x0, float x1, float y0, float y1) {
-  asm("{\n\t.reg .b64 a, x, y;\n\t"
-      "mov.b64 a, {%0, %1};\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %5};\n\t"
-      "fma.rn.f32x2 a, x, y, a;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+// Pairs of fp32 values in one 64-bit register, and their packed arithmetic
+// (each element rounded to nearest, as the scalar forms do).  Running sums are
+// kept in this form: built from single registers at each use they cost a move
+// an element.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-__device__ __forceinline__ void mul2(float& r0, float& r1, float x0, float x1, float y0, float y1) {
-  asm("{\n\t.reg .b64 r, x, y;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 r, x, y;\n\t"
-      "mov.b64 {%0, %1}, r;\n\t}"
-      : "=f"(r0), "=f"(r1)
-      : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+__device__ __forceinline__ void unpack2(f32x2 x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ void fma2(f32x2& a, f32x2 x, f32x2 y) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(x), "l"(y));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 x, f32x2 y) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ void ld_shared_pairs(uint32_t addr, f32x2& a, f32x2& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
 
 // The scales of one epilogue warp: its 32 rows and `kCols` columns (or the one
@@ -88,61 +97,97 @@ struct ScaleRing {
   static constexpr int kDepth = 8;
   static constexpr int kSlot = 32 + (kColVec ? kCols : 32);        // floats
   static constexpr int kBytes = kDepth * kSlot * 4;
+  static constexpr int kColLoads = kColVec ? (kCols + 31) / 32 : 1;
   uint32_t base;
-  const float* row_src;
-  const float* col_src[kColVec ? (kCols + 31) / 32 : 1];
+  const float* row_src;                  // the next block's to fetch
+  const float* col_src[kColLoads];
   int64_t row_k, col_k;
-  int lane;
+  int lane, left;                        // blocks still to fetch
 
   // rows row0 .. row0 + 31, columns col0 .. col0 + kCols - 1, clamped to the
-  // operands' last line; k-block kb0 is block 0 of this ring
-  __device__ __forceinline__ void start(const Fp8GemmParams& p, uint32_t smem, int lane_, int row0, int col0, int kb0) {
+  // operands' last line, of `n` blocks from k-block kb0 on; fetches the first
+  __device__ __forceinline__ void start(const Fp8GemmParams& p, uint32_t smem, int lane_, int row0, int col0, int kb0,
+                                        int n) {
     base = smem;
     lane = lane_;
+    left = n;
     row_k = p.sr_k;
     col_k = p.sc_k;
     const int r = min(row0 + lane, p.rows - 1) >> p.sr_shift;
     row_src = p.sr + (int64_t)r * p.sr_row + (int64_t)kb0 * p.sr_k;
 #pragma unroll
-    for (int i = 0; i < (kColVec ? (kCols + 31) / 32 : 1); ++i) {
+    for (int i = 0; i < kColLoads; ++i) {
       const int c = min(kColVec ? col0 + i * 32 + lane : col0, p.cols - 1) >> p.sc_shift;
       col_src[i] = p.sc + (int64_t)c * p.sc_row + (int64_t)kb0 * p.sc_k;
     }
-  }
-  __device__ __forceinline__ uint32_t slot(int i) const { return base + (uint32_t)(i % kDepth) * (kSlot * 4); }
-  __device__ __forceinline__ void fetch(int i, int n) const {
-    if (i < n) {
-      const uint32_t s = slot(i);
-      cp_async4(s + lane * 4, row_src + i * row_k);
-      if constexpr (kColVec) {
 #pragma unroll
-        for (int j = 0; j < (kCols + 31) / 32; ++j)
-          if (kCols % 32 == 0 || j * 32 + lane < kCols) cp_async4(s + 128 + (j * 32 + lane) * 4, col_src[j] + i * col_k);
-      } else {
-        cp_async4(s + 128 + lane * 4, col_src[0] + i * col_k);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i);
+  }
+  __device__ __forceinline__ uint32_t slot(uint32_t i) const { return base + (i % kDepth) * (kSlot * 4); }
+  // the next block's scales into slot i, if there is one
+  __device__ __forceinline__ void fetch(uint32_t i) {
+    if (left > 0) {
+      --left;
+      const uint32_t s = slot(i) + lane * 4;
+      cp_async4(s, row_src);
+      row_src += row_k;
+#pragma unroll
+      for (int j = 0; j < kColLoads; ++j) {
+        if (!kColVec || kCols % 32 == 0 || j * 32 + lane < kCols) cp_async4(s + 128 + j * 128, col_src[j]);
+        col_src[j] += col_k;
       }
     }
     cp_async_commit();
   }
 };
 
-// acc[j] += row scale * column scale * v[j] for `kN` columns from column
-// offset c0 of the warp's slot.
+// acc += row scale * column scale * v on kN columns from column c0 of the
+// warp's slot.
 template <int kN, bool kColVec>
-__device__ __forceinline__ void scale_add(float* acc, const float* v, uint32_t slot, int c0, float rs, float rcs) {
+__device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t slot, int c0, f32x2 rs) {
   if constexpr (kColVec) {
 #pragma unroll
     for (int j = 0; j < kN; j += 4) {
-      const float4 s = ld_shared_f4(slot + 128 + (c0 + j) * 4);
-      float x0, x1, x2, x3;
-      mul2(x0, x1, v[j], v[j + 1], s.x, s.y);
-      mul2(x2, x3, v[j + 2], v[j + 3], s.z, s.w);
-      fma2(acc[j], acc[j + 1], x0, x1, rs, rs);
-      fma2(acc[j + 2], acc[j + 3], x2, x3, rs, rs);
+      f32x2 s0, s1;
+      ld_shared_pairs(slot + 128 + (c0 + j) * 4, s0, s1);
+      fma2(acc[j / 2], mul2(pack2(v[j], v[j + 1]), s0), rs);
+      fma2(acc[j / 2 + 1], mul2(pack2(v[j + 2], v[j + 3]), s1), rs);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kN; j += 2) fma2(acc[j], acc[j + 1], v[j], v[j + 1], rcs, rcs);
+    for (int j = 0; j < kN; j += 2) fma2(acc[j / 2], pack2(v[j], v[j + 1]), rs);
+  }
+}
+
+// One block of k: the accumulator at `ta` (kCols columns of this warp's 32
+// lanes) added to the running sums under the scales in `slot`.  A tcgen05.ld
+// takes far longer to arrive than its columns take to add, so two loads of 32
+// columns are in flight.  `release` runs when all columns are in registers.
+template <int kCols, bool kColVec, class Release>
+__device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, uint32_t slot, int lane,
+                                          Release release) {
+  constexpr int kChunk = kCols >= 32 ? 32 : 16;
+  constexpr int kN = kCols / kChunk;
+  constexpr int kFly = kN > 1 ? 2 : 1;
+  float v[kFly][kChunk];
+  auto load = [&](int c) {
+    if constexpr (kChunk == 32) tmem_ld_32cols(ta + c * kChunk, v[c % kFly]);
+    else tmem_ld_16cols(ta + c * kChunk, v[c % kFly]);
+  };
+#pragma unroll
+  for (int c = 0; c < kFly; ++c) load(c);
+  float s = ld_shared_f32(slot + lane * 4);
+  if (!kColVec) s *= ld_shared_f32(slot + 128 + lane * 4);
+  const f32x2 rs = pack2(s, s);
+#pragma unroll
+  for (int c0 = 0; c0 < kN; c0 += kFly) {
+    tmem_ld_wait();
+    if (c0 + kFly >= kN) release();
+#pragma unroll
+    for (int c = c0; c < c0 + kFly; ++c) {
+      scale_add<kChunk, kColVec>(acc + c * kChunk / 2, v[c % kFly], slot, c * kChunk, rs);
+      if (c + kFly < kN) load(c + kFly);
+    }
   }
 }
 

@@ -74,12 +74,16 @@ __device__ __forceinline__ void raise_abort(const WaitCtl& c, uint32_t code) {
 // when another role of the CTA has already aborted.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
   if (mbar_test(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
+  // the clock starts at the 64th poll: reading %globaltimer takes far longer
+  // than most waits last
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_test(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (*c.abort) return false;
-      if (global_timer_ns() - t0 > c.limit_ns || it > (1u << 30)) {
+      const uint64_t t = global_timer_ns();
+      if (it == 64) t0 = t;
+      if (t - t0 > c.limit_ns || it > (1u << 30)) {
         raise_abort(c, kStatusTimeout);
         return false;
       }

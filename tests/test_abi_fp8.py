@@ -80,6 +80,9 @@ def test_product_refuses(kw, expect):
     (dict(splitk=9), mpg.ERR_INVALID_ARG),
     (dict(splitk=-1), mpg.ERR_INVALID_ARG),
     (dict(c_dtype=3), mpg.ERR_INVALID_ARG),
+    (dict(cta_pair=2), mpg.ERR_INVALID_ARG),
+    (dict(cta_pair=1, tile_n=128), mpg.ERR_INVALID_ARG),
+    (dict(cta_pair=1, splitk=2), mpg.ERR_INVALID_ARG),
     (dict(wait_timeout_ns=-1), mpg.ERR_INVALID_ARG),
 ])
 def test_product_refuses_options(o, expect):

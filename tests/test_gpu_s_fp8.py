@@ -175,6 +175,20 @@ def test_product_tiles_and_ranges(tile, splits):
     check(90, 200, 200, sizes=(1, 1), opts=dict(tile_n=tile, splitk=splits), seed=tile + splits)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (100, 300, 130), (256, 256, 128), (257, 255, 640), (513, 700, 1500),
+                                   (300, 129, 128 * 40 + 16)])
+@pytest.mark.parametrize("sizes", [(1, 128), (1, 1), (128, 128)])
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+def test_product_on_pairs(m, n, k, sizes, out):
+    check(m, n, k, sizes=sizes, out=out, opts=dict(cta_pair=1), alpha=0.5, beta=0.25 if m == 513 else 0.0, seed=m)
+
+
+def test_product_on_pairs_many_tiles():
+    """More tiles than clusters, each cluster several, and formats that differ."""
+    check(2500, 2600, 300, ("e5m2", "e4m3"), (1, 1), opts=dict(cta_pair=1), seed=3)
+    check(2500, 2600, 400, ("e4m3", "e4m3"), (1, 128), out="bf16", seed=4)
+
+
 @pytest.mark.parametrize("m", [3, 150])
 @pytest.mark.parametrize("out", ["fp32", "fp16", "bf16"])
 def test_product_outputs_alpha_beta(m, out):
