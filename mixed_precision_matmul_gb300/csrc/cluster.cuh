@@ -82,6 +82,12 @@ __device__ __forceinline__ bool mbar_wait_relaxed(uint64_t* bar, uint32_t parity
   }
 }
 
+// All lanes of the warp wait; true if every lane succeeded.
+__device__ __forceinline__ bool warp_wait_relaxed(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
+  const bool ok = mbar_wait_relaxed(bar, parity, c);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // 3-D tiled load into this CTA's shared memory; completion is signalled on
 // the barrier at `bar_cluster_addr`, which may sit in the peer CTA.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster_addr,

@@ -130,21 +130,32 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_gemm_kernel(const __grid_c
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = make_idesc(0u, false, false, T::BM, T::BN) | p.fmt_bits;
-      for (int i = 0; i < nkb; ++i) {
-        const int st = i % T::kStages, ab = i % T::kAccBufs;
-        if (!mbar_wait(&acc_empty[ab], ((i / T::kAccBufs) & 1u) ^ 1u, ctl)) break;
-        if (!mbar_wait(&op_full[st], (i / T::kStages) & 1u, ctl)) break;
-        tc_fence_after_sync();
-        const uint32_t r_tile = op_smem + st * T::kStage;
-        const uint32_t c_tile = r_tile + T::BM * kFp8RowBytes;
+    const bool leader = elect_one();
+    const uint32_t idesc = make_idesc(0u, false, false, T::BM, T::BN) | p.fmt_bits;
+    const uint64_t r_desc = fp8_desc(op_smem, 0), c_desc = fp8_desc(op_smem + T::BM * kFp8RowBytes, 0);
+    const uint32_t d_base = __shfl_sync(0xffffffffu, tmem_base, 0);
+    int st = 0;
+    uint32_t st_ph = 0;
+    for (int i = 0; i < nkb; ++i) {
+      const int ab = i % T::kAccBufs;
+      if (!warp_wait(&op_full[st], st_ph, ctl)) break;
+      if (!warp_wait(&acc_empty[ab], ((i / T::kAccBufs) & 1u) ^ 1u, ctl)) break;
+      tc_fence_after_sync();
+      const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+      if (leader) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_f8(tmem_base + ab * T::kAccStride, fp8_desc(r_tile, ks), fp8_desc(c_tile, ks), idesc, ks > 0 ? 1u : 0u);
-        mma_commit(&op_empty[st]);
+          mma_f8(d_base + ab * T::kAccStride, r_desc + at + 2 * ks, c_desc + at + 2 * ks, idesc, ks > 0 ? 1u : 0u);
         mma_commit(&acc_full[ab]);
+        mma_commit(&op_empty[st]);
       }
+      __syncwarp();
+      if (++st == T::kStages) {
+        st = 0;
+        st_ph ^= 1u;
+      }
+    }
+    if (leader) {
       mma_commit(done_bar);
       drain_wait(done_bar, 0, p.wait_limit_ns);
     }

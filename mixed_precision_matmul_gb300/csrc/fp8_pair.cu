@@ -66,27 +66,30 @@ __device__ __forceinline__ PairTile pair_tile(const Fp8GemmParams& p, int t) {
   return c;
 }
 
-// alpha x + beta C for 32 rows (one a lane) and 32 columns.  Rows pass through
-// 64-byte lines of shared memory (32 16-bit values, or 16 fp32 values twice),
-// chunk c of row r at slot c ^ ((r / 2) & 3): writes (a row a lane) and reads
-// (four lanes a row) reach all banks.  Each store then covers 8 rows x 64 bytes.
-__device__ __forceinline__ void store_rows32(const Fp8GemmParams& p, uint32_t stg, int lane, const float (&x)[32],
+// alpha x + beta C for 32 rows (one a lane) and 32 columns (x[j]: columns 2j
+// and 2j + 1).  Rows pass through 64-byte lines of shared memory (32 16-bit values, or 16
+// fp32 values twice), chunk c of row r at slot c ^ ((r / 2) & 3): writes and
+// reads (four lanes a row) reach all banks.  Each store then covers 8 rows x
+// 64 bytes.
+__device__ __forceinline__ void store_rows32(const Fp8GemmParams& p, uint32_t stg, int lane, const f32x2* x,
                                              int row_base, int col_base) {
-  const uint32_t wr = stg + lane * 64, wsw = (lane >> 1) & 3;
+  auto at = [&](int r, int c) { return stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };   // 16-byte chunk c of row r
   const int dt = p.out_dtype;
   if (dt != kOutF32 && p.beta == 0.0f && p.out_vec16 && col_base + 32 <= p.cols) {
     uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      w[j] = dt == kOutF16 ? pack_f16x2(p.alpha * x[2 * j], p.alpha * x[2 * j + 1])
-                           : pack_bf16x2(p.alpha * x[2 * j], p.alpha * x[2 * j + 1]);
+    for (int j = 0; j < 16; ++j) {
+      float lo, hi;
+      unpack2(x[j], lo, hi);
+      w[j] = dt == kOutF16 ? pack_f16x2(p.alpha * lo, p.alpha * hi) : pack_bf16x2(p.alpha * lo, p.alpha * hi);
+    }
 #pragma unroll
-    for (uint32_t c = 0; c < 4; ++c) st_shared_v4(wr + ((c ^ wsw) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    for (int c = 0; c < 4; ++c) st_shared_v4(at(lane, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2), c = lane & 3;
-      const float4 y = stage_ld16(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+      const float4 y = stage_ld16(at(r, c));
       if (row_base + r < p.rows)
         *reinterpret_cast<float4*>(static_cast<uint16_t*>(p.out) + (int64_t)(row_base + r) * p.ld_out + col_base + c * 8) = y;
     }
@@ -94,16 +97,18 @@ __device__ __forceinline__ void store_rows32(const Fp8GemmParams& p, uint32_t st
     return;
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int hc = 0; hc < 2; ++hc) {                        // 16 columns
 #pragma unroll
-    for (uint32_t c = 0; c < 4; ++c)
-      stage_st16(wr + ((c ^ wsw) << 4), x[16 * h + 4 * c], x[16 * h + 4 * c + 1], x[16 * h + 4 * c + 2], x[16 * h + 4 * c + 3]);
+      for (int c = 0; c < 4; ++c) {
+        st_shared_b64(at(lane, c), x[hc * 8 + 2 * c]);
+        st_shared_b64(at(lane, c) + 8, x[hc * 8 + 2 * c + 1]);
+      }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2), c = lane & 3;
-      const float4 y = stage_ld16(stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-      const int row = row_base + r, col = col_base + 16 * h + 4 * c;
+      const float4 y = stage_ld16(at(r, c));
+      const int row = row_base + r, col = col_base + 16 * hc + 4 * c;
       if (row >= p.rows) continue;
       const int64_t idx = (int64_t)row * p.ld_out + col;
       if (p.out_vec && col + 4 <= p.cols) {
@@ -216,32 +221,40 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (rank 0)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool leader = elect_one();
       const uint32_t idesc = make_idesc(0u, false, false, T::kTile, T::kTile) | p.fmt_bits;
       // the start address sits in the descriptor's low bits, in units of 16 bytes
       const uint64_t r_desc = fp8_desc(op_smem, 0), c_desc = fp8_desc(op_smem + T::kRTile, 0);
+      const uint32_t d_base = __shfl_sync(0xffffffffu, tmem_base, 0);
       uint32_t it = 0, st = 0, st_ph = 0;
       bool ok = true;
       for (int t = worker; t < p.num_tiles && ok; t += workers) {
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const uint32_t ab = it % T::kAccBufs;
-          if (!mbar_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
-          if (!mbar_wait_relaxed(&acc_empty[ab], ((it / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
+          if (!warp_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
+          if (!warp_wait_relaxed(&acc_empty[ab], ((it / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
           tc_fence_after_sync();
           const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f8_pair(tmem_base + ab * T::kTile, r_desc + at + 2 * ks, c_desc + at + 2 * ks, idesc, ks > 0 ? 1u : 0u);
-          mma_commit_multicast(&acc_full[ab], 0x3);
-          mma_commit_multicast(&op_empty[st], 0x3);
+            for (int ks = 0; ks < 4; ++ks)
+              mma_f8_pair(d_base + ab * T::kTile, r_desc + at + 2 * ks, c_desc + at + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+            mma_commit_multicast(&acc_full[ab], 0x3);
+            mma_commit_multicast(&op_empty[st], 0x3);
+          }
+          __syncwarp();
           if (++st == T::kStages) {
             st = 0;
             st_ph ^= 1u;
           }
         }
       }
-      mma_commit_multicast(done_bar, 0x1);
-      drain_wait(done_bar, 0, p.wait_limit_ns);
+      if (leader) {
+        mma_commit_multicast(done_bar, 0x1);
+        drain_wait(done_bar, 0, p.wait_limit_ns);
+      }
+      __syncwarp();
     }
   } else if (T::kColVec) {
     // ------------------------------------------------------------ column scales
@@ -251,15 +264,16 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
       const PairTile tc = pair_tile(p, t);
       // this lane's columns (clamped to the operand's last line)
       const int c0 = (warp - 2) * T::kCols + lane;
-      const float* src[4];
+      constexpr int kN = T::kCols / 32;
+      const float* src[kN];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kN; ++i)
         src[i] = p.sc + (int64_t)(min(tc.cb * T::kTile + c0 + 32 * i, p.cols - 1) >> p.sc_shift) * p.sc_row;
       for (int kb = 0; kb < nkb; ++kb) {
         if (!warp_wait(&scale_empty[slot], ph ^ 1u, ctl)) { ok = false; break; }
         const uint32_t dst = smem_addr(scale_base) + (slot * T::kScaleSlot + c0) * 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kN; ++i) {
           cp_async4(dst + i * 128, src[i]);
           src[i] += p.sc_k;
         }
@@ -280,81 +294,86 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
     const uint32_t half = (uint32_t)(ew / 4);
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + half * T::kCols;
     const uint32_t stg = smem_addr(epi_base) + ew * 2048;
-    const uint32_t scales = smem_addr(scale_base);
     const uint32_t acc_empty0 = cluster_smem_addr(smem_addr(acc_empty), 0);
-    constexpr int kN = T::kCols / 32;
+    // One block of k's hand-over: the buffer goes back to rank 0, and the next
+    // block's product is waited for (`ready`: its barrier, asked early, said
+    // that it is complete).
+    auto hand_over = [&](uint32_t it, bool more, bool ready) {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + (it % T::kAccBufs) * 8u);
+      if (more && !__all_sync(0xffffffffu, ready) &&
+          !warp_wait(&acc_full[(it + 1) % T::kAccBufs], ((it + 1) / T::kAccBufs) & 1u, ctl))
+        return false;
+      tc_fence_after_sync();
+      return true;
+    };
     uint32_t it = 0, slot = 0, slot_ph = 0;
     bool ok = true;
     for (int t = worker; t < p.num_tiles && ok; t += workers) {
-      const PairTile tc = pair_tile(p, t);
-      const int row_base = tc.rb * T::kTile + (int)rank * T::BM + 32 * q;
-      const int col_first = tc.cb * T::kTile + (int)half * T::kCols;
       f32x2 acc[T::kCols / 2];
 #pragma unroll
       for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
-      // This lane's row scale, and the scale of this half's columns, go from
-      // global memory straight into registers, three blocks ahead.
-      const float* row_src =
-          p.sr + (int64_t)(min(row_base + lane, p.rows - 1) >> p.sr_shift) * p.sr_row;
-      const float* col_src = p.sc + (int64_t)(min(col_first, p.cols - 1) >> p.sc_shift) * p.sc_row;
+      if (!warp_wait(&acc_full[it % T::kAccBufs], (it / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
+      tc_fence_after_sync();
+      // A row a lane.  The row's scale (and that of this half's columns, where
+      // they share one) goes from global memory straight into registers, three
+      // blocks ahead: shared memory is busy with operands, and a load from it
+      // takes longer than a block's additions.
+      const PairTile tc0 = pair_tile(p, t);
+      const int row = tc0.rb * T::kTile + (int)rank * T::BM + 32 * q + lane;
+      const int col = tc0.cb * T::kTile + (int)half * T::kCols;
+      const float* row_src = p.sr + (int64_t)(min(row, p.rows - 1) >> p.sr_shift) * p.sr_row;
+      const float* col_src = p.sc + (int64_t)(min(col, p.cols - 1) >> p.sc_shift) * p.sc_row;
       float rsc[4], csc[4];
-      int fetched = 0;
-      auto fetch_scales = [&](int i) {
-        if (fetched < nkb) {
+      auto fetch_scales = [&](int i, int kb) {
+        if (kb < nkb) {
           rsc[i] = __ldg(row_src);
           row_src += p.sr_k;
           if (!T::kColVec) {
             csc[i] = __ldg(col_src);
             col_src += p.sc_k;
           }
-          ++fetched;
         }
       };
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        rsc[i] = csc[i] = 0.0f;
-        if (i < 3) fetch_scales(i);
+        rsc[i] = 0.0f;
+        csc[i] = 1.0f;
+        if (i < 3) fetch_scales(i, i);
       }
-      // Columns are read 32 at a time, the next 32 on their way while the last
-      // are added, across the blocks of k too: the wait for the next block's
-      // product and its first read go before the last additions of this one.
+      // Columns are read 32 at a time, two reads on their way, across the
+      // blocks of k too.  (Beside running MMAs a tcgen05.ld takes about 190
+      // cycles to arrive, five times as long as without; with one on its way
+      // a block took 4 x 190.)
+      constexpr int kN = T::kCols / 32;
+      static_assert(kN == 4, "two pairs of reads a block");
+      const uint32_t scales = smem_addr(scale_base) + half * (T::kCols * 4);
       float v[2][32];
-      if (!warp_wait(&acc_full[it % T::kAccBufs], (it / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
-      tc_fence_after_sync();
-      tmem_ld_32cols(tacc + (it % T::kAccBufs) * T::kTile, v[0]);
+      tmem_ld_32cols(tacc + (it & 1u) * T::kTile, v[0]);
+      tmem_ld_32cols(tacc + (it & 1u) * T::kTile + 32, v[1]);
 #pragma unroll 1
-      for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
-        const uint32_t ab = it % T::kAccBufs, nx = (it + 1) % T::kAccBufs;
-        const uint32_t nx_ph = ((it + 1) / T::kAccBufs) & 1u;
-        fetch_scales(3);
-        const float s = T::kColVec ? rsc[0] : rsc[0] * csc[0];
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const bool more = kb + 1 < nkb;
+        const uint32_t here = tacc + (it & 1u) * T::kTile, next = tacc + ((it + 1) & 1u) * T::kTile;
+        fetch_scales(3, kb + 3);
+        const float s = rsc[0] * csc[0];
         const f32x2 rs = pack2(s, s);
-        uint32_t sl = 0;
-        if constexpr (T::kColVec) {
-          if (!warp_wait(&scale_full[slot], slot_ph, ctl)) { ok = false; break; }
-          sl = scales + slot * (T::kScaleSlot * 4) + half * (T::kCols * 4) - 128;
-        }
-        bool ready = false;
-#pragma unroll
-        for (int c = 0; c < kN; ++c) {
-          tmem_ld_wait();
-          if (c + 1 < kN) {
-            tmem_ld_32cols(tacc + ab * T::kTile + (c + 1) * 32, v[(c + 1) & 1]);
-            // the barrier's answer takes a while (shared memory is busy with
-            // operands), so it is asked for early
-            if (c + 2 == kN && kb + 1 < nkb) ready = mbar_test(&acc_full[nx], nx_ph);
-          } else {
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + ab * 8u);
-            if (kb + 1 < nkb) {
-              if (!__all_sync(0xffffffffu, ready) && !warp_wait(&acc_full[nx], nx_ph, ctl)) { ok = false; break; }
-              tc_fence_after_sync();
-              tmem_ld_32cols(tacc + nx * T::kTile, v[(c + 1) & 1]);
-            }
-          }
-          scale_add<32, T::kColVec>(acc + c * 16, v[c & 1], sl, c * 32, rs);
-        }
+        if (T::kColVec && !warp_wait(&scale_full[slot], slot_ph, ctl)) { ok = false; break; }
+        const uint32_t sl = scales + slot * (T::kScaleSlot * 4) - 128;
+        tmem_ld_wait();
+        scale_add<32, T::kColVec>(acc, v[0], sl, 0, rs);
+        tmem_ld_32cols(here + 64, v[0]);
+        scale_add<32, T::kColVec>(acc + 16, v[1], sl, 32, rs);
+        tmem_ld_32cols(here + 96, v[1]);
+        // the barrier takes a while to answer: asked early
+        const bool ready = more && mbar_test(&acc_full[(it + 1) & 1u], ((it + 1) >> 1) & 1u);
+        tmem_ld_wait();
+        if (!hand_over(it, more, ready)) { ok = false; break; }
+        scale_add<32, T::kColVec>(acc + 32, v[0], sl, 64, rs);
+        if (more) tmem_ld_32cols(next, v[0]);
+        scale_add<32, T::kColVec>(acc + 48, v[1], sl, 96, rs);
+        if (more) tmem_ld_32cols(next + 32, v[1]);
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
           rsc[i] = rsc[i + 1];
@@ -371,16 +390,14 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
       }
       if (!ok) break;
       // ---------------------------------------------------------- C
+      const PairTile tc = pair_tile(p, t);
+      const int row_base = tc.rb * T::kTile + (int)rank * T::BM + 32 * q;
+      const int col_first = tc.cb * T::kTile + (int)half * T::kCols;
       if (row_base >= p.rows) continue;
 #pragma unroll
-      for (int cc = 0; cc < kN; ++cc) {
-        const int col_base = col_first + cc * 32;
-        if (col_base >= p.cols) continue;
-        float x[32];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) unpack2(acc[cc * 16 + j], x[2 * j], x[2 * j + 1]);
-        store_rows32(p, stg, lane, x, row_base, col_base);
-      }
+      for (int cc = 0; cc < T::kCols / 32; ++cc)
+        if (col_first + cc * 32 < p.cols)
+          store_rows32(p, stg, lane, acc + cc * 16, row_base, col_first + cc * 32);
     }
   }
 

@@ -416,42 +416,54 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool leader = elect_one();
       const bool a_mn = p.a_mn_major != 0, b_mn = p.b_mn_major != 0;
       const uint32_t idesc = make_idesc(0u /* f16 */, a_mn, b_mn, T::kTile, T::kTile);
+      // the start address sits in the descriptor's low bits, in units of 16 bytes
+      const uint64_t a_desc = operand_desc<T>(op_smem, a_mn, 0), b_desc = operand_desc<T>(op_smem + T::kATile, b_mn, 0);
+      const uint32_t a_step = (a_mn ? T::kInstrK * T::kRowBytes : 32) / 16, b_step = (b_mn ? T::kInstrK * T::kRowBytes : 32) / 16;
+      const uint32_t d_base = __shfl_sync(0xffffffffu, tmem_base, 0);
       auto commit = [&](uint64_t* bar, uint16_t mask) {
         if constexpr (T::kPair) mma_commit_multicast(bar, mask);
         else mma_commit(bar);
       };
-      uint32_t it = 0, g = 0;
+      uint32_t g = 0, st = 0, st_ph = 0;
       bool ok = true;
       for (int t = worker; t < p.num_tiles && ok; t += workers, ++g) {
         const uint32_t ab = g % T::kAccBufs;
-        if (!mbar_wait(&acc_empty[ab], ((g / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
+        if (!warp_wait(&acc_empty[ab], ((g / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
         if constexpr (T::kPair) asm volatile("fence.acq_rel.cluster;" ::: "memory");
         tc_fence_after_sync();
-        const uint32_t d0 = tmem_base + ab * T::kTile;
-        for (int kb = 0; kb < p.num_k_blk; ++kb, ++it) {
-          const uint32_t st = it % T::kStages;
-          if (!mbar_wait(&op_full[st], (it / T::kStages) & 1u, ctl)) { ok = false; break; }
+        const uint32_t d0 = d_base + ab * T::kTile;
+        for (int kb = 0; kb < p.num_k_blk; ++kb) {
+          if (!warp_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
           tc_fence_after_sync();
-          const uint32_t a_tile = op_smem + st * T::kStage;
-          const uint32_t b_tile = a_tile + T::kATile;
+          const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < T::kKSteps; ++ks) {
-            const uint64_t da = operand_desc<T>(a_tile, a_mn, ks), db = operand_desc<T>(b_tile, b_mn, ks);
-            const uint32_t acc = (kb > 0 || ks > 0) ? 1u : 0u;
-            if constexpr (T::kPair) mma_f16_pair(d0, da, db, idesc, acc);
-            else mma_f16(d0, da, db, idesc, acc);
+            for (int ks = 0; ks < T::kKSteps; ++ks) {
+              const uint64_t da = a_desc + at + ks * a_step, db = b_desc + at + ks * b_step;
+              const uint32_t acc = (kb > 0 || ks > 0) ? 1u : 0u;
+              if constexpr (T::kPair) mma_f16_pair(d0, da, db, idesc, acc);
+              else mma_f16(d0, da, db, idesc, acc);
+            }
+            commit(&op_empty[st], 0x3);
+            if (kb + 1 == p.num_k_blk) commit(&acc_full[ab], 0x3);
           }
-          commit(&op_empty[st], 0x3);
+          __syncwarp();
+          if (++st == T::kStages) {
+            st = 0;
+            st_ph ^= 1u;
+          }
         }
-        if (!ok) break;
-        commit(&acc_full[ab], 0x3);
       }
       // every MMA completes before TMEM is released
-      commit(done_bar, 0x1);
-      drain_wait(done_bar, 0, p.wait_limit_ns);
+      if (leader) {
+        commit(done_bar, 0x1);
+        drain_wait(done_bar, 0, p.wait_limit_ns);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue

@@ -103,6 +103,20 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  An MMA loop that the whole warp runs,
+// with only the instructions themselves under this predicate, keeps its
+// descriptors in uniform registers, where tcgen05.mma wants them; in a branch
+// of one lane each is moved there first (about 80 cycles an instruction).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------------------
 // proxy fences
 // ---------------------------------------------------------------------------
