@@ -15,7 +15,7 @@ struct Fp8QuantParams {
   const void* x;
   int64_t ldx;
   int32_t rows, cols;
-  int32_t x_vec;              // 8-element chunks of a line of x are 16-byte aligned
+  int32_t x_align;            // alignment of every line of x in bytes: 16, 8, 4 or 2
   uint8_t* q;                 // rows x cols, or null
   int64_t ldq;
   int32_t q_vec;              // 8-byte chunks of q are aligned
@@ -63,6 +63,7 @@ struct Fp8GemmParams {
 struct Fp8Kernel {
   const void* fn;
   int block, smem_bytes;
+  int ctas_per_sm;
   int tile_rows, tile_cols;
 };
 // One-CTA tiles of 128 x bn: bn = 128 (D as the caller's C; col_vec: a scale

@@ -79,7 +79,19 @@ Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, int 
   if (o.splitk > 0) {
     s = o.splitk;
   } else {
-    while (s < 8 && tiles * (s + 1) <= sm_count && kb / (s + 1) >= 4) ++s;
+    // An SM's CTAs take turns at its bandwidth, so the time is that of the
+    // busiest SM's blocks of k, and for each CTA that of its start and end
+    // (about 6 blocks of a 128 x 128 tile, 2 where several CTAs share an SM
+    // and overlap); a division adds the exchange of the partial sums.
+    const int64_t edge = p.swapped ? 2 : 6;
+    int64_t best = -1;
+    for (int64_t d = 1; d <= std::min<int64_t>(8, kb); ++d) {
+      const int64_t cost = (tiles * d + sm_count - 1) / sm_count * ((kb + d - 1) / d + edge) + (d > 1 ? 2 : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        s = d;
+      }
+    }
   }
   s = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(s, 8), kb));
   const int64_t per = (kb + s - 1) / s;
@@ -212,7 +224,8 @@ mpg_status mpg_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t l
   p.ldx = ldx;
   p.rows = (int32_t)rows;
   p.cols = (int32_t)cols;
-  p.x_vec = aligned(X, 16) && (ldx * elem_bytes(x_dtype)) % 16 == 0;
+  p.x_align = 16;
+  while (p.x_align > 2 && (!aligned(X, (size_t)p.x_align) || (ldx * elem_bytes(x_dtype)) % p.x_align != 0)) p.x_align /= 2;
   p.q = static_cast<uint8_t*>(Q);
   p.ldq = ldq;
   p.q_vec = aligned(Q, 8) && ldq % 8 == 0;

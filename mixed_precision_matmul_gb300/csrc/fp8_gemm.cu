@@ -30,20 +30,23 @@ struct Fp8Traits {
   static constexpr bool kSwapped = kSwapped_;
   static constexpr bool kColVec = kColVec_;
   static constexpr int kStage = (BM + BN) * kFp8RowBytes;
-  static constexpr int kStages = BN >= 128 ? 6 : BN >= 64 ? 7 : 9;
+  // few columns: three CTAs to an SM, so that one's start and end overlap the
+  // others' loads
+  static constexpr int kCtasPerSm = BN >= 128 ? 1 : BN >= 64 ? 2 : 3;
+  static constexpr int kStages = BN >= 128 ? 6 : BN >= 64 ? 4 : 3;
   static constexpr int kAccBufs = 4;
   static constexpr int kAccStride = BN < 32 ? 32 : BN;
   static constexpr int kTmemCols = kAccBufs * kAccStride;
   static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
   static constexpr int kCols = BN / (kEpiWarps / 4);      // columns of one epilogue warp
   static constexpr int kThreads = (2 + kEpiWarps) * 32;
-  using Ring = ScaleRing<kCols, kColVec>;
+  using Ring = ScaleRing<kCols, kColVec, kSwapped ? 4 : 8>;
   static constexpr int kPitch = BN + 1;                   // floats per row of the staged tile
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
   static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiWarps * Ring::kBytes + kNumBars * 8 + 16;
-  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory budget");
   static_assert(BM * kPitch * 4 <= kStages * kStage, "the staged tile reuses the operand stages");
-  static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
+  static_assert(kCtasPerSm * kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
 };
 
 // One 32-bit word of the shared memory of CTA `rank` of the cluster.
@@ -54,7 +57,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(T::kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
+__global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the same offset in every CTA of a cluster (the partial sums are read by address)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -213,48 +216,76 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_gemm_kernel(const __grid_c
     uint32_t peer[8];
 #pragma unroll
     for (int s = 0; s < 8; ++s) peer[s] = s < splits ? cluster_smem_addr(op_smem, (uint32_t)s) : 0u;
-    auto sum_at = [&](int r, int c) {
-      const uint32_t off = ((uint32_t)(ra + r) * T::kPitch + c) * 4u;
-      if (splits == 1) return ld_shared_f32(op_smem + off);
-      float x = ld_cluster_f32(peer[0] + off);
+    // kN sums of one row at a time, all their loads issued before the first
+    // addition: a load from another SM takes about a microsecond
+    auto sums_at = [&](int r, const int* c, auto& x) {
+      constexpr int kN = sizeof(x) / sizeof(float);
+      const uint32_t row = (uint32_t)(ra + r) * T::kPitch * 4u;
+      if (splits == 1) {
 #pragma unroll
-      for (int s = 1; s < 8; ++s)
-        if (s < splits) x += ld_cluster_f32(peer[s] + off);
-      return x;
+        for (int j = 0; j < kN; ++j) x[j] = ld_shared_f32(op_smem + row + c[j] * 4);
+        return;
+      }
+      float part[8][kN];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (s < splits) part[s][j] = ld_cluster_f32(peer[s] + row + c[j] * 4);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        x[j] = part[0][j];
+#pragma unroll
+        for (int s = 1; s < 8; ++s)
+          if (s < splits) x[j] += part[s][j];
+      }
     };
     if constexpr (T::kSwapped) {
-      // C[col, row]: lanes along the rows
-      const int groups = (rows_here + 31) / 32;
-      for (int u = warp; u < groups * cols_here; u += warps) {
-        const int c = u / groups, r = (u - c * groups) * 32 + lane;
-        if (r < rows_here) {
-          const float x = p.alpha * sum_at(r, c);
-          const int64_t idx = (int64_t)(col0 + c) * p.ld_out + row0 + ra + r;
-          out_store(p.out, idx, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx, p.out_dtype), x) : x, p.out_dtype);
+      // C[col, row]: lanes along the rows, four columns to a warp
+      const int groups = (rows_here + 31) / 32, quads = (cols_here + 3) / 4;
+      for (int u = warp; u < groups * quads; u += warps) {
+        const int cq = u / groups, r = (u - cq * groups) * 32 + lane;
+        if (r >= rows_here) continue;
+        int c[4];
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = min(cq * 4 + j, cols_here - 1);
+        sums_at(r, c, x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (cq * 4 + j >= cols_here) break;
+          const int64_t idx = (int64_t)(col0 + c[j]) * p.ld_out + row0 + ra + r;
+          const float y = p.alpha * x[j];
+          out_store(p.out, idx, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx, p.out_dtype), y) : y, p.out_dtype);
         }
       }
     } else {
       for (int r = warp; r < rows_here; r += warps) {
         const int64_t line = (int64_t)(row0 + ra + r) * p.ld_out + col0;
+        float x[4];
         if (p.out_vec && cols_here == T::BN) {
-#pragma unroll
-          for (int c = lane * 4; c < T::BN; c += 128) {
-            float4 o = make_float4(p.alpha * sum_at(r, c), p.alpha * sum_at(r, c + 1), p.alpha * sum_at(r, c + 2),
-                                   p.alpha * sum_at(r, c + 3));
-            if (p.beta != 0.0f) {
-              const float4 z = out_load4(p.out, line + c, p.out_dtype);
-              o.x = fmaf(p.beta, z.x, o.x);
-              o.y = fmaf(p.beta, z.y, o.y);
-              o.z = fmaf(p.beta, z.z, o.z);
-              o.w = fmaf(p.beta, z.w, o.w);
-            }
-            out_store4(p.out, line + c, o, p.out_dtype);
+          const int c[4] = {lane * 4, lane * 4 + 1, lane * 4 + 2, lane * 4 + 3};
+          sums_at(r, c, x);
+          float4 o = make_float4(p.alpha * x[0], p.alpha * x[1], p.alpha * x[2], p.alpha * x[3]);
+          if (p.beta != 0.0f) {
+            const float4 z = out_load4(p.out, line + c[0], p.out_dtype);
+            o.x = fmaf(p.beta, z.x, o.x);
+            o.y = fmaf(p.beta, z.y, o.y);
+            o.z = fmaf(p.beta, z.z, o.z);
+            o.w = fmaf(p.beta, z.w, o.w);
           }
+          out_store4(p.out, line + c[0], o, p.out_dtype);
         } else {
-          for (int c = lane; c < cols_here; c += 32) {
-            const float x = p.alpha * sum_at(r, c);
-            out_store(p.out, line + c, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, line + c, p.out_dtype), x) : x,
-                      p.out_dtype);
+          int c[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[j] = min(lane + 32 * j, cols_here - 1);
+          sums_at(r, c, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (lane + 32 * j >= cols_here) break;
+            const float y = p.alpha * x[j];
+            out_store(p.out, line + c[j],
+                      p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, line + c[j], p.out_dtype), y) : y, p.out_dtype);
           }
         }
       }
@@ -274,6 +305,7 @@ bool fill(Fp8Kernel* out) {
   out->fn = reinterpret_cast<const void*>(&fp8_gemm_kernel<T>);
   out->block = T::kThreads;
   out->smem_bytes = T::kSmemBytes;
+  out->ctas_per_sm = T::kCtasPerSm;
   out->tile_rows = T::BM;
   out->tile_cols = T::BN;
   return true;

@@ -416,6 +416,7 @@ bool fill(Fp8Kernel* out) {
   out->fn = reinterpret_cast<const void*>(&fp8_pair_kernel<T>);
   out->block = T::kThreads;
   out->smem_bytes = T::kSmemBytes;
+  out->ctas_per_sm = 1;
   out->tile_rows = T::kTile;
   out->tile_cols = T::kTile;
   return true;

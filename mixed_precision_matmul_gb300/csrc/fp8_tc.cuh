@@ -98,9 +98,9 @@ __device__ __forceinline__ void ld_shared_pairs(uint32_t addr, f32x2& a, f32x2& 
 // The scales of one epilogue warp: its 32 rows and `kCols` columns (or the one
 // scale of all its columns), fetched kDepth - 1 blocks of k ahead into a ring
 // in shared memory that only this warp uses.
-template <int kCols, bool kColVec>
+template <int kCols, bool kColVec, int kDepth_>
 struct ScaleRing {
-  static constexpr int kDepth = 8;
+  static constexpr int kDepth = kDepth_;
   static constexpr int kSlot = 32 + (kColVec ? kCols : 32);        // floats
   static constexpr int kBytes = kDepth * kSlot * 4;
   static constexpr int kColLoads = kColVec ? (kCols + 31) / 32 : 1;
