@@ -30,10 +30,15 @@ struct Fp8QuantParams {
 cudaError_t launch_fp8_quantize(const Fp8QuantParams& p, int x_dtype, int format, int scale_rows,
                                 cudaStream_t stream);
 
-// Lines of `cols` bytes copied to lines of ld_out bytes (ld_out % 16 == 0,
-// out 16-byte aligned, padding zeroed), from any alignment.
-cudaError_t launch_fp8_align(const uint8_t* in, int64_t ld_in, int64_t rows, int64_t cols, uint8_t* out,
-                             int64_t ld_out, int sm_count, cudaStream_t stream);
+// Lines of `cols` bytes copied, from any alignment, to lines of ld_out bytes
+// (ld_out = 16 chunks, out 16-byte aligned, padding zeroed).  rows 0: no copy.
+struct Fp8AlignJob {
+  const uint8_t* in;
+  int64_t ld_in, rows, cols, chunks;
+  uint8_t* out;
+  int64_t ld_out;
+};
+cudaError_t launch_fp8_align(const Fp8AlignJob& a, const Fp8AlignJob& b, int sm_count, cudaStream_t stream);
 
 // The product D[r, c] = sum_kb sr[r, kb] sc[c, kb] (R_kb C_kb^T)[r, c], where
 // R (rows x k) feeds the 128 rows of a tensor-core tile and C (cols x k) its

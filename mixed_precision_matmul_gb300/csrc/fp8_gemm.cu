@@ -41,18 +41,24 @@ struct Fp8Traits {
   static constexpr int kCols = BN / (kEpiWarps / 4);      // columns of one epilogue warp
   static constexpr int kThreads = (2 + kEpiWarps) * 32;
   using Ring = ScaleRing<kCols, kColVec, kSwapped ? 4 : 8>;
-  static constexpr int kPitch = BN + 1;                   // floats per row of the staged tile
+  // The staged tile's lines run along C's: columns of a row, or, swapped, the
+  // rows of a column.  (132: rows written by 16 bytes a lane reach all banks.)
+  static constexpr int kLines = kSwapped ? BN : BM;
+  static constexpr int kPitch = kSwapped ? BM : BN + 4;   // floats
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
   static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiWarps * Ring::kBytes + kNumBars * 8 + 16;
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory budget");
-  static_assert(BM * kPitch * 4 <= kStages * kStage, "the staged tile reuses the operand stages");
+  static_assert(kLines * kPitch * 4 <= kStages * kStage, "the staged tile reuses the operand stages");
   static_assert(kCtasPerSm * kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
 };
 
-// One 32-bit word of the shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+// 16 bytes of the shared memory of another CTA of the cluster.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
   return v;
 }
 
@@ -169,35 +175,95 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
     const int ew = warp - 2;
     const int wc0 = (ew / 4) * T::kCols;                  // this warp's first column in the tile
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + wc0;
-    typename T::Ring ring;
-    ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row0 + 32 * q, col0 + wc0, kb0, nkb);
     f32x2 acc[T::kCols / 2];
 #pragma unroll
     for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
+    auto release = [&](int ab) {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+    };
+    if constexpr (T::kColVec) {
+      typename T::Ring ring;
+      ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row0 + 32 * q, col0 + wc0, kb0, nkb);
 #pragma unroll 1
-    for (int i = 0; i < nkb; ++i) {
-      const int ab = i % T::kAccBufs;
-      __syncwarp();                                      // every lane is done with block i - 1's slot
-      ring.fetch(i + T::Ring::kDepth - 1);
-      cp_async_wait<T::Ring::kDepth - 1>();
-      if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
-      tc_fence_after_sync();
-      add_block<T::kCols, T::kColVec>(acc, tacc + ab * T::kAccStride, ring.slot(i), lane, [&]() {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[ab]);
-      });
+      for (int i = 0; i < nkb; ++i) {
+        const int ab = i % T::kAccBufs;
+        __syncwarp();                                    // every lane is done with block i - 1's slot
+        ring.fetch(i + T::Ring::kDepth - 1);
+        cp_async_wait<T::Ring::kDepth - 1>();
+        if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
+        tc_fence_after_sync();
+        const uint32_t slot = ring.slot(i);
+        const float s = ld_shared_f32(slot + lane * 4);
+        add_block<T::kCols, true>(acc, tacc + ab * T::kAccStride, slot, pack2(s, s), [&]() { release(ab); });
+      }
+    } else {
+      // A row a lane: its scale and that of all columns go from global memory
+      // into registers, three blocks ahead; two reads of 32 columns are on
+      // their way while the last block's are added.
+      static_assert(T::kCols == 64, "two reads a block");
+      const float* row_src = p.sr + (int64_t)(min(row0 + 32 * q + lane, p.rows - 1) >> p.sr_shift) * p.sr_row + kb0 * p.sr_k;
+      const float* col_src = p.sc + (int64_t)(min(col0 + wc0, p.cols - 1) >> p.sc_shift) * p.sc_row + kb0 * p.sc_k;
+      float rsc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, csc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      auto fetch_scales = [&](int j, int i) {
+        if (i < nkb) {
+          rsc[j] = __ldg(row_src);
+          csc[j] = __ldg(col_src);
+          row_src += p.sr_k;
+          col_src += p.sc_k;
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < 3; ++j) fetch_scales(j, j);
+      float v[2][32];
+      auto load = [&](int i) {
+        if (!warp_wait(&acc_full[i % T::kAccBufs], (i / T::kAccBufs) & 1u, ctl)) return false;
+        tc_fence_after_sync();
+        return true;
+      };
+      ok = nkb > 0 && load(0);
+      if (ok) {
+        tmem_ld_32cols(tacc, v[0]);
+        tmem_ld_32cols(tacc + 32, v[1]);
+      }
+#pragma unroll 1
+      for (int i = 0; i < nkb && ok; ++i) {
+        const bool more = i + 1 < nkb;
+        const uint32_t next = tacc + ((i + 1) % T::kAccBufs) * T::kAccStride;
+        fetch_scales(3, i + 3);
+        const float s = rsc[0] * csc[0];
+        const f32x2 rs = pack2(s, s);
+        tmem_ld_wait();
+        release(i % T::kAccBufs);
+        if (more && !load(i + 1)) { ok = false; break; }
+        scale_add<32, false>(acc, v[0], 0, 0, rs);
+        if (more) tmem_ld_32cols(next, v[0]);
+        scale_add<32, false>(acc + 16, v[1], 0, 32, rs);
+        if (more) tmem_ld_32cols(next + 32, v[1]);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          rsc[j] = rsc[j + 1];
+          csc[j] = csc[j + 1];
+        }
+      }
     }
     cp_async_wait<0>();
     if (ok) {
       // every MMA of this CTA is complete: the operand stages are free
-      const uint32_t dst = op_smem + ((uint32_t)(32 * q + lane) * T::kPitch + wc0) * 4u;
+      const int r = 32 * q + lane;
 #pragma unroll
-      for (int j = 0; j < T::kCols; j += 2) {
-        float lo, hi;
-        unpack2(acc[j / 2], lo, hi);
-        st_shared_f32(dst + j * 4, lo);
-        st_shared_f32(dst + j * 4 + 4, hi);
+      for (int j = 0; j < T::kCols; j += 4) {
+        float x[4];
+        unpack2(acc[j / 2], x[0], x[1]);
+        unpack2(acc[j / 2 + 1], x[2], x[3]);
+        if constexpr (T::kSwapped) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared_f32(op_smem + (uint32_t)((wc0 + j + i) * T::kPitch + r) * 4u, x[i]);
+        } else {
+          st_shared_v4(op_smem + (uint32_t)(r * T::kPitch + wc0 + j) * 4u, __float_as_uint(x[0]), __float_as_uint(x[1]),
+                       __float_as_uint(x[2]), __float_as_uint(x[3]));
+        }
       }
     }
   }
@@ -207,87 +273,67 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
   if (*abort_flag == 0) {
+    // This CTA's share of the tile's rows, in vectors of four elements that
+    // are neighbours in C and in the staged lines; of each, the ranges' partial
+    // sums are loaded before the first is added (a load from another SM takes
+    // about a microsecond).
     const int splits = p.splits;
-    const int rows_per = (T::BM + splits - 1) / splits;
+    const int rows_per = ((T::BM + splits - 1) / splits + 3) & ~3;
     const int ra = (int)rank * rows_per;
-    const int rows_here = min(min(T::BM, ra + rows_per), p.rows - row0) - ra;    // rows that this CTA stores
+    const int rows_here = min(min(T::BM, ra + rows_per), p.rows - row0) - ra;
     const int cols_here = min(T::BN, p.cols - col0);
-    const int warps = T::kThreads / 32;
+    const int lines = T::kSwapped ? cols_here : rows_here;               // of C, in this share
+    const int length = T::kSwapped ? rows_here : cols_here;
+    const int first = T::kSwapped ? ra : 0;                              // offset in a staged line
+    const int line0 = T::kSwapped ? 0 : ra;
+    const int vecs = (length + 3) / 4;
     uint32_t peer[8];
 #pragma unroll
     for (int s = 0; s < 8; ++s) peer[s] = s < splits ? cluster_smem_addr(op_smem, (uint32_t)s) : 0u;
-    // kN sums of one row at a time, all their loads issued before the first
-    // addition: a load from another SM takes about a microsecond
-    auto sums_at = [&](int r, const int* c, auto& x) {
-      constexpr int kN = sizeof(x) / sizeof(float);
-      const uint32_t row = (uint32_t)(ra + r) * T::kPitch * 4u;
+    const int64_t c0 = T::kSwapped ? (int64_t)col0 * p.ld_out + row0 + ra : (int64_t)(row0 + ra) * p.ld_out + col0;
+    const bool vec = p.out_vec != 0;
+    for (int u = threadIdx.x; length > 0 && u < lines * vecs; u += T::kThreads) {
+      const int line = u / vecs, c = (u - line * vecs) * 4;
+      const uint32_t off = (uint32_t)((line0 + line) * T::kPitch + first + c) * 4u;
+      float4 x;
       if (splits == 1) {
+        x = ld_shared_f4(op_smem + off);
+      } else {
+        float4 part[8];
 #pragma unroll
-        for (int j = 0; j < kN; ++j) x[j] = ld_shared_f32(op_smem + row + c[j] * 4);
-        return;
-      }
-      float part[8][kN];
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if (s < splits) part[s][j] = ld_cluster_f32(peer[s] + row + c[j] * 4);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        x[j] = part[0][j];
+        for (int s = 0; s < 8; ++s)
+          if (s < splits) part[s] = ld_cluster_f4(peer[s] + off);
+        x = part[0];
 #pragma unroll
         for (int s = 1; s < 8; ++s)
-          if (s < splits) x[j] += part[s][j];
-      }
-    };
-    if constexpr (T::kSwapped) {
-      // C[col, row]: lanes along the rows, four columns to a warp
-      const int groups = (rows_here + 31) / 32, quads = (cols_here + 3) / 4;
-      for (int u = warp; u < groups * quads; u += warps) {
-        const int cq = u / groups, r = (u - cq * groups) * 32 + lane;
-        if (r >= rows_here) continue;
-        int c[4];
-        float x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = min(cq * 4 + j, cols_here - 1);
-        sums_at(r, c, x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (cq * 4 + j >= cols_here) break;
-          const int64_t idx = (int64_t)(col0 + c[j]) * p.ld_out + row0 + ra + r;
-          const float y = p.alpha * x[j];
-          out_store(p.out, idx, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx, p.out_dtype), y) : y, p.out_dtype);
-        }
-      }
-    } else {
-      for (int r = warp; r < rows_here; r += warps) {
-        const int64_t line = (int64_t)(row0 + ra + r) * p.ld_out + col0;
-        float x[4];
-        if (p.out_vec && cols_here == T::BN) {
-          const int c[4] = {lane * 4, lane * 4 + 1, lane * 4 + 2, lane * 4 + 3};
-          sums_at(r, c, x);
-          float4 o = make_float4(p.alpha * x[0], p.alpha * x[1], p.alpha * x[2], p.alpha * x[3]);
-          if (p.beta != 0.0f) {
-            const float4 z = out_load4(p.out, line + c[0], p.out_dtype);
-            o.x = fmaf(p.beta, z.x, o.x);
-            o.y = fmaf(p.beta, z.y, o.y);
-            o.z = fmaf(p.beta, z.z, o.z);
-            o.w = fmaf(p.beta, z.w, o.w);
+          if (s < splits) {
+            x.x += part[s].x;
+            x.y += part[s].y;
+            x.z += part[s].z;
+            x.w += part[s].w;
           }
-          out_store4(p.out, line + c[0], o, p.out_dtype);
-        } else {
-          int c[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[j] = min(lane + 32 * j, cols_here - 1);
-          sums_at(r, c, x);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (lane + 32 * j >= cols_here) break;
-            const float y = p.alpha * x[j];
-            out_store(p.out, line + c[j],
-                      p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, line + c[j], p.out_dtype), y) : y, p.out_dtype);
-          }
+      }
+      const int64_t idx = c0 + (int64_t)line * p.ld_out + c;
+      x.x *= p.alpha;
+      x.y *= p.alpha;
+      x.z *= p.alpha;
+      x.w *= p.alpha;
+      if (vec && c + 4 <= length) {
+        if (p.beta != 0.0f) {
+          const float4 z = out_load4(p.out, idx, p.out_dtype);
+          x.x = fmaf(p.beta, z.x, x.x);
+          x.y = fmaf(p.beta, z.y, x.y);
+          x.z = fmaf(p.beta, z.z, x.z);
+          x.w = fmaf(p.beta, z.w, x.w);
         }
+        out_store4(p.out, idx, x, p.out_dtype);
+      } else {
+        const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < length)
+            out_store(p.out, idx + j, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx + j, p.out_dtype), e[j]) : e[j],
+                      p.out_dtype);
       }
     }
   }

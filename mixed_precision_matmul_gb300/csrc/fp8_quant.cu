@@ -331,33 +331,39 @@ __global__ void __launch_bounds__(kThreads) fp8_quant_kernel(const __grid_consta
 
 // Each thread builds 16 bytes of an output line from the aligned 4-byte words
 // that hold them (only words with at least one byte of the line are read).
-__global__ void __launch_bounds__(256) fp8_align_kernel(const uint8_t* __restrict__ in, int64_t ld_in, int64_t rows,
-                                                        int64_t cols, uint8_t* __restrict__ out, int64_t ld_out) {
+// One launch copies one or two operands.
+__global__ void __launch_bounds__(256) fp8_align_kernel(const __grid_constant__ Fp8AlignJob ja,
+                                                        const __grid_constant__ Fp8AlignJob jb) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t per = ld_out / 16;
-  const int64_t total = rows * per;
+  const int64_t ta = ja.rows * ja.chunks, total = ta + jb.rows * jb.chunks;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = i / per, c = (i - r * per) * 16;
-    const int64_t left = cols - c;                                 // bytes of the line from here on
-    uint32_t o[4] = {0, 0, 0, 0};
-    if (left > 0) {
-      const uint8_t* src = in + r * ld_in + c;
-      const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 3u);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(src - sh);
-      uint32_t x[5];
-#pragma unroll
-      for (int j = 0; j < 5; ++j) x[j] = (4 * j - (int64_t)sh < left && (j < 4 || sh > 0)) ? __ldg(w + j) : 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __funnelshift_r(x[j], x[j + 1], 8 * sh);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t valid = left - 4 * j;                        // bytes of this word inside the line
-        if (valid <= 0) o[j] = 0;
-        else if (valid < 4) o[j] &= (1u << (8 * valid)) - 1u;
-      }
+    const Fp8AlignJob& j = i < ta ? ja : jb;
+    const int64_t k = i < ta ? i : i - ta;
+    int64_t r, ch;
+    if (total < (int64_t(1) << 31)) {                              // (64-bit division is a long routine)
+      r = (uint32_t)k / (uint32_t)j.chunks;
+      ch = (uint32_t)k - (uint32_t)r * (uint32_t)j.chunks;
+    } else {
+      r = k / j.chunks;
+      ch = k - r * j.chunks;
     }
-    *reinterpret_cast<uint4*>(out + r * ld_out + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    const int64_t c = ch * 16;
+    const int64_t left = j.cols - c;                               // bytes of the line from here on (>= 1)
+    const uint8_t* src = j.in + r * j.ld_in + c;
+    const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 3u);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(src - sh);
+    uint32_t x[5], o[4];
+#pragma unroll
+    for (int n = 0; n < 5; ++n) x[n] = (4 * n - (int64_t)sh < left && (n < 4 || sh > 0)) ? __ldg(w + n) : 0u;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      o[n] = __funnelshift_r(x[n], x[n + 1], 8 * sh);
+      const int64_t valid = left - 4 * n;                          // bytes of this word inside the line
+      if (valid <= 0) o[n] = 0;
+      else if (valid < 4) o[n] &= (1u << (8 * valid)) - 1u;
+    }
+    *reinterpret_cast<uint4*>(j.out + r * j.ld_out + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -393,11 +399,10 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams& p, int x_dtype, int format
   }
 }
 
-cudaError_t launch_fp8_align(const uint8_t* in, int64_t ld_in, int64_t rows, int64_t cols, uint8_t* out,
-                             int64_t ld_out, int sm_count, cudaStream_t stream) {
-  const int64_t total = rows * (ld_out / 16);
+cudaError_t launch_fp8_align(const Fp8AlignJob& a, const Fp8AlignJob& b, int sm_count, cudaStream_t stream) {
+  const int64_t total = a.rows * a.chunks + b.rows * b.chunks;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)min((total + 255) / 256, (int64_t)sm_count * 8));
+  cfg.gridDim = dim3((unsigned)min((total + 255) / 256, (int64_t)sm_count * 16));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -405,7 +410,7 @@ cudaError_t launch_fp8_align(const uint8_t* in, int64_t ld_in, int64_t rows, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_align_kernel, in, ld_in, rows, cols, out, ld_out);
+  return cudaLaunchKernelEx(&cfg, fp8_align_kernel, a, b);
 }
 
 }  // namespace mpg

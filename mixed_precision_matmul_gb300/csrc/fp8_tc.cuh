@@ -170,7 +170,7 @@ __device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t s
 // takes far longer to arrive than its columns take to add, so two loads of 32
 // columns are in flight.  `release` runs when all columns are in registers.
 template <int kCols, bool kColVec, class Release>
-__device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, uint32_t slot, int lane,
+__device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, uint32_t slot, f32x2 rs,
                                           Release release) {
   constexpr int kChunk = kCols >= 32 ? 32 : 16;
   constexpr int kN = kCols / kChunk;
@@ -182,9 +182,6 @@ __device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, 
   };
 #pragma unroll
   for (int c = 0; c < kFly; ++c) load(c);
-  float s = ld_shared_f32(slot + lane * 4);
-  if (!kColVec) s *= ld_shared_f32(slot + 128 + lane * 4);
-  const f32x2 rs = pack2(s, s);
 #pragma unroll
   for (int c0 = 0; c0 < kN; c0 += kFly) {
     tmem_ld_wait();

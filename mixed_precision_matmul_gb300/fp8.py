@@ -51,11 +51,11 @@ def _on_stream(stream, tensors, call):
 def _device_index(*tensors) -> int:
     """The CUDA device that all given tensors are on."""
     index = tensors[0].get_device()
-    if index < 0:
-        raise ValueError("CUDA tensors expected")
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError("operands are on different devices")
+    if index < 0:
+        raise ValueError("CUDA tensors expected")
     return index
 
 
