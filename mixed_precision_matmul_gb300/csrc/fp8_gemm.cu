@@ -52,16 +52,6 @@ struct Fp8Traits {
   static_assert(kCtasPerSm * kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
 };
 
-// 16 bytes of the shared memory of another CTA of the cluster.
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
-}
-
 template <class T>
 __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];

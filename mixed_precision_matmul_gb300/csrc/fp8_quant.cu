@@ -385,12 +385,9 @@ cudaError_t launch_fp8_quantize(const Fp8QuantParams& p, int x_dtype, int format
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((p.cols + 127) / 128) * ((p.rows + 127) / 128)));
   cfg.blockDim = dim3(kThreads);
+  // (an ordinary launch: as a programmatic dependent it costs the host 2.4 us
+  // more, of 14 a call)
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const bool tile = scale_rows != 1;
   switch (x_dtype) {
     case 0: return launch_type<float>(p, format, tile, cfg);

@@ -643,6 +643,257 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
   }
 }
 
+// ---------------------------------------------------------------------------
+// the product when there are few tiles
+// ---------------------------------------------------------------------------
+// One 128 x 128 tile per cluster of 1 .. 8 CTAs, each with a range of k.  The
+// ranges' sums meet in shared memory: every CTA reads its share of the tile's
+// rows from all of them (in rank order: the result does not depend on timing)
+// and stores it.  One launch has to fill the machine with a handful of tiles,
+// and its time is that of one CTA's range and the way in and out.
+struct DividedTraits {
+  static constexpr int kTile = 128;
+  static constexpr int BK = 64;
+  static constexpr int kRowBytes = 128;
+  static constexpr uint32_t kSwizzle = kSwizzle128B;
+  static constexpr int kInstrK = 16;
+  static constexpr int kKSteps = BK / kInstrK;
+  static constexpr int kATile = kTile * kRowBytes;
+  static constexpr int kStage = 2 * kATile;
+  static constexpr int kStages = 6;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = (2 + kEpiWarps) * 32;
+  static constexpr int kPitch = kTile + 4;                   // floats of a staged row
+  static constexpr int kMirrorPitch = kTile + 8;             // 16-bit values of a transposed one
+  static constexpr int kMirrorOffset = kTile * kPitch * 4;
+  static constexpr int kNumBars = 2 * kStages + 1;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kNumBars * 8 + 16;
+  static_assert(kMirrorOffset + kTile * kMirrorPitch * 2 <= kStages * kStage, "staging reuses the operand stages");
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+__global__ void __launch_bounds__(DividedTraits::kThreads, 1)
+    ortho_divided_kernel(const __grid_constant__ OrthoGemmParams p) {
+  using T = DividedTraits;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kStages * T::kStage);
+  uint64_t* op_full = bars;
+  uint64_t* op_empty = bars + T::kStages;
+  uint64_t* done_bar = bars + 2 * T::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const OrthoTile tc = ortho_tile(p, (int)(blockIdx.x / (uint32_t)p.splits));
+  const int row0 = tc.mb * T::kTile, col0 = tc.nb * T::kTile;
+  const int kb0 = (int)rank * p.kb_per_split;
+  const int nkb = max(0, min(p.num_k_blk, kb0 + p.kb_per_split) - kb0);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::kStages; ++i) {
+      mbar_init(&op_full[i], 1);
+      mbar_init(&op_empty[i], 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&p.map_a);
+    tma_prefetch_map(&p.map_b);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, T::kTile);
+    tmem_relinquish();
+    tc_fence_before_sync();
+  }
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  WaitCtl ctl;
+  ctl.abort = abort_flag;
+  ctl.status = p.status;
+  ctl.limit_ns = p.wait_limit_ns;
+  const uint32_t op_smem = smem_addr(smem);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int i = 0;
+      for (; i < nkb; ++i) {
+        const int st = i % T::kStages;
+        if (!mbar_wait(&op_empty[st], ((i / T::kStages) & 1u) ^ 1u, ctl)) break;
+        mbar_arrive_expect_tx(&op_full[st], T::kStage);
+        uint8_t* dst = smem + st * T::kStage;
+        const int k0 = (kb0 + i) * T::BK;
+        auto load = [&](const CUtensorMap* map, uint8_t* to, bool mn, int r) {
+          if (!mn) {
+            tma_load_3d(to, map, &op_full[st], k0, r, tc.b);
+          } else {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) tma_load_3d(to + g * T::BK * T::kRowBytes, map, &op_full[st], r + g * T::BK, k0, tc.b);
+          }
+        };
+        load(&p.map_a, dst, p.a_mn_major != 0, row0);
+        load(&p.map_b, dst + T::kATile, p.b_mn_major != 0, col0);
+      }
+      for (int j = max(0, i - T::kStages); j < i; ++j)
+        drain_wait(&op_empty[j % T::kStages], (j / T::kStages) & 1u, p.wait_limit_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_one();
+    const bool a_mn = p.a_mn_major != 0, b_mn = p.b_mn_major != 0;
+    const uint32_t idesc = make_idesc(0u /* f16 */, a_mn, b_mn, T::kTile, T::kTile);
+    const uint64_t a_desc = operand_desc<T>(op_smem, a_mn, 0), b_desc = operand_desc<T>(op_smem + T::kATile, b_mn, 0);
+    const uint32_t a_step = (a_mn ? T::kInstrK * T::kRowBytes : 32) / 16, b_step = (b_mn ? T::kInstrK * T::kRowBytes : 32) / 16;
+    const uint32_t d0 = __shfl_sync(0xffffffffu, tmem_base, 0);
+    int st = 0;
+    uint32_t st_ph = 0;
+    for (int i = 0; i < nkb; ++i) {
+      if (!warp_wait(&op_full[st], st_ph, ctl)) break;
+      tc_fence_after_sync();
+      const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < T::kKSteps; ++ks)
+          mma_f16(d0, a_desc + at + ks * a_step, b_desc + at + ks * b_step, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+        mma_commit(&op_empty[st]);
+      }
+      __syncwarp();
+      if (++st == T::kStages) {
+        st = 0;
+        st_ph ^= 1u;
+      }
+    }
+    if (leader) mma_commit(done_bar);
+    if (!warp_wait(done_bar, 0, ctl) && leader) drain_wait(done_bar, 0, p.wait_limit_ns);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ this range's sums
+    const int q = warp & 3;
+    const int wc0 = ((warp - 2) / 4) * 64;
+    if (warp_wait(done_bar, 0, ctl)) {
+      // every MMA is complete: the operand stages are free
+      tc_fence_after_sync();
+      const uint32_t t = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + wc0;
+      float v[2][32];
+      tmem_ld_32cols(t, v[0]);
+      tmem_ld_32cols(t + 32, v[1]);
+      tmem_ld_wait();
+      const uint32_t dst = op_smem + (uint32_t)((32 * q + lane) * T::kPitch + wc0) * 4u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          stage_st16(dst + (h * 32 + j) * 4, v[h][j], v[h][j + 1], v[h][j + 2], v[h][j + 3]);
+    }
+  }
+
+  // ---------------------------------------------------------------- D
+  tc_fence_before_sync();
+  if (p.splits > 1) cluster_sync_all();
+  else __syncthreads();
+  const int rows_per = ((T::kTile + p.splits - 1) / p.splits + 7) & ~7;
+  const int ra = (int)rank * rows_per;
+  const int rows_here = min(min(T::kTile, ra + rows_per), p.m - row0) - ra;
+  const int cols_here = min(T::kTile, p.n - col0);
+  const bool mirror = p.symmetric && tc.mb != tc.nb;
+  const bool live = *abort_flag == 0 && rows_here > 0;
+  const int dt = p.d_dtype;
+  uint8_t* d = static_cast<uint8_t*>(p.d) + (int64_t)tc.b * p.stride_d * (dt == kOutF32 ? 4 : 2);
+  uint16_t* mir = reinterpret_cast<uint16_t*>(smem + T::kMirrorOffset);
+  if (live) {
+    const float f = p.factor ? __ldg(p.factor + tc.b) : 1.0f;
+    const float ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
+    const float cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
+    uint32_t peer[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) peer[s] = s < p.splits ? cluster_smem_addr(op_smem, (uint32_t)s) : 0u;
+    const int c = (threadIdx.x & 31) * 4;                    // four columns of a row: a warp takes whole rows
+    for (int r = warp; r < rows_here; r += T::kThreads / 32) {
+      const int row = row0 + ra + r;
+      float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = z;
+      const bool in = c < cols_here;
+      if (p.z && in) z = out_load4(p.z + (int64_t)tc.b * p.stride_z, (int64_t)row * p.ldz + col0 + c, kOutF16);
+      const int64_t idx = (int64_t)row * p.ldd + col0 + c;
+      const bool vec = p.vec && c + 4 <= cols_here;
+      if (p.co != 0.0f && in) {
+        if (vec) y = out_load4(d, idx, dt);
+        else
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c + j < cols_here) reinterpret_cast<float*>(&y)[j] = out_load(d, idx + j, dt);
+      }
+      const uint32_t off = (uint32_t)((ra + r) * T::kPitch + c) * 4u;
+      float4 part[8];
+      part[0] = p.splits == 1 ? stage_ld16(op_smem + off) : ld_cluster_f4(peer[0] + off);
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < p.splits) part[s] = ld_cluster_f4(peer[s] + off);
+      float4 o = part[0];
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < p.splits) {
+          o.x += part[s].x;
+          o.y += part[s].y;
+          o.z += part[s].z;
+          o.w += part[s].w;
+        }
+      o.x = fmaf(p.co, y.x, fmaf(cz, z.x, ca * o.x));
+      o.y = fmaf(p.co, y.y, fmaf(cz, z.y, ca * o.y));
+      o.z = fmaf(p.co, y.z, fmaf(cz, z.z, ca * o.z));
+      o.w = fmaf(p.co, y.w, fmaf(cz, z.w, ca * o.w));
+      if (vec) {
+        out_store4(d, idx, o, dt);
+      } else {
+        const float e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < cols_here) out_store(d, idx + j, e[j], dt);
+      }
+      if (mirror) {
+        // (D is fp16 here: the operator's own S and B)
+        const uint32_t w0 = pack_f16x2(o.x, o.y), w1 = pack_f16x2(o.z, o.w);
+        mir[(c + 0) * T::kMirrorPitch + r] = (uint16_t)w0;
+        mir[(c + 1) * T::kMirrorPitch + r] = (uint16_t)(w0 >> 16);
+        mir[(c + 2) * T::kMirrorPitch + r] = (uint16_t)w1;
+        mir[(c + 3) * T::kMirrorPitch + r] = (uint16_t)(w1 >> 16);
+      }
+    }
+  }
+  if (mirror) {
+    __syncthreads();
+    if (live) {
+      // rows of D^T: 8 values (16 bytes) a thread
+      const int vecs = rows_per / 8;
+      for (int u = threadIdx.x; u < cols_here * vecs; u += T::kThreads) {
+        const int c = u / vecs, r = (u - c * vecs) * 8;
+        if (r >= rows_here) continue;
+        uint16_t* to = reinterpret_cast<uint16_t*>(d) + (int64_t)(col0 + c) * p.ldd + row0 + ra + r;
+        const uint16_t* from = mir + c * T::kMirrorPitch + r;
+        if (r + 8 <= rows_here) {
+          *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+        } else {
+          for (int j = 0; j < rows_here - r; ++j) to[j] = from[j];
+        }
+      }
+    }
+  }
+  // no CTA exits while another may still read its shared memory
+  __syncwarp();
+  if (p.splits > 1) cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, T::kTile);
+  }
+}
+
 template <class T>
 void fill(OrthoKernel* out) {
   out->fn = reinterpret_cast<const void*>(&ortho_gemm_kernel<T>);
@@ -660,9 +911,15 @@ cudaError_t launch_scale_type(const OrthoScaleParams& p, cudaLaunchConfig_t& cfg
 
 }  // namespace
 
-void ortho_lookup(bool pair, OrthoKernel* out) {
-  if (pair) fill<OrthoTraits<true>>(out);
-  else fill<OrthoTraits<false>>(out);
+void ortho_lookup(OrthoForm form, OrthoKernel* out) {
+  if (form == OrthoForm::kPair) {
+    fill<OrthoTraits<true>>(out);
+  } else if (form == OrthoForm::kOne) {
+    fill<OrthoTraits<false>>(out);
+  } else {
+    *out = OrthoKernel{reinterpret_cast<const void*>(&ortho_divided_kernel), DividedTraits::kThreads,
+                       DividedTraits::kSmemBytes, DividedTraits::kTile, 1};
+  }
 }
 
 cudaError_t launch_ortho_scale(const OrthoScaleParams& p, int g_dtype, cudaStream_t stream) {

@@ -44,6 +44,7 @@ struct OrthoGemmParams {
   float ca, cz, co;
   const float* factor;        // per matrix, or null
   int32_t ca_power, cz_power; // ca and cz are multiplied by factor to these powers (0, 1, 2)
+  int32_t splits, kb_per_split;   // divided form: ranges of k, each on a CTA of one cluster
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -54,6 +55,7 @@ struct OrthoKernel {
   int tile;                   // tiles are tile x tile
   int ctas;                   // CTAs that share a tile
 };
-void ortho_lookup(bool pair, OrthoKernel* out);
+enum class OrthoForm { kOne, kPair, kDivided };
+void ortho_lookup(OrthoForm form, OrthoKernel* out);
 
 }  // namespace mpg

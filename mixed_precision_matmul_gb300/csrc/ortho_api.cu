@@ -55,45 +55,56 @@ mpg_status operand_map(CUtensorMap* map, const Matrix& x, bool mn_major, int64_t
 }
 
 mpg_status launch_gemm(DeviceInfo* dev, OrthoGemmParams p, cudaStream_t stream) {
-  // Tiles of 256 x 256 on CTA pairs read half the operand bytes per flop, but
-  // leave more of the machine idle when there are few tiles.  A 128 x 128
-  // tile keeps the shared memory of its SM busy for as long as a pair takes
-  // for four times the work on two SMs (k = 4096: 22 us against 25 us), so
-  // single CTAs pay only where they need fewer rounds.
-  OrthoKernel one, two;
-  ortho_lookup(false, &one);
-  ortho_lookup(true, &two);
+  OrthoKernel one, two, div;
+  ortho_lookup(OrthoForm::kOne, &one);
+  ortho_lookup(OrthoForm::kPair, &two);
+  ortho_lookup(OrthoForm::kDivided, &div);
   int clusters = 0;
   mpg_status s = resident_clusters(dev, two.fn, two.block, two.smem_bytes, 2, &clusters);
   if (s != MPG_OK) return s;
   if ((s = allow_smem(dev, one.fn, one.smem_bytes)) != MPG_OK) return s;
+  if ((s = allow_smem(dev, div.fn, div.smem_bytes)) != MPG_OK) return s;
   auto tiles = [&](int64_t t) {
     const int64_t mb = (p.m + t - 1) / t, nb = (p.n + t - 1) / t;
-    return p.symmetric ? nb * (nb + 1) / 2 : mb * nb;
+    return (p.symmetric ? nb * (nb + 1) / 2 : mb * nb) * p.batch;
   };
-  const int64_t t1 = tiles(one.tile), t2 = tiles(two.tile);
-  const int64_t r1 = (t1 * p.batch + dev->sm_count - 1) / dev->sm_count;
-  const int64_t r2 = (t2 * p.batch + clusters - 1) / clusters;
-  const bool pair = r2 < r1;
-  const OrthoKernel& k = pair ? two : one;
-  const int64_t per = pair ? t2 : t1;
-  if (per * p.batch > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
+  const int64_t t1 = tiles(one.tile), t2 = tiles(two.tile), sms = dev->sm_count;
+  const int64_t kb = (p.k + 63) / 64;
+  // Few tiles: k is divided, as long as each CTA has an SM of its own and two
+  // blocks of k.
+  int64_t splits = 1;
+  while (splits < 8 && t1 * (splits + 1) <= sms && kb / (splits + 1) >= 2) ++splits;
+  const int64_t per = (kb + splits - 1) / splits;
+  splits = (kb + per - 1) / per;
+  // A 128 x 128 tile on one CTA takes 0.40 us for a block of k (its operands'
+  // way to the SM), a pair's 256 x 256 tile 0.34 us for four times the work on
+  // two SMs, so single CTAs pay only where they need fewer rounds, or where k
+  // is divided (about 1 us for the exchange).
+  const double time1 = (double)((t1 + sms - 1) / sms) * 0.40 * (double)per + (splits > 1 ? 1.0 : 0.0);
+  const double time2 = (double)((t2 + clusters - 1) / clusters) * 0.34 * (double)kb;
+  const bool pair = time2 < time1;
+  const bool divided = !pair && t1 <= sms;
+  const OrthoKernel& k = pair ? two : divided ? div : one;
+  const int64_t all = pair ? t2 : t1;
+  if (all * splits > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
   p.num_m_blk = (p.m + k.tile - 1) / k.tile;
   p.num_n_blk = (p.n + k.tile - 1) / k.tile;
-  p.num_k_blk = (p.k + 63) / 64;
-  p.tiles_per_matrix = (int32_t)per;
-  p.num_tiles = (int32_t)(per * p.batch);
+  p.num_k_blk = (int32_t)kb;
+  p.tiles_per_matrix = (int32_t)(all / p.batch);
+  p.num_tiles = (int32_t)all;
+  p.splits = divided ? (int32_t)splits : 1;
+  p.kb_per_split = (int32_t)per;
   p.group_m = pair ? 8 : 16;
   p.status = dev->status;
   p.wait_limit_ns = kDefaultWaitNs;
-  const int64_t workers = std::min<int64_t>(p.num_tiles, pair ? clusters : dev->sm_count);
+  const int64_t ctas = divided ? all * splits : pair ? 2 * std::min<int64_t>(all, clusters) : std::min(all, sms);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(workers * k.ctas));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3((unsigned)k.block);
   cfg.dynamicSmemBytes = (size_t)k.smem_bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  cfg.numAttrs = (unsigned)launch_attributes(attr, k.ctas);
+  cfg.numAttrs = (unsigned)launch_attributes(attr, divided ? (int)splits : k.ctas);
   cfg.attrs = attr;
   void* args[] = {&p};
   cudaError_t e = cudaLaunchKernelExC(&cfg, k.fn, args);
