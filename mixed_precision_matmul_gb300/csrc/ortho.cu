@@ -291,6 +291,12 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 struct OrthoTile {
   int b, mb, nb;
 };
@@ -646,7 +652,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
 // ---------------------------------------------------------------------------
 // the product when there are few tiles
 // ---------------------------------------------------------------------------
-// One 128 x 128 tile per cluster of 1 .. 8 CTAs, each with a range of k.  The
+// One 128 x 128 tile per cluster of 2 or 4 CTAs, each with a range of k.  The
 // ranges' sums meet in shared memory: every CTA reads its share of the tile's
 // rows from all of them (in rank order: the result does not depend on timing)
 // and stores it.  One launch has to fill the machine with a handful of tiles,
@@ -664,20 +670,142 @@ struct DividedTraits {
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = (2 + kEpiWarps) * 32;
   static constexpr int kPitch = kTile + 4;                   // floats of a staged row
-  static constexpr int kMirrorPitch = kTile + 8;             // 16-bit values of a transposed one
   static constexpr int kMirrorOffset = kTile * kPitch * 4;
+  static constexpr int kZBytes = kTile * kTile * 2;          // Z's elements
   static constexpr int kNumBars = 2 * kStages + 1;
-  static constexpr int kSmemBytes = 1024 + kStages * kStage + kNumBars * 8 + 16;
-  static_assert(kMirrorOffset + kTile * kMirrorPitch * 2 <= kStages * kStage, "staging reuses the operand stages");
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kZBytes + kNumBars * 8 + 16;
+  static_assert(kMirrorOffset + kTile * kTile * 2 <= kStages * kStage, "staging reuses the operand stages");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
+
+// Where a CTA's share of the tile's rows goes.
+struct DividedOut {
+  uint8_t* d;            // this matrix of D
+  int row0, col0;        // of the share's first row, of the tile
+  float ca, cz;
+  uint16_t* mir;         // staged transpose, or null
+};
+
+// Position of (column c, row r) in the staged transpose: lines of 128 16-bit
+// values, chunk r / 8 at slot (r / 8) ^ ((c / 4) & 15), so that the lanes of a
+// warp, four columns apart, reach eight groups of banks (unswizzled, two: the
+// stores then took longer than the product).
+__device__ __forceinline__ uint32_t mirror_at(int c, int r) {
+  return (uint32_t)(c * 128 + (((r >> 3) ^ ((c >> 2) & 15)) << 3) + (r & 7));
+}
+
+constexpr int kDividedGroup = 4;   // rows that a warp takes at a time
+
+// Z's elements of a warp's rows of the share, copied to shared memory beside
+// the products (rows of 128 16-bit values, four a lane, zeros beyond D).
+__device__ __forceinline__ void divided_fetch_z(const OrthoGemmParams& p, const DividedOut& out, int b, uint32_t zs,
+                                                int r0, int rows, int rows_here, int cols_here, int lane) {
+  for (int i = 0; i < rows; ++i) {
+    const int r = r0 + i;
+    const bool in = p.z && r < rows_here && lane * 4 < cols_here;
+    const uint16_t* src =
+        in ? p.z + (int64_t)b * p.stride_z + (int64_t)(out.row0 + r) * p.ldz + out.col0 + lane * 4 : p.z;
+    if (p.z)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(zs + r * 256 + lane * 8), "l"(src),
+                   "r"(in ? 8 : 0)
+                   : "memory");
+  }
+}
+
+// A warp's rows of the share (neighbours, so that two rows' values of a column
+// go to the transpose in one store), four at a time; four columns a lane.  The
+// ranges' sums of a group are loaded before the first is added.  The loop over
+// groups stays rolled: a launch runs this code once.
+template <int kSplits>
+__device__ __forceinline__ void divided_rows(const OrthoGemmParams& p, const DividedOut& out, uint32_t op_smem,
+                                             uint32_t zs, int ra, int rows_here, int cols_here, int warp, int lane) {
+  using T = DividedTraits;
+  constexpr int kRows = T::kTile / kSplits / 8;                       // of one warp
+  constexpr int kAtOnce = kDividedGroup;
+  static_assert(kRows % kAtOnce == 0, "rows in groups");
+  uint32_t peer[kSplits];
+#pragma unroll
+  for (int s = 0; s < kSplits; ++s) peer[s] = cluster_smem_addr(op_smem, (uint32_t)s);
+  const int c = lane * 4;
+  const int dt = p.d_dtype;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kRows; i0 += kAtOnce) {
+    float4 part[kAtOnce][kSplits];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+      for (int s = 0; s < kSplits; ++s) {
+        const uint32_t off = (uint32_t)((ra + warp * kRows + i0 + i) * T::kPitch + c) * 4u;
+        part[i][s] = ld_cluster_f4(peer[s] + off);
+      }
+    uint32_t before[2];                                     // the even row's values, as fp16
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int r = warp * kRows + i0 + i;
+      float4 o = part[i][0];
+#pragma unroll
+      for (int s = 1; s < kSplits; ++s) {
+        o.x += part[i][s].x;
+        o.y += part[i][s].y;
+        o.z += part[i][s].z;
+        o.w += part[i][s].w;
+      }
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (p.z) {
+        const uint2 w = ld_shared_u2(zs + r * 256 + lane * 8);
+        __half2 h0, h1;
+        memcpy(&h0, &w.x, 4);
+        memcpy(&h1, &w.y, 4);
+        const float2 y0 = __half22float2(h0), y1 = __half22float2(h1);
+        y = make_float4(y0.x, y0.y, y1.x, y1.y);
+      }
+      o.x = fmaf(out.cz, y.x, out.ca * o.x);
+      o.y = fmaf(out.cz, y.y, out.ca * o.y);
+      o.z = fmaf(out.cz, y.z, out.ca * o.z);
+      o.w = fmaf(out.cz, y.w, out.ca * o.w);
+      if (r < rows_here && c < cols_here) {
+        const int64_t idx = (int64_t)(out.row0 + r) * p.ldd + out.col0 + c;
+        if (p.vec && c + 4 <= cols_here) {
+          if (p.co != 0.0f) {
+            const float4 y = out_load4(out.d, idx, dt);
+            o.x = fmaf(p.co, y.x, o.x);
+            o.y = fmaf(p.co, y.y, o.y);
+            o.z = fmaf(p.co, y.z, o.z);
+            o.w = fmaf(p.co, y.w, o.w);
+          }
+          out_store4(out.d, idx, o, dt);
+        } else {
+          const float e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c + j < cols_here)
+              out_store(out.d, idx + j, p.co != 0.0f ? fmaf(p.co, out_load(out.d, idx + j, dt), e[j]) : e[j], dt);
+        }
+      }
+      if (out.mir) {
+        // (D is fp16 here: the operator's own S and B)
+        const uint32_t w0 = pack_f16x2(o.x, o.y), w1 = pack_f16x2(o.z, o.w);
+        if (i & 1) {
+          uint32_t* m = reinterpret_cast<uint32_t*>(out.mir);
+          m[mirror_at(c + 0, r - 1) / 2] = __byte_perm(before[0], w0, 0x5410);
+          m[mirror_at(c + 1, r - 1) / 2] = __byte_perm(before[0], w0, 0x7632);
+          m[mirror_at(c + 2, r - 1) / 2] = __byte_perm(before[1], w1, 0x5410);
+          m[mirror_at(c + 3, r - 1) / 2] = __byte_perm(before[1], w1, 0x7632);
+        } else {
+          before[0] = w0;
+          before[1] = w1;
+        }
+      }
+    }
+  }
+}
 
 __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
     ortho_divided_kernel(const __grid_constant__ OrthoGemmParams p) {
   using T = DividedTraits;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kStages * T::kStage);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kStages * T::kStage + T::kZBytes);
   uint64_t* op_full = bars;
   uint64_t* op_empty = bars + T::kStages;
   uint64_t* done_bar = bars + 2 * T::kStages;
@@ -719,6 +847,18 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
   ctl.status = p.status;
   ctl.limit_ns = p.wait_limit_ns;
   const uint32_t op_smem = smem_addr(smem);
+
+  // this CTA's share of the tile's rows, and Z's elements there
+  const int rows_per = T::kTile / p.splits;                  // (2 or 4 ranges)
+  const int ra = (int)rank * rows_per;
+  const int rows_here = min(rows_per, p.m - row0 - ra);
+  const int cols_here = min(T::kTile, p.n - col0);
+  DividedOut out;
+  out.d = static_cast<uint8_t*>(p.d) + (int64_t)tc.b * p.stride_d * (p.d_dtype == kOutF32 ? 4 : 2);
+  out.row0 = row0 + ra;
+  out.col0 = col0;
+  out.mir = p.symmetric && tc.mb != tc.nb ? reinterpret_cast<uint16_t*>(smem + T::kMirrorOffset) : nullptr;
+  const uint32_t zs = op_smem + T::kStages * T::kStage;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -778,6 +918,7 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
     // ------------------------------------------------------------ this range's sums
     const int q = warp & 3;
     const int wc0 = ((warp - 2) / 4) * 64;
+    divided_fetch_z(p, out, tc.b, zs, (warp - 2) * (rows_per / 8), rows_per / 8, rows_here, cols_here, lane);
     if (warp_wait(done_bar, 0, ctl)) {
       // every MMA is complete: the operand stages are free
       tc_fence_after_sync();
@@ -786,6 +927,10 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
       tmem_ld_32cols(t, v[0]);
       tmem_ld_32cols(t + 32, v[1]);
       tmem_ld_wait();
+      if (nkb == 0) {                                        // an empty last range
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[0][j] = v[1][j] = 0.0f;
+      }
       const uint32_t dst = op_smem + (uint32_t)((32 * q + lane) * T::kPitch + wc0) * 4u;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -793,81 +938,27 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
         for (int j = 0; j < 32; j += 4)
           stage_st16(dst + (h * 32 + j) * 4, v[h][j], v[h][j + 1], v[h][j + 2], v[h][j + 3]);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   // ---------------------------------------------------------------- D
   tc_fence_before_sync();
-  if (p.splits > 1) cluster_sync_all();
-  else __syncthreads();
-  const int rows_per = ((T::kTile + p.splits - 1) / p.splits + 7) & ~7;
-  const int ra = (int)rank * rows_per;
-  const int rows_here = min(min(T::kTile, ra + rows_per), p.m - row0) - ra;
-  const int cols_here = min(T::kTile, p.n - col0);
-  const bool mirror = p.symmetric && tc.mb != tc.nb;
+  cluster_sync_all();
   const bool live = *abort_flag == 0 && rows_here > 0;
-  const int dt = p.d_dtype;
-  uint8_t* d = static_cast<uint8_t*>(p.d) + (int64_t)tc.b * p.stride_d * (dt == kOutF32 ? 4 : 2);
-  uint16_t* mir = reinterpret_cast<uint16_t*>(smem + T::kMirrorOffset);
-  if (live) {
+  if (live && warp >= 2) {
     const float f = p.factor ? __ldg(p.factor + tc.b) : 1.0f;
-    const float ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
-    const float cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
-    uint32_t peer[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s) peer[s] = s < p.splits ? cluster_smem_addr(op_smem, (uint32_t)s) : 0u;
-    const int c = (threadIdx.x & 31) * 4;                    // four columns of a row: a warp takes whole rows
-    for (int r = warp; r < rows_here; r += T::kThreads / 32) {
-      const int row = row0 + ra + r;
-      float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = z;
-      const bool in = c < cols_here;
-      if (p.z && in) z = out_load4(p.z + (int64_t)tc.b * p.stride_z, (int64_t)row * p.ldz + col0 + c, kOutF16);
-      const int64_t idx = (int64_t)row * p.ldd + col0 + c;
-      const bool vec = p.vec && c + 4 <= cols_here;
-      if (p.co != 0.0f && in) {
-        if (vec) y = out_load4(d, idx, dt);
-        else
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (c + j < cols_here) reinterpret_cast<float*>(&y)[j] = out_load(d, idx + j, dt);
-      }
-      const uint32_t off = (uint32_t)((ra + r) * T::kPitch + c) * 4u;
-      float4 part[8];
-      part[0] = p.splits == 1 ? stage_ld16(op_smem + off) : ld_cluster_f4(peer[0] + off);
-#pragma unroll
-      for (int s = 1; s < 8; ++s)
-        if (s < p.splits) part[s] = ld_cluster_f4(peer[s] + off);
-      float4 o = part[0];
-#pragma unroll
-      for (int s = 1; s < 8; ++s)
-        if (s < p.splits) {
-          o.x += part[s].x;
-          o.y += part[s].y;
-          o.z += part[s].z;
-          o.w += part[s].w;
-        }
-      o.x = fmaf(p.co, y.x, fmaf(cz, z.x, ca * o.x));
-      o.y = fmaf(p.co, y.y, fmaf(cz, z.y, ca * o.y));
-      o.z = fmaf(p.co, y.z, fmaf(cz, z.z, ca * o.z));
-      o.w = fmaf(p.co, y.w, fmaf(cz, z.w, ca * o.w));
-      if (vec) {
-        out_store4(d, idx, o, dt);
-      } else {
-        const float e[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c + j < cols_here) out_store(d, idx + j, e[j], dt);
-      }
-      if (mirror) {
-        // (D is fp16 here: the operator's own S and B)
-        const uint32_t w0 = pack_f16x2(o.x, o.y), w1 = pack_f16x2(o.z, o.w);
-        mir[(c + 0) * T::kMirrorPitch + r] = (uint16_t)w0;
-        mir[(c + 1) * T::kMirrorPitch + r] = (uint16_t)(w0 >> 16);
-        mir[(c + 2) * T::kMirrorPitch + r] = (uint16_t)w1;
-        mir[(c + 3) * T::kMirrorPitch + r] = (uint16_t)(w1 >> 16);
-      }
+    out.ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
+    out.cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
+    switch (p.splits) {
+      case 2: divided_rows<2>(p, out, op_smem, zs, ra, rows_here, cols_here, warp - 2, lane); break;
+      default: divided_rows<4>(p, out, op_smem, zs, ra, rows_here, cols_here, warp - 2, lane); break;
     }
   }
-  if (mirror) {
+  // the other CTAs' shared memory has been read: only that is announced
+  // (waiting for the stores as well takes a microsecond)
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  if (out.mir) {
     __syncthreads();
     if (live) {
       // rows of D^T: 8 values (16 bytes) a thread
@@ -875,8 +966,8 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
       for (int u = threadIdx.x; u < cols_here * vecs; u += T::kThreads) {
         const int c = u / vecs, r = (u - c * vecs) * 8;
         if (r >= rows_here) continue;
-        uint16_t* to = reinterpret_cast<uint16_t*>(d) + (int64_t)(col0 + c) * p.ldd + row0 + ra + r;
-        const uint16_t* from = mir + c * T::kMirrorPitch + r;
+        uint16_t* to = reinterpret_cast<uint16_t*>(out.d) + (int64_t)(col0 + c) * p.ldd + row0 + ra + r;
+        const uint16_t* from = out.mir + mirror_at(c, r);
         if (r + 8 <= rows_here) {
           *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
         } else {
@@ -885,13 +976,12 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
       }
     }
   }
-  // no CTA exits while another may still read its shared memory
-  __syncwarp();
-  if (p.splits > 1) cluster_sync_all();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem_base, T::kTile);
   }
+  // no CTA exits while another may still read its shared memory
+  asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
 template <class T>

@@ -70,23 +70,25 @@ mpg_status launch_gemm(DeviceInfo* dev, OrthoGemmParams p, cudaStream_t stream) 
   };
   const int64_t t1 = tiles(one.tile), t2 = tiles(two.tile), sms = dev->sm_count;
   const int64_t kb = (p.k + 63) / 64;
-  // Few tiles: k is divided, as long as each CTA has an SM of its own and two
-  // blocks of k.
+  // The form that ends first, by what the forms take on a GB300 (us, from
+  // their times at 64^2 .. 2048^2): a way in and out, and a time for each
+  // block of 64 k in each round of tiles.  A 128 x 128 tile on one CTA is
+  // bound by its operands' way to the SM; a pair's 256 x 256 tile does four
+  // times the work on two SMs in hardly more time a block, but takes longer to
+  // store; with few tiles k is divided among up to 4 CTAs (one to an SM), which
+  // exchange their sums.
+  constexpr double kOneEdge = 4.3, kDividedEdge = 5.4, kPairEdge = 7.5, kOneBlock = 0.29, kPairBlock = 0.31;
   int64_t splits = 1;
-  while (splits < 8 && t1 * (splits + 1) <= sms && kb / (splits + 1) >= 2) ++splits;
+  while (splits < 4 && t1 * splits * 2 <= sms && kb / (splits * 2) >= 1) splits *= 2;   // (8: slower, 128 x 4096: 28 against 19 us a step)
   const int64_t per = (kb + splits - 1) / splits;
-  splits = (kb + per - 1) / per;
-  // A 128 x 128 tile on one CTA takes 0.40 us for a block of k (its operands'
-  // way to the SM), a pair's 256 x 256 tile 0.34 us for four times the work on
-  // two SMs, so single CTAs pay only where they need fewer rounds, or where k
-  // is divided (about 1 us for the exchange).
-  const double time1 = (double)((t1 + sms - 1) / sms) * 0.40 * (double)per + (splits > 1 ? 1.0 : 0.0);
-  const double time2 = (double)((t2 + clusters - 1) / clusters) * 0.34 * (double)kb;
-  const bool pair = time2 < time1;
-  const bool divided = !pair && t1 <= sms;
+  const double time_one = kOneEdge + (double)((t1 + sms - 1) / sms * kb) * kOneBlock;
+  const double time_div = kDividedEdge + (double)per * kOneBlock;
+  const double time_pair = kPairEdge + (double)((t2 + clusters - 1) / clusters * kb) * kPairBlock;
+  const bool divided = splits > 1 && time_div < std::min(time_one, time_pair);
+  const bool pair = !divided && time_pair < time_one;
   const OrthoKernel& k = pair ? two : divided ? div : one;
   const int64_t all = pair ? t2 : t1;
-  if (all * splits > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
+  if (all > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
   p.num_m_blk = (p.m + k.tile - 1) / k.tile;
   p.num_n_blk = (p.n + k.tile - 1) / k.tile;
   p.num_k_blk = (int32_t)kb;

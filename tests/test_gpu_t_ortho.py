@@ -103,6 +103,8 @@ def test_one_step_within_its_roundings(b, m, n, dtype, out):
     (1, 256, 1000, "bf16"), (2, 768, 500, "fp32"), (1, 1030, 1025, "bf16"), (20, 520, 260, "bf16"),
     (76, 256, 256, "bf16"),                            # enough tiles for pairs of CTAs
     (10, 700, 900, "fp32"),
+    (1, 100, 576, "bf16"),                             # 9 blocks of 64: a division that leaves the last range empty
+    (1, 384, 1100, "bf16"), (1, 260, 2000, "fp16"),
 ])
 def test_five_steps(b, m, n, dtype):
     g = momentum(b, m, n, m * 3 + n, dtype)
