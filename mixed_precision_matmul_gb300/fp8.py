@@ -75,21 +75,19 @@ def fp8_quantize_raw(rows, cols, X, ldx, x_dtype, fmt, scale_rows, Q, ldq, S, s_
     return st
 
 
-def _codes(rows, cols, dtype, device):
-    """(rows x cols 8-bit tensor whose lines start on 16-byte boundaries, leading dimension)."""
-    ld = (cols + 15) & ~15
-    t = _types()[0].empty((rows, ld), dtype=dtype, device=device)
-    return (t if ld == cols else t[:, :cols]), max(ld, 1)
-
-
-def _scales(rows, cols, scale_rows, device):
-    """(scales of a rows x cols matrix, row stride, k stride).  Per-row scales lie
-    block by block, which is how the product reads them fastest."""
-    torch = _types()[0]
-    kb = -(-cols // BLOCK)
+def _form(rows, cols, code, scale_rows, device):
+    """(codes, their leading dimension, scales, row stride, k stride) of a rows x
+    cols matrix: lines of codes start on 16-byte boundaries, and the scales of
+    single rows lie block by block, which is how the product reads them
+    fastest."""
+    empty = _types()[0].empty_strided
+    ld = (cols + 15) & ~15 or 1
+    q = empty((rows, cols), (ld, 1), dtype=code, device=device)
+    kb = (cols + BLOCK - 1) // BLOCK
     if scale_rows == 1:
-        return torch.empty_strided((rows, kb), (1, rows), dtype=torch.float32, device=device), 1, rows
-    return torch.empty((-(-rows // BLOCK), kb), dtype=torch.float32, device=device), kb, 1
+        return q, ld, empty((rows, kb), (1, rows or 1), device=device, dtype=_types()[0].float32), 1, rows or 1
+    sr = (rows + BLOCK - 1) // BLOCK
+    return q, ld, empty((sr, kb), (kb or 1, 1), device=device, dtype=_types()[0].float32), kb or 1, 1
 
 
 def fp8_quantize(x, fmt="e4m3", block: str = "row", transpose: bool = False, stream=None):
@@ -110,38 +108,41 @@ def fp8_quantize(x, fmt="e4m3", block: str = "row", transpose: bool = False, str
     code = dtypes.get(fmt)
     if code is None:
         raise ValueError(f"unknown 8-bit format {fmt!r}")
-    if block not in ("row", "tile"):
+    scale_rows = 1 if block == "row" else BLOCK
+    if scale_rows == BLOCK and block != "tile":
         raise ValueError("block is 'row' or 'tile'")
     if x.dim() != 2:
         raise ValueError("a 2-D tensor is expected")
     x_dtype = codes.get(x.dtype)
     if x_dtype is None:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    index = _device_index(x)
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("CUDA tensors expected")
     if index != torch.cuda.current_device():
         return _on_device(index, lambda: fp8_quantize(x, fmt, block, transpose))
     rows, cols = x.shape
     ldx, unit = x.stride()
-    if rows and cols > 1 and unit != 1:
+    if unit != 1 and rows and cols > 1:
         raise ValueError("x must be row-major with unit column stride")
     if rows < 2:
-        ldx = max(cols, 1)
-    if ldx < cols:
+        ldx = cols or 1
+    elif ldx < cols:
         raise ValueError("the rows of x overlap")
     device = x.device
-    scale_rows = 1 if block == "row" else BLOCK
-    q, ldq = _codes(rows, cols, code, device)
-    s, s_row, s_k = _scales(rows, cols, scale_rows, device)
-    qt = st = None
-    t_args = (0, 0, 0, 0, 0)
-    if transpose:
-        qt, ldqt = _codes(cols, rows, code, device)
-        st, st_row, st_k = _scales(cols, rows, scale_rows, device)
-        t_args = (qt.data_ptr(), ldqt, st.data_ptr(), st_row, st_k)
+    q, ldq, s, s_row, s_k = _form(rows, cols, code, scale_rows, device)
+    if not transpose:
+        if rows and cols:
+            _m._check(_m.lib().mpg_fp8_quantize(rows, cols, x.data_ptr(), ldx, x_dtype, fmt, scale_rows, q.data_ptr(),
+                                                ldq, s.data_ptr(), s_row, s_k, None, 0, None, 0, 0,
+                                                _raw_stream()(index)))
+        return q, s
+    qt, ldqt, st, st_row, st_k = _form(cols, rows, code, scale_rows, device)
     if rows and cols:
-        fp8_quantize_raw(rows, cols, x.data_ptr(), ldx, x_dtype, fmt, scale_rows, q.data_ptr(), ldq, s.data_ptr(),
-                         s_row, s_k, *t_args, _raw_stream()(index))
-    return (q, s, qt, st) if transpose else (q, s)
+        _m._check(_m.lib().mpg_fp8_quantize(rows, cols, x.data_ptr(), ldx, x_dtype, fmt, scale_rows, q.data_ptr(), ldq,
+                                            s.data_ptr(), s_row, s_k, qt.data_ptr(), ldqt, st.data_ptr(), st_row, st_k,
+                                            _raw_stream()(index)))
+    return q, s, qt, st
 
 
 def gemm_fp8_raw(m, n, k, A, B, C, ldc, alpha, beta, workspace=0, workspace_bytes=0, stream=0, opts=None,
@@ -156,32 +157,36 @@ def gemm_fp8_raw(m, n, k, A, B, C, ldc, alpha, beta, workspace=0, workspace_byte
     return st
 
 
-def _operand(t, scale, name, formats):
+def _operand(t, scale, name, index):
     """(description of an 8-bit tensor and its scales, rows, k)."""
-    if t.dim() != 2 or scale.dim() != 2:
-        raise ValueError(f"{name} and its scales are 2-D tensors")
+    torch, formats, _, _ = _types()
     fmt = formats.get(t.dtype)
     if fmt is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if scale.dtype != _types()[0].float32:
+    if scale.dtype != torch.float32:
         raise TypeError(f"{name}: scales must be fp32")
+    if t.get_device() != index or scale.get_device() != index:
+        raise ValueError("operands are on different devices" if index >= 0 else "CUDA tensors expected")
+    if t.dim() != 2 or scale.dim() != 2:
+        raise ValueError(f"{name} and its scales are 2-D tensors")
     rows, k = t.shape
+    ld, unit = t.stride()
     sr, sk = scale.shape
-    if sk == (k + BLOCK - 1) // BLOCK and sr == rows:
+    s_row, s_k = scale.stride()
+    kb = (k + BLOCK - 1) // BLOCK
+    if sk == kb and sr == rows:
         scale_rows = 1
-    elif sk == (k + BLOCK - 1) // BLOCK and sr == (rows + BLOCK - 1) // BLOCK:
+    elif sk == kb and sr == (rows + BLOCK - 1) // BLOCK:
         scale_rows = BLOCK
     else:
         raise ValueError(f"{name}: scales of shape {tuple(scale.shape)} fit neither 1 x 128 nor 128 x 128 blocks of "
                          f"{tuple(t.shape)}")
-    ld, unit = t.stride()
-    if k > 1 and unit != 1 and rows:
+    if unit != 1 and k > 1 and rows:
         raise ValueError(f"{name} must be row-major with unit column stride")
     if rows < 2:
         ld = k
     elif ld < k:
         raise ValueError(f"the rows of {name} overlap")
-    s_row, s_k = scale.stride()
     return _m.Fp8Operand(t.data_ptr(), ld or 1, fmt, scale_rows, scale.data_ptr(), s_row, s_k), rows, k
 
 
@@ -198,15 +203,17 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
     the gradient of its input ``gemm_fp8(dyq, dys, wqt, wst)`` and that of its
     weights ``gemm_fp8(dyqt, dyst, xqt, xst)``.
     """
-    torch, formats, _, codes = _types()
+    torch, _, _, codes = _types()
     if stream is not None:
         return _on_stream(stream, [A, a_scale, B, b_scale, C, workspace],
                           lambda: gemm_fp8(A, a_scale, B, b_scale, C, alpha, beta, out_dtype, workspace, opts))
-    index = _device_index(A, a_scale, B, b_scale, C, workspace)
+    index = A.get_device()
+    if index < 0:
+        raise ValueError("CUDA tensors expected")
     if index != torch.cuda.current_device():
         return _on_device(index, lambda: gemm_fp8(A, a_scale, B, b_scale, C, alpha, beta, out_dtype, workspace, opts))
-    a, m, k = _operand(A, a_scale, "A", formats)
-    b, n, kb = _operand(B, b_scale, "B", formats)
+    a, m, k = _operand(A, a_scale, "A", index)
+    b, n, kb = _operand(B, b_scale, "B", index)
     if kb != k:
         raise ValueError("A and B have different k")
     if C is None:
@@ -215,6 +222,8 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
         C = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=A.device)
         ldc = n
     else:
+        if C.get_device() != index:
+            raise ValueError("operands are on different devices")
         if out_dtype is not None and C.dtype != out_dtype:
             raise ValueError("C has another dtype than out_dtype")
         if C.shape != (m, n):
@@ -245,6 +254,9 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
     if workspace is not None:
+        if workspace.get_device() != index:
+            raise ValueError("operands are on different devices")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    gemm_fp8_raw(m, n, k, a, b, C.data_ptr(), ldc, alpha, beta, ws, ws_bytes, _raw_stream()(index), opts)
+    _m._check(_m.lib().mpg_gemm_fp8(m, n, k, a, b, C.data_ptr(), ldc, alpha, beta, ws, ws_bytes, _raw_stream()(index),
+                                    opts))
     return C
