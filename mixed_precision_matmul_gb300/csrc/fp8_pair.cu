@@ -264,16 +264,15 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
       const PairTile tc = pair_tile(p, t);
       // this lane's columns (clamped to the operand's last line)
       const int c0 = (warp - 2) * T::kCols + lane;
-      constexpr int kN = T::kCols / 32;
-      const float* src[kN];
+      const float* src[4];
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
+      for (int i = 0; i < 4; ++i)
         src[i] = p.sc + (int64_t)(min(tc.cb * T::kTile + c0 + 32 * i, p.cols - 1) >> p.sc_shift) * p.sc_row;
       for (int kb = 0; kb < nkb; ++kb) {
         if (!warp_wait(&scale_empty[slot], ph ^ 1u, ctl)) { ok = false; break; }
         const uint32_t dst = smem_addr(scale_base) + (slot * T::kScaleSlot + c0) * 4;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
+        for (int i = 0; i < 4; ++i) {
           cp_async4(dst + i * 128, src[i]);
           src[i] += p.sc_k;
         }
@@ -343,15 +342,14 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
         if (i < 3) fetch_scales(i, i);
       }
       // Columns are read 32 at a time, two reads on their way, across the
-      // blocks of k too.  (Beside running MMAs a tcgen05.ld takes about 190
-      // cycles to arrive, five times as long as without; with one on its way
-      // a block took 4 x 190.)
+      // blocks of k too.
       constexpr int kN = T::kCols / 32;
       static_assert(kN == 4, "two pairs of reads a block");
       const uint32_t scales = smem_addr(scale_base) + half * (T::kCols * 4);
       float v[2][32];
       tmem_ld_32cols(tacc + (it & 1u) * T::kTile, v[0]);
       tmem_ld_32cols(tacc + (it & 1u) * T::kTile + 32, v[1]);
+      bool known = false;
 #pragma unroll 1
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const bool more = kb + 1 < nkb;
@@ -359,19 +357,23 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
         fetch_scales(3, kb + 3);
         const float s = rsc[0] * csc[0];
         const f32x2 rs = pack2(s, s);
-        if (T::kColVec && !warp_wait(&scale_full[slot], slot_ph, ctl)) { ok = false; break; }
+        if (T::kColVec && !__all_sync(0xffffffffu, known) && !warp_wait(&scale_full[slot], slot_ph, ctl)) { ok = false; break; }
         const uint32_t sl = scales + slot * (T::kScaleSlot * 4) - 128;
         tmem_ld_wait();
         scale_add<32, T::kColVec>(acc, v[0], sl, 0, rs);
         tmem_ld_32cols(here + 64, v[0]);
         scale_add<32, T::kColVec>(acc + 16, v[1], sl, 32, rs);
         tmem_ld_32cols(here + 96, v[1]);
-        // the barrier takes a while to answer: asked early
+        // barriers take a while to answer: asked early
         const bool ready = more && mbar_test(&acc_full[(it + 1) & 1u], ((it + 1) >> 1) & 1u);
         tmem_ld_wait();
         if (!hand_over(it, more, ready)) { ok = false; break; }
         scale_add<32, T::kColVec>(acc + 32, v[0], sl, 64, rs);
         if (more) tmem_ld_32cols(next, v[0]);
+        if constexpr (T::kColVec) {
+          const uint32_t ns = slot + 1 == T::kScaleSlots ? 0 : slot + 1;
+          known = more && mbar_test(&scale_full[ns], ns == 0 ? slot_ph ^ 1u : slot_ph);
+        }
         scale_add<32, T::kColVec>(acc + 48, v[1], sl, 96, rs);
         if (more) tmem_ld_32cols(next + 32, v[1]);
 #pragma unroll
