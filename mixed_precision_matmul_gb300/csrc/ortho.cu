@@ -438,8 +438,8 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
       bool ok = true;
       for (int t = worker; t < p.num_tiles && ok; t += workers, ++g) {
         const uint32_t ab = g % T::kAccBufs;
-        if (!warp_wait(&acc_empty[ab], ((g / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
-        if constexpr (T::kPair) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        const uint32_t ph = ((g / T::kAccBufs) & 1u) ^ 1u;
+        if (!(T::kPair ? warp_wait_relaxed(&acc_empty[ab], ph, ctl) : warp_wait(&acc_empty[ab], ph, ctl))) { ok = false; break; }
         tc_fence_after_sync();
         const uint32_t d0 = d_base + ab * T::kTile;
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) {
-            if constexpr (T::kPair) mbar_arrive_cluster(acc_empty0 + ab * 8u);
+            // (TMEM alone is handed over: a release would wait for the stores)
+            if constexpr (T::kPair) mbar_arrive_cluster_relaxed(acc_empty0 + ab * 8u);
             else mbar_arrive(&acc_empty[ab]);
           }
         }

@@ -10,7 +10,7 @@
 namespace mpg {
 
 // Blocks that sum the squares of one matrix, at most.
-constexpr int kOrthoNormBlocks = 256;
+constexpr int kOrthoNormBlocks = 384;
 
 struct OrthoScaleParams {
   const void* g;

@@ -178,9 +178,10 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
   // single entry that holds the whole norm stays within fp16
   sp.target_exp = std::min((int)std::floor(0.5 * std::log2((double)m * (double)n)), 14);
   sp.eps = eps;
-  // two loads in flight per thread at least, at most enough blocks to fill the machine
+  // blocks that fill the machine (8 to an SM), of two chunks a thread at least
   const int64_t chunks = m * (l.ldx / 8);
-  sp.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>((chunks + 511) / 512, kOrthoNormBlocks));
+  const int64_t fill = (8 * (int64_t)dev->sm_count + batch - 1) / batch;
+  sp.blocks = (int32_t)std::max<int64_t>(1, std::min(std::min((chunks + 511) / 512, fill), (int64_t)kOrthoNormBlocks));
   cudaError_t e = launch_ortho_scale(sp, (int)g_dtype, st);
   if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "scaling launch: %s", cudaGetErrorString(e));
 
