@@ -42,49 +42,28 @@ __device__ __forceinline__ float as_f32<__half>(__half v) { return __half2float(
 template <>
 __device__ __forceinline__ float as_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Elements 8c .. 8c+7 of a line (zeros beyond its end).
-template <class XT>
-__device__ __forceinline__ void read8(const XT* line, int c, int cols, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    if constexpr (sizeof(XT) == 4) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(line + c));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(line + c) + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(line + c));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint16_t l = (uint16_t)(w[i] & 0xFFFFu), h = (uint16_t)(w[i] >> 16);
-        XT lo, hi;
-        memcpy(&lo, &l, 2);
-        memcpy(&hi, &h, 2);
-        v[2 * i] = as_f32<XT>(lo);
-        v[2 * i + 1] = as_f32<XT>(hi);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? as_f32<XT>(line[c + j]) : 0.0f;
-  }
-}
-
 constexpr int kScaleThreads = 256;
-constexpr int kBatch = 4;   // loads of 16 or 32 bytes that a thread has in flight
+constexpr int kBatch = 4;   // chunks of 8 elements that a thread has in flight
 
 // The chunks of 8 elements of a matrix that one thread takes: its index, then
 // every grid's width further, as (row, chunk of the row) without divisions in
-// the loop.
+// the loop.  A matrix without gaps is one long row.
 struct ChunkWalk {
-  int64_t row;
-  int chunk, rows, per, step_rows, step_chunks;
-  __device__ __forceinline__ ChunkWalk(int per_, int rows_) : rows(rows_), per(per_) {
-    const uint32_t i = blockIdx.x * kScaleThreads + threadIdx.x, n = gridDim.x * kScaleThreads;
-    row = i / (uint32_t)per;
-    chunk = (int)(i % (uint32_t)per);
-    step_rows = (int)(n / (uint32_t)per);
-    step_chunks = (int)(n % (uint32_t)per);
+  int64_t row, chunk, rows, per, step_rows, step_chunks;
+  __device__ __forceinline__ ChunkWalk(const OrthoScaleParams& p, int64_t per_) : rows(p.flat ? 1 : p.rows), per(per_) {
+    const int64_t i = blockIdx.x * kScaleThreads + threadIdx.x, n = gridDim.x * kScaleThreads;
+    if (p.flat) {
+      per = p.rows * per_;
+      row = i < per ? 0 : 1;
+      chunk = i;
+      step_rows = 0;
+      step_chunks = n;
+    } else {
+      row = (uint32_t)i / (uint32_t)per;
+      chunk = (uint32_t)i % (uint32_t)per;
+      step_rows = (uint32_t)n / (uint32_t)per;
+      step_chunks = (uint32_t)n % (uint32_t)per;
+    }
   }
   __device__ __forceinline__ bool inside() const { return row < rows; }
   __device__ __forceinline__ void next() {
@@ -100,41 +79,54 @@ struct ChunkWalk {
 // The thread's next kBatch chunks, their loads issued together (zeros beyond
 // the matrix).
 template <class XT>
-__device__ __forceinline__ void read_batch(ChunkWalk& at, const XT* g, int64_t ldg, int cols, bool vec,
+__device__ __forceinline__ void read_batch(const OrthoScaleParams& p, ChunkWalk& at, const XT* g,
                                            float (&v)[kBatch][8]) {
+  const int64_t cols = p.flat ? (int64_t)p.rows * p.cols : p.cols;
   const XT* line[kBatch];
-  int c[kBatch];
-  bool fast = vec;
+  int left[kBatch];                        // elements of the line from there on, 8 at most
+  bool fast = p.g_vec != 0;
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    line[u] = at.inside() ? g + at.row * ldg : nullptr;
-    c[u] = at.chunk * 8;
-    fast = fast && line[u] && c[u] + 8 <= cols;
+    line[u] = g + at.row * p.ldg + at.chunk * 8;
+    left[u] = at.inside() ? (int)max((int64_t)0, min((int64_t)8, cols - at.chunk * 8)) : 0;
+    fast = fast && left[u] == 8;
     at.next();
   }
   if (fast) {
+    uint4 w[kBatch][sizeof(XT) / 2];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) read8<XT>(line[u], c[u], c[u] + 8, true, v[u]);
+    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(XT) / 2; ++h) w[u][h] = __ldg(reinterpret_cast<const uint4*>(line[u]) + h);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      XT e[8];
+      memcpy(e, w[u], sizeof(e));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = as_f32<XT>(e[j]);
+    }
   } else {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) read8<XT>(line[u], c[u], line[u] ? cols : 0, vec, v[u]);
+    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = j < left[u] ? as_f32<XT>(line[u][j]) : 0.0f;
   }
 }
 
-// Squares of 8 elements whose sum fp32 cannot hold safely, in 64 bits.  (Kept
-// out of line: 64-bit arithmetic is very slow here, and inlined it was done for
-// every element and discarded.)
-__device__ __noinline__ void add_wide(double* wide, const float (&v)[8]) {
+// Squares whose sum fp32 cannot hold safely, in 64 bits.  (Kept out of line:
+// 64-bit arithmetic is very slow here, and inlined it was done for every
+// element and discarded.)
+__device__ __noinline__ void add_wide(double* wide, const float (&v)[kBatch][8]) {
   double s = 0.0;
 #pragma unroll 1
-  for (int j = 0; j < 8; ++j) s += (double)v[j] * (double)v[j];
+  for (int j = 0; j < kBatch * 8; ++j) s += (double)v[j >> 3][j & 7] * (double)v[j >> 3][j & 7];
   *wide += s;
 }
 
 // partial[b][block] = sum of squares over the block's share of matrix b.  The
-// squares of 8 elements are added in fp32 where that is safe (the sum neither
-// near overflow nor near underflow) and in 64 bits elsewhere; so are the
-// threads' sums, always in the same order.
+// squares of a batch of elements are added in fp32 where that is safe (the sum
+// neither near overflow nor near underflow) and in 64 bits elsewhere; so are
+// the threads' sums, always in the same order.
 template <class XT>
 __global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_constant__ OrthoScaleParams p) {
   __shared__ float red[kScaleThreads / 32];
@@ -144,31 +136,43 @@ __global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_
   griddep_launch_dependents();
   const int b = blockIdx.y;
   const XT* g = reinterpret_cast<const XT*>(p.g) + (int64_t)b * p.stride_g;
-  ChunkWalk at((p.cols + 7) / 8, p.rows);
+  ChunkWalk at(p, (p.cols + 7) / 8);
   float sum = 0.0f;
   bool unsafe = false;
   while (at.inside()) {
     float v[kBatch][8];
-    read_batch<XT>(at, g, p.ldg, p.cols, p.g_vec != 0, v);
+    read_batch<XT>(p, at, g, v);
+    float s[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      float s = 0.0f, any = 0.0f;
+    for (int u = 0; u < kBatch; ++u) s[u] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s = fmaf(v[u][j], v[u][j], s);
-        any = fmaxf(any, fabsf(v[u][j]));
-      }
-      if ((s >= 1e-30f && s <= 1e30f) || (s == 0.0f && any == 0.0f)) {
-        sum += s;
-      } else {
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) s[u] = fmaf(v[u][j], v[u][j], s[u]);
+    const float batch = (s[0] + s[1]) + (s[2] + s[3]);
+    if (batch >= 1e-28f && batch <= 1e30f) {
+      sum += batch;
+    } else {
+      bool any = false;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) any = any || v[u][j] != 0.0f;
+      if (any) {
         unsafe = true;
-        add_wide(&red_wide[threadIdx.x], v[u]);
+        float w[kBatch][8];                  // (a copy: only this one has an address)
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[u][j] = v[u][j];
+        add_wide(&red_wide[threadIdx.x], w);
       }
     }
     if (sum > 1e30f) {
       unsafe = true;
-      const float v[8] = {sqrtf(sum)};   // a square root and its square: half a step of fp32 each
-      add_wide(&red_wide[threadIdx.x], v);
+      float w[kBatch][8] = {};
+      w[0][0] = sqrtf(sum);                // a square root and its square: half a step of fp32 each
+      add_wide(&red_wide[threadIdx.x], w);
       sum = 0.0f;
     }
   }
@@ -230,11 +234,11 @@ __global__ void __launch_bounds__(kScaleThreads) ortho_scale_kernel(const __grid
   const float scale = scale_sh;
   const XT* g = reinterpret_cast<const XT*>(p.g) + (int64_t)b * p.stride_g;
   uint16_t* x = p.x + (int64_t)b * p.rows * p.ldx;
-  ChunkWalk at((int)(p.ldx / 8), p.rows);
+  ChunkWalk at(p, p.ldx / 8);
   while (at.inside()) {
     float v[kBatch][8];
     ChunkWalk to = at;
-    read_batch<XT>(at, g, p.ldg, p.cols, p.g_vec != 0, v);
+    read_batch<XT>(p, at, g, v);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u, to.next()) {
       if (!to.inside()) continue;

@@ -17,6 +17,7 @@ struct OrthoScaleParams {
   int64_t ldg, stride_g;
   int32_t rows, cols, batch;
   int32_t g_vec;              // 8-element chunks of a line of g are 16-byte aligned
+  int32_t flat;               // neither g nor x has gaps between its lines
   double* partial;            // [batch][kOrthoNormBlocks]
   int32_t blocks;             // partial sums of one matrix
   uint16_t* x;                // fp16 [batch][rows][ldx], ldx % 8 == 0

@@ -170,6 +170,7 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
   sp.batch = (int32_t)batch;
   const int64_t eg = elem_bytes(g_dtype);
   sp.g_vec = aligned(G, 16) && (ldg * eg) % 16 == 0 && (strideG * eg) % 16 == 0;
+  sp.flat = ldg == n && l.ldx == n;
   sp.partial = reinterpret_cast<double*>(ws + l.partial);
   sp.x = reinterpret_cast<uint16_t*>(ws + l.x[0]);
   sp.ldx = l.ldx;
