@@ -116,7 +116,7 @@ struct Pair<__nv_bfloat16> {
 constexpr int kThreads = 256;
 
 template <class XT, int kFmt, bool kTile, bool kTrans>
-__global__ void __launch_bounds__(kThreads) fp8_quant_kernel(const __grid_constant__ Fp8QuantParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(XT) == 2 ? 4 : 2) fp8_quant_kernel(const __grid_constant__ Fp8QuantParams p) {
   using P = Pair<XT>;
   using PT = typename P::T;
   __shared__ __align__(16) float red[8][128];                    // column maxima of each warp / tile maxima
