@@ -38,7 +38,12 @@ __device__ __forceinline__ T* cluster_generic_ptr(T* p, uint32_t rank) {
   return reinterpret_cast<T*>(r);
 }
 
-// 16 bytes of the shared memory of another CTA of the cluster.
+// 4 and 16 bytes of the shared memory of another CTA of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"

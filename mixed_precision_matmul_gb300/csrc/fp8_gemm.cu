@@ -281,49 +281,82 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
 #pragma unroll
     for (int s = 0; s < 8; ++s) peer[s] = s < splits ? cluster_smem_addr(op_smem, (uint32_t)s) : 0u;
     const int64_t c0 = T::kSwapped ? (int64_t)col0 * p.ld_out + row0 + ra : (int64_t)(row0 + ra) * p.ld_out + col0;
-    const bool vec = p.out_vec != 0;
-    for (int u = threadIdx.x; length > 0 && u < lines * vecs; u += T::kThreads) {
-      const int line = u / vecs, c = (u - line * vecs) * 4;
-      const uint32_t off = (uint32_t)((line0 + line) * T::kPitch + first + c) * 4u;
-      float4 x;
-      if (splits == 1) {
-        x = ld_shared_f4(op_smem + off);
-      } else {
-        float4 part[8];
+    if (p.out_vec) {
+      for (int u = threadIdx.x; length > 0 && u < lines * vecs; u += T::kThreads) {
+        const int line = u / vecs, c = (u - line * vecs) * 4;
+        const uint32_t off = (uint32_t)((line0 + line) * T::kPitch + first + c) * 4u;
+        float4 x;
+        if (splits == 1) {
+          x = ld_shared_f4(op_smem + off);
+        } else {
+          float4 part[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          if (s < splits) part[s] = ld_cluster_f4(peer[s] + off);
-        x = part[0];
+          for (int s = 0; s < 8; ++s)
+            if (s < splits) part[s] = ld_cluster_f4(peer[s] + off);
+          x = part[0];
 #pragma unroll
-        for (int s = 1; s < 8; ++s)
-          if (s < splits) {
-            x.x += part[s].x;
-            x.y += part[s].y;
-            x.z += part[s].z;
-            x.w += part[s].w;
-          }
-      }
-      const int64_t idx = c0 + (int64_t)line * p.ld_out + c;
-      x.x *= p.alpha;
-      x.y *= p.alpha;
-      x.z *= p.alpha;
-      x.w *= p.alpha;
-      if (vec && c + 4 <= length) {
-        if (p.beta != 0.0f) {
-          const float4 z = out_load4(p.out, idx, p.out_dtype);
-          x.x = fmaf(p.beta, z.x, x.x);
-          x.y = fmaf(p.beta, z.y, x.y);
-          x.z = fmaf(p.beta, z.z, x.z);
-          x.w = fmaf(p.beta, z.w, x.w);
+          for (int s = 1; s < 8; ++s)
+            if (s < splits) {
+              x.x += part[s].x;
+              x.y += part[s].y;
+              x.z += part[s].z;
+              x.w += part[s].w;
+            }
         }
-        out_store4(p.out, idx, x, p.out_dtype);
-      } else {
-        const float e[4] = {x.x, x.y, x.z, x.w};
+        const int64_t idx = c0 + (int64_t)line * p.ld_out + c;
+        x.x *= p.alpha;
+        x.y *= p.alpha;
+        x.z *= p.alpha;
+        x.w *= p.alpha;
+        if (c + 4 <= length) {
+          if (p.beta != 0.0f) {
+            const float4 z = out_load4(p.out, idx, p.out_dtype);
+            x.x = fmaf(p.beta, z.x, x.x);
+            x.y = fmaf(p.beta, z.y, x.y);
+            x.z = fmaf(p.beta, z.z, x.z);
+            x.w = fmaf(p.beta, z.w, x.w);
+          }
+          out_store4(p.out, idx, x, p.out_dtype);
+        } else {
+          const float e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c + j < length)
-            out_store(p.out, idx + j, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx + j, p.out_dtype), e[j]) : e[j],
-                      p.out_dtype);
+          for (int j = 0; j < 4; ++j)
+            if (c + j < length)
+              out_store(p.out, idx + j, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx + j, p.out_dtype), e[j]) : e[j],
+                        p.out_dtype);
+        }
+      }
+    } else {
+      // lines of C off the vectors' alignment: neighbouring threads take
+      // neighbouring elements, four of a line each
+      for (int u = threadIdx.x; length > 0 && u < lines * vecs; u += T::kThreads) {
+        const int line = u / vecs, v = u - line * vecs;
+        const uint32_t row = (uint32_t)((line0 + line) * T::kPitch + first) * 4u;
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t off = row + (uint32_t)min(v + j * vecs, length - 1) * 4u;
+          if (splits == 1) {
+            x[j] = ld_shared_f32(op_smem + off);
+          } else {
+            float part[8];
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              if (s < splits) part[s] = ld_cluster_f32(peer[s] + off);
+            x[j] = part[0];
+#pragma unroll
+            for (int s = 1; s < 8; ++s)
+              if (s < splits) x[j] += part[s];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = v + j * vecs;
+          if (c >= length) break;
+          const int64_t idx = c0 + (int64_t)line * p.ld_out + c;
+          const float y = p.alpha * x[j];
+          out_store(p.out, idx, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx, p.out_dtype), y) : y, p.out_dtype);
+        }
       }
     }
   }
