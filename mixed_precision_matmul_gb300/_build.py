@@ -2,7 +2,8 @@
 
 Every translation unit under ``csrc/`` is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked (static CUDA runtime)
-into ``mixed_precision_matmul_gb300/_build/libmpgemm.so``.  The ptxas resource
+into ``mixed_precision_matmul_gb300/_build/libmpgemm.so``; g++ compiles the
+marshalling extension of the torch forms beside it.  The ptxas resource
 report (``-Xptxas -v``: registers, spills, shared memory) of each unit is kept
 in ``_build/ptxas.log``.
 """
@@ -90,9 +91,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for f in os.listdir(BUILD):
             if f.endswith(".o"):
                 os.remove(os.path.join(BUILD, f))
-    jobs = min(len(SOURCES), max(2, os.cpu_count() or 2))
+    jobs = min(len(SOURCES) + 1, max(2, os.cpu_count() or 2))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls = ex.submit(build_torch_calls)
         results = list(ex.map(_compile, SOURCES))
+        calls.result()
     objs = [o for o, _ in results]
     logs = "".join(f"== {s}\n{log}" for s, (_, log) in zip(SOURCES, results) if log)
     if logs:
@@ -108,6 +111,36 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB
+
+
+def torch_calls_path() -> str:
+    """The marshalling extension, built for the torch that is installed."""
+    import torch
+    return os.path.join(BUILD, f"_torch_calls-{torch.__version__}.so")
+
+
+def build_torch_calls() -> str:
+    """Compile csrc/torch_calls.cpp (host code only) against the installed torch."""
+    import sysconfig
+
+    import torch
+    os.makedirs(BUILD, exist_ok=True)
+    src, out = os.path.join(CSRC, "torch_calls.cpp"), torch_calls_path()
+    if not _stale(out, [src, os.path.join(INCLUDE, "mpgemm.h")]):
+        return out
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    tmp = out + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           src, "-o", tmp] + [f"-I{d}" for d in inc] + [f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu",
+                                                       "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for torch_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
 
 
 if __name__ == "__main__":

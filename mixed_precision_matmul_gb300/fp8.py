@@ -22,6 +22,24 @@ def _types():
 
 
 @functools.cache
+def _calls():
+    """The extension that makes the plain calls (csrc/torch_calls.cpp)."""
+    import importlib.machinery
+    import importlib.util
+
+    _types()                                    # torch first: the extension links to it
+    path = _m._build.torch_calls_path()
+    loader = importlib.machinery.ExtensionFileLoader("_torch_calls", path)
+    spec = importlib.util.spec_from_file_location("_torch_calls", path, loader=loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    lib = _m.lib()
+    module.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                  for f in (lib.mpg_gemm_fp8, lib.mpg_gemm_fp8_workspace_size, lib.mpg_fp8_quantize)))
+    return module
+
+
+@functools.cache
 def _default_options(c_dtype: int):
     return _m.options(c_dtype=c_dtype)
 
@@ -111,6 +129,11 @@ def fp8_quantize(x, fmt="e4m3", block: str = "row", transpose: bool = False, str
     scale_rows = 1 if block == "row" else BLOCK
     if scale_rows == BLOCK and block != "tile":
         raise ValueError("block is 'row' or 'tile'")
+    r = _calls().quantize(x, fmt, scale_rows, transpose)
+    if r is not None:
+        if r.__class__ is int:
+            _m._check(r)
+        return r
     if x.dim() != 2:
         raise ValueError("a 2-D tensor is expected")
     x_dtype = codes.get(x.dtype)
@@ -207,6 +230,14 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
     if stream is not None:
         return _on_stream(stream, [A, a_scale, B, b_scale, C, workspace],
                           lambda: gemm_fp8(A, a_scale, B, b_scale, C, alpha, beta, out_dtype, workspace, opts))
+    if C is None and opts is None and workspace is None and beta == 0.0:
+        code = codes.get(out_dtype) if out_dtype is not None else _m.BF16
+        if code is not None:
+            r = _calls().gemm_fp8(A, a_scale, B, b_scale, alpha, code)
+            if r is not None:
+                if r.__class__ is int:
+                    _m._check(r)
+                return r
     index = A.get_device()
     if index < 0:
         raise ValueError("CUDA tensors expected")
