@@ -40,13 +40,14 @@ struct Fp8Traits {
   static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
   static constexpr int kCols = BN / (kEpiWarps / 4);      // columns of one epilogue warp
   static constexpr int kThreads = (2 + kEpiWarps) * 32;
-  using Ring = ScaleRing<kCols, kColVec, kSwapped ? 4 : 8>;
+  using Ring = ScaleRing<kCols, kSwapped ? 4 : 8>;
+  static constexpr int kRingBytes = kColVec ? kEpiWarps * Ring::kBytes : 0;
   // The staged tile's lines run along C's: columns of a row, or, swapped, the
   // rows of a column.  (132: rows written by 16 bytes a lane reach all banks.)
   static constexpr int kLines = kSwapped ? BN : BM;
   static constexpr int kPitch = kSwapped ? BM : BN + 4;   // floats
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
-  static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiWarps * Ring::kBytes + kNumBars * 8 + 16;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kRingBytes + kNumBars * 8 + 16;
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory budget");
   static_assert(kLines * kPitch * 4 <= kStages * kStage, "the staged tile reuses the operand stages");
   static_assert(kCtasPerSm * kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   // the same offset in every CTA of a cluster (the partial sums are read by address)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring_base = smem + T::kStages * T::kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_base + T::kEpiWarps * T::Ring::kBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_base + T::kRingBytes);
   uint64_t* op_full = bars;
   uint64_t* op_empty = bars + T::kStages;
   uint64_t* acc_full = bars + 2 * T::kStages;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
         tc_fence_after_sync();
         const uint32_t slot = ring.slot(i);
         const float s = ld_shared_f32(slot + lane * 4);
-        add_block<T::kCols, true>(acc, tacc + ab * T::kAccStride, slot, pack2(s, s), [&]() { release(ab); });
+        add_block<T::kCols>(acc, tacc + ab * T::kAccStride, slot, pack2(s, s), [&]() { release(ab); });
       }
     } else {
       // A row a lane: its scale and that of all columns go from global memory

@@ -100,15 +100,15 @@ __device__ __forceinline__ void ld_shared_pairs(uint32_t addr, f32x2& a, f32x2& 
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
 
-// The scales of one epilogue warp: its 32 rows and `kCols` columns (or the one
-// scale of all its columns), fetched kDepth - 1 blocks of k ahead into a ring
-// in shared memory that only this warp uses.
-template <int kCols, bool kColVec, int kDepth_>
+// The scales of one epilogue warp, its 32 rows and `kCols` columns, fetched
+// kDepth - 1 blocks of k ahead into a ring in shared memory that only this
+// warp uses.
+template <int kCols, int kDepth_>
 struct ScaleRing {
   static constexpr int kDepth = kDepth_;
-  static constexpr int kSlot = 32 + (kColVec ? kCols : 32);        // floats
+  static constexpr int kSlot = 32 + kCols;                          // floats
   static constexpr int kBytes = kDepth * kSlot * 4;
-  static constexpr int kColLoads = kColVec ? (kCols + 31) / 32 : 1;
+  static constexpr int kColLoads = (kCols + 31) / 32;
   uint32_t base;
   const float* row_src;                  // the next block's to fetch
   const float* col_src[kColLoads];
@@ -124,13 +124,10 @@ struct ScaleRing {
     left = n;
     row_k = p.sr_k;
     col_k = p.sc_k;
-    const int r = min(row0 + lane, p.rows - 1) >> p.sr_shift;
-    row_src = p.sr + (int64_t)r * p.sr_row + (int64_t)kb0 * p.sr_k;
+    row_src = p.sr + (int64_t)(min(row0 + lane, p.rows - 1) >> p.sr_shift) * p.sr_row + (int64_t)kb0 * p.sr_k;
 #pragma unroll
-    for (int i = 0; i < kColLoads; ++i) {
-      const int c = min(kColVec ? col0 + i * 32 + lane : col0, p.cols - 1) >> p.sc_shift;
-      col_src[i] = p.sc + (int64_t)c * p.sc_row + (int64_t)kb0 * p.sc_k;
-    }
+    for (int i = 0; i < kColLoads; ++i)
+      col_src[i] = p.sc + (int64_t)(min(col0 + i * 32 + lane, p.cols - 1) >> p.sc_shift) * p.sc_row + (int64_t)kb0 * p.sc_k;
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) fetch(i);
   }
@@ -144,7 +141,7 @@ struct ScaleRing {
       row_src += row_k;
 #pragma unroll
       for (int j = 0; j < kColLoads; ++j) {
-        if (!kColVec || kCols % 32 == 0 || j * 32 + lane < kCols) cp_async4(s + 128 + j * 128, col_src[j]);
+        if (kCols % 32 == 0 || j * 32 + lane < kCols) cp_async4(s + 128 + j * 128, col_src[j]);
         col_src[j] += col_k;
       }
     }
@@ -170,33 +167,26 @@ __device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t s
   }
 }
 
-// One block of k: the accumulator at `ta` (kCols columns of this warp's 32
-// lanes) added to the running sums under the scales in `slot`.  A tcgen05.ld
-// takes far longer to arrive than its columns take to add, so two loads of 32
-// columns are in flight.  `release` runs when all columns are in registers.
-template <int kCols, bool kColVec, class Release>
+// One block of k with a scale for each column: the accumulator at `ta` (kCols
+// columns of this warp's 32 lanes) added to the running sums under the row
+// scale rs and the column scales in `slot`, two reads of 32 columns on their
+// way.  `release` runs when all columns are in registers.
+template <int kCols, class Release>
 __device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, uint32_t slot, f32x2 rs,
                                           Release release) {
   constexpr int kChunk = kCols >= 32 ? 32 : 16;
   constexpr int kN = kCols / kChunk;
-  constexpr int kFly = kN > 1 ? 2 : 1;
-  float v[kFly][kChunk];
-  auto load = [&](int c) {
-    if constexpr (kChunk == 32) tmem_ld_32cols(ta + c * kChunk, v[c % kFly]);
-    else tmem_ld_16cols(ta + c * kChunk, v[c % kFly]);
-  };
+  static_assert(kN <= 2, "all reads at once");
+  float v[kN][kChunk];
 #pragma unroll
-  for (int c = 0; c < kFly; ++c) load(c);
-#pragma unroll
-  for (int c0 = 0; c0 < kN; c0 += kFly) {
-    tmem_ld_wait();
-    if (c0 + kFly >= kN) release();
-#pragma unroll
-    for (int c = c0; c < c0 + kFly; ++c) {
-      scale_add<kChunk, kColVec>(acc + c * kChunk / 2, v[c % kFly], slot, c * kChunk, rs);
-      if (c + kFly < kN) load(c + kFly);
-    }
+  for (int c = 0; c < kN; ++c) {
+    if constexpr (kChunk == 32) tmem_ld_32cols(ta + c * kChunk, v[c]);
+    else tmem_ld_16cols(ta + c * kChunk, v[c]);
   }
+  tmem_ld_wait();
+  release();
+#pragma unroll
+  for (int c = 0; c < kN; ++c) scale_add<kChunk, true>(acc + c * kChunk / 2, v[c], slot, c * kChunk, rs);
 }
 
 }  // namespace mpg
