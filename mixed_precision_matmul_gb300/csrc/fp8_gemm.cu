@@ -1,11 +1,11 @@
 // The block-scaled 8-bit product on single CTAs (sm_103a, cta_group::1): one
-// 128 x BN tile of D per CTA, or per cluster of 2, 4 or 8 CTAs that divide the
+// 128 x BN tile of D per CTA, or per cluster of up to 8 CTAs that divide the
 // tile's k-blocks among them.
 //
 // Roles:
 //   warp 0      TMA producer (one line of 128 k per row and stage)
-//   warp 1      TMEM allocation; lane 0 issues the MMAs, one accumulator
-//               buffer per k-block (four buffers in turn)
+//   warp 1      TMEM allocation; one elected lane issues the MMAs, one
+//               accumulator buffer per k-block (four buffers in turn)
 //   warps 2..   epilogue: read each k-block's accumulator, add it to the
 //               running sums under its scales (fp8_tc.cuh), and at the end
 //               put the sums into shared memory, where the tile is read back
@@ -18,6 +18,12 @@
 // are the columns (BN = 16, 32 or 64), so that the tensor core's rows are full
 // and each weight byte is read once; the kernel is then bound by the weights'
 // bytes, and the k range is divided so that every SM has some in flight.
+//
+// On a GB300 (from a graph, operands in the L2 cache where they fit): 1 x 8192
+// by 8192 x 8192 takes 11.7 us, 5.7 TB/s of weights; 33 x 4160 by 4096 x 4160
+// takes 8.0 us and 1000 x 4112 by 1531 x 4112 19.6 us, both bound by the
+// latency of a chain of blocks (a block's load, MMAs and addition) and by the
+// way in and out of the kernel, neither by bytes nor by the tensor cores.
 #include "fp8_tc.cuh"
 
 namespace mpg {
