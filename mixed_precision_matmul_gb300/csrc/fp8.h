@@ -73,7 +73,8 @@ struct Fp8Kernel {
 };
 // One-CTA tiles of 128 x bn: bn = 128 (D as the caller's C; col_vec: a scale
 // for each column, else one for all 128), bn = 16, 32, 64 (swapped).
-bool fp8_lookup(int bn, bool swapped, bool col_vec, Fp8Kernel* out);
+// `direct`: tile after tile on one CTA; else a tile, or a share of its k, to each.
+bool fp8_lookup(int bn, bool swapped, bool col_vec, bool direct, Fp8Kernel* out);
 // 256 x 256 tiles on CTA pairs.
 bool fp8_lookup_pair(bool col_vec, Fp8Kernel* out);
 

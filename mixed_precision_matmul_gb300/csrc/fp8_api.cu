@@ -63,7 +63,13 @@ struct Fp8Plan {
   int splits = 1;
 };
 
-Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, int sm_count, int clusters) {
+struct FormCost {
+  int64_t round, block;
+};
+constexpr int64_t kExchange = 7;   // blocks of k
+
+// col_vec: a scale for each column (row of B).
+Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool col_vec, int sm_count, int clusters) {
   Fp8Plan p;
   // Few tokens: the weights' rows fill the tensor core's 128 rows.
   p.swapped = m <= 64;
@@ -81,19 +87,29 @@ Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, int 
   } else {
     // As many ranges as keep every CTA on an SM of its own, of two blocks at
     // least: 64 x 4096 x 4096 takes 16.0, 11.4, 9.1, 7.6 us with 1 .. 4 ranges
-    // (128 CTAs) and 11.4 with 5 (160).
+    // (128 CTAs) and 11.4 with 5 (160).  Of 128 x 128 tiles the exchange takes
+    // as long as kExchange blocks: 256 x 4096 x 512 takes 7.3 us with two
+    // ranges of two blocks and 5.4 with one, 256 x 4096 x 4096 12.0 and 15.2.
     while (s < 8 && tiles * (s + 1) <= sm_count && kb / (s + 1) >= 2) ++s;
+    if (!p.swapped && kb - (kb + s - 1) / s <= kExchange) s = 1;
   }
   s = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(s, 8), kb));
   const int64_t per = (kb + s - 1) / s;
   p.splits = (int)((kb + per - 1) / per);
-  // A 128 x 128 tile of one CTA keeps its SM's shared memory busy for a block
-  // of k as long as a pair's 256 x 256 tile does (a copy in and a read of 32
-  // KB either way), so the form with fewer rounds of blocks wins.
-  const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  const int64_t pair_rounds = (pair_tiles + clusters - 1) / clusters * kb;
-  const int64_t rounds = (tiles * p.splits + sm_count - 1) / sm_count * per;
-  if (o.cta_pair == 1 || (o.cta_pair == 0 && o.tile_n == 0 && o.splitk == 0 && !p.swapped && pair_rounds < rounds)) {
+  // The form that ends first, by what the forms take on a GB300 (ns): each
+  // round of tiles, and each block of k in it.  One CTA's 128 x 128 tile keeps
+  // the way to its SM busy for a block of k as long as a pair's 256 x 256 tile
+  // does (32 KB either way), but a pair's SM has twice the additions to do, and
+  // with a scale for each column those take longest.  With a scale for 128
+  // columns 4096^3 takes 69 us on pairs and 91 on single CTAs, 4096 x 4096 x
+  // 512 22 and 21; with one for each column 121 and 118, 38 and 29.
+  const int64_t pair_rounds = ((m + 255) / 256 * ((n + 255) / 256) + clusters - 1) / clusters;
+  const int64_t rounds = (tiles * p.splits + sm_count - 1) / sm_count;
+  const FormCost one = col_vec ? FormCost{1900, 460} : FormCost{1150, 355};
+  const FormCost two = col_vec ? FormCost{5750, 730} : FormCost{3000, 420};
+  const int64_t one_time = rounds * (one.round + one.block * (per + (p.splits > 1 ? kExchange : 0)));
+  const int64_t pair_time = pair_rounds * (two.round + two.block * kb);
+  if (o.cta_pair == 1 || (o.cta_pair == 0 && o.tile_n == 0 && o.splitk == 0 && !p.swapped && pair_time < one_time)) {
     p.pair = true;
     p.swapped = false;
     p.splits = 1;
@@ -121,11 +137,11 @@ mpg_status launch_product(DeviceInfo* dev, int64_t m, int64_t n, int64_t k, cons
   int clusters = 0;
   mpg_status s = resident_clusters(dev, kern.fn, kern.block, kern.smem_bytes, 2, &clusters);
   if (s != MPG_OK) return s;
-  const Fp8Plan plan = plan_product(m, n, k, o, dev->sm_count, clusters);
+  const Fp8Plan plan = plan_product(m, n, k, o, B.scale_rows == 1, dev->sm_count, clusters);
   const mpg_fp8_operand& R = plan.swapped ? B : A;
   const mpg_fp8_operand& S = plan.swapped ? A : B;
   if (!plan.pair) {
-    if (!fp8_lookup(plan.bn, plan.swapped, plan.swapped || S.scale_rows == 1, &kern))
+    if (!fp8_lookup(plan.bn, plan.swapped, plan.swapped || S.scale_rows == 1, !plan.swapped && plan.splits == 1, &kern))
       return fail(MPG_ERR_UNSUPPORTED, "no 8-bit kernel for tile_n %d", plan.bn);
     if ((s = allow_smem(dev, kern.fn, kern.smem_bytes)) != MPG_OK) return s;
   }
@@ -165,7 +181,8 @@ mpg_status launch_product(DeviceInfo* dev, int64_t m, int64_t n, int64_t k, cons
   if (tiles * p.splits > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
   p.num_tiles = (int32_t)tiles;
   p.group = 8;
-  const int64_t ctas = plan.pair ? 2 * std::min<int64_t>(tiles, clusters) : tiles * p.splits;
+  const int64_t ctas = plan.pair ? 2 * std::min<int64_t>(tiles, clusters)
+                       : !plan.swapped && p.splits == 1 ? std::min<int64_t>(tiles, dev->sm_count) : tiles * p.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3((unsigned)kern.block);

@@ -1,6 +1,6 @@
 // The block-scaled 8-bit product on single CTAs (sm_103a, cta_group::1): one
 // 128 x BN tile of D per CTA, or per cluster of up to 8 CTAs that divide the
-// tile's k-blocks among them.
+// tile's k-blocks among them; or, direct, 128 x 128 tiles one after another.
 //
 // Roles:
 //   warp 0      TMA producer (one line of 128 k per row and stage)
@@ -9,7 +9,9 @@
 //   warps 2..   epilogue: read each k-block's accumulator, add it to the
 //               running sums under its scales (fp8_tc.cuh), and at the end
 //               put the sums into shared memory, where the tile is read back
-//               in the order that C is stored in.  With a cluster, each CTA
+//               in the order that C is stored in.  Direct: each warp stores
+//               its own rows, while the tensor cores are on the next tile (up
+//               to four blocks ahead).  With a cluster, each CTA
 //               reads its share of the rows from all CTAs' shared memory and
 //               adds the partial sums in rank order, so the result does not
 //               depend on timing and needs no workspace.
@@ -21,39 +23,48 @@
 //
 // On a GB300 (from a graph, operands in the L2 cache where they fit): 1 x 8192
 // by 8192 x 8192 takes 11.7 us, 5.7 TB/s of weights; 33 x 4160 by 4096 x 4160
-// takes 8.0 us and 1000 x 4112 by 1531 x 4112 19.6 us, both bound by the
-// latency of a chain of blocks (a block's load, MMAs and addition) and by the
-// way in and out of the kernel, neither by bytes nor by the tensor cores.
+// takes 8.0 us, bound by the latency of a chain of blocks (a block's load, MMAs
+// and addition) and by the way in and out of the kernel.  Direct tiles take 355
+// ns a block of k, which is the operands' way from the L2 cache (32 KB an SM, 14
+// TB/s in all; the tensor cores need 140 ns), 460 with a scale for each column:
+// 1000 x 4112 by 1531 x 4112 takes 17.4 us, 4096^3 with a scale for each
+// column 118 us in fp32 (with eight epilogue warps instead of sixteen 123; one
+// tile a CTA 121; the next block's columns read during the additions 139).
 #include "fp8_tc.cuh"
 
 namespace mpg {
 namespace {
 
-template <int BN_, bool kSwapped_, bool kColVec_>
+// kDirect: tile after tile on one CTA, sums from registers to C; else one tile,
+// of which the CTAs of a cluster may have shares.
+template <int BN_, bool kSwapped_, bool kColVec_, bool kDirect_>
 struct Fp8Traits {
   static constexpr int BM = 128;
   static constexpr int BN = BN_;
   static constexpr bool kSwapped = kSwapped_;
   static constexpr bool kColVec = kColVec_;
+  static constexpr bool kDirect = kDirect_;
+  static_assert(!kDirect || !kSwapped, "rows of C");
   static constexpr int kStage = (BM + BN) * kFp8RowBytes;
   // few columns: three CTAs to an SM, so that one's start and end overlap the
   // others' loads
   static constexpr int kCtasPerSm = BN >= 128 ? 1 : BN >= 64 ? 2 : 3;
-  static constexpr int kStages = BN >= 128 ? 6 : BN >= 64 ? 4 : 3;
+  static constexpr int kStages = BN >= 128 ? (kDirect ? 5 : 6) : BN >= 64 ? 4 : 3;
   static constexpr int kAccBufs = 4;
   static constexpr int kAccStride = BN < 32 ? 32 : BN;
   static constexpr int kTmemCols = kAccBufs * kAccStride;
-  static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
+  static constexpr int kEpiWarps = kDirect ? 16 : BN >= 64 ? 8 : 4;
   static constexpr int kCols = BN / (kEpiWarps / 4);      // columns of one epilogue warp
   static constexpr int kThreads = (2 + kEpiWarps) * 32;
-  using Ring = ScaleRing<kCols, kSwapped ? 4 : 8>;
+  using Ring = ScaleRing<kCols, kSwapped || kDirect ? 4 : 8>;
   static constexpr int kRingBytes = kColVec ? kEpiWarps * Ring::kBytes : 0;
   // The staged tile's lines run along C's: columns of a row, or, swapped, the
   // rows of a column.  (132: rows written by 16 bytes a lane reach all banks.)
   static constexpr int kLines = kSwapped ? BN : BM;
   static constexpr int kPitch = kSwapped ? BM : BN + 4;   // floats
+  static constexpr int kEpiBytes = kDirect ? kEpiWarps * 2048 : 0;   // rows on their way to C, tile after tile
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
-  static constexpr int kSmemBytes = 1024 + kStages * kStage + kRingBytes + kNumBars * 8 + 16;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kRingBytes + kEpiBytes + kNumBars * 8 + 16;
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory budget");
   static_assert(kLines * kPitch * 4 <= kStages * kStage, "the staged tile reuses the operand stages");
   static_assert(kCtasPerSm * kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
@@ -65,7 +76,8 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   // the same offset in every CTA of a cluster (the partial sums are read by address)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring_base = smem + T::kStages * T::kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_base + T::kRingBytes);
+  uint8_t* epi_base = ring_base + T::kRingBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_base + T::kEpiBytes);
   uint64_t* op_full = bars;
   uint64_t* op_empty = bars + T::kStages;
   uint64_t* acc_full = bars + 2 * T::kStages;
@@ -78,8 +90,10 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();          // this CTA's share of the k range
   const int tile = (int)(blockIdx.x / (uint32_t)p.splits);
-  const int cblk = tile / p.num_r_blk, rblk = tile - cblk * p.num_r_blk;
-  const int row0 = rblk * T::BM, col0 = cblk * T::BN;
+  const int step = T::kDirect ? (int)gridDim.x : p.num_tiles;
+  auto row_of = [&](int t) { return t % p.num_r_blk * T::BM; };
+  auto col_of = [&](int t) { return t / p.num_r_blk * T::BN; };
+  const int row0 = row_of(tile), col0 = col_of(tile);
   const int kb0 = (int)rank * p.kb_per_split;
   const int nkb = max(0, min(p.num_k_blk, kb0 + p.kb_per_split) - kb0);
 
@@ -119,18 +133,21 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int i = 0;
-      for (; i < nkb; ++i) {
-        const int st = i % T::kStages;
-        if (!mbar_wait(&op_empty[st], ((i / T::kStages) & 1u) ^ 1u, ctl)) break;
-        mbar_arrive_expect_tx(&op_full[st], T::kStage);
-        uint8_t* dst = smem + st * T::kStage;
-        const int k0 = (kb0 + i) * kFp8Block;
-        tma_load_3d(dst, &p.map_r, &op_full[st], k0, row0, 0);
-        tma_load_3d(dst + T::BM * kFp8RowBytes, &p.map_c, &op_full[st], k0, col0, 0);
+      uint32_t i = 0;
+      for (int t = tile; t < p.num_tiles && ok; t += step) {
+        const int r = row_of(t), c = col_of(t);
+        for (int kb = 0; kb < nkb; ++kb, ++i) {
+          const uint32_t st = i % T::kStages;
+          if (!mbar_wait(&op_empty[st], ((i / T::kStages) & 1u) ^ 1u, ctl)) { ok = false; break; }
+          mbar_arrive_expect_tx(&op_full[st], T::kStage);
+          uint8_t* dst = smem + st * T::kStage;
+          const int k0 = (kb0 + kb) * kFp8Block;
+          tma_load_3d(dst, &p.map_r, &op_full[st], k0, r, 0);
+          tma_load_3d(dst + T::BM * kFp8RowBytes, &p.map_c, &op_full[st], k0, c, 0);
+        }
       }
       // the stages' last releases cover the copies still in flight
-      for (int j = max(0, i - T::kStages); j < i; ++j)
+      for (uint32_t j = i < (uint32_t)T::kStages ? 0u : i - T::kStages; j < i; ++j)
         drain_wait(&op_empty[j % T::kStages], (j / T::kStages) & 1u, p.wait_limit_ns);
     }
     __syncwarp();
@@ -140,25 +157,26 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
     const uint32_t idesc = make_idesc(0u, false, false, T::BM, T::BN) | p.fmt_bits;
     const uint64_t r_desc = fp8_desc(op_smem, 0), c_desc = fp8_desc(op_smem + T::BM * kFp8RowBytes, 0);
     const uint32_t d_base = __shfl_sync(0xffffffffu, tmem_base, 0);
-    int st = 0;
-    uint32_t st_ph = 0;
-    for (int i = 0; i < nkb; ++i) {
-      const int ab = i % T::kAccBufs;
-      if (!warp_wait(&op_full[st], st_ph, ctl)) break;
-      if (!warp_wait(&acc_empty[ab], ((i / T::kAccBufs) & 1u) ^ 1u, ctl)) break;
-      tc_fence_after_sync();
-      const uint64_t at = (uint64_t)(st * (T::kStage / 16));
-      if (leader) {
+    uint32_t i = 0, st = 0, st_ph = 0;
+    for (int t = tile; t < p.num_tiles && ok; t += step) {
+      for (int kb = 0; kb < nkb; ++kb, ++i) {
+        const uint32_t ab = i % T::kAccBufs;
+        if (!warp_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
+        if (!warp_wait(&acc_empty[ab], ((i / T::kAccBufs) & 1u) ^ 1u, ctl)) { ok = false; break; }
+        tc_fence_after_sync();
+        const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_f8(d_base + ab * T::kAccStride, r_desc + at + 2 * ks, c_desc + at + 2 * ks, idesc, ks > 0 ? 1u : 0u);
-        mma_commit(&acc_full[ab]);
-        mma_commit(&op_empty[st]);
-      }
-      __syncwarp();
-      if (++st == T::kStages) {
-        st = 0;
-        st_ph ^= 1u;
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f8(d_base + ab * T::kAccStride, r_desc + at + 2 * ks, c_desc + at + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+          mma_commit(&acc_full[ab]);
+          mma_commit(&op_empty[st]);
+        }
+        __syncwarp();
+        if (++st == T::kStages) {
+          st = 0;
+          st_ph ^= 1u;
+        }
       }
     }
     if (leader) {
@@ -173,80 +191,119 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
     const int wc0 = (ew / 4) * T::kCols;                  // this warp's first column in the tile
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + wc0;
     f32x2 acc[T::kCols / 2];
-#pragma unroll
-    for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
-    auto release = [&](int ab) {
+    auto release = [&](uint32_t ab) {
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
     };
+    // a whole tile's sums to C, while the tensor cores are on the next tile
+    auto store = [&](int t) {
+      if constexpr (T::kDirect) {
+        const int row = row_of(t) + 32 * q, col = col_of(t) + wc0;
+        if (row >= p.rows) return;
+#pragma unroll
+        for (int cc = 0; cc < T::kCols / 32; ++cc)
+          if (col + cc * 32 < p.cols)
+            store_rows32(p, smem_addr(epi_base) + ew * 2048, lane, acc + cc * 16, row, col + cc * 32);
+      }
+    };
+    uint32_t i = 0;
     if constexpr (T::kColVec) {
+      // scales by way of shared memory, a ring of blocks that only this warp uses
       typename T::Ring ring;
-      ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row0 + 32 * q, col0 + wc0, kb0, nkb);
+      auto begin = [&](int t) {
+        ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row_of(t) + 32 * q, col_of(t) + wc0, kb0, nkb);
+      };
+      begin(tile);
+      for (int t = tile; t < p.num_tiles && ok; t += step) {
+#pragma unroll
+        for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
 #pragma unroll 1
-      for (int i = 0; i < nkb; ++i) {
-        const int ab = i % T::kAccBufs;
-        __syncwarp();                                    // every lane is done with block i - 1's slot
-        ring.fetch(i + T::Ring::kDepth - 1);
-        cp_async_wait<T::Ring::kDepth - 1>();
-        if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
-        tc_fence_after_sync();
-        const uint32_t slot = ring.slot(i);
-        const float s = ld_shared_f32(slot + lane * 4);
-        add_block<T::kCols>(acc, tacc + ab * T::kAccStride, slot, pack2(s, s), [&]() { release(ab); });
+        for (int kb = 0; kb < nkb; ++kb, ++i) {
+          const uint32_t ab = i % T::kAccBufs;
+          __syncwarp();                                  // every lane is done with the last block's slot
+          ring.fetch(kb + T::Ring::kDepth - 1);
+          cp_async_wait<T::Ring::kDepth - 1>();
+          if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
+          __syncwarp();
+          tc_fence_after_sync();
+          const uint32_t slot = ring.slot(kb);
+          const float s = ld_shared_f32(slot + lane * 4);
+          add_block<T::kCols>(acc, tacc + ab * T::kAccStride, slot, pack2(s, s), [&]() { release(ab); });
+        }
+        if (!T::kDirect || !ok) break;
+        __syncwarp();
+        if (t + step < p.num_tiles) begin(t + step);     // (its scales are on their way during the stores)
+        store(t);
       }
     } else {
       // A row a lane: its scale and that of all columns go from global memory
-      // into registers, three blocks ahead; two reads of 32 columns are on
-      // their way while the last block's are added.
-      static_assert(T::kCols == 64, "two reads a block");
-      const float* row_src = p.sr + (int64_t)(min(row0 + 32 * q + lane, p.rows - 1) >> p.sr_shift) * p.sr_row + kb0 * p.sr_k;
-      const float* col_src = p.sc + (int64_t)(min(col0 + wc0, p.cols - 1) >> p.sc_shift) * p.sc_row + kb0 * p.sc_k;
-      float rsc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, csc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      auto fetch_scales = [&](int j, int i) {
-        if (i < nkb) {
+      // into registers, three blocks ahead.  Columns are read 32 at a time, the
+      // next block's as soon as this one's are added.
+      static_assert(T::kCols % 32 == 0, "whole reads");
+      constexpr int kReads = T::kCols / 32;
+      const float* row_src;
+      const float* col_src;
+      float rsc[4], csc[4];
+      auto fetch_scales = [&](int j, int kb) {
+        if (kb < nkb) {
           rsc[j] = __ldg(row_src);
           csc[j] = __ldg(col_src);
           row_src += p.sr_k;
           col_src += p.sc_k;
         }
       };
+      auto begin = [&](int t) {
+        row_src = p.sr + (int64_t)(min(row_of(t) + 32 * q + lane, p.rows - 1) >> p.sr_shift) * p.sr_row + kb0 * p.sr_k;
+        col_src = p.sc + (int64_t)(min(col_of(t) + wc0, p.cols - 1) >> p.sc_shift) * p.sc_row + kb0 * p.sc_k;
 #pragma unroll
-      for (int j = 0; j < 3; ++j) fetch_scales(j, j);
-      float v[2][32];
-      auto load = [&](int i) {
-        if (!warp_wait(&acc_full[i % T::kAccBufs], (i / T::kAccBufs) & 1u, ctl)) return false;
+        for (int j = 0; j < 4; ++j) rsc[j] = csc[j] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) fetch_scales(j, j);
+      };
+      float v[kReads][32];
+      auto load = [&](uint32_t it) {
+        if (!warp_wait(&acc_full[it % T::kAccBufs], (it / T::kAccBufs) & 1u, ctl)) return false;
         tc_fence_after_sync();
         return true;
       };
-      ok = nkb > 0 && load(0);
-      if (ok) {
-        tmem_ld_32cols(tacc, v[0]);
-        tmem_ld_32cols(tacc + 32, v[1]);
-      }
-#pragma unroll 1
-      for (int i = 0; i < nkb && ok; ++i) {
-        const bool more = i + 1 < nkb;
-        const uint32_t next = tacc + ((i + 1) % T::kAccBufs) * T::kAccStride;
-        fetch_scales(3, i + 3);
-        const float s = rsc[0] * csc[0];
-        const f32x2 rs = pack2(s, s);
-        tmem_ld_wait();
-        release(i % T::kAccBufs);
-        if (more && !load(i + 1)) { ok = false; break; }
-        scale_add<32, false>(acc, v[0], 0, 0, rs);
-        if (more) tmem_ld_32cols(next, v[0]);
-        scale_add<32, false>(acc + 16, v[1], 0, 32, rs);
-        if (more) tmem_ld_32cols(next + 32, v[1]);
+      begin(tile);
+      for (int t = tile; t < p.num_tiles && ok; t += step) {
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          rsc[j] = rsc[j + 1];
-          csc[j] = csc[j + 1];
+        for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
+        ok = nkb > 0 && load(i);
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < kReads; ++c) tmem_ld_32cols(tacc + (i % T::kAccBufs) * T::kAccStride + c * 32, v[c]);
         }
+#pragma unroll 1
+        for (int kb = 0; kb < nkb && ok; ++kb, ++i) {
+          const bool more = kb + 1 < nkb;
+          const uint32_t next = tacc + ((i + 1) % T::kAccBufs) * T::kAccStride;
+          fetch_scales(3, kb + 3);
+          const float s = rsc[0] * csc[0];
+          const f32x2 rs = pack2(s, s);
+          tmem_ld_wait();
+          release(i % T::kAccBufs);
+          if (more && !load(i + 1)) { ok = false; break; }
+#pragma unroll
+          for (int c = 0; c < kReads; ++c) {
+            scale_add<32, false>(acc + c * 16, v[c], 0, 0, rs);
+            if (more) tmem_ld_32cols(next + c * 32, v[c]);
+          }
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            rsc[j] = rsc[j + 1];
+            csc[j] = csc[j + 1];
+          }
+        }
+        if (!T::kDirect || !ok) break;
+        if (t + step < p.num_tiles) begin(t + step);
+        store(t);
       }
     }
     cp_async_wait<0>();
-    if (ok) {
+    if (!T::kDirect && ok) {
       // every MMA of this CTA is complete: the operand stages are free
       const int r = 32 * q + lane;
 #pragma unroll
@@ -269,7 +326,7 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   tc_fence_before_sync();
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
-  if (*abort_flag == 0) {
+  if (!T::kDirect && *abort_flag == 0) {
     // This CTA's share of the tile's rows, in vectors of four elements that
     // are neighbours in C and in the staged lines; of each, the ranges' partial
     // sums are loaded before the first is added (a load from another SM takes
@@ -389,17 +446,18 @@ bool fill(Fp8Kernel* out) {
 
 }  // namespace
 
-bool fp8_lookup(int bn, bool swapped, bool col_vec, Fp8Kernel* out) {
+bool fp8_lookup(int bn, bool swapped, bool col_vec, bool direct, Fp8Kernel* out) {
   if (swapped) {
     switch (bn) {
-      case 16: return fill<Fp8Traits<16, true, true>>(out);
-      case 32: return fill<Fp8Traits<32, true, true>>(out);
-      case 64: return fill<Fp8Traits<64, true, true>>(out);
+      case 16: return fill<Fp8Traits<16, true, true, false>>(out);
+      case 32: return fill<Fp8Traits<32, true, true, false>>(out);
+      case 64: return fill<Fp8Traits<64, true, true, false>>(out);
       default: return false;
     }
   }
   if (bn != 128) return false;
-  return col_vec ? fill<Fp8Traits<128, false, true>>(out) : fill<Fp8Traits<128, false, false>>(out);
+  if (direct) return col_vec ? fill<Fp8Traits<128, false, true, true>>(out) : fill<Fp8Traits<128, false, false, true>>(out);
+  return col_vec ? fill<Fp8Traits<128, false, true, false>>(out) : fill<Fp8Traits<128, false, false, false>>(out);
 }
 
 }  // namespace mpg

@@ -12,6 +12,7 @@
 #include "cluster.cuh"
 #include "fp8.h"
 #include "outio.cuh"
+#include "staging.cuh"
 #include "tc_gemm.cuh"
 
 namespace mpg {
@@ -184,6 +185,87 @@ __device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, 
   release();
 #pragma unroll
   for (int c = 0; c < kN; ++c) scale_add<kChunk, true>(acc + c * kChunk / 2, v[c], slot, c * kChunk, rs);
+}
+
+// alpha x + beta C for 32 rows (one a lane) and 32 columns (x[j]: columns 2j
+// and 2j + 1).  Rows pass through 64-byte lines of shared memory (32 16-bit values, or 16
+// fp32 values twice), chunk c of row r at slot c ^ ((r / 2) & 3): writes and
+// reads (four lanes a row) reach all banks.  Each store then covers 8 rows x
+// 64 bytes.
+__device__ __forceinline__ void store_rows32(const Fp8GemmParams& p, uint32_t stg, int lane, const f32x2* x,
+                                             int row_base, int col_base) {
+  auto at = [&](int r, int c) { return stg + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };   // 16-byte chunk c of row r
+  const int dt = p.out_dtype;
+  if (dt != kOutF32 && p.beta == 0.0f) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float lo, hi;
+      unpack2(x[j], lo, hi);
+      w[j] = dt == kOutF16 ? pack_f16x2(p.alpha * lo, p.alpha * hi) : pack_bf16x2(p.alpha * lo, p.alpha * hi);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) st_shared_v4(at(lane, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+    uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)row_base * p.ld_out + col_base;
+    if (p.out_vec16 && col_base + 32 <= p.cols) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), c = lane & 3;
+        const float4 y = stage_ld16(at(r, c));
+        if (row_base + r < p.rows) *reinterpret_cast<float4*>(out + (int64_t)r * p.ld_out + c * 8) = y;
+      }
+    } else if (col_base + lane < p.cols) {
+      // lines off 16 bytes: a row at a time, a column a lane
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+        const uint16_t y = ld_shared_u16(at(r, lane >> 3) + (lane & 7) * 2);
+        if (row_base + r < p.rows) out[(int64_t)r * p.ld_out + lane] = y;
+      }
+    }
+    __syncwarp();
+    return;
+  }
+#pragma unroll
+  for (int hc = 0; hc < 2; ++hc) {                        // 16 columns
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        st_shared_b64(at(lane, c), x[hc * 8 + 2 * c]);
+        st_shared_b64(at(lane, c) + 8, x[hc * 8 + 2 * c + 1]);
+      }
+    __syncwarp();
+    if (p.out_vec && col_base + 16 * hc + 16 <= p.cols) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), c = lane & 3;
+        const float4 y = stage_ld16(at(r, c));
+        if (row_base + r >= p.rows) continue;
+        const int64_t idx = (int64_t)(row_base + r) * p.ld_out + col_base + 16 * hc + 4 * c;
+        float4 o = make_float4(p.alpha * y.x, p.alpha * y.y, p.alpha * y.z, p.alpha * y.w);
+        if (p.beta != 0.0f) {
+          const float4 z = out_load4(p.out, idx, dt);
+          o.x = fmaf(p.beta, z.x, o.x);
+          o.y = fmaf(p.beta, z.y, o.y);
+          o.z = fmaf(p.beta, z.z, o.z);
+          o.w = fmaf(p.beta, z.w, o.w);
+        }
+        out_store4(p.out, idx, o, dt);
+      }
+    } else {
+      // two rows at a time, a column a lane
+      const int col = col_base + 16 * hc + (lane & 15);
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        const float y = p.alpha * stage_ld4(at(r, (lane & 15) >> 2) + (lane & 3) * 4);
+        if (row_base + r < p.rows && col < p.cols) {
+          const int64_t idx = (int64_t)(row_base + r) * p.ld_out + col;
+          out_store(p.out, idx, p.beta != 0.0f ? fmaf(p.beta, out_load(p.out, idx, dt), y) : y, dt);
+        }
+      }
+    }
+    __syncwarp();
+  }
 }
 
 }  // namespace mpg

@@ -189,6 +189,13 @@ def test_product_on_pairs_many_tiles():
     check(2500, 2600, 400, ("e4m3", "e4m3"), (1, 128), out="bf16", seed=4)
 
 
+@pytest.mark.parametrize("m,n,k", [(2500, 2600, 300), (2433, 2561, 900)])
+@pytest.mark.parametrize("fmts,sizes,out", [(("e5m2", "e4m3"), (1, 1), "fp32"), (("e4m3", "e4m3"), (1, 128), "bf16")])
+def test_product_tile_after_tile(m, n, k, fmts, sizes, out):
+    """More 128 x 128 tiles than SMs, each CTA several; lines of C on and off the vectors' alignment; beta."""
+    check(m, n, k, fmts, sizes, out=out, opts=dict(cta_pair=-1), alpha=0.5, beta=-0.5 if m == 2433 else 0.0, seed=m)
+
+
 @pytest.mark.parametrize("m", [3, 150])
 @pytest.mark.parametrize("out", ["fp32", "fp16", "bf16"])
 def test_product_outputs_alpha_beta(m, out):
