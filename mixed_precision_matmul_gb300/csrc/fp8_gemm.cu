@@ -19,17 +19,18 @@
 // Few tokens (m <= 64): R, the 128-row operand, is the weights and the tokens
 // are the columns (BN = 16, 32 or 64), so that the tensor core's rows are full
 // and each weight byte is read once; the kernel is then bound by the weights'
-// bytes, and the k range is divided so that every SM has some in flight.
+// bytes, and the k range is divided so that most SMs have some in flight.
 //
-// On a GB300 (from a graph, operands in the L2 cache where they fit): 1 x 8192
-// by 8192 x 8192 takes 11.7 us, 5.7 TB/s of weights; 33 x 4160 by 4096 x 4160
-// takes 8.0 us, bound by the latency of a chain of blocks (a block's load, MMAs
-// and addition) and by the way in and out of the kernel.  Direct tiles take 355
-// ns a block of k, which is the operands' way from the L2 cache (32 KB an SM, 14
-// TB/s in all; the tensor cores need 140 ns), 460 with a scale for each column:
-// 1000 x 4112 by 1531 x 4112 takes 17.4 us, 4096^3 with a scale for each
-// column 118 us in fp32 (with eight epilogue warps instead of sixteen 123; one
-// tile a CTA 121; the next block's columns read during the additions 139).
+// On a GB300, from a graph: 1 x 8192 by 8192 x 8192 takes 14.7 us with weights
+// from DRAM (4.6 TB/s), 11.9 with what the L2 cache keeps of them; 33 x 4160 by
+// 4096 x 4160 takes 8.8 and 8.2 us, bound by the latency of a chain of blocks (a
+// block's load, MMAs and addition) and by the way in and out of the kernel.
+// Direct tiles take 355 ns a block of k, which is the operands' way from the L2
+// cache (32 KB an SM, 14 TB/s in all; the tensor cores need 140 ns), 460 with a
+// scale for each column: 1000 x 4112 by 1531 x 4112 takes 17.4 us, 4096^3 with a
+// scale for each column 118 us in fp32 (with eight epilogue warps instead of
+// sixteen 123; one tile a CTA 121; the next block's columns read during the
+// additions 139).
 #include "fp8_tc.cuh"
 
 namespace mpg {
@@ -46,10 +47,14 @@ struct Fp8Traits {
   static constexpr bool kDirect = kDirect_;
   static_assert(!kDirect || !kSwapped, "rows of C");
   static constexpr int kStage = (BM + BN) * kFp8RowBytes;
-  // few columns: three CTAs to an SM, so that one's start and end overlap the
-  // others' loads
-  static constexpr int kCtasPerSm = BN >= 128 ? 1 : BN >= 64 ? 2 : 3;
-  static constexpr int kStages = BN >= 128 ? (kDirect ? 5 : 6) : BN >= 64 ? 4 : 3;
+  // few columns: two CTAs to an SM, so that one's start and end overlap the
+  // other's loads, and as many stages as fit: the weights come from DRAM, and
+  // with one CTA on most SMs the copies in flight bound the rate.  1 x 8192 by
+  // 8192 x 8192, weights not in the L2 cache: 14.7 us; three CTAs of three
+  // stages 17.0; one of ten stages 14.7, but 64 x 2048 x 8192 12.0 and 15.7,
+  // where clusters of eight SMs of their own do not all find room at once.
+  static constexpr int kCtasPerSm = BN >= 128 ? 1 : 2;
+  static constexpr int kStages = BN >= 128 ? (kDirect ? 5 : 6) : BN >= 64 ? 4 : BN >= 32 ? 5 : 6;
   static constexpr int kAccBufs = 4;
   static constexpr int kAccStride = BN < 32 ? 32 : BN;
   static constexpr int kTmemCols = kAccBufs * kAccStride;
