@@ -66,7 +66,7 @@ struct Fp8Plan {
 struct FormCost {
   int64_t round, block;
 };
-constexpr int64_t kExchange = 7;   // blocks of k
+constexpr int64_t kExchange = 7, kNarrowExchange = 4;   // blocks of k
 
 // col_vec: a scale for each column (row of B).
 Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool col_vec, int sm_count, int clusters) {
@@ -90,8 +90,10 @@ Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool
     // (128 CTAs) and 11.4 with 5 (160).  Of 128 x 128 tiles the exchange takes
     // as long as kExchange blocks: 256 x 4096 x 512 takes 7.3 us with two
     // ranges of two blocks and 5.4 with one, 256 x 4096 x 4096 12.0 and 15.2.
+    // Of narrow tiles it takes about four: 1 x 8192 x 1024 5.4 and 5.1 us, 1 x
+    // 8192 x 512 4.5 and 4.0, 1 x 8192 x 4096 9.0 and 11.8.
     while (s < 8 && tiles * (s + 1) <= sm_count && kb / (s + 1) >= 2) ++s;
-    if (!p.swapped && kb - (kb + s - 1) / s <= kExchange) s = 1;
+    if (kb - (kb + s - 1) / s <= (p.swapped ? kNarrowExchange : kExchange)) s = 1;
   }
   s = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(s, 8), kb));
   const int64_t per = (kb + s - 1) / s;
