@@ -68,8 +68,11 @@ struct FormCost {
 };
 constexpr int64_t kExchange = 7, kNarrowExchange = 4;   // blocks of k
 
-// col_vec: a scale for each column (row of B).
-Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool col_vec, int sm_count, int clusters) {
+// col_vec: a scale for each column (row of B).  room(s): clusters of s CTAs
+// that find an SM for each CTA at a time.
+template <class Room>
+Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool col_vec, int sm_count, int clusters,
+                     Room room) {
   Fp8Plan p;
   // Few tokens: the weights' rows fill the tensor core's 128 rows.
   p.swapped = m <= 64;
@@ -92,7 +95,9 @@ Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool
     // ranges of two blocks and 5.4 with one, 256 x 4096 x 4096 12.0 and 15.2.
     // Of narrow tiles it takes about four: 1 x 8192 x 1024 5.4 and 5.1 us, 1 x
     // 8192 x 512 4.5 and 4.0, 1 x 8192 x 4096 9.0 and 11.8.
-    while (s < 8 && tiles * (s + 1) <= sm_count && kb / (s + 1) >= 2) ++s;
+    // Clusters lie within a group of SMs, so large ones leave some unused: 64 x
+    // 2048 x 8192 (16 tiles) takes 9.7 us with six ranges, 11.9 with eight.
+    while (s < 8 && tiles * (s + 1) <= sm_count && kb / (s + 1) >= 2 && tiles <= room((int)s + 1)) ++s;
     if (kb - (kb + s - 1) / s <= (p.swapped ? kNarrowExchange : kExchange)) s = 1;
   }
   s = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(s, 8), kb));
@@ -139,7 +144,14 @@ mpg_status launch_product(DeviceInfo* dev, int64_t m, int64_t n, int64_t k, cons
   int clusters = 0;
   mpg_status s = resident_clusters(dev, kern.fn, kern.block, kern.smem_bytes, 2, &clusters);
   if (s != MPG_OK) return s;
-  const Fp8Plan plan = plan_product(m, n, k, o, B.scale_rows == 1, dev->sm_count, clusters);
+  // (the divided form of wide tiles has one CTA to an SM)
+  Fp8Kernel wide;
+  fp8_lookup(128, false, true, false, &wide);
+  auto room = [&](int size) {
+    int fit = 0;
+    return resident_clusters(dev, wide.fn, wide.block, wide.smem_bytes, size, &fit) == MPG_OK ? fit : 0;
+  };
+  const Fp8Plan plan = plan_product(m, n, k, o, B.scale_rows == 1, dev->sm_count, clusters, room);
   const mpg_fp8_operand& R = plan.swapped ? B : A;
   const mpg_fp8_operand& S = plan.swapped ? A : B;
   if (!plan.pair) {
