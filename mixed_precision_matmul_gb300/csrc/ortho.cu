@@ -18,8 +18,8 @@
 // are computed, and stored twice.  A step costs m^2 n + m^3 + 2 m^2 n flops
 // (m the shorter side) instead of 2 m^2 n + 2 m^3 + 2 m^2 n.
 //
-// On a GB300, five steps from a graph: 4096^2 takes 905 us (1520 TFLOP/s of
-// those flops, 0.78 of what a large library product reaches), bound by the
+// On a GB300, five steps from a graph: 4096^2 takes 905 to 940 us (about 1500
+// TFLOP/s of those flops, 0.78 of what a large library product reaches), bound by the
 // tensor cores, by the last rounds of tiles (256 and 136 tiles on 76 pairs) and
 // by the ways in and out of fifteen launches; 12 matrices of 2048 x 768 take
 // 329 us, where those two weigh most; 256 x 1000 takes 106 us, all of it
