@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
       float rsc[4], csc[4];
       auto fetch_scales = [&](int j, int kb) {
         if (kb < nkb) {
-          rsc[j] = __ldg(row_src);
-          csc[j] = __ldg(col_src);
+          rsc[j] = ld_global(row_src);
+          csc[j] = ld_global(col_src);
           row_src += p.sr_k;
           col_src += p.sc_k;
         }

@@ -268,10 +268,10 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
       float rsc[4], csc[4];
       auto fetch_scales = [&](int i, int kb) {
         if (kb < nkb) {
-          rsc[i] = __ldg(row_src);
+          rsc[i] = ld_global(row_src);
           row_src += p.sr_k;
           if (!T::kColVec) {
-            csc[i] = __ldg(col_src);
+            csc[i] = ld_global(col_src);
             col_src += p.sc_k;
           }
         }

@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(XT) == 2 ? 4 : 2) fp8_quant_k
   PT v[8][4];
   const XT* src = reinterpret_cast<const XT*>(p.x) + (int64_t)row0 * p.ldx + col;
   if (full_cols && p.x_align > (int)sizeof(XT) && row0 + 8 <= p.rows) {
-    // the widest loads that the lines' alignment allows
+    // the widest loads that the lines' alignment allows (non-coherent: an
+    // ordinary launch, which starts after the kernel that wrote x)
     auto load_patch = [&](auto unit) {
       using U = decltype(unit);
       constexpr int kUnits = 8 * sizeof(XT) / sizeof(U);
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(256) fp8_align_kernel(const __grid_constant__ 
     const uint32_t* w = reinterpret_cast<const uint32_t*>(src - sh);
     uint32_t x[5], o[4];
 #pragma unroll
-    for (int n = 0; n < 5; ++n) x[n] = (4 * n - (int64_t)sh < left && (n < 4 || sh > 0)) ? __ldg(w + n) : 0u;
+    for (int n = 0; n < 5; ++n) x[n] = (4 * n - (int64_t)sh < left && (n < 4 || sh > 0)) ? ld_global(w + n) : 0u;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       o[n] = __funnelshift_r(x[n], x[n + 1], 8 * sh);

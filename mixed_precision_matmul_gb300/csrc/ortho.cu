@@ -104,7 +104,7 @@ __device__ __forceinline__ void read_batch(const OrthoScaleParams& p, ChunkWalk&
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
 #pragma unroll
-      for (int h = 0; h < (int)sizeof(XT) / 2; ++h) w[u][h] = __ldg(reinterpret_cast<const uint4*>(line[u]) + h);
+      for (int h = 0; h < (int)sizeof(XT) / 2; ++h) w[u][h] = ld_global(reinterpret_cast<const uint4*>(line[u]) + h);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       XT e[8];
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
     uint32_t g = 0;
     for (int t = worker; t < p.num_tiles; t += workers, ++g) {
       const OrthoTile tc = ortho_tile(p, t);
-      const float f = p.factor ? __ldg(p.factor + tc.b) : 1.0f;
+      const float f = p.factor ? ld_global(p.factor + tc.b) : 1.0f;
       const float ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
       const float cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
       const float co = p.co;
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
         const int c0 = tc.nb * T::kTile + cc * 32;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          z[i] = zrow && c0 + 8 * i < p.n ? __ldg(reinterpret_cast<const uint4*>(zrow + c0) + i) : make_uint4(0, 0, 0, 0);
+          z[i] = zrow && c0 + 8 * i < p.n ? ld_global(reinterpret_cast<const uint4*>(zrow + c0) + i) : make_uint4(0, 0, 0, 0);
       };
       fetch_z(cc0);
       if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
   cluster_sync_all();
   const bool live = *abort_flag == 0 && rows_here > 0;
   if (live && warp >= 2) {
-    const float f = p.factor ? __ldg(p.factor + tc.b) : 1.0f;
+    const float f = p.factor ? ld_global(p.factor + tc.b) : 1.0f;
     out.ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
     out.cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
     switch (p.splits) {

@@ -103,6 +103,29 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Reads of what the kernel before this one may have written, after
+// griddep_wait.  An ordinary load: the non-coherent path (__ldg) is for memory
+// that nothing writes while the kernel is resident, and a programmatic
+// dependent is resident before its predecessor's stores.
+__device__ __forceinline__ float ld_global(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_global(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_global(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // True in one lane of a converged warp.  An MMA loop that the whole warp runs,
 // with only the instructions themselves under this predicate, keeps its
 // descriptors in uniform registers, where tcgen05.mma wants them; in a branch
