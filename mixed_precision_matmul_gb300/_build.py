@@ -2,8 +2,9 @@
 
 Every translation unit under ``csrc/`` is compiled by nvcc in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked (static CUDA runtime)
-into ``mixed_precision_matmul_gb300/_build/libmpgemm.so``; g++ compiles the
-marshalling extension of the torch forms beside it.  The ptxas resource
+into ``mixed_precision_matmul_gb300/_build/libmpgemm.so``; where torch and g++
+are there, the marshalling extension of the torch forms is compiled beside it
+(without it those calls are marshalled in Python).  The ptxas resource
 report (``-Xptxas -v``: registers, spills, shared memory) of each unit is kept
 in ``_build/ptxas.log``.
 """
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -85,7 +87,9 @@ def _compile(src: str) -> tuple[str, str]:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (when sources changed) and link libmpgemm.so; returns its path."""
+    """Compile (when sources changed) and link libmpgemm.so; returns its path.
+    The library needs nvcc alone; the marshalling extension of the torch forms
+    is left out, with a warning, where it does not compile."""
     os.makedirs(BUILD, exist_ok=True)
     if force:
         for f in os.listdir(BUILD):
@@ -95,7 +99,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         calls = ex.submit(build_torch_calls)
         results = list(ex.map(_compile, SOURCES))
-        calls.result()
     objs = [o for o, _ in results]
     logs = "".join(f"== {s}\n{log}" for s, (_, log) in zip(SOURCES, results) if log)
     if logs:
@@ -108,15 +111,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    failure = calls.exception()
+    if failure is not None and not isinstance(failure, ModuleNotFoundError):     # (no torch: nothing to marshal)
+        warnings.warn(f"the torch forms' calls will be marshalled in Python: {failure}", RuntimeWarning)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB
 
 
 def torch_calls_path() -> str:
-    """The marshalling extension, built for the torch that is installed."""
+    """The marshalling extension, built for the torch and the Python that are running."""
+    import sysconfig
+
     import torch
-    return os.path.join(BUILD, f"_torch_calls-{torch.__version__}.so")
+    return os.path.join(BUILD, f"_torch_calls-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
 
 
 def build_torch_calls() -> str:

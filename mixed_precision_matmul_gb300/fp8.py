@@ -23,17 +23,24 @@ def _types():
 
 @functools.cache
 def _calls():
-    """The extension that makes the plain calls (csrc/torch_calls.cpp)."""
+    """The extension that makes the plain calls (csrc/torch_calls.cpp), or None
+    where there is none for this torch and Python: every call then takes the
+    Python form below, which costs the host 9 us more."""
     import importlib.machinery
     import importlib.util
+    import warnings
 
     _types()                                    # torch first: the extension links to it
+    lib = _m.lib()
     path = _m._build.torch_calls_path()
     loader = importlib.machinery.ExtensionFileLoader("_torch_calls", path)
     spec = importlib.util.spec_from_file_location("_torch_calls", path, loader=loader)
-    module = importlib.util.module_from_spec(spec)
-    loader.exec_module(module)
-    lib = _m.lib()
+    try:
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"8-bit calls are marshalled in Python, build() makes the extension: {e}", RuntimeWarning)
+        return None
     module.init(*(ctypes.cast(f, ctypes.c_void_p).value
                   for f in (lib.mpg_gemm_fp8, lib.mpg_gemm_fp8_workspace_size, lib.mpg_fp8_quantize)))
     return module
@@ -129,7 +136,8 @@ def fp8_quantize(x, fmt="e4m3", block: str = "row", transpose: bool = False, str
     scale_rows = 1 if block == "row" else BLOCK
     if scale_rows == BLOCK and block != "tile":
         raise ValueError("block is 'row' or 'tile'")
-    r = _calls().quantize(x, fmt, scale_rows, transpose)
+    calls = _calls()
+    r = calls.quantize(x, fmt, scale_rows, transpose) if calls else None
     if r is not None:
         if r.__class__ is int:
             _m._check(r)
@@ -232,8 +240,9 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
                           lambda: gemm_fp8(A, a_scale, B, b_scale, C, alpha, beta, out_dtype, workspace, opts))
     if C is None and opts is None and workspace is None and beta == 0.0:
         code = codes.get(out_dtype) if out_dtype is not None else _m.BF16
-        if code is not None:
-            r = _calls().gemm_fp8(A, a_scale, B, b_scale, alpha, code)
+        calls = _calls()
+        if calls and code is not None:
+            r = calls.gemm_fp8(A, a_scale, B, b_scale, alpha, code)
             if r is not None:
                 if r.__class__ is int:
                     _m._check(r)
