@@ -124,7 +124,9 @@ typedef struct {
   /* Tile width along N: 0 = chosen by the library, else 64, 128 or 256
    * (256 only for the direct fp16/bf16/tf32 paths). */
   int32_t tile_n;
-  /* Upper bound for any single wait inside a kernel, in nanoseconds.
+  /* Upper bound for any single wait inside a kernel, in nanoseconds, counted
+   * from the wait's start and looked at every 64 polls (about 5 us); the 8-bit
+   * product and the orthogonalised update count from the 64th poll.
    * 0 = default (2 s).  On expiry the kernel stops, records MPG_ERR_TIMEOUT in
    * the device status word and returns without hanging the GPU. */
   int64_t wait_timeout_ns;

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   ctl.abort = abort_flag;
   ctl.status = p.status;
   ctl.limit_ns = p.wait_limit_ns;
+  ctl.late_clock = true;
   const uint32_t op_smem = smem_addr(smem);
   bool ok = true;
 

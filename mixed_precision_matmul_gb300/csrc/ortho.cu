@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
   if constexpr (T::kPair) ctl.peer_abort = cluster_generic_ptr(const_cast<int*>(abort_flag), rank ^ 1u);
   ctl.status = p.status;
   ctl.limit_ns = p.wait_limit_ns;
+  ctl.late_clock = true;
   const uint32_t op_smem = smem_addr(smem);
 
   if (warp == 0) {
@@ -861,6 +862,7 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
   ctl.abort = abort_flag;
   ctl.status = p.status;
   ctl.limit_ns = p.wait_limit_ns;
+  ctl.late_clock = true;
   const uint32_t op_smem = smem_addr(smem);
 
   // this CTA's share of the tile's rows, and Z's elements there

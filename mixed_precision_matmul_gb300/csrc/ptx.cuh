@@ -61,6 +61,7 @@ struct WaitCtl {
   volatile int* peer_abort = nullptr;   // the other CTA's flag in a CTA pair (distributed shared memory)
   uint32_t* status;        // global device status word
   uint64_t limit_ns;
+  bool late_clock = false; // the limit counts from a wait's 64th poll (see mbar_wait)
 };
 
 __device__ __forceinline__ void raise_abort(const WaitCtl& c, uint32_t code) {
@@ -71,18 +72,18 @@ __device__ __forceinline__ void raise_abort(const WaitCtl& c, uint32_t code) {
 
 // Wait until the phase with the given parity of `bar` has completed.  Returns
 // false (after raising the CTA's abort flag) when the time limit passes, or
-// when another role of the CTA has already aborted.
+// when another role of the CTA has already aborted.  Reading %globaltimer takes
+// far longer than most waits of a loop last; with late_clock it is not read
+// before the 64th poll, and the limit counts from there.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
   if (mbar_test(bar, parity)) return true;
-  // the clock starts at the 64th poll: reading %globaltimer takes far longer
-  // than most waits last
-  uint64_t t0 = 0;
+  uint64_t t0 = c.late_clock ? 0 : global_timer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_test(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (*c.abort) return false;
       const uint64_t t = global_timer_ns();
-      if (it == 64) t0 = t;
+      if (c.late_clock && it == 64) t0 = t;
       if (t - t0 > c.limit_ns || it > (1u << 30)) {
         raise_abort(c, kStatusTimeout);
         return false;
