@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
           tc_fence_after_sync();
           const uint32_t slot = ring.slot(kb);
           const float s = ld_shared_f32(slot + lane * 4);
-          add_block<T::kCols>(acc, tacc + ab * T::kAccStride, slot, pack2(s, s), [&]() { release(ab); });
+          add_block<T::kCols>(acc, tacc + ab * T::kAccStride, slot, s, [&]() { release(ab); });
         }
         if (!T::kDirect || !ok) break;
         __syncwarp();
@@ -287,14 +287,13 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
           const bool more = kb + 1 < nkb;
           const uint32_t next = tacc + ((i + 1) % T::kAccBufs) * T::kAccStride;
           fetch_scales(3, kb + 3);
-          const float s = rsc[0] * csc[0];
-          const f32x2 rs = pack2(s, s);
+          const BlockScale s = block_scale<false>(rsc[0], csc[0]);
           tmem_ld_wait();
           release(i % T::kAccBufs);
           if (more && !load(i + 1)) { ok = false; break; }
 #pragma unroll
           for (int c = 0; c < kReads; ++c) {
-            scale_add<32, false>(acc + c * 16, v[c], 0, 0, rs);
+            scale_add<32, false>(acc + c * 16, v[c], 0, 0, s, rsc[0], csc[0]);
             if (more) tmem_ld_32cols(next + c * 32, v[c]);
           }
 #pragma unroll

@@ -297,26 +297,25 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
         const bool more = kb + 1 < nkb;
         const uint32_t here = tacc + (it & 1u) * T::kTile, next = tacc + ((it + 1) & 1u) * T::kTile;
         fetch_scales(3, kb + 3);
-        const float s = rsc[0] * csc[0];
-        const f32x2 rs = pack2(s, s);
+        const BlockScale s = block_scale<T::kColVec>(rsc[0], csc[0]);
         if (T::kColVec && !__all_sync(0xffffffffu, known) && !warp_wait(&scale_full[slot], slot_ph, ctl)) { ok = false; break; }
         const uint32_t sl = scales + slot * (T::kScaleSlot * 4) - 128;
         tmem_ld_wait();
-        scale_add<32, T::kColVec>(acc, v[0], sl, 0, rs);
+        scale_add<32, T::kColVec>(acc, v[0], sl, 0, s, rsc[0], csc[0]);
         tmem_ld_32cols(here + 64, v[0]);
-        scale_add<32, T::kColVec>(acc + 16, v[1], sl, 32, rs);
+        scale_add<32, T::kColVec>(acc + 16, v[1], sl, 32, s, rsc[0], csc[0]);
         tmem_ld_32cols(here + 96, v[1]);
         // barriers take a while to answer: asked early
         const bool ready = more && mbar_test(&acc_full[(it + 1) & 1u], ((it + 1) >> 1) & 1u);
         tmem_ld_wait();
         if (!hand_over(it, more, ready)) { ok = false; break; }
-        scale_add<32, T::kColVec>(acc + 32, v[0], sl, 64, rs);
+        scale_add<32, T::kColVec>(acc + 32, v[0], sl, 64, s, rsc[0], csc[0]);
         if (more) tmem_ld_32cols(next, v[0]);
         if constexpr (T::kColVec) {
           const uint32_t ns = slot + 1 == T::kScaleSlots ? 0 : slot + 1;
           known = more && mbar_test(&scale_full[ns], ns == 0 ? slot_ph ^ 1u : slot_ph);
         }
-        scale_add<32, T::kColVec>(acc + 48, v[1], sl, 96, rs);
+        scale_add<32, T::kColVec>(acc + 48, v[1], sl, 96, s, rsc[0], csc[0]);
         if (more) tmem_ld_32cols(next + 32, v[1]);
 #pragma unroll
         for (int i = 0; i < 3; ++i) {

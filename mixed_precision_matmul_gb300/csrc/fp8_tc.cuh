@@ -147,30 +147,79 @@ struct ScaleRing {
   }
 };
 
+// How a block's two scales meet its sum P, |P| in [2^-32, 2^39) or 0: scales may
+// be any fp32 values, and no step but the last may leave fp32's normal range.
+//   one scale for all columns   P * (row * column), where that product of the
+//                               scales is in the normal range;
+//   a scale for each column     (P * row) * column, where the row's scale is in
+//                               [2^-94, 2^89), so that P * row is in range.
+// Elsewhere the row's scale is taken in two parts, first * last, last a power
+// of two: ((P * first) * column) * last.  For tiny rows first is in
+// [2^-94, 2^-39): P * first * column cannot overflow, and where it is below the
+// normal range the result is below 2^-181.  For huge rows first is in
+// [2^69, 2^89): the reverse.
+struct BlockScale {
+  f32x2 row;           // of the plain form: the row's scale, or with one scale for all columns their product
+  bool plain;          // for all lanes of the warp
+};
+template <bool kColVec>
+__device__ __forceinline__ BlockScale block_scale(float row, float col) {
+  const float s = kColVec ? row : row * col;
+  const uint32_t e = (__float_as_uint(s) >> 23) & 255u;
+  BlockScale r;
+  r.row = pack2(s, s);
+  r.plain = __all_sync(0xffffffffu, kColVec ? e - (127u - 94u) < 94u + 89u : e - 1u < 254u) != 0;
+  return r;
+}
+__device__ __forceinline__ void split_scale(float row, float& first, float& last) {
+  const int e = (int)((__float_as_uint(row) >> 23) & 255u) - 127;
+  int shift = 0;                                 // (also of infinities and NaN, e = 128)
+  if (e < -94) shift = -55;
+  else if (e >= 108 && e < 128) shift = 39;
+  else if (e >= 89 && e < 128) shift = 20;
+  first = row * __uint_as_float((uint32_t)(127 - shift) << 23);
+  last = __uint_as_float((uint32_t)(127 + shift) << 23);
+}
+
 // acc += row scale * column scale * v on kN columns from column c0 of the
-// warp's slot.
+// warp's slot (col: the scale of all columns).
 template <int kN, bool kColVec>
-__device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t slot, int c0, f32x2 rs) {
-  if constexpr (kColVec) {
+__device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t slot, int c0, const BlockScale& s, float row,
+                                          float col) {
+  if (s.plain) {
 #pragma unroll
     for (int j = 0; j < kN; j += 4) {
-      f32x2 s0, s1;
-      ld_shared_pairs(slot + 128 + (c0 + j) * 4, s0, s1);
-      fma2(acc[j / 2], mul2(pack2(v[j], v[j + 1]), s0), rs);
-      fma2(acc[j / 2 + 1], mul2(pack2(v[j + 2], v[j + 3]), s1), rs);
+      const f32x2 v0 = pack2(v[j], v[j + 1]), v1 = pack2(v[j + 2], v[j + 3]);
+      if constexpr (kColVec) {
+        f32x2 s0, s1;
+        ld_shared_pairs(slot + 128 + (c0 + j) * 4, s0, s1);
+        fma2(acc[j / 2], mul2(v0, s.row), s0);
+        fma2(acc[j / 2 + 1], mul2(v1, s.row), s1);
+      } else {
+        fma2(acc[j / 2], v0, s.row);
+        fma2(acc[j / 2 + 1], v1, s.row);
+      }
     }
   } else {
+    float f, l;
+    split_scale(row, f, l);
+    const f32x2 first = pack2(f, f), last = pack2(l, l);
 #pragma unroll
-    for (int j = 0; j < kN; j += 2) fma2(acc[j / 2], pack2(v[j], v[j + 1]), rs);
+    for (int j = 0; j < kN; j += 4) {
+      f32x2 s0 = pack2(col, col), s1 = s0;
+      if constexpr (kColVec) ld_shared_pairs(slot + 128 + (c0 + j) * 4, s0, s1);
+      fma2(acc[j / 2], mul2(mul2(pack2(v[j], v[j + 1]), first), s0), last);
+      fma2(acc[j / 2 + 1], mul2(mul2(pack2(v[j + 2], v[j + 3]), first), s1), last);
+    }
   }
 }
 
 // One block of k with a scale for each column: the accumulator at `ta` (kCols
-// columns of this warp's 32 lanes) added to the running sums under the row
-// scale rs and the column scales in `slot`, two reads of 32 columns on their
+// columns of this warp's 32 lanes) added to the running sums under the row's
+// scale and the column scales in `slot`, two reads of 32 columns on their
 // way.  `release` runs when all columns are in registers.
 template <int kCols, class Release>
-__device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, uint32_t slot, f32x2 rs,
+__device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, uint32_t slot, float row,
                                           Release release) {
   constexpr int kChunk = kCols >= 32 ? 32 : 16;
   constexpr int kN = kCols / kChunk;
@@ -181,10 +230,11 @@ __device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, 
     if constexpr (kChunk == 32) tmem_ld_32cols(ta + c * kChunk, v[c]);
     else tmem_ld_16cols(ta + c * kChunk, v[c]);
   }
+  const BlockScale s = block_scale<true>(row, 1.0f);
   tmem_ld_wait();
   release();
 #pragma unroll
-  for (int c = 0; c < kN; ++c) scale_add<kChunk, true>(acc + c * kChunk / 2, v[c], slot, c * kChunk, rs);
+  for (int c = 0; c < kN; ++c) scale_add<kChunk, true>(acc + c * kChunk / 2, v[c], slot, c * kChunk, s, row, 1.0f);
 }
 
 // alpha x + beta C for 32 rows (one a lane) and 32 columns (x[j]: columns 2j
