@@ -447,7 +447,8 @@ mpg_status mpg_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t l
  *     C[i, j] = alpha * sum_kb sA[i, kb] sB[j, kb] sum_{l in block kb} A[i, l] B[j, l] + beta * C[i, j].
  * The tensor cores sum each block of 128 k in fp32; the blocks' sums are
  * scaled and added in fp32 with round-to-nearest fused multiply-adds, in the
- * order of k (per range, where k is divided).  A and B may differ in format
+ * order of k (per range, where k is divided).  The scales may be anywhere in
+ * fp32's range: what counts is whether the scaled sums are.  A and B may differ in format
  * and in scale_rows.  C is row-major, ldc >= n, of type opt->c_dtype (fp32 by
  * default), rounded once when stored; beta == 0: C is not read; k == 0 or
  * alpha == 0: C = beta*C and the operands are not read.

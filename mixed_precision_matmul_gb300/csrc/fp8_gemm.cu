@@ -31,6 +31,8 @@
 // scale for each column 118 us in fp32 (with eight epilogue warps instead of
 // sixteen 123; one tile a CTA 121; the next block's columns read during the
 // additions 139).
+#include <type_traits>
+
 #include "fp8_tc.cuh"
 
 namespace mpg {
@@ -60,7 +62,8 @@ struct Fp8Traits {
   static constexpr int kTmemCols = kAccBufs * kAccStride;
   static constexpr int kEpiWarps = kDirect ? 16 : BN >= 64 ? 8 : 4;
   static constexpr int kCols = BN / (kEpiWarps / 4);      // columns of one epilogue warp
-  static constexpr int kThreads = (2 + kEpiWarps) * 32;
+  static constexpr bool kScans = kDirect && kColVec;     // a warp looks at later tiles' column scales
+  static constexpr int kThreads = (2 + kEpiWarps + kScans) * 32;
   using Ring = ScaleRing<kCols, kSwapped || kDirect ? 4 : 8>;
   static constexpr int kRingBytes = kColVec ? kEpiWarps * Ring::kBytes : 0;
   // The staged tile's lines run along C's: columns of a row, or, swapped, the
@@ -69,7 +72,7 @@ struct Fp8Traits {
   static constexpr int kPitch = kSwapped ? BM : BN + 4;   // floats
   static constexpr int kEpiBytes = kDirect ? kEpiWarps * 2048 : 0;   // rows on their way to C, tile after tile
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
-  static constexpr int kSmemBytes = 1024 + kStages * kStage + kRingBytes + kEpiBytes + kNumBars * 8 + 16;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kRingBytes + kEpiBytes + kNumBars * 8 + 16 + (kScans ? Notes::kBytes : 0);
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory budget");
   static_assert(kLines * kPitch * 4 <= kStages * kStage, "the staged tile reuses the operand stages");
   static_assert(kCtasPerSm * kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
@@ -90,6 +93,10 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
   uint64_t* done_bar = acc_empty + T::kAccBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Notes notes;
+  notes.full = reinterpret_cast<uint64_t*>(tmem_slot + 2);
+  notes.empty = notes.full + kNotes;
+  notes.word = reinterpret_cast<uint32_t*>(notes.empty + kNotes);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -112,6 +119,10 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
       mbar_init(&acc_empty[i], T::kEpiWarps);
     }
     mbar_init(done_bar, 1);
+    for (int i = 0; i < (T::kScans ? (int)kNotes : 0); ++i) {
+      mbar_init(&notes.full[i], 1);
+      mbar_init(&notes.empty[i], T::kEpiWarps);
+    }
     *abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_map(&p.map_r);
@@ -190,6 +201,11 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
       drain_wait(done_bar, 0, p.wait_limit_ns);
     }
     __syncwarp();
+  } else if (T::kScans && warp == 2 + T::kEpiWarps) {
+    // ------------------------------------------------------------ column scales of the tiles to come
+    uint32_t n = 0;
+    for (int t = tile + step; t < p.num_tiles && ok; t += step, ++n)
+      ok = notes.leave(n, scan_alone<T::BN>(p, lane, col_of(t), kb0, nkb), lane, ctl);
   } else {
     // ------------------------------------------------------------ running sums
     const int q = warp & 3;
@@ -220,23 +236,32 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
       auto begin = [&](int t) {
         ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row_of(t) + 32 * q, col_of(t) + wc0, kb0, nkb);
       };
-      begin(tile);
-      for (int t = tile; t < p.num_tiles && ok; t += step) {
-#pragma unroll
-        for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
+      auto blocks = [&](auto plain) {
 #pragma unroll 1
         for (int kb = 0; kb < nkb; ++kb, ++i) {
           const uint32_t ab = i % T::kAccBufs;
           __syncwarp();                                  // every lane is done with the last block's slot
           ring.fetch(kb + T::Ring::kDepth - 1);
           cp_async_wait<T::Ring::kDepth - 1>();
-          if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; break; }
+          if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) return false;
           __syncwarp();
           tc_fence_after_sync();
           const uint32_t slot = ring.slot(kb);
           const float s = ld_shared_f32(slot + lane * 4);
-          add_block<T::kCols>(acc, tacc + ab * T::kAccStride, slot, s, [&]() { release(ab); });
+          add_block<T::kCols, decltype(plain)::value>(acc, tacc + ab * T::kAccStride, slot, s, [&]() { release(ab); });
         }
+        return true;
+      };
+      begin(tile);
+      bool plain;                                        // the form of this tile's blocks
+      if constexpr (T::kSwapped) plain = scan_alone<T::kCols>(p, lane, col0 + wc0, kb0, nkb);
+      else plain = scan_together<T::kEpiWarps * 32, T::BN>(p, ew * 32 + lane, col0, kb0, nkb);
+      uint32_t n = 0;
+      for (int t = tile; t < p.num_tiles && ok; t += step, ++n) {
+#pragma unroll
+        for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
+        if (T::kScans && n > 0 && !notes.read(n - 1, lane, ctl, &plain)) { ok = false; break; }
+        ok = plain ? blocks(std::true_type()) : blocks(std::false_type());
         if (!T::kDirect || !ok) break;
         __syncwarp();
         if (t + step < p.num_tiles) begin(t + step);     // (its scales are on their way during the stores)
@@ -287,15 +312,19 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
           const bool more = kb + 1 < nkb;
           const uint32_t next = tacc + ((i + 1) % T::kAccBufs) * T::kAccStride;
           fetch_scales(3, kb + 3);
-          const BlockScale s = block_scale<false>(rsc[0], csc[0]);
+          const bool plain_here = __all_sync(0xffffffffu, plain_scale(rsc[0], csc[0])) != 0;
           tmem_ld_wait();
           release(i % T::kAccBufs);
           if (more && !load(i + 1)) { ok = false; break; }
+          auto add = [&](auto plain) {
 #pragma unroll
-          for (int c = 0; c < kReads; ++c) {
-            scale_add<32, false>(acc + c * 16, v[c], 0, 0, s, rsc[0], csc[0]);
-            if (more) tmem_ld_32cols(next + c * 32, v[c]);
-          }
+            for (int c = 0; c < kReads; ++c) {
+              scale_add<32, false, decltype(plain)::value>(acc + c * 16, v[c], 0, 0, rsc[0], csc[0]);
+              if (more) tmem_ld_32cols(next + c * 32, v[c]);
+            }
+          };
+          if (plain_here) add(std::true_type());
+          else add(std::false_type());
 #pragma unroll
           for (int j = 0; j < 3; ++j) {
             rsc[j] = rsc[j + 1];

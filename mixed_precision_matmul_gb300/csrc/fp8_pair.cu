@@ -6,8 +6,9 @@
 // block's product in one of two TMEM buffers (256 columns each), and eight
 // epilogue warps in each CTA (32 rows x 128 columns a warp, 128 running sums a
 // thread, in registers for the whole k range) add it under its scales while
-// the tensor cores fill the other buffer.  A warp of its own fetches the
-// scales, eight blocks ahead.
+// the tensor cores fill the other buffer.  Where each column has a scale of its
+// own, two warps fetch those, up to eight blocks ahead; rows' scales (and those
+// of 128 columns) go straight to registers, three blocks ahead.
 //
 // A block's products take the tensor cores 512 cycles (about 620 here: the
 // operands' way in and out of shared memory).  The epilogue has to keep up:
@@ -24,6 +25,8 @@
 // buffers (642 us: the tensor cores read R twice), 256 x 128 tiles (644 us);
 // at 4096^3, the 16-lane read of TMEM that lets a thread keep its columns'
 // scales in registers (112 us: that read takes three times as long).
+#include <type_traits>
+
 #include "fp8_tc.cuh"
 
 namespace mpg {
@@ -40,6 +43,7 @@ struct Fp8PairTraits {
   static constexpr int kAccBufs = 2;
   static constexpr int kTmemCols = kAccBufs * kTile;
   static constexpr int kEpiWarps = 8;
+  static constexpr int kScaleWarps = kColVec ? 2 : 0;      // each fetches the scales of half the columns
   static constexpr int kCols = kTile / (kEpiWarps / 4);
   static constexpr int kThreads = (4 + kEpiWarps) * 32;
   // Registers: the block is launched with 168 a thread; the first warpgroup
@@ -53,7 +57,7 @@ struct Fp8PairTraits {
   static constexpr int kScaleBytes = (kScaleSlots * kScaleSlot * 4 + 15) / 16 * 16;
   static constexpr int kEpiBytes = kEpiWarps * 2048;
   static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 2 * kScaleSlots + 1;
-  static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiBytes + kScaleBytes + kNumBars * 8 + 16;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiBytes + kScaleBytes + kNumBars * 8 + 16 + kScaleWarps * Notes::kBytes;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
@@ -90,6 +94,14 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
   uint64_t* done_bar = scale_empty + T::kScaleSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // each half's notes on the tiles' column scales
+  auto notes_of = [&](int h) {
+    Notes x;
+    x.full = reinterpret_cast<uint64_t*>(tmem_slot + 2) + h * 2 * kNotes;
+    x.empty = x.full + kNotes;
+    x.word = reinterpret_cast<uint32_t*>(reinterpret_cast<uint64_t*>(tmem_slot + 2) + T::kScaleWarps * 2 * kNotes) + h * kNotes;
+    return x;
+  };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -111,6 +123,10 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
       mbar_init(&scale_empty[i], T::kEpiWarps);
     }
     mbar_init(done_bar, 1);
+    for (int i = 0; i < T::kScaleWarps * (int)kNotes; ++i) {
+      mbar_init(&notes_of(i / kNotes).full[i % kNotes], 1);
+      mbar_init(&notes_of(i / kNotes).empty[i % kNotes], T::kEpiWarps / 2);
+    }
     *abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_map(&p.map_r);
@@ -200,30 +216,30 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
     }
   } else if (T::kColVec) {
     // ------------------------------------------------------------ column scales
-    uint32_t slot = 0, ph = 0;
+    uint32_t slot = 0, ph = 0, n = 0;
     bool ok = true;
-    for (int t = worker; t < p.num_tiles && ok; t += workers) {
-      const PairTile tc = pair_tile(p, t);
-      // this lane's columns (clamped to the operand's last line)
-      const int c0 = (warp - 2) * T::kCols + lane;
-      const float* src[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        src[i] = p.sc + (int64_t)(min(tc.cb * T::kTile + c0 + 32 * i, p.cols - 1) >> p.sc_shift) * p.sc_row;
+    const Notes notes = notes_of(warp - 2);
+    ColumnScan scan;                                   // of the next tile
+    for (int t = worker; t < p.num_tiles && ok; t += workers, ++n) {
+      ColumnLines lines;
+      lines.start(p, pair_tile(p, t).cb * T::kTile + (warp - 2) * T::kCols, lane);
+      const bool more = t + workers < p.num_tiles;
+      if (more) scan.start(p, pair_tile(p, t + workers).cb * T::kTile + (warp - 2) * T::kCols, lane);
       for (int kb = 0; kb < nkb; ++kb) {
         if (!warp_wait(&scale_empty[slot], ph ^ 1u, ctl)) { ok = false; break; }
-        const uint32_t dst = smem_addr(scale_base) + (slot * T::kScaleSlot + c0) * 4;
+        const uint32_t dst = smem_addr(scale_base) + (slot * T::kScaleSlot + (warp - 2) * T::kCols + lane) * 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cp_async4(dst + i * 128, src[i]);
-          src[i] += p.sc_k;
-        }
+        for (int i = 0; i < 4; ++i)
+          if (i < lines.count) cp_async4(dst + i * 128, lines.column(p, i));
+        lines.next(p);
         cp_async_arrive(&scale_full[slot]);
+        if (more) scan.block(p);
         if (++slot == T::kScaleSlots) {
           slot = 0;
           ph ^= 1u;
         }
       }
+      if (ok && more) ok = notes.leave(n, scan.result(), lane, ctl);
     }
     cp_async_wait_all();
   }
@@ -249,9 +265,13 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
       tc_fence_after_sync();
       return true;
     };
-    uint32_t it = 0, slot = 0, slot_ph = 0;
+    uint32_t it = 0, slot = 0, slot_ph = 0, n = 0;
     bool ok = true;
-    for (int t = worker; t < p.num_tiles && ok; t += workers) {
+    bool plain_tile = true;                           // the columns' scales, where each has its own
+    if constexpr (T::kColVec)
+      plain_tile = scan_together<T::kEpiWarps * 32, T::kTile>(p, ew * 32 + lane, pair_tile(p, worker).cb * T::kTile, 0, nkb);
+    for (int t = worker; t < p.num_tiles && ok; t += workers, ++n) {
+      if (T::kColVec && n > 0 && !notes_of((int)half).read(n - 1, lane, ctl, &plain_tile)) break;
       f32x2 acc[T::kCols / 2];
 #pragma unroll
       for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
@@ -292,31 +312,36 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
       tmem_ld_32cols(tacc + (it & 1u) * T::kTile, v[0]);
       tmem_ld_32cols(tacc + (it & 1u) * T::kTile + 32, v[1]);
       bool known = false;
-#pragma unroll 1
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const bool more = kb + 1 < nkb;
-        const uint32_t here = tacc + (it & 1u) * T::kTile, next = tacc + ((it + 1) & 1u) * T::kTile;
+      bool plain_next = true;                         // one scale for all columns: the next block's form
+      auto begin_block = [&](int kb) {
         fetch_scales(3, kb + 3);
-        const BlockScale s = block_scale<T::kColVec>(rsc[0], csc[0]);
-        if (T::kColVec && !__all_sync(0xffffffffu, known) && !warp_wait(&scale_full[slot], slot_ph, ctl)) { ok = false; break; }
+        return !T::kColVec || __all_sync(0xffffffffu, known) || warp_wait(&scale_full[slot], slot_ph, ctl);
+      };
+      auto add = [&](bool more, auto plain) {
+        constexpr bool kPlain = decltype(plain)::value;
+        const uint32_t here = tacc + (it & 1u) * T::kTile, next = tacc + ((it + 1) & 1u) * T::kTile;
         const uint32_t sl = scales + slot * (T::kScaleSlot * 4) - 128;
         tmem_ld_wait();
-        scale_add<32, T::kColVec>(acc, v[0], sl, 0, s, rsc[0], csc[0]);
+        scale_add<32, T::kColVec, kPlain>(acc, v[0], sl, 0, rsc[0], csc[0]);
         tmem_ld_32cols(here + 64, v[0]);
-        scale_add<32, T::kColVec>(acc + 16, v[1], sl, 32, s, rsc[0], csc[0]);
+        scale_add<32, T::kColVec, kPlain>(acc + 16, v[1], sl, 32, rsc[0], csc[0]);
         tmem_ld_32cols(here + 96, v[1]);
         // barriers take a while to answer: asked early
         const bool ready = more && mbar_test(&acc_full[(it + 1) & 1u], ((it + 1) >> 1) & 1u);
+        if constexpr (!T::kColVec) plain_next = __all_sync(0xffffffffu, plain_scale(rsc[1], csc[1])) != 0;
         tmem_ld_wait();
-        if (!hand_over(it, more, ready)) { ok = false; break; }
-        scale_add<32, T::kColVec>(acc + 32, v[0], sl, 64, s, rsc[0], csc[0]);
+        if (!hand_over(it, more, ready)) return false;
+        scale_add<32, T::kColVec, kPlain>(acc + 32, v[0], sl, 64, rsc[0], csc[0]);
         if (more) tmem_ld_32cols(next, v[0]);
         if constexpr (T::kColVec) {
           const uint32_t ns = slot + 1 == T::kScaleSlots ? 0 : slot + 1;
           known = more && mbar_test(&scale_full[ns], ns == 0 ? slot_ph ^ 1u : slot_ph);
         }
-        scale_add<32, T::kColVec>(acc + 48, v[1], sl, 96, s, rsc[0], csc[0]);
+        scale_add<32, T::kColVec, kPlain>(acc + 48, v[1], sl, 96, rsc[0], csc[0]);
         if (more) tmem_ld_32cols(next + 32, v[1]);
+        return true;
+      };
+      auto end_block = [&]() {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
           rsc[i] = rsc[i + 1];
@@ -329,6 +354,30 @@ __global__ void __launch_bounds__(T::kThreads, 1) fp8_pair_kernel(const __grid_c
             slot = 0;
             slot_ph ^= 1u;
           }
+        }
+      };
+      if constexpr (T::kColVec) {
+        auto blocks = [&](auto plain) {
+#pragma unroll 1
+          for (int kb = 0; kb < nkb; ++kb) {
+            const bool more = kb + 1 < nkb;
+            if (!begin_block(kb)) return false;
+            if (!add(more, plain)) return false;
+            end_block();
+            ++it;
+          }
+          return true;
+        };
+        ok = plain_tile ? blocks(std::true_type()) : blocks(std::false_type());
+      } else {
+        bool plain_block = __all_sync(0xffffffffu, plain_scale(rsc[0], csc[0])) != 0;
+#pragma unroll 1
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          begin_block(kb);
+          ok = plain_block ? add(kb + 1 < nkb, std::true_type()) : add(kb + 1 < nkb, std::false_type());
+          if (!ok) break;
+          plain_block = plain_next;
+          end_block();
         }
       }
       if (!ok) break;

@@ -61,6 +61,11 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint16_t ld_shared_u16(uint32_t addr) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
@@ -97,6 +102,161 @@ __device__ __forceinline__ f32x2 mul2(f32x2 x, f32x2 y) {
 __device__ __forceinline__ void ld_shared_pairs(uint32_t addr, f32x2& a, f32x2& b) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
+
+// How a block's two scales meet its sum P, |P| in [2^-32, 2^39) or 0: scales may
+// be any fp32 values, and no step but the last may leave fp32's normal range.
+//   one scale for all columns   P * (row * column), where that product of the
+//                               scales is in the normal range;
+//   a scale for each column     (P * column) * row, where the columns' scales
+//                               are 0 or in [2^-94, 2^89), so that P * column is
+//                               in range.  (In the other order the multiply-add
+//                               has three operands that change: 126 us instead
+//                               of 118 at 4096^3.)
+// With one scale for all columns each block's form is chosen by itself (8192^3:
+// 437 us; 432 without the choice, 487 with one for every 32 columns).  With a
+// scale for each column that takes too long beside the additions (4096^3: 126
+// us; 118 without the choice): a tile's form is chosen by its columns' scales in
+// all blocks (120 us), which the epilogue's threads look at before the first
+// tile, while its first operands are on their way, and a warp beside them for
+// each tile after.
+// Elsewhere the row's scale is taken in two parts, first * last, last a power
+// of two: ((P * first) * column) * last.  For tiny rows first is in
+// [2^-94, 2^-39): P * first * column cannot overflow, and where it is below the
+// normal range the result is below 2^-181.  For huge rows first is in
+// [2^69, 2^89): the reverse.
+__device__ __forceinline__ uint32_t scale_field(float s) { return (__float_as_uint(s) >> 23) & 255u; }
+__device__ __forceinline__ bool plain_scale(float row, float col) { return scale_field(row * col) - 1u < 254u; }
+__device__ __forceinline__ bool plain_column(float col) {
+  return scale_field(col) - (127u - 94u) < 94u + 89u || col == 0.0f;
+}
+__device__ __forceinline__ void split_scale(float row, float& first, float& last) {
+  const int e = (int)scale_field(row) - 127;
+  int shift = 0;                                 // (also of infinities and NaN, e = 128)
+  if (e < -94) shift = -55;
+  else if (e >= 108 && e < 128) shift = 39;
+  else if (e >= 89 && e < 128) shift = 20;
+  first = row * __uint_as_float((uint32_t)(127 - shift) << 23);
+  last = __uint_as_float((uint32_t)(127 + shift) << 23);
+}
+
+// Whether the scales of kTileCols columns from col0 on are plain in n blocks;
+// `thread` of kThreads looks at its share of them, sixteen loads at a time.
+template <int kThreads, int kTileCols>
+__device__ __forceinline__ bool scan_share(const Fp8GemmParams& p, int thread, int col0, int kb0, int n) {
+  static_assert(kThreads % kTileCols == 0 || kTileCols % kThreads == 0, "whole blocks at a time");
+  constexpr int kStep = kThreads > kTileCols ? kThreads / kTileCols : 1;     // blocks side by side
+  constexpr int kPer = kTileCols > kThreads ? kTileCols / kThreads : 1;      // columns of a thread
+  constexpr int kAtOnce = 16 / kPer;
+  const int col = col0 + thread % kTileCols;
+  bool ok = true;
+#pragma unroll 1
+  for (int kb = thread / kTileCols; kb < n; kb += kAtOnce * kStep) {
+    float x[kPer][kAtOnce];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) {
+      const float* src = p.sc + (int64_t)((col + c * kThreads) >> p.sc_shift) * p.sc_row + (int64_t)kb0 * p.sc_k;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        x[c][u] = col + c * kThreads < p.cols && kb + u * kStep < n ? ld_global(src + (kb + u * kStep) * p.sc_k) : 1.0f;
+    }
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) ok = ok && plain_column(x[c][u]);
+  }
+  return ok;
+}
+// By the kThreads threads of the epilogue together, before anything that they
+// may give up waiting for.
+constexpr int kScanBarrier = 1;
+template <int kThreads, int kTileCols>
+__device__ __forceinline__ bool scan_together(const Fp8GemmParams& p, int thread, int col0, int kb0, int n) {
+  const bool ok = scan_share<kThreads, kTileCols>(p, thread, col0, kb0, n);
+  __syncwarp();
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "barrier.cta.red.and.pred b, %2, %3, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "n"(kScanBarrier), "n"(kThreads)
+      : "memory");
+  return all != 0;
+}
+// By a warp, for itself.
+template <int kTileCols>
+__device__ __forceinline__ bool scan_alone(const Fp8GemmParams& p, int lane, int col0, int kb0, int n) {
+  const bool ok = scan_share<32, kTileCols>(p, lane, col0, kb0, n);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// A lane's columns of 128 (lane, lane + 32, ..) where each has its own scale, in
+// the block `at` points to: few registers, for warps that have few.
+struct ColumnLines {
+  const float* at;
+  int count;                 // of the lane's columns inside the matrix
+  __device__ __forceinline__ void start(const Fp8GemmParams& p, int col0, int lane) {
+    count = (p.cols - 1 - col0 - lane + 32) / 32;        // (<= 0: none)
+    at = p.sc + (int64_t)(col0 + lane) * p.sc_row;
+  }
+  __device__ __forceinline__ const float* column(const Fp8GemmParams& p, int i) const { return at + (int64_t)(32 * i) * p.sc_row; }
+  __device__ __forceinline__ void next(const Fp8GemmParams& p) { at += p.sc_k; }
+};
+// Looks at such columns a block at each call (at its loads in the next one).
+struct ColumnScan {
+  ColumnLines lines;
+  float x[4];
+  bool ok;
+  __device__ __forceinline__ void start(const Fp8GemmParams& p, int col0, int lane) {
+    ok = true;
+    lines.start(p, col0, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = 1.0f;
+  }
+  __device__ __forceinline__ void look() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ok = ok && plain_column(x[i]);
+  }
+  __device__ __forceinline__ void block(const Fp8GemmParams& p) {
+    look();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < lines.count) x[i] = ld_global(lines.column(p, i));
+    lines.next(p);
+  }
+  __device__ __forceinline__ bool result() {
+    look();
+    return __all_sync(0xffffffffu, ok) != 0;
+  }
+};
+
+// What a warp beside the epilogue finds for the tiles after a CTA's first is
+// left in notes, a ring of kNotes.
+constexpr uint32_t kNotes = 4;
+struct Notes {
+  uint32_t* word;
+  uint64_t* full;        // one arrival: the note is there
+  uint64_t* empty;       // kReaders arrivals: it has been read
+  static constexpr int kBytes = kNotes * (4 + 2 * 8);
+  // note number i (from 0), written by one warp; false when a wait gave up
+  __device__ __forceinline__ bool leave(uint32_t i, bool plain, int lane, const WaitCtl& ctl) const {
+    if (!warp_wait(&empty[i % kNotes], ((i / kNotes) & 1u) ^ 1u, ctl)) return false;
+    if (lane == 0) {
+      word[i % kNotes] = plain;
+      mbar_arrive(&full[i % kNotes]);
+    }
+    __syncwarp();
+    return true;
+  }
+  __device__ __forceinline__ bool read(uint32_t i, int lane, const WaitCtl& ctl, bool* plain) const {
+    if (!warp_wait(&full[i % kNotes], (i / kNotes) & 1u, ctl)) return false;
+    *plain = ld_shared_u32(smem_addr(word + i % kNotes)) != 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[i % kNotes]);
+    return true;
+  }
+};
 
 // The scales of one epilogue warp, its 32 rows and `kCols` columns, fetched
 // kDepth - 1 blocks of k ahead into a ring in shared memory that only this
@@ -147,69 +307,30 @@ struct ScaleRing {
   }
 };
 
-// How a block's two scales meet its sum P, |P| in [2^-32, 2^39) or 0: scales may
-// be any fp32 values, and no step but the last may leave fp32's normal range.
-//   one scale for all columns   P * (row * column), where that product of the
-//                               scales is in the normal range;
-//   a scale for each column     (P * row) * column, where the row's scale is in
-//                               [2^-94, 2^89), so that P * row is in range.
-// Elsewhere the row's scale is taken in two parts, first * last, last a power
-// of two: ((P * first) * column) * last.  For tiny rows first is in
-// [2^-94, 2^-39): P * first * column cannot overflow, and where it is below the
-// normal range the result is below 2^-181.  For huge rows first is in
-// [2^69, 2^89): the reverse.
-struct BlockScale {
-  f32x2 row;           // of the plain form: the row's scale, or with one scale for all columns their product
-  bool plain;          // for all lanes of the warp
-};
-template <bool kColVec>
-__device__ __forceinline__ BlockScale block_scale(float row, float col) {
-  const float s = kColVec ? row : row * col;
-  const uint32_t e = (__float_as_uint(s) >> 23) & 255u;
-  BlockScale r;
-  r.row = pack2(s, s);
-  r.plain = __all_sync(0xffffffffu, kColVec ? e - (127u - 94u) < 94u + 89u : e - 1u < 254u) != 0;
-  return r;
-}
-__device__ __forceinline__ void split_scale(float row, float& first, float& last) {
-  const int e = (int)((__float_as_uint(row) >> 23) & 255u) - 127;
-  int shift = 0;                                 // (also of infinities and NaN, e = 128)
-  if (e < -94) shift = -55;
-  else if (e >= 108 && e < 128) shift = 39;
-  else if (e >= 89 && e < 128) shift = 20;
-  first = row * __uint_as_float((uint32_t)(127 - shift) << 23);
-  last = __uint_as_float((uint32_t)(127 + shift) << 23);
-}
-
 // acc += row scale * column scale * v on kN columns from column c0 of the
-// warp's slot (col: the scale of all columns).
-template <int kN, bool kColVec>
-__device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t slot, int c0, const BlockScale& s, float row,
-                                          float col) {
-  if (s.plain) {
+// warp's slot (col: the scale of all columns).  kPlain: the caller branches
+// once a block or a tile, and this code stays in one piece with the reads of
+// TMEM around it.
+template <int kN, bool kColVec, bool kPlain>
+__device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t slot, int c0, float row, float col) {
+  float f, l;
+  if constexpr (kPlain) f = l = kColVec ? row : row * col;
+  else split_scale(row, f, l);
+  const f32x2 first = pack2(f, f), last = pack2(l, l), cols = pack2(col, col);
 #pragma unroll
-    for (int j = 0; j < kN; j += 4) {
-      const f32x2 v0 = pack2(v[j], v[j + 1]), v1 = pack2(v[j + 2], v[j + 3]);
-      if constexpr (kColVec) {
-        f32x2 s0, s1;
-        ld_shared_pairs(slot + 128 + (c0 + j) * 4, s0, s1);
-        fma2(acc[j / 2], mul2(v0, s.row), s0);
-        fma2(acc[j / 2 + 1], mul2(v1, s.row), s1);
-      } else {
-        fma2(acc[j / 2], v0, s.row);
-        fma2(acc[j / 2 + 1], v1, s.row);
-      }
-    }
-  } else {
-    float f, l;
-    split_scale(row, f, l);
-    const f32x2 first = pack2(f, f), last = pack2(l, l);
-#pragma unroll
-    for (int j = 0; j < kN; j += 4) {
-      f32x2 s0 = pack2(col, col), s1 = s0;
-      if constexpr (kColVec) ld_shared_pairs(slot + 128 + (c0 + j) * 4, s0, s1);
-      fma2(acc[j / 2], mul2(mul2(pack2(v[j], v[j + 1]), first), s0), last);
-      fma2(acc[j / 2 + 1], mul2(mul2(pack2(v[j + 2], v[j + 3]), first), s1), last);
+  for (int j = 0; j < kN; j += 4) {
+    const f32x2 v0 = pack2(v[j], v[j + 1]), v1 = pack2(v[j + 2], v[j + 3]);
+    f32x2 s0 = cols, s1 = cols;
+    if constexpr (kColVec) ld_shared_pairs(slot + 128 + (c0 + j) * 4, s0, s1);
+    if constexpr (!kPlain) {
+      fma2(acc[j / 2], mul2(mul2(v0, first), s0), last);
+      fma2(acc[j / 2 + 1], mul2(mul2(v1, first), s1), last);
+    } else if constexpr (kColVec) {
+      fma2(acc[j / 2], mul2(v0, s0), last);
+      fma2(acc[j / 2 + 1], mul2(v1, s1), last);
+    } else {
+      fma2(acc[j / 2], v0, last);
+      fma2(acc[j / 2 + 1], v1, last);
     }
   }
 }
@@ -218,7 +339,7 @@ __device__ __forceinline__ void scale_add(f32x2* acc, const float* v, uint32_t s
 // columns of this warp's 32 lanes) added to the running sums under the row's
 // scale and the column scales in `slot`, two reads of 32 columns on their
 // way.  `release` runs when all columns are in registers.
-template <int kCols, class Release>
+template <int kCols, bool kPlain, class Release>
 __device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, uint32_t slot, float row,
                                           Release release) {
   constexpr int kChunk = kCols >= 32 ? 32 : 16;
@@ -230,11 +351,10 @@ __device__ __forceinline__ void add_block(f32x2 (&acc)[kCols / 2], uint32_t ta, 
     if constexpr (kChunk == 32) tmem_ld_32cols(ta + c * kChunk, v[c]);
     else tmem_ld_16cols(ta + c * kChunk, v[c]);
   }
-  const BlockScale s = block_scale<true>(row, 1.0f);
   tmem_ld_wait();
   release();
 #pragma unroll
-  for (int c = 0; c < kN; ++c) scale_add<kChunk, true>(acc + c * kChunk / 2, v[c], slot, c * kChunk, s, row, 1.0f);
+  for (int c = 0; c < kN; ++c) scale_add<kChunk, true, kPlain>(acc + c * kChunk / 2, v[c], slot, c * kChunk, row, 1.0f);
 }
 
 // alpha x + beta C for 32 rows (one a lane) and 32 columns (x[j]: columns 2j

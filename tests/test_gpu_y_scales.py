@@ -114,3 +114,36 @@ def test_zeros_under_the_largest_scales_and_infinities(form):
     bad = np.zeros((m, n), bool)
     bad[[2, 5]] = True
     assert np.array_equal(~np.isfinite(got), bad)
+
+
+@pytest.mark.parametrize("pair", [-1, 1])
+@pytest.mark.parametrize("k", [100, 900])
+def test_a_few_columns_far_from_the_others(pair, k):
+    """More tiles than SMs, several to each CTA: one column in one block of k has
+    a scale that leaves the range, in the first, a middle and the last tiles;
+    the tiles before and after it are right too, and those without one have the
+    bits that they have when no column is far."""
+    import torch
+    m, n = 2433, 2561
+    rng = np.random.default_rng(7)
+    a, b = codes(m, k, rng, "e4m3", -9, 8), codes(n, k, rng, "e4m3", -9, 8)
+    sa = (2.0 ** (-60 + rng.uniform(-3, 3, (m, blocks(k))))).astype(np.float32)
+    sb = (2.0 ** (60 + rng.uniform(-3, 3, (n, blocks(k))))).astype(np.float32)
+    far = sb.copy()
+    last = blocks(k) - 1
+    for c, e in ((7, 115), (700, -120), (1500, 118), (1501, 0), (2560, 110)):
+        far[c, min(c % 3, last)] = 2.0 ** e * 1.3
+    A, SA, B = a.cuda(), torch.from_numpy(sa).cuda(), b.cuda()
+    plain, got = (mpg.gemm_fp8(A, SA, B, torch.from_numpy(s).cuda(), out_dtype=torch.float32, opts=mpg.options(cta_pair=pair))
+                  for s in (sb, far))
+    assert mpg.device_status() == mpg.OK
+    wa, wb = widen(a.double().numpy(), sa.astype(np.float64), 1), widen(b.double().numpy(), far.astype(np.float64), 1)
+    want, den = wa @ wb.T, np.abs(wa) @ np.abs(wb).T
+    bound = sum_bound(k) * den + np.abs(want) * 2.0 ** -24 + 4 * blocks(k) * 2.0 ** -149
+    err = np.abs(got.cpu().double().numpy() - want)
+    assert np.max(np.abs(want)) < 3e38 and np.all(err <= bound), float(np.max(err / bound))
+    tile = 256
+    touched = {c // tile for c in (7, 700, 1500, 2560)}
+    for t in range(-(-n // tile)):
+        if t not in touched:
+            assert torch.equal(got[:, t * tile:(t + 1) * tile], plain[:, t * tile:(t + 1) * tile])
