@@ -6,7 +6,10 @@
 // about 1.2, so fp16's 11 bits can be used without fear of its range: X is
 // stored times a power of two near the root of its longer side (its entries
 // then have a root mean square near 1 when X is orthogonal), S and b S + c S S
-// as they are.  bf16 storage would lose three bits at every rounding; rounding
+// as they are.  Where |G| is far below eps the iterates start that small and
+// grow by |a| a step: a bound on their norm, |G| / (|G| + eps) taken through the
+// polynomial's absolute values, gives each matrix and step a power of two of
+// its own beside that one, as long as the bound is below 1.  bf16 storage would lose three bits at every rounding; rounding
 // errors of X grow by up to a = 3.4 a step in the directions of small singular
 // values.  With five steps on a matrix of noise and a few strong directions
 // the result is off by 1.3e-3 of its norm with fp16 storage and by 1.1e-2 with
@@ -201,40 +204,86 @@ __global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_
   }
 }
 
+// What the sum of a matrix's squares says.  Norm and eps are held as a fraction
+// in [1, 2) and an exponent, which has no limits here.
+struct OrthoNorm {
+  int e;             // the matrix is stored times 2^e
+  float first;       // 2^-e / (norm + eps)
+  float u;           // norm / (norm + eps) = u * 2^ue
+  int ue;
+};
+__device__ __forceinline__ float split_exponent(float v, int* e) {        // v > 0
+  const float f = frexpf(v, e);
+  --*e;
+  return 2.0f * f;
+}
+__device__ __forceinline__ OrthoNorm ortho_norm(const OrthoScaleParams& p, double s) {
+  OrthoNorm n{0, 0.0f, 1.0f, 0};
+  const uint32_t hi = (uint32_t)__double2hiint(s);
+  const int exponent = (int)(hi >> 20) - 1023;                   // s = fraction * 2^exponent
+  if (hi == 0u || exponent == 1024) {
+    // zero, infinite or NaN
+    n.first = 1.0f / (hi == 0u ? p.eps : __uint_as_float(0x7F800000u | (hi & 0xFFFFFu)));
+    return n;
+  }
+  const float fraction = __uint_as_float(0x3F800000u | ((hi & 0xFFFFFu) << 3) | ((uint32_t)__double2loint(s) >> 29));
+  // norm = root * 2^half, root in [1, 2)
+  const int half = exponent >> 1;
+  const float root = sqrtf((exponent & 1) ? 2.0f * fraction : fraction);
+  // norm + eps = sum * 2^top, sum in [1, 4)
+  int top = half;
+  float sum = root;
+  if (p.eps > 0.0f) {
+    int ee;
+    const float ef = split_exponent(p.eps, &ee);
+    top = max(half, ee);
+    sum = scalbnf(root, half - top) + scalbnf(ef, ee - top);
+  }
+  // one factor of fp32 carries the tiniest norms of fp32 inputs only part of the way
+  n.e = min(max(p.target_exp - half, -126), 127);
+  n.first = scalbnf(1.0f / sum, -n.e - top);
+  n.u = split_exponent(root / sum, &n.ue);
+  n.ue += half - top;
+  return n;
+}
+
+// The iterates' factors: later ones are stored times 2^(store_exp + extra), where
+// extra brings a bound on their singular values (the polynomial of its
+// coefficients' sizes, applied to u * 2^ue) to [1/2, 1) as long as it is below.
+__device__ __forceinline__ void ortho_factors(const OrthoScaleParams& p, int b, OrthoNorm n) {
+  p.factor[b] = n.first;
+  for (int i = 1; i < p.steps; ++i) {
+    if (n.ue < 0) {
+      const float x = scalbnf(n.u, max(n.ue, -60)), x2 = x * x;
+      const float v = n.u * (p.coeff_size[0] + x2 * (p.coeff_size[1] + x2 * p.coeff_size[2]));
+      int up = 0;
+      if (v > 3e38f) n.ue = 0;
+      else if (v > 0.0f) n.u = split_exponent(v, &up);
+      n.ue += up;
+    }
+    const int extra = min(max(-n.ue - 1, 0), 120 - p.store_exp);
+    p.factor[(int64_t)i * p.batch + b] = scalbnf(1.0f, -p.store_exp - extra);
+  }
+}
+
 // x = fp16(g * 2^e) with the power of two that brings the norm to [2^t, 2^(t+1))
-// (t: target_exp), and factor = 2^-e / (norm + eps).  Every block works them
-// out from the partial sums: a few additions in 64 bits, the rest on the
-// sum's exponent and fraction.
+// (t: target_exp).  Every block works it out from the partial sums, by a few
+// additions in 64 bits and on the sum's exponent and fraction.
 template <class XT>
 __global__ void __launch_bounds__(kScaleThreads) ortho_scale_kernel(const __grid_constant__ OrthoScaleParams p) {
   __shared__ float scale_sh;
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.y;
+  OrthoNorm norm;                                                // (thread 0)
   if (threadIdx.x < 32) {
     double s = 0.0;
     for (int i = threadIdx.x; i < p.blocks; i += 32) s += p.partial[(int64_t)b * kOrthoNormBlocks + i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (threadIdx.x == 0) {
-      const uint32_t hi = (uint32_t)__double2hiint(s);
-      const int exponent = (int)(hi >> 20) - 1023;               // s = fraction * 2^exponent
-      float scale = 1.0f, factor;
-      if (hi == 0u || exponent == 1024) {
-        // zero, infinite or NaN
-        factor = 1.0f / (hi == 0u ? p.eps : __uint_as_float(0x7F800000u | (hi & 0xFFFFFu)));
-      } else {
-        const float fraction = __uint_as_float(0x3F800000u | ((hi & 0xFFFFFu) << 3) | ((uint32_t)__double2loint(s) >> 29));
-        // norm = root * 2^half, root in [1, 2)
-        const int half = exponent >> 1;
-        const float root = sqrtf((exponent & 1) ? 2.0f * fraction : fraction);
-        // one factor of fp32 carries the tiniest norms of fp32 inputs only part of the way
-        const int e = min(max(p.target_exp - half, -126), 127);
-        scale = scalbnf(1.0f, e);
-        factor = 1.0f / (scalbnf(root, half + e) + scalbnf(p.eps, e));
-      }
-      scale_sh = scale;
-      if (blockIdx.x == 0) p.factor[b] = factor;
+      norm = ortho_norm(p, s);
+      scale_sh = scalbnf(1.0f, norm.e);
     }
   }
   __syncthreads();
@@ -254,6 +303,7 @@ __global__ void __launch_bounds__(kScaleThreads) ortho_scale_kernel(const __grid
                      pack_f16x2(v[u][4] * scale, v[u][5] * scale), pack_f16x2(v[u][6] * scale, v[u][7] * scale));
     }
   }
+  if (threadIdx.x == 0 && blockIdx.x == 0) ortho_factors(p, b, norm);
 }
 
 // ---------------------------------------------------------------------------
@@ -306,6 +356,19 @@ __device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
+}
+
+// ca and cz for matrix b.
+struct OrthoScales {
+  float ca, cz;
+};
+__device__ __forceinline__ OrthoScales ortho_scales(const OrthoGemmParams& p, int b) {
+  float f = 1.0f, f2 = 1.0f;
+  if (p.factor) f = ld_global(p.factor + b);
+  // (the next iterate's is a power of two: its inverse by the exponent)
+  if (p.next) f2 = __uint_as_float(0x7F000000u - __float_as_uint(ld_global(p.next + b)));
+  if (p.square) f2 = f;
+  return OrthoScales{p.ca * f * f2, p.cz * f * f2};
 }
 
 struct OrthoTile {
@@ -500,9 +563,6 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
     uint32_t g = 0;
     for (int t = worker; t < p.num_tiles; t += workers, ++g) {
       const OrthoTile tc = ortho_tile(p, t);
-      const float f = p.factor ? ld_global(p.factor + tc.b) : 1.0f;
-      const float ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
-      const float cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
       const float co = p.co;
       uint8_t* d = static_cast<uint8_t*>(p.d) + (int64_t)tc.b * p.stride_d * es;
       const uint32_t ab = g % T::kAccBufs;
@@ -519,6 +579,8 @@ __global__ void __launch_bounds__(T::kThreads, 1) ortho_gemm_kernel(const __grid
           z[i] = zrow && c0 + 8 * i < p.n ? ld_global(reinterpret_cast<const uint4*>(zrow + c0) + i) : make_uint4(0, 0, 0, 0);
       };
       fetch_z(cc0);
+      const OrthoScales sc = ortho_scales(p, tc.b);
+      const float ca = sc.ca, cz = sc.cz;
       if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
       tc_fence_after_sync();
 #pragma unroll 1
@@ -877,6 +939,8 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
   out.mir = p.symmetric && tc.mb != tc.nb ? reinterpret_cast<uint16_t*>(smem + T::kMirrorOffset) : nullptr;
   const uint32_t zs = op_smem + T::kStages * T::kStage;
 
+  const OrthoScales sc = ortho_scales(p, tc.b);
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -963,9 +1027,8 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
   cluster_sync_all();
   const bool live = *abort_flag == 0 && rows_here > 0;
   if (live && warp >= 2) {
-    const float f = p.factor ? ld_global(p.factor + tc.b) : 1.0f;
-    out.ca = p.ca * (p.ca_power > 0 ? f : 1.0f) * (p.ca_power > 1 ? f : 1.0f);
-    out.cz = p.cz * (p.cz_power > 0 ? f : 1.0f);
+    out.ca = sc.ca;
+    out.cz = sc.cz;
     switch (p.splits) {
       case 2: divided_rows<2>(p, out, op_smem, zs, ra, rows_here, cols_here, warp - 2, lane); break;
       default: divided_rows<4>(p, out, op_smem, zs, ra, rows_here, cols_here, warp - 2, lane); break;

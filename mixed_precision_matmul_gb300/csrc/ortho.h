@@ -11,6 +11,7 @@ namespace mpg {
 
 // Blocks that sum the squares of one matrix, at most.
 constexpr int kOrthoNormBlocks = 384;
+constexpr int kOrthoMaxSteps = 100;
 
 struct OrthoScaleParams {
   const void* g;
@@ -22,8 +23,11 @@ struct OrthoScaleParams {
   int32_t blocks;             // partial sums of one matrix
   uint16_t* x;                // fp16 [batch][rows][ldx], ldx % 8 == 0
   int64_t ldx;
-  float* factor;              // [batch]: normalised matrix = factor * x
+  float* factor;              // [step][batch]: the iterate is factor * what is stored of it; powers of two but for the first
+  int32_t steps;
+  float coeff_size[3];        // |a|, |b|, |c|
   int32_t target_exp;         // x is scaled by a power of two to a norm in [2^t, 2^(t+1))
+  int32_t store_exp;          // iterates with singular values near 1 are stored times 2^s
   float eps;
 };
 cudaError_t launch_ortho_scale(const OrthoScaleParams& p, int g_dtype, cudaStream_t stream);
@@ -43,8 +47,9 @@ struct OrthoGemmParams {
   int32_t vec;                // 4-element vectors of D are aligned
   int32_t vec16;              // 16-byte chunks of a 16-bit D are aligned
   float ca, cz, co;
-  const float* factor;        // per matrix, or null
-  int32_t ca_power, cz_power; // ca and cz are multiplied by factor to these powers (0, 1, 2)
+  const float* factor;        // of each matrix, or null
+  const float* next;          // of each matrix's next iterate, or null
+  int32_t square;             // ca is multiplied by factor^2; else ca and cz by factor / next
   int32_t splits, kb_per_split;   // divided form: ranges of k, each on a CTA of one cluster
   uint32_t* status;
   uint64_t wait_limit_ns;

@@ -12,7 +12,6 @@ namespace {
 
 constexpr int64_t kMaxExtent = 0x7FFFFFFF;
 constexpr int64_t kMaxBatch = 65535;
-constexpr int kMaxSteps = 100;
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int64_t line8(int64_t n) { return (n + 7) / 8 * 8; }
@@ -33,7 +32,7 @@ Layout layout(int64_t m, int64_t n, int64_t batch) {
     return r;
   };
   l.partial = take((size_t)batch * kOrthoNormBlocks * sizeof(double));
-  l.factor = take((size_t)batch * sizeof(float));
+  l.factor = take((size_t)batch * kOrthoMaxSteps * sizeof(float));
   for (size_t& x : l.x) x = take((size_t)batch * (size_t)m * (size_t)l.ldx * 2);
   l.s = take((size_t)batch * (size_t)l.side * (size_t)l.lds * 2);
   l.b = take((size_t)batch * (size_t)l.side * (size_t)l.lds * 2);
@@ -133,7 +132,7 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
   if (batch > kMaxBatch) return fail(MPG_ERR_INVALID_ARG, "more than 65535 matrices");
   if ((int)g_dtype < 0 || (int)g_dtype > 2 || (int)o_dtype < 0 || (int)o_dtype > 2)
     return fail(MPG_ERR_INVALID_ARG, "unknown dtype");
-  if (steps < 1 || steps > kMaxSteps) return fail(MPG_ERR_INVALID_ARG, "steps %d outside [1, 100]", steps);
+  if (steps < 1 || steps > kOrthoMaxSteps) return fail(MPG_ERR_INVALID_ARG, "steps %d outside [1, 100]", steps);
   if (!coeffs) return fail(MPG_ERR_INVALID_ARG, "NULL coefficients");
   if (!std::isfinite(coeffs[0]) || !std::isfinite(coeffs[1]) || !std::isfinite(coeffs[2]) || !std::isfinite(alpha) ||
       !std::isfinite(beta))
@@ -175,6 +174,9 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
   sp.x = reinterpret_cast<uint16_t*>(ws + l.x[0]);
   sp.ldx = l.ldx;
   sp.factor = factor;
+  sp.steps = steps;
+  for (int i = 0; i < 3; ++i) sp.coeff_size[i] = std::fabs(coeffs[i]);
+  sp.store_exp = (int)std::lround(0.5 * std::log2((double)std::max(m, n)));
   // a norm near sqrt(m n) gives entries near 1; below 2^15, so that even a
   // single entry that holds the whole norm stays within fp16
   sp.target_exp = std::min((int)std::floor(0.5 * std::log2((double)m * (double)n)), 14);
@@ -186,13 +188,12 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
   cudaError_t e = launch_ortho_scale(sp, (int)g_dtype, st);
   if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "scaling launch: %s", cudaGetErrorString(e));
 
-  // X is stored times sx after the first step
-  const float sx = std::ldexp(1.0f, (int)std::lround(0.5 * std::log2((double)std::max(m, n))));
   const bool wide = m <= n;
   const int64_t side = l.side, length = std::max(m, n);
   const Matrix S{ws + l.s, l.lds, side}, B{ws + l.b, l.lds, side};
   for (int i = 0; i < steps; ++i) {
-    const bool first = i == 0, last = i == steps - 1;
+    const bool last = i == steps - 1;
+    const float* here = factor + (int64_t)i * batch;
     const Matrix X{ws + l.x[i & 1], l.ldx, m}, Y{ws + l.x[(i & 1) ^ 1], l.ldx, m};
     OrthoGemmParams p;
     // S = X X^T (tall X: X^T X)
@@ -209,9 +210,9 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
     p.stride_d = side * S.ld;
     p.d_dtype = MPG_F16;
     p.vec = p.vec16 = 1;
-    p.ca = first ? 1.0f : 1.0f / (sx * sx);
-    p.factor = first ? factor : nullptr;
-    p.ca_power = first ? 2 : 0;
+    p.ca = 1.0f;
+    p.factor = here;
+    p.square = 1;
     if ((s = launch_gemm(dev, p, st)) != MPG_OK) return s;
     // B = b S + c S S
     std::memset(&p, 0, sizeof(p));
@@ -248,11 +249,10 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
     p.z = static_cast<const uint16_t*>(X.ptr);
     p.ldz = X.ld;
     p.stride_z = m * X.ld;
-    const float unit = (first ? 1.0f : 1.0f / sx) * (last ? alpha : sx);
-    p.ca = unit;
-    p.cz = coeffs[0] * unit;
-    p.factor = first ? factor : nullptr;
-    p.ca_power = p.cz_power = first ? 1 : 0;
+    p.ca = last ? alpha : 1.0f;
+    p.cz = coeffs[0] * p.ca;
+    p.factor = here;
+    p.next = last ? nullptr : here + batch;
     if (last) {
       p.d = O;
       p.ldd = ldo;
