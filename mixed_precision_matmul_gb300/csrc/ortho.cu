@@ -222,8 +222,8 @@ __device__ __forceinline__ OrthoNorm ortho_norm(const OrthoScaleParams& p, doubl
   const uint32_t hi = (uint32_t)__double2hiint(s);
   const int exponent = (int)(hi >> 20) - 1023;                   // s = fraction * 2^exponent
   if (hi == 0u || exponent == 1024) {
-    // zero, infinite or NaN
-    n.first = 1.0f / (hi == 0u ? p.eps : __uint_as_float(0x7F800000u | (hi & 0xFFFFFu)));
+    // zero (times any factor, whose square has to be finite too), 0 / 0, infinite or NaN
+    n.first = hi == 0u && p.eps > 0.0f ? 0.0f : __uint_as_float(0x7FC00000u);
     return n;
   }
   const float fraction = __uint_as_float(0x3F800000u | ((hi & 0xFFFFFu) << 3) | ((uint32_t)__double2loint(s) >> 29));

@@ -103,3 +103,18 @@ def test_small_updates_folded_into_a_weight():
     sim = (rounded_at_any_scale(g, 5, 1e-7) * 4096.0 - part).norm() / part.norm()
     # (the weights' rounding: half a step of each, 2^-24)
     assert (o.cpu().double() - want).norm() <= (2 * sim + 1e-5) * part.norm() + 2.0 ** -23 * w.double().norm()
+
+
+@pytest.mark.parametrize("eps", [1e-7, 1e-20, 1e-30, 1e-38, 1e-44])
+@pytest.mark.parametrize("shape", [(3, 40, 50), (2, 300, 200), (2, 1, 1)])
+def test_zero_matrices_stay_zero_with_any_eps(eps, shape):
+    """0 / (0 + eps) is 0, and a weight that takes the update keeps its own."""
+    import torch
+    g = torch.randn(shape, generator=torch.Generator().manual_seed(1)).cuda()
+    g[0] = 0
+    o = mpg.orthogonalize(g, eps=eps, out_dtype=tdtype("fp32"))
+    assert (o[0] == 0).all() and torch.isfinite(o).all() and (o[1] != 0).any()
+    w = torch.randn(shape, generator=torch.Generator().manual_seed(2)).cuda()
+    w0 = w.clone()
+    mpg.orthogonalize(g, O=w, eps=eps, alpha=-0.1, beta=0.5)
+    assert torch.equal(w[0], 0.5 * w0[0]) and torch.isfinite(w).all()
