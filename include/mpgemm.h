@@ -437,7 +437,7 @@ typedef struct {
  * is x / scale rounded once, to nearest even (the division is exact).
  * Infinities and NaN do not set the scale and become NaN.  Blocks cut by the
  * matrix's edge hold what is inside.  scale_rows 128 gives Q and QT the same
- * scales (transposed). */
+ * scales (transposed).  rows, cols <= 2^31 - 256. */
 mpg_status mpg_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t ldx, mpg_dtype x_dtype,
                             mpg_fp8_format format, int32_t scale_rows, void* Q, int64_t ldq, float* S,
                             int64_t s_row_stride, int64_t s_k_stride, void* QT, int64_t ldqt, float* ST,
@@ -461,6 +461,7 @@ mpg_status mpg_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t l
  * Data pointers that are not 16-byte aligned or whose ld is no multiple of 16
  * are copied to aligned lines in the workspace first
  * (mpg_gemm_fp8_workspace_size bytes, else 0; MPG_ERR_WORKSPACE without it).
+ * m, n, k <= 2^31 - 256.
  * Results do not depend on timing. */
 size_t mpg_gemm_fp8_workspace_size(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* A,
                                    const mpg_fp8_operand* B);
@@ -480,7 +481,7 @@ mpg_status mpg_gemm_fp8(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* 
  *   G        fp32, fp16 or bf16, row-major, ldg >= n; strideG 0 = m*ldg.
  *   O        fp32, fp16 or bf16, ldo >= n; strideO 0 = m*ldo; the matrices of O
  *            must not overlap; beta == 0: O is not read.  O may be G.
- *   steps    1 .. 100.  eps >= 0.  batch <= 65535.
+ *   steps    1 .. 100.  eps >= 0.  batch <= 65535.  m, n <= 2^31 - 256.
  *   workspace  mpg_orthogonalize_workspace_size() bytes, 16-byte aligned.
  * Products run in fp16 with fp32 accumulation, X scaled by a power of two; the
  * norm is summed in 64 bits.  Against 64 bits the result is off by about 1e-3

@@ -10,7 +10,8 @@ using namespace mpg;
 
 namespace {
 
-constexpr int64_t kMaxExtent = 0x7FFFFFFF;
+// the last tile's end, and a block beyond it, still fit 32 bits
+constexpr int64_t kMaxExtent = 0x7FFFFFFF - 255;
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int64_t blocks_of(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
@@ -221,7 +222,7 @@ mpg_status mpg_fp8_quantize(int64_t rows, int64_t cols, const void* X, int64_t l
                             int64_t st_row_stride, int64_t st_k_stride, void* stream) {
   t_err.clear();
   if (rows < 0 || cols < 0) return fail(MPG_ERR_INVALID_ARG, "negative size");
-  if (rows > kMaxExtent || cols > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "size beyond 2^31-1");
+  if (rows > kMaxExtent || cols > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "size beyond 2^31-256");
   if ((int)x_dtype < 0 || (int)x_dtype > 2) return fail(MPG_ERR_INVALID_ARG, "unknown dtype %d", (int)x_dtype);
   if ((int)format < 0 || (int)format > 1) return fail(MPG_ERR_UNSUPPORTED, "unknown 8-bit format %d", (int)format);
   if (scale_rows != 1 && scale_rows != kFp8Block)
@@ -276,7 +277,7 @@ mpg_status mpg_gemm_fp8(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* 
                         const mpg_options* opt) {
   t_err.clear();
   if (m < 0 || n < 0 || k < 0) return fail(MPG_ERR_INVALID_ARG, "negative size");
-  if (m > kMaxExtent || n > kMaxExtent || k > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "size beyond 2^31-1");
+  if (m > kMaxExtent || n > kMaxExtent || k > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "size beyond 2^31-256");
   if (!A || !B) return fail(MPG_ERR_INVALID_ARG, "NULL operand description");
   mpg_options o;
   resolve_options(opt, &o);

@@ -10,7 +10,8 @@ using namespace mpg;
 
 namespace {
 
-constexpr int64_t kMaxExtent = 0x7FFFFFFF;
+// the last tile's end, and a block beyond it, still fit 32 bits
+constexpr int64_t kMaxExtent = 0x7FFFFFFF - 255;
 constexpr int64_t kMaxBatch = 65535;
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -128,7 +129,7 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
                              size_t workspace_bytes, void* stream) {
   t_err.clear();
   if (m < 0 || n < 0 || batch < 0) return fail(MPG_ERR_INVALID_ARG, "negative size");
-  if (m > kMaxExtent || n > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "size beyond 2^31-1");
+  if (m > kMaxExtent || n > kMaxExtent) return fail(MPG_ERR_INVALID_ARG, "size beyond 2^31-256");
   if (batch > kMaxBatch) return fail(MPG_ERR_INVALID_ARG, "more than 65535 matrices");
   if ((int)g_dtype < 0 || (int)g_dtype > 2 || (int)o_dtype < 0 || (int)o_dtype > 2)
     return fail(MPG_ERR_INVALID_ARG, "unknown dtype");
