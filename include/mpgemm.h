@@ -480,7 +480,9 @@ mpg_status mpg_gemm_fp8(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* 
  * weight: O = W, alpha = -learning rate, beta = 1 - learning rate * decay.
  *   G        fp32, fp16 or bf16, row-major, ldg >= n; strideG 0 = m*ldg.
  *   O        fp32, fp16 or bf16, ldo >= n; strideO 0 = m*ldo; the matrices of O
- *            must not overlap; beta == 0: O is not read.  O may be G.
+ *            must not overlap: one after another (strideO >= (m-1)*ldo + n) or
+ *            side by side within the lines (strideO >= n, all within ldo);
+ *            beta == 0: O is not read.  O may be G.
  *   steps    1 .. 100.  eps >= 0.  batch <= 65535.  m, n <= 2^31 - 256.
  *   workspace  mpg_orthogonalize_workspace_size() bytes, 16-byte aligned.
  * Products run in fp16 with fp32 accumulation, X scaled by a power of two; the

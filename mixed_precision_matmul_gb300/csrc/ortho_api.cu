@@ -148,7 +148,9 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
     return fail(MPG_ERR_INVALID_ARG, "operand not aligned to its element");
   if (strideG == 0) strideG = m * ldg;
   if (strideO == 0) strideO = m * ldo;
-  if (batch > 1 && strideO < (m - 1) * ldo + n) return fail(MPG_ERR_INVALID_ARG, "the matrices of O overlap");
+  // one after another, or side by side within the lines
+  const bool apart = strideO >= (m - 1) * ldo + n || (strideO >= n && (batch - 1) * strideO + n <= ldo);
+  if (batch > 1 && !apart) return fail(MPG_ERR_INVALID_ARG, "the matrices of O overlap");
   const Layout l = layout(m, n, batch);
   if (!workspace || workspace_bytes < l.bytes || !aligned(workspace, 16))
     return fail(MPG_ERR_WORKSPACE, "%zu workspace bytes needed (16-byte aligned), got %zu", l.bytes,

@@ -41,3 +41,17 @@ def test_workspace_queries_end_where_the_operators_do():
     assert size(TOP, 5, 16, ctypes.byref(odd), ctypes.byref(even)) == TOP * 16
     assert size(TOP + 1, 5, 16, ctypes.byref(odd), ctypes.byref(even)) == 0
     assert mpg.orthogonalize_workspace_size(1, TOP) > 4 * TOP and mpg.orthogonalize_workspace_size(1, TOP + 1) == 0
+
+
+def orthogonalize(batch, m, n, ldo, stride):
+    return mpg.orthogonalize_raw(m, n, batch, 4096, n, 0, mpg.BF16, 4096, ldo, stride, mpg.BF16, workspace=0, check=False)
+
+
+def test_matrices_of_o_may_lie_beside_one_another():
+    """Batches along the columns of one wide matrix do not overlap (what is refused is the missing workspace)."""
+    assert orthogonalize(4, 8, 16, 64, 16) == mpg.ERR_WORKSPACE
+    assert orthogonalize(4, 8, 16, 70, 18) == mpg.ERR_WORKSPACE
+    assert orthogonalize(4, 8, 16, 16, 128) == mpg.ERR_WORKSPACE
+    for ldo, stride in ((64, 15), (63, 16), (66, 17), (16, 16), (16, 127)):
+        assert orthogonalize(4, 8, 16, ldo, stride) == mpg.ERR_INVALID_ARG
+        assert "overlap" in mpg.last_error()

@@ -118,3 +118,28 @@ def test_zero_matrices_stay_zero_with_any_eps(eps, shape):
     w0 = w.clone()
     mpg.orthogonalize(g, O=w, eps=eps, alpha=-0.1, beta=0.5)
     assert torch.equal(w[0], 0.5 * w0[0]) and torch.isfinite(w).all()
+
+
+@pytest.mark.parametrize("b,m,n", [(4, 70, 96), (3, 130, 65), (2, 300, 260)])
+def test_matrices_beside_one_another(b, m, n):
+    """The blocks of columns of one wide weight as a batch, in and out, without touching what lies between."""
+    import torch
+    g = momentum(b, m, n, 9, "bf16").cuda()
+    want = mpg.orthogonalize(g, out_dtype=tdtype("fp32"))
+    wide_g = torch.full((m, b, n + 3), 7.0, dtype=g.dtype, device="cuda")
+    wide_g[:, :, :n] = g.permute(1, 0, 2)
+    wide_o = torch.full((m, b, n + 3), 7.0, device="cuda")
+    o = wide_o[:, :, :n].permute(1, 0, 2)
+    mpg.orthogonalize(wide_g[:, :, :n].permute(1, 0, 2), O=o)
+    assert torch.equal(o, want)
+    assert (wide_o[:, :, n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("norm", [1e-36, 1e-39, 3e-42])
+@pytest.mark.parametrize("eps", [0.0, 1e-40])
+def test_norms_below_the_normal_range(norm, eps):
+    """fp32 gradients of subnormal size: every bit that they still have counts."""
+    import torch
+    eps = float(torch.tensor(eps))                             # (as the operator receives it)
+    g = of_norm(1, 40, 60, 4, "fp32", norm)
+    check_small(g, 5, eps)
