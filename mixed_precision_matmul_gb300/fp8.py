@@ -64,8 +64,9 @@ def _on_stream(stream, tensors, call):
     """Run ``call()`` with ``stream`` current, so that what it allocates belongs
     to that stream, and keep ``tensors`` alive for the work enqueued there."""
     torch = _types()[0]
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=tensors[0].device)
+    if not isinstance(stream, torch.cuda.Stream):      # a handle, or any object that has one
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch.cuda.ExternalStream(handle, device=tensors[0].device)
     with torch.cuda.stream(stream):
         for t in tensors:
             if t is not None:

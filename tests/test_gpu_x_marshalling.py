@@ -1,5 +1,6 @@
-"""GPU: the 8-bit torch forms give the same whether their calls are marshalled
-by the extension or in Python."""
+"""GPU: the torch forms of the 8-bit operators and the update: the same results
+whether their calls are marshalled by the extension or in Python, on any stream
+and from any thread."""
 import pytest
 
 import mixed_precision_matmul_gb300 as mpg
@@ -27,3 +28,63 @@ def test_python_form_is_the_extension_s(m, n, k, block, monkeypatch):
     monkeypatch.setattr(fp8, "_calls", lambda: None)
     for a, b in zip(one, run()):
         assert a.dtype == b.dtype and a.stride() == b.stride() and torch.equal(a.float(), b.float())
+
+
+def chain(x, w, stream):
+    import torch
+    q, s = mpg.fp8_quantize(x, stream=stream)
+    wq, ws = mpg.fp8_quantize(w, block="tile", stream=stream)
+    y = mpg.gemm_fp8(q, s, wq, ws, out_dtype=torch.float32, stream=stream)
+    return y, mpg.orthogonalize(y, out_dtype=torch.float32, stream=stream)
+
+
+@pytest.mark.parametrize("kind", ["torch stream", "handle", "an object with the handle", "the default stream's handle"])
+def test_streams_as_the_other_entry_points_take_them(kind):
+    import torch
+    mpg.build()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, w = (torch.randn(s, generator=g, device="cuda") for s in ((40, 256), (96, 256)))
+    want = chain(x, w, None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    class Holder:
+        cuda_stream = side.cuda_stream
+    stream = {"torch stream": side, "handle": side.cuda_stream, "an object with the handle": Holder(),
+              "the default stream's handle": 0}[kind]
+    got = chain(x, w, stream)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_calls_from_several_threads():
+    import threading
+
+    import torch
+    mpg.build()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    shapes = [(5, 300, 256), (70, 129, 640), (300, 260, 512), (33, 96, 1024)]
+    data = [tuple(torch.randn(t, generator=g, device="cuda") for t in ((m, k), (n, k))) for m, n, k in shapes]
+    want = [chain(x, w, None) for x, w in data]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            side = torch.cuda.Stream()
+            for r in range(12):
+                j = (i + r) % len(data)
+                got = chain(*data[j], side)
+                side.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[j])):
+                    wrong.append((i, r))
+        except Exception as e:                                  # noqa: BLE001 (reported below)
+            wrong.append((i, repr(e)))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert mpg.device_status() == mpg.OK
