@@ -64,6 +64,7 @@ def _on_stream(stream, tensors, call):
     """Run ``call()`` with ``stream`` current, so that what it allocates belongs
     to that stream, and keep ``tensors`` alive for the work enqueued there."""
     torch = _types()[0]
+    _device_index(*tensors)
     if not isinstance(stream, torch.cuda.Stream):      # a handle, or any object that has one
         handle = stream if isinstance(stream, int) else stream.cuda_stream
         stream = torch.cuda.ExternalStream(handle, device=tensors[0].device)

@@ -58,6 +58,18 @@ def test_streams_as_the_other_entry_points_take_them(kind):
         assert torch.equal(a, b)
 
 
+def test_tensors_on_the_host_are_refused_with_a_stream_too():
+    import torch
+    mpg.build()
+    side = torch.cuda.Stream()
+    x = torch.zeros((4, 256))
+    a, s = x.to(torch.float8_e4m3fn), torch.zeros((4, 2))
+    for call in (lambda: mpg.fp8_quantize(x, stream=side), lambda: mpg.gemm_fp8(a, s, a, s, stream=side),
+                 lambda: mpg.orthogonalize(x, stream=side), lambda: mpg.fp8_quantize(x, stream=side.cuda_stream)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
 def test_calls_from_several_threads():
     import threading
 
