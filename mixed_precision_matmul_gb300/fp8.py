@@ -86,6 +86,13 @@ def _device_index(*tensors) -> int:
     return index
 
 
+def _workspace(workspace):
+    """(address, bytes) of a given workspace, whose bytes have to be its own."""
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _on_device(index, call):
     """``call`` with device ``index`` current."""
     with _types()[0].cuda.device(index):
@@ -298,7 +305,7 @@ def gemm_fp8(A, a_scale, B, b_scale, C=None, alpha: float = 1.0, beta: float = 0
     if workspace is not None:
         if workspace.get_device() != index:
             raise ValueError("operands are on different devices")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _workspace(workspace)
     _m._check(_m.lib().mpg_gemm_fp8(m, n, k, a, b, C.data_ptr(), ldc, alpha, beta, ws, ws_bytes, _raw_stream()(index),
                                     opts))
     return C

@@ -6,7 +6,7 @@ import ctypes
 
 import mixed_precision_matmul_gb300 as _m
 
-from .fp8 import _device_index, _on_device, _on_stream, _raw_stream, _types
+from .fp8 import _device_index, _on_device, _on_stream, _raw_stream, _types, _workspace
 
 #: a, b, c of the quintic step whose five applications bring singular values to 0.7 .. 1.2
 NS_COEFFS = (3.4445, -4.7750, 2.0315)
@@ -89,6 +89,5 @@ def orthogonalize(G, O=None, steps: int = 5, coeffs=NS_COEFFS, eps: float = 1e-7
     if workspace is None:
         workspace = torch.empty(orthogonalize_workspace_size(m, n, batch), dtype=torch.uint8, device=G.device)
     orthogonalize_raw(m, n, batch, g3.data_ptr(), ldg, sg, codes[G.dtype], o3.data_ptr(), ldo, so, codes[O.dtype],
-                      steps, coeffs, eps, alpha, beta, workspace.data_ptr(),
-                      workspace.numel() * workspace.element_size(), _raw_stream()(index))
+                      steps, coeffs, eps, alpha, beta, *_workspace(workspace), _raw_stream()(index))
     return O

@@ -70,6 +70,23 @@ def test_tensors_on_the_host_are_refused_with_a_stream_too():
             call()
 
 
+def test_workspaces_with_gaps_or_repeats_are_refused():
+    """An expanded tensor's bytes are not there; one with gaps is not what its size says."""
+    import torch
+    mpg.build()
+    x = torch.randn((70, 515), device="cuda")
+    q, s = mpg.fp8_quantize(x)
+    odd = q[:, 1:513]
+    need = mpg.orthogonalize_workspace_size(70, 515)
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 22),
+               torch.empty(1 << 23, dtype=torch.uint8, device="cuda")[::2]):
+        assert ws.numel() >= need
+        with pytest.raises(ValueError, match="contiguous"):
+            mpg.orthogonalize(x, workspace=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            mpg.gemm_fp8(odd, s[:, :4], odd, s[:, :4], workspace=ws)
+
+
 def test_calls_from_several_threads():
     import threading
 
