@@ -236,45 +236,59 @@ __global__ void __launch_bounds__(T::kThreads, T::kCtasPerSm) fp8_gemm_kernel(co
       auto begin = [&](int t) {
         ring.start(p, smem_addr(ring_base) + ew * T::Ring::kBytes, lane, row_of(t) + 32 * q, col_of(t) + wc0, kb0, nkb);
       };
-      // Tiles of one form from tile t on; the first of the other form (or the
-      // end) is left in t.  (Each form has a loop of its own: chosen inside one
-      // loop over the tiles, 4096^3 takes 120 us instead of 117.)
-      int t = tile;
-      uint32_t n = 0;
-      auto tiles = [&](auto form) {
-        constexpr bool kPlain = decltype(form)::value;
-        for (;;) {
-#pragma unroll
-          for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
-#pragma unroll 1
-          for (int kb = 0; kb < nkb; ++kb, ++i) {
-            const uint32_t ab = i % T::kAccBufs;
-            __syncwarp();                                // every lane is done with the last block's slot
-            ring.fetch(kb + T::Ring::kDepth - 1);
-            cp_async_wait<T::Ring::kDepth - 1>();
-            if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) { ok = false; return false; }
-            __syncwarp();
-            tc_fence_after_sync();
-            const uint32_t slot = ring.slot(kb);
-            const float s = ld_shared_f32(slot + lane * 4);
-            add_block<T::kCols, kPlain>(acc, tacc + ab * T::kAccStride, slot, s, [&]() { release(ab); });
-          }
-          if (!T::kDirect) return false;
-          __syncwarp();
-          const bool more = t + step < p.num_tiles;
-          if (more) begin(t + step);                     // (its scales are on their way during the stores)
-          store(t);
-          t += step;
-          bool plain = true;
-          if (!more || !(ok = notes.read(n++, lane, ctl, &plain))) return false;
-          if (plain != kPlain) return true;
-        }
+      auto block = [&](int kb, auto form) {
+        const uint32_t ab = i % T::kAccBufs;
+        __syncwarp();                                    // every lane is done with the last block's slot
+        ring.fetch(kb + T::Ring::kDepth - 1);
+        cp_async_wait<T::Ring::kDepth - 1>();
+        if (!warp_wait(&acc_full[ab], (i / T::kAccBufs) & 1u, ctl)) return false;
+        __syncwarp();
+        tc_fence_after_sync();
+        const uint32_t slot = ring.slot(kb);
+        const float s = ld_shared_f32(slot + lane * 4);
+        add_block<T::kCols, decltype(form)::value>(acc, tacc + ab * T::kAccStride, slot, s, [&]() { release(ab); });
+        return true;
       };
       begin(tile);
-      bool plain;                                        // the first tile's form
-      if constexpr (T::kSwapped) plain = scan_alone<T::kCols>(p, lane, col0 + wc0, kb0, nkb);
-      else plain = scan_together<T::kEpiWarps * 32, T::BN>(p, ew * 32 + lane, col0, kb0, nkb);
-      while (plain ? tiles(std::true_type()) : tiles(std::false_type())) plain = !plain;
+      if constexpr (T::kDirect) {
+        // Tiles of one form from tile t on; the first of the other form (or the
+        // end) is left in t.  (Each form has a loop of its own: chosen inside
+        // one loop over the tiles, 4096^3 takes 120 us instead of 117.)
+        int t = tile;
+        uint32_t n = 0;
+        auto tiles = [&](auto form) {
+          for (;;) {
+#pragma unroll
+            for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
+#pragma unroll 1
+            for (int kb = 0; kb < nkb; ++kb, ++i)
+              if (!block(kb, form)) { ok = false; return false; }
+            __syncwarp();
+            const bool more = t + step < p.num_tiles;
+            if (more) begin(t + step);                   // (its scales are on their way during the stores)
+            store(t);
+            t += step;
+            bool plain = true;
+            if (!more || !(ok = notes.read(n++, lane, ctl, &plain))) return false;
+            if (plain != decltype(form)::value) return true;
+          }
+        };
+        bool plain = scan_together<T::kEpiWarps * 32, T::BN>(p, ew * 32 + lane, col0, kb0, nkb);
+        while (plain ? tiles(std::true_type()) : tiles(std::false_type())) plain = !plain;
+      } else {
+        auto blocks = [&](auto form) {
+#pragma unroll 1
+          for (int kb = 0; kb < nkb; ++kb, ++i)
+            if (!block(kb, form)) return false;
+          return true;
+        };
+        bool plain;
+        if constexpr (T::kSwapped) plain = scan_alone<T::kCols>(p, lane, col0 + wc0, kb0, nkb);
+        else plain = scan_together<T::kEpiWarps * 32, T::BN>(p, ew * 32 + lane, col0, kb0, nkb);
+#pragma unroll
+        for (int j = 0; j < T::kCols / 2; ++j) acc[j] = 0;
+        ok = plain ? blocks(std::true_type()) : blocks(std::false_type());
+      }
     } else {
       // A row a lane: its scale and that of all columns go from global memory
       // into registers, three blocks ahead.  Columns are read 32 at a time, the
