@@ -68,7 +68,6 @@ struct Fp8GemmParams {
 struct Fp8Kernel {
   const void* fn;
   int block, smem_bytes;
-  int ctas_per_sm;
   int tile_rows, tile_cols;
 };
 // One-CTA tiles of 128 x bn: bn = 128 (D as the caller's C; col_vec: a scale

@@ -90,14 +90,14 @@ Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool
     s = o.splitk;
   } else {
     // As many ranges as keep every CTA on an SM of its own, of two blocks at
-    // least: 64 x 4096 x 4096 takes 16.0, 11.4, 9.1, 7.6 us with 1 .. 4 ranges
-    // (128 CTAs) and 11.4 with 5 (160).  Of 128 x 128 tiles the exchange takes
-    // as long as kExchange blocks: 256 x 4096 x 512 takes 7.3 us with two
-    // ranges of two blocks and 5.4 with one, 256 x 4096 x 4096 12.0 and 15.2.
-    // Of narrow tiles it takes about four: 1 x 8192 x 1024 5.4 and 5.1 us, 1 x
-    // 8192 x 512 4.5 and 4.0, 1 x 8192 x 4096 9.0 and 11.8.
+    // least: 64 x 4096 x 4096 takes 17.9, 12.3, 9.6, 7.9 us with 1 .. 4 ranges
+    // (128 CTAs) and 12.0 with 5 (160).  Of 128 x 128 tiles the exchange takes
+    // as long as kExchange blocks: 256 x 4096 x 512 takes 7.1 us with two
+    // ranges of two blocks and 5.2 with one, 256 x 4096 x 4096 12.0 and 14.6.
+    // Of narrow tiles it takes about four: 1 x 8192 x 1024 4.6 and 4.7 us, 1 x
+    // 8192 x 512 4.0 and 3.6, 1 x 8192 x 4096 7.7 and 11.3.
     // Clusters lie within a group of SMs, so large ones leave some unused: 64 x
-    // 2048 x 8192 (16 tiles) takes 9.7 us with six ranges, 11.9 with eight.
+    // 2048 x 8192 (16 tiles) takes 9.9 us with six ranges, 12.1 with eight.
     while (s < 8 && tiles * (s + 1) <= sm_count && kb / (s + 1) >= 2 && tiles <= room((int)s + 1)) ++s;
     if (kb - (kb + s - 1) / s <= (p.swapped ? kNarrowExchange : kExchange)) s = 1;
   }
@@ -109,8 +109,8 @@ Fp8Plan plan_product(int64_t m, int64_t n, int64_t k, const mpg_options& o, bool
   // the way to its SM busy for a block of k as long as a pair's 256 x 256 tile
   // does (32 KB either way), but a pair's SM has twice the additions to do, and
   // with a scale for each column those take longest.  With a scale for 128
-  // columns 4096^3 takes 69 us on pairs and 91 on single CTAs, 4096 x 4096 x
-  // 512 22 and 21; with one for each column 121 and 118, 38 and 29.
+  // columns 4096^3 takes 71 us on pairs and 86 on single CTAs, 4096 x 4096 x
+  // 512 22 and 21; with one for each column (fp32 C) 125 and 117, 39 and 32.
   const int64_t pair_rounds = ((m + 255) / 256 * ((n + 255) / 256) + clusters - 1) / clusters;
   const int64_t rounds = (tiles * p.splits + sm_count - 1) / sm_count;
   const FormCost one = col_vec ? FormCost{1900, 460} : FormCost{1150, 355};

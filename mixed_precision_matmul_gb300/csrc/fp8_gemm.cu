@@ -6,6 +6,8 @@
 //   warp 0      TMA producer (one line of 128 k per row and stage)
 //   warp 1      TMEM allocation; one elected lane issues the MMAs, one
 //               accumulator buffer per k-block (four buffers in turn)
+//   the last    (direct, a scale for each column) looks at the column scales of
+//               the tiles to come (fp8_tc.cuh)
 //   warps 2..   epilogue: read each k-block's accumulator, add it to the
 //               running sums under its scales (fp8_tc.cuh), and at the end
 //               put the sums into shared memory, where the tile is read back
@@ -21,16 +23,16 @@
 // and each weight byte is read once; the kernel is then bound by the weights'
 // bytes, and the k range is divided so that most SMs have some in flight.
 //
-// On a GB300, from a graph: 1 x 8192 by 8192 x 8192 takes 14.7 us with weights
-// from DRAM (4.6 TB/s), 11.9 with what the L2 cache keeps of them; 33 x 4160 by
-// 4096 x 4160 takes 8.8 and 8.2 us, bound by the latency of a chain of blocks (a
+// On a GB300, from a graph: 1 x 8192 by 8192 x 8192 takes 15.0 us with weights
+// from DRAM (4.5 TB/s), 12.4 with what the L2 cache keeps of them; 33 x 4160 by
+// 4096 x 4160 takes 9.0 and 8.9 us, bound by the latency of a chain of blocks (a
 // block's load, MMAs and addition) and by the way in and out of the kernel.
-// Direct tiles take 355 ns a block of k, which is the operands' way from the L2
-// cache (32 KB an SM, 14 TB/s in all; the tensor cores need 140 ns), 460 with a
-// scale for each column: 1000 x 4112 by 1531 x 4112 takes 17.4 us, 4096^3 with a
-// scale for each column 118 us in fp32 (with eight epilogue warps instead of
-// sixteen 123; one tile a CTA 121; the next block's columns read during the
-// additions 139).
+// Direct tiles take 335 ns a block of k, which is the operands' way from the L2
+// cache (32 KB an SM, 15 TB/s in all; the tensor cores need 140 ns), 460 with a
+// scale for each column: 1000 x 4112 by 1531 x 4112 takes 17.3 us, 4096^3 with a
+// scale for each column 117 us in fp32.  Measured and not kept for the latter,
+// beside 118: eight epilogue warps instead of sixteen (123), one tile a CTA
+// (121), the next block's columns read during the additions (139).
 #include <type_traits>
 
 #include "fp8_tc.cuh"
@@ -494,7 +496,6 @@ bool fill(Fp8Kernel* out) {
   out->fn = reinterpret_cast<const void*>(&fp8_gemm_kernel<T>);
   out->block = T::kThreads;
   out->smem_bytes = T::kSmemBytes;
-  out->ctas_per_sm = T::kCtasPerSm;
   out->tile_rows = T::BM;
   out->tile_cols = T::BN;
   return true;

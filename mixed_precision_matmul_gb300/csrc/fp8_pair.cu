@@ -17,14 +17,15 @@
 // It is bound by latencies, so everything that is not one of these is on other
 // warps, and reads overlap additions.
 //
-// On a GB300, from a graph: 8192^3 with a scale for each 128 columns takes 432
-// us (2545 TFLOP/s; the MMAs alone, never read, 299 us), about 860 cycles a
+// On a GB300, from a graph: 8192^3 with a scale for each 128 columns takes 437
+// us (2516 TFLOP/s; the MMAs alone, never read, 299 us), about 870 cycles a
 // block: the way round MMA, commit, read and release through two buffers, all
-// that 512 columns of TMEM hold.  4096^3 with a scale for each column takes
-// 108 us.  Measured and not kept, at 8192^3: half-width accumulators in four
-// buffers (642 us: the tensor cores read R twice), 256 x 128 tiles (644 us);
-// at 4096^3, the 16-lane read of TMEM that lets a thread keep its columns'
-// scales in registers (112 us: that read takes three times as long).
+// that 512 columns of TMEM hold.  With a scale for each column and fp32 C 4096^3
+// takes 125 us (single CTAs: 117), 8192^3 770 (829).  Measured and not kept, at
+// 8192^3: half-width accumulators in four buffers (642 us: the tensor cores read
+// R twice), 256 x 128 tiles (644 us); at 4096^3, the 16-lane read of TMEM that
+// lets a thread keep its columns' scales in registers (4 us slower: that read
+// takes three times as long).
 #include <type_traits>
 
 #include "fp8_tc.cuh"
@@ -408,7 +409,6 @@ bool fill(Fp8Kernel* out) {
   out->fn = reinterpret_cast<const void*>(&fp8_pair_kernel<T>);
   out->block = T::kThreads;
   out->smem_bytes = T::kSmemBytes;
-  out->ctas_per_sm = 1;
   out->tile_rows = T::kTile;
   out->tile_cols = T::kTile;
   return true;

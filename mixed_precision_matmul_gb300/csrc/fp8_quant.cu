@@ -15,9 +15,12 @@
 // The kernel is bound by memory: x is read once, in 128 x 128 tiles held in
 // registers (an 8 x 8 patch per thread), and both the row-wise and the
 // transposed form come from that one read.  On a GB300: 8190 x 8192 bf16 in
-// both directions takes 49 us, 5.5 TB/s (a plain copy: 6.8); 4096 x 11008 fp32
-// in tiles 43 us, 6.3 TB/s; 1531 x 4100 fp16 8.4 us, where lines of the
-// transpose start off its vectors; one row of 8192 3 us, a launch's latency.
+// both directions takes 50 us, 5.4 TB/s (a plain copy: 6.8); 4096 x 11008 fp32
+// in tiles 43 us, 6.3 TB/s; one row of 8192 3 us, a launch's latency.  1531 x
+// 4100 fp16 takes 8.3 us where 1536 x 4096 takes 5.4: the tiles at the edges,
+// whose cut patches are loaded element by element and whose lines end in single
+// bytes, take 2 us longer than the others, either edge as much as both (1531 x
+// 4096 7.7, 1536 x 4100 7.6 us); that lines of x start off 16 bytes costs nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

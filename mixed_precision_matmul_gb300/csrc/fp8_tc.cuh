@@ -116,7 +116,7 @@ __device__ __forceinline__ void ld_shared_pairs(uint32_t addr, f32x2& a, f32x2& 
 // 437 us; 432 without the choice, 487 with one for every 32 columns).  With a
 // scale for each column that takes too long beside the additions (4096^3: 126
 // us; 118 without the choice): a tile's form is chosen by its columns' scales in
-// all blocks (120 us), which the epilogue's threads look at before the first
+// all blocks (117 us), which the epilogue's threads look at before the first
 // tile, while its first operands are on their way, and a warp beside them for
 // each tile after.
 // Elsewhere the row's scale is taken in two parts, first * last, last a power

@@ -21,12 +21,12 @@
 // are computed, and stored twice.  A step costs m^2 n + m^3 + 2 m^2 n flops
 // (m the shorter side) instead of 2 m^2 n + 2 m^3 + 2 m^2 n.
 //
-// On a GB300, five steps from a graph: 4096^2 takes 905 to 940 us (about 1500
+// On a GB300, five steps from a graph: 4096^2 takes 910 to 950 us (about 1500
 // TFLOP/s of those flops, 0.78 of what a large library product reaches), bound by the
 // tensor cores, by the last rounds of tiles (256 and 136 tiles on 76 pairs) and
 // by the ways in and out of fifteen launches; 12 matrices of 2048 x 768 take
-// 329 us, where those two weigh most; 256 x 1000 takes 106 us, all of it
-// launches and latencies (seven for a product).
+// 332 to 345 us, where those two weigh most; 1024^2 takes 116 us and 256 x 1000
+// 110 us, all of it launches and latencies (seven for a product).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -134,9 +134,11 @@ __device__ __noinline__ void add_wide(double* wide, const float (&v)[kBatch][8])
 }
 
 // partial[b][block] = sum of squares over the block's share of matrix b.  The
-// squares of a batch of elements are added in fp32 where that is safe (the sum
-// neither near overflow nor near underflow) and in 64 bits elsewhere; so are
-// the threads' sums, always in the same order.
+// squares of a batch of 32 elements, a thread's batches and the block's threads
+// are added in fp32 where that is safe (the sum neither near overflow nor near
+// underflow) and in 64 bits elsewhere, always in the same order.  With q batches
+// to a thread the sum is off by at most (23 + q) 2^-24 of itself, the norm by
+// half of that: 9e-7 for 4096^2 (q = 6).
 template <class XT>
 __global__ void __launch_bounds__(kScaleThreads) ortho_norm_kernel(const __grid_constant__ OrthoScaleParams p) {
   __shared__ float red[kScaleThreads / 32];
@@ -1037,7 +1039,7 @@ __global__ void __launch_bounds__(DividedTraits::kThreads, 1)
   // The other CTAs' shared memory has been read: the value of every load from
   // it went into a store above (lane 0 stores in each row that is loaded).  Only
   // that is announced: a release waits for the stores as well, and takes 0.6 us
-  // a launch even where it comes before them (1024^2: 128 us instead of 119).
+  // a launch even where it comes before them (1024^2: 128 us instead of 115).
   __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   if (out.mir) {
