@@ -493,7 +493,9 @@ mpg_status mpg_gemm_fp8(int64_t m, int64_t n, int64_t k, const mpg_fp8_operand* 
  * about 1e-3 of its norm (before its rounding to O's type), whatever G's norm is
  * beside eps; directions whose singular value is below about 2^-12 of the
  * largest come out as noise of that size times a^steps, and coefficients whose
- * iterates grow far beyond 1 overflow fp16.  A NaN or infinity in a matrix makes
+ * iterates grow far beyond 1 overflow fp16.  The tensor cores' fp32 sums over the
+ * longer side do not round to nearest: with longer sides above about 2^19 their
+ * error is the larger one (3e-3 for 64 x 2^20, 2e-2 for 4 x 2^22).  A NaN or infinity in a matrix makes
  * the whole of its result NaN; other matrices of the batch are not touched by it. */
 size_t mpg_orthogonalize_workspace_size(int64_t m, int64_t n, int64_t batch);
 mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G, int64_t ldg, int64_t strideG,
