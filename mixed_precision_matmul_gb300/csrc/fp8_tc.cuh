@@ -106,7 +106,8 @@ __device__ __forceinline__ void ld_shared_pairs(uint32_t addr, f32x2& a, f32x2& 
 // How a block's two scales meet its sum P, |P| in [2^-32, 2^39) or 0: scales may
 // be any fp32 values, and no step but the last may leave fp32's normal range.
 //   one scale for all columns   P * (row * column), where that product of the
-//                               scales is in the normal range;
+//                               scales is in the normal range or one of them
+//                               is 0;
 //   a scale for each column     (P * column) * row, where the columns' scales
 //                               are 0 or in [2^-94, 2^89), so that P * column is
 //                               in range.  (In the other order the multiply-add
@@ -123,9 +124,12 @@ __device__ __forceinline__ void ld_shared_pairs(uint32_t addr, f32x2& a, f32x2& 
 // of two: ((P * first) * column) * last.  For tiny rows first is in
 // [2^-94, 2^-39): P * first * column cannot overflow, and where it is below the
 // normal range the result is below 2^-181.  For huge rows first is in
-// [2^69, 2^89): the reverse.
+// [2^69, 2^89): the reverse.  (All blocks in that form: 8192^3 856 us, 4096^3
+// with a scale for each column 133.)
 __device__ __forceinline__ uint32_t scale_field(float s) { return (__float_as_uint(s) >> 23) & 255u; }
-__device__ __forceinline__ bool plain_scale(float row, float col) { return scale_field(row * col) - 1u < 254u; }
+__device__ __forceinline__ bool plain_scale(float row, float col) {
+  return scale_field(row * col) - 1u < 254u || fminf(fabsf(row), fabsf(col)) == 0.0f;
+}
 __device__ __forceinline__ bool plain_column(float col) {
   return scale_field(col) - (127u - 94u) < 94u + 89u || col == 0.0f;
 }

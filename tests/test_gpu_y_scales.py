@@ -147,3 +147,26 @@ def test_a_few_columns_far_from_the_others(pair, k):
     for t in range(-(-n // tile)):
         if t not in touched:
             assert torch.equal(got[:, t * tile:(t + 1) * tile], plain[:, t * tile:(t + 1) * tile])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_scales_of_zero(form):
+    """Blocks that a caller's own quantiser gave the scale 0: their sums count nothing, the other rows and
+    columns keep their bits."""
+    m, size, _ = FORMS[form]
+    n, k = 300, 500
+    rng = np.random.default_rng(8)
+    a, b = codes(m, k, rng, "e4m3", -9, 8), codes(n, k, rng, "e4m3", -9, 8)
+    sa = (2.0 ** rng.uniform(-8, 8, (m, blocks(k)))).astype(np.float32)
+    sb = (2.0 ** rng.uniform(-8, 8, (-(-n // size), blocks(k)))).astype(np.float32)
+    before = run(form, a, sa, b, sb)[0]
+    za, zb = sa.copy(), sb.copy()
+    za[::3] = 0
+    za[1, 2] = 0
+    zb[1] = 0
+    got, want, bound = run(form, a, za, b, zb)
+    assert np.all(np.abs(got - want) <= bound)
+    assert np.all(got[::3] == 0) and np.all(got[:, size:2 * size] == 0)
+    rows = [r for r in range(m) if r % 3 and r != 1]
+    cols = [c for c in range(n) if c // size != 1]
+    assert np.array_equal(got[np.ix_(rows, cols)], before[np.ix_(rows, cols)])
