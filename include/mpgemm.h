@@ -503,6 +503,100 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
                              int32_t steps, const float* coeffs, float eps, float alpha, float beta, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* ---- gated feed-forward product ------------------------------------------
+ * Y = act(X Wg^T) * (X Wu^T): both projections of a gated feed-forward layer,
+ * the activation and the product in one kernel; and its gradients.
+ *   X   tokens x hidden;  Wg, Wu  inner x hidden;  Y, G, U, dY  tokens x inner.
+ * All matrices are row-major and of one 16-bit type, with leading dimensions of
+ * at least their lines, any alignment of an element; 16-byte aligned bases and
+ * leading dimensions of whole 16 bytes are fastest (others are copied to such
+ * lines in the workspace, or read element by element for up to 32 tokens).
+ * Sizes <= 2^31 - 256.  Results do not depend on timing.  Results may not
+ * overlap operands or each other. */
+typedef enum { MPG_ACT_SILU = 0, MPG_ACT_GELU = 1, MPG_ACT_GELU_TANH = 2 } mpg_activation;
+typedef struct {
+  int64_t tokens, hidden, inner;
+  mpg_dtype dtype;              /* MPG_F16 or MPG_BF16 */
+  mpg_activation act;
+  const void *x, *wg, *wu;
+  int64_t ldx, ldwg, ldwu;
+} mpg_gated_layer;
+
+/* Y, and with G and U (both or neither NULL) the projections X Wg^T and X Wu^T
+ * for the backward pass.  Sums are fp32; Y is computed from them before they
+ * are rounded, and every result is rounded once.  hidden 0: Y = 0. */
+size_t mpg_gated_gemm_workspace_size(const mpg_gated_layer* layer);
+mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, void* G, int64_t ldg, void* U, int64_t ldu,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* With dG = dY * U * act'(G) and dU = dY * act(G):
+ *     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X.
+ * dX may be NULL, and dWg and dWu together (frozen weights).  G, U: what
+ * mpg_gated_gemm kept; both NULL: the projections are computed again (half as
+ * many operations more, and the better gradient: they are not rounded between).
+ * dG and dU are rounded once to the 16-bit type, as operands of the products;
+ * in fp16 they carry a power of two meanwhile, which brings the largest of dY
+ * to [16, 32), so that small gradients keep their precision; products up * act'
+ * above 2^11 then overflow.  tokens or inner 0: gradients of 0. */
+size_t mpg_gated_gemm_backward_workspace_size(const mpg_gated_layer* layer);
+mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY, int64_t lddy, const void* G, int64_t ldg,
+                                   const void* U, int64_t ldu, void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
+                                   int64_t lddwu, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- cross entropy of a projection onto a vocabulary ----------------------
+ * For each token, with logits l = X W^T (never kept):
+ *     lse = log sum_c e^(l[c]),  loss = lse - l[target];  both 0 where target == ignore_index.
+ *   X  tokens x hidden;  W  vocab x hidden, 16 bits as above;  target  tokens
+ *   integers of 4 or 8 bytes, target_stride apart (in integers).
+ * A target that is neither ignore_index nor a class makes loss and lse NaN, and
+ * in the backward pass its row of dX and all of dW.  loss and lse: tokens fp32.
+ * Maxima, sums and logits are fp32; a NaN in a row makes its loss NaN. */
+typedef struct {
+  int64_t tokens, hidden, vocab;
+  mpg_dtype dtype;              /* MPG_F16 or MPG_BF16 */
+  const void *x, *w;
+  int64_t ldx, ldw;
+  const void* target;
+  int32_t target_bytes;         /* 4 or 8 */
+  int64_t target_stride;
+  int64_t ignore_index;
+} mpg_vocab_loss;
+size_t mpg_linear_cross_entropy_workspace_size(const mpg_vocab_loss* desc);
+mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Gradients for dloss, tokens fp32 dloss_stride apart (0: one for all; those of
+ * ignored tokens are not used): with
+ *     D = (e^(l - lse) - [c == target]) * dloss,
+ *     dX = D W,  dW = D^T X  (either may be NULL).
+ * D is made for a piece of the vocabulary at a time (512 MB at most, or 256
+ * classes), from logits that are computed again; it is rounded once to the
+ * 16-bit type, in fp16 times a power of two that brings the largest dloss to
+ * [2^14, 2^15).  dX is summed over the pieces in fp32.  tokens 0: dW = 0. */
+size_t mpg_linear_cross_entropy_backward_workspace_size(const mpg_vocab_loss* desc);
+mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const float* lse, const float* dloss,
+                                             int64_t dloss_stride, void* dX, int64_t lddx, void* dW, int64_t lddw,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- norm of many gradients, and clipping ---------------------------------
+ * norm = sqrt(sum over all gradients of g^2), to device memory, and for each
+ *     out = g * min(1, max_norm / (norm + eps)),  rounded once to out's type.
+ * Tensors are packed, of any size (0 too) and type each; out may be g (in the
+ * same type), and overlap nothing else of the call (MPG_ERR_INVALID_ARG).
+ * max_norm >= 0, infinity to scale by 1.  Squares are summed in fp32 by eights
+ * and in 64 bits beyond, wherever fp32 cannot hold them too; norms above fp32's
+ * range are infinity.  An infinite norm makes the factor 0 (infinities become
+ * NaN), a NaN makes everything NaN.  n <= 2^20. */
+typedef struct {
+  const void* g;
+  void* out;
+  int64_t count;
+  mpg_dtype g_dtype, out_dtype;
+} mpg_grad;
+size_t mpg_clip_grad_norm_workspace_size(int64_t n, const mpg_grad* grads);
+mpg_status mpg_clip_grad_norm(int64_t n, const mpg_grad* grads, float max_norm, float eps, float* norm, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Bytes of workspace for this exact call: mpg_gemm_workspace_size() plus
  * room for copies of the operands the TMA path cannot take as given:
  * 16-bit operands (FP16 / BF16 modes) and fp32 operands (TF32) whose base is

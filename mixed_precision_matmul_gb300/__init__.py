@@ -14,6 +14,11 @@ Entry points mirror ``include/mpgemm.h``:
 * :func:`fp8_quantize`, :func:`gemm_fp8`   8-bit operands with a scale for
   each block of 128: the quantiser and the product.
 * :func:`orthogonalize`   Newton-Schulz orthogonalisation of an update.
+* :func:`gated_gemm`, :func:`gated_gemm_backward`   act(X Wg^T) * (X Wu^T) of a
+  gated feed-forward layer, and its gradients.
+* :func:`linear_cross_entropy`, :func:`linear_cross_entropy_backward`   the loss of
+  a projection onto a vocabulary without keeping the logits, and its gradients.
+* :func:`clip_grad_norm`   the norm of many gradients, and the gradients scaled.
 * :func:`acc_coords`, :func:`acc_offset`, :func:`acc_matrix_offset`,
   :func:`acc_decode`, :func:`tmem_acc_coords`, :func:`tmem_acc_decode`   host decode of accumulator
   fragments.
@@ -148,6 +153,8 @@ def lib():
         L.mpg_orthogonalize.argtypes = [i64, i64, i64, vp, i64, i64, i32, vp, i64, i64, i32, i32,
                                         ctypes.POINTER(ctypes.c_float), f32, f32, f32, vp, sz, vp]
         L.mpg_orthogonalize.restype = i32
+        for module in (gated, loss, clip):
+            module._declare(L)
         L.mpg_options_init.argtypes = [ctypes.POINTER(Options)]
         L.mpg_options_init.restype = None
         L.mpg_device_status.argtypes = [vp]
@@ -626,3 +633,9 @@ def selftest_wait_timeout(timeout_ns: int, stream=None) -> int:
 
 from .fp8 import E4M3, E5M2, fp8_quantize, fp8_quantize_raw, gemm_fp8, gemm_fp8_raw  # noqa: E402,F401
 from .ortho import NS_COEFFS, orthogonalize, orthogonalize_raw, orthogonalize_workspace_size  # noqa: E402,F401
+from . import clip, gated, loss  # noqa: E402
+from .gated import (ACT_GELU, ACT_GELU_TANH, ACT_SILU, GatedLayer, gated_gemm, gated_gemm_backward,  # noqa: E402,F401
+                    gated_gemm_backward_raw, gated_gemm_raw)
+from .loss import (VocabLoss, linear_cross_entropy, linear_cross_entropy_backward,  # noqa: E402,F401
+                   linear_cross_entropy_backward_raw, linear_cross_entropy_raw)
+from .clip import CLIP_EPS, Grad, clip_grad_norm, clip_grad_norm_raw  # noqa: E402,F401

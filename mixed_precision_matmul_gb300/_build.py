@@ -46,9 +46,16 @@ SOURCES = [
     "fp8_pair.cu",
     "ortho_api.cu",
     "ortho.cu",
+    "fused_plan.cu",
+    "fused_gemm.cu",
+    "few_rows.cu",
+    "fused_aux.cu",
+    "gated_api.cu",
+    "loss_api.cu",
+    "clip.cu",
 ]
 HEADERS = ["ptx.cuh", "cluster.cuh", "internal.h", "tc_gemm.cuh", "outio.cuh", "host.h", "staging.cuh",
-           "fp8.h", "fp8_tc.cuh", "ortho.h"]
+           "fp8.h", "fp8_tc.cuh", "ortho.h", "fused.h", "fused.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,169 @@
+// Internal structures of the 16-bit products with fused epilogues: the gated
+// feed-forward product, the projection onto a vocabulary with its cross
+// entropy, and the products of their gradients (fused_gemm.cu, few_rows.cu,
+// fused_aux.cu), launched from gated_api.cu and loss_api.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "host.h"
+
+namespace mpg {
+
+// What a product's accumulators become.
+enum class FusedEpi {
+  kPlain,      // C = inverse * sum (+ what earlier products left), fp32 or 16 bits
+  kGated,      // Y = act(gate) * up; gate and up too, where they are kept
+  kGatedGrad,  // gradients of gate and up from that of Y
+  kStats,      // maximum and sum of exponentials of a row's part; the target's logit
+  kProb,       // gradient of the logits
+};
+
+constexpr int kMaxCtas = 160;          // workers of a launch, at most: the slots of split tiles are laid out for them
+constexpr int kScaleBlocks = 152;      // partial maxima behind a scale
+
+// Rows that a product of few rows takes (few_rows.cu).
+constexpr int kFewRows = 32;
+
+struct FusedGemmParams {
+  CUtensorMap map_a[2], map_b[2];   // boxes of 64 x 64
+  int32_t a_mn_major, b_mn_major, bf16;
+  int32_t m, n;                     // of the result (kGated, kGatedGrad: n of each half)
+  int32_t num_m_blk, num_n_blk, num_k_blk;
+  int32_t kb_second;                // first block of k that comes from map_a[1] and map_b[1]
+  int32_t mb_second;                // first row block of the second matrix: map_a[1], out[1]
+  int32_t num_tiles, group_m;
+  int32_t whole_tiles;              // taken round by round; the others' blocks of k are dealt out evenly
+  int64_t units;                    // blocks of k of those others
+  float* slots;                     // partial tiles, two for each worker
+
+  int32_t act;
+  void* out[3];                     // kPlain: C, second C; kGated: Y, gate, up (or null); kGatedGrad: dgate, dup; kProb: D
+  int64_t ldo[3];
+  int32_t out_vec[3];               // 8 elements of 16 bits (4 of fp32) are aligned
+  int32_t out_dtype;
+  const float* add;                 // kPlain: fp32, added to the result, or null
+  int64_t ldadd;
+  const void* dy;                   // kGatedGrad
+  int64_t lddy;
+  int32_t dy_vec;
+  const float* scale;               // partial maxima behind the power of two that fp16 gradients carry, or null
+  int32_t scale_exp;                // the largest is brought to [2^e, 2^(e+1))
+
+  // cross entropy
+  const void* target;
+  int32_t target_bytes;
+  int64_t target_stride, ignore_index;
+  int32_t col0;                     // class of the first column
+  int32_t vocab;
+  float2* stats;                    // [part][m]: maximum (of logits times log2 e) and sum of 2^(. - maximum)
+  float* target_logit;              // [m]
+  const float* lse;
+  const float* dloss;
+  int64_t dloss_stride;
+
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+struct FusedKernel {
+  const void* fn;
+  int block, smem_bytes;
+  int tile;                         // rows of a tile, and columns of its accumulators
+  int ctas;
+};
+void fused_lookup(FusedEpi epi, bool pair, FusedKernel* out);
+// Sums the parts of split tiles (kPlain).
+cudaError_t launch_fused_join(const FusedGemmParams& p, int tile, int workers, cudaStream_t stream);
+
+// The product of few rows: gated (wu given) or the statistics of logits.
+struct FewRowsParams {
+  const void *x, *w, *wu;           // X: rows x k; weights: n x k
+  int64_t ldx, ldw, ldwu;
+  int32_t bf16, rows, n, k;
+  int32_t vec;                      // lines of all operands start on 16-byte boundaries
+  int32_t act;
+  void *y, *g, *u;
+  int64_t ldy, ldg, ldu;
+  const void* target;
+  int32_t target_bytes;
+  int64_t target_stride, ignore_index;
+  float2* stats;
+  float* target_logit;
+};
+cudaError_t launch_few_rows(const FewRowsParams& p, bool gated, cudaStream_t stream);
+int few_rows_parts(int rows, int64_t n);   // of the statistics of n logits
+
+// Copies of matrices whose lines TMA cannot describe.
+struct PadParams {
+  struct Matrix {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t ld_src, ld_dst, rows, cols;
+  } mat[4];
+  int32_t count;
+};
+cudaError_t launch_pad(const PadParams& p, int sm_count, cudaStream_t stream);
+
+// Partial maxima of |x| over a matrix (16 bits) or of |dloss| over the tokens that count.
+struct MaxParams {
+  const void* x;
+  int64_t ld, rows, cols;
+  int32_t vec;
+  const float* dloss;
+  int64_t dloss_stride;
+  const void* target;
+  int32_t target_bytes;
+  int64_t target_stride, ignore_index;
+  float* partial;                   // [kScaleBlocks]
+};
+cudaError_t launch_max(const MaxParams& p, cudaStream_t stream);
+
+// dgate and dup from dY and the kept gate and up.
+struct GatedGradParams {
+  const void *dy, *g, *u;
+  int64_t lddy, ldg, ldu;
+  uint16_t *dg, *du;
+  int64_t ldd;
+  int64_t rows, cols;
+  int32_t vec, act, bf16;
+  const float* scale;
+  int32_t scale_exp;
+};
+cudaError_t launch_gated_grad(const GatedGradParams& p, int sm_count, cudaStream_t stream);
+
+// loss and lse from the parts' maxima and sums.
+struct LossJoinParams {
+  const float2* stats;
+  int32_t parts;
+  int64_t rows;
+  const float* target_logit;
+  const void* target;
+  int32_t target_bytes;
+  int64_t target_stride, ignore_index, vocab;
+  float *loss, *lse;
+};
+cudaError_t launch_loss_join(const LossJoinParams& p, cudaStream_t stream);
+
+// ---- host services shared by the two APIs (fused_plan.cu)
+struct FusedLaunch {
+  FusedEpi epi;
+  int64_t m, n, k;                  // k: of the first part where there are two
+  bool second_k = false;            // the second part of k has the same length
+  bool second_m = false;            // a second matrix of m rows
+  bool split = false;               // tiles may be split along k (kPlain)
+};
+mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& p, float* slots, cudaStream_t stream);
+size_t fused_slot_bytes(const FusedLaunch& l);   // of the slots that a launch may need
+// rows x k operand of a product: K-major if k is the matrix's contiguous side.
+mpg_status fused_map(CUtensorMap* map, const void* ptr, int64_t ld, mpg_dtype dt, bool mn_major, int64_t rows, int64_t k);
+
+constexpr int64_t kFusedMaxExtent = 0x7FFFFFFF - 255;   // the last tile's end, and a block beyond it, still fit 32 bits
+inline int64_t fused_line(int64_t n) { return (n + 7) / 8 * 8; }
+inline bool fused_aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// TMA can describe rows x cols lines of 16-bit elements
+inline bool fused_lines_ok(const void* p, int64_t ld) { return fused_aligned(p, 16) && ld % 8 == 0; }
+
+}  // namespace mpg

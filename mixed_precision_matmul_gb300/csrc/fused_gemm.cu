@@ -1,0 +1,703 @@
+// 16-bit products whose epilogues do the work around them (sm_103a).
+//
+// One persistent kernel, on pairs of CTAs (256 x 256 accumulators, M = 256
+// instructions of cta_group::2) or on single CTAs (128 x 128), for five
+// epilogues:
+//
+//   kGated      Y = act(X Wg^T) * (X Wu^T).  The B operand of a tile is half of
+//               lines of Wg and half of the same lines of Wu, so gate and up
+//               are two halves of one accumulator, and a thread of the
+//               epilogue holds both of an element.  On a pair the instruction
+//               splits B between the CTAs: rank 0 holds Wg's lines, rank 1 Wu's.
+//   kGatedGrad  the same accumulators; dgate = dY up act'(gate), dup = dY act(gate).
+//   kStats      logits X W^T; a thread holds a row's part of the tile and keeps
+//               the maximum and the sum of exponentials in one pass, and the
+//               target's logit.  Logits are in units of ln 2, so that the exponential is
+//               one instruction.
+//   kProb       the same logits; (e^(l - lse) - [target]) dloss, rounded to 16 bits,
+//               for a piece of the vocabulary.
+//   kPlain      the gradients' products.  Both operands may be MN-major, k may
+//               consist of two parts with maps of their own (dgate Wg + dup Wu:
+//               one sum in fp32), and so may the rows (dgate^T X and dup^T X:
+//               one launch).
+//
+// Roles (320 threads): warp 0 loads by TMA, warp 1 (of rank 0) issues the MMAs,
+// warps 2-9 are the epilogue: 32 rows and half of the tile's columns each.
+// Accumulators are double-buffered in TMEM, so the epilogue runs beside the
+// next tile's products.
+//
+// Tiles go round by round to the workers.  What does not fill a round is split
+// (kPlain): its blocks of k are dealt out evenly, each worker getting one run of
+// them, and a worker whose run holds only a part of a tile's k leaves its sums
+// in a slot.  A second launch adds the slots of a tile in the order of k: the
+// result does not depend on timing.
+//
+// Waits are bounded, and a timeout raises the abort flag of both CTAs: every
+// role drains what it has in flight before TMEM is released.
+#include <climits>
+
+#include "cluster.cuh"
+#include "fused.cuh"
+#include "outio.cuh"
+#include "staging.cuh"
+#include "tc_gemm.cuh"
+
+namespace mpg {
+namespace {
+
+template <FusedEpi E, bool kPair_>
+struct FusedTraits {
+  static constexpr FusedEpi kEpi = E;
+  static constexpr bool kPair = kPair_;
+  static constexpr bool kTwo = E == FusedEpi::kGated || E == FusedEpi::kGatedGrad;   // gate and up
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kTile = 128 * kCtas;         // rows, and columns of the accumulators
+  static constexpr int kTileN = kTwo ? kTile / 2 : kTile;
+  static constexpr int BM = 128;                    // rows of A held by one CTA
+  static constexpr int BK = 64;
+  static constexpr int kRowBytes = 128;
+  static constexpr uint32_t kSwizzle = kSwizzle128B;
+  static constexpr int kInstrK = 16;
+  static constexpr int kKSteps = BK / kInstrK;
+  static constexpr int kHalf = 64 * kRowBytes;      // one 64 x 64 box
+  static constexpr int kATile = 2 * kHalf;
+  static constexpr int kStage = 2 * kATile;
+  static constexpr int kStages = 6;
+  static constexpr int kAccBufs = 2;
+  static constexpr int kTmemCols = kAccBufs * kTile;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = (2 + kEpiWarps) * 32;
+  static constexpr int kEpiBytes = kEpiWarps * 4096;
+  static constexpr int kNumBars = 2 * kStages + 2 * kAccBufs + 1;
+  static constexpr int kSmemBytes = 1024 + kStages * kStage + kEpiBytes + kNumBars * 8 + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_shared_h(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_h(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+// 32 rows of 64 bytes: chunk c (16 bytes) of row r at slot c ^ ((r / 2) & 3),
+// which spreads writes (a row a lane) and reads (four lanes a row) over all banks.
+__device__ __forceinline__ uint32_t half_chunk(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// 32 x 32 block of 16-bit values, a row a lane, to rows row0.. and columns col0.. .
+__device__ __forceinline__ void store_block16(uint32_t stg, int lane, const uint32_t (&w)[16], void* base, int64_t ld,
+                                              int row0, int rows, int col0, int cols, bool vec) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    st_shared_v4(stg + half_chunk(lane, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+  uint16_t* out = static_cast<uint16_t*>(base);
+  if (vec && col0 + 32 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), c = lane & 3;
+      if (row0 + r < rows)
+        *reinterpret_cast<uint4*>(out + (int64_t)(row0 + r) * ld + col0 + c * 8) = ld_shared_v4(stg + half_chunk(r, c));
+    }
+  } else if (col0 + lane < cols) {
+#pragma unroll 4
+    for (int r = 0; r < 32; ++r)
+      if (row0 + r < rows)
+        out[(int64_t)(row0 + r) * ld + col0 + lane] = ld_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2);
+  }
+  __syncwarp();
+}
+// The same read: row row0 + lane, 32 columns (0 beyond the matrix).
+__device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&w)[16], const void* base, int64_t ld,
+                                             int row0, int rows, int col0, int cols, bool vec) {
+  const uint16_t* src = static_cast<const uint16_t*>(base);
+  if (vec && col0 + 32 <= cols) {
+    const bool in = row0 + lane < rows;
+    const uint4* at = reinterpret_cast<const uint4*>(src + (int64_t)(in ? row0 + lane : row0) * ld + col0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 x = in ? ld_global(at + c) : make_uint4(0, 0, 0, 0);
+      w[4 * c] = x.x;
+      w[4 * c + 1] = x.y;
+      w[4 * c + 2] = x.z;
+      w[4 * c + 3] = x.w;
+    }
+    return;
+  }
+  const bool in = col0 + lane < cols;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r)
+    st_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2,
+                in && row0 + r < rows ? src[(int64_t)(row0 + r) * ld + col0 + lane] : (uint16_t)0);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint4 x = ld_shared_v4(stg + half_chunk(lane, c));
+    w[4 * c] = x.x;
+    w[4 * c + 1] = x.y;
+    w[4 * c + 2] = x.z;
+    w[4 * c + 3] = x.w;
+  }
+  __syncwarp();
+}
+
+struct FusedTile {
+  int mb, nb;
+};
+__device__ __forceinline__ FusedTile fused_tile(const FusedGemmParams& p, int t) {
+  // groups of tile rows, walked column by column, every other group backwards
+  const int per = p.group_m * p.num_n_blk;
+  const int g = t / per;
+  const int first = g * p.group_m;
+  const int gm = min(p.group_m, p.num_m_blk - first);
+  const int within = t - g * per;
+  FusedTile c;
+  c.mb = first + within % gm;
+  c.nb = within / gm;
+  if (g & 1) c.nb = p.num_n_blk - 1 - c.nb;
+  return c;
+}
+
+// The first of the split tiles' blocks of k that worker w takes.
+__host__ __device__ __forceinline__ int64_t first_unit(int64_t units, int w, int workers) { return units * w / workers; }
+
+// A worker's tiles: whole ones round by round, then its run of the others'
+// blocks of k.
+struct FusedItem {
+  int mb, nb, kb0, kb1;
+  int slot;                          // of a part of a tile's k; -1: all of it
+};
+struct FusedItems {
+  int t, worker, workers;
+  int64_t u, u0, u1;
+  __device__ __forceinline__ FusedItems(const FusedGemmParams& p, int w, int n) : t(w), worker(w), workers(n) {
+    u = u0 = u1 = 0;
+    if (p.units) {
+      u = u0 = first_unit(p.units, w, n);
+      u1 = first_unit(p.units, w + 1, n);
+    }
+  }
+  __device__ __forceinline__ bool next(const FusedGemmParams& p, FusedItem& x) {
+    int tile;
+    if (t < p.whole_tiles) {
+      tile = t;
+      t += workers;
+      x.kb0 = 0;
+      x.kb1 = p.num_k_blk;
+      x.slot = -1;
+    } else if (u < u1) {
+      const int64_t j = u / p.num_k_blk;
+      tile = p.whole_tiles + (int)j;
+      x.kb0 = (int)(u - j * p.num_k_blk);
+      x.kb1 = (int)min((int64_t)p.num_k_blk, x.kb0 + (u1 - u));
+      x.slot = x.kb1 - x.kb0 == p.num_k_blk ? -1 : 2 * worker + (u == u0 ? 0 : 1);
+      u += x.kb1 - x.kb0;
+    } else {
+      return false;
+    }
+    const FusedTile c = fused_tile(p, tile);
+    x.mb = c.mb;
+    x.nb = c.nb;
+    return true;
+  }
+};
+
+template <class T>
+__global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid_constant__ FusedGemmParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* epi_base = smem + T::kStages * T::kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi_base + T::kEpiBytes);
+  uint64_t* op_full = bars;                         // rank 0: a stage's copies landed in every CTA
+  uint64_t* op_empty = bars + T::kStages;           // each CTA: the MMAs consumed the stage
+  uint64_t* acc_full = bars + 2 * T::kStages;       // each CTA: an accumulator is complete
+  uint64_t* acc_empty = acc_full + T::kAccBufs;     // rank 0: every epilogue warp has read it
+  uint64_t* done_bar = acc_empty + T::kAccBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = T::kPair ? cluster_ctarank() : 0u;
+  const int worker = T::kPair ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int workers = T::kPair ? (int)num_clusters_x() : (int)gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::kStages; ++i) {
+      mbar_init(&op_full[i], 1);
+      mbar_init(&op_empty[i], 1);
+    }
+    for (int i = 0; i < T::kAccBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], T::kCtas * T::kEpiWarps);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&p.map_a[0]);
+    tma_prefetch_map(&p.map_b[0]);
+  }
+  if (warp == 1) {
+    if constexpr (T::kPair) {
+      tmem_alloc_pair(tmem_slot, T::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, T::kTmemCols);
+      tmem_relinquish();
+    }
+    tc_fence_before_sync();
+  }
+  if constexpr (T::kPair) cluster_sync_all();
+  else __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  WaitCtl ctl;
+  ctl.abort = abort_flag;
+  if constexpr (T::kPair) ctl.peer_abort = cluster_generic_ptr(const_cast<int*>(abort_flag), rank ^ 1u);
+  ctl.status = p.status;
+  ctl.limit_ns = p.wait_limit_ns;
+  ctl.late_clock = true;
+  const uint32_t op_smem = smem_addr(smem);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint32_t full0 = T::kPair ? cluster_smem_addr(smem_addr(op_full), 0) : smem_addr(op_full);
+      uint32_t it = 0;
+      bool ok = true;
+      FusedItems items(p, worker, workers);
+      FusedItem x;
+      while (ok && items.next(p, x)) {
+        const bool second = x.mb >= p.mb_second;
+        const int arow = (second ? x.mb - p.mb_second : x.mb) * T::kTile + (int)rank * T::BM;
+        for (int kb = x.kb0; kb < x.kb1; ++kb, ++it) {
+          const uint32_t st = it % T::kStages;
+          if (!mbar_wait(&op_empty[st], ((it / T::kStages) & 1u) ^ 1u, ctl)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&op_full[st], T::kCtas * T::kStage);
+          uint8_t* dst = smem + st * T::kStage;
+          const bool late = kb >= p.kb_second;
+          const int k0 = (late ? kb - p.kb_second : kb) * T::BK;
+          auto box = [&](const CUtensorMap* map, uint8_t* to, bool mn, int row) {
+            const int c0 = mn ? row : k0, c1 = mn ? k0 : row;
+            if constexpr (T::kPair) tma_load_3d_pair(to, map, full0 + st * 8u, c0, c1, 0);
+            else tma_load_3d(to, map, &op_full[st], c0, c1, 0);
+          };
+          const CUtensorMap* ma = &p.map_a[second || late ? 1 : 0];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) box(ma, dst + h * T::kHalf, p.a_mn_major != 0, arow + h * 64);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint8_t* to = dst + T::kATile + h * T::kHalf;
+            if constexpr (T::kTwo) {
+              // a pair: this CTA's 128 lines of one weight; one CTA: 64 of each
+              const int which = T::kPair ? (int)rank : h;
+              box(&p.map_b[which], to, false, x.nb * T::kTileN + (T::kPair ? h * 64 : 0));
+            } else {
+              box(&p.map_b[late ? 1 : 0], to, p.b_mn_major != 0, x.nb * T::kTile + (int)rank * 128 + h * 64);
+            }
+          }
+        }
+      }
+      // a stage is released after its copies landed and were read
+      const uint32_t n_drain = it < (uint32_t)T::kStages ? it : (uint32_t)T::kStages;
+      for (uint32_t i = it - n_drain; i < it; ++i)
+        drain_wait(&op_empty[i % T::kStages], (i / T::kStages) & 1u, p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (rank == 0) {
+      const bool leader = elect_one();
+      const bool a_mn = p.a_mn_major != 0, b_mn = p.b_mn_major != 0;
+      const uint32_t idesc = make_idesc(p.bf16 ? 1u : 0u, a_mn, b_mn, T::kTile, T::kTile);
+      // the start address sits in the descriptor's low bits, in units of 16 bytes
+      const uint64_t a_desc = operand_desc<T>(op_smem, a_mn, 0), b_desc = operand_desc<T>(op_smem + T::kATile, b_mn, 0);
+      const uint32_t a_step = (a_mn ? T::kInstrK * T::kRowBytes : 32) / 16, b_step = (b_mn ? T::kInstrK * T::kRowBytes : 32) / 16;
+      const uint32_t d_base = __shfl_sync(0xffffffffu, tmem_base, 0);
+      auto commit = [&](uint64_t* bar, uint16_t mask) {
+        if constexpr (T::kPair) mma_commit_multicast(bar, mask);
+        else mma_commit(bar);
+      };
+      uint32_t g = 0, st = 0, st_ph = 0;
+      bool ok = true;
+      FusedItems items(p, worker, workers);
+      FusedItem x;
+      for (; ok && items.next(p, x); ++g) {
+        const uint32_t ab = g % T::kAccBufs;
+        const uint32_t ph = ((g / T::kAccBufs) & 1u) ^ 1u;
+        if (!(T::kPair ? warp_wait_relaxed(&acc_empty[ab], ph, ctl) : warp_wait(&acc_empty[ab], ph, ctl))) { ok = false; break; }
+        tc_fence_after_sync();
+        const uint32_t d0 = d_base + ab * T::kTile;
+        for (int kb = x.kb0; kb < x.kb1; ++kb) {
+          if (!warp_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
+          tc_fence_after_sync();
+          const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+          if (leader) {
+#pragma unroll
+            for (int ks = 0; ks < T::kKSteps; ++ks) {
+              const uint64_t da = a_desc + at + ks * a_step, db = b_desc + at + ks * b_step;
+              const uint32_t acc = (kb > x.kb0 || ks > 0) ? 1u : 0u;
+              if constexpr (T::kPair) mma_f16_pair(d0, da, db, idesc, acc);
+              else mma_f16(d0, da, db, idesc, acc);
+            }
+            commit(&op_empty[st], 0x3);
+            if (kb + 1 == x.kb1) commit(&acc_full[ab], 0x3);
+          }
+          __syncwarp();
+          if (++st == T::kStages) {
+            st = 0;
+            st_ph ^= 1u;
+          }
+        }
+      }
+      // every MMA completes before TMEM is released
+      if (leader) {
+        commit(done_bar, 0x1);
+        drain_wait(done_bar, 0, p.wait_limit_ns);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    const int half = (warp - 2) / 4;
+    const uint32_t stg = smem_addr(epi_base) + (warp - 2) * 4096;
+    const uint32_t acc_empty0 = T::kPair ? cluster_smem_addr(smem_addr(acc_empty), 0) : 0u;
+    constexpr int kCc = T::kTileN / 32 / 2;         // 32-column chunks of one warp
+    const int cc0 = half * kCc;
+    const bool bf16 = p.bf16 != 0;
+    const Pow2 sc = warp_scale(p.scale, p.scale_exp);
+    uint32_t g = 0;
+    FusedItems items(p, worker, workers);
+    FusedItem x;
+    for (; items.next(p, x); ++g) {
+      const bool second = x.mb >= p.mb_second;
+      const uint32_t ab = g % T::kAccBufs;
+      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + ab * T::kTile;
+      const int row0 = (second ? x.mb - p.mb_second : x.mb) * T::kTile + (int)rank * T::BM + 32 * q;
+      const int row = row0 + lane;
+      const int col_tile = x.nb * T::kTileN;
+      auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          // (TMEM alone is handed over: a release would wait for the stores)
+          if constexpr (T::kPair) mbar_arrive_cluster_relaxed(acc_empty0 + ab * 8u);
+          else mbar_arrive(&acc_empty[ab]);
+        }
+      };
+      // what a row needs is fetched before the accumulator is waited for
+      int64_t target = -1;
+      float lse2 = 0.0f, weight = 0.0f;
+      if constexpr (T::kEpi == FusedEpi::kStats || T::kEpi == FusedEpi::kProb) {
+        if (row < p.m) {
+          target = target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, row);
+          if constexpr (T::kEpi == FusedEpi::kProb) {
+            lse2 = kLog2e * ld_global(p.lse + row);
+            // an ignored token has no gradient, whatever its dloss; one of no class gives NaN
+            weight = target == -1 ? 0.0f : target == -2 ? __int_as_float(0x7fffffff) : sc.mul * ld_global(p.dloss + (int64_t)row * p.dloss_stride);
+          }
+        }
+      }
+      if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
+      tc_fence_after_sync();
+
+      if constexpr (T::kTwo) {
+#pragma unroll 1
+        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
+          const int col0 = col_tile + cc * 32;
+          uint32_t dyw[16];
+          if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
+            if (row0 < p.m && col0 < p.n)
+              load_block16(stg, lane, dyw, p.dy, p.lddy, row0, p.m, col0, p.n, p.dy_vec != 0);
+          }
+          float gt[32], up[32];
+          tmem_ld_32cols(tacc + cc * 32, gt);
+          tmem_ld_32cols(tacc + T::kTile / 2 + cc * 32, up);
+          tmem_ld_wait();
+          if (cc == cc0 + kCc - 1) release();
+          if (row0 >= p.m || col0 >= p.n) continue;
+          auto store = [&](int i, auto value) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = pack16(value(2 * j), value(2 * j + 1), bf16);
+            store_block16(stg, lane, w, p.out[i], p.ldo[i], row0, p.m, col0, p.n, p.out_vec[i] != 0);
+          };
+          if constexpr (T::kEpi == FusedEpi::kGated) {
+            if (p.out[1]) {
+              store(1, [&](int j) { return gt[j]; });
+              store(2, [&](int j) { return up[j]; });
+            }
+            store(0, [&](int j) { return act_value(gt[j], p.act) * up[j]; });
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float2 y2 = unpack16(dyw[j >> 1], bf16);
+              const float dy = sc.mul * ((j & 1) ? y2.y : y2.x);
+              float a, d;
+              act_both(gt[j], p.act, a, d);
+              gt[j] = dy * up[j] * d;
+              up[j] = dy * a;
+            }
+            store(0, [&](int j) { return gt[j]; });
+            store(1, [&](int j) { return up[j]; });
+          }
+        }
+      } else if constexpr (T::kEpi == FusedEpi::kStats) {
+        float top = -INFINITY, sum = 0.0f;
+        const int last = p.n - col_tile;            // columns of the tile inside the matrix
+#pragma unroll 1
+        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
+          float v[32];
+          tmem_ld_32cols(tacc + cc * 32, v);
+          tmem_ld_wait();
+          if (cc == cc0 + kCc - 1) release();
+          if (cc * 32 >= last) continue;
+          // (a bit for the target's column: compared with its index, the values went to local memory)
+          const int64_t at = target - (p.col0 + col_tile + cc * 32);
+          const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
+          if (mine) {
+            float l = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) l = mine & (1u << j) ? v[j] : l;
+            p.target_logit[row] = l;
+          }
+          float here = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            v[j] = cc * 32 + j < last ? kLog2e * v[j] : -INFINITY;
+            here = fmaxf(here, v[j]);
+          }
+          // (a row of -infinities, or one that has +infinity, keeps its maximum and a sum of NaN-free terms)
+          const float base = fmaxf(top, here);
+          if (base == -INFINITY) {
+            bool nan = false;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) nan = nan || v[j] != v[j];
+            if (nan) sum = NAN;
+            continue;
+          }
+          const float b = base == INFINITY ? 0.0f : base;
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            s0 += ex2(v[j] - b);
+            s1 += ex2(v[j + 1] - b);
+          }
+          sum = (top == -INFINITY ? sum : sum * ex2(top - b)) + (s0 + s1);
+          top = base;
+        }
+        if (row < p.m) p.stats[(int64_t)(x.nb * 2 + half) * p.m + row] = make_float2(top, sum);
+      } else if constexpr (T::kEpi == FusedEpi::kProb) {
+#pragma unroll 1
+        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
+          float v[32];
+          tmem_ld_32cols(tacc + cc * 32, v);
+          tmem_ld_wait();
+          if (cc == cc0 + kCc - 1) release();
+          const int col0 = col_tile + cc * 32;
+          if (row0 >= p.m || col0 >= p.n) continue;
+          const int64_t at = target - (p.col0 + col0);
+          const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
+          const bool any = __any_sync(0xffffffffu, mine != 0u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(kLog2e, v[j], -lse2));
+          if (any) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = mine & (1u << j) ? v[j] - 1.0f : v[j];
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = weight == 0.0f ? 0u : pack16(weight * v[2 * j], weight * v[2 * j + 1], bf16);
+          store_block16(stg, lane, w, p.out[0], p.ldo[0], row0, p.m, col0, p.n, p.out_vec[0] != 0);
+        }
+      } else {
+        const int dt = p.out_dtype;
+        const bool part = x.slot >= 0;
+        void* out = p.out[second ? 1 : 0];
+        const int64_t ldo = p.ldo[second ? 1 : 0];
+        const bool vec = p.out_vec[second ? 1 : 0] != 0;
+        float* slot = p.slots + (int64_t)max(x.slot, 0) * (T::kTile * T::kTile);
+#pragma unroll 1
+        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
+          float v[32];
+          tmem_ld_32cols(tacc + cc * 32, v);
+          tmem_ld_wait();
+          if (cc == cc0 + kCc - 1) release();
+          const int col0 = col_tile + cc * 32;
+          if (row0 >= p.m || col0 >= p.n) continue;
+          if (part) {
+            // sums of a part of k, as they are: rows of the tile, whole lines a store
+            stage_write_row(stg, lane, v);
+            __syncwarp();
+            float* to = slot + (int64_t)((int)rank * T::BM + 32 * q) * T::kTile + cc * 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(to + (i * 4 + (lane >> 3)) * T::kTile + (lane & 7) * 4) = stage_read_chunk(stg, lane, i);
+            __syncwarp();
+            continue;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= sc.inv;
+          if (dt != kOutF32 && !p.add) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], dt == kOutBF16);
+            store_block16(stg, lane, w, out, ldo, row0, p.m, col0, p.n, vec);
+            continue;
+          }
+          stage_write_row(stg, lane, v);
+          __syncwarp();
+          // (add has lines of whole 16-byte chunks)
+          if (vec && col0 + 32 <= p.n) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = row0 + i * 4 + (lane >> 3), c = col0 + (lane & 7) * 4;
+              float4 o = stage_read_chunk(stg, lane, i);
+              if (r < p.m) {
+                if (p.add) {
+                  const float4 y = out_load4(p.add, (int64_t)r * p.ldadd + c, kOutF32);
+                  o.x += y.x;
+                  o.y += y.y;
+                  o.z += y.z;
+                  o.w += y.w;
+                }
+                out_store4(out, (int64_t)r * ldo + c, o, dt);
+              }
+            }
+          } else if (col0 + lane < p.n) {
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r) {
+              float o = stage_read_elem(stg, lane, r);
+              if (row0 + r < p.m) {
+                if (p.add) o += out_load(p.add, (int64_t)(row0 + r) * p.ldadd + col0 + lane, kOutF32);
+                out_store(out, (int64_t)(row0 + r) * ldo + col0 + lane, o, dt);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+
+  // neither CTA of a pair leaves while the other may address its shared memory
+  __syncwarp();
+  tc_fence_before_sync();
+  if constexpr (T::kPair) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    if constexpr (T::kPair) tmem_dealloc_pair(tmem_base, T::kTmemCols);
+    else tmem_dealloc(tmem_base, T::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// split tiles
+// ---------------------------------------------------------------------------
+// Adds a tile's parts in the order of k: four columns a thread, sixteen rows a
+// block.  Tiles that one worker had whole are done already.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(256) fused_join_kernel(const __grid_constant__ FusedGemmParams p, int tile, int workers) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const Pow2 sc = warp_scale(p.scale, p.scale_exp);
+  const int64_t u0 = (int64_t)blockIdx.x * p.num_k_blk, u1 = u0 + p.num_k_blk;
+  int w0 = (int)min((int64_t)workers - 1, u0 * workers / p.units);
+  while (w0 > 0 && first_unit(p.units, w0, workers) > u0) --w0;
+  while (first_unit(p.units, w0 + 1, workers) <= u0) ++w0;
+  if (first_unit(p.units, w0 + 1, workers) >= u1) return;
+  const FusedTile tc = fused_tile(p, p.whole_tiles + (int)blockIdx.x);
+  const bool second = tc.mb >= p.mb_second;
+  void* out = p.out[second ? 1 : 0];
+  const int64_t ldo = p.ldo[second ? 1 : 0];
+  const bool vec = p.out_vec[second ? 1 : 0] != 0;
+  const int per_row = tile / 4;
+  for (int i = threadIdx.x; i < kJoinRows * per_row; i += 256) {
+    const int r = blockIdx.y * kJoinRows + i / per_row, c = i % per_row * 4;
+    const int row = (second ? tc.mb - p.mb_second : tc.mb) * tile + r, col = tc.nb * tile + c;
+    if (row >= p.m || col >= p.n) continue;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int w = w0; w < workers; ++w) {
+      const int64_t a = first_unit(p.units, w, workers), b = first_unit(p.units, w + 1, workers);
+      if (a >= u1) break;
+      if (a == b) continue;
+      const int slot = 2 * w + (a >= u0 ? 0 : 1);   // (a run that starts in an earlier tile has this one second)
+      const uint4 y = ld_global(reinterpret_cast<const uint4*>(p.slots + ((int64_t)slot * tile + r) * tile + c));
+      o.x += __uint_as_float(y.x);
+      o.y += __uint_as_float(y.y);
+      o.z += __uint_as_float(y.z);
+      o.w += __uint_as_float(y.w);
+    }
+    o.x *= sc.inv;
+    o.y *= sc.inv;
+    o.z *= sc.inv;
+    o.w *= sc.inv;
+    if (vec && col + 4 <= p.n) {
+      if (p.add) {
+        const float4 y = out_load4(p.add, (int64_t)row * p.ldadd + col, kOutF32);
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+      }
+      out_store4(out, (int64_t)row * ldo + col, o, p.out_dtype);
+    } else {
+      const float e[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col + j < p.n)
+          out_store(out, (int64_t)row * ldo + col + j,
+                    p.add ? e[j] + out_load(p.add, (int64_t)row * p.ldadd + col + j, kOutF32) : e[j], p.out_dtype);
+    }
+  }
+}
+
+template <FusedEpi E>
+void fill(bool pair, FusedKernel* out) {
+  using One = FusedTraits<E, false>;
+  using Two = FusedTraits<E, true>;
+  out->fn = pair ? reinterpret_cast<const void*>(&fused_gemm_kernel<Two>) : reinterpret_cast<const void*>(&fused_gemm_kernel<One>);
+  out->block = Two::kThreads;
+  out->smem_bytes = pair ? Two::kSmemBytes : One::kSmemBytes;
+  out->tile = pair ? Two::kTile : One::kTile;
+  out->ctas = pair ? 2 : 1;
+}
+
+}  // namespace
+
+void fused_lookup(FusedEpi epi, bool pair, FusedKernel* out) {
+  switch (epi) {
+    case FusedEpi::kPlain: fill<FusedEpi::kPlain>(pair, out); break;
+    case FusedEpi::kGated: fill<FusedEpi::kGated>(pair, out); break;
+    case FusedEpi::kGatedGrad: fill<FusedEpi::kGatedGrad>(pair, out); break;
+    case FusedEpi::kStats: fill<FusedEpi::kStats>(pair, out); break;
+    case FusedEpi::kProb: fill<FusedEpi::kProb>(pair, out); break;
+  }
+}
+
+cudaError_t launch_fused_join(const FusedGemmParams& p, int tile, int workers, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.num_tiles - p.whole_tiles), (unsigned)(tile / kJoinRows));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  cfg.numAttrs = (unsigned)launch_attributes(attr, 1);
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, fused_join_kernel, p, tile, workers);
+}
+
+}  // namespace mpg

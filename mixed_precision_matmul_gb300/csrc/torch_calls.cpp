@@ -16,6 +16,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <vector>
+
 #include "mpgemm.h"
 
 namespace {
@@ -23,6 +25,16 @@ namespace {
 decltype(&mpg_gemm_fp8) g_gemm = nullptr;
 decltype(&mpg_gemm_fp8_workspace_size) g_gemm_workspace = nullptr;
 decltype(&mpg_fp8_quantize) g_quantize = nullptr;
+decltype(&mpg_gated_gemm) g_gated = nullptr;
+decltype(&mpg_gated_gemm_workspace_size) g_gated_workspace = nullptr;
+decltype(&mpg_gated_gemm_backward) g_gated_back = nullptr;
+decltype(&mpg_gated_gemm_backward_workspace_size) g_gated_back_workspace = nullptr;
+decltype(&mpg_linear_cross_entropy) g_loss = nullptr;
+decltype(&mpg_linear_cross_entropy_workspace_size) g_loss_workspace = nullptr;
+decltype(&mpg_linear_cross_entropy_backward) g_loss_back = nullptr;
+decltype(&mpg_linear_cross_entropy_backward_workspace_size) g_loss_back_workspace = nullptr;
+decltype(&mpg_clip_grad_norm) g_clip = nullptr;
+decltype(&mpg_clip_grad_norm_workspace_size) g_clip_workspace = nullptr;
 mpg_options g_options[3];
 
 constexpr int64_t kBlock = 128;
@@ -57,10 +69,22 @@ bool operand(PyObject* po, PyObject* ps, c10::DeviceIndex dev, at::Tensor* t, at
 }
 
 PyObject* init(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 3) return PyErr_Format(PyExc_TypeError, "three addresses are expected");
-  g_gemm = reinterpret_cast<decltype(g_gemm)>(PyLong_AsVoidPtr(args[0]));
-  g_gemm_workspace = reinterpret_cast<decltype(g_gemm_workspace)>(PyLong_AsVoidPtr(args[1]));
-  g_quantize = reinterpret_cast<decltype(g_quantize)>(PyLong_AsVoidPtr(args[2]));
+  if (n != 13) return PyErr_Format(PyExc_TypeError, "thirteen addresses are expected");
+  int i = 0;
+  auto take = [&](auto& f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(PyLong_AsVoidPtr(args[i++])); };
+  take(g_gemm);
+  take(g_gemm_workspace);
+  take(g_quantize);
+  take(g_gated);
+  take(g_gated_workspace);
+  take(g_gated_back);
+  take(g_gated_back_workspace);
+  take(g_loss);
+  take(g_loss_workspace);
+  take(g_loss_back);
+  take(g_loss_back_workspace);
+  take(g_clip);
+  take(g_clip_workspace);
   if (PyErr_Occurred()) return nullptr;
   for (int i = 0; i < 3; ++i) {
     g_options[i] = mpg_options{};
@@ -154,10 +178,240 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
+// A 16-bit matrix of the given type on device `dev` (rows, cols: -1 for any).
+bool matrix16(PyObject* o, c10::DeviceIndex dev, at::ScalarType type, int64_t rows, int64_t cols, at::Tensor* t, int64_t* ld) {
+  if (!tensor(o, t) || t->get_device() != dev || t->scalar_type() != type) return false;
+  const int64_t r = t->size(0), c = t->size(1);
+  if (r < 1 || c < 1 || (rows >= 0 && r != rows) || (cols >= 0 && c != cols)) return false;
+  if ((c > 1 && t->stride(1) != 1) || (r > 1 && t->stride(0) < c)) return false;
+  *ld = r > 1 ? t->stride(0) : c;
+  return true;
+}
+at::Tensor scratch(size_t bytes, const at::Tensor& like) { return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte)); }
+void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// The first `n` of a call's results (None for one that is not there).
+PyObject* results(at::Tensor* t, int n) {
+  PyObject* r = PyTuple_New(n);
+  if (!r) return nullptr;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].defined()) {
+      PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(t[i])));
+    } else {
+      Py_INCREF(Py_None);
+      PyTuple_SET_ITEM(r, i, Py_None);
+    }
+  }
+  return r;
+}
+
+// X, Wg and Wu of a layer; false unless plain ones on the current device.
+bool layer_of(PyObject* px, PyObject* pg, PyObject* pu, long act, at::Tensor* x, at::Tensor* wg, at::Tensor* wu,
+              c10::DeviceIndex* dev, mpg_gated_layer* l) {
+  if (!tensor(px, x)) return false;
+  *dev = c10::cuda::current_device();
+  const at::ScalarType type = x->scalar_type();
+  if (type != at::kHalf && type != at::kBFloat16) return false;
+  if (!matrix16(px, *dev, type, -1, -1, x, &l->ldx) || !matrix16(pg, *dev, type, -1, x->size(1), wg, &l->ldwg) ||
+      !matrix16(pu, *dev, type, wg->size(0), x->size(1), wu, &l->ldwu))
+    return false;
+  l->tokens = x->size(0);
+  l->hidden = x->size(1);
+  l->inner = wg->size(0);
+  l->dtype = type == at::kHalf ? MPG_F16 : MPG_BF16;
+  l->act = (mpg_activation)act;
+  l->x = x->data_ptr();
+  l->wg = wg->data_ptr();
+  l->wu = wu->data_ptr();
+  return true;
+}
+
+// (x, wg, wu, activation, keep) -> y or (y, g, u)
+PyObject* gated_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 5 || !g_gated) return PyErr_Format(PyExc_TypeError, "five arguments are expected");
+  try {
+    const long act = PyLong_AsLong(args[3]);
+    const int keep = PyObject_IsTrue(args[4]);
+    if (PyErr_Occurred()) return nullptr;
+    at::Tensor x, wg, wu, out[3];
+    c10::DeviceIndex dev;
+    mpg_gated_layer l;
+    if (!layer_of(args[0], args[1], args[2], act, &x, &wg, &wu, &dev, &l)) Py_RETURN_NONE;
+    for (int i = 0; i < (keep ? 3 : 1); ++i) out[i] = at::empty({l.tokens, l.inner}, x.options());
+    const size_t bytes = g_gated_workspace(&l);
+    const at::Tensor ws = bytes ? scratch(bytes, x) : at::Tensor();
+    const mpg_status st = g_gated(&l, address(out[0]), l.inner, address(out[1]), l.inner, address(out[2]), l.inner,
+                                  address(ws), bytes, c10::cuda::getCurrentCUDAStream(dev).stream());
+    if (st != MPG_OK) return PyLong_FromLong(st);
+    return keep ? results(out, 3) : THPVariable_Wrap(std::move(out[0]));
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+  }
+}
+
+// (dy, x, wg, wu, activation, g, u, need_dx, need_dw) -> (dx, dwg, dwu)
+PyObject* gated_gemm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 9 || !g_gated_back) return PyErr_Format(PyExc_TypeError, "nine arguments are expected");
+  try {
+    const long act = PyLong_AsLong(args[4]);
+    const int need_dx = PyObject_IsTrue(args[7]), need_dw = PyObject_IsTrue(args[8]);
+    if (PyErr_Occurred()) return nullptr;
+    at::Tensor dy, x, wg, wu, g, u, out[3];
+    c10::DeviceIndex dev;
+    mpg_gated_layer l;
+    int64_t lddy = 0, ldg = 0, ldu = 0;
+    if (!layer_of(args[1], args[2], args[3], act, &x, &wg, &wu, &dev, &l)) Py_RETURN_NONE;
+    if (!matrix16(args[0], dev, x.scalar_type(), l.tokens, l.inner, &dy, &lddy)) Py_RETURN_NONE;
+    if (args[5] != Py_None || args[6] != Py_None)
+      if (!matrix16(args[5], dev, x.scalar_type(), l.tokens, l.inner, &g, &ldg) ||
+          !matrix16(args[6], dev, x.scalar_type(), l.tokens, l.inner, &u, &ldu))
+        Py_RETURN_NONE;
+    if (need_dx) out[0] = at::empty({l.tokens, l.hidden}, x.options());
+    for (int i = 1; i < 3 && need_dw; ++i) out[i] = at::empty({l.inner, l.hidden}, x.options());
+    const size_t bytes = g_gated_back_workspace(&l);
+    const at::Tensor ws = bytes ? scratch(bytes, x) : at::Tensor();
+    const mpg_status st = g_gated_back(&l, address(dy), lddy, address(g), ldg, address(u), ldu, address(out[0]), l.hidden,
+                                       address(out[1]), l.hidden, address(out[2]), l.hidden, address(ws), bytes,
+                                       c10::cuda::getCurrentCUDAStream(dev).stream());
+    return st == MPG_OK ? results(out, 3) : PyLong_FromLong(st);
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+  }
+}
+
+// X, W and the targets; false unless plain ones on the current device.
+bool loss_of(PyObject* px, PyObject* pw, PyObject* pt, PyObject* ignore, at::Tensor* x, at::Tensor* w, at::Tensor* t,
+             c10::DeviceIndex* dev, mpg_vocab_loss* l) {
+  if (!tensor(px, x) || !THPVariable_Check(pt)) return false;
+  *dev = c10::cuda::current_device();
+  const at::ScalarType type = x->scalar_type();
+  if (type != at::kHalf && type != at::kBFloat16) return false;
+  if (!matrix16(px, *dev, type, -1, -1, x, &l->ldx) || !matrix16(pw, *dev, type, -1, x->size(1), w, &l->ldw)) return false;
+  *t = THPVariable_Unpack(pt);
+  if (!t->is_cuda() || t->layout() != at::kStrided || t->get_device() != *dev || t->dim() != 1 || t->size(0) != x->size(0)) return false;
+  if (t->scalar_type() != at::kLong && t->scalar_type() != at::kInt) return false;
+  l->tokens = x->size(0);
+  l->hidden = x->size(1);
+  l->vocab = w->size(0);
+  l->dtype = type == at::kHalf ? MPG_F16 : MPG_BF16;
+  l->x = x->data_ptr();
+  l->w = w->data_ptr();
+  l->target = t->data_ptr();
+  l->target_bytes = t->scalar_type() == at::kLong ? 8 : 4;
+  l->target_stride = t->stride(0);
+  l->ignore_index = PyLong_AsLongLong(ignore);
+  return true;
+}
+
+// (x, w, target, ignore_index) -> (loss, lse)
+PyObject* linear_cross_entropy(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 4 || !g_loss) return PyErr_Format(PyExc_TypeError, "four arguments are expected");
+  try {
+    at::Tensor x, w, t, out[2];
+    c10::DeviceIndex dev;
+    mpg_vocab_loss l;
+    if (!loss_of(args[0], args[1], args[2], args[3], &x, &w, &t, &dev, &l)) Py_RETURN_NONE;
+    if (PyErr_Occurred()) return nullptr;
+    for (at::Tensor& o : out) o = at::empty({l.tokens}, x.options().dtype(at::kFloat));
+    const size_t bytes = g_loss_workspace(&l);
+    const at::Tensor ws = bytes ? scratch(bytes, x) : at::Tensor();
+    const mpg_status st = g_loss(&l, static_cast<float*>(out[0].data_ptr()), static_cast<float*>(out[1].data_ptr()),
+                                 address(ws), bytes, c10::cuda::getCurrentCUDAStream(dev).stream());
+    return st == MPG_OK ? results(out, 2) : PyLong_FromLong(st);
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+  }
+}
+
+// One fp32 number for each of `tokens` on device `dev`.
+bool vector32(PyObject* o, c10::DeviceIndex dev, int64_t tokens, at::Tensor* t) {
+  if (!THPVariable_Check(o)) return false;
+  *t = THPVariable_Unpack(o);
+  return t->is_cuda() && t->layout() == at::kStrided && t->get_device() == dev && t->dim() == 1 && t->size(0) == tokens &&
+         t->scalar_type() == at::kFloat;
+}
+
+// (x, w, target, lse, dloss, ignore_index, need_dx, need_dw) -> (dx, dw)
+PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 8 || !g_loss_back) return PyErr_Format(PyExc_TypeError, "eight arguments are expected");
+  try {
+    const int need_dx = PyObject_IsTrue(args[6]), need_dw = PyObject_IsTrue(args[7]);
+    if (PyErr_Occurred()) return nullptr;
+    at::Tensor x, w, t, lse, dloss, out[2];
+    c10::DeviceIndex dev;
+    mpg_vocab_loss l;
+    if (!loss_of(args[0], args[1], args[2], args[5], &x, &w, &t, &dev, &l)) Py_RETURN_NONE;
+    if (PyErr_Occurred()) return nullptr;
+    if (!vector32(args[3], dev, l.tokens, &lse) || !vector32(args[4], dev, l.tokens, &dloss) ||
+        (l.tokens > 1 && lse.stride(0) != 1))
+      Py_RETURN_NONE;
+    if (need_dx) out[0] = at::empty({l.tokens, l.hidden}, x.options());
+    if (need_dw) out[1] = at::empty({l.vocab, l.hidden}, x.options());
+    const size_t bytes = g_loss_back_workspace(&l);
+    const at::Tensor ws = bytes ? scratch(bytes, x) : at::Tensor();
+    const mpg_status st = g_loss_back(&l, static_cast<const float*>(lse.data_ptr()), static_cast<const float*>(dloss.data_ptr()),
+                                      dloss.stride(0), address(out[0]), l.hidden, address(out[1]), l.hidden, address(ws),
+                                      bytes, c10::cuda::getCurrentCUDAStream(dev).stream());
+    return st == MPG_OK ? results(out, 2) : PyLong_FromLong(st);
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+  }
+}
+
+// A gradient and its result, packed alike; false for anything else.
+bool grad_of(PyObject* pg, PyObject* po, c10::DeviceIndex dev, mpg_grad* x) {
+  if (!THPVariable_Check(pg) || !THPVariable_Check(po)) return false;
+  const at::Tensor &g = THPVariable_Unpack(pg), &o = THPVariable_Unpack(po);
+  for (const at::Tensor* t : {&g, &o})
+    if (!t->is_cuda() || t->layout() != at::kStrided || t->get_device() != dev || !t->is_contiguous()) return false;
+  if (g.sizes() != o.sizes()) return false;
+  int tg = 0, to = 0;
+  while (tg < 3 && g.scalar_type() != kTypes[tg]) ++tg;
+  while (to < 3 && o.scalar_type() != kTypes[to]) ++to;
+  if (tg == 3 || to == 3) return false;
+  *x = mpg_grad{g.data_ptr(), o.data_ptr(), g.numel(), (mpg_dtype)tg, (mpg_dtype)to};
+  return true;
+}
+
+// (gradients, results, max_norm, eps) -> norm; both lists or tuples of one length
+PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 4 || !g_clip) return PyErr_Format(PyExc_TypeError, "four arguments are expected");
+  try {
+    const double max_norm = PyFloat_AsDouble(args[2]), eps = PyFloat_AsDouble(args[3]);
+    if (PyErr_Occurred()) return nullptr;
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(args[0]);
+    if (count < 1 || PySequence_Fast_GET_SIZE(args[1]) != count) Py_RETURN_NONE;
+    PyObject* first = PySequence_Fast_GET_ITEM(args[0], 0);
+    if (!THPVariable_Check(first) || !THPVariable_Unpack(first).is_cuda()) Py_RETURN_NONE;
+    const c10::DeviceIndex dev = c10::cuda::current_device();
+    std::vector<mpg_grad> table((size_t)count);
+    for (Py_ssize_t i = 0; i < count; ++i)
+      if (!grad_of(PySequence_Fast_GET_ITEM(args[0], i), PySequence_Fast_GET_ITEM(args[1], i), dev, &table[(size_t)i]))
+        Py_RETURN_NONE;
+    const at::TensorOptions o = at::TensorOptions().device(at::kCUDA, dev);
+    at::Tensor norm = at::empty({}, o.dtype(at::kFloat));
+    const size_t bytes = g_clip_workspace(count, table.data());
+    const at::Tensor ws = at::empty({(int64_t)bytes}, o.dtype(at::kByte));
+    const mpg_status st = g_clip(count, table.data(), (float)max_norm, (float)eps, static_cast<float*>(norm.data_ptr()),
+                                 ws.data_ptr(), bytes, c10::cuda::getCurrentCUDAStream(dev).stream());
+    return st == MPG_OK ? THPVariable_Wrap(std::move(norm)) : PyLong_FromLong(st);
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+  }
+}
+
 PyMethodDef g_methods[] = {
     {"init", reinterpret_cast<PyCFunction>(init), METH_FASTCALL, "addresses of the C ABI's functions"},
     {"gemm_fp8", reinterpret_cast<PyCFunction>(gemm_fp8), METH_FASTCALL, "mpg_gemm_fp8 on torch tensors"},
     {"quantize", reinterpret_cast<PyCFunction>(quantize), METH_FASTCALL, "mpg_fp8_quantize on torch tensors"},
+    {"gated_gemm", reinterpret_cast<PyCFunction>(gated_gemm), METH_FASTCALL, "mpg_gated_gemm on torch tensors"},
+    {"gated_gemm_backward", reinterpret_cast<PyCFunction>(gated_gemm_backward), METH_FASTCALL,
+     "mpg_gated_gemm_backward on torch tensors"},
+    {"linear_cross_entropy", reinterpret_cast<PyCFunction>(linear_cross_entropy), METH_FASTCALL,
+     "mpg_linear_cross_entropy on torch tensors"},
+    {"linear_cross_entropy_backward", reinterpret_cast<PyCFunction>(linear_cross_entropy_backward), METH_FASTCALL,
+     "mpg_linear_cross_entropy_backward on torch tensors"},
+    {"clip_grad_norm", reinterpret_cast<PyCFunction>(clip_grad_norm), METH_FASTCALL, "mpg_clip_grad_norm on torch tensors"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

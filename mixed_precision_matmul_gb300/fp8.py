@@ -42,7 +42,12 @@ def _calls():
         warnings.warn(f"8-bit calls are marshalled in Python, build() makes the extension: {e}", RuntimeWarning)
         return None
     module.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                  for f in (lib.mpg_gemm_fp8, lib.mpg_gemm_fp8_workspace_size, lib.mpg_fp8_quantize)))
+                  for f in (lib.mpg_gemm_fp8, lib.mpg_gemm_fp8_workspace_size, lib.mpg_fp8_quantize, lib.mpg_gated_gemm,
+                            lib.mpg_gated_gemm_workspace_size, lib.mpg_gated_gemm_backward,
+                            lib.mpg_gated_gemm_backward_workspace_size, lib.mpg_linear_cross_entropy,
+                            lib.mpg_linear_cross_entropy_workspace_size, lib.mpg_linear_cross_entropy_backward,
+                            lib.mpg_linear_cross_entropy_backward_workspace_size, lib.mpg_clip_grad_norm,
+                            lib.mpg_clip_grad_norm_workspace_size)))
     return module
 
 
