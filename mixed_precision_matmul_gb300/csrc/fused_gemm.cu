@@ -268,7 +268,6 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
   if constexpr (T::kPair) ctl.peer_abort = cluster_generic_ptr(const_cast<int*>(abort_flag), rank ^ 1u);
   ctl.status = p.status;
   ctl.limit_ns = p.wait_limit_ns;
-  ctl.late_clock = true;
   const uint32_t op_smem = smem_addr(smem);
 
   if (warp == 0) {
