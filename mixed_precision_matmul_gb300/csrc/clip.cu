@@ -5,13 +5,15 @@
 // Two passes over the gradients, bound by memory: 2 reads and a write of each
 // (the norm has to be known before the first element is scaled).  The second
 // pass walks them backwards, so that what the first one read last is still in
-// L2 (129 MB).  Tensors are cut into chunks of 8192 elements, numbered through
-// over all of them; a launch's parameters hold the table of its tensors.
+// L2 (129 MB).  Tensors are cut into chunks, numbered through over all of them,
+// and a block takes a run of chunks; a launch's parameters hold the table of its
+// tensors.  A thread has four loads of eight elements on their way.
 //
-// Squares: a thread sums eight in fp32 and the threads' sums are carried in 64
-// bits.  fp32 cannot hold the square of what is below 2^-63 or above 2^64; eight
-// elements whose sum leaves [2^-90, 2^120] are summed in 64 bits instead (all
-// zeros apart, which need no sum).
+// Squares: a thread sums 32 in fp32 and carries the sums in 64 bits (a sum of
+// eight at a time was bound by the 64-bit adder: 1.0e9 bf16 gradients 483 us).
+// fp32 cannot hold the square of what is below 2^-63 or above 2^64; elements
+// whose sum leaves [2^-90, 2^120] are squared in 64 bits instead (all zeros
+// apart, which need no sum).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -25,8 +27,9 @@ namespace mpg {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipChunk = 8192;       // elements
-constexpr int kClipBlocks = 608;       // 4 to an SM
+constexpr int kClipStep = kClipThreads * 8;       // elements that a block loads at once
+constexpr int kClipBatch = 4;                     // such loads on their way
+constexpr int kClipBlocks = 608;                  // 4 to an SM
 struct ClipTensor {
   const void* g;
   void* out;
@@ -40,6 +43,7 @@ struct ClipParams {
   int32_t partials;                    // all of them
   int32_t count;
   uint32_t chunks;
+  int32_t chunk;                       // elements of a chunk
   float max_norm, eps;
   float* norm;                         // written by this launch, or null
   ClipTensor tensor[kMost];
@@ -47,6 +51,7 @@ struct ClipParams {
 constexpr int kClipFew = 64, kClipMany = 896;
 static_assert(sizeof(ClipParams<kClipMany>) <= 32764, "kernel parameters");
 
+// The tensor of a chunk.
 template <int kMost>
 __device__ __forceinline__ int tensor_of(const ClipParams<kMost>& p, uint32_t chunk) {
   int lo = 0, hi = p.count - 1;
@@ -56,6 +61,10 @@ __device__ __forceinline__ int tensor_of(const ClipParams<kMost>& p, uint32_t ch
     else hi = mid - 1;
   }
   return lo;
+}
+// The first chunk of block b's run.
+__device__ __forceinline__ uint32_t first_chunk(uint32_t chunks, uint32_t b, uint32_t blocks) {
+  return (uint32_t)((uint64_t)chunks * b / blocks);
 }
 
 // Eight elements from i on (0 beyond the end).
@@ -83,22 +92,22 @@ __device__ __forceinline__ void load_eight(float (&v)[8], const void* base, int6
   }
 }
 
-__device__ __forceinline__ double eight_squares(const float (&v)[8]) {
-  float a = 0.0f, b = 0.0f;
+template <int kN>
+__device__ __forceinline__ double squares(const float (&v)[kN]) {
+  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    a = fmaf(v[j], v[j], a);
-    b = fmaf(v[j + 1], v[j + 1], b);
-  }
-  const float s = a + b;
+  for (int j = 0; j < kN; ++j) a[j % 4] = fmaf(v[j], v[j], a[j % 4]);
+  const float s = (a[0] + a[1]) + (a[2] + a[3]);
   if (s >= 8.0779357e-28f && s <= 1.329228e36f) return (double)s;    // [2^-90, 2^120]
   float any = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) any = fmaxf(any, fabsf(v[j]));
+  for (int j = 0; j < kN; ++j) any = fmaxf(any, fabsf(v[j]));
   if (any == 0.0f && s == 0.0f) return 0.0;
   double d = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < kN; j += 8)
 #pragma unroll
-  for (int j = 0; j < 8; ++j) d = fma((double)v[j], (double)v[j], d);
+    for (int k = 0; k < 8; ++k) d = fma((double)v[j + k], (double)v[j + k], d);
   return d;
 }
 
@@ -112,28 +121,81 @@ __device__ __forceinline__ double block_sum(double x, double* warps) {
   return x;
 }
 
+// Four times eight elements of a thread: raw 16-byte words on their way together.
+template <int kType>
+struct Batch {
+  static constexpr int kWords = kType == kOutF32 ? 2 : 1;
+  uint4 w[kClipBatch][kWords];
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+#pragma unroll
+    for (int j = 0; j < kClipBatch; ++j) {
+      const uint4* at = kType == kOutF32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i + j * kClipStep)
+                                         : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i + j * kClipStep);
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) w[j][k] = ld_global(at + k);
+    }
+  }
+  __device__ __forceinline__ void values(int j, float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const uint32_t x[4] = {w[j][k].x, w[j][k].y, w[j][k].z, w[j][k].w};
+#pragma unroll
+      for (int l = 0; l < 4; ++l) {
+        if constexpr (kType == kOutF32) {
+          v[4 * k + l] = __uint_as_float(x[l]);
+        } else {
+          const float2 y = unpack16(x[l], kType == kOutBF16);
+          v[2 * l] = y.x;
+          v[2 * l + 1] = y.y;
+        }
+      }
+    }
+  }
+};
+
+// whole(i, v) for batches (eight elements from i on, eight from i + kClipStep ..)
+// and f(i, v) for eight elements v from i on, of what lies in i0 .. end.
+template <class W, class F>
+__device__ __forceinline__ void for_chunk(const void* g, int type, bool vec, int64_t i0, int64_t end, W&& whole, F&& f) {
+  int64_t i = i0 + (int64_t)threadIdx.x * 8;
+  auto batches = [&](auto batch) {
+    for (; i - threadIdx.x * 8 + kClipBatch * kClipStep <= end; i += kClipBatch * kClipStep) {
+      batch.load(g, i);
+      whole(i, batch);
+    }
+  };
+  if (vec) {
+    if (type == kOutF32) batches(Batch<kOutF32>());
+    else if (type == kOutF16) batches(Batch<kOutF16>());
+    else batches(Batch<kOutBF16>());
+  }
+  for (; i < end; i += kClipStep) {
+    float v[8];
+    load_eight(v, g, i, end, type, vec);
+    f(i, v);
+  }
+}
+
 template <int kMost>
 __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_constant__ ClipParams<kMost> p) {
   __shared__ double warps[kClipThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
   double sum = 0.0;
-  for (uint32_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-    const ClipTensor& t = p.tensor[tensor_of(p, c)];
-    const int64_t i0 = (int64_t)(c - t.first) * kClipChunk;
-    const void* g = t.g;
-    const int64_t count = t.count;
-    const int type = t.g_type;
-    const bool vec = t.vec & 1;
-#pragma unroll 4
-    for (int j = 0; j < kClipChunk / 8 / kClipThreads; ++j) {
-      const int64_t i = i0 + (j * kClipThreads + (int)threadIdx.x) * 8;
-      if (i < count) {
-        float v[8];
-        load_eight(v, g, i, count, type, vec);
-        sum += eight_squares(v);
-      }
-    }
+  uint32_t c = first_chunk(p.chunks, blockIdx.x, gridDim.x);
+  const uint32_t last = first_chunk(p.chunks, blockIdx.x + 1, gridDim.x);
+  for (int k = tensor_of(p, c); c < last; ++k) {
+    const ClipTensor& t = p.tensor[k];
+    const uint32_t next = k + 1 < p.count ? min(last, p.tensor[k + 1].first) : last;
+    for_chunk(t.g, t.g_type, t.vec & 1, (int64_t)(c - t.first) * p.chunk, min(t.count, (int64_t)(next - t.first) * p.chunk),
+              [&](int64_t, const auto& batch) {
+                float v[8 * kClipBatch];
+#pragma unroll
+                for (int j = 0; j < kClipBatch; ++j) batch.values(j, *reinterpret_cast<float(*)[8]>(v + 8 * j));
+                sum += squares(v);
+              },
+              [&](int64_t, const float (&v)[8]) { sum += squares(v); });
+    c = next;
   }
   sum = block_sum(sum, warps);
   if (threadIdx.x == 0) p.partial[blockIdx.x] = sum;
@@ -152,40 +214,54 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
   float f = p.max_norm / (norm + p.eps);
   if (f >= 1.0f) f = 1.0f;                                  // (a NaN stays)
-  for (uint32_t n = blockIdx.x; n < p.chunks; n += gridDim.x) {
-    const uint32_t c = p.chunks - 1 - n;
-    const ClipTensor& t = p.tensor[tensor_of(p, c)];
-    const int64_t i0 = (int64_t)(c - t.first) * kClipChunk;
+  const uint32_t first = first_chunk(p.chunks, blockIdx.x, gridDim.x);
+  uint32_t c = first_chunk(p.chunks, blockIdx.x + 1, gridDim.x);
+  if (first == c) return;
+  // the run backwards: chunks of the batch's length
+  for (int k = tensor_of(p, c - 1); c > first; --k) {
+    const ClipTensor& t = p.tensor[k];
     const void* g = t.g;
     void* out = t.out;
-    const int64_t count = t.count;
     const int type = t.g_type, out_type = t.out_type;
     const bool vec = t.vec & 1, out_vec = t.vec & 2;
-    if (t.same && f == 1.0f) continue;                      // nothing changes
-#pragma unroll 4
-    for (int j = 0; j < kClipChunk / 8 / kClipThreads; ++j) {
-      const int64_t i = i0 + (j * kClipThreads + (int)threadIdx.x) * 8;
-      if (i < count) {
-        float v[8];
-        load_eight(v, g, i, count, type, vec);
+    const int64_t count = t.count;
+    const uint32_t here = max(first, t.first);
+    if (t.same && f == 1.0f) {                              // nothing changes
+      c = here;
+      continue;
+    }
+    auto store = [&](int64_t i, int64_t end, float (&v)[8]) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= f;
-        if (out_vec && i + 8 <= count) {
-          if (out_type == kOutF32) {
-            float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + i);
-            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-            to[1] = make_float4(v[4], v[5], v[6], v[7]);
-          } else {
-            const bool bf16 = out_type == kOutBF16;
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + i) =
-                make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
-          }
+      for (int j = 0; j < 8; ++j) v[j] *= f;
+      if (out_vec && i + 8 <= end) {
+        if (out_type == kOutF32) {
+          float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + i);
+          to[0] = make_float4(v[0], v[1], v[2], v[3]);
+          to[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i + k < count) out_store(out, i + k, v[k], out_type);
+          const bool bf16 = out_type == kOutBF16;
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + i) =
+              make_uint4(pack16(v[0], v[1], bf16), pack16(v[2], v[3], bf16), pack16(v[4], v[5], bf16), pack16(v[6], v[7], bf16));
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < end) out_store(out, i + j, v[j], out_type);
       }
+    };
+    for (; c > here; --c) {
+      const int64_t i0 = (int64_t)(c - 1 - t.first) * p.chunk;
+      const int64_t end = min(count, i0 + p.chunk);
+      for_chunk(g, type, vec, i0, end,
+                [&](int64_t i, const auto& batch) {
+#pragma unroll
+                  for (int j = 0; j < kClipBatch; ++j) {
+                    float v[8];
+                    batch.values(j, v);
+                    store(i + j * kClipStep, end, v);
+                  }
+                },
+                [&](int64_t i, float (&v)[8]) { store(i, end, v); });
     }
   }
 }
@@ -204,17 +280,25 @@ cudaError_t launch(void (*kernel)(P), unsigned blocks, const P& p, cudaStream_t 
 
 int type_bytes(int t) { return t == MPG_F32 ? 4 : 2; }
 
+// Elements of a chunk: a batch of loads, or with few elements one load, so that
+// more blocks share them.
+int chunk_for(int64_t n, const mpg_grad* grads) {
+  int64_t few = (int64_t)kClipBlocks * kClipBatch * kClipStep;
+  for (int64_t i = 0; i < n && few > 0; ++i) few -= grads[i].count;
+  return few > 0 ? kClipStep : kClipBatch * kClipStep;
+}
+
 // Tensors that one launch takes: as many as its table holds, below 2^31 chunks.
 struct Group {
   int64_t begin, end, chunks;
 };
-int64_t chunks_of(int64_t count) { return (count + kClipChunk - 1) / kClipChunk; }
-std::vector<Group> groups_of(int64_t n, const mpg_grad* grads) {
+int64_t chunks_of(int64_t count, int chunk) { return (count + chunk - 1) / chunk; }
+std::vector<Group> groups_of(int64_t n, const mpg_grad* grads, int chunk) {
   std::vector<Group> r;
   Group g{0, 0, 0};
   int64_t filled = 0;
   for (int64_t i = 0; i < n; ++i) {
-    const int64_t c = chunks_of(grads[i].count);
+    const int64_t c = chunks_of(grads[i].count, chunk);
     if (filled == kClipMany || g.chunks + c > INT32_MAX) {
       r.push_back(g);
       g = Group{i, i, 0};
@@ -230,8 +314,9 @@ std::vector<Group> groups_of(int64_t n, const mpg_grad* grads) {
 unsigned blocks_of(const Group& g) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(g.chunks, kClipBlocks)); }
 
 template <int kMost>
-void fill(ClipParams<kMost>& p, const mpg_grad* grads, const Group& g) {
+void fill(ClipParams<kMost>& p, const mpg_grad* grads, const Group& g, int chunk) {
   p.count = 0;
+  p.chunk = chunk;
   uint32_t at = 0;
   for (int64_t i = g.begin; i < g.end; ++i) {
     const mpg_grad& x = grads[i];
@@ -245,19 +330,19 @@ void fill(ClipParams<kMost>& p, const mpg_grad* grads, const Group& g) {
     t.out_type = (uint8_t)x.out_dtype;
     t.vec = (uint8_t)((fused_aligned(x.g, 16) ? 1 : 0) | (fused_aligned(x.out, 16) ? 2 : 0));
     t.same = x.g == x.out;
-    at += (uint32_t)chunks_of(x.count);
+    at += (uint32_t)chunks_of(x.count, chunk);
   }
   p.chunks = at;
 }
 
 template <int kMost>
-cudaError_t run(int64_t n, const mpg_grad* grads, const std::vector<Group>& groups, float max_norm, float eps, float* norm,
-                double* partial, cudaStream_t stream) {
+cudaError_t run(int64_t n, const mpg_grad* grads, const std::vector<Group>& groups, int chunk, float max_norm, float eps,
+                float* norm, double* partial, cudaStream_t stream) {
   // (the table is a launch's parameter: 32 KB of it stay off the caller's stack)
   static thread_local ClipParams<kMost> p;
   int32_t partials = 0;
   for (const Group& g : groups) {
-    fill(p, grads, g);
+    fill(p, grads, g, chunk);
     p.partial = partial + partials;
     const unsigned blocks = blocks_of(g);
     partials += (int32_t)blocks;
@@ -269,7 +354,7 @@ cudaError_t run(int64_t n, const mpg_grad* grads, const std::vector<Group>& grou
   p.max_norm = max_norm;
   p.eps = eps;
   for (size_t i = groups.size(); i-- > 0;) {
-    if (groups.size() > 1) fill(p, grads, groups[i]);
+    if (groups.size() > 1) fill(p, grads, groups[i], chunk);
     p.norm = i == 0 ? norm : nullptr;
     const cudaError_t e = launch(clip_scale_kernel<kMost>, blocks_of(groups[i]), p, stream);
     if (e != cudaSuccess) return e;
@@ -338,7 +423,7 @@ size_t mpg_clip_grad_norm_workspace_size(int64_t n, const mpg_grad* grads) {
   if (check(n, grads) != MPG_OK) return 0;
   try {
     size_t blocks = 0;
-    for (const Group& g : groups_of(n, grads)) blocks += blocks_of(g);
+    for (const Group& g : groups_of(n, grads, chunk_for(n, grads))) blocks += blocks_of(g);
     return align256(blocks * sizeof(double));
   } catch (const std::bad_alloc&) {
     return 0;
@@ -355,7 +440,8 @@ mpg_status mpg_clip_grad_norm(int64_t n, const mpg_grad* grads, float max_norm, 
   if (!norm || !fused_aligned(norm, 4)) return fail(MPG_ERR_INVALID_ARG, "NULL or misaligned norm");
   try {
     if ((s = check_overlap(n, grads)) != MPG_OK) return s;
-    const std::vector<Group> groups = groups_of(n, grads);
+    const int chunk = chunk_for(n, grads);
+    const std::vector<Group> groups = groups_of(n, grads, chunk);
     size_t need = 0, tensors = 0;
     for (const Group& g : groups) need += blocks_of(g);
     for (int64_t i = 0; i < n; ++i) tensors += grads[i].count > 0;
@@ -366,8 +452,8 @@ mpg_status mpg_clip_grad_norm(int64_t n, const mpg_grad* grads, float max_norm, 
     if ((s = get_device(&dev)) != MPG_OK) return s;
     double* partial = static_cast<double*>(workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = tensors <= kClipFew ? run<kClipFew>(n, grads, groups, max_norm, eps, norm, partial, st)
-                                              : run<kClipMany>(n, grads, groups, max_norm, eps, norm, partial, st);
+    const cudaError_t e = tensors <= kClipFew ? run<kClipFew>(n, grads, groups, chunk, max_norm, eps, norm, partial, st)
+                                              : run<kClipMany>(n, grads, groups, chunk, max_norm, eps, norm, partial, st);
     return e == cudaSuccess ? MPG_OK : fail(MPG_ERR_CUDA, "clipping launch: %s", cudaGetErrorString(e));
   } catch (const std::bad_alloc&) {
     return fail(MPG_ERR_INVALID_ARG, "out of host memory");

@@ -22,10 +22,10 @@ enum class FusedEpi {
 };
 
 constexpr int kMaxCtas = 160;          // workers of a launch, at most: the slots of split tiles are laid out for them
-constexpr int kScaleBlocks = 152;      // partial maxima behind a scale
+constexpr int kScaleBlocks = 304;      // partial maxima behind a scale
 
 // Rows that a product of few rows takes (few_rows.cu).
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 16;
 
 struct FusedGemmParams {
   CUtensorMap map_a[2], map_b[2];   // boxes of 64 x 64
@@ -83,7 +83,8 @@ struct FewRowsParams {
   const void *x, *w, *wu;           // X: rows x k; weights: n x k
   int64_t ldx, ldw, ldwu;
   int32_t bf16, rows, n, k;
-  int32_t vec;                      // lines of all operands start on 16-byte boundaries
+  int32_t vec;                      // lines of all operands start on 16-byte boundaries and are whole 16 bytes
+  int32_t strips;
   int32_t act;
   void *y, *g, *u;
   int64_t ldy, ldg, ldu;
@@ -92,8 +93,10 @@ struct FewRowsParams {
   int64_t target_stride, ignore_index;
   float2* stats;
   float* target_logit;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
 };
-cudaError_t launch_few_rows(const FewRowsParams& p, bool gated, cudaStream_t stream);
+mpg_status launch_few_rows(DeviceInfo* dev, FewRowsParams& p, bool gated, cudaStream_t stream);
 int few_rows_parts(int rows, int64_t n);   // of the statistics of n logits
 
 // Copies of matrices whose lines TMA cannot describe.
@@ -111,7 +114,7 @@ cudaError_t launch_pad(const PadParams& p, int sm_count, cudaStream_t stream);
 struct MaxParams {
   const void* x;
   int64_t ld, rows, cols;
-  int32_t vec;
+  int32_t vec, flat;                // flat: aligned lines of whole 16 bytes without gaps
   const float* dloss;
   int64_t dloss_stride;
   const void* target;

@@ -67,10 +67,23 @@ __global__ void __launch_bounds__(512) max_kernel(const __grid_constant__ MaxPar
   griddep_launch_dependents();
   float x = 0.0f;
   if (p.x) {
+    // (fp16: only its gradients are scaled); four loads on their way
     const int64_t per_line = (p.cols + 7) / 8, n = p.rows * per_line;
     const bool small = n < INT_MAX;
-#pragma unroll 4
-    for (int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x; i < n; i += (int64_t)kScaleBlocks * 512) {
+    constexpr int kAtOnce = 4;
+    constexpr int64_t kStep = (int64_t)kScaleBlocks * 512;
+    int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x;
+    if (p.flat) {
+      const uint4* at = static_cast<const uint4*>(p.x);
+      for (; i + (kAtOnce - 1) * kStep < n; i += kAtOnce * kStep) {
+        uint4 v[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) v[j] = ld_global(at + i + j * kStep);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) x = fmaxf(x, abs_max8(v[j], false));
+      }
+    }
+    for (; i < n; i += kStep) {
       const Chunk c = chunk_at(i, per_line, small);
       x = fmaxf(x, abs_max8(load_chunk(p.x, c.row * p.ld + c.col, p.cols - c.col, p.vec != 0), false));
     }

@@ -607,61 +607,59 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
 // ---------------------------------------------------------------------------
 // split tiles
 // ---------------------------------------------------------------------------
-// Adds a tile's parts in the order of k: four columns a thread, sixteen rows a
-// block.  Tiles that one worker had whole are done already.
-constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(256) fused_join_kernel(const __grid_constant__ FusedGemmParams p, int tile, int workers) {
+// Adds a tile's parts in the order of k, four columns a thread.  Tiles that one
+// worker had whole are done already.  Every worker has a block of k at least,
+// so the parts of a tile are those of consecutive workers, and only the first
+// can have begun in an earlier tile (its second slot).
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_constant__ FusedGemmParams p, int tile, int workers) {
   griddep_wait();
   griddep_launch_dependents();
-  const Pow2 sc = warp_scale(p.scale, p.scale_exp);
   const int64_t u0 = (int64_t)blockIdx.x * p.num_k_blk, u1 = u0 + p.num_k_blk;
-  int w0 = (int)min((int64_t)workers - 1, u0 * workers / p.units);
-  while (w0 > 0 && first_unit(p.units, w0, workers) > u0) --w0;
-  while (first_unit(p.units, w0 + 1, workers) <= u0) ++w0;
-  if (first_unit(p.units, w0 + 1, workers) >= u1) return;
+  const int w0 = (int)(((u0 + 1) * workers - 1) / p.units);                     // the last that begins at u0 or before
+  const int n = (int)((u1 * workers + p.units - 1) / p.units) - w0;             // up to the last that begins before u1
+  if (n == 1) return;
   const FusedTile tc = fused_tile(p, p.whole_tiles + (int)blockIdx.x);
   const bool second = tc.mb >= p.mb_second;
+  const int per_row = tile / 4;
+  const int i = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int r = i / per_row, c = i % per_row * 4;
+  const int row = (second ? tc.mb - p.mb_second : tc.mb) * tile + r, col = tc.nb * tile + c;
+  const Pow2 sc = warp_scale(p.scale, p.scale_exp);
+  if (row >= p.m || col >= p.n) return;
+  const int64_t slot = (int64_t)tile * tile;
+  const float* at = p.slots + (int64_t)r * tile + c;
+  float4 o = out_load4(at, (2 * w0 + (first_unit(p.units, w0, workers) < u0 ? 1 : 0)) * slot, kOutF32);
+#pragma unroll 4
+  for (int j = 1; j < n; ++j) {
+    const float4 y = out_load4(at, 2 * (w0 + j) * slot, kOutF32);
+    o.x += y.x;
+    o.y += y.y;
+    o.z += y.z;
+    o.w += y.w;
+  }
+  o.x *= sc.inv;
+  o.y *= sc.inv;
+  o.z *= sc.inv;
+  o.w *= sc.inv;
   void* out = p.out[second ? 1 : 0];
   const int64_t ldo = p.ldo[second ? 1 : 0];
-  const bool vec = p.out_vec[second ? 1 : 0] != 0;
-  const int per_row = tile / 4;
-  for (int i = threadIdx.x; i < kJoinRows * per_row; i += 256) {
-    const int r = blockIdx.y * kJoinRows + i / per_row, c = i % per_row * 4;
-    const int row = (second ? tc.mb - p.mb_second : tc.mb) * tile + r, col = tc.nb * tile + c;
-    if (row >= p.m || col >= p.n) continue;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int w = w0; w < workers; ++w) {
-      const int64_t a = first_unit(p.units, w, workers), b = first_unit(p.units, w + 1, workers);
-      if (a >= u1) break;
-      if (a == b) continue;
-      const int slot = 2 * w + (a >= u0 ? 0 : 1);   // (a run that starts in an earlier tile has this one second)
-      const uint4 y = ld_global(reinterpret_cast<const uint4*>(p.slots + ((int64_t)slot * tile + r) * tile + c));
-      o.x += __uint_as_float(y.x);
-      o.y += __uint_as_float(y.y);
-      o.z += __uint_as_float(y.z);
-      o.w += __uint_as_float(y.w);
+  if (p.out_vec[second ? 1 : 0] && col + 4 <= p.n) {
+    if (p.add) {
+      const float4 y = out_load4(p.add, (int64_t)row * p.ldadd + col, kOutF32);
+      o.x += y.x;
+      o.y += y.y;
+      o.z += y.z;
+      o.w += y.w;
     }
-    o.x *= sc.inv;
-    o.y *= sc.inv;
-    o.z *= sc.inv;
-    o.w *= sc.inv;
-    if (vec && col + 4 <= p.n) {
-      if (p.add) {
-        const float4 y = out_load4(p.add, (int64_t)row * p.ldadd + col, kOutF32);
-        o.x += y.x;
-        o.y += y.y;
-        o.z += y.z;
-        o.w += y.w;
-      }
-      out_store4(out, (int64_t)row * ldo + col, o, p.out_dtype);
-    } else {
-      const float e[4] = {o.x, o.y, o.z, o.w};
+    out_store4(out, (int64_t)row * ldo + col, o, p.out_dtype);
+  } else {
+    const float e[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (col + j < p.n)
-          out_store(out, (int64_t)row * ldo + col + j,
-                    p.add ? e[j] + out_load(p.add, (int64_t)row * p.ldadd + col + j, kOutF32) : e[j], p.out_dtype);
-    }
+    for (int j = 0; j < 4; ++j)
+      if (col + j < p.n)
+        out_store(out, (int64_t)row * ldo + col + j,
+                  p.add ? e[j] + out_load(p.add, (int64_t)row * p.ldadd + col + j, kOutF32) : e[j], p.out_dtype);
   }
 }
 
@@ -690,8 +688,8 @@ void fused_lookup(FusedEpi epi, bool pair, FusedKernel* out) {
 
 cudaError_t launch_fused_join(const FusedGemmParams& p, int tile, int workers, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.num_tiles - p.whole_tiles), (unsigned)(tile / kJoinRows));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)(p.num_tiles - p.whole_tiles), (unsigned)(tile * tile / 4 / kJoinThreads));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   cfg.numAttrs = (unsigned)launch_attributes(attr, 1);

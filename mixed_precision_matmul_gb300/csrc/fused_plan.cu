@@ -25,15 +25,22 @@ Shape shape_of(const FusedLaunch& l, int64_t tile) {
   return s;
 }
 
-// What the forms take on a GB300 (us): a way in and out, a time for each block
-// of 64 k of a round of tiles, and for split tiles the second launch.
-constexpr double kOneEdge = 4.3, kPairEdge = 7.5, kOneBlock = 0.29, kPairBlock = 0.31, kJoin = 4.0;
+// What the forms take on a GB300 (us): a way in and out, and a time for each
+// block of 64 k of a round of tiles.  Workers with parts of split tiles are at
+// different places of k: where the operands do not fit into L2 each fetches its
+// own blocks, at about 8300 bytes a ns together (a last round of 52 pairs' tiles
+// over k = 32768, dealt to 76: 210 us where the round takes 173), so that
+// splitting pays where it gives many idle workers something to do.  The parts
+// go through memory twice, and the second launch takes 3 us.
+constexpr double kOneEdge = 4.3, kPairEdge = 7.5, kOneBlock = 0.29, kPairBlock = 0.31;
+constexpr double kJoin = 3.0, kApartBytes = 8.3e6, kPartBytes = 5.0e6;     // bytes a us
+constexpr double kL2Bytes = 100e6;
 
 struct Deal {
   int64_t workers, whole;              // whole: tiles taken round by round
   double time;
 };
-Deal deal(const Shape& s, int64_t most, bool may_split, double edge, double block) {
+Deal deal(const FusedLaunch& l, const Shape& s, int64_t tile, int64_t most, double edge, double block, bool may_split) {
   const int64_t kb = s.units / s.tiles;
   const int64_t rounds = (s.tiles + most - 1) / most;
   Deal d{std::min(s.tiles, most), s.tiles, edge + (double)(rounds * kb) * block};
@@ -41,7 +48,11 @@ Deal deal(const Shape& s, int64_t most, bool may_split, double edge, double bloc
   if (!may_split || !rest) return d;
   const int64_t whole = s.tiles - rest;
   const int64_t workers = whole ? most : std::min(most, std::max(rest, rest * kb / kMinUnits));
-  const double time = edge + kJoin + ((double)(whole / most * kb) + (double)((rest * kb + workers - 1) / workers)) * block;
+  const double operands = 128.0 * (double)kb * (double)((l.second_m ? 2 : 1) * l.m + l.n);
+  const double apart = operands < kL2Bytes ? block : std::max(block, 256.0 * (double)tile * (double)workers / kApartBytes);
+  const double parts = (double)(rest + workers) * (double)(tile * tile) * 4.0;
+  const double time = edge + kJoin + 2.0 * parts / kPartBytes + (double)(whole / most * kb) * block +
+                      (double)((rest * kb + workers - 1) / workers) * apart;
   if (time < d.time) d = Deal{workers, whole, time};
   return d;
 }
@@ -73,8 +84,8 @@ mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& 
   if ((st = allow_smem(dev, one.fn, one.smem_bytes)) != MPG_OK) return st;
   const Shape s1 = shape_of(l, one.tile), s2 = shape_of(l, two.tile);
   const bool split = l.split && slots;
-  const Deal d1 = deal(s1, std::min(dev->sm_count, kMaxCtas), split, kOneEdge, kOneBlock);
-  const Deal d2 = deal(s2, std::min<int64_t>(pairs, kMaxPairs), split, kPairEdge, kPairBlock);
+  const Deal d1 = deal(l, s1, one.tile, std::min(dev->sm_count, kMaxCtas), kOneEdge, kOneBlock, split);
+  const Deal d2 = deal(l, s2, two.tile, std::min<int64_t>(pairs, kMaxPairs), kPairEdge, kPairBlock, split);
   const bool pair = d2.time < d1.time;
   const Shape& s = pair ? s2 : s1;
   const Deal& d = pair ? d2 : d1;

@@ -171,7 +171,7 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
     p.rows = (int32_t)l.tokens;
     p.n = (int32_t)l.inner;
     p.k = (int32_t)l.hidden;
-    p.vec = !o.x.copy && !o.wg.copy && !o.wu.copy;
+    p.vec = !o.x.copy && !o.wg.copy && !o.wu.copy && l.hidden % 8 == 0;
     p.act = (int32_t)l.act;
     p.y = Y;
     p.ldy = ldy;
@@ -179,8 +179,7 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
     p.ldg = ldg;
     p.u = U;
     p.ldu = ldu;
-    const cudaError_t e = launch_few_rows(p, true, st);
-    return e == cudaSuccess ? MPG_OK : fail(MPG_ERR_CUDA, "few rows launch: %s", cudaGetErrorString(e));
+    return launch_few_rows(dev, p, true, st);
   }
 
   if ((s = make_copies(dev, {&o.x, &o.wg, &o.wu}, static_cast<uint8_t*>(workspace), st)) != MPG_OK) return s;
@@ -261,6 +260,7 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     p.rows = l.tokens;
     p.cols = l.inner;
     p.vec = fused_lines_ok(dY, l.tokens > 1 ? lddy : 0);
+    p.flat = p.vec && l.inner % 8 == 0 && (lddy == l.inner || l.tokens == 1);
     p.partial = partial;
     const cudaError_t e = launch_max(p, st);
     if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "maximum launch: %s", cudaGetErrorString(e));

@@ -161,15 +161,14 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
     p.rows = (int32_t)l.tokens;
     p.n = (int32_t)l.vocab;
     p.k = (int32_t)l.hidden;
-    p.vec = !o.x.copy && !o.w.copy;
+    p.vec = !o.x.copy && !o.w.copy && l.hidden % 8 == 0;
     p.target = l.target;
     p.target_bytes = l.target_bytes;
     p.target_stride = l.target_stride;
     p.ignore_index = l.ignore_index;
     p.stats = stats;
     p.target_logit = target_logit;
-    const cudaError_t e = launch_few_rows(p, false, st);
-    if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "few rows launch: %s", cudaGetErrorString(e));
+    if ((s = launch_few_rows(dev, p, false, st)) != MPG_OK) return s;
     j.parts = few_rows_parts((int)l.tokens, l.vocab);
   } else {
     if ((s = make_copies(dev, o, ws, st)) != MPG_OK) return s;
