@@ -92,22 +92,23 @@ __device__ __forceinline__ void load_eight(float (&v)[8], const void* base, int6
   }
 }
 
-template <int kN>
-__device__ __forceinline__ double squares(const float (&v)[kN]) {
+__device__ __forceinline__ void add_squares(const float (&v)[8], float (&a)[4]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a[j % 4] = fmaf(v[j], v[j], a[j % 4]);
+}
+__device__ __forceinline__ bool squares_hold(float s) { return s >= 8.0779357e-28f && s <= 1.329228e36f; }   // [2^-90, 2^120]
+__device__ __forceinline__ void add_squares64(const float (&v)[8], double& d) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (v[j] != 0.0f) d = fma((double)v[j], (double)v[j], d);
+}
+__device__ __forceinline__ double squares(const float (&v)[8]) {
   float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int j = 0; j < kN; ++j) a[j % 4] = fmaf(v[j], v[j], a[j % 4]);
+  add_squares(v, a);
   const float s = (a[0] + a[1]) + (a[2] + a[3]);
-  if (s >= 8.0779357e-28f && s <= 1.329228e36f) return (double)s;    // [2^-90, 2^120]
-  float any = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kN; ++j) any = fmaxf(any, fabsf(v[j]));
-  if (any == 0.0f && s == 0.0f) return 0.0;
+  if (squares_hold(s)) return (double)s;
   double d = 0.0;
-#pragma unroll 1
-  for (int j = 0; j < kN; j += 8)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) d = fma((double)v[j + k], (double)v[j + k], d);
+  add_squares64(v, d);
   return d;
 }
 
@@ -189,10 +190,22 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_co
     const uint32_t next = k + 1 < p.count ? min(last, p.tensor[k + 1].first) : last;
     for_chunk(t.g, t.g_type, t.vec & 1, (int64_t)(c - t.first) * p.chunk, min(t.count, (int64_t)(next - t.first) * p.chunk),
               [&](int64_t, const auto& batch) {
-                float v[8 * kClipBatch];
+                float v[8], a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < kClipBatch; ++j) batch.values(j, *reinterpret_cast<float(*)[8]>(v + 8 * j));
-                sum += squares(v);
+                for (int j = 0; j < kClipBatch; ++j) {
+                  batch.values(j, v);
+                  add_squares(v, a);
+                }
+                const float s = (a[0] + a[1]) + (a[2] + a[3]);
+                if (squares_hold(s)) {
+                  sum += (double)s;
+                  return;
+                }
+#pragma unroll
+                for (int j = 0; j < kClipBatch; ++j) {
+                  batch.values(j, v);
+                  add_squares64(v, sum);
+                }
               },
               [&](int64_t, const float (&v)[8]) { sum += squares(v); });
     c = next;
