@@ -47,7 +47,10 @@ SOURCES = [
     "ortho_api.cu",
     "ortho.cu",
     "fused_plan.cu",
-    "fused_gemm.cu",
+    "fused_plain.cu",
+    "fused_gated.cu",
+    "fused_gated_grad.cu",
+    "fused_loss.cu",
     "few_rows.cu",
     "fused_aux.cu",
     "gated_api.cu",
@@ -55,7 +58,7 @@ SOURCES = [
     "clip.cu",
 ]
 HEADERS = ["ptx.cuh", "cluster.cuh", "internal.h", "tc_gemm.cuh", "outio.cuh", "host.h", "staging.cuh",
-           "fp8.h", "fp8_tc.cuh", "ortho.h", "fused.h", "fused.cuh"]
+           "fp8.h", "fp8_tc.cuh", "ortho.h", "fused.h", "fused.cuh", "fused_gemm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

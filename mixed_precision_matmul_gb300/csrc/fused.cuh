@@ -28,11 +28,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 1 / (1 + e^-x): 0 far below 0, where e^-x is infinite.
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-kLog2e * x)); }
 
-// Standard normal distribution function, (1 + erf(x / sqrt 2)) / 2; below 0 by
-// erfc, which keeps its relative precision there.
-__device__ __forceinline__ float normal_cdf(float x) {
-  return x < 0.0f ? 0.5f * erfcf(x * -0.70710678118654752f) : 0.5f + 0.5f * erff(x * 0.70710678118654752f);
-}
+// Standard normal distribution function, (1 + erf(x / sqrt 2)) / 2, by erfc, which
+// keeps its relative precision far below 0.
+__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -0.70710678118654752f); }
 
 // act(x), and with it act'(x).
 //   silu       x s(x), s(x) = 1 / (1 + e^-x);        s (1 + x (1 - s))

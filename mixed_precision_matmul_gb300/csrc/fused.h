@@ -1,6 +1,6 @@
 // Internal structures of the 16-bit products with fused epilogues: the gated
 // feed-forward product, the projection onto a vocabulary with its cross
-// entropy, and the products of their gradients (fused_gemm.cu, few_rows.cu,
+// entropy, and the products of their gradients (fused_gemm.cuh, few_rows.cu,
 // fused_aux.cu), launched from gated_api.cu and loss_api.cu.
 #pragma once
 
@@ -27,25 +27,32 @@ constexpr int kScaleBlocks = 304;      // partial maxima behind a scale
 // Rows that a product of few rows takes (few_rows.cu).
 constexpr int kFewRows = 16;
 
-struct FusedGemmParams {
+// One product: operands, extents and where the result goes.
+struct FusedProduct {
   CUtensorMap map_a[2], map_b[2];   // boxes of 64 x 64
-  int32_t a_mn_major, b_mn_major, bf16;
+  int32_t a_mn_major, b_mn_major;
   int32_t m, n;                     // of the result (kGated, kGatedGrad: n of each half)
   int32_t num_m_blk, num_n_blk, num_k_blk;
   int32_t kb_second;                // first block of k that comes from map_a[1] and map_b[1]
   int32_t mb_second;                // first row block of the second matrix: map_a[1], out[1]
   int32_t num_tiles, group_m;
-  int32_t whole_tiles;              // taken round by round; the others' blocks of k are dealt out evenly
-  int64_t units;                    // blocks of k of those others
-  float* slots;                     // partial tiles, two for each worker
-
-  int32_t act;
   void* out[3];                     // kPlain: C, second C; kGated: Y, gate, up (or null); kGatedGrad: dgate, dup; kProb: D
   int64_t ldo[3];
   int32_t out_vec[3];               // 8 elements of 16 bits (4 of fp32) are aligned
   int32_t out_dtype;
   const float* add;                 // kPlain: fp32, added to the result, or null
   int64_t ldadd;
+};
+
+struct FusedGemmParams {
+  FusedProduct prod[2];             // kPlain: two products may share a launch, the longer k first
+  int32_t bf16;
+  int32_t whole_tiles;              // of the first: taken round by round; the others' blocks of k are dealt out evenly
+  int64_t units;                    // blocks of k of those others
+  float* slots;                     // partial tiles, two for each worker
+  int32_t late, late_workers, late_rounds;   // the second's tiles: see FusedItems
+
+  int32_t act;
   const void* dy;                   // kGatedGrad
   int64_t lddy;
   int32_t dy_vec;
@@ -74,7 +81,10 @@ struct FusedKernel {
   int tile;                         // rows of a tile, and columns of its accumulators
   int ctas;
 };
-void fused_lookup(FusedEpi epi, bool pair, FusedKernel* out);
+void fused_lookup_plain(bool pair, FusedKernel* out);
+void fused_lookup_gated(bool pair, int act, FusedKernel* out);
+void fused_lookup_gated_grad(bool pair, int act, FusedKernel* out);
+void fused_lookup_loss(FusedEpi epi, bool pair, FusedKernel* out);
 // Sums the parts of split tiles (kPlain).
 cudaError_t launch_fused_join(const FusedGemmParams& p, int tile, int workers, cudaStream_t stream);
 
@@ -159,6 +169,9 @@ struct FusedLaunch {
   bool split = false;               // tiles may be split along k (kPlain)
 };
 mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& p, float* slots, cudaStream_t stream);
+// Both of p's products, in one launch where that takes less.
+mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedLaunch& l1, FusedGemmParams& p, float* slots,
+                            cudaStream_t stream);
 size_t fused_slot_bytes(const FusedLaunch& l);   // of the slots that a launch may need
 // rows x k operand of a product: K-major if k is the matrix's contiguous side.
 mpg_status fused_map(CUtensorMap* map, const void* ptr, int64_t ld, mpg_dtype dt, bool mn_major, int64_t rows, int64_t k);

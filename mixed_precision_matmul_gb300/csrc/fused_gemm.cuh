@@ -26,14 +26,18 @@
 // Accumulators are double-buffered in TMEM, so the epilogue runs beside the
 // next tile's products.
 //
-// Tiles go round by round to the workers.  What does not fill a round is split
+// Tiles go round by round to the workers.  What does not fill a round may be split
 // (kPlain): its blocks of k are dealt out evenly, each worker getting one run of
 // them, and a worker whose run holds only a part of a tile's k leaves its sums
 // in a slot.  A second launch adds the slots of a tile in the order of k: the
-// result does not depend on timing.
+// result does not depend on timing.  Or a second product's tiles, shorter ones,
+// fill the first's last round: the gradients of an input and of a weight are two
+// products from the same D, and in one launch no worker waits for the other's end.
 //
 // Waits are bounded, and a timeout raises the abort flag of both CTAs: every
 // role drains what it has in flight before TMEM is released.
+#pragma once
+
 #include <climits>
 
 #include "cluster.cuh"
@@ -45,10 +49,11 @@
 namespace mpg {
 namespace {
 
-template <FusedEpi E, bool kPair_>
+template <FusedEpi E, bool kPair_, int kAct_ = 0>
 struct FusedTraits {
   static constexpr FusedEpi kEpi = E;
   static constexpr bool kPair = kPair_;
+  static constexpr int kAct = kAct_;
   static constexpr bool kTwo = E == FusedEpi::kGated || E == FusedEpi::kGatedGrad;   // gate and up
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kTile = 128 * kCtas;         // rows, and columns of the accumulators
@@ -93,36 +98,56 @@ __device__ __forceinline__ void st_shared_h(uint32_t addr, uint16_t v) {
 // which spreads writes (a row a lane) and reads (four lanes a row) over all banks.
 __device__ __forceinline__ uint32_t half_chunk(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
 
-// 32 x 32 block of 16-bit values, a row a lane, to rows row0.. and columns col0.. .
-__device__ __forceinline__ void store_block16(uint32_t stg, int lane, const uint32_t (&w)[16], void* base, int64_t ld,
-                                              int row0, int rows, int col0, int cols, bool vec) {
+// 32 x 32 block of 16-bit values, a row a lane, to rows row0.. and columns col0..
+// (The way from shared memory to the matrix is a function of its own: inlined at
+// every store the code outgrows the instruction caches, and a kernel of few tiles
+// waits for it: 1531 x 1001 x 2741 in two rounds of tiles 22 us, 9 of them MMAs.)
+struct Block16 {
+  void* base;
+  int64_t ld;
+  int row0, rows, col0, cols;
+  bool vec;
+};
+__device__ __noinline__ void flush_block16(uint32_t stg, const Block16 b) {
+  const int lane = threadIdx.x & 31;
+  uint16_t* out = static_cast<uint16_t*>(b.base);
+  if (b.vec && b.col0 + 32 <= b.cols) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), c = lane & 3;
+      if (b.row0 + r < b.rows)
+        *reinterpret_cast<uint4*>(out + (int64_t)(b.row0 + r) * b.ld + b.col0 + c * 8) = ld_shared_v4(stg + half_chunk(r, c));
+    }
+  } else if (b.col0 + lane < b.cols) {
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r)
+      if (b.row0 + r < b.rows)
+        out[(int64_t)(b.row0 + r) * b.ld + b.col0 + lane] = ld_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void store_block16(uint32_t stg, int lane, const uint32_t (&w)[16], const Block16& b) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     st_shared_v4(stg + half_chunk(lane, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   __syncwarp();
-  uint16_t* out = static_cast<uint16_t*>(base);
-  if (vec && col0 + 32 <= cols) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2), c = lane & 3;
-      if (row0 + r < rows)
-        *reinterpret_cast<uint4*>(out + (int64_t)(row0 + r) * ld + col0 + c * 8) = ld_shared_v4(stg + half_chunk(r, c));
-    }
-  } else if (col0 + lane < cols) {
-#pragma unroll 4
-    for (int r = 0; r < 32; ++r)
-      if (row0 + r < rows)
-        out[(int64_t)(row0 + r) * ld + col0 + lane] = ld_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2);
-  }
+  flush_block16(stg, b);
+}
+// The same read into the staging: row row0 + lane, 32 columns (0 beyond the matrix).
+__device__ __noinline__ void fill_block16(uint32_t stg, const Block16 b) {
+  const int lane = threadIdx.x & 31;
+  const uint16_t* src = static_cast<const uint16_t*>(b.base);
+  const bool in = b.col0 + lane < b.cols;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r)
+    st_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2,
+                in && b.row0 + r < b.rows ? src[(int64_t)(b.row0 + r) * b.ld + b.col0 + lane] : (uint16_t)0);
   __syncwarp();
 }
-// The same read: row row0 + lane, 32 columns (0 beyond the matrix).
-__device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&w)[16], const void* base, int64_t ld,
-                                             int row0, int rows, int col0, int cols, bool vec) {
-  const uint16_t* src = static_cast<const uint16_t*>(base);
-  if (vec && col0 + 32 <= cols) {
-    const bool in = row0 + lane < rows;
-    const uint4* at = reinterpret_cast<const uint4*>(src + (int64_t)(in ? row0 + lane : row0) * ld + col0);
+__device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&w)[16], const Block16& b) {
+  if (b.vec && b.col0 + 32 <= b.cols) {
+    const bool in = b.row0 + lane < b.rows;
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(b.base) + (int64_t)(in ? b.row0 + lane : b.row0) * b.ld + b.col0);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint4 x = in ? ld_global(at + c) : make_uint4(0, 0, 0, 0);
@@ -133,12 +158,7 @@ __device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&
     }
     return;
   }
-  const bool in = col0 + lane < cols;
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r)
-    st_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2,
-                in && row0 + r < rows ? src[(int64_t)(row0 + r) * ld + col0 + lane] : (uint16_t)0);
-  __syncwarp();
+  fill_block16(stg, b);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const uint4 x = ld_shared_v4(stg + half_chunk(lane, c));
@@ -153,7 +173,7 @@ __device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&
 struct FusedTile {
   int mb, nb;
 };
-__device__ __forceinline__ FusedTile fused_tile(const FusedGemmParams& p, int t) {
+__device__ __forceinline__ FusedTile fused_tile(const FusedProduct& p, int t) {
   // groups of tile rows, walked column by column, every other group backwards
   const int per = p.group_m * p.num_n_blk;
   const int g = t / per;
@@ -170,41 +190,60 @@ __device__ __forceinline__ FusedTile fused_tile(const FusedGemmParams& p, int t)
 // The first of the split tiles' blocks of k that worker w takes.
 __host__ __device__ __forceinline__ int64_t first_unit(int64_t units, int w, int workers) { return units * w / workers; }
 
-// A worker's tiles: whole ones round by round, then its run of the others'
-// blocks of k.
+// A worker's tiles: the first product's whole ones round by round, then its run of
+// that product's split tiles' blocks of k, then the second product's.  Workers
+// p.late .. have one tile of the first product less than those before them; they
+// take p.late_rounds rounds of the second's alone, about as long as that tile,
+// and then go first in the rounds of all.
 struct FusedItem {
+  int which;                         // product
   int mb, nb, kb0, kb1;
   int slot;                          // of a part of a tile's k; -1: all of it
 };
 struct FusedItems {
-  int t, worker, workers;
+  int t, round, worker, workers;
   int64_t u, u0, u1;
-  __device__ __forceinline__ FusedItems(const FusedGemmParams& p, int w, int n) : t(w), worker(w), workers(n) {
+  __device__ __forceinline__ FusedItems(const FusedGemmParams& p, int w, int n) : t(w), round(0), worker(w), workers(n) {
     u = u0 = u1 = 0;
     if (p.units) {
       u = u0 = first_unit(p.units, w, n);
       u1 = first_unit(p.units, w + 1, n);
     }
   }
+  template <bool kMore>
   __device__ __forceinline__ bool next(const FusedGemmParams& p, FusedItem& x) {
     int tile;
+    x.which = 0;
+    x.kb0 = 0;
+    x.kb1 = p.prod[0].num_k_blk;
+    x.slot = -1;
     if (t < p.whole_tiles) {
       tile = t;
       t += workers;
-      x.kb0 = 0;
-      x.kb1 = p.num_k_blk;
-      x.slot = -1;
-    } else if (u < u1) {
-      const int64_t j = u / p.num_k_blk;
+    } else if (kMore && u < u1) {
+      const int64_t j = u / p.prod[0].num_k_blk;
       tile = p.whole_tiles + (int)j;
-      x.kb0 = (int)(u - j * p.num_k_blk);
-      x.kb1 = (int)min((int64_t)p.num_k_blk, x.kb0 + (u1 - u));
-      x.slot = x.kb1 - x.kb0 == p.num_k_blk ? -1 : 2 * worker + (u == u0 ? 0 : 1);
+      x.kb0 = (int)(u - j * p.prod[0].num_k_blk);
+      x.kb1 = (int)min((int64_t)p.prod[0].num_k_blk, x.kb0 + (u1 - u));
+      x.slot = x.kb1 - x.kb0 == p.prod[0].num_k_blk ? -1 : 2 * worker + (u == u0 ? 0 : 1);
       u += x.kb1 - x.kb0;
+    } else if (kMore && p.prod[1].num_tiles) {
+      int rank = worker - p.late;
+      if (rank >= 0 && round < p.late_rounds) {
+        tile = round * p.late_workers + rank;
+      } else {
+        if (rank < 0) rank += workers;
+        const int more = worker >= p.late ? round - p.late_rounds : round;
+        tile = p.late_rounds * p.late_workers + more * workers + rank;
+      }
+      ++round;
+      if (tile >= p.prod[1].num_tiles) return false;
+      x.which = 1;
+      x.kb1 = p.prod[1].num_k_blk;
     } else {
       return false;
     }
-    const FusedTile c = fused_tile(p, tile);
+    const FusedTile c = fused_tile(p.prod[kMore ? x.which : 0], tile);
     x.mb = c.mb;
     x.nb = c.nb;
     return true;
@@ -243,8 +282,8 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     mbar_fence_init();
-    tma_prefetch_map(&p.map_a[0]);
-    tma_prefetch_map(&p.map_b[0]);
+    tma_prefetch_map(&p.prod[0].map_a[0]);
+    tma_prefetch_map(&p.prod[0].map_b[0]);
   }
   if (warp == 1) {
     if constexpr (T::kPair) {
@@ -278,33 +317,34 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
       bool ok = true;
       FusedItems items(p, worker, workers);
       FusedItem x;
-      while (ok && items.next(p, x)) {
-        const bool second = x.mb >= p.mb_second;
-        const int arow = (second ? x.mb - p.mb_second : x.mb) * T::kTile + (int)rank * T::BM;
+      while (ok && items.template next<T::kEpi == FusedEpi::kPlain>(p, x)) {
+        const FusedProduct& pr = p.prod[x.which];
+        const bool second = x.mb >= pr.mb_second;
+        const int arow = (second ? x.mb - pr.mb_second : x.mb) * T::kTile + (int)rank * T::BM;
         for (int kb = x.kb0; kb < x.kb1; ++kb, ++it) {
           const uint32_t st = it % T::kStages;
           if (!mbar_wait(&op_empty[st], ((it / T::kStages) & 1u) ^ 1u, ctl)) { ok = false; break; }
           if (rank == 0) mbar_arrive_expect_tx(&op_full[st], T::kCtas * T::kStage);
           uint8_t* dst = smem + st * T::kStage;
-          const bool late = kb >= p.kb_second;
-          const int k0 = (late ? kb - p.kb_second : kb) * T::BK;
+          const bool late = kb >= pr.kb_second;
+          const int k0 = (late ? kb - pr.kb_second : kb) * T::BK;
           auto box = [&](const CUtensorMap* map, uint8_t* to, bool mn, int row) {
             const int c0 = mn ? row : k0, c1 = mn ? k0 : row;
             if constexpr (T::kPair) tma_load_3d_pair(to, map, full0 + st * 8u, c0, c1, 0);
             else tma_load_3d(to, map, &op_full[st], c0, c1, 0);
           };
-          const CUtensorMap* ma = &p.map_a[second || late ? 1 : 0];
+          const CUtensorMap* ma = &pr.map_a[second || late ? 1 : 0];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) box(ma, dst + h * T::kHalf, p.a_mn_major != 0, arow + h * 64);
+          for (int h = 0; h < 2; ++h) box(ma, dst + h * T::kHalf, pr.a_mn_major != 0, arow + h * 64);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint8_t* to = dst + T::kATile + h * T::kHalf;
             if constexpr (T::kTwo) {
               // a pair: this CTA's 128 lines of one weight; one CTA: 64 of each
               const int which = T::kPair ? (int)rank : h;
-              box(&p.map_b[which], to, false, x.nb * T::kTileN + (T::kPair ? h * 64 : 0));
+              box(&pr.map_b[which], to, false, x.nb * T::kTileN + (T::kPair ? h * 64 : 0));
             } else {
-              box(&p.map_b[late ? 1 : 0], to, p.b_mn_major != 0, x.nb * T::kTile + (int)rank * 128 + h * 64);
+              box(&pr.map_b[late ? 1 : 0], to, pr.b_mn_major != 0, x.nb * T::kTile + (int)rank * 128 + h * 64);
             }
           }
         }
@@ -318,11 +358,6 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
       const bool leader = elect_one();
-      const bool a_mn = p.a_mn_major != 0, b_mn = p.b_mn_major != 0;
-      const uint32_t idesc = make_idesc(p.bf16 ? 1u : 0u, a_mn, b_mn, T::kTile, T::kTile);
-      // the start address sits in the descriptor's low bits, in units of 16 bytes
-      const uint64_t a_desc = operand_desc<T>(op_smem, a_mn, 0), b_desc = operand_desc<T>(op_smem + T::kATile, b_mn, 0);
-      const uint32_t a_step = (a_mn ? T::kInstrK * T::kRowBytes : 32) / 16, b_step = (b_mn ? T::kInstrK * T::kRowBytes : 32) / 16;
       const uint32_t d_base = __shfl_sync(0xffffffffu, tmem_base, 0);
       auto commit = [&](uint64_t* bar, uint16_t mask) {
         if constexpr (T::kPair) mma_commit_multicast(bar, mask);
@@ -332,12 +367,17 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
       bool ok = true;
       FusedItems items(p, worker, workers);
       FusedItem x;
-      for (; ok && items.next(p, x); ++g) {
+      for (; ok && items.template next<T::kEpi == FusedEpi::kPlain>(p, x); ++g) {
         const uint32_t ab = g % T::kAccBufs;
         const uint32_t ph = ((g / T::kAccBufs) & 1u) ^ 1u;
         if (!(T::kPair ? warp_wait_relaxed(&acc_empty[ab], ph, ctl) : warp_wait(&acc_empty[ab], ph, ctl))) { ok = false; break; }
         tc_fence_after_sync();
         const uint32_t d0 = d_base + ab * T::kTile;
+        const bool a_mn = p.prod[x.which].a_mn_major != 0, b_mn = p.prod[x.which].b_mn_major != 0;
+        const uint32_t idesc = make_idesc(p.bf16 ? 1u : 0u, a_mn, b_mn, T::kTile, T::kTile);
+        // the start address sits in the descriptor's low bits, in units of 16 bytes
+        const uint64_t a_desc = operand_desc<T>(op_smem, a_mn, 0), b_desc = operand_desc<T>(op_smem + T::kATile, b_mn, 0);
+        const uint32_t a_step = (a_mn ? T::kInstrK * T::kRowBytes : 32) / 16, b_step = (b_mn ? T::kInstrK * T::kRowBytes : 32) / 16;
         for (int kb = x.kb0; kb < x.kb1; ++kb) {
           if (!warp_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
           tc_fence_after_sync();
@@ -380,11 +420,12 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
     uint32_t g = 0;
     FusedItems items(p, worker, workers);
     FusedItem x;
-    for (; items.next(p, x); ++g) {
-      const bool second = x.mb >= p.mb_second;
+    for (; items.template next<T::kEpi == FusedEpi::kPlain>(p, x); ++g) {
+      const FusedProduct& pr = p.prod[x.which];
+      const bool second = x.mb >= pr.mb_second;
       const uint32_t ab = g % T::kAccBufs;
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + ab * T::kTile;
-      const int row0 = (second ? x.mb - p.mb_second : x.mb) * T::kTile + (int)rank * T::BM + 32 * q;
+      const int row0 = (second ? x.mb - pr.mb_second : x.mb) * T::kTile + (int)rank * T::BM + 32 * q;
       const int row = row0 + lane;
       const int col_tile = x.nb * T::kTileN;
       auto release = [&]() {
@@ -400,7 +441,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
       int64_t target = -1;
       float lse2 = 0.0f, weight = 0.0f;
       if constexpr (T::kEpi == FusedEpi::kStats || T::kEpi == FusedEpi::kProb) {
-        if (row < p.m) {
+        if (row < pr.m) {
           target = target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, row);
           if constexpr (T::kEpi == FusedEpi::kProb) {
             lse2 = kLog2e * ld_global(p.lse + row);
@@ -418,34 +459,34 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           const int col0 = col_tile + cc * 32;
           uint32_t dyw[16];
           if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
-            if (row0 < p.m && col0 < p.n)
-              load_block16(stg, lane, dyw, p.dy, p.lddy, row0, p.m, col0, p.n, p.dy_vec != 0);
+            if (row0 < pr.m && col0 < pr.n)
+              load_block16(stg, lane, dyw, Block16{const_cast<void*>(p.dy), p.lddy, row0, pr.m, col0, pr.n, p.dy_vec != 0});
           }
           float gt[32], up[32];
           tmem_ld_32cols(tacc + cc * 32, gt);
           tmem_ld_32cols(tacc + T::kTile / 2 + cc * 32, up);
           tmem_ld_wait();
           if (cc == cc0 + kCc - 1) release();
-          if (row0 >= p.m || col0 >= p.n) continue;
+          if (row0 >= pr.m || col0 >= pr.n) continue;
           auto store = [&](int i, auto value) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = pack16(value(2 * j), value(2 * j + 1), bf16);
-            store_block16(stg, lane, w, p.out[i], p.ldo[i], row0, p.m, col0, p.n, p.out_vec[i] != 0);
+            store_block16(stg, lane, w, Block16{pr.out[i], pr.ldo[i], row0, pr.m, col0, pr.n, pr.out_vec[i] != 0});
           };
           if constexpr (T::kEpi == FusedEpi::kGated) {
-            if (p.out[1]) {
+            if (pr.out[1]) {
               store(1, [&](int j) { return gt[j]; });
               store(2, [&](int j) { return up[j]; });
             }
-            store(0, [&](int j) { return act_value(gt[j], p.act) * up[j]; });
+            store(0, [&](int j) { return act_value(gt[j], T::kAct) * up[j]; });
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float2 y2 = unpack16(dyw[j >> 1], bf16);
               const float dy = sc.mul * ((j & 1) ? y2.y : y2.x);
               float a, d;
-              act_both(gt[j], p.act, a, d);
+              act_both(gt[j], T::kAct, a, d);
               gt[j] = dy * up[j] * d;
               up[j] = dy * a;
             }
@@ -455,7 +496,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
         }
       } else if constexpr (T::kEpi == FusedEpi::kStats) {
         float top = -INFINITY, sum = 0.0f;
-        const int last = p.n - col_tile;            // columns of the tile inside the matrix
+        const int last = pr.n - col_tile;            // columns of the tile inside the matrix
 #pragma unroll 1
         for (int cc = cc0; cc < cc0 + kCc; ++cc) {
           float v[32];
@@ -497,7 +538,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           sum = (top == -INFINITY ? sum : sum * ex2(top - b)) + (s0 + s1);
           top = base;
         }
-        if (row < p.m) p.stats[(int64_t)(x.nb * 2 + half) * p.m + row] = make_float2(top, sum);
+        if (row < pr.m) p.stats[(int64_t)(x.nb * 2 + half) * pr.m + row] = make_float2(top, sum);
       } else if constexpr (T::kEpi == FusedEpi::kProb) {
 #pragma unroll 1
         for (int cc = cc0; cc < cc0 + kCc; ++cc) {
@@ -506,7 +547,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           tmem_ld_wait();
           if (cc == cc0 + kCc - 1) release();
           const int col0 = col_tile + cc * 32;
-          if (row0 >= p.m || col0 >= p.n) continue;
+          if (row0 >= pr.m || col0 >= pr.n) continue;
           const int64_t at = target - (p.col0 + col0);
           const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
           const bool any = __any_sync(0xffffffffu, mine != 0u);
@@ -520,14 +561,14 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             w[j] = weight == 0.0f ? 0u : pack16(weight * v[2 * j], weight * v[2 * j + 1], bf16);
-          store_block16(stg, lane, w, p.out[0], p.ldo[0], row0, p.m, col0, p.n, p.out_vec[0] != 0);
+          store_block16(stg, lane, w, Block16{pr.out[0], pr.ldo[0], row0, pr.m, col0, pr.n, pr.out_vec[0] != 0});
         }
       } else {
-        const int dt = p.out_dtype;
+        const int dt = pr.out_dtype;
         const bool part = x.slot >= 0;
-        void* out = p.out[second ? 1 : 0];
-        const int64_t ldo = p.ldo[second ? 1 : 0];
-        const bool vec = p.out_vec[second ? 1 : 0] != 0;
+        void* out = pr.out[second ? 1 : 0];
+        const int64_t ldo = pr.ldo[second ? 1 : 0];
+        const bool vec = pr.out_vec[second ? 1 : 0] != 0;
         float* slot = p.slots + (int64_t)max(x.slot, 0) * (T::kTile * T::kTile);
 #pragma unroll 1
         for (int cc = cc0; cc < cc0 + kCc; ++cc) {
@@ -536,7 +577,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           tmem_ld_wait();
           if (cc == cc0 + kCc - 1) release();
           const int col0 = col_tile + cc * 32;
-          if (row0 >= p.m || col0 >= p.n) continue;
+          if (row0 >= pr.m || col0 >= pr.n) continue;
           if (part) {
             // sums of a part of k, as they are: rows of the tile, whole lines a store
             stage_write_row(stg, lane, v);
@@ -550,24 +591,24 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= sc.inv;
-          if (dt != kOutF32 && !p.add) {
+          if (dt != kOutF32 && !pr.add) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], dt == kOutBF16);
-            store_block16(stg, lane, w, out, ldo, row0, p.m, col0, p.n, vec);
+            store_block16(stg, lane, w, Block16{out, ldo, row0, pr.m, col0, pr.n, vec});
             continue;
           }
           stage_write_row(stg, lane, v);
           __syncwarp();
           // (add has lines of whole 16-byte chunks)
-          if (vec && col0 + 32 <= p.n) {
+          if (vec && col0 + 32 <= pr.n) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int r = row0 + i * 4 + (lane >> 3), c = col0 + (lane & 7) * 4;
               float4 o = stage_read_chunk(stg, lane, i);
-              if (r < p.m) {
-                if (p.add) {
-                  const float4 y = out_load4(p.add, (int64_t)r * p.ldadd + c, kOutF32);
+              if (r < pr.m) {
+                if (pr.add) {
+                  const float4 y = out_load4(pr.add, (int64_t)r * pr.ldadd + c, kOutF32);
                   o.x += y.x;
                   o.y += y.y;
                   o.z += y.z;
@@ -576,12 +617,12 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
                 out_store4(out, (int64_t)r * ldo + c, o, dt);
               }
             }
-          } else if (col0 + lane < p.n) {
+          } else if (col0 + lane < pr.n) {
 #pragma unroll 4
             for (int r = 0; r < 32; ++r) {
               float o = stage_read_elem(stg, lane, r);
-              if (row0 + r < p.m) {
-                if (p.add) o += out_load(p.add, (int64_t)(row0 + r) * p.ldadd + col0 + lane, kOutF32);
+              if (row0 + r < pr.m) {
+                if (pr.add) o += out_load(pr.add, (int64_t)(row0 + r) * pr.ldadd + col0 + lane, kOutF32);
                 out_store(out, (int64_t)(row0 + r) * ldo + col0 + lane, o, dt);
               }
             }
@@ -604,97 +645,10 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
   }
 }
 
-// ---------------------------------------------------------------------------
-// split tiles
-// ---------------------------------------------------------------------------
-// Adds a tile's parts in the order of k, four columns a thread.  Tiles that one
-// worker had whole are done already.  Every worker has a block of k at least,
-// so the parts of a tile are those of consecutive workers, and only the first
-// can have begun in an earlier tile (its second slot).
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_constant__ FusedGemmParams p, int tile, int workers) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t u0 = (int64_t)blockIdx.x * p.num_k_blk, u1 = u0 + p.num_k_blk;
-  const int w0 = (int)(((u0 + 1) * workers - 1) / p.units);                     // the last that begins at u0 or before
-  const int n = (int)((u1 * workers + p.units - 1) / p.units) - w0;             // up to the last that begins before u1
-  if (n == 1) return;
-  const FusedTile tc = fused_tile(p, p.whole_tiles + (int)blockIdx.x);
-  const bool second = tc.mb >= p.mb_second;
-  const int per_row = tile / 4;
-  const int i = blockIdx.y * kJoinThreads + threadIdx.x;
-  const int r = i / per_row, c = i % per_row * 4;
-  const int row = (second ? tc.mb - p.mb_second : tc.mb) * tile + r, col = tc.nb * tile + c;
-  const Pow2 sc = warp_scale(p.scale, p.scale_exp);
-  if (row >= p.m || col >= p.n) return;
-  const int64_t slot = (int64_t)tile * tile;
-  const float* at = p.slots + (int64_t)r * tile + c;
-  float4 o = out_load4(at, (2 * w0 + (first_unit(p.units, w0, workers) < u0 ? 1 : 0)) * slot, kOutF32);
-#pragma unroll 4
-  for (int j = 1; j < n; ++j) {
-    const float4 y = out_load4(at, 2 * (w0 + j) * slot, kOutF32);
-    o.x += y.x;
-    o.y += y.y;
-    o.z += y.z;
-    o.w += y.w;
-  }
-  o.x *= sc.inv;
-  o.y *= sc.inv;
-  o.z *= sc.inv;
-  o.w *= sc.inv;
-  void* out = p.out[second ? 1 : 0];
-  const int64_t ldo = p.ldo[second ? 1 : 0];
-  if (p.out_vec[second ? 1 : 0] && col + 4 <= p.n) {
-    if (p.add) {
-      const float4 y = out_load4(p.add, (int64_t)row * p.ldadd + col, kOutF32);
-      o.x += y.x;
-      o.y += y.y;
-      o.z += y.z;
-      o.w += y.w;
-    }
-    out_store4(out, (int64_t)row * ldo + col, o, p.out_dtype);
-  } else {
-    const float e[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (col + j < p.n)
-        out_store(out, (int64_t)row * ldo + col + j,
-                  p.add ? e[j] + out_load(p.add, (int64_t)row * p.ldadd + col + j, kOutF32) : e[j], p.out_dtype);
-  }
-}
-
-template <FusedEpi E>
-void fill(bool pair, FusedKernel* out) {
-  using One = FusedTraits<E, false>;
-  using Two = FusedTraits<E, true>;
-  out->fn = pair ? reinterpret_cast<const void*>(&fused_gemm_kernel<Two>) : reinterpret_cast<const void*>(&fused_gemm_kernel<One>);
-  out->block = Two::kThreads;
-  out->smem_bytes = pair ? Two::kSmemBytes : One::kSmemBytes;
-  out->tile = pair ? Two::kTile : One::kTile;
-  out->ctas = pair ? 2 : 1;
+template <class T>
+FusedKernel fused_describe() {
+  return FusedKernel{reinterpret_cast<const void*>(&fused_gemm_kernel<T>), T::kThreads, T::kSmemBytes, T::kTile, T::kCtas};
 }
 
 }  // namespace
-
-void fused_lookup(FusedEpi epi, bool pair, FusedKernel* out) {
-  switch (epi) {
-    case FusedEpi::kPlain: fill<FusedEpi::kPlain>(pair, out); break;
-    case FusedEpi::kGated: fill<FusedEpi::kGated>(pair, out); break;
-    case FusedEpi::kGatedGrad: fill<FusedEpi::kGatedGrad>(pair, out); break;
-    case FusedEpi::kStats: fill<FusedEpi::kStats>(pair, out); break;
-    case FusedEpi::kProb: fill<FusedEpi::kProb>(pair, out); break;
-  }
-}
-
-cudaError_t launch_fused_join(const FusedGemmParams& p, int tile, int workers, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.num_tiles - p.whole_tiles), (unsigned)(tile * tile / 4 / kJoinThreads));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  cfg.numAttrs = (unsigned)launch_attributes(attr, 1);
-  cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, fused_join_kernel, p, tile, workers);
-}
-
 }  // namespace mpg

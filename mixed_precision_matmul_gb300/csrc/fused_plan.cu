@@ -1,6 +1,7 @@
 // Host side of the products with fused epilogues: which form a product takes,
 // how its tiles are dealt out, and the launch.
 #include <cstring>
+#include <utility>
 
 #include "fused.h"
 
@@ -74,22 +75,37 @@ mpg_status fused_map(CUtensorMap* map, const void* ptr, int64_t ld, mpg_dtype dt
   return mn_major ? encode_map(map, x, rows, k, 1, 64, 64) : encode_map(map, x, k, rows, 1, 64, 64);
 }
 
-mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& p, float* slots, cudaStream_t stream) {
-  FusedKernel one, two;
-  fused_lookup(l.epi, false, &one);
-  fused_lookup(l.epi, true, &two);
+namespace {
+
+struct Forms {
+  FusedKernel kernel[2];               // on single CTAs, on pairs
+  int64_t workers[2];
+};
+mpg_status forms_of(DeviceInfo* dev, FusedEpi epi, int act, Forms* f) {
+  for (int pair = 0; pair < 2; ++pair) {
+    FusedKernel* k = &f->kernel[pair];
+    switch (epi) {
+      case FusedEpi::kPlain: fused_lookup_plain(pair, k); break;
+      case FusedEpi::kGated: fused_lookup_gated(pair, act, k); break;
+      case FusedEpi::kGatedGrad: fused_lookup_gated_grad(pair, act, k); break;
+      default: fused_lookup_loss(epi, pair, k);
+    }
+  }
   int pairs = 0;
+  const FusedKernel& two = f->kernel[1];
   mpg_status st = resident_clusters(dev, two.fn, two.block, two.smem_bytes, 2, &pairs);
   if (st != MPG_OK) return st;
-  if ((st = allow_smem(dev, one.fn, one.smem_bytes)) != MPG_OK) return st;
-  const Shape s1 = shape_of(l, one.tile), s2 = shape_of(l, two.tile);
-  const bool split = l.split && slots;
-  const Deal d1 = deal(l, s1, one.tile, std::min(dev->sm_count, kMaxCtas), kOneEdge, kOneBlock, split);
-  const Deal d2 = deal(l, s2, two.tile, std::min<int64_t>(pairs, kMaxPairs), kPairEdge, kPairBlock, split);
-  const bool pair = d2.time < d1.time;
-  const Shape& s = pair ? s2 : s1;
-  const Deal& d = pair ? d2 : d1;
-  const FusedKernel& k = pair ? two : one;
+  f->workers[0] = std::min(dev->sm_count, kMaxCtas);
+  f->workers[1] = std::min<int64_t>(pairs, kMaxPairs);
+  return allow_smem(dev, f->kernel[0].fn, f->kernel[0].smem_bytes);
+}
+Deal deal_form(const FusedLaunch& l, const Forms& f, int pair, bool split) {
+  const int64_t tile = f.kernel[pair].tile;
+  return deal(l, shape_of(l, tile), tile, f.workers[pair], pair ? kPairEdge : kOneEdge, pair ? kPairBlock : kOneBlock, split);
+}
+
+mpg_status fill_product(FusedProduct& p, const FusedLaunch& l, int64_t tile, bool pair) {
+  const Shape s = shape_of(l, tile);
   if (s.tiles > kFusedMaxExtent || s.units / s.tiles > kFusedMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
   p.m = (int32_t)l.m;
   p.n = (int32_t)l.n;
@@ -100,13 +116,16 @@ mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& 
   p.mb_second = l.second_m ? (int32_t)s.mb : INT32_MAX;
   p.num_tiles = (int32_t)s.tiles;
   p.group_m = pair ? 8 : 16;
-  p.whole_tiles = (int32_t)d.whole;
-  p.units = (s.tiles - d.whole) * p.num_k_blk;
+  return MPG_OK;
+}
+
+mpg_status launch(DeviceInfo* dev, const FusedKernel& k, FusedGemmParams& p, int64_t workers, float* slots, cudaStream_t stream) {
+  p.units = (int64_t)(p.prod[0].num_tiles - p.whole_tiles) * p.prod[0].num_k_blk;
   p.slots = slots;
   p.status = dev->status;
   p.wait_limit_ns = kDefaultWaitNs;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(d.workers * k.ctas));
+  cfg.gridDim = dim3((unsigned)(workers * k.ctas));
   cfg.blockDim = dim3((unsigned)k.block);
   cfg.dynamicSmemBytes = (size_t)k.smem_bytes;
   cfg.stream = stream;
@@ -117,10 +136,82 @@ mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& 
   cudaError_t e = cudaLaunchKernelExC(&cfg, k.fn, args);
   if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "product launch: %s", cudaGetErrorString(e));
   if (p.units) {
-    e = launch_fused_join(p, k.tile, (int)d.workers, stream);
+    e = launch_fused_join(p, k.tile, (int)workers, stream);
     if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "join launch: %s", cudaGetErrorString(e));
   }
   return MPG_OK;
+}
+
+}  // namespace
+
+mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& p, float* slots, cudaStream_t stream) {
+  Forms f;
+  mpg_status s = forms_of(dev, l.epi, p.act, &f);
+  if (s != MPG_OK) return s;
+  const bool split = l.split && slots;
+  const Deal d1 = deal_form(l, f, 0, split), d2 = deal_form(l, f, 1, split);
+  const int pair = d2.time < d1.time;
+  const Deal& d = pair ? d2 : d1;
+  if ((s = fill_product(p.prod[0], l, f.kernel[pair].tile, pair)) != MPG_OK) return s;
+  p.prod[1].num_tiles = 0;
+  p.whole_tiles = (int32_t)d.whole;
+  return launch(dev, f.kernel[pair], p, d.workers, slots, stream);
+}
+
+// In one launch the second product's tiles fill what the first's last round
+// leaves, and one way in and out is saved: 4096 tokens' gradients over 32768
+// classes and 2048 channels take 1728 blocks of k a worker instead of 1920.
+mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedLaunch& l1, FusedGemmParams& p, float* slots,
+                            cudaStream_t stream) {
+  Forms f;
+  mpg_status s = forms_of(dev, FusedEpi::kPlain, 0, &f);
+  if (s != MPG_OK) return s;
+  const FusedLaunch* l[2] = {&l0, &l1};
+  const Shape first = shape_of(l0, 256), second = shape_of(l1, 256);
+  const bool swap = second.units / second.tiles > first.units / first.tiles;     // the longer k goes first
+  if (swap) {
+    std::swap(l[0], l[1]);
+    std::swap(p.prod[0], p.prod[1]);
+  }
+  double apart = 0.0;
+  for (const FusedLaunch* x : l) apart += std::min(deal_form(*x, f, 0, slots != nullptr).time, deal_form(*x, f, 1, slots != nullptr).time);
+  double best = apart;
+  int form = -1;
+  int64_t late = 0, late_workers = 0, late_rounds = 0;
+  for (int pair = 0; pair < 2; ++pair) {
+    const int64_t tile = f.kernel[pair].tile, w = f.workers[pair];
+    const Shape a = shape_of(*l[0], tile), b = shape_of(*l[1], tile);
+    const int64_t ka = a.units / a.tiles, kb = b.units / b.tiles;
+    const int64_t busy = a.tiles % w;                                             // workers with one tile more than the others
+    const int64_t idle = busy ? w - busy : 0;
+    const int64_t rounds = std::min(idle ? ka / kb : 0, idle ? (b.tiles + idle - 1) / idle : 0);
+    const int64_t rest = std::max<int64_t>(0, b.tiles - rounds * idle);
+    const double blocks = (double)((a.tiles + w - 1) / w * ka + (rest + w - 1) / w * kb);
+    const double time = (pair ? kPairEdge : kOneEdge) + blocks * (pair ? kPairBlock : kOneBlock);
+    if (time < best) {
+      best = time;
+      form = pair;
+      late = busy;
+      late_workers = idle;
+      late_rounds = rounds;
+    }
+  }
+  if (form < 0) {
+    // apart: one after the other
+    FusedProduct other = p.prod[1];
+    if ((s = launch_fused(dev, *l[0], p, slots, stream)) != MPG_OK) return s;
+    p.prod[0] = other;
+    return launch_fused(dev, *l[1], p, slots, stream);
+  }
+  const FusedKernel& k = f.kernel[form];
+  for (int i = 0; i < 2; ++i)
+    if ((s = fill_product(p.prod[i], *l[i], k.tile, form)) != MPG_OK) return s;
+  p.whole_tiles = p.prod[0].num_tiles;
+  p.late = (int32_t)late;
+  p.late_workers = (int32_t)late_workers;
+  p.late_rounds = (int32_t)late_rounds;
+  const int64_t tiles = (int64_t)p.prod[0].num_tiles + p.prod[1].num_tiles;
+  return launch(dev, k, p, std::min(f.workers[form], tiles), slots, stream);
 }
 
 }  // namespace mpg

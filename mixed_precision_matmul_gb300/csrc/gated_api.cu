@@ -185,17 +185,17 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
   if ((s = make_copies(dev, {&o.x, &o.wg, &o.wu}, static_cast<uint8_t*>(workspace), st)) != MPG_OK) return s;
   FusedGemmParams p;
   std::memset(&p, 0, sizeof(p));
-  if ((s = fused_map(&p.map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
-  if ((s = fused_map(&p.map_b[0], o.wg.ptr, o.wg.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
-  if ((s = fused_map(&p.map_b[1], o.wu.ptr, o.wu.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
+  if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
+  if ((s = fused_map(&p.prod[0].map_b[0], o.wg.ptr, o.wg.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
+  if ((s = fused_map(&p.prod[0].map_b[1], o.wu.ptr, o.wu.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
   p.bf16 = l.dtype == MPG_BF16;
   p.act = (int32_t)l.act;
   void* const out[3] = {Y, G, U};
   const int64_t ld[3] = {ldy, ldg, ldu};
   for (int i = 0; i < 3; ++i) {
-    p.out[i] = out[i];
-    p.ldo[i] = ld[i];
-    p.out_vec[i] = fused_lines_ok(out[i], ld[i]);
+    p.prod[0].out[i] = out[i];
+    p.prod[0].ldo[i] = ld[i];
+    p.prod[0].out_vec[i] = fused_lines_ok(out[i], ld[i]);
   }
   return launch_fused(dev, product(FusedEpi::kGated, l.tokens, l.inner, l.hidden), p, nullptr, st);
 }
@@ -289,15 +289,15 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
   } else {
     FusedGemmParams p;
     std::memset(&p, 0, sizeof(p));
-    if ((s = fused_map(&p.map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
-    if ((s = fused_map(&p.map_b[0], o.wg.ptr, o.wg.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
-    if ((s = fused_map(&p.map_b[1], o.wu.ptr, o.wu.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
+    if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
+    if ((s = fused_map(&p.prod[0].map_b[0], o.wg.ptr, o.wg.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
+    if ((s = fused_map(&p.prod[0].map_b[1], o.wu.ptr, o.wu.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
     p.bf16 = l.dtype == MPG_BF16;
     p.act = (int32_t)l.act;
-    p.out[0] = dg;
-    p.out[1] = du;
-    p.ldo[0] = p.ldo[1] = o.ldd;
-    p.out_vec[0] = p.out_vec[1] = 1;
+    p.prod[0].out[0] = dg;
+    p.prod[0].out[1] = du;
+    p.prod[0].ldo[0] = p.prod[0].ldo[1] = o.ldd;
+    p.prod[0].out_vec[0] = p.prod[0].out_vec[1] = 1;
     p.dy = dY;
     p.lddy = lddy;
     p.dy_vec = fused_lines_ok(dY, lddy);
@@ -305,48 +305,44 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     p.scale_exp = kExp;
     if ((s = launch_fused(dev, product(FusedEpi::kGatedGrad, l.tokens, l.inner, l.hidden), p, nullptr, st)) != MPG_OK) return s;
   }
+  FusedGemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.bf16 = !half;
+  p.scale = half ? partial : nullptr;
+  p.scale_exp = kExp;
+  const void* const d[2] = {dg, du};
+  int count = 0;
   if (dX) {
     // dX = dgate Wg + dup Wu
-    FusedGemmParams p;
-    std::memset(&p, 0, sizeof(p));
-    const void* const d[2] = {dg, du};
+    FusedProduct& x = p.prod[count++];
     const Source* const w[2] = {&o.wg, &o.wu};
     for (int i = 0; i < 2; ++i) {
-      if ((s = fused_map(&p.map_a[i], d[i], o.ldd, l.dtype, false, l.tokens, l.inner)) != MPG_OK) return s;
-      if ((s = fused_map(&p.map_b[i], w[i]->ptr, w[i]->ld, l.dtype, true, l.hidden, l.inner)) != MPG_OK) return s;
+      if ((s = fused_map(&x.map_a[i], d[i], o.ldd, l.dtype, false, l.tokens, l.inner)) != MPG_OK) return s;
+      if ((s = fused_map(&x.map_b[i], w[i]->ptr, w[i]->ld, l.dtype, true, l.hidden, l.inner)) != MPG_OK) return s;
     }
-    p.b_mn_major = 1;
-    p.bf16 = l.dtype == MPG_BF16;
-    p.out[0] = dX;
-    p.ldo[0] = lddx;
-    p.out_vec[0] = fused_lines_ok(dX, lddx);
-    p.out_dtype = (int32_t)l.dtype;
-    p.scale = half ? partial : nullptr;
-    p.scale_exp = kExp;
-    if ((s = launch_fused(dev, input_gradient(layer), p, slots, st)) != MPG_OK) return s;
+    x.b_mn_major = 1;
+    x.out[0] = dX;
+    x.ldo[0] = lddx;
+    x.out_vec[0] = fused_lines_ok(dX, lddx);
+    x.out_dtype = (int32_t)l.dtype;
   }
   if (dWg) {
     // dWg = dgate^T X, dWu = dup^T X
-    FusedGemmParams p;
-    std::memset(&p, 0, sizeof(p));
-    const void* const d[2] = {dg, du};
+    FusedProduct& w = p.prod[count++];
     for (int i = 0; i < 2; ++i)
-      if ((s = fused_map(&p.map_a[i], d[i], o.ldd, l.dtype, true, l.inner, l.tokens)) != MPG_OK) return s;
-    if ((s = fused_map(&p.map_b[0], o.x.ptr, o.x.ld, l.dtype, true, l.hidden, l.tokens)) != MPG_OK) return s;
-    p.a_mn_major = p.b_mn_major = 1;
-    p.bf16 = l.dtype == MPG_BF16;
-    p.out[0] = dWg;
-    p.out[1] = dWu;
-    p.ldo[0] = lddwg;
-    p.ldo[1] = lddwu;
-    p.out_vec[0] = fused_lines_ok(dWg, lddwg);
-    p.out_vec[1] = fused_lines_ok(dWu, lddwu);
-    p.out_dtype = (int32_t)l.dtype;
-    p.scale = half ? partial : nullptr;
-    p.scale_exp = kExp;
-    if ((s = launch_fused(dev, weight_gradient(layer), p, slots, st)) != MPG_OK) return s;
+      if ((s = fused_map(&w.map_a[i], d[i], o.ldd, l.dtype, true, l.inner, l.tokens)) != MPG_OK) return s;
+    if ((s = fused_map(&w.map_b[0], o.x.ptr, o.x.ld, l.dtype, true, l.hidden, l.tokens)) != MPG_OK) return s;
+    w.a_mn_major = w.b_mn_major = 1;
+    w.out[0] = dWg;
+    w.out[1] = dWu;
+    w.ldo[0] = lddwg;
+    w.ldo[1] = lddwu;
+    w.out_vec[0] = fused_lines_ok(dWg, lddwg);
+    w.out_vec[1] = fused_lines_ok(dWu, lddwu);
+    w.out_dtype = (int32_t)l.dtype;
   }
-  return MPG_OK;
+  if (count == 2) return launch_fused_two(dev, input_gradient(layer), weight_gradient(layer), p, slots, st);
+  return launch_fused(dev, dX ? input_gradient(layer) : weight_gradient(layer), p, slots, st);
 }
 
 }  // extern "C"

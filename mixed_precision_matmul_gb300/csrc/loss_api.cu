@@ -174,8 +174,8 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
     if ((s = make_copies(dev, o, ws, st)) != MPG_OK) return s;
     FusedGemmParams p;
     std::memset(&p, 0, sizeof(p));
-    if ((s = fused_map(&p.map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
-    if ((s = fused_map(&p.map_b[0], o.w.ptr, o.w.ld, l.dtype, false, l.vocab, l.hidden)) != MPG_OK) return s;
+    if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
+    if ((s = fused_map(&p.prod[0].map_b[0], o.w.ptr, o.w.ld, l.dtype, false, l.vocab, l.hidden)) != MPG_OK) return s;
     p.bf16 = l.dtype == MPG_BF16;
     p.target = l.target;
     p.target_bytes = l.target_bytes;
@@ -185,7 +185,7 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
     p.stats = stats;
     p.target_logit = target_logit;
     if ((s = launch_fused(dev, product(FusedEpi::kStats, l.tokens, l.vocab, l.hidden), p, nullptr, st)) != MPG_OK) return s;
-    j.parts = 2 * p.num_n_blk;
+    j.parts = 2 * p.prod[0].num_n_blk;
   }
   j.stats = stats;
   j.rows = l.tokens;
@@ -263,12 +263,12 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
     const uint16_t* w = static_cast<const uint16_t*>(o.w.ptr) + c0 * o.w.ld;
     FusedGemmParams p;
     std::memset(&p, 0, sizeof(p));
-    if ((s = fused_map(&p.map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
-    if ((s = fused_map(&p.map_b[0], w, o.w.ld, l.dtype, false, cols, l.hidden)) != MPG_OK) return s;
+    if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
+    if ((s = fused_map(&p.prod[0].map_b[0], w, o.w.ld, l.dtype, false, cols, l.hidden)) != MPG_OK) return s;
     p.bf16 = !half;
-    p.out[0] = grad;
-    p.ldo[0] = o.piece;
-    p.out_vec[0] = 1;
+    p.prod[0].out[0] = grad;
+    p.prod[0].ldo[0] = o.piece;
+    p.prod[0].out_vec[0] = 1;
     p.target = l.target;
     p.target_bytes = l.target_bytes;
     p.target_stride = l.target_stride;
@@ -281,37 +281,38 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
     p.scale = half ? partial : nullptr;
     p.scale_exp = kExp;
     if ((s = launch_fused(dev, product(FusedEpi::kProb, l.tokens, cols, l.hidden), p, nullptr, st)) != MPG_OK) return s;
+    std::memset(&p, 0, sizeof(p));
+    p.bf16 = !half;
+    p.scale = half ? partial : nullptr;
+    p.scale_exp = kExp;
+    int count = 0;
+    const FusedLaunch to_x = product(FusedEpi::kPlain, l.tokens, l.hidden, cols);
+    const FusedLaunch to_w = product(FusedEpi::kPlain, cols, l.hidden, l.tokens);
     if (dX) {
       const bool last = i + 1 == o.pieces;
-      std::memset(&p, 0, sizeof(p));
-      if ((s = fused_map(&p.map_a[0], grad, o.piece, l.dtype, false, l.tokens, cols)) != MPG_OK) return s;
-      if ((s = fused_map(&p.map_b[0], w, o.w.ld, l.dtype, true, l.hidden, cols)) != MPG_OK) return s;
-      p.b_mn_major = 1;
-      p.bf16 = !half;
-      p.out[0] = last ? dX : sum;
-      p.ldo[0] = last ? lddx : o.ldsum;
-      p.out_dtype = last ? (int32_t)l.dtype : (int32_t)MPG_F32;
-      p.out_vec[0] = last ? fused_lines_ok(dX, lddx) : 1;
-      p.add = i > 0 ? sum : nullptr;
-      p.ldadd = o.ldsum;
-      p.scale = half ? partial : nullptr;
-      p.scale_exp = kExp;
-      if ((s = launch_fused(dev, product(FusedEpi::kPlain, l.tokens, l.hidden, cols), p, slots, st)) != MPG_OK) return s;
+      FusedProduct& x = p.prod[count++];
+      if ((s = fused_map(&x.map_a[0], grad, o.piece, l.dtype, false, l.tokens, cols)) != MPG_OK) return s;
+      if ((s = fused_map(&x.map_b[0], w, o.w.ld, l.dtype, true, l.hidden, cols)) != MPG_OK) return s;
+      x.b_mn_major = 1;
+      x.out[0] = last ? dX : sum;
+      x.ldo[0] = last ? lddx : o.ldsum;
+      x.out_dtype = last ? (int32_t)l.dtype : (int32_t)MPG_F32;
+      x.out_vec[0] = last ? fused_lines_ok(dX, lddx) : 1;
+      x.add = i > 0 ? sum : nullptr;
+      x.ldadd = o.ldsum;
     }
     if (dW) {
-      std::memset(&p, 0, sizeof(p));
-      if ((s = fused_map(&p.map_a[0], grad, o.piece, l.dtype, true, cols, l.tokens)) != MPG_OK) return s;
-      if ((s = fused_map(&p.map_b[0], o.x.ptr, o.x.ld, l.dtype, true, l.hidden, l.tokens)) != MPG_OK) return s;
-      p.a_mn_major = p.b_mn_major = 1;
-      p.bf16 = !half;
-      p.out[0] = static_cast<uint16_t*>(dW) + c0 * lddw;
-      p.ldo[0] = lddw;
-      p.out_dtype = (int32_t)l.dtype;
-      p.out_vec[0] = fused_lines_ok(p.out[0], lddw);
-      p.scale = half ? partial : nullptr;
-      p.scale_exp = kExp;
-      if ((s = launch_fused(dev, product(FusedEpi::kPlain, cols, l.hidden, l.tokens), p, slots, st)) != MPG_OK) return s;
+      FusedProduct& y = p.prod[count++];
+      if ((s = fused_map(&y.map_a[0], grad, o.piece, l.dtype, true, cols, l.tokens)) != MPG_OK) return s;
+      if ((s = fused_map(&y.map_b[0], o.x.ptr, o.x.ld, l.dtype, true, l.hidden, l.tokens)) != MPG_OK) return s;
+      y.a_mn_major = y.b_mn_major = 1;
+      y.out[0] = static_cast<uint16_t*>(dW) + c0 * lddw;
+      y.ldo[0] = lddw;
+      y.out_dtype = (int32_t)l.dtype;
+      y.out_vec[0] = fused_lines_ok(y.out[0], lddw);
     }
+    s = count == 2 ? launch_fused_two(dev, to_x, to_w, p, slots, st) : launch_fused(dev, dX ? to_x : to_w, p, slots, st);
+    if (s != MPG_OK) return s;
   }
   return MPG_OK;
 }
