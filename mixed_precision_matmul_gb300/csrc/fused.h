@@ -80,14 +80,13 @@ struct FusedKernel {
   int block, smem_bytes;
   int tile;                         // rows of a tile, and columns of its accumulators
   int ctas;
+  // sums the parts of split tiles and does the epilogue's work
+  cudaError_t (*join)(const FusedGemmParams& p, int workers, cudaStream_t stream);
 };
 void fused_lookup_plain(bool pair, FusedKernel* out);
 void fused_lookup_gated(bool pair, int act, FusedKernel* out);
 void fused_lookup_gated_grad(bool pair, int act, FusedKernel* out);
 void fused_lookup_loss(FusedEpi epi, bool pair, FusedKernel* out);
-// Sums the parts of split tiles (kPlain).
-cudaError_t launch_fused_join(const FusedGemmParams& p, int tile, int workers, cudaStream_t stream);
-
 // The product of few rows: gated (wu given) or the statistics of logits.
 struct FewRowsParams {
   const void *x, *w, *wu;           // X: rows x k; weights: n x k
@@ -166,7 +165,6 @@ struct FusedLaunch {
   int64_t m, n, k;                  // k: of the first part where there are two
   bool second_k = false;            // the second part of k has the same length
   bool second_m = false;            // a second matrix of m rows
-  bool split = false;               // tiles may be split along k (kPlain)
 };
 mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& p, float* slots, cudaStream_t stream);
 // Both of p's products, in one launch where that takes less.

@@ -26,13 +26,14 @@
 // Accumulators are double-buffered in TMEM, so the epilogue runs beside the
 // next tile's products.
 //
-// Tiles go round by round to the workers.  What does not fill a round may be split
-// (kPlain): its blocks of k are dealt out evenly, each worker getting one run of
-// them, and a worker whose run holds only a part of a tile's k leaves its sums
-// in a slot.  A second launch adds the slots of a tile in the order of k: the
-// result does not depend on timing.  Or a second product's tiles, shorter ones,
-// fill the first's last round: the gradients of an input and of a weight are two
-// products from the same D, and in one launch no worker waits for the other's end.
+// Tiles go round by round to the workers.  What does not fill a round may be split:
+// its blocks of k are dealt out evenly, each worker getting one run of them, and a
+// worker whose run holds only a part of a tile's k leaves its sums in a slot.  A
+// second launch adds the slots of a tile in the order of k and does the epilogue's
+// work: the result does not depend on timing.  Or (kPlain) a second product's
+// tiles, shorter ones, fill the first's last round: the gradients of an input and
+// of a weight are two products from the same D, and in one launch no worker waits
+// for the other's end.
 //
 // Waits are bounded, and a timeout raises the abort flag of both CTAs: every
 // role drains what it has in flight before TMEM is released.
@@ -170,6 +171,16 @@ __device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&
   __syncwarp();
 }
 
+// The class of a token (-1: ignored, -2: none), and the weight of its gradient: an
+// ignored token has none, whatever its dloss; one of no class gives NaN.
+__device__ __forceinline__ int64_t row_target(const FusedGemmParams& p, int row) {
+  return target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, row);
+}
+__device__ __forceinline__ float row_weight(const FusedGemmParams& p, int row, int64_t target, float mul) {
+  if (target < 0) return target == -1 ? 0.0f : NAN;
+  return mul * ld_global(p.dloss + (int64_t)row * p.dloss_stride);
+}
+
 struct FusedTile {
   int mb, nb;
 };
@@ -210,7 +221,7 @@ struct FusedItems {
       u1 = first_unit(p.units, w + 1, n);
     }
   }
-  template <bool kMore>
+  template <bool kMore>                              // whether there may be a second product
   __device__ __forceinline__ bool next(const FusedGemmParams& p, FusedItem& x) {
     int tile;
     x.which = 0;
@@ -220,7 +231,7 @@ struct FusedItems {
     if (t < p.whole_tiles) {
       tile = t;
       t += workers;
-    } else if (kMore && u < u1) {
+    } else if (u < u1) {
       const int64_t j = u / p.prod[0].num_k_blk;
       tile = p.whole_tiles + (int)j;
       x.kb0 = (int)(u - j * p.prod[0].num_k_blk);
@@ -442,16 +453,36 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
       float lse2 = 0.0f, weight = 0.0f;
       if constexpr (T::kEpi == FusedEpi::kStats || T::kEpi == FusedEpi::kProb) {
         if (row < pr.m) {
-          target = target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, row);
+          target = row_target(p, row);
           if constexpr (T::kEpi == FusedEpi::kProb) {
             lse2 = kLog2e * ld_global(p.lse + row);
-            // an ignored token has no gradient, whatever its dloss; one of no class gives NaN
-            weight = target == -1 ? 0.0f : target == -2 ? __int_as_float(0x7fffffff) : sc.mul * ld_global(p.dloss + (int64_t)row * p.dloss_stride);
+            weight = row_weight(p, row, target, sc.mul);
           }
         }
       }
       if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
       tc_fence_after_sync();
+      if (x.slot >= 0) {
+        // sums of a part of k, as they are: rows of the tile, whole lines a store
+        float* slot = p.slots + (int64_t)x.slot * (T::kTile * T::kTile) + (int64_t)((int)rank * T::BM + 32 * q) * T::kTile;
+        constexpr int kAll = T::kTile / 64;
+#pragma unroll 1
+        for (int cc = half * kAll; cc < (half + 1) * kAll; ++cc) {
+          float v[32];
+          tmem_ld_32cols(tacc + cc * 32, v);
+          tmem_ld_wait();
+          if (cc == (half + 1) * kAll - 1) release();
+          if (row0 >= pr.m) continue;
+          stage_write_row(stg, lane, v);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(slot + (i * 4 + (lane >> 3)) * T::kTile + cc * 32 + (lane & 7) * 4) =
+                stage_read_chunk(stg, lane, i);
+          __syncwarp();
+        }
+        continue;
+      }
 
       if constexpr (T::kTwo) {
 #pragma unroll 1
@@ -505,7 +536,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           if (cc == cc0 + kCc - 1) release();
           if (cc * 32 >= last) continue;
           // (a bit for the target's column: compared with its index, the values went to local memory)
-          const int64_t at = target - (p.col0 + col_tile + cc * 32);
+          const int64_t at = target - (p.col0 + col_tile + cc * 32);   // (without a class: below 0)
           const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
           if (mine) {
             float l = 0.0f;
@@ -565,11 +596,9 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
         }
       } else {
         const int dt = pr.out_dtype;
-        const bool part = x.slot >= 0;
         void* out = pr.out[second ? 1 : 0];
         const int64_t ldo = pr.ldo[second ? 1 : 0];
         const bool vec = pr.out_vec[second ? 1 : 0] != 0;
-        float* slot = p.slots + (int64_t)max(x.slot, 0) * (T::kTile * T::kTile);
 #pragma unroll 1
         for (int cc = cc0; cc < cc0 + kCc; ++cc) {
           float v[32];
@@ -578,17 +607,6 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           if (cc == cc0 + kCc - 1) release();
           const int col0 = col_tile + cc * 32;
           if (row0 >= pr.m || col0 >= pr.n) continue;
-          if (part) {
-            // sums of a part of k, as they are: rows of the tile, whole lines a store
-            stage_write_row(stg, lane, v);
-            __syncwarp();
-            float* to = slot + (int64_t)((int)rank * T::BM + 32 * q) * T::kTile + cc * 32;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(to + (i * 4 + (lane >> 3)) * T::kTile + (lane & 7) * 4) = stage_read_chunk(stg, lane, i);
-            __syncwarp();
-            continue;
-          }
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= sc.inv;
           if (dt != kOutF32 && !pr.add) {
@@ -645,9 +663,170 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
   }
 }
 
+// ---------------------------------------------------------------------------
+// split tiles
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void store_four(void* out, int64_t at, const float (&v)[4], int left, bool vec, int dt) {
+  if (vec && left >= 4) {
+    out_store4(out, at, make_float4(v[0], v[1], v[2], v[3]), dt);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < left) out_store(out, at + j, v[j], dt);
+  }
+}
+__device__ __forceinline__ void load_four(float (&v)[4], const void* src, int64_t at, int left, bool vec, int dt) {
+  if (vec && left >= 4) {
+    const float4 y = out_load4(src, at, dt);
+    v[0] = y.x;
+    v[1] = y.y;
+    v[2] = y.z;
+    v[3] = y.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < left ? out_load(src, at + j, dt) : 0.0f;
+  }
+}
+
+// Adds a tile's parts in the order of k, four columns a thread, and does what the
+// epilogue does with the sums.  Tiles that one worker had whole are done already.
+// Every worker has a block of k at least, so the parts of a tile are those of
+// consecutive workers, and only the first can have begun in an earlier tile (its
+// second slot).
+constexpr int kJoinThreads = 256;
+template <class T>
+__global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_constant__ FusedGemmParams p, int workers) {
+  constexpr int kPerRow = T::kTileN / 4;
+  griddep_wait();
+  griddep_launch_dependents();
+  const FusedProduct& pr = p.prod[0];
+  const int64_t u0 = (int64_t)blockIdx.x * pr.num_k_blk, u1 = u0 + pr.num_k_blk;
+  const int w0 = (int)(((u0 + 1) * workers - 1) / p.units);                     // the last that begins at u0 or before
+  const int n = (int)((u1 * workers + p.units - 1) / p.units) - w0;             // up to the last that begins before u1
+  if (n == 1) return;
+  const FusedTile tc = fused_tile(pr, p.whole_tiles + (int)blockIdx.x);
+  const bool second = tc.mb >= pr.mb_second;
+  const int i = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int r = i / kPerRow, c = i % kPerRow * 4;
+  const int row = (second ? tc.mb - pr.mb_second : tc.mb) * T::kTile + r, col = tc.nb * T::kTileN + c;
+  const Pow2 sc = warp_scale(p.scale, p.scale_exp);
+  const bool in = row < pr.m;
+  const int left = pr.n - col;                       // columns of the matrix from here on
+  constexpr int64_t kSlot = T::kTile * T::kTile;
+  const int first = 2 * w0 + (first_unit(p.units, w0, workers) < u0 ? 1 : 0);
+  auto sum = [&](int column, float (&v)[4]) {
+    const float* at = p.slots + (int64_t)r * T::kTile + column;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (in && left > 0) {
+      o = out_load4(at, first * kSlot, kOutF32);
+#pragma unroll 4
+      for (int j = 1; j < n; ++j) {
+        const float4 y = out_load4(at, 2 * (w0 + j) * kSlot, kOutF32);
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+      }
+    }
+    v[0] = o.x;
+    v[1] = o.y;
+    v[2] = o.z;
+    v[3] = o.w;
+  };
+  const int type = p.bf16 ? kOutBF16 : kOutF16;
+  if constexpr (T::kTwo) {
+    float gt[4], up[4];
+    sum(c, gt);
+    sum(T::kTile / 2 + c, up);
+    if (!in || left <= 0) return;
+    auto at = [&](int k) { return (int64_t)row * pr.ldo[k] + col; };
+    if constexpr (T::kEpi == FusedEpi::kGated) {
+      if (pr.out[1]) {
+        store_four(pr.out[1], at(1), gt, left, pr.out_vec[1], type);
+        store_four(pr.out[2], at(2), up, left, pr.out_vec[2], type);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gt[j] = act_value(gt[j], T::kAct) * up[j];
+    } else {
+      float dy[4];
+      load_four(dy, p.dy, (int64_t)row * p.lddy + col, left, p.dy_vec, type);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a, d;
+        act_both(gt[j], T::kAct, a, d);
+        const float y = sc.mul * dy[j];
+        gt[j] = y * up[j] * d;
+        up[j] = y * a;
+      }
+      store_four(pr.out[1], at(1), up, left, pr.out_vec[1], type);
+    }
+    store_four(pr.out[0], at(0), gt, left, pr.out_vec[0], type);
+  } else {
+    float v[4];
+    sum(c, v);
+    if constexpr (T::kEpi == FusedEpi::kPlain) {
+      if (!in || left <= 0) return;
+      const int k = second ? 1 : 0;
+      float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (pr.add) load_four(y, pr.add, (int64_t)row * pr.ldadd + col, left, pr.out_vec[k], kOutF32);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], sc.inv, y[j]);
+      store_four(pr.out[k], (int64_t)row * pr.ldo[k] + col, v, left, pr.out_vec[k], pr.out_dtype);
+    } else {
+      const int64_t target = in ? row_target(p, row) : -1;
+      const int64_t at = target >= 0 ? target - (p.col0 + col) : -1;       // of these four columns: 0 .. 3
+      if constexpr (T::kEpi == FusedEpi::kStats) {
+        // half of the tile's columns of a row: kTile / 8 neighbouring lanes
+        constexpr int kWidth = T::kTile / 8;
+        float top = -INFINITY, s = 0.0f;
+        bool nan = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (at == j && j < left) p.target_logit[row] = v[j];
+          v[j] = j < left ? kLog2e * v[j] : -INFINITY;
+          nan = nan || v[j] != v[j];
+          top = fmaxf(top, v[j]);
+        }
+#pragma unroll
+        for (int o = kWidth / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float b = fabsf(top) == INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s += ex2(v[j] - b);
+        if (nan) s = NAN;
+#pragma unroll
+        for (int o = kWidth / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (in && i % kWidth == 0)
+          p.stats[(int64_t)(tc.nb * 2 + c / (T::kTile / 2)) * pr.m + row] = make_float2(top, s);
+      } else {
+        if (!in || left <= 0) return;
+        const float lse2 = kLog2e * ld_global(p.lse + row), weight = row_weight(p, row, target, sc.mul);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = ex2(fmaf(kLog2e, v[j], -lse2));
+          v[j] = weight == 0.0f ? 0.0f : weight * (at == j ? e - 1.0f : e);
+        }
+        store_four(pr.out[0], (int64_t)row * pr.ldo[0] + col, v, left, pr.out_vec[0], type);
+      }
+    }
+  }
+}
+
+template <class T>
+cudaError_t launch_fused_join(const FusedGemmParams& p, int workers, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.prod[0].num_tiles - p.whole_tiles), (unsigned)(T::kTile * T::kTileN / 4 / kJoinThreads));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  cfg.numAttrs = (unsigned)launch_attributes(attr, 1);
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, fused_join_kernel<T>, p, workers);
+}
+
 template <class T>
 FusedKernel fused_describe() {
-  return FusedKernel{reinterpret_cast<const void*>(&fused_gemm_kernel<T>), T::kThreads, T::kSmemBytes, T::kTile, T::kCtas};
+  return FusedKernel{reinterpret_cast<const void*>(&fused_gemm_kernel<T>), T::kThreads, T::kSmemBytes, T::kTile, T::kCtas,
+                     &launch_fused_join<T>};
 }
 
 }  // namespace

@@ -46,7 +46,7 @@ Deal deal(const FusedLaunch& l, const Shape& s, int64_t tile, int64_t most, doub
   const int64_t rounds = (s.tiles + most - 1) / most;
   Deal d{std::min(s.tiles, most), s.tiles, edge + (double)(rounds * kb) * block};
   const int64_t rest = s.tiles % most;
-  if (!may_split || !rest) return d;
+  if (!may_split || !rest || kb < 2) return d;
   const int64_t whole = s.tiles - rest;
   const int64_t workers = whole ? most : std::min(most, std::max(rest, rest * kb / kMinUnits));
   const double operands = 128.0 * (double)kb * (double)((l.second_m ? 2 : 1) * l.m + l.n);
@@ -64,6 +64,7 @@ size_t fused_slot_bytes(const FusedLaunch& l) {
   size_t most = 0;
   for (int64_t tile : {(int64_t)128, (int64_t)256}) {
     const Shape s = shape_of(l, tile);
+    if (s.units == s.tiles) return 0;                 // (one block of k is not split)
     const int64_t workers = std::min(tile == 256 ? kMaxPairs : (int64_t)kMaxCtas, std::max(s.tiles, s.units / kMinUnits));
     most = std::max(most, (size_t)(2 * workers * tile * tile) * sizeof(float));
   }
@@ -136,7 +137,7 @@ mpg_status launch(DeviceInfo* dev, const FusedKernel& k, FusedGemmParams& p, int
   cudaError_t e = cudaLaunchKernelExC(&cfg, k.fn, args);
   if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "product launch: %s", cudaGetErrorString(e));
   if (p.units) {
-    e = launch_fused_join(p, k.tile, (int)workers, stream);
+    e = k.join(p, (int)workers, stream);
     if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "join launch: %s", cudaGetErrorString(e));
   }
   return MPG_OK;
@@ -148,7 +149,7 @@ mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& 
   Forms f;
   mpg_status s = forms_of(dev, l.epi, p.act, &f);
   if (s != MPG_OK) return s;
-  const bool split = l.split && slots;
+  const bool split = slots != nullptr;
   const Deal d1 = deal_form(l, f, 0, split), d2 = deal_form(l, f, 1, split);
   const int pair = d2.time < d1.time;
   const Deal& d = pair ? d2 : d1;

@@ -1,5 +1,6 @@
 // mpg_gated_gemm and mpg_gated_gemm_backward: argument checks, workspace
 // layout, and the sequence of launches.
+#include <algorithm>
 #include <cstring>
 
 #include "fused.h"
@@ -56,7 +57,6 @@ FusedLaunch product(FusedEpi epi, int64_t m, int64_t n, int64_t k) {
   l.m = m;
   l.n = n;
   l.k = k;
-  l.split = epi == FusedEpi::kPlain;
   return l;
 }
 FusedLaunch input_gradient(const mpg_gated_layer* l) {
@@ -89,8 +89,12 @@ Layout layout(const mpg_gated_layer* l, bool backward) {
     o.dg = take((size_t)l->tokens * (size_t)o.ldd * 2);
     o.du = take((size_t)l->tokens * (size_t)o.ldd * 2);
     o.partial = take(kScaleBlocks * sizeof(float));
-    o.slots = take(std::max(fused_slot_bytes(input_gradient(l)), fused_slot_bytes(weight_gradient(l))));
   }
+  if (backward)
+    o.slots = take(std::max({fused_slot_bytes(input_gradient(l)), fused_slot_bytes(weight_gradient(l)),
+                             fused_slot_bytes(product(FusedEpi::kGatedGrad, l->tokens, l->inner, l->hidden))}));
+  else if (l->tokens > kFewRows)
+    o.slots = take(fused_slot_bytes(product(FusedEpi::kGated, l->tokens, l->inner, l->hidden)));
   o.bytes = at;
   return o;
 }
@@ -197,7 +201,8 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
     p.prod[0].ldo[i] = ld[i];
     p.prod[0].out_vec[i] = fused_lines_ok(out[i], ld[i]);
   }
-  return launch_fused(dev, product(FusedEpi::kGated, l.tokens, l.inner, l.hidden), p, nullptr, st);
+  return launch_fused(dev, product(FusedEpi::kGated, l.tokens, l.inner, l.hidden), p,
+                      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + o.slots), st);
 }
 
 size_t mpg_gated_gemm_backward_workspace_size(const mpg_gated_layer* layer) {
@@ -303,7 +308,7 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     p.dy_vec = fused_lines_ok(dY, lddy);
     p.scale = half ? partial : nullptr;
     p.scale_exp = kExp;
-    if ((s = launch_fused(dev, product(FusedEpi::kGatedGrad, l.tokens, l.inner, l.hidden), p, nullptr, st)) != MPG_OK) return s;
+    if ((s = launch_fused(dev, product(FusedEpi::kGatedGrad, l.tokens, l.inner, l.hidden), p, slots, st)) != MPG_OK) return s;
   }
   FusedGemmParams p;
   std::memset(&p, 0, sizeof(p));

@@ -1,5 +1,6 @@
 // mpg_linear_cross_entropy and mpg_linear_cross_entropy_backward: argument
 // checks, workspace layout, and the sequence of launches.
+#include <algorithm>
 #include <cstring>
 
 #include "fused.h"
@@ -59,7 +60,6 @@ FusedLaunch product(FusedEpi epi, int64_t m, int64_t n, int64_t k) {
   l.m = m;
   l.n = n;
   l.k = k;
-  l.split = epi == FusedEpi::kPlain;
   return l;
 }
 Layout layout(const mpg_vocab_loss* l, bool backward) {
@@ -81,6 +81,7 @@ Layout layout(const mpg_vocab_loss* l, bool backward) {
     const int64_t parts = t <= kFewRows ? few_rows_parts((int)t, l->vocab) : 2 * ((l->vocab + 127) / 128);
     o.stats = take((size_t)parts * (size_t)t * sizeof(float2));
     o.target_logit = take((size_t)t * sizeof(float));
+    if (t > kFewRows) o.slots = take(fused_slot_bytes(product(FusedEpi::kStats, t, l->vocab, l->hidden)));
   } else {
     int64_t piece = std::max<int64_t>(256, kPieceBytes / 2 / t / 256 * 256);
     o.pieces = (l->vocab + piece - 1) / piece;
@@ -91,8 +92,9 @@ Layout layout(const mpg_vocab_loss* l, bool backward) {
     o.ldsum = (l->hidden + 3) / 4 * 4;
     if (o.pieces > 1) o.sum = take((size_t)t * (size_t)o.ldsum * sizeof(float));
     o.partial = take(kScaleBlocks * sizeof(float));
-    o.slots = take(std::max(fused_slot_bytes(product(FusedEpi::kPlain, t, l->hidden, o.piece)),
-                            fused_slot_bytes(product(FusedEpi::kPlain, o.piece, l->hidden, t))));
+    o.slots = take(std::max({fused_slot_bytes(product(FusedEpi::kPlain, t, l->hidden, o.piece)),
+                             fused_slot_bytes(product(FusedEpi::kPlain, o.piece, l->hidden, t)),
+                             fused_slot_bytes(product(FusedEpi::kProb, t, o.piece, l->hidden))}));
   }
   o.bytes = at;
   return o;
@@ -184,7 +186,8 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
     p.vocab = (int32_t)l.vocab;
     p.stats = stats;
     p.target_logit = target_logit;
-    if ((s = launch_fused(dev, product(FusedEpi::kStats, l.tokens, l.vocab, l.hidden), p, nullptr, st)) != MPG_OK) return s;
+    if ((s = launch_fused(dev, product(FusedEpi::kStats, l.tokens, l.vocab, l.hidden), p,
+                          reinterpret_cast<float*>(ws + o.slots), st)) != MPG_OK) return s;
     j.parts = 2 * p.prod[0].num_n_blk;
   }
   j.stats = stats;
@@ -280,7 +283,7 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
     p.dloss_stride = dloss_stride;
     p.scale = half ? partial : nullptr;
     p.scale_exp = kExp;
-    if ((s = launch_fused(dev, product(FusedEpi::kProb, l.tokens, cols, l.hidden), p, nullptr, st)) != MPG_OK) return s;
+    if ((s = launch_fused(dev, product(FusedEpi::kProb, l.tokens, cols, l.hidden), p, slots, st)) != MPG_OK) return s;
     std::memset(&p, 0, sizeof(p));
     p.bf16 = !half;
     p.scale = half ? partial : nullptr;

@@ -51,7 +51,8 @@ def test_product(t, h, i, act):
         plain.check(ku, u, eu)
 
 
-@pytest.mark.parametrize("t,h,i,dtype", [(2048, 512, 4096, "bf16"), (1531, 520, 2741, "fp16"), (4100, 264, 1030, "bf16")])
+@pytest.mark.parametrize("t,h,i,dtype", [(2048, 512, 4096, "bf16"), (1531, 520, 2741, "fp16"), (4100, 264, 1030, "bf16"),
+                                         (200, 4000, 300, "bf16"), (40, 3999, 70, "fp16"), (600, 4096, 515, "bf16")])
 def test_product_on_pairs(t, h, i, dtype):
     x, wg, wu, _ = operands(t, h, i, dtype, 2)
     (y, g, u), (ey, eg, eu) = plain.gated(x, wg, wu, "silu")
@@ -76,7 +77,8 @@ def test_gradients(t, h, i, act):
                 plain.check(o, r, b)
 
 
-@pytest.mark.parametrize("t,h,i,dtype", [(2048, 512, 2000, "bf16"), (1500, 1032, 3000, "fp16"), (4200, 256, 1030, "bf16")])
+@pytest.mark.parametrize("t,h,i,dtype", [(2048, 512, 2000, "bf16"), (1500, 1032, 3000, "fp16"), (4200, 256, 1030, "bf16"),
+                                         (200, 4000, 300, "fp16"), (40, 3999, 70, "bf16"), (600, 4096, 515, "fp16")])
 def test_gradients_on_pairs(t, h, i, dtype):
     x, wg, wu, dy = operands(t, h, i, dtype, 4)
     _, g, u = mpg.gated_gemm(x, wg, wu, keep=True)
@@ -178,7 +180,11 @@ def test_nothing_is_written_beyond_the_results(t):
         return torch.full((rows + 2, cols + pad), mark, dtype=torch.bfloat16, device="cuda")
     import ctypes
     y, g, u = (room(t, i) for _ in range(3))
-    mpg.gated_gemm_raw(lay, *(v for b in (y, g, u) for v in (b.data_ptr(), i + pad)))
+    need = int(mpg.lib().mpg_gated_gemm_workspace_size(ctypes.byref(lay)))
+    ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+    mpg.gated_gemm_raw(lay, *(v for b in (y, g, u) for v in (b.data_ptr(), i + pad)), ws.data_ptr(), need)
+    ok()
+    assert (ws[need:] == 77).all()
     need = int(mpg.lib().mpg_gated_gemm_backward_workspace_size(ctypes.byref(lay)))
     ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
     outs = [room(t, h), room(i, h), room(i, h)]

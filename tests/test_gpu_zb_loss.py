@@ -33,7 +33,7 @@ SHAPES = [(1, 1, 1), (1, 64, 1000), (3, 100, 33), (8, 513, 40), (9, 64, 1003), (
           (33, 64, 64), (33, 1, 5), (40, 72, 1), (64, 100, 1003), (127, 128, 65), (130, 65, 70), (257, 200, 129), (300, 1001, 515)]
 
 
-@pytest.mark.parametrize("t,h,v", SHAPES + [(2048, 264, 4099), (600, 512, 20000)])
+@pytest.mark.parametrize("t,h,v", SHAPES + [(2048, 264, 4099), (600, 512, 20000), (200, 4000, 300), (40, 3999, 70), (600, 4096, 1003)])
 def test_loss(t, h, v):
     for dtype, pad, shift in (("bf16", 0, 0), ("fp16", 8, 8), ("bf16", 3, 1)):
         x, w, target = operands(t, h, v, dtype, 1, pad, shift)
@@ -45,7 +45,7 @@ def test_loss(t, h, v):
             plain.check(b, lse, el)
 
 
-@pytest.mark.parametrize("t,h,v", SHAPES + [(2000, 264, 4099), (40, 64, 30000), (5, 72, 50000)])
+@pytest.mark.parametrize("t,h,v", SHAPES + [(2000, 264, 4099), (40, 64, 30000), (5, 72, 50000), (200, 4000, 300), (40, 3999, 70), (600, 4096, 1003)])
 def test_gradients(t, h, v):
     for dtype, pad, shift in (("fp16", 0, 0), ("bf16", 8, 8), ("fp16", 3, 1)):
         x, w, target = operands(t, h, v, dtype, 2, pad, shift)
