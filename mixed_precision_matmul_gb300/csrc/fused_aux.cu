@@ -175,11 +175,11 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 }
 
 constexpr int kJoinThreads = 1024;
-// kRows rows a block (32: neighbouring lanes read neighbouring rows).
+// kRows rows a block (8: neighbouring lanes read 64 bytes of neighbouring rows).
 template <int kRows>
 __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_constant__ LossJoinParams p) {
   constexpr int kPer = kJoinThreads / kRows;            // threads of a row
-  __shared__ float2 part[kPer > 32 ? 32 : kPer][kRows > 1 ? kRows : 1];
+  __shared__ float2 part[kRows > 1 ? kPer : 32][kRows];
   griddep_wait();
   griddep_launch_dependents();
   const int r = threadIdx.x % kRows, s = threadIdx.x / kRows;
@@ -205,10 +205,13 @@ __global__ void __launch_bounds__(kJoinThreads) loss_join_kernel(const __grid_co
       x = join(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
     if (threadIdx.x) return;
   } else {
+    // pairs of threads, halving: the same order at any time
     part[s][r] = x;
-    __syncthreads();
+    for (int w = kPer / 2; w; w >>= 1) {
+      __syncthreads();
+      if (s < w) part[s][r] = x = join(x, part[s + w][r]);
+    }
     if (s) return;
-    for (int i = 1; i < kPer; ++i) x = join(x, part[i][r]);
   }
   if (row >= p.rows) return;
   const int64_t t = target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, row);
@@ -250,8 +253,8 @@ cudaError_t launch_gated_grad(const GatedGradParams& p, int sm_count, cudaStream
   return launch(gated_grad_kernel, dim3(blocks_for(p.rows * ((p.cols + 7) / 8), 32 * (int64_t)sm_count)), 256, p, stream);
 }
 cudaError_t launch_loss_join(const LossJoinParams& p, cudaStream_t stream) {
-  if (p.rows <= kFewRows) return launch(loss_join_kernel<1>, dim3((unsigned)p.rows), kJoinThreads, p, stream);
-  return launch(loss_join_kernel<32>, dim3((unsigned)((p.rows + 31) / 32)), kJoinThreads, p, stream);
+  if (p.rows <= 2 * kFewRows) return launch(loss_join_kernel<1>, dim3((unsigned)p.rows), kJoinThreads, p, stream);
+  return launch(loss_join_kernel<8>, dim3((unsigned)((p.rows + 7) / 8)), kJoinThreads, p, stream);
 }
 
 }  // namespace mpg

@@ -39,6 +39,7 @@
 // role drains what it has in flight before TMEM is released.
 #pragma once
 
+#include <algorithm>
 #include <climits>
 
 #include "cluster.cuh"
@@ -430,8 +431,19 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
     const Pow2 sc = warp_scale(p.scale, p.scale_exp);
     uint32_t g = 0;
     FusedItems items(p, worker, workers);
-    FusedItem x;
-    for (; items.template next<T::kEpi == FusedEpi::kPlain>(p, x); ++g) {
+    FusedItem x, ahead;
+    bool more = items.template next<T::kEpi == FusedEpi::kPlain>(p, ahead);
+    // dY's elements of a chunk, a row a lane, on their way while the accumulator is waited for
+    uint32_t dyw[16];
+    auto first_row = [&](const FusedItem& i) { return i.mb * T::kTile + (int)rank * T::BM + 32 * q; };
+    auto fetch_dy = [&](int row, int col) {
+      if (row < p.prod[0].m && col < p.prod[0].n)
+        load_block16(stg, lane, dyw, Block16{const_cast<void*>(p.dy), p.lddy, row, p.prod[0].m, col, p.prod[0].n, p.dy_vec != 0});
+    };
+    if (T::kEpi == FusedEpi::kGatedGrad && more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
+    for (; more; ++g) {
+      x = ahead;
+      more = items.template next<T::kEpi == FusedEpi::kPlain>(p, ahead);
       const FusedProduct& pr = p.prod[x.which];
       const bool second = x.mb >= pr.mb_second;
       const uint32_t ab = g % T::kAccBufs;
@@ -481,6 +493,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
                 stage_read_chunk(stg, lane, i);
           __syncwarp();
         }
+        if (T::kEpi == FusedEpi::kGatedGrad && more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
         continue;
       }
 
@@ -488,16 +501,19 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
 #pragma unroll 1
         for (int cc = cc0; cc < cc0 + kCc; ++cc) {
           const int col0 = col_tile + cc * 32;
-          uint32_t dyw[16];
-          if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
-            if (row0 < pr.m && col0 < pr.n)
-              load_block16(stg, lane, dyw, Block16{const_cast<void*>(p.dy), p.lddy, row0, pr.m, col0, pr.n, p.dy_vec != 0});
-          }
           float gt[32], up[32];
           tmem_ld_32cols(tacc + cc * 32, gt);
           tmem_ld_32cols(tacc + T::kTile / 2 + cc * 32, up);
           tmem_ld_wait();
           if (cc == cc0 + kCc - 1) release();
+          uint32_t here[16];
+          if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) here[j] = dyw[j];
+            // dY's elements of the next chunk, the next tile's first after the last
+            if (cc + 1 < cc0 + kCc) fetch_dy(row0, col0 + 32);
+            else if (more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
+          }
           if (row0 >= pr.m || col0 >= pr.n) continue;
           auto store = [&](int i, auto value) {
             uint32_t w[16];
@@ -514,7 +530,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const float2 y2 = unpack16(dyw[j >> 1], bf16);
+              const float2 y2 = unpack16(here[j >> 1], bf16);
               const float dy = sc.mul * ((j & 1) ? y2.y : y2.x);
               float a, d;
               act_both(gt[j], T::kAct, a, d);
@@ -571,53 +587,66 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
         }
         if (row < pr.m) p.stats[(int64_t)(x.nb * 2 + half) * pr.m + row] = make_float2(top, sum);
       } else if constexpr (T::kEpi == FusedEpi::kProb) {
+        float v[32];
+        tmem_ld_32cols(tacc + cc0 * 32, v);
 #pragma unroll 1
         for (int cc = cc0; cc < cc0 + kCc; ++cc) {
-          float v[32];
-          tmem_ld_32cols(tacc + cc * 32, v);
           tmem_ld_wait();
-          if (cc == cc0 + kCc - 1) release();
           const int col0 = col_tile + cc * 32;
-          if (row0 >= pr.m || col0 >= pr.n) continue;
-          const int64_t at = target - (p.col0 + col0);
-          const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
-          const bool any = __any_sync(0xffffffffu, mine != 0u);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(kLog2e, v[j], -lse2));
-          if (any) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = mine & (1u << j) ? v[j] - 1.0f : v[j];
-          }
           uint32_t w[16];
+          const bool in = row0 < pr.m && col0 < pr.n;
+          if (in) {
+            const int64_t at = target - (p.col0 + col0);
+            const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
+            const bool any = __any_sync(0xffffffffu, mine != 0u);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            w[j] = weight == 0.0f ? 0u : pack16(weight * v[2 * j], weight * v[2 * j + 1], bf16);
-          store_block16(stg, lane, w, Block16{pr.out[0], pr.ldo[0], row0, pr.m, col0, pr.n, pr.out_vec[0] != 0});
+            for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(kLog2e, v[j], -lse2));
+            if (any) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = mine & (1u << j) ? v[j] - 1.0f : v[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = weight == 0.0f ? 0u : pack16(weight * v[2 * j], weight * v[2 * j + 1], bf16);
+          }
+          if (cc + 1 < cc0 + kCc) tmem_ld_32cols(tacc + (cc + 1) * 32, v);
+          else release();
+          if (in) store_block16(stg, lane, w, Block16{pr.out[0], pr.ldo[0], row0, pr.m, col0, pr.n, pr.out_vec[0] != 0});
         }
       } else {
         const int dt = pr.out_dtype;
         void* out = pr.out[second ? 1 : 0];
         const int64_t ldo = pr.ldo[second ? 1 : 0];
         const bool vec = pr.out_vec[second ? 1 : 0] != 0;
+        // (the next chunk's accumulators are on their way while this one is stored)
+        float v[32];
+        tmem_ld_32cols(tacc + cc0 * 32, v);
 #pragma unroll 1
         for (int cc = cc0; cc < cc0 + kCc; ++cc) {
-          float v[32];
-          tmem_ld_32cols(tacc + cc * 32, v);
           tmem_ld_wait();
-          if (cc == cc0 + kCc - 1) release();
           const int col0 = col_tile + cc * 32;
-          if (row0 >= pr.m || col0 >= pr.n) continue;
+          const bool in = row0 < pr.m && col0 < pr.n;
+          auto next_chunk = [&]() {
+            if (cc + 1 < cc0 + kCc) tmem_ld_32cols(tacc + (cc + 1) * 32, v);
+            else release();
+          };
+          if (!in) {
+            next_chunk();
+            continue;
+          }
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= sc.inv;
           if (dt != kOutF32 && !pr.add) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], dt == kOutBF16);
+            next_chunk();
             store_block16(stg, lane, w, Block16{out, ldo, row0, pr.m, col0, pr.n, vec});
             continue;
           }
           stage_write_row(stg, lane, v);
           __syncwarp();
+          next_chunk();
           // (add has lines of whole 16-byte chunks)
           if (vec && col0 + 32 <= pr.n) {
 #pragma unroll
@@ -692,11 +721,14 @@ __device__ __forceinline__ void load_four(float (&v)[4], const void* src, int64_
 // epilogue does with the sums.  Tiles that one worker had whole are done already.
 // Every worker has a block of k at least, so the parts of a tile are those of
 // consecutive workers, and only the first can have begun in an earlier tile (its
-// second slot).
+// second slot).  A tile of many parts (few tiles, long k) has kSlices warps that
+// add a run of them each: 150 parts of one tile 27 us with one.
 constexpr int kJoinThreads = 256;
-template <class T>
+template <class T, int kSlices>
 __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_constant__ FusedGemmParams p, int workers) {
   constexpr int kPerRow = T::kTileN / 4;
+  constexpr int kAt = kJoinThreads / kSlices;        // places of a block
+  __shared__ float4 slices[kSlices > 1 ? kSlices : 1][T::kTwo ? 2 : 1][kSlices > 1 ? kAt : 1];
   griddep_wait();
   griddep_launch_dependents();
   const FusedProduct& pr = p.prod[0];
@@ -706,7 +738,8 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   if (n == 1) return;
   const FusedTile tc = fused_tile(pr, p.whole_tiles + (int)blockIdx.x);
   const bool second = tc.mb >= pr.mb_second;
-  const int i = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int place = threadIdx.x % kAt, slice = threadIdx.x / kAt;
+  const int i = blockIdx.y * kAt + place;
   const int r = i / kPerRow, c = i % kPerRow * 4;
   const int row = (second ? tc.mb - pr.mb_second : tc.mb) * T::kTile + r, col = tc.nb * T::kTileN + c;
   const Pow2 sc = warp_scale(p.scale, p.scale_exp);
@@ -714,19 +747,27 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   const int left = pr.n - col;                       // columns of the matrix from here on
   constexpr int64_t kSlot = T::kTile * T::kTile;
   const int first = 2 * w0 + (first_unit(p.units, w0, workers) < u0 ? 1 : 0);
-  auto sum = [&](int column, float (&v)[4]) {
+  auto sum = [&](int which, int column, float (&v)[4]) {
     const float* at = p.slots + (int64_t)r * T::kTile + column;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float4& y) {
+      o.x += y.x;
+      o.y += y.y;
+      o.z += y.z;
+      o.w += y.w;
+    };
     if (in && left > 0) {
-      o = out_load4(at, first * kSlot, kOutF32);
+      const int j0 = kSlices > 1 ? n * slice / kSlices : 0, j1 = kSlices > 1 ? n * (slice + 1) / kSlices : n;
+      if (j0 == 0) add(out_load4(at, first * kSlot, kOutF32));
 #pragma unroll 4
-      for (int j = 1; j < n; ++j) {
-        const float4 y = out_load4(at, 2 * (w0 + j) * kSlot, kOutF32);
-        o.x += y.x;
-        o.y += y.y;
-        o.z += y.z;
-        o.w += y.w;
-      }
+      for (int j = max(j0, 1); j < j1; ++j) add(out_load4(at, 2 * (w0 + j) * kSlot, kOutF32));
+    }
+    if constexpr (kSlices > 1) {
+      slices[slice][which][place] = o;
+      __syncthreads();
+      o = slices[0][which][place];
+#pragma unroll
+      for (int j = 1; j < kSlices; ++j) add(slices[j][which][place]);
     }
     v[0] = o.x;
     v[1] = o.y;
@@ -736,9 +777,9 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   const int type = p.bf16 ? kOutBF16 : kOutF16;
   if constexpr (T::kTwo) {
     float gt[4], up[4];
-    sum(c, gt);
-    sum(T::kTile / 2 + c, up);
-    if (!in || left <= 0) return;
+    sum(0, c, gt);
+    sum(1, T::kTile / 2 + c, up);
+    if (slice > 0 || !in || left <= 0) return;
     auto at = [&](int k) { return (int64_t)row * pr.ldo[k] + col; };
     if constexpr (T::kEpi == FusedEpi::kGated) {
       if (pr.out[1]) {
@@ -763,7 +804,8 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
     store_four(pr.out[0], at(0), gt, left, pr.out_vec[0], type);
   } else {
     float v[4];
-    sum(c, v);
+    sum(0, c, v);
+    if (slice > 0) return;
     if constexpr (T::kEpi == FusedEpi::kPlain) {
       if (!in || left <= 0) return;
       const int k = second ? 1 : 0;
@@ -814,13 +856,17 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
 template <class T>
 cudaError_t launch_fused_join(const FusedGemmParams& p, int workers, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.prod[0].num_tiles - p.whole_tiles), (unsigned)(T::kTile * T::kTileN / 4 / kJoinThreads));
+  const int tiles = p.prod[0].num_tiles - p.whole_tiles;
+  const bool many = workers >= 8 * tiles;
+  const int places = std::min(T::kTile, p.prod[0].m) * (T::kTileN / 4), at = many ? kJoinThreads / 8 : kJoinThreads;
+  cfg.gridDim = dim3((unsigned)tiles, (unsigned)((places + at - 1) / at));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   cfg.numAttrs = (unsigned)launch_attributes(attr, 1);
   cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, fused_join_kernel<T>, p, workers);
+  return many ? cudaLaunchKernelEx(&cfg, fused_join_kernel<T, 8>, p, workers)
+              : cudaLaunchKernelEx(&cfg, fused_join_kernel<T, 1>, p, workers);
 }
 
 template <class T>
