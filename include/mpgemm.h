@@ -510,7 +510,7 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
  * All matrices are row-major and of one 16-bit type, with leading dimensions of
  * at least their lines, any alignment of an element; 16-byte aligned bases and
  * leading dimensions of whole 16 bytes are fastest (others are copied to such
- * lines in the workspace, or read element by element for up to 32 tokens).
+ * lines in the workspace first).
  * Sizes <= 2^31 - 256.  Results do not depend on timing.  Results may not
  * overlap operands or each other. */
 typedef enum { MPG_ACT_SILU = 0, MPG_ACT_GELU = 1, MPG_ACT_GELU_TANH = 2 } mpg_activation;

@@ -78,6 +78,22 @@ __device__ __forceinline__ float load16(const void* base, int64_t idx, bool bf16
   return bf16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
 }
 
+// Eight 16-bit elements from element `shift` (0 .. 7) of two neighbouring words on.
+__device__ __forceinline__ uint4 shift_words(const uint4& a, const uint4& b, int shift) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t t[5], r[4];
+  // by whole registers (shift / 2, in two steps), then by half of one
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    const uint32_t lo = shift & 4 ? w[j + 2 < 8 ? j + 2 : 7] : w[j];
+    const uint32_t hi = shift & 4 ? w[j + 3 < 8 ? j + 3 : 7] : w[j + 1];
+    t[j] = shift & 2 ? hi : lo;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = shift & 1 ? __funnelshift_r(t[j], t[j + 1], 16) : t[j];
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 // The class of a token: -1 where it is ignored, -2 where it is no class.
 __device__ __forceinline__ int64_t target_of(const void* target, int bytes, int64_t stride, int64_t ignore, int64_t vocab,
                                              int64_t row) {

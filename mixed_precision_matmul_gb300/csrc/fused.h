@@ -48,7 +48,7 @@ struct FusedGemmParams {
   FusedProduct prod[2];             // kPlain: two products may share a launch, the longer k first
   int32_t bf16;
   int32_t whole_tiles;              // of the first: taken round by round; the others' blocks of k are dealt out evenly
-  int64_t units;                    // blocks of k of those others
+  int64_t units, units_first;       // blocks of k of those others (and of all of the second's tiles); of the first's
   float* slots;                     // partial tiles, two for each worker
   int32_t late, late_workers, late_rounds;   // the second's tiles: see FusedItems
 
@@ -89,10 +89,9 @@ void fused_lookup_gated_grad(bool pair, int act, FusedKernel* out);
 void fused_lookup_loss(FusedEpi epi, bool pair, FusedKernel* out);
 // The product of few rows: gated (wu given) or the statistics of logits.
 struct FewRowsParams {
-  const void *x, *w, *wu;           // X: rows x k; weights: n x k
+  const void *x, *w, *wu;           // X: rows x k; weights: n x k; lines of whole 16 bytes, k a multiple of 8
   int64_t ldx, ldw, ldwu;
   int32_t bf16, rows, n, k;
-  int32_t vec;                      // lines of all operands start on 16-byte boundaries and are whole 16 bytes
   int32_t strips;
   int32_t act;
   void *y, *g, *u;
@@ -106,7 +105,7 @@ struct FewRowsParams {
   uint64_t wait_limit_ns;
 };
 mpg_status launch_few_rows(DeviceInfo* dev, FewRowsParams& p, bool gated, cudaStream_t stream);
-int few_rows_parts(int rows, int64_t n);   // of the statistics of n logits
+int few_rows_parts(int64_t n);      // of the statistics of n logits
 
 // Copies of matrices whose lines TMA cannot describe.
 struct PadParams {
@@ -170,12 +169,16 @@ mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& 
 // Both of p's products, in one launch where that takes less.
 mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedLaunch& l1, FusedGemmParams& p, float* slots,
                             cudaStream_t stream);
-size_t fused_slot_bytes(const FusedLaunch& l);   // of the slots that a launch may need
+// Bytes of the slots that a launch (of two products) may need.
+size_t fused_slot_bytes(const FusedLaunch& l, const FusedLaunch* second = nullptr);
 // rows x k operand of a product: K-major if k is the matrix's contiguous side.
 mpg_status fused_map(CUtensorMap* map, const void* ptr, int64_t ld, mpg_dtype dt, bool mn_major, int64_t rows, int64_t k);
 
 constexpr int64_t kFusedMaxExtent = 0x7FFFFFFF - 255;   // the last tile's end, and a block beyond it, still fit 32 bits
 inline int64_t fused_line(int64_t n) { return (n + 7) / 8 * 8; }
+// Lines of the library's own matrices start on 128 bytes: a TMA box of lines that
+// cross those takes half as long again (900 cycles a block of k instead of 600).
+inline int64_t fused_wide_line(int64_t n) { return (n + 63) / 64 * 64; }
 inline bool fused_aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 // TMA can describe rows x cols lines of 16-bit elements
 inline bool fused_lines_ok(const void* p, int64_t ld) { return fused_aligned(p, 16) && ld % 8 == 0; }

@@ -59,22 +59,16 @@ __global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadPar
       const uintptr_t addr = reinterpret_cast<uintptr_t>(at);
       const uint4* word = reinterpret_cast<const uint4*>(addr & ~(uintptr_t)15);
       const int shift = (int)(addr & 15) / 2;          // elements
-      const uint4 a = ld_global(word), b = shift ? ld_global(word + 1) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t t[5], r[4];
-      // by whole words (shift / 2, in two steps), then by half a word
-      const int s = shift >> 1;
-#pragma unroll
-      for (int j = 0; j < 5; ++j) {
-        const uint32_t lo = s & 2 ? w[j + 2 < 8 ? j + 2 : 7] : w[j];
-        const uint32_t hi = s & 2 ? w[j + 3 < 8 ? j + 3 : 7] : w[j + 1];
-        t[j] = s & 1 ? hi : lo;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r[j] = shift & 1 ? __funnelshift_r(t[j], t[j + 1], 16) : t[j];
-      v = make_uint4(r[0], r[1], r[2], r[3]);
+      v = shift_words(ld_global(word), shift ? ld_global(word + 1) : make_uint4(0, 0, 0, 0), shift);
     }
-    // (what lies beyond a line's end is the next one's: it is not read)
+    const int64_t left = m.cols - c.col;
+    if (left < 8) {
+      // zeros behind the line's end
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = 2 * j >= left ? 0u : 2 * j + 1 == left ? w[j] & 0xffffu : w[j];
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
     *reinterpret_cast<uint4*>(m.dst + c.row * m.ld_dst + c.col) = v;
   }
 }

@@ -113,18 +113,37 @@ struct Block16 {
 __device__ __noinline__ void flush_block16(uint32_t stg, const Block16 b) {
   const int lane = threadIdx.x & 31;
   uint16_t* out = static_cast<uint16_t*>(b.base);
-  if (b.vec && b.col0 + 32 <= b.cols) {
+  if (b.vec) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2), c = lane & 3;
-      if (b.row0 + r < b.rows)
-        *reinterpret_cast<uint4*>(out + (int64_t)(b.row0 + r) * b.ld + b.col0 + c * 8) = ld_shared_v4(stg + half_chunk(r, c));
+      const int left = b.row0 + r < b.rows ? b.cols - b.col0 - c * 8 : 0;
+      uint16_t* to = out + (int64_t)(b.row0 + r) * b.ld + b.col0 + c * 8;
+      const uint4 x = ld_shared_v4(stg + half_chunk(r, c));
+      if (left >= 8) {
+        *reinterpret_cast<uint4*>(to) = x;
+      } else if (left > 0) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (j < left) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+      }
     }
-  } else if (b.col0 + lane < b.cols) {
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-      if (b.row0 + r < b.rows)
-        out[(int64_t)(b.row0 + r) * b.ld + b.col0 + lane] = ld_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2);
+  } else {
+    // by elements, sixteen rows at a time
+    uint16_t* to = out + (int64_t)b.row0 * b.ld + b.col0 + lane;
+    const int rows = b.col0 + lane < b.cols ? b.rows - b.row0 : 0;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      uint16_t x[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[r] = ld_shared_h(stg + half_chunk(r0 + r, lane >> 3) + (lane & 7) * 2);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        if (r0 + r < rows) *to = x[r];
+        to += b.ld;
+      }
+    }
   }
   __syncwarp();
 }
@@ -135,41 +154,48 @@ __device__ __forceinline__ void store_block16(uint32_t stg, int lane, const uint
   __syncwarp();
   flush_block16(stg, b);
 }
-// The same read into the staging: row row0 + lane, 32 columns (0 beyond the matrix).
+// The same block read: row row0 + lane, 32 columns (0 beyond the matrix).
 __device__ __noinline__ void fill_block16(uint32_t stg, const Block16 b) {
   const int lane = threadIdx.x & 31;
-  const uint16_t* src = static_cast<const uint16_t*>(b.base);
-  const bool in = b.col0 + lane < b.cols;
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r)
-    st_shared_h(stg + half_chunk(r, lane >> 3) + (lane & 7) * 2,
-                in && b.row0 + r < b.rows ? src[(int64_t)(b.row0 + r) * b.ld + b.col0 + lane] : (uint16_t)0);
+  const uint16_t* src = static_cast<const uint16_t*>(b.base) + (int64_t)b.row0 * b.ld + b.col0 + lane;
+  const int rows = b.col0 + lane < b.cols ? b.rows - b.row0 : 0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 16) {
+    uint16_t x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      x[r] = r0 + r < rows ? *src : (uint16_t)0;
+      src += b.ld;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) st_shared_h(stg + half_chunk(r0 + r, lane >> 3) + (lane & 7) * 2, x[r]);
+  }
   __syncwarp();
 }
 __device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&w)[16], const Block16& b) {
-  if (b.vec && b.col0 + 32 <= b.cols) {
-    const bool in = b.row0 + lane < b.rows;
-    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(b.base) + (int64_t)(in ? b.row0 + lane : b.row0) * b.ld + b.col0);
+  if (!b.vec || (b.col0 + 32 > b.cols && b.cols % 8 != 0)) {
+    fill_block16(stg, b);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const uint4 x = in ? ld_global(at + c) : make_uint4(0, 0, 0, 0);
+      const uint4 x = ld_shared_v4(stg + half_chunk(lane, c));
       w[4 * c] = x.x;
       w[4 * c + 1] = x.y;
       w[4 * c + 2] = x.z;
       w[4 * c + 3] = x.w;
     }
+    __syncwarp();
     return;
   }
-  fill_block16(stg, b);
+  const bool in = b.row0 + lane < b.rows;
+  const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(b.base) + (int64_t)(in ? b.row0 + lane : b.row0) * b.ld + b.col0);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const uint4 x = ld_shared_v4(stg + half_chunk(lane, c));
+    const uint4 x = in && b.col0 + 8 * c < b.cols ? ld_global(at + c) : make_uint4(0, 0, 0, 0);
     w[4 * c] = x.x;
     w[4 * c + 1] = x.y;
     w[4 * c + 2] = x.z;
     w[4 * c + 3] = x.w;
   }
-  __syncwarp();
 }
 
 // The class of a token (-1: ignored, -2: none), and the weight of its gradient: an
@@ -203,8 +229,9 @@ __device__ __forceinline__ FusedTile fused_tile(const FusedProduct& p, int t) {
 __host__ __device__ __forceinline__ int64_t first_unit(int64_t units, int w, int workers) { return units * w / workers; }
 
 // A worker's tiles: the first product's whole ones round by round, then its run of
-// that product's split tiles' blocks of k, then the second product's.  Workers
-// p.late .. have one tile of the first product less than those before them; they
+// the split tiles' blocks of k (that product's, then the second's where all of
+// its tiles are dealt out: p.units_first of the blocks are the first's), then the
+// second product's whole ones.  Workers p.late .. have one tile of the first product less than those before them; they
 // take p.late_rounds rounds of the second's alone, about as long as that tile,
 // and then go first in the rounds of all.
 struct FusedItem {
@@ -233,13 +260,16 @@ struct FusedItems {
       tile = t;
       t += workers;
     } else if (u < u1) {
-      const int64_t j = u / p.prod[0].num_k_blk;
-      tile = p.whole_tiles + (int)j;
-      x.kb0 = (int)(u - j * p.prod[0].num_k_blk);
-      x.kb1 = (int)min((int64_t)p.prod[0].num_k_blk, x.kb0 + (u1 - u));
-      x.slot = x.kb1 - x.kb0 == p.prod[0].num_k_blk ? -1 : 2 * worker + (u == u0 ? 0 : 1);
+      x.which = kMore && u >= p.units_first ? 1 : 0;
+      const int kb = p.prod[x.which].num_k_blk;
+      const int64_t v = x.which ? u - p.units_first : u;
+      const int64_t j = v / kb;
+      tile = (x.which ? 0 : p.whole_tiles) + (int)j;
+      x.kb0 = (int)(v - j * kb);
+      x.kb1 = (int)min((int64_t)kb, x.kb0 + (u1 - u));
+      x.slot = x.kb1 - x.kb0 == kb ? -1 : 2 * worker + (u == u0 ? 0 : 1);
       u += x.kb1 - x.kb0;
-    } else if (kMore && p.prod[1].num_tiles) {
+    } else if (kMore && p.prod[1].num_tiles && p.units <= p.units_first) {
       int rank = worker - p.late;
       if (rank >= 0 && round < p.late_rounds) {
         tile = round * p.late_workers + rank;
@@ -731,12 +761,16 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   __shared__ float4 slices[kSlices > 1 ? kSlices : 1][T::kTwo ? 2 : 1][kSlices > 1 ? kAt : 1];
   griddep_wait();
   griddep_launch_dependents();
-  const FusedProduct& pr = p.prod[0];
-  const int64_t u0 = (int64_t)blockIdx.x * pr.num_k_blk, u1 = u0 + pr.num_k_blk;
+  const int tiles0 = p.prod[0].num_tiles - p.whole_tiles;                       // the second product's come after them
+  const int which = T::kEpi == FusedEpi::kPlain && (int)blockIdx.x >= tiles0 ? 1 : 0;
+  const FusedProduct& pr = p.prod[which];
+  const int tile = which ? (int)blockIdx.x - tiles0 : p.whole_tiles + (int)blockIdx.x;
+  const int64_t u0 = which ? p.units_first + (int64_t)tile * pr.num_k_blk : (int64_t)blockIdx.x * pr.num_k_blk;
+  const int64_t u1 = u0 + pr.num_k_blk;
   const int w0 = (int)(((u0 + 1) * workers - 1) / p.units);                     // the last that begins at u0 or before
   const int n = (int)((u1 * workers + p.units - 1) / p.units) - w0;             // up to the last that begins before u1
   if (n == 1) return;
-  const FusedTile tc = fused_tile(pr, p.whole_tiles + (int)blockIdx.x);
+  const FusedTile tc = fused_tile(pr, tile);
   const bool second = tc.mb >= pr.mb_second;
   const int place = threadIdx.x % kAt, slice = threadIdx.x / kAt;
   const int i = blockIdx.y * kAt + place;
@@ -856,9 +890,11 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
 template <class T>
 cudaError_t launch_fused_join(const FusedGemmParams& p, int workers, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  const int tiles = p.prod[0].num_tiles - p.whole_tiles;
+  const bool both = p.units > p.units_first;
+  const int tiles = p.prod[0].num_tiles - p.whole_tiles + (both ? p.prod[1].num_tiles : 0);
   const bool many = workers >= 8 * tiles;
-  const int places = std::min(T::kTile, p.prod[0].m) * (T::kTileN / 4), at = many ? kJoinThreads / 8 : kJoinThreads;
+  const int rows = both ? std::max(p.prod[0].m, p.prod[1].m) : p.prod[0].m;
+  const int places = std::min(T::kTile, rows) * (T::kTileN / 4), at = many ? kJoinThreads / 8 : kJoinThreads;
   cfg.gridDim = dim3((unsigned)tiles, (unsigned)((places + at - 1) / at));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;

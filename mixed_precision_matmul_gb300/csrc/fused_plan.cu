@@ -33,6 +33,7 @@ Shape shape_of(const FusedLaunch& l, int64_t tile) {
 // over k = 32768, dealt to 76: 210 us where the round takes 173), so that
 // splitting pays where it gives many idle workers something to do.  The parts
 // go through memory twice, and the second launch takes 3 us.
+constexpr double kOneEpi = 1.9, kPairEpi = 3.8;    // a tile's way out, beside the next one's products
 constexpr double kOneEdge = 4.3, kPairEdge = 7.5, kOneBlock = 0.29, kPairBlock = 0.31;
 constexpr double kJoin = 3.0, kApartBytes = 8.3e6, kPartBytes = 5.0e6;     // bytes a us
 constexpr double kL2Bytes = 100e6;
@@ -44,7 +45,8 @@ struct Deal {
 Deal deal(const FusedLaunch& l, const Shape& s, int64_t tile, int64_t most, double edge, double block, bool may_split) {
   const int64_t kb = s.units / s.tiles;
   const int64_t rounds = (s.tiles + most - 1) / most;
-  Deal d{std::min(s.tiles, most), s.tiles, edge + (double)(rounds * kb) * block};
+  const double round = std::max((double)kb * block, tile == 256 ? kPairEpi : kOneEpi);
+  Deal d{std::min(s.tiles, most), s.tiles, edge + (double)rounds * round};
   const int64_t rest = s.tiles % most;
   if (!may_split || !rest || kb < 2) return d;
   const int64_t whole = s.tiles - rest;
@@ -52,7 +54,7 @@ Deal deal(const FusedLaunch& l, const Shape& s, int64_t tile, int64_t most, doub
   const double operands = 128.0 * (double)kb * (double)((l.second_m ? 2 : 1) * l.m + l.n);
   const double apart = operands < kL2Bytes ? block : std::max(block, 256.0 * (double)tile * (double)workers / kApartBytes);
   const double parts = (double)(rest + workers) * (double)(tile * tile) * 4.0;
-  const double time = edge + kJoin + 2.0 * parts / kPartBytes + (double)(whole / most * kb) * block +
+  const double time = edge + kJoin + 2.0 * parts / kPartBytes + (double)(whole / most) * round +
                       (double)((rest * kb + workers - 1) / workers) * apart;
   if (time < d.time) d = Deal{workers, whole, time};
   return d;
@@ -60,10 +62,15 @@ Deal deal(const FusedLaunch& l, const Shape& s, int64_t tile, int64_t most, doub
 
 }  // namespace
 
-size_t fused_slot_bytes(const FusedLaunch& l) {
+size_t fused_slot_bytes(const FusedLaunch& l, const FusedLaunch* second) {
   size_t most = 0;
   for (int64_t tile : {(int64_t)128, (int64_t)256}) {
-    const Shape s = shape_of(l, tile);
+    Shape s = shape_of(l, tile);
+    if (second) {
+      const Shape t = shape_of(*second, tile);
+      s.tiles += t.tiles;
+      s.units += t.units;
+    }
     if (s.units == s.tiles) return 0;                 // (one block of k is not split)
     const int64_t workers = std::min(tile == 256 ? kMaxPairs : (int64_t)kMaxCtas, std::max(s.tiles, s.units / kMinUnits));
     most = std::max(most, (size_t)(2 * workers * tile * tile) * sizeof(float));
@@ -120,8 +127,11 @@ mpg_status fill_product(FusedProduct& p, const FusedLaunch& l, int64_t tile, boo
   return MPG_OK;
 }
 
-mpg_status launch(DeviceInfo* dev, const FusedKernel& k, FusedGemmParams& p, int64_t workers, float* slots, cudaStream_t stream) {
-  p.units = (int64_t)(p.prod[0].num_tiles - p.whole_tiles) * p.prod[0].num_k_blk;
+// dealt: the blocks of k of both products' tiles are dealt out.
+mpg_status launch(DeviceInfo* dev, const FusedKernel& k, FusedGemmParams& p, int64_t workers, bool dealt, float* slots,
+                  cudaStream_t stream) {
+  p.units_first = (int64_t)(p.prod[0].num_tiles - p.whole_tiles) * p.prod[0].num_k_blk;
+  p.units = p.units_first + (dealt ? (int64_t)p.prod[1].num_tiles * p.prod[1].num_k_blk : 0);
   p.slots = slots;
   p.status = dev->status;
   p.wait_limit_ns = kDefaultWaitNs;
@@ -156,12 +166,15 @@ mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& 
   if ((s = fill_product(p.prod[0], l, f.kernel[pair].tile, pair)) != MPG_OK) return s;
   p.prod[1].num_tiles = 0;
   p.whole_tiles = (int32_t)d.whole;
-  return launch(dev, f.kernel[pair], p, d.workers, slots, stream);
+  return launch(dev, f.kernel[pair], p, d.workers, false, slots, stream);
 }
 
 // In one launch the second product's tiles fill what the first's last round
 // leaves, and one way in and out is saved: 4096 tokens' gradients over 32768
 // classes and 2048 channels take 1728 blocks of k a worker instead of 1920.
+// Where both have few tiles of many blocks, all blocks are dealt out: 5377
+// tokens' gradients of 64 channels and 1408 inner values 25 blocks a worker
+// instead of 85.
 mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedLaunch& l1, FusedGemmParams& p, float* slots,
                             cudaStream_t stream) {
   Forms f;
@@ -178,7 +191,8 @@ mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedL
   for (const FusedLaunch* x : l) apart += std::min(deal_form(*x, f, 0, slots != nullptr).time, deal_form(*x, f, 1, slots != nullptr).time);
   double best = apart;
   int form = -1;
-  int64_t late = 0, late_workers = 0, late_rounds = 0;
+  int64_t late = 0, late_workers = 0, late_rounds = 0, workers = 0;
+  bool dealt = false;
   for (int pair = 0; pair < 2; ++pair) {
     const int64_t tile = f.kernel[pair].tile, w = f.workers[pair];
     const Shape a = shape_of(*l[0], tile), b = shape_of(*l[1], tile);
@@ -187,14 +201,29 @@ mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedL
     const int64_t idle = busy ? w - busy : 0;
     const int64_t rounds = std::min(idle ? ka / kb : 0, idle ? (b.tiles + idle - 1) / idle : 0);
     const int64_t rest = std::max<int64_t>(0, b.tiles - rounds * idle);
-    const double blocks = (double)((a.tiles + w - 1) / w * ka + (rest + w - 1) / w * kb);
-    const double time = (pair ? kPairEdge : kOneEdge) + blocks * (pair ? kPairBlock : kOneBlock);
+    const double block = pair ? kPairBlock : kOneBlock, way_out = pair ? kPairEpi : kOneEpi;
+    const double time = (pair ? kPairEdge : kOneEdge) + (double)((a.tiles + w - 1) / w) * std::max((double)ka * block, way_out) +
+                        (double)((rest + w - 1) / w) * std::max((double)kb * block, way_out);
     if (time < best) {
       best = time;
       form = pair;
+      dealt = false;
       late = busy;
       late_workers = idle;
       late_rounds = rounds;
+    }
+    const int64_t units = a.units + b.units, all = std::min(w, std::max(units / kMinUnits, (int64_t)1));
+    const double operands = 128.0 * ((double)ka * (double)((l[0]->second_m ? 2 : 1) * l[0]->m + l[0]->n) +
+                                     (double)kb * (double)((l[1]->second_m ? 2 : 1) * l[1]->m + l[1]->n));
+    const double apart_block = operands < kL2Bytes ? block : std::max(block, 256.0 * (double)tile * (double)all / kApartBytes);
+    const double parts = (double)std::min(2 * all, a.tiles + b.tiles + all) * (double)(tile * tile) * 4.0;
+    const double even = (pair ? kPairEdge : kOneEdge) + kJoin + 2.0 * parts / kPartBytes +
+                        std::max((double)((units + all - 1) / all) * apart_block, (double)((a.tiles + b.tiles) / all) * way_out);
+    if (slots && a.tiles + b.tiles <= 2 * w && even < best) {
+      best = even;
+      form = pair;
+      dealt = true;
+      workers = all;
     }
   }
   if (form < 0) {
@@ -207,12 +236,16 @@ mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedL
   const FusedKernel& k = f.kernel[form];
   for (int i = 0; i < 2; ++i)
     if ((s = fill_product(p.prod[i], *l[i], k.tile, form)) != MPG_OK) return s;
+  if (dealt) {
+    p.whole_tiles = 0;
+    return launch(dev, k, p, workers, true, slots, stream);
+  }
   p.whole_tiles = p.prod[0].num_tiles;
   p.late = (int32_t)late;
   p.late_workers = (int32_t)late_workers;
   p.late_rounds = (int32_t)late_rounds;
   const int64_t tiles = (int64_t)p.prod[0].num_tiles + p.prod[1].num_tiles;
-  return launch(dev, k, p, std::min(f.workers[form], tiles), slots, stream);
+  return launch(dev, k, p, std::min(f.workers[form], tiles), false, slots, stream);
 }
 
 }  // namespace mpg

@@ -81,19 +81,22 @@ Layout layout(const mpg_gated_layer* l, bool backward) {
   o.wg = source(l->wg, l->ldwg, l->inner, l->hidden);
   o.wu = source(l->wu, l->ldwu, l->inner, l->hidden);
   o.dg = o.du = o.partial = o.slots = 0;
-  o.ldd = fused_line(l->inner);
-  if (backward || l->tokens > kFewRows)
-    for (Source* s : {&o.x, &o.wg, &o.wu})
-      if (s->copy) s->at = take((size_t)s->rows * (size_t)fused_line(s->cols) * 2);
+  o.ldd = fused_wide_line(l->inner);
+  // (few rows are multiplied in whole chunks of eight: zeros behind all of them, or none needed)
+  const bool all = !backward && l->tokens <= kFewRows && l->hidden % 8 != 0;
+  for (Source* s : {&o.x, &o.wg, &o.wu}) {
+    s->copy = s->copy || all;
+    if (s->copy) s->at = take((size_t)s->rows * (size_t)fused_wide_line(s->cols) * 2);
+  }
   if (backward) {
     o.dg = take((size_t)l->tokens * (size_t)o.ldd * 2);
     o.du = take((size_t)l->tokens * (size_t)o.ldd * 2);
     o.partial = take(kScaleBlocks * sizeof(float));
   }
-  if (backward)
-    o.slots = take(std::max({fused_slot_bytes(input_gradient(l)), fused_slot_bytes(weight_gradient(l)),
-                             fused_slot_bytes(product(FusedEpi::kGatedGrad, l->tokens, l->inner, l->hidden))}));
-  else if (l->tokens > kFewRows)
+  if (backward) {
+    const FusedLaunch to_x = input_gradient(l), to_w = weight_gradient(l);
+    o.slots = take(std::max(fused_slot_bytes(to_x, &to_w), fused_slot_bytes(product(FusedEpi::kGatedGrad, l->tokens, l->inner, l->hidden))));
+  } else if (l->tokens > kFewRows)
     o.slots = take(fused_slot_bytes(product(FusedEpi::kGated, l->tokens, l->inner, l->hidden)));
   o.bytes = at;
   return o;
@@ -105,7 +108,7 @@ mpg_status make_copies(DeviceInfo* dev, std::initializer_list<Source*> list, uin
   std::memset(&p, 0, sizeof(p));
   for (Source* s : list) {
     if (!s->copy) continue;
-    const int64_t ld = fused_line(s->cols);
+    const int64_t ld = fused_wide_line(s->cols);
     p.mat[p.count++] = PadParams::Matrix{static_cast<const uint16_t*>(s->ptr), reinterpret_cast<uint16_t*>(ws + s->at), s->ld,
                                          ld, s->rows, s->cols};
     s->ptr = ws + s->at;
@@ -162,20 +165,20 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
   DeviceInfo* dev = nullptr;
   if ((s = get_device(&dev)) != MPG_OK) return s;
 
+  if ((s = make_copies(dev, {&o.x, &o.wg, &o.wu}, static_cast<uint8_t*>(workspace), st)) != MPG_OK) return s;
   if (l.tokens <= kFewRows) {
     FewRowsParams p;
     std::memset(&p, 0, sizeof(p));
-    p.x = l.x;
-    p.ldx = l.ldx;
-    p.w = l.wg;
-    p.ldw = l.ldwg;
-    p.wu = l.wu;
-    p.ldwu = l.ldwu;
+    p.x = o.x.ptr;
+    p.ldx = o.x.ld;
+    p.w = o.wg.ptr;
+    p.ldw = o.wg.ld;
+    p.wu = o.wu.ptr;
+    p.ldwu = o.wu.ld;
     p.bf16 = l.dtype == MPG_BF16;
     p.rows = (int32_t)l.tokens;
     p.n = (int32_t)l.inner;
-    p.k = (int32_t)l.hidden;
-    p.vec = !o.x.copy && !o.wg.copy && !o.wu.copy && l.hidden % 8 == 0;
+    p.k = (int32_t)fused_line(l.hidden);
     p.act = (int32_t)l.act;
     p.y = Y;
     p.ldy = ldy;
@@ -186,7 +189,6 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
     return launch_few_rows(dev, p, true, st);
   }
 
-  if ((s = make_copies(dev, {&o.x, &o.wg, &o.wu}, static_cast<uint8_t*>(workspace), st)) != MPG_OK) return s;
   FusedGemmParams p;
   std::memset(&p, 0, sizeof(p));
   if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;

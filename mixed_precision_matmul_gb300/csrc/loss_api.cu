@@ -74,11 +74,14 @@ Layout layout(const mpg_vocab_loss* l, bool backward) {
   const int64_t t = l->tokens;
   o.x = source(l->x, l->ldx, t, l->hidden);
   o.w = source(l->w, l->ldw, l->vocab, l->hidden);
-  if (backward || t > kFewRows)
-    for (Source* s : {&o.x, &o.w})
-      if (s->copy) s->at = take((size_t)s->rows * (size_t)fused_line(s->cols) * 2);
+  // (few rows are multiplied in whole chunks of eight: zeros behind all of them, or none needed)
+  const bool all = !backward && t <= kFewRows && l->hidden % 8 != 0;
+  for (Source* s : {&o.x, &o.w}) {
+    s->copy = s->copy || all;
+    if (s->copy) s->at = take((size_t)s->rows * (size_t)fused_wide_line(s->cols) * 2);
+  }
   if (!backward) {
-    const int64_t parts = t <= kFewRows ? few_rows_parts((int)t, l->vocab) : 2 * ((l->vocab + 127) / 128);
+    const int64_t parts = t <= kFewRows ? few_rows_parts(l->vocab) : 2 * ((l->vocab + 127) / 128);
     o.stats = take((size_t)parts * (size_t)t * sizeof(float2));
     o.target_logit = take((size_t)t * sizeof(float));
     if (t > kFewRows) o.slots = take(fused_slot_bytes(product(FusedEpi::kStats, t, l->vocab, l->hidden)));
@@ -87,14 +90,13 @@ Layout layout(const mpg_vocab_loss* l, bool backward) {
     o.pieces = (l->vocab + piece - 1) / piece;
     piece = ((l->vocab + o.pieces - 1) / o.pieces + 255) / 256 * 256;
     o.pieces = (l->vocab + piece - 1) / piece;
-    o.piece = std::min(piece, fused_line(l->vocab));
+    o.piece = std::min(piece, fused_wide_line(l->vocab));
     o.grad = take((size_t)t * (size_t)o.piece * 2);
     o.ldsum = (l->hidden + 3) / 4 * 4;
     if (o.pieces > 1) o.sum = take((size_t)t * (size_t)o.ldsum * sizeof(float));
     o.partial = take(kScaleBlocks * sizeof(float));
-    o.slots = take(std::max({fused_slot_bytes(product(FusedEpi::kPlain, t, l->hidden, o.piece)),
-                             fused_slot_bytes(product(FusedEpi::kPlain, o.piece, l->hidden, t)),
-                             fused_slot_bytes(product(FusedEpi::kProb, t, o.piece, l->hidden))}));
+    const FusedLaunch to_x = product(FusedEpi::kPlain, t, l->hidden, o.piece), to_w = product(FusedEpi::kPlain, o.piece, l->hidden, t);
+    o.slots = take(std::max(fused_slot_bytes(to_x, &to_w), fused_slot_bytes(product(FusedEpi::kProb, t, o.piece, l->hidden))));
   }
   o.bytes = at;
   return o;
@@ -105,7 +107,7 @@ mpg_status make_copies(DeviceInfo* dev, Layout& o, uint8_t* ws, cudaStream_t str
   std::memset(&p, 0, sizeof(p));
   for (Source* s : {&o.x, &o.w}) {
     if (!s->copy) continue;
-    const int64_t ld = fused_line(s->cols);
+    const int64_t ld = fused_wide_line(s->cols);
     p.mat[p.count++] = PadParams::Matrix{static_cast<const uint16_t*>(s->ptr), reinterpret_cast<uint16_t*>(ws + s->at), s->ld,
                                          ld, s->rows, s->cols};
     s->ptr = ws + s->at;
@@ -152,18 +154,18 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
   LossJoinParams j;
   std::memset(&j, 0, sizeof(j));
 
+  if ((s = make_copies(dev, o, ws, st)) != MPG_OK) return s;
   if (l.tokens <= kFewRows) {
     FewRowsParams p;
     std::memset(&p, 0, sizeof(p));
-    p.x = l.x;
-    p.ldx = l.ldx;
-    p.w = l.w;
-    p.ldw = l.ldw;
+    p.x = o.x.ptr;
+    p.ldx = o.x.ld;
+    p.w = o.w.ptr;
+    p.ldw = o.w.ld;
     p.bf16 = l.dtype == MPG_BF16;
     p.rows = (int32_t)l.tokens;
     p.n = (int32_t)l.vocab;
-    p.k = (int32_t)l.hidden;
-    p.vec = !o.x.copy && !o.w.copy && l.hidden % 8 == 0;
+    p.k = (int32_t)fused_line(l.hidden);
     p.target = l.target;
     p.target_bytes = l.target_bytes;
     p.target_stride = l.target_stride;
@@ -171,9 +173,8 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
     p.stats = stats;
     p.target_logit = target_logit;
     if ((s = launch_few_rows(dev, p, false, st)) != MPG_OK) return s;
-    j.parts = few_rows_parts((int)l.tokens, l.vocab);
+    j.parts = few_rows_parts(l.vocab);
   } else {
-    if ((s = make_copies(dev, o, ws, st)) != MPG_OK) return s;
     FusedGemmParams p;
     std::memset(&p, 0, sizeof(p));
     if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
