@@ -524,7 +524,10 @@ typedef struct {
 
 /* Y, and with G and U (both or neither NULL) the projections X Wg^T and X Wu^T
  * for the backward pass.  Sums are fp32; Y is computed from them before they
- * are rounded, and every result is rounded once.  hidden 0: Y = 0. */
+ * are rounded, and every result is rounded once.  G and U are fp16 in an fp16
+ * layer; in a bf16 layer they are 16-bit codes with a sign, 6 bits of exponent
+ * (bias 31) and 9 of fraction, subnormals from 2^-39 on, infinity (0x7e00) above
+ * 2^32 and NaN: a quarter of bf16's rounding.  hidden 0: Y = 0. */
 size_t mpg_gated_gemm_workspace_size(const mpg_gated_layer* layer);
 mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, void* G, int64_t ldg, void* U, int64_t ldu,
                           void* workspace, size_t workspace_bytes, void* stream);
@@ -550,7 +553,9 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
  *   integers of 4 or 8 bytes, target_stride apart (in integers).
  * A target that is neither ignore_index nor a class makes loss and lse NaN, and
  * in the backward pass its row of dX and all of dW.  loss and lse: tokens fp32.
- * Maxima, sums and logits are fp32; a NaN in a row makes its loss NaN. */
+ * Maxima, sums and logits are fp32, logits summed by the tensor cores over at
+ * most 1024 of hidden at a time: loss and lse are off by about 5e-7 of lse.  A NaN
+ * in a row makes its loss NaN. */
 typedef struct {
   int64_t tokens, hidden, vocab;
   mpg_dtype dtype;              /* MPG_F16 or MPG_BF16 */
@@ -570,9 +575,9 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
  *     D = (e^(l - lse) - [c == target]) * dloss,
  *     dX = D W,  dW = D^T X  (either may be NULL).
  * D is made for a piece of the vocabulary at a time (512 MB at most, or 256
- * classes), from logits that are computed again; it is rounded once to the
- * 16-bit type, in fp16 times a power of two that brings the largest dloss to
- * [2^14, 2^15).  dX is summed over the pieces in fp32.  tokens 0: dW = 0. */
+ * classes), from logits that are computed again; divided by the largest dloss (and
+ * in fp16 times 2^14) it is rounded once to the 16-bit type.  dX is summed over the
+ * pieces in fp32.  tokens 0: dW = 0. */
 size_t mpg_linear_cross_entropy_backward_workspace_size(const mpg_vocab_loss* desc);
 mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const float* lse, const float* dloss,
                                              int64_t dloss_stride, void* dX, int64_t lddx, void* dW, int64_t lddw,
@@ -583,10 +588,10 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
  *     out = g * min(1, max_norm / (norm + eps)),  rounded once to out's type.
  * Tensors are packed, of any size (0 too) and type each; out may be g (in the
  * same type), and overlap nothing else of the call (MPG_ERR_INVALID_ARG).
- * max_norm >= 0, infinity to scale by 1.  Squares are summed in fp32 by eights
- * and in 64 bits beyond, wherever fp32 cannot hold them too; norms above fp32's
- * range are infinity.  An infinite norm makes the factor 0 (infinities become
- * NaN), a NaN makes everything NaN.  n <= 2^20. */
+ * max_norm >= 0; infinity: factor 1, whatever the norm.  Squares are summed in
+ * fp32 by 32 at most and in 64 bits beyond, and in 64 bits wherever fp32 cannot hold
+ * them; norms above fp32's range are infinity.  An infinite norm makes the factor 0
+ * (infinities become NaN), a NaN makes everything NaN.  n <= 2^20. */
 typedef struct {
   const void* g;
   void* out;

@@ -59,7 +59,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, eps: float = CLIP_EPS, work
         raise ValueError("no gradients")
     if stream is not None:
         return _on_stream(stream, [*grads, *([] if outs is grads else outs), workspace],
-                          lambda: clip_grad_norm(grads, max_norm, out, eps, workspace))
+                          lambda: clip_grad_norm(grads, max_norm, outs, eps, workspace))
     if workspace is None:
         calls = _calls()
         r = calls.clip_grad_norm(grads, outs, max_norm, eps) if calls else None
@@ -69,7 +69,7 @@ def clip_grad_norm(grads, max_norm: float, out=None, eps: float = CLIP_EPS, work
             return r
     index = _device_index(*grads, *outs, workspace)
     if index != torch.cuda.current_device():
-        return _on_device(index, lambda: clip_grad_norm(grads, max_norm, out, eps, workspace))
+        return _on_device(index, lambda: clip_grad_norm(grads, max_norm, outs, eps, workspace))
     table = []
     for i, (g, o) in enumerate(zip(grads, outs)):
         for t in (g, o):

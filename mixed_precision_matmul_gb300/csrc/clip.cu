@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
   const float norm = (float)sqrt(sum);
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
   float f = p.max_norm / (norm + p.eps);
-  if (f >= 1.0f) f = 1.0f;                                  // (a NaN stays)
+  if (f >= 1.0f || p.max_norm == INFINITY) f = 1.0f;        // (a NaN stays)
   const uint32_t first = first_chunk(p.chunks, blockIdx.x, gridDim.x);
   uint32_t c = first_chunk(p.chunks, blockIdx.x + 1, gridDim.x);
   if (first == c) return;

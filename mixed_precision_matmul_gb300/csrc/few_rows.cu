@@ -62,13 +62,11 @@ __device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, int thr
         up += red[w][j + 8][t];
       }
       if (t < p.rows && first + j < p.n) {
-        auto store = [&](void* base, int64_t ld, float v) {
-          static_cast<uint16_t*>(base)[(int64_t)t * ld + first + j] = (uint16_t)pack16(v, 0.0f, bf16);
-        };
-        store(p.y, p.ldy, act_value(gt, p.act) * up);
+        auto store = [&](void* base, int64_t ld, uint32_t w) { static_cast<uint16_t*>(base)[(int64_t)t * ld + first + j] = (uint16_t)w; };
+        store(p.y, p.ldy, pack16(act_value(gt, p.act) * up, 0.0f, bf16));
         if (p.g) {
-          store(p.g, p.ldg, gt);
-          store(p.u, p.ldu, up);
+          store(p.g, p.ldg, pack_kept(gt, 0.0f, bf16));
+          store(p.u, p.ldu, pack_kept(up, 0.0f, bf16));
         }
       }
     }

@@ -78,6 +78,29 @@ __device__ __forceinline__ float load16(const void* base, int64_t idx, bool bf16
   return bf16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
 }
 
+// Codes of the projections that a bf16 layer keeps: sign, 6 bits of exponent (bias
+// 31), 9 of fraction, subnormals down to 2^-39, infinity and NaN above 2^32.  Their
+// rounding is a quarter of bf16's, so that the gradients are off by the two roundings
+// that any 16-bit product has (of its operand and its result; in bf16 codes 0.0031
+// of the norm instead of 0.0024 at 8192 x 4096 x 11008), and their range is far
+// beyond fp16's, which an activation may leave.
+__device__ __forceinline__ uint32_t encode_kept(float x) {
+  const uint32_t b = __float_as_uint(fabsf(x) * 0x1p-96f);        // the exponent's bias, subnormals too
+  const uint32_t c = min((b + 0x1fffu + ((b >> 14) & 1u)) >> 14, 0x7e00u);
+  return (x != x ? 0x7fffu : c) | (__float_as_uint(x) >> 16 & 0x8000u);
+}
+__device__ __forceinline__ float decode_kept(uint32_t w) {
+  const uint32_t c = w & 0x7fffu;
+  const float x = __uint_as_float(c << 14) * 0x1p96f;
+  return __uint_as_float((c >= 0x7e00u ? 0x7f800000u | (c & 0x1ffu) << 14 : __float_as_uint(x)) | (w & 0x8000u) << 16);
+}
+__device__ __forceinline__ uint32_t pack_kept(float lo, float hi, bool bf16) {
+  return bf16 ? encode_kept(lo) | encode_kept(hi) << 16 : pack16(lo, hi, false);
+}
+__device__ __forceinline__ float2 unpack_kept(uint32_t w, bool bf16) {
+  return bf16 ? make_float2(decode_kept(w & 0xffffu), decode_kept(w >> 16)) : unpack16(w, false);
+}
+
 // Eight 16-bit elements from element `shift` (0 .. 7) of two neighbouring words on.
 __device__ __forceinline__ uint4 shift_words(const uint4& a, const uint4& b, int shift) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -102,28 +125,35 @@ __device__ __forceinline__ int64_t target_of(const void* target, int bytes, int6
   return t == ignore ? -1 : t < 0 || t >= vocab ? -2 : t;
 }
 
-// The power of two that brings the largest of a tensor's absolute values to
-// [2^exp, 2^(exp+1)), and its inverse; 1 where the largest is 0 or not finite.
-// Gradients in fp16 are multiplied by it before they are rounded for the
-// tensor cores, and the products by the inverse: fp16 has 5 bits of exponent,
-// and a gradient of a mean over thousands of tokens leaves them.
-struct Pow2 {
-  float mul, inv;
+// The scale of gradients that are rounded to 16 bits for the tensor cores: they
+// are divided by `div` and multiplied by `mul` before, and the products by `inv`.
+// fp16 has 5 bits of exponent, and a gradient of a mean over thousands of tokens
+// leaves them.
+//   by a power of two  the largest of the tensor's absolute values comes to
+//                      [2^exp, 2^(exp+1));
+//   by the largest     it comes to 2^exp: where all tokens weigh the same, their
+//                      weight is then exact, and not off by one rounding in all of
+//                      them at once (half a step of bf16 in the whole gradient).
+// 1 where the largest is 0 or not finite.
+struct Scale {
+  float div, mul, inv;
 };
-__device__ __forceinline__ Pow2 scale_pow2(float largest, int exp) {
-  if (!(largest > 0.0f) || largest > 3.0e38f) return Pow2{1.0f, 1.0f};
-  int e = exp - (ilogbf(largest));
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ Scale make_scale(float largest, int exp, bool by_largest) {
+  if (!(largest > 0.0f) || largest > 3.0e38f) return Scale{1.0f, 1.0f, 1.0f};
+  if (by_largest) return Scale{largest, pow2(exp), largest * pow2(-exp)};
+  int e = exp - ilogbf(largest);
   e = e > 126 ? 126 : e < -126 ? -126 : e;
-  return Pow2{__uint_as_float((uint32_t)(127 + e) << 23), __uint_as_float((uint32_t)(127 - e) << 23)};
+  return Scale{1.0f, pow2(e), pow2(-e)};
 }
 // By a whole warp, after griddep_wait.
-__device__ __forceinline__ Pow2 warp_scale(const float* partial, int exp) {
-  if (!partial) return Pow2{1.0f, 1.0f};
+__device__ __forceinline__ Scale warp_scale(const float* partial, int exp, bool by_largest) {
+  if (!partial) return Scale{1.0f, 1.0f, 1.0f};
   float x = 0.0f;
   for (int i = threadIdx.x & 31; i < kScaleBlocks; i += 32) x = fmaxf(x, ld_global(partial + i));
 #pragma unroll
   for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return scale_pow2(x, exp);
+  return make_scale(x, exp, by_largest);
 }
 
 }  // namespace mpg

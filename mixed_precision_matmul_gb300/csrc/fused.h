@@ -56,8 +56,8 @@ struct FusedGemmParams {
   const void* dy;                   // kGatedGrad
   int64_t lddy;
   int32_t dy_vec;
-  const float* scale;               // partial maxima behind the power of two that fp16 gradients carry, or null
-  int32_t scale_exp;                // the largest is brought to [2^e, 2^(e+1))
+  const float* scale;               // partial maxima behind the scale that 16-bit gradients carry, or null
+  int32_t scale_exp, scale_largest; // see Scale
 
   // cross entropy
   const void* target;

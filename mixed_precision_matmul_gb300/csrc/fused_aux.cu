@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const __grid_constant__
   griddep_wait();
   griddep_launch_dependents();
   const bool bf16 = p.bf16 != 0, vec = p.vec != 0;
-  const float s = warp_scale(p.scale, p.scale_exp).mul;
+  const float s = warp_scale(p.scale, p.scale_exp, false).mul;
   const int64_t per_line = (p.cols + 7) / 8, n = p.rows * per_line;
   const bool small = n < INT_MAX;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const __grid_constant__
     uint32_t dg[4], du[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 yy = unpack16(y[j], bf16), gg = unpack16(g[j], bf16), uu = unpack16(u[j], bf16);
+      const float2 yy = unpack16(y[j], bf16), gg = unpack_kept(g[j], bf16), uu = unpack_kept(u[j], bf16);
       float a0, d0, a1, d1;
       act_both(gg.x, p.act, a0, d0);
       act_both(gg.y, p.act, a1, d1);

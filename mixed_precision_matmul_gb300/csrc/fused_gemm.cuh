@@ -70,6 +70,10 @@ struct FusedTraits {
   static constexpr int kATile = 2 * kHalf;
   static constexpr int kStage = 2 * kATile;
   static constexpr int kStages = 6;
+  // Blocks of k that are summed by the tensor cores at a time: their sums cut off
+  // what fp32 does not hold, always towards zero, and the loss is an fp32 number
+  // (2e-6 off at k = 4096 in one sum, 5e-7 in sums of 1024 added by the epilogue).
+  static constexpr int kChunk = E == FusedEpi::kStats ? 16 : INT_MAX;
   static constexpr int kAccBufs = 2;
   static constexpr int kTmemCols = kAccBufs * kTile;
   static constexpr int kEpiWarps = 8;
@@ -203,9 +207,9 @@ __device__ __forceinline__ void load_block16(uint32_t stg, int lane, uint32_t (&
 __device__ __forceinline__ int64_t row_target(const FusedGemmParams& p, int row) {
   return target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, row);
 }
-__device__ __forceinline__ float row_weight(const FusedGemmParams& p, int row, int64_t target, float mul) {
+__device__ __forceinline__ float row_weight(const FusedGemmParams& p, int row, int64_t target, const Scale& sc) {
   if (target < 0) return target == -1 ? 0.0f : NAN;
-  return mul * ld_global(p.dloss + (int64_t)row * p.dloss_stride);
+  return sc.mul * (ld_global(p.dloss + (int64_t)row * p.dloss_stride) / sc.div);
 }
 
 struct FusedTile {
@@ -409,37 +413,41 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
       bool ok = true;
       FusedItems items(p, worker, workers);
       FusedItem x;
-      for (; ok && items.template next<T::kEpi == FusedEpi::kPlain>(p, x); ++g) {
-        const uint32_t ab = g % T::kAccBufs;
-        const uint32_t ph = ((g / T::kAccBufs) & 1u) ^ 1u;
-        if (!(T::kPair ? warp_wait_relaxed(&acc_empty[ab], ph, ctl) : warp_wait(&acc_empty[ab], ph, ctl))) { ok = false; break; }
-        tc_fence_after_sync();
-        const uint32_t d0 = d_base + ab * T::kTile;
+      while (ok && items.template next<T::kEpi == FusedEpi::kPlain>(p, x)) {
         const bool a_mn = p.prod[x.which].a_mn_major != 0, b_mn = p.prod[x.which].b_mn_major != 0;
         const uint32_t idesc = make_idesc(p.bf16 ? 1u : 0u, a_mn, b_mn, T::kTile, T::kTile);
         // the start address sits in the descriptor's low bits, in units of 16 bytes
         const uint64_t a_desc = operand_desc<T>(op_smem, a_mn, 0), b_desc = operand_desc<T>(op_smem + T::kATile, b_mn, 0);
         const uint32_t a_step = (a_mn ? T::kInstrK * T::kRowBytes : 32) / 16, b_step = (b_mn ? T::kInstrK * T::kRowBytes : 32) / 16;
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
-          if (!warp_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
+        for (int c0 = x.kb0; ok && c0 < x.kb1; ++g) {
+          const int c1 = x.kb1 - c0 > T::kChunk ? c0 + T::kChunk : x.kb1;
+          const uint32_t ab = g % T::kAccBufs;
+          const uint32_t ph = ((g / T::kAccBufs) & 1u) ^ 1u;
+          if (!(T::kPair ? warp_wait_relaxed(&acc_empty[ab], ph, ctl) : warp_wait(&acc_empty[ab], ph, ctl))) { ok = false; break; }
           tc_fence_after_sync();
-          const uint64_t at = (uint64_t)(st * (T::kStage / 16));
-          if (leader) {
+          const uint32_t d0 = d_base + ab * T::kTile;
+          for (int kb = c0; kb < c1; ++kb) {
+            if (!warp_wait(&op_full[st], st_ph, ctl)) { ok = false; break; }
+            tc_fence_after_sync();
+            const uint64_t at = (uint64_t)(st * (T::kStage / 16));
+            if (leader) {
 #pragma unroll
-            for (int ks = 0; ks < T::kKSteps; ++ks) {
-              const uint64_t da = a_desc + at + ks * a_step, db = b_desc + at + ks * b_step;
-              const uint32_t acc = (kb > x.kb0 || ks > 0) ? 1u : 0u;
-              if constexpr (T::kPair) mma_f16_pair(d0, da, db, idesc, acc);
-              else mma_f16(d0, da, db, idesc, acc);
+              for (int ks = 0; ks < T::kKSteps; ++ks) {
+                const uint64_t da = a_desc + at + ks * a_step, db = b_desc + at + ks * b_step;
+                const uint32_t acc = (kb > c0 || ks > 0) ? 1u : 0u;
+                if constexpr (T::kPair) mma_f16_pair(d0, da, db, idesc, acc);
+                else mma_f16(d0, da, db, idesc, acc);
+              }
+              commit(&op_empty[st], 0x3);
+              if (kb + 1 == c1) commit(&acc_full[ab], 0x3);
             }
-            commit(&op_empty[st], 0x3);
-            if (kb + 1 == x.kb1) commit(&acc_full[ab], 0x3);
+            __syncwarp();
+            if (++st == T::kStages) {
+              st = 0;
+              st_ph ^= 1u;
+            }
           }
-          __syncwarp();
-          if (++st == T::kStages) {
-            st = 0;
-            st_ph ^= 1u;
-          }
+          c0 = c1;
         }
       }
       // every MMA completes before TMEM is released
@@ -458,11 +466,12 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
     constexpr int kCc = T::kTileN / 32 / 2;         // 32-column chunks of one warp
     const int cc0 = half * kCc;
     const bool bf16 = p.bf16 != 0;
-    const Pow2 sc = warp_scale(p.scale, p.scale_exp);
+    const Scale sc = warp_scale(p.scale, p.scale_exp, p.scale_largest != 0);
     uint32_t g = 0;
     FusedItems items(p, worker, workers);
+    constexpr bool kAhead = T::kEpi == FusedEpi::kGatedGrad;
     FusedItem x, ahead;
-    bool more = items.template next<T::kEpi == FusedEpi::kPlain>(p, ahead);
+    bool more = kAhead && items.template next<false>(p, ahead);
     // dY's elements of a chunk, a row a lane, on their way while the accumulator is waited for
     uint32_t dyw[16];
     auto first_row = [&](const FusedItem& i) { return i.mb * T::kTile + (int)rank * T::BM + 32 * q; };
@@ -470,10 +479,15 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
       if (row < p.prod[0].m && col < p.prod[0].n)
         load_block16(stg, lane, dyw, Block16{const_cast<void*>(p.dy), p.lddy, row, p.prod[0].m, col, p.prod[0].n, p.dy_vec != 0});
     };
-    if (T::kEpi == FusedEpi::kGatedGrad && more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
-    for (; more; ++g) {
-      x = ahead;
-      more = items.template next<T::kEpi == FusedEpi::kPlain>(p, ahead);
+    if (more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
+    while (true) {
+      if constexpr (kAhead) {
+        if (!more) break;
+        x = ahead;
+        more = items.template next<false>(p, ahead);
+      } else {
+        if (!items.template next<T::kEpi == FusedEpi::kPlain>(p, x)) break;
+      }
       const FusedProduct& pr = p.prod[x.which];
       const bool second = x.mb >= pr.mb_second;
       const uint32_t ab = g % T::kAccBufs;
@@ -498,12 +512,83 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           target = row_target(p, row);
           if constexpr (T::kEpi == FusedEpi::kProb) {
             lse2 = kLog2e * ld_global(p.lse + row);
-            weight = row_weight(p, row, target, sc.mul);
+            weight = row_weight(p, row, target, sc);
           }
         }
       }
+      if constexpr (T::kEpi == FusedEpi::kStats) {
+        // the chunks' sums, in registers: a row's half of the tile
+        constexpr int kCols = T::kTile / 2;
+        float acc[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+        bool live = true;
+        for (int c0 = x.kb0; c0 < x.kb1; c0 = x.kb1 - c0 > T::kChunk ? c0 + T::kChunk : x.kb1, ++g) {
+          const uint32_t buf = g % T::kAccBufs;
+          if (!warp_wait(&acc_full[buf], (g / T::kAccBufs) & 1u, ctl)) { live = false; break; }
+          tc_fence_after_sync();
+          const uint32_t from = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * T::kTile + half * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16) {
+            float v[16];
+            tmem_ld_16cols(from + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (T::kPair) mbar_arrive_cluster_relaxed(acc_empty0 + buf * 8u);
+            else mbar_arrive(&acc_empty[buf]);
+          }
+        }
+        if (!live) break;
+        if (x.slot >= 0) {
+          if (row0 >= pr.m) continue;
+          float* slot = p.slots + (int64_t)x.slot * (T::kTile * T::kTile) + (int64_t)((int)rank * T::BM + 32 * q) * T::kTile + half * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) {
+            stage_write_row(stg, lane, acc + c);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(slot + (i * 4 + (lane >> 3)) * T::kTile + c + (lane & 7) * 4) = stage_read_chunk(stg, lane, i);
+            __syncwarp();
+          }
+          continue;
+        }
+        const int left = pr.n - col_tile - half * kCols;        // columns of the matrix from here on
+        const int64_t at = target - (p.col0 + col_tile + half * kCols);   // (without a class: below 0)
+        float top = -INFINITY, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        bool nan = false;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          // (a bit for the target's column: compared with its index, the values went to local memory)
+          const uint32_t mine = at >= c && at < c + 32 ? 1u << (at - c) : 0u;
+          if (mine) {
+            float l = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) l = mine & (1u << j) ? acc[c + j] : l;
+            p.target_logit[row] = l;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            acc[c + j] = c + j < left ? kLog2e * acc[c + j] : -INFINITY;
+            nan = nan || acc[c + j] != acc[c + j];
+            top = fmaxf(top, acc[c + j]);
+          }
+        }
+        const float base = fabsf(top) == INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sum[j % 4] += ex2(acc[j] - base);
+        if (row < pr.m)
+          p.stats[(int64_t)(x.nb * 2 + half) * pr.m + row] = make_float2(top, nan ? NAN : (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        continue;
+      } else {
       if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
       tc_fence_after_sync();
+      ++g;
       if (x.slot >= 0) {
         // sums of a part of k, as they are: rows of the tile, whole lines a store
         float* slot = p.slots + (int64_t)x.slot * (T::kTile * T::kTile) + (int64_t)((int)rank * T::BM + 32 * q) * T::kTile;
@@ -523,7 +608,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
                 stage_read_chunk(stg, lane, i);
           __syncwarp();
         }
-        if (T::kEpi == FusedEpi::kGatedGrad && more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
+        if (kAhead && more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
         continue;
       }
 
@@ -545,18 +630,20 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
             else if (more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
           }
           if (row0 >= pr.m || col0 >= pr.n) continue;
-          auto store = [&](int i, auto value) {
+          auto store = [&](int i, auto word) {
             uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = pack16(value(2 * j), value(2 * j + 1), bf16);
+            for (int j = 0; j < 16; ++j) w[j] = word(2 * j);
             store_block16(stg, lane, w, Block16{pr.out[i], pr.ldo[i], row0, pr.m, col0, pr.n, pr.out_vec[i] != 0});
           };
           if constexpr (T::kEpi == FusedEpi::kGated) {
             if (pr.out[1]) {
-              store(1, [&](int j) { return gt[j]; });
-              store(2, [&](int j) { return up[j]; });
+              store(1, [&](int j) { return pack_kept(gt[j], gt[j + 1], bf16); });
+              store(2, [&](int j) { return pack_kept(up[j], up[j + 1], bf16); });
             }
-            store(0, [&](int j) { return act_value(gt[j], T::kAct) * up[j]; });
+            store(0, [&](int j) {
+              return pack16(act_value(gt[j], T::kAct) * up[j], act_value(gt[j + 1], T::kAct) * up[j + 1], bf16);
+            });
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -567,55 +654,10 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
               gt[j] = dy * up[j] * d;
               up[j] = dy * a;
             }
-            store(0, [&](int j) { return gt[j]; });
-            store(1, [&](int j) { return up[j]; });
+            store(0, [&](int j) { return pack16(gt[j], gt[j + 1], bf16); });
+            store(1, [&](int j) { return pack16(up[j], up[j + 1], bf16); });
           }
         }
-      } else if constexpr (T::kEpi == FusedEpi::kStats) {
-        float top = -INFINITY, sum = 0.0f;
-        const int last = pr.n - col_tile;            // columns of the tile inside the matrix
-#pragma unroll 1
-        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
-          float v[32];
-          tmem_ld_32cols(tacc + cc * 32, v);
-          tmem_ld_wait();
-          if (cc == cc0 + kCc - 1) release();
-          if (cc * 32 >= last) continue;
-          // (a bit for the target's column: compared with its index, the values went to local memory)
-          const int64_t at = target - (p.col0 + col_tile + cc * 32);   // (without a class: below 0)
-          const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
-          if (mine) {
-            float l = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) l = mine & (1u << j) ? v[j] : l;
-            p.target_logit[row] = l;
-          }
-          float here = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            v[j] = cc * 32 + j < last ? kLog2e * v[j] : -INFINITY;
-            here = fmaxf(here, v[j]);
-          }
-          // (a row of -infinities, or one that has +infinity, keeps its maximum and a sum of NaN-free terms)
-          const float base = fmaxf(top, here);
-          if (base == -INFINITY) {
-            bool nan = false;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) nan = nan || v[j] != v[j];
-            if (nan) sum = NAN;
-            continue;
-          }
-          const float b = base == INFINITY ? 0.0f : base;
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            s0 += ex2(v[j] - b);
-            s1 += ex2(v[j + 1] - b);
-          }
-          sum = (top == -INFINITY ? sum : sum * ex2(top - b)) + (s0 + s1);
-          top = base;
-        }
-        if (row < pr.m) p.stats[(int64_t)(x.nb * 2 + half) * pr.m + row] = make_float2(top, sum);
       } else if constexpr (T::kEpi == FusedEpi::kProb) {
         float v[32];
         tmem_ld_32cols(tacc + cc0 * 32, v);
@@ -707,6 +749,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           __syncwarp();
         }
       }
+      }
     }
   }
 
@@ -732,6 +775,17 @@ __device__ __forceinline__ void store_four(void* out, int64_t at, const float (&
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j < left) out_store(out, at + j, v[j], dt);
+  }
+}
+__device__ __forceinline__ void store_kept(void* out, int64_t at, const float (&v)[4], int left, bool vec, bool bf16) {
+  const uint32_t w[2] = {pack_kept(v[0], v[1], bf16), pack_kept(v[2], v[3], bf16)};
+  uint16_t* to = static_cast<uint16_t*>(out) + at;
+  if (vec && left >= 4) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < left) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
   }
 }
 __device__ __forceinline__ void load_four(float (&v)[4], const void* src, int64_t at, int left, bool vec, int dt) {
@@ -776,7 +830,7 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   const int i = blockIdx.y * kAt + place;
   const int r = i / kPerRow, c = i % kPerRow * 4;
   const int row = (second ? tc.mb - pr.mb_second : tc.mb) * T::kTile + r, col = tc.nb * T::kTileN + c;
-  const Pow2 sc = warp_scale(p.scale, p.scale_exp);
+  const Scale sc = warp_scale(p.scale, p.scale_exp, p.scale_largest != 0);
   const bool in = row < pr.m;
   const int left = pr.n - col;                       // columns of the matrix from here on
   constexpr int64_t kSlot = T::kTile * T::kTile;
@@ -817,8 +871,8 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
     auto at = [&](int k) { return (int64_t)row * pr.ldo[k] + col; };
     if constexpr (T::kEpi == FusedEpi::kGated) {
       if (pr.out[1]) {
-        store_four(pr.out[1], at(1), gt, left, pr.out_vec[1], type);
-        store_four(pr.out[2], at(2), up, left, pr.out_vec[2], type);
+        store_kept(pr.out[1], at(1), gt, left, pr.out_vec[1], p.bf16 != 0);
+        store_kept(pr.out[2], at(2), up, left, pr.out_vec[2], p.bf16 != 0);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) gt[j] = act_value(gt[j], T::kAct) * up[j];
@@ -875,7 +929,7 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
           p.stats[(int64_t)(tc.nb * 2 + c / (T::kTile / 2)) * pr.m + row] = make_float2(top, s);
       } else {
         if (!in || left <= 0) return;
-        const float lse2 = kLog2e * ld_global(p.lse + row), weight = row_weight(p, row, target, sc.mul);
+        const float lse2 = kLog2e * ld_global(p.lse + row), weight = row_weight(p, row, target, sc);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float e = ex2(fmaf(kLog2e, v[j], -lse2));

@@ -243,12 +243,12 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
   uint16_t* grad = reinterpret_cast<uint16_t*>(ws + o.grad);
   if ((s = make_copies(dev, o, ws, st)) != MPG_OK) return s;
 
-  // fp16: the logits' gradient carries a power of two that brings the largest
-  // dloss to [2^14, 2^15): no element is larger, and a probability of 2^-28 is
-  // still a normal number.
+  // The logits' gradient is divided by the largest dloss; in fp16 it is multiplied
+  // by 2^14 too: no element is larger, and a probability of 2^-28 is still a normal
+  // number.
   const bool half = l.dtype == MPG_F16;
-  constexpr int kExp = 14;
-  if (half) {
+  const int exp = half ? 14 : 0;
+  {
     MaxParams p;
     std::memset(&p, 0, sizeof(p));
     p.rows = l.tokens;
@@ -282,13 +282,15 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
     p.lse = lse;
     p.dloss = dloss;
     p.dloss_stride = dloss_stride;
-    p.scale = half ? partial : nullptr;
-    p.scale_exp = kExp;
+    p.scale = partial;
+    p.scale_exp = exp;
+    p.scale_largest = 1;
     if ((s = launch_fused(dev, product(FusedEpi::kProb, l.tokens, cols, l.hidden), p, slots, st)) != MPG_OK) return s;
     std::memset(&p, 0, sizeof(p));
     p.bf16 = !half;
-    p.scale = half ? partial : nullptr;
-    p.scale_exp = kExp;
+    p.scale = partial;
+    p.scale_exp = exp;
+    p.scale_largest = 1;
     int count = 0;
     const FusedLaunch to_x = product(FusedEpi::kPlain, l.tokens, l.hidden, cols);
     const FusedLaunch to_w = product(FusedEpi::kPlain, cols, l.hidden, l.tokens);

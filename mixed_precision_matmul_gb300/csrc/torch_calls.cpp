@@ -226,6 +226,9 @@ bool layer_of(PyObject* px, PyObject* pg, PyObject* pu, long act, at::Tensor* x,
   return true;
 }
 
+// Of the projections that a layer keeps: fp16, or codes in a bf16 layer.
+at::ScalarType kept_type(const at::Tensor& x) { return x.scalar_type() == at::kHalf ? at::kHalf : at::kShort; }
+
 // (x, wg, wu, activation, keep) -> y or (y, g, u)
 PyObject* gated_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 5 || !g_gated) return PyErr_Format(PyExc_TypeError, "five arguments are expected");
@@ -237,7 +240,8 @@ PyObject* gated_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     c10::DeviceIndex dev;
     mpg_gated_layer l;
     if (!layer_of(args[0], args[1], args[2], act, &x, &wg, &wu, &dev, &l)) Py_RETURN_NONE;
-    for (int i = 0; i < (keep ? 3 : 1); ++i) out[i] = at::empty({l.tokens, l.inner}, x.options());
+    for (int i = 0; i < (keep ? 3 : 1); ++i)
+      out[i] = at::empty({l.tokens, l.inner}, x.options().dtype(i ? kept_type(x) : x.scalar_type()));
     const size_t bytes = g_gated_workspace(&l);
     const at::Tensor ws = bytes ? scratch(bytes, x) : at::Tensor();
     const mpg_status st = g_gated(&l, address(out[0]), l.inner, address(out[1]), l.inner, address(out[2]), l.inner,
@@ -263,8 +267,8 @@ PyObject* gated_gemm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!layer_of(args[1], args[2], args[3], act, &x, &wg, &wu, &dev, &l)) Py_RETURN_NONE;
     if (!matrix16(args[0], dev, x.scalar_type(), l.tokens, l.inner, &dy, &lddy)) Py_RETURN_NONE;
     if (args[5] != Py_None || args[6] != Py_None)
-      if (!matrix16(args[5], dev, x.scalar_type(), l.tokens, l.inner, &g, &ldg) ||
-          !matrix16(args[6], dev, x.scalar_type(), l.tokens, l.inner, &u, &ldu))
+      if (!matrix16(args[5], dev, kept_type(x), l.tokens, l.inner, &g, &ldg) ||
+          !matrix16(args[6], dev, kept_type(x), l.tokens, l.inner, &u, &ldu))
         Py_RETURN_NONE;
     if (need_dx) out[0] = at::empty({l.tokens, l.hidden}, x.options());
     for (int i = 1; i < 3 && need_dw; ++i) out[i] = at::empty({l.inner, l.hidden}, x.options());

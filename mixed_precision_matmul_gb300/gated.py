@@ -59,11 +59,11 @@ def gated_gemm_backward_raw(layer, dY, lddy, G, ldg, U, ldu, dX, lddx, dWg, lddw
 
 
 def _matrix(t, name, dtype=None, shape=None):
-    """Leading dimension of a 16-bit matrix with unit column stride."""
+    """Leading dimension of a 16-bit matrix (of one type, or fp16 or bf16) with unit column stride."""
     torch = _types()[0]
     if t.dim() != 2:
         raise ValueError(f"{name} is a 2-D tensor")
-    if t.dtype not in (torch.float16, torch.bfloat16):
+    if dtype is None and t.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
@@ -84,6 +84,12 @@ def _act(act):
     if code is None:
         raise ValueError(f"unknown activation {act!r}")
     return code
+
+
+def _kept_dtype(dtype):
+    """Of the projections that a layer keeps: fp16, or the codes of mpg_gated_gemm in a bf16 layer."""
+    torch = _types()[0]
+    return torch.int16 if dtype == torch.bfloat16 else dtype
 
 
 def _layer(x, wg, wu, act):
@@ -110,7 +116,9 @@ def gated_gemm(x, wg, wu, act: str = "silu", keep: bool = False, workspace=None,
     (inner, hidden), in one kernel.
 
     ``act`` is "silu", "gelu" or "gelu_tanh".  With ``keep`` returns ``(y, g, u)``,
-    where g and u are the projections that :func:`gated_gemm_backward` can take.
+    where g and u are the projections for :func:`gated_gemm_backward`: fp16 in an
+    fp16 layer, and in a bf16 layer int16 codes of a 16-bit type with more precision
+    than bf16 (mpgemm.h says which).
     """
     torch = _types()[0]
     if stream is not None:
@@ -127,7 +135,9 @@ def gated_gemm(x, wg, wu, act: str = "silu", keep: bool = False, workspace=None,
     if index != torch.cuda.current_device():
         return _on_device(index, lambda: gated_gemm(x, wg, wu, act, keep, workspace))
     layer = _layer(x, wg, wu, code)
-    outs = [torch.empty((layer.tokens, layer.inner), dtype=x.dtype, device=x.device) for _ in range(3 if keep else 1)]
+    kept = _kept_dtype(x.dtype)
+    outs = [torch.empty((layer.tokens, layer.inner), dtype=d, device=x.device)
+            for d in ((x.dtype, kept, kept) if keep else (x.dtype,))]
     args = [v for t in outs for v in (t.data_ptr(), max(layer.inner, 1))] + [0, 0] * (3 - len(outs))
     _hold, *ws = _scratch(_m.lib().mpg_gated_gemm_workspace_size, layer, workspace, x.device)
     gated_gemm_raw(layer, *args, *ws, _raw_stream()(index))
@@ -163,7 +173,7 @@ def gated_gemm_backward(dy, x, wg, wu, act: str = "silu", kept=None, need_dx: bo
     for t, name in ((g, "g"), (u, "u")):
         if (t is None) != (kept is None):
             raise ValueError("g and u are kept together")
-        args += [0, 0] if t is None else [t.data_ptr(), _matrix(t, name, x.dtype, shape)]
+        args += [0, 0] if t is None else [t.data_ptr(), _matrix(t, name, _kept_dtype(x.dtype), shape)]
     # (a weight whose lines have gaps gets a gradient without them)
     outs = [torch.empty(t.shape, dtype=x.dtype, device=x.device) if need else None
             for t, need in ((x, need_dx), (wg, need_dw), (wu, need_dw))]

@@ -58,6 +58,24 @@ def gated(x, wg, wu, name):
     return (a * u, g, u), (ey, eg, eu)
 
 
+def kept_values(t):
+    """The values of kept projections in 64 bits: fp16, or codes with 6 bits of exponent and 9 of fraction."""
+    if t.dtype != torch.int16:
+        return t.to(F64)
+    c = t.to(torch.int32) & 0x7fff
+    e, f = c >> 9, (c & 511).to(F64) / 512
+    v = torch.where(e == 0, f * 2.0 ** -30, (1 + f) * torch.exp2(e.to(F64) - 31))
+    v = torch.where(e == 63, torch.where(f == 0, torch.inf, torch.nan), v)
+    return torch.where(t < 0, -v, v)
+
+
+def check_kept(t, ref, bound):
+    """Kept projections are ref rounded once: half a step is 2^-11 of the value in fp16, 2^-10 in codes."""
+    r, least = (2.0 ** -10, 2.0 ** -40) if t.dtype == torch.int16 else (2.0 ** -11, 2.0 ** -25)
+    off = (kept_values(t) - ref).abs()
+    assert bool((off <= bound * (1 + r) + r * ref.abs() + least).all())
+
+
 def gated_gradients(dy, x, wg, wu, name, kept=None):
     """(dx, dwg, dwu) in 64 bits and bounds of each but for the final rounding."""
     dtype = x.dtype
@@ -67,7 +85,7 @@ def gated_gradients(dy, x, wg, wu, name, kept=None):
         g, u = x @ wg.t(), x @ wu.t()
         eg, eu = e * (x.abs() @ wg.abs().t()), e * (x.abs() @ wu.abs().t())
     else:
-        g, u = (t.to(F64) for t in kept)
+        g, u = (kept_values(t) for t in kept)
         eg = eu = torch.zeros_like(g)
     a, d = act(g, name)
     dg, du = dy * u * d, dy * a
@@ -95,6 +113,7 @@ def loss(x, w, target, ignore=-100):
     counts = target != ignore
     at = torch.where(counts, target, 0).long()
     value = torch.where(counts, lse - l.gather(1, at[:, None])[:, 0], 0.0)
+    # (sums of at most 1024 of k are added in fp32 on the way: no more than the bound of one sum)
     # terms: logits' errors, the logits in units of ln 2 and their differences
     # (2^-24 each of the largest logit), exponentials 2^-22, sums of at most 256 in a
     # row and 2^11 parts after them

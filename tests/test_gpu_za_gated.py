@@ -47,8 +47,8 @@ def test_product(t, h, i, act):
         out, kg, ku = mpg.gated_gemm(x, wg, wu, act=act, keep=True)
         ok()
         plain.check(out, y, ey)
-        plain.check(kg, g, eg)
-        plain.check(ku, u, eu)
+        plain.check_kept(kg, g, eg)
+        plain.check_kept(ku, u, eu)
 
 
 @pytest.mark.parametrize("t,h,i,dtype", [(2048, 512, 4096, "bf16"), (1531, 520, 2741, "fp16"), (4100, 264, 1030, "bf16"),
@@ -59,8 +59,8 @@ def test_product_on_pairs(t, h, i, dtype):
     out, kg, ku = mpg.gated_gemm(x, wg, wu, keep=True)
     ok()
     plain.check(out, y, ey)
-    plain.check(kg, g, eg)
-    plain.check(ku, u, eu)
+    plain.check_kept(kg, g, eg)
+    plain.check_kept(ku, u, eu)
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
@@ -139,6 +139,27 @@ def test_small_and_large_gradients_in_fp16():
     assert all(not t.any() for t in zero)
 
 
+@pytest.mark.parametrize("t", [3, 40])
+def test_kept_projections_over_their_range(t):
+    """One input channel and weights of every size: projections from 2^-60 to 2^120, infinities and NaN."""
+    x = torch.zeros(t, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    x[1, 0] = -1.0
+    w = torch.zeros(256, 8, dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = (1.0 + torch.rand(256, generator=torch.Generator().manual_seed(3))).cuda() * torch.exp2(torch.arange(256, device="cuda") % 90 - 45.0)
+    w[7, 0], w[8, 0], w[9, 0] = float("inf"), float("nan"), 2.0 ** 120
+    _, g, u = mpg.gated_gemm(x, w, w, keep=True)
+    ok()
+    exact = (x[:, :1].double() @ w[:, :1].double().t())
+    for k in (g, u):
+        v = plain.kept_values(k)
+        inside = (exact.abs() < 2.0 ** 32) & ~exact.isnan()
+        off = (v - exact).abs()
+        assert bool((off[inside] <= (2.0 ** -10 * exact.abs() + 2.0 ** -40)[inside]).all())
+        assert torch.equal(v[:, 7].isinf(), torch.ones(t, dtype=torch.bool, device="cuda")) and v[:, 8].isnan().all()
+        assert v[:, 9].isinf().all() and bool((torch.sign(v[1:2, 7]) == -1).all())
+
+
 @pytest.mark.parametrize("t", [5, 100])
 def test_without_elements(t):
     dev = "cuda"
@@ -179,7 +200,8 @@ def test_nothing_is_written_beyond_the_results(t):
     def room(rows, cols):
         return torch.full((rows + 2, cols + pad), mark, dtype=torch.bfloat16, device="cuda")
     import ctypes
-    y, g, u = (room(t, i) for _ in range(3))
+    y, g, u = room(t, i), room(t, i).view(torch.int16), room(t, i).view(torch.int16)
+    gap = int(g[-1, -1])
     need = int(mpg.lib().mpg_gated_gemm_workspace_size(ctypes.byref(lay)))
     ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
     mpg.gated_gemm_raw(lay, *(v for b in (y, g, u) for v in (b.data_ptr(), i + pad)), ws.data_ptr(), need)
@@ -193,7 +215,8 @@ def test_nothing_is_written_beyond_the_results(t):
     ok()
     assert (ws[need:] == 77).all()
     for b, rows, cols in ((y, t, i), (g, t, i), (u, t, i), (outs[0], t, h), (outs[1], i, h), (outs[2], i, h)):
-        assert (b[rows:] == mark).all() and (b[:, cols:] == mark).all() and not (b[:rows, :cols] == mark).any()
+        m = gap if b.dtype == torch.int16 else mark
+        assert (b[rows:] == m).all() and (b[:, cols:] == m).all() and not (b[:rows, :cols] == m).all(dim=1).any()
     # lines with gaps give the same values
     ref = mpg.gated_gemm_backward(dy, x, wg, wu, kept=(g[:t, :i], u[:t, :i]))
     for b, r in zip(outs, ref):
@@ -252,12 +275,13 @@ def test_calls_that_the_plain_path_leaves_to_python():
     for bad in (lambda: mpg.gated_gemm(x, wg, wu[:-1]), lambda: mpg.gated_gemm(x, wg[:, :-8], wu[:, :-8]),
                 lambda: mpg.gated_gemm(x[0], wg, wu), lambda: mpg.gated_gemm(x.t().contiguous().t(), wg, wu),
                 lambda: mpg.gated_gemm_backward(dy[:-1], x, wg, wu),
-                lambda: mpg.gated_gemm_backward(dy, x, wg, wu, kept=(dy, None)),
-                lambda: mpg.gated_gemm_backward(dy, x, wg, wu, kept=(dy, dy[:, 1:])),
+                lambda: mpg.gated_gemm_backward(dy, x, wg, wu, kept=(dy.view(torch.int16), None)),
+                lambda: mpg.gated_gemm_backward(dy, x, wg, wu, kept=(dy.view(torch.int16), dy.view(torch.int16)[:, 1:])),
                 lambda: mpg.gated_gemm(x, wg.cpu(), wu)):
         with pytest.raises(ValueError):
             bad()
-    for bad in (lambda: mpg.gated_gemm(x.float(), wg.float(), wu.float()), lambda: mpg.gated_gemm(x, wg.half(), wu)):
+    for bad in (lambda: mpg.gated_gemm(x.float(), wg.float(), wu.float()), lambda: mpg.gated_gemm(x, wg.half(), wu),
+                lambda: mpg.gated_gemm_backward(dy, x, wg, wu, kept=(dy, dy))):
         with pytest.raises(TypeError):
             bad()
     one = x[:1].expand(40, 64)

@@ -126,6 +126,10 @@ def test_gradients_that_are_no_numbers():
     assert float(mpg.clip_grad_norm(a, 1.0)) == float("inf")
     assert a[1][7].isnan() and not a[0].any() and int((a[1] != 0).sum()) == 1
     a = fresh()
+    a[1][7] = float("inf")
+    assert float(mpg.clip_grad_norm(a, float("inf"))) == float("inf")
+    assert int((a[1] == 1).sum()) == 49 and bool((a[0] == 1).all())
+    a = fresh()
     before = [t.clone() for t in a]
     n = mpg.clip_grad_norm(a, float("inf"))
     assert abs(float(n) - 3050 ** 0.5) < 1e-4 and all(torch.equal(x, y) for x, y in zip(a, before))
@@ -166,6 +170,8 @@ def test_graph_stream_and_workspace():
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     assert torch.equal(mpg.clip_grad_norm(grads, 1.0, out=out2, workspace=ws, stream=side), n2)
+    assert torch.equal(mpg.clip_grad_norm(iter(grads), 1.0, out=iter(out2), stream=side), n2)
+    side.synchronize()
     with pytest.raises(Exception):
         mpg.clip_grad_norm(grads, 1.0, out=out2, workspace=ws[:8])
     ok()
