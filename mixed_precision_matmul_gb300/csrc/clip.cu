@@ -7,7 +7,8 @@
 // pass walks them backwards, so that what the first one read last is still in
 // L2 (129 MB).  Tensors are cut into chunks, numbered through over all of them,
 // and a block takes a run of chunks; a launch's parameters hold the table of its
-// tensors.  A thread has four loads of eight elements on their way.
+// tensors.  A thread has four loads of eight elements on their way.  1.0e9 bf16
+// gradients take 278 us for the norm (7.3 TB/s) and 622 for the scaling (6.5).
 //
 // Squares: a thread sums 32 in fp32 and carries the sums in 64 bits (a sum of
 // eight at a time was bound by the 64-bit adder: 1.0e9 bf16 gradients 483 us).
