@@ -52,6 +52,7 @@ SOURCES = [
     "fused_gated_grad.cu",
     "fused_loss.cu",
     "few_rows.cu",
+    "few_grad.cu",
     "fused_aux.cu",
     "gated_api.cu",
     "loss_api.cu",

@@ -107,6 +107,21 @@ struct FewRowsParams {
 mpg_status launch_few_rows(DeviceInfo* dev, FewRowsParams& p, bool gated, cudaStream_t stream);
 int few_rows_parts(int64_t n);      // of the statistics of n logits
 
+// Weight gradients of few tokens: out[i] = inverse * d[i]^T x (few_grad.cu).  Blocks
+// of rows are counted in a grid's second dimension.
+constexpr int kFewGradTokens = 64;
+constexpr int64_t kFewGradRows = 65535ll * 128;
+struct FewGradParams {
+  const uint16_t *d[2], *x;         // tokens x rows, tokens x cols; lines start on 16 bytes
+  int64_t ldd, ldx;
+  int32_t tokens, rows, cols, count, bf16;
+  void* out[2];                     // lines start on 16 bytes
+  int64_t ldo[2];
+  const float* scale;
+  int32_t scale_exp, scale_largest;
+};
+cudaError_t launch_few_grad(const FewGradParams& p, cudaStream_t stream);
+
 // Copies of matrices whose lines TMA cannot describe.
 struct PadParams {
   struct Matrix {

@@ -219,7 +219,7 @@ mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedL
     const double parts = (double)std::min(2 * all, a.tiles + b.tiles + all) * (double)(tile * tile) * 4.0;
     const double even = (pair ? kPairEdge : kOneEdge) + kJoin + 2.0 * parts / kPartBytes +
                         std::max((double)((units + all - 1) / all) * apart_block, (double)((a.tiles + b.tiles) / all) * way_out);
-    if (slots && a.tiles + b.tiles <= 2 * w && even < best) {
+    if (slots && kb >= kMinUnits && a.tiles + b.tiles <= 2 * w && even < best) {
       best = even;
       form = pair;
       dealt = true;

@@ -307,7 +307,9 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
       x.add = i > 0 ? sum : nullptr;
       x.ldadd = o.ldsum;
     }
-    if (dW) {
+    // (elements of lines off 16 bytes are written faster by the tiles' epilogue)
+    const bool few = dW && l.tokens <= kFewGradTokens && cols <= kFewGradRows && fused_lines_ok(dW, lddw);
+    if (dW && !few) {
       FusedProduct& y = p.prod[count++];
       if ((s = fused_map(&y.map_a[0], grad, o.piece, l.dtype, true, cols, l.tokens)) != MPG_OK) return s;
       if ((s = fused_map(&y.map_b[0], o.x.ptr, o.x.ld, l.dtype, true, l.hidden, l.tokens)) != MPG_OK) return s;
@@ -316,6 +318,28 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
       y.ldo[0] = lddw;
       y.out_dtype = (int32_t)l.dtype;
       y.out_vec[0] = fused_lines_ok(y.out[0], lddw);
+    }
+    if (few) {
+      if (dX && (s = launch_fused(dev, to_x, p, slots, st)) != MPG_OK) return s;
+      FewGradParams y;
+      std::memset(&y, 0, sizeof(y));
+      y.d[0] = grad;
+      y.x = static_cast<const uint16_t*>(o.x.ptr);
+      y.ldd = o.piece;
+      y.ldx = o.x.ld;
+      y.tokens = (int32_t)l.tokens;
+      y.rows = (int32_t)cols;
+      y.cols = (int32_t)l.hidden;
+      y.count = 1;
+      y.bf16 = !half;
+      y.out[0] = static_cast<uint16_t*>(dW) + c0 * lddw;
+      y.ldo[0] = lddw;
+      y.scale = partial;
+      y.scale_exp = exp;
+      y.scale_largest = 1;
+      const cudaError_t e = launch_few_grad(y, st);
+      if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "weight gradient launch: %s", cudaGetErrorString(e));
+      continue;
     }
     s = count == 2 ? launch_fused_two(dev, to_x, to_w, p, slots, st) : launch_fused(dev, dX ? to_x : to_w, p, slots, st);
     if (s != MPG_OK) return s;
