@@ -26,14 +26,14 @@ def product(a, b):
 
 def gradients(x, target, wg, wu, wd, wv):
     """The mean loss over the tokens that count, and the gradients of x, wg, wu, wd and wv."""
-    y, g, u = mpg.gated_gemm(x, wg, wu, keep=True)
+    y, *kept = mpg.gated_gemm(x, wg, wu, keep=True)
     h = product(y, wd.t())
     loss, lse = mpg.linear_cross_entropy(h, wv, target, ignore_index=IGNORE)
     share = 1.0 / (target != IGNORE).sum().clamp(min=1).float()
     dh, dwv = mpg.linear_cross_entropy_backward(h, wv, target, lse, share.expand(target.shape), ignore_index=IGNORE)
     dy = product(dh, wd)
     dwd = product(dh.t(), y)
-    dx, dwg, dwu = mpg.gated_gemm_backward(dy, x, wg, wu, kept=(g, u))
+    dx, dwg, dwu = mpg.gated_gemm_backward(dy, x, wg, wu, kept=kept)
     return loss.sum() * share, (dx, dwg, dwu, dwd, dwv)
 
 

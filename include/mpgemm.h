@@ -506,7 +506,7 @@ mpg_status mpg_orthogonalize(int64_t m, int64_t n, int64_t batch, const void* G,
 /* ---- gated feed-forward product ------------------------------------------
  * Y = act(X Wg^T) * (X Wu^T): both projections of a gated feed-forward layer,
  * the activation and the product in one kernel; and its gradients.
- *   X   tokens x hidden;  Wg, Wu  inner x hidden;  Y, G, U, dY  tokens x inner.
+ *   X   tokens x hidden;  Wg, Wu  inner x hidden;  Y, A, B, dY  tokens x inner.
  * All matrices are row-major and of one 16-bit type, with leading dimensions of
  * at least their lines, any alignment of an element; 16-byte aligned bases and
  * leading dimensions of whole 16 bytes are fastest (others are copied to such
@@ -522,28 +522,28 @@ typedef struct {
   int64_t ldx, ldwg, ldwu;
 } mpg_gated_layer;
 
-/* Y, and with G and U (both or neither NULL) the projections X Wg^T and X Wu^T
- * for the backward pass.  Sums are fp32; Y is computed from them before they
- * are rounded, and every result is rounded once.  G and U are fp16 in an fp16
+/* Y, and with A and B (both or neither NULL) what the gradients are made from: with
+ * G = X Wg^T and U = X Wu^T, A = act(G) and B = U * act'(G).  Sums are fp32; every
+ * result is computed from them and rounded once.  A and B are fp16 in an fp16
  * layer; in a bf16 layer they are 16-bit codes with a sign, 6 bits of exponent
  * (bias 31) and 9 of fraction, subnormals from 2^-39 on, infinity (0x7e00) above
- * 2^32 and NaN: a quarter of bf16's rounding.  hidden 0: Y = 0. */
+ * 2^32 and NaN: a quarter of bf16's rounding.  hidden 0: Y, A and B are 0. */
 size_t mpg_gated_gemm_workspace_size(const mpg_gated_layer* layer);
-mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, void* G, int64_t ldg, void* U, int64_t ldu,
+mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, void* A, int64_t lda, void* B, int64_t ldb,
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* With dG = dY * U * act'(G) and dU = dY * act(G):
  *     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X.
- * dX may be NULL, and dWg and dWu together (frozen weights).  G, U: what
+ * dX may be NULL, and dWg and dWu together (frozen weights).  A, B: what
  * mpg_gated_gemm kept; both NULL: the projections are computed again (half as
- * many operations more, and the better gradient: they are not rounded between).
+ * many operations more).
  * dG and dU are rounded once to the 16-bit type, as operands of the products;
  * in fp16 they carry a power of two meanwhile, which brings the largest of dY
  * to [16, 32), so that small gradients keep their precision; products up * act'
  * above 2^11 then overflow.  tokens or inner 0: gradients of 0. */
 size_t mpg_gated_gemm_backward_workspace_size(const mpg_gated_layer* layer);
-mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY, int64_t lddy, const void* G, int64_t ldg,
-                                   const void* U, int64_t ldu, void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
+mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY, int64_t lddy, const void* A, int64_t lda,
+                                   const void* B, int64_t ldb, void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
                                    int64_t lddwu, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- cross entropy of a projection onto a vocabulary ----------------------

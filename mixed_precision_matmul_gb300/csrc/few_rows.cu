@@ -64,9 +64,11 @@ __device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, int thr
       if (t < p.rows && first + j < p.n) {
         auto store = [&](void* base, int64_t ld, uint32_t w) { static_cast<uint16_t*>(base)[(int64_t)t * ld + first + j] = (uint16_t)w; };
         store(p.y, p.ldy, pack16(act_value(gt, p.act) * up, 0.0f, bf16));
-        if (p.g) {
-          store(p.g, p.ldg, pack_kept(gt, 0.0f, bf16));
-          store(p.u, p.ldu, pack_kept(up, 0.0f, bf16));
+        if (p.ka) {
+          float a, d;
+          act_both(gt, p.act, a, d);
+          store(p.ka, p.lda, pack_kept(a, 0.0f, bf16));
+          store(p.kb, p.ldb, pack_kept(up * d, 0.0f, bf16));
         }
       }
     }

@@ -78,12 +78,13 @@ __device__ __forceinline__ float load16(const void* base, int64_t idx, bool bf16
   return bf16 ? __uint_as_float((uint32_t)w << 16) : __half2float(__ushort_as_half(w));
 }
 
-// Codes of the projections that a bf16 layer keeps: sign, 6 bits of exponent (bias
-// 31), 9 of fraction, subnormals down to 2^-39, infinity and NaN above 2^32.  Their
-// rounding is a quarter of bf16's, so that the gradients are off by the two roundings
-// that any 16-bit product has (of its operand and its result; in bf16 codes 0.0031
-// of the norm instead of 0.0024 at 8192 x 4096 x 11008), and their range is far
-// beyond fp16's, which an activation may leave.
+// Codes of what a bf16 layer keeps for its gradients, act(gate) and up act'(gate):
+// sign, 6 bits of exponent (bias 31), 9 of fraction, subnormals down to 2^-39,
+// infinity and NaN above 2^32.  Their rounding is a quarter of bf16's, so that the
+// gradients are off by the two roundings that any 16-bit product has, of its operand
+// and its result (with gate and up kept in bf16 0.0031 of the norm instead of 0.0024
+// at 8192 x 4096 x 11008), and their range is far beyond fp16's, which an activation
+// may leave.
 __device__ __forceinline__ uint32_t encode_kept(float x) {
   const uint32_t b = __float_as_uint(fabsf(x) * 0x1p-96f);        // the exponent's bias, subnormals too
   const uint32_t c = min((b + 0x1fffu + ((b >> 14) & 1u)) >> 14, 0x7e00u);

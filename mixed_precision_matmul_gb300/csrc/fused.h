@@ -15,7 +15,7 @@ namespace mpg {
 // What a product's accumulators become.
 enum class FusedEpi {
   kPlain,      // C = inverse * sum (+ what earlier products left), fp32 or 16 bits
-  kGated,      // Y = act(gate) * up; gate and up too, where they are kept
+  kGated,      // Y = act(gate) * up; act(gate) and up act'(gate) too, where they are kept
   kGatedGrad,  // gradients of gate and up from that of Y
   kStats,      // maximum and sum of exponentials of a row's part; the target's logit
   kProb,       // gradient of the logits
@@ -36,7 +36,7 @@ struct FusedProduct {
   int32_t kb_second;                // first block of k that comes from map_a[1] and map_b[1]
   int32_t mb_second;                // first row block of the second matrix: map_a[1], out[1]
   int32_t num_tiles, group_m;
-  void* out[3];                     // kPlain: C, second C; kGated: Y, gate, up (or null); kGatedGrad: dgate, dup; kProb: D
+  void* out[3];                     // kPlain: C, second C; kGated: Y, and act(gate), up act'(gate) (or null); kGatedGrad: dgate, dup; kProb: D
   int64_t ldo[3];
   int32_t out_vec[3];               // 8 elements of 16 bits (4 of fp32) are aligned
   int32_t out_dtype;
@@ -94,8 +94,8 @@ struct FewRowsParams {
   int32_t bf16, rows, n, k;
   int32_t strips;
   int32_t act;
-  void *y, *g, *u;
-  int64_t ldy, ldg, ldu;
+  void *y, *ka, *kb;                // Y; act(gate) and up act'(gate), or null
+  int64_t ldy, lda, ldb;
   const void* target;
   int32_t target_bytes;
   int64_t target_stride, ignore_index;
@@ -147,14 +147,14 @@ struct MaxParams {
 };
 cudaError_t launch_max(const MaxParams& p, cudaStream_t stream);
 
-// dgate and dup from dY and the kept gate and up.
+// dgate = dY b and dup = dY a from the kept a = act(gate) and b = up act'(gate).
 struct GatedGradParams {
-  const void *dy, *g, *u;
-  int64_t lddy, ldg, ldu;
+  const void *dy, *a, *b;
+  int64_t lddy, lda, ldb;
   uint16_t *dg, *du;
   int64_t ldd;
   int64_t rows, cols;
-  int32_t vec, act, bf16;
+  int32_t vec, bf16;
   const float* scale;
   int32_t scale_exp;
 };

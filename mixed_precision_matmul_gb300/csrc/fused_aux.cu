@@ -139,19 +139,16 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const __grid_constant__
     const Chunk c = chunk_at(i, per_line, small);
     const int64_t left = p.cols - c.col;
     const uint4 y4 = load_chunk(p.dy, c.row * p.lddy + c.col, left, vec);
-    const uint4 g4 = load_chunk(p.g, c.row * p.ldg + c.col, left, vec);
-    const uint4 u4 = load_chunk(p.u, c.row * p.ldu + c.col, left, vec);
-    const uint32_t y[4] = {y4.x, y4.y, y4.z, y4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+    const uint4 a4 = load_chunk(p.a, c.row * p.lda + c.col, left, vec);
+    const uint4 b4 = load_chunk(p.b, c.row * p.ldb + c.col, left, vec);
+    const uint32_t y[4] = {y4.x, y4.y, y4.z, y4.w}, a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
     uint32_t dg[4], du[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 yy = unpack16(y[j], bf16), gg = unpack_kept(g[j], bf16), uu = unpack_kept(u[j], bf16);
-      float a0, d0, a1, d1;
-      act_both(gg.x, p.act, a0, d0);
-      act_both(gg.y, p.act, a1, d1);
+      const float2 yy = unpack16(y[j], bf16), aa = unpack_kept(a[j], bf16), bb = unpack_kept(b[j], bf16);
       const float y0 = s * yy.x, y1 = s * yy.y;
-      dg[j] = pack16(y0 * uu.x * d0, y1 * uu.y * d1, bf16);
-      du[j] = pack16(y0 * a0, y1 * a1, bf16);
+      dg[j] = pack16(y0 * bb.x, y1 * bb.y, bf16);
+      du[j] = pack16(y0 * aa.x, y1 * aa.y, bf16);
     }
     // (the lines of dg and du are padded to whole chunks; what lies beyond the columns is not read)
     *reinterpret_cast<uint4*>(p.dg + c.row * p.ldd + c.col) = make_uint4(dg[0], dg[1], dg[2], dg[3]);

@@ -4,7 +4,8 @@
 // instructions of cta_group::2) or on single CTAs (128 x 128), for five
 // epilogues:
 //
-//   kGated      Y = act(X Wg^T) * (X Wu^T).  The B operand of a tile is half of
+//   kGated      Y = act(gate) * up, gate = X Wg^T, up = X Wu^T; for the backward
+//               pass act(gate) and up act'(gate) too.  The B operand of a tile is half of
 //               lines of Wg and half of the same lines of Wu, so gate and up
 //               are two halves of one accumulator, and a thread of the
 //               epilogue holds both of an element.  On a pair the instruction
@@ -596,169 +597,182 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
           p.stats[(int64_t)(x.nb * 2 + half) * pr.m + row] = make_float2(top, nan ? NAN : (sum[0] + sum[1]) + (sum[2] + sum[3]));
         continue;
       } else {
-      if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
-      tc_fence_after_sync();
-      ++g;
-      if (x.slot >= 0) {
-        // sums of a part of k, as they are: rows of the tile, whole lines a store
-        float* slot = p.slots + (int64_t)x.slot * (T::kTile * T::kTile) + (int64_t)((int)rank * T::BM + 32 * q) * T::kTile;
-        constexpr int kAll = T::kTile / 64;
+        if (!warp_wait(&acc_full[ab], (g / T::kAccBufs) & 1u, ctl)) break;
+        tc_fence_after_sync();
+        ++g;
+        if (x.slot >= 0) {
+          // sums of a part of k, as they are: rows of the tile, whole lines a store
+          float* slot = p.slots + (int64_t)x.slot * (T::kTile * T::kTile) + (int64_t)((int)rank * T::BM + 32 * q) * T::kTile;
+          constexpr int kAll = T::kTile / 64;
 #pragma unroll 1
-        for (int cc = half * kAll; cc < (half + 1) * kAll; ++cc) {
-          float v[32];
-          tmem_ld_32cols(tacc + cc * 32, v);
-          tmem_ld_wait();
-          if (cc == (half + 1) * kAll - 1) release();
-          if (row0 >= pr.m) continue;
-          stage_write_row(stg, lane, v);
-          __syncwarp();
+          for (int cc = half * kAll; cc < (half + 1) * kAll; ++cc) {
+            float v[32];
+            tmem_ld_32cols(tacc + cc * 32, v);
+            tmem_ld_wait();
+            if (cc == (half + 1) * kAll - 1) release();
+            if (row0 >= pr.m) continue;
+            stage_write_row(stg, lane, v);
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(slot + (i * 4 + (lane >> 3)) * T::kTile + cc * 32 + (lane & 7) * 4) =
-                stage_read_chunk(stg, lane, i);
-          __syncwarp();
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(slot + (i * 4 + (lane >> 3)) * T::kTile + cc * 32 + (lane & 7) * 4) =
+                  stage_read_chunk(stg, lane, i);
+            __syncwarp();
+          }
+          if (kAhead && more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
+          continue;
         }
-        if (kAhead && more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
-        continue;
-      }
 
-      if constexpr (T::kTwo) {
+        if constexpr (T::kTwo) {
 #pragma unroll 1
-        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
-          const int col0 = col_tile + cc * 32;
-          float gt[32], up[32];
-          tmem_ld_32cols(tacc + cc * 32, gt);
-          tmem_ld_32cols(tacc + T::kTile / 2 + cc * 32, up);
-          tmem_ld_wait();
-          if (cc == cc0 + kCc - 1) release();
-          uint32_t here[16];
-          if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
+          for (int cc = cc0; cc < cc0 + kCc; ++cc) {
+            const int col0 = col_tile + cc * 32;
+            float gt[32], up[32];
+            tmem_ld_32cols(tacc + cc * 32, gt);
+            tmem_ld_32cols(tacc + T::kTile / 2 + cc * 32, up);
+            tmem_ld_wait();
+            if (cc == cc0 + kCc - 1) release();
+            uint32_t here[16];
+            if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) here[j] = dyw[j];
-            // dY's elements of the next chunk, the next tile's first after the last
-            if (cc + 1 < cc0 + kCc) fetch_dy(row0, col0 + 32);
-            else if (more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
-          }
-          if (row0 >= pr.m || col0 >= pr.n) continue;
-          auto store = [&](int i, auto word) {
+              for (int j = 0; j < 16; ++j) here[j] = dyw[j];
+              // dY's elements of the next chunk, the next tile's first after the last
+              if (cc + 1 < cc0 + kCc) fetch_dy(row0, col0 + 32);
+              else if (more) fetch_dy(first_row(ahead), ahead.nb * T::kTileN + cc0 * 32);
+            }
+            if (row0 >= pr.m || col0 >= pr.n) continue;
+            auto store = [&](int i, const uint32_t (&w)[16]) {
+              store_block16(stg, lane, w, Block16{pr.out[i], pr.ldo[i], row0, pr.m, col0, pr.n, pr.out_vec[i] != 0});
+            };
             uint32_t w[16];
+            if constexpr (T::kEpi == FusedEpi::kGated) {
+              if (pr.out[1]) {
+                // act(gate) and up act'(gate), which the gradients are dY's multiples of
+                uint32_t ka[16], kb[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = word(2 * j);
-            store_block16(stg, lane, w, Block16{pr.out[i], pr.ldo[i], row0, pr.m, col0, pr.n, pr.out_vec[i] != 0});
-          };
-          if constexpr (T::kEpi == FusedEpi::kGated) {
-            if (pr.out[1]) {
-              store(1, [&](int j) { return pack_kept(gt[j], gt[j + 1], bf16); });
-              store(2, [&](int j) { return pack_kept(up[j], up[j + 1], bf16); });
-            }
-            store(0, [&](int j) {
-              return pack16(act_value(gt[j], T::kAct) * up[j], act_value(gt[j + 1], T::kAct) * up[j + 1], bf16);
-            });
-          } else {
+                for (int j = 0; j < 32; j += 2) {
+                  float a0, d0, a1, d1;
+                  act_both(gt[j], T::kAct, a0, d0);
+                  act_both(gt[j + 1], T::kAct, a1, d1);
+                  ka[j >> 1] = pack_kept(a0, a1, bf16);
+                  kb[j >> 1] = pack_kept(up[j] * d0, up[j + 1] * d1, bf16);
+                  w[j >> 1] = pack16(a0 * up[j], a1 * up[j + 1], bf16);
+                }
+                store(1, ka);
+                store(2, kb);
+              } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 y2 = unpack16(here[j >> 1], bf16);
-              const float dy = sc.mul * ((j & 1) ? y2.y : y2.x);
-              float a, d;
-              act_both(gt[j], T::kAct, a, d);
-              gt[j] = dy * up[j] * d;
-              up[j] = dy * a;
+                for (int j = 0; j < 32; j += 2)
+                  w[j >> 1] = pack16(act_value(gt[j], T::kAct) * up[j], act_value(gt[j + 1], T::kAct) * up[j + 1], bf16);
+              }
+              store(0, w);
+            } else {
+              uint32_t wu[16];
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 dy = unpack16(here[j >> 1], bf16);
+                const float y0 = sc.mul * dy.x, y1 = sc.mul * dy.y;
+                float a0, d0, a1, d1;
+                act_both(gt[j], T::kAct, a0, d0);
+                act_both(gt[j + 1], T::kAct, a1, d1);
+                w[j >> 1] = pack16(y0 * (up[j] * d0), y1 * (up[j + 1] * d1), bf16);
+                wu[j >> 1] = pack16(y0 * a0, y1 * a1, bf16);
+              }
+              store(0, w);
+              store(1, wu);
             }
-            store(0, [&](int j) { return pack16(gt[j], gt[j + 1], bf16); });
-            store(1, [&](int j) { return pack16(up[j], up[j + 1], bf16); });
           }
-        }
-      } else if constexpr (T::kEpi == FusedEpi::kProb) {
-        float v[32];
-        tmem_ld_32cols(tacc + cc0 * 32, v);
+        } else if constexpr (T::kEpi == FusedEpi::kProb) {
+          float v[32];
+          tmem_ld_32cols(tacc + cc0 * 32, v);
 #pragma unroll 1
-        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
-          tmem_ld_wait();
-          const int col0 = col_tile + cc * 32;
-          uint32_t w[16];
-          const bool in = row0 < pr.m && col0 < pr.n;
-          if (in) {
-            const int64_t at = target - (p.col0 + col0);
-            const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
-            const bool any = __any_sync(0xffffffffu, mine != 0u);
+          for (int cc = cc0; cc < cc0 + kCc; ++cc) {
+            tmem_ld_wait();
+            const int col0 = col_tile + cc * 32;
+            uint32_t w[16];
+            const bool in = row0 < pr.m && col0 < pr.n;
+            if (in) {
+              const int64_t at = target - (p.col0 + col0);
+              const uint32_t mine = at >= 0 && at < 32 ? 1u << at : 0u;
+              const bool any = __any_sync(0xffffffffu, mine != 0u);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(kLog2e, v[j], -lse2));
-            if (any) {
+              for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(kLog2e, v[j], -lse2));
+              if (any) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = mine & (1u << j) ? v[j] - 1.0f : v[j];
+                for (int j = 0; j < 32; ++j) v[j] = mine & (1u << j) ? v[j] - 1.0f : v[j];
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[j] = weight == 0.0f ? 0u : pack16(weight * v[2 * j], weight * v[2 * j + 1], bf16);
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[j] = weight == 0.0f ? 0u : pack16(weight * v[2 * j], weight * v[2 * j + 1], bf16);
-          }
-          if (cc + 1 < cc0 + kCc) tmem_ld_32cols(tacc + (cc + 1) * 32, v);
-          else release();
-          if (in) store_block16(stg, lane, w, Block16{pr.out[0], pr.ldo[0], row0, pr.m, col0, pr.n, pr.out_vec[0] != 0});
-        }
-      } else {
-        const int dt = pr.out_dtype;
-        void* out = pr.out[second ? 1 : 0];
-        const int64_t ldo = pr.ldo[second ? 1 : 0];
-        const bool vec = pr.out_vec[second ? 1 : 0] != 0;
-        // (the next chunk's accumulators are on their way while this one is stored)
-        float v[32];
-        tmem_ld_32cols(tacc + cc0 * 32, v);
-#pragma unroll 1
-        for (int cc = cc0; cc < cc0 + kCc; ++cc) {
-          tmem_ld_wait();
-          const int col0 = col_tile + cc * 32;
-          const bool in = row0 < pr.m && col0 < pr.n;
-          auto next_chunk = [&]() {
             if (cc + 1 < cc0 + kCc) tmem_ld_32cols(tacc + (cc + 1) * 32, v);
             else release();
-          };
-          if (!in) {
-            next_chunk();
-            continue;
+            if (in) store_block16(stg, lane, w, Block16{pr.out[0], pr.ldo[0], row0, pr.m, col0, pr.n, pr.out_vec[0] != 0});
           }
+        } else {
+          const int dt = pr.out_dtype;
+          void* out = pr.out[second ? 1 : 0];
+          const int64_t ldo = pr.ldo[second ? 1 : 0];
+          const bool vec = pr.out_vec[second ? 1 : 0] != 0;
+          // (the next chunk's accumulators are on their way while this one is stored)
+          float v[32];
+          tmem_ld_32cols(tacc + cc0 * 32, v);
+#pragma unroll 1
+          for (int cc = cc0; cc < cc0 + kCc; ++cc) {
+            tmem_ld_wait();
+            const int col0 = col_tile + cc * 32;
+            const bool in = row0 < pr.m && col0 < pr.n;
+            auto next_chunk = [&]() {
+              if (cc + 1 < cc0 + kCc) tmem_ld_32cols(tacc + (cc + 1) * 32, v);
+              else release();
+            };
+            if (!in) {
+              next_chunk();
+              continue;
+            }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= sc.inv;
-          if (dt != kOutF32 && !pr.add) {
-            uint32_t w[16];
+            for (int j = 0; j < 32; ++j) v[j] *= sc.inv;
+            if (dt != kOutF32 && !pr.add) {
+              uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], dt == kOutBF16);
+              for (int j = 0; j < 16; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], dt == kOutBF16);
+              next_chunk();
+              store_block16(stg, lane, w, Block16{out, ldo, row0, pr.m, col0, pr.n, vec});
+              continue;
+            }
+            stage_write_row(stg, lane, v);
+            __syncwarp();
             next_chunk();
-            store_block16(stg, lane, w, Block16{out, ldo, row0, pr.m, col0, pr.n, vec});
-            continue;
-          }
-          stage_write_row(stg, lane, v);
-          __syncwarp();
-          next_chunk();
-          // (add has lines of whole 16-byte chunks)
-          if (vec && col0 + 32 <= pr.n) {
+            // (add has lines of whole 16-byte chunks)
+            if (vec && col0 + 32 <= pr.n) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = row0 + i * 4 + (lane >> 3), c = col0 + (lane & 7) * 4;
-              float4 o = stage_read_chunk(stg, lane, i);
-              if (r < pr.m) {
-                if (pr.add) {
-                  const float4 y = out_load4(pr.add, (int64_t)r * pr.ldadd + c, kOutF32);
-                  o.x += y.x;
-                  o.y += y.y;
-                  o.z += y.z;
-                  o.w += y.w;
+              for (int i = 0; i < 8; ++i) {
+                const int r = row0 + i * 4 + (lane >> 3), c = col0 + (lane & 7) * 4;
+                float4 o = stage_read_chunk(stg, lane, i);
+                if (r < pr.m) {
+                  if (pr.add) {
+                    const float4 y = out_load4(pr.add, (int64_t)r * pr.ldadd + c, kOutF32);
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                  }
+                  out_store4(out, (int64_t)r * ldo + c, o, dt);
                 }
-                out_store4(out, (int64_t)r * ldo + c, o, dt);
               }
-            }
-          } else if (col0 + lane < pr.n) {
+            } else if (col0 + lane < pr.n) {
 #pragma unroll 4
-            for (int r = 0; r < 32; ++r) {
-              float o = stage_read_elem(stg, lane, r);
-              if (row0 + r < pr.m) {
-                if (pr.add) o += out_load(pr.add, (int64_t)(row0 + r) * pr.ldadd + col0 + lane, kOutF32);
-                out_store(out, (int64_t)(row0 + r) * ldo + col0 + lane, o, dt);
+              for (int r = 0; r < 32; ++r) {
+                float o = stage_read_elem(stg, lane, r);
+                if (row0 + r < pr.m) {
+                  if (pr.add) o += out_load(pr.add, (int64_t)(row0 + r) * pr.ldadd + col0 + lane, kOutF32);
+                  out_store(out, (int64_t)(row0 + r) * ldo + col0 + lane, o, dt);
+                }
               }
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
-      }
       }
     }
   }
@@ -881,8 +895,15 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
     auto at = [&](int k) { return (int64_t)row * pr.ldo[k] + col; };
     if constexpr (T::kEpi == FusedEpi::kGated) {
       if (pr.out[1]) {
-        store_kept(pr.out[1], at(1), gt, left, pr.out_vec[1], p.bf16 != 0);
-        store_kept(pr.out[2], at(2), up, left, pr.out_vec[2], p.bf16 != 0);
+        float ka[4], kb[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float d;
+          act_both(gt[j], T::kAct, ka[j], d);
+          kb[j] = up[j] * d;
+        }
+        store_kept(pr.out[1], at(1), ka, left, pr.out_vec[1], p.bf16 != 0);
+        store_kept(pr.out[2], at(2), kb, left, pr.out_vec[2], p.bf16 != 0);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) gt[j] = act_value(gt[j], T::kAct) * up[j];
@@ -894,7 +915,7 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
         float a, d;
         act_both(gt[j], T::kAct, a, d);
         const float y = sc.mul * dy[j];
-        gt[j] = y * up[j] * d;
+        gt[j] = y * (up[j] * d);
         up[j] = y * a;
       }
       store_four(pr.out[1], at(1), up, left, pr.out_vec[1], type);

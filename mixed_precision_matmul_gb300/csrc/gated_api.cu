@@ -135,23 +135,23 @@ size_t mpg_gated_gemm_workspace_size(const mpg_gated_layer* layer) {
   return layout(layer, false).bytes;
 }
 
-mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, void* G, int64_t ldg, void* U, int64_t ldu,
+mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, void* A, int64_t lda, void* B, int64_t ldb,
                           void* workspace, size_t workspace_bytes, void* stream) {
   t_err.clear();
   mpg_status s = check_layer(layer);
   if (s != MPG_OK) return s;
   const mpg_gated_layer& l = *layer;
-  if ((G == nullptr) != (U == nullptr)) return fail(MPG_ERR_INVALID_ARG, "G and U are kept together");
+  if ((A == nullptr) != (B == nullptr)) return fail(MPG_ERR_INVALID_ARG, "A and B are kept together");
   if (l.tokens == 0 || l.inner == 0) return MPG_OK;
   if ((s = check_matrix(Y, ldy, l.tokens, l.inner, 2, "Y")) != MPG_OK) return s;
-  if (G && (s = check_matrix(G, ldg, l.tokens, l.inner, 2, "G")) != MPG_OK) return s;
-  if (U && (s = check_matrix(U, ldu, l.tokens, l.inner, 2, "U")) != MPG_OK) return s;
+  if (A && (s = check_matrix(A, lda, l.tokens, l.inner, 2, "A")) != MPG_OK) return s;
+  if (B && (s = check_matrix(B, ldb, l.tokens, l.inner, 2, "B")) != MPG_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (l.hidden == 0) {
     // sums of nothing: act(0) * 0
     DeviceInfo* dev = nullptr;
     if ((s = get_device(&dev)) != MPG_OK) return s;
-    const struct { void* p; int64_t ld; } out[3] = {{Y, ldy}, {G, ldg}, {U, ldu}};
+    const struct { void* p; int64_t ld; } out[3] = {{Y, ldy}, {A, lda}, {B, ldb}};
     for (const auto& o : out) {
       if (!o.p) continue;
       const cudaError_t e = cudaMemset2DAsync(o.p, (size_t)(l.tokens > 1 ? o.ld : l.inner) * 2, 0, (size_t)l.inner * 2,
@@ -182,10 +182,10 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
     p.act = (int32_t)l.act;
     p.y = Y;
     p.ldy = ldy;
-    p.g = G;
-    p.ldg = ldg;
-    p.u = U;
-    p.ldu = ldu;
+    p.ka = A;
+    p.lda = lda;
+    p.kb = B;
+    p.ldb = ldb;
     return launch_few_rows(dev, p, true, st);
   }
 
@@ -196,8 +196,8 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
   if ((s = fused_map(&p.prod[0].map_b[1], o.wu.ptr, o.wu.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
   p.bf16 = l.dtype == MPG_BF16;
   p.act = (int32_t)l.act;
-  void* const out[3] = {Y, G, U};
-  const int64_t ld[3] = {ldy, ldg, ldu};
+  void* const out[3] = {Y, A, B};
+  const int64_t ld[3] = {ldy, lda, ldb};
   for (int i = 0; i < 3; ++i) {
     p.prod[0].out[i] = out[i];
     p.prod[0].ldo[i] = ld[i];
@@ -213,14 +213,14 @@ size_t mpg_gated_gemm_backward_workspace_size(const mpg_gated_layer* layer) {
   return layout(layer, true).bytes;
 }
 
-mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY, int64_t lddy, const void* G, int64_t ldg,
-                                   const void* U, int64_t ldu, void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
+mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY, int64_t lddy, const void* A, int64_t lda,
+                                   const void* B, int64_t ldb, void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
                                    int64_t lddwu, void* workspace, size_t workspace_bytes, void* stream) {
   t_err.clear();
   mpg_status s = check_layer(layer);
   if (s != MPG_OK) return s;
   const mpg_gated_layer& l = *layer;
-  if ((G == nullptr) != (U == nullptr)) return fail(MPG_ERR_INVALID_ARG, "G and U are kept together");
+  if ((A == nullptr) != (B == nullptr)) return fail(MPG_ERR_INVALID_ARG, "A and B are kept together");
   if ((dWg == nullptr) != (dWu == nullptr)) return fail(MPG_ERR_INVALID_ARG, "dWg and dWu are made together");
   if (l.hidden == 0) return MPG_OK;                 // (gradients without elements)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -242,8 +242,8 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     return MPG_OK;
   }
   if ((s = check_matrix(dY, lddy, l.tokens, l.inner, 2, "dY")) != MPG_OK) return s;
-  if (G && (s = check_matrix(G, ldg, l.tokens, l.inner, 2, "G")) != MPG_OK) return s;
-  if (U && (s = check_matrix(U, ldu, l.tokens, l.inner, 2, "U")) != MPG_OK) return s;
+  if (A && (s = check_matrix(A, lda, l.tokens, l.inner, 2, "A")) != MPG_OK) return s;
+  if (B && (s = check_matrix(B, ldb, l.tokens, l.inner, 2, "B")) != MPG_OK) return s;
   Layout o = layout(layer, true);
   if ((s = check_workspace(o, workspace, workspace_bytes)) != MPG_OK) return s;
   if ((s = get_device(&dev)) != MPG_OK) return s;
@@ -272,22 +272,21 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     const cudaError_t e = launch_max(p, st);
     if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "maximum launch: %s", cudaGetErrorString(e));
   }
-  if (G) {
+  if (A) {
     GatedGradParams p;
     std::memset(&p, 0, sizeof(p));
     p.dy = dY;
     p.lddy = lddy;
-    p.g = G;
-    p.ldg = ldg;
-    p.u = U;
-    p.ldu = ldu;
+    p.a = A;
+    p.lda = lda;
+    p.b = B;
+    p.ldb = ldb;
     p.dg = dg;
     p.du = du;
     p.ldd = o.ldd;
     p.rows = l.tokens;
     p.cols = l.inner;
-    p.vec = fused_lines_ok(dY, lddy) && fused_lines_ok(G, ldg) && fused_lines_ok(U, ldu);
-    p.act = (int32_t)l.act;
+    p.vec = fused_lines_ok(dY, lddy) && fused_lines_ok(A, lda) && fused_lines_ok(B, ldb);
     p.bf16 = l.dtype == MPG_BF16;
     p.scale = half ? partial : nullptr;
     p.scale_exp = kExp;

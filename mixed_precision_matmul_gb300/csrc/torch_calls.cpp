@@ -226,10 +226,10 @@ bool layer_of(PyObject* px, PyObject* pg, PyObject* pu, long act, at::Tensor* x,
   return true;
 }
 
-// Of the projections that a layer keeps: fp16, or codes in a bf16 layer.
+// Of what a layer keeps for its gradients: fp16, or codes in a bf16 layer.
 at::ScalarType kept_type(const at::Tensor& x) { return x.scalar_type() == at::kHalf ? at::kHalf : at::kShort; }
 
-// (x, wg, wu, activation, keep) -> y or (y, g, u)
+// (x, wg, wu, activation, keep) -> y or (y, a, b)
 PyObject* gated_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 5 || !g_gated) return PyErr_Format(PyExc_TypeError, "five arguments are expected");
   try {
@@ -253,28 +253,28 @@ PyObject* gated_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
-// (dy, x, wg, wu, activation, g, u, need_dx, need_dw) -> (dx, dwg, dwu)
+// (dy, x, wg, wu, activation, a, b, need_dx, need_dw) -> (dx, dwg, dwu)
 PyObject* gated_gemm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 9 || !g_gated_back) return PyErr_Format(PyExc_TypeError, "nine arguments are expected");
   try {
     const long act = PyLong_AsLong(args[4]);
     const int need_dx = PyObject_IsTrue(args[7]), need_dw = PyObject_IsTrue(args[8]);
     if (PyErr_Occurred()) return nullptr;
-    at::Tensor dy, x, wg, wu, g, u, out[3];
+    at::Tensor dy, x, wg, wu, a, b, out[3];
     c10::DeviceIndex dev;
     mpg_gated_layer l;
-    int64_t lddy = 0, ldg = 0, ldu = 0;
+    int64_t lddy = 0, lda = 0, ldb = 0;
     if (!layer_of(args[1], args[2], args[3], act, &x, &wg, &wu, &dev, &l)) Py_RETURN_NONE;
     if (!matrix16(args[0], dev, x.scalar_type(), l.tokens, l.inner, &dy, &lddy)) Py_RETURN_NONE;
     if (args[5] != Py_None || args[6] != Py_None)
-      if (!matrix16(args[5], dev, kept_type(x), l.tokens, l.inner, &g, &ldg) ||
-          !matrix16(args[6], dev, kept_type(x), l.tokens, l.inner, &u, &ldu))
+      if (!matrix16(args[5], dev, kept_type(x), l.tokens, l.inner, &a, &lda) ||
+          !matrix16(args[6], dev, kept_type(x), l.tokens, l.inner, &b, &ldb))
         Py_RETURN_NONE;
     if (need_dx) out[0] = at::empty({l.tokens, l.hidden}, x.options());
     for (int i = 1; i < 3 && need_dw; ++i) out[i] = at::empty({l.inner, l.hidden}, x.options());
     const size_t bytes = g_gated_back_workspace(&l);
     const at::Tensor ws = bytes ? scratch(bytes, x) : at::Tensor();
-    const mpg_status st = g_gated_back(&l, address(dy), lddy, address(g), ldg, address(u), ldu, address(out[0]), l.hidden,
+    const mpg_status st = g_gated_back(&l, address(dy), lddy, address(a), lda, address(b), ldb, address(out[0]), l.hidden,
                                        address(out[1]), l.hidden, address(out[2]), l.hidden, address(ws), bytes,
                                        c10::cuda::getCurrentCUDAStream(dev).stream());
     return st == MPG_OK ? results(out, 3) : PyLong_FromLong(st);

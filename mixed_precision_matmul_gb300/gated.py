@@ -37,21 +37,21 @@ def _declare(L):
     L.mpg_gated_gemm_backward.argtypes, L.mpg_gated_gemm_backward.restype = [p] + [vp, i64] * 6 + [vp, sz, vp], i32
 
 
-def gated_gemm_raw(layer, Y, ldy, G=0, ldg=0, U=0, ldu=0, workspace=0, workspace_bytes=0, stream=0,
+def gated_gemm_raw(layer, Y, ldy, A=0, lda=0, B=0, ldb=0, workspace=0, workspace_bytes=0, stream=0,
                    check: bool = True) -> int:
     """mpg_gated_gemm with a :class:`GatedLayer` and device addresses."""
-    st = _m.lib().mpg_gated_gemm(ctypes.byref(layer) if layer is not None else None, Y or None, ldy, G or None, ldg,
-                                 U or None, ldu, workspace or None, workspace_bytes, stream or None)
+    st = _m.lib().mpg_gated_gemm(ctypes.byref(layer) if layer is not None else None, Y or None, ldy, A or None, lda,
+                                 B or None, ldb, workspace or None, workspace_bytes, stream or None)
     if check and st:
         _m._check(st)
     return st
 
 
-def gated_gemm_backward_raw(layer, dY, lddy, G, ldg, U, ldu, dX, lddx, dWg, lddwg, dWu, lddwu, workspace=0,
+def gated_gemm_backward_raw(layer, dY, lddy, A, lda, B, ldb, dX, lddx, dWg, lddwg, dWu, lddwu, workspace=0,
                             workspace_bytes=0, stream=0, check: bool = True) -> int:
     """mpg_gated_gemm_backward with a :class:`GatedLayer` and device addresses."""
-    st = _m.lib().mpg_gated_gemm_backward(ctypes.byref(layer) if layer is not None else None, dY or None, lddy, G or None,
-                                          ldg, U or None, ldu, dX or None, lddx, dWg or None, lddwg, dWu or None, lddwu,
+    st = _m.lib().mpg_gated_gemm_backward(ctypes.byref(layer) if layer is not None else None, dY or None, lddy, A or None,
+                                          lda, B or None, ldb, dX or None, lddx, dWg or None, lddwg, dWu or None, lddwu,
                                           workspace or None, workspace_bytes, stream or None)
     if check and st:
         _m._check(st)
@@ -87,7 +87,7 @@ def _act(act):
 
 
 def _kept_dtype(dtype):
-    """Of the projections that a layer keeps: fp16, or the codes of mpg_gated_gemm in a bf16 layer."""
+    """Of what a layer keeps for its gradients: fp16, or the codes of mpg_gated_gemm in a bf16 layer."""
     torch = _types()[0]
     return torch.int16 if dtype == torch.bfloat16 else dtype
 
@@ -115,10 +115,11 @@ def gated_gemm(x, wg, wu, act: str = "silu", keep: bool = False, workspace=None,
     """``act(x @ wg.T) * (x @ wu.T)`` for 16-bit x (tokens, hidden) and wg and wu
     (inner, hidden), in one kernel.
 
-    ``act`` is "silu", "gelu" or "gelu_tanh".  With ``keep`` returns ``(y, g, u)``,
-    where g and u are the projections for :func:`gated_gemm_backward`: fp16 in an
-    fp16 layer, and in a bf16 layer int16 codes of a 16-bit type with more precision
-    than bf16 (mpgemm.h says which).
+    ``act`` is "silu", "gelu" or "gelu_tanh".  With ``keep`` returns ``(y, a, b)``,
+    where a and b are what :func:`gated_gemm_backward` makes gradients from, act(g)
+    and u act'(g) of the projections g and u: fp16 in an fp16 layer, and in a bf16
+    layer int16 codes of a 16-bit type with more precision than bf16 (mpgemm.h says
+    which).
     """
     torch = _types()[0]
     if stream is not None:
@@ -148,31 +149,31 @@ def gated_gemm_backward(dy, x, wg, wu, act: str = "silu", kept=None, need_dx: bo
                         workspace=None, stream=None):
     """Gradients ``(dx, dwg, dwu)`` of :func:`gated_gemm` for dy (tokens, inner).
 
-    ``kept`` is the ``(g, u)`` of ``gated_gemm(..., keep=True)``; without it the
+    ``kept`` is the ``(a, b)`` of ``gated_gemm(..., keep=True)``; without it the
     projections are computed again.  What is not needed is None.
     """
     torch = _types()[0]
-    g, u = kept if kept is not None else (None, None)
+    a, b = kept if kept is not None else (None, None)
     if stream is not None:
-        return _on_stream(stream, [dy, x, wg, wu, g, u, workspace],
+        return _on_stream(stream, [dy, x, wg, wu, a, b, workspace],
                           lambda: gated_gemm_backward(dy, x, wg, wu, act, kept, need_dx, need_dw, workspace))
     code = _act(act)
     if workspace is None:
         calls = _calls()
-        r = calls.gated_gemm_backward(dy, x, wg, wu, code, g, u, need_dx, need_dw) if calls else None
+        r = calls.gated_gemm_backward(dy, x, wg, wu, code, a, b, need_dx, need_dw) if calls else None
         if r is not None:
             if r.__class__ is int:
                 _m._check(r)
             return r
-    index = _device_index(dy, x, wg, wu, g, u, workspace)
+    index = _device_index(dy, x, wg, wu, a, b, workspace)
     if index != torch.cuda.current_device():
         return _on_device(index, lambda: gated_gemm_backward(dy, x, wg, wu, act, kept, need_dx, need_dw, workspace))
     layer = _layer(x, wg, wu, code)
     shape = (layer.tokens, layer.inner)
     args = [dy.data_ptr(), _matrix(dy, "dy", x.dtype, shape)]
-    for t, name in ((g, "g"), (u, "u")):
+    for t, name in ((a, "a"), (b, "b")):
         if (t is None) != (kept is None):
-            raise ValueError("g and u are kept together")
+            raise ValueError("a and b are kept together")
         args += [0, 0] if t is None else [t.data_ptr(), _matrix(t, name, _kept_dtype(x.dtype), shape)]
     # (a weight whose lines have gaps gets a gradient without them)
     outs = [torch.empty(t.shape, dtype=x.dtype, device=x.device) if need else None

@@ -48,18 +48,20 @@ ACT = 2.0 ** -17
 
 
 def gated(x, wg, wu, name):
-    """(y, g, u) in 64 bits and bounds of each but for the final rounding."""
+    """y and what is kept for the gradients, act(g) and u act'(g), in 64 bits, and bounds of each but for the final rounding."""
     x, wg, wu = x.to(F64), wg.to(F64), wu.to(F64)
     g, u = x @ wg.t(), x @ wu.t()
     e = sum_error(x.shape[1])
     eg, eu = e * (x.abs() @ wg.abs().t()), e * (x.abs() @ wu.abs().t())
-    a, _ = act(g, name)
+    a, d = act(g, name)
+    ea = SLOPE * eg + ACT * (a.abs() + 2.0 ** -10)
+    eb = SLOPE * (u.abs() + eu) * eg + SLOPE * eu + ACT * u.abs()
     ey = (SLOPE * u.abs() + SLOPE * eu) * eg + a.abs() * eu + ACT * (a.abs() + 2.0 ** -10) * u.abs()
-    return (a * u, g, u), (ey, eg, eu)
+    return (a * u, a, u * d), (ey, ea, eb)
 
 
 def kept_values(t):
-    """The values of kept projections in 64 bits: fp16, or codes with 6 bits of exponent and 9 of fraction."""
+    """The values of what is kept in 64 bits: fp16, or codes with 6 bits of exponent and 9 of fraction."""
     if t.dtype != torch.int16:
         return t.to(F64)
     c = t.to(torch.int32) & 0x7fff
@@ -70,7 +72,7 @@ def kept_values(t):
 
 
 def check_kept(t, ref, bound):
-    """Kept projections are ref rounded once: half a step is 2^-11 of the value in fp16, 2^-10 in codes."""
+    """What is kept is ref rounded once: half a step is 2^-11 of the value in fp16, 2^-10 in codes."""
     r, least = (2.0 ** -10, 2.0 ** -40) if t.dtype == torch.int16 else (2.0 ** -11, 2.0 ** -25)
     off = (kept_values(t) - ref).abs()
     assert bool((off <= bound * (1 + r) + r * ref.abs() + least).all())
@@ -84,17 +86,19 @@ def gated_gradients(dy, x, wg, wu, name, kept=None):
         e = sum_error(x.shape[1])
         g, u = x @ wg.t(), x @ wu.t()
         eg, eu = e * (x.abs() @ wg.abs().t()), e * (x.abs() @ wu.abs().t())
+        a, d = act(g, name)
+        b = u * d
+        ea, eb = SLOPE * eg + ACT * (a.abs() + 2.0 ** -10), SLOPE * (u.abs() + eu) * eg + SLOPE * eu + ACT * u.abs()
     else:
-        g, u = (kept_values(t) for t in kept)
-        eg = eu = torch.zeros_like(g)
-    a, d = act(g, name)
-    dg, du = dy * u * d, dy * a
+        a, b = (kept_values(t) for t in kept)
+        ea, eb = ACT * a.abs(), ACT * b.abs()
+    dg, du = dy * b, dy * a
     # one rounding of dg and du each, as operands; in fp16 with a scale that leaves
     # subnormals 2^-28 of the largest dy, whose halves are 2^-29
     r = half_step(dtype)
     floor = float(dy.abs().max()) * 2.0 ** -29 if dtype == torch.float16 and dy.numel() else 0.0
-    edg = dy.abs() * (SLOPE * (u.abs() + eu) * eg + SLOPE * eu + ACT * u.abs()) + r * dg.abs() + floor
-    edu = dy.abs() * (SLOPE * eg + ACT * (a.abs() + 2.0 ** -10)) + r * du.abs() + floor
+    edg = dy.abs() * eb + r * dg.abs() + floor
+    edu = dy.abs() * ea + r * du.abs() + floor
     i, t = wg.shape[0], x.shape[0]
     dx = dg @ wg + du @ wu
     ex = edg @ wg.abs() + edu @ wu.abs() + sum_error(2 * i) * (dg.abs() @ wg.abs() + du.abs() @ wu.abs())

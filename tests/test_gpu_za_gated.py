@@ -40,27 +40,27 @@ SHAPES = [
 def test_product(t, h, i, act):
     for dtype, pad, shift in (("bf16", 0, 0), ("fp16", 8, 8), ("bf16", 3, 1)):
         x, wg, wu, _ = operands(t, h, i, dtype, 1, pad, shift)
-        (y, g, u), (ey, eg, eu) = plain.gated(x, wg, wu, act)
+        (y, a, b), (ey, ea, eb) = plain.gated(x, wg, wu, act)
         out = mpg.gated_gemm(x, wg, wu, act=act)
         ok()
         plain.check(out, y, ey)
         out, kg, ku = mpg.gated_gemm(x, wg, wu, act=act, keep=True)
         ok()
         plain.check(out, y, ey)
-        plain.check_kept(kg, g, eg)
-        plain.check_kept(ku, u, eu)
+        plain.check_kept(kg, a, ea)
+        plain.check_kept(ku, b, eb)
 
 
 @pytest.mark.parametrize("t,h,i,dtype", [(2048, 512, 4096, "bf16"), (1531, 520, 2741, "fp16"), (4100, 264, 1030, "bf16"),
                                          (200, 4000, 300, "bf16"), (40, 3999, 70, "fp16"), (600, 4096, 515, "bf16")])
 def test_product_on_pairs(t, h, i, dtype):
     x, wg, wu, _ = operands(t, h, i, dtype, 2)
-    (y, g, u), (ey, eg, eu) = plain.gated(x, wg, wu, "silu")
+    (y, a, b), (ey, ea, eb) = plain.gated(x, wg, wu, "silu")
     out, kg, ku = mpg.gated_gemm(x, wg, wu, keep=True)
     ok()
     plain.check(out, y, ey)
-    plain.check_kept(kg, g, eg)
-    plain.check_kept(ku, u, eu)
+    plain.check_kept(kg, a, ea)
+    plain.check_kept(ku, b, eb)
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
@@ -140,24 +140,25 @@ def test_small_and_large_gradients_in_fp16():
 
 
 @pytest.mark.parametrize("t", [3, 40])
-def test_kept_projections_over_their_range(t):
-    """One input channel and weights of every size: projections from 2^-60 to 2^120, infinities and NaN."""
+def test_what_is_kept_over_its_range(t):
+    """Gates and ups from 2^-45 to 2^44 (and 2^120, and NaN): one input channel and weights of every size."""
     x = torch.zeros(t, 8, dtype=torch.bfloat16, device="cuda")
     x[:, 0] = 1.0
     x[1, 0] = -1.0
     w = torch.zeros(256, 8, dtype=torch.bfloat16, device="cuda")
     w[:, 0] = (1.0 + torch.rand(256, generator=torch.Generator().manual_seed(3))).cuda() * torch.exp2(torch.arange(256, device="cuda") % 90 - 45.0)
-    w[7, 0], w[8, 0], w[9, 0] = float("inf"), float("nan"), 2.0 ** 120
-    _, g, u = mpg.gated_gemm(x, w, w, keep=True)
+    w[8, 0], w[9, 0] = float("nan"), 2.0 ** 120
+    _, ka, kb = mpg.gated_gemm(x, w, w, keep=True)
     ok()
-    exact = (x[:, :1].double() @ w[:, :1].double().t())
-    for k in (g, u):
+    g = x[:, :1].double() @ w[:, :1].double().t()
+    a, d = plain.act(g, "silu")
+    for k, exact in ((ka, a), (kb, g * d)):
         v = plain.kept_values(k)
         inside = (exact.abs() < 2.0 ** 32) & ~exact.isnan()
         off = (v - exact).abs()
-        assert bool((off[inside] <= (2.0 ** -10 * exact.abs() + 2.0 ** -40)[inside]).all())
-        assert torch.equal(v[:, 7].isinf(), torch.ones(t, dtype=torch.bool, device="cuda")) and v[:, 8].isnan().all()
-        assert v[:, 9].isinf().all() and bool((torch.sign(v[1:2, 7]) == -1).all())
+        # (far below 0 act and act' vanish; what is left of them is off by the exponential's argument)
+        assert bool((off[inside] <= ((2.0 ** -10 + plain.ACT) * exact.abs() + 2.0 ** -40)[inside]).all())
+        assert v[:, 8].isnan().all() and v[0, 9].isinf() and bool((v[0][exact[0].abs() >= 2.0 ** 33].isinf()).all())
 
 
 @pytest.mark.parametrize("t", [5, 100])

@@ -53,6 +53,16 @@ def test_sizes_and_types(dtype):
     check([grads[0], grads[2]], 0.0)
 
 
+@pytest.mark.parametrize("most", [262144 - 2048, 262144, 262145, 700001])
+def test_around_what_one_launch_holds(most):
+    g = torch.Generator("cuda").manual_seed(8)
+    for dtype in (F32, BF16):
+        grads = [torch.randn(n, device="cuda", generator=g).to(dtype) for n in (most - 5000, 2999, 2001)]
+        check(grads, 1.0, [torch.empty_like(t, dtype=F32) for t in grads])
+        check(grads, 1e9)
+        check(grads, 0.25)
+
+
 def test_mixed_types_shapes_and_alignment():
     g = torch.Generator("cuda").manual_seed(2)
     flat = torch.randn(300000, device="cuda", generator=g)
