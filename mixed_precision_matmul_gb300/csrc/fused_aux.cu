@@ -1,7 +1,7 @@
 // Memory-bound kernels around the products with fused epilogues (sm_103a):
 // copies of operands whose lines TMA cannot describe, the largest absolute
 // value behind the scale of fp16 gradients, the gradients of gate and up from
-// kept projections, and the joining of a row's parts into its loss.
+// what the forward pass kept, and the joining of a row's parts into its loss.
 #include <climits>
 
 #include "fused.cuh"

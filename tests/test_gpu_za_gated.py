@@ -224,6 +224,42 @@ def test_nothing_is_written_beyond_the_results(t):
         assert torch.equal(b[:r.shape[0], :r.shape[1]], r)
 
 
+@pytest.mark.parametrize("t", [1, 5, 16, 30, 60, 64, 65])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_lines_of_odd_length_on_aligned_places(t, dtype):
+    """100 columns (and 77 inner values) in lines of 104 and 80 elements, all on 16 bytes: chunks cut by the
+    matrix's edge, the last line's end at the end of its memory, and gaps that stay as they were."""
+    import ctypes
+    h, i, ldh, ldi = 100, 77, 104, 80
+    code = mpg.BF16 if dtype == "bf16" else mpg.F16
+
+    def lined(m, ld):
+        flat = torch.full(((m.shape[0] - 1) * ld + m.shape[1],), float("nan"), dtype=m.dtype, device="cuda")
+        v = flat.as_strided(m.shape, (ld, 1))
+        v.copy_(m)
+        return v
+    x, wg, wu, dy = operands(t, h, i, dtype, 12)
+    x, wg, wu, dy = lined(x, ldh), lined(wg, ldh), lined(wu, ldh), lined(dy, ldi)
+    lay = mpg.GatedLayer(t, h, i, code, 0, x.data_ptr(), wg.data_ptr(), wu.data_ptr(), ldh, ldh, ldh)
+    mark = 12345.0 if dtype == "fp16" else 12352.0
+    outs = [torch.full((r + 1, ldh), mark, dtype=x.dtype, device="cuda") for r in (t, i, i)]
+    y = torch.full((t + 1, ldi), mark, dtype=x.dtype, device="cuda")
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    need = int(mpg.lib().mpg_gated_gemm_backward_workspace_size(ctypes.byref(lay)))
+    assert need <= ws.numel()
+    mpg.gated_gemm_raw(lay, y.data_ptr(), ldi, 0, 0, 0, 0, ws.data_ptr(), ws.numel())
+    mpg.gated_gemm_backward_raw(lay, dy.data_ptr(), ldi, 0, 0, 0, 0, *(v for b in outs for v in (b.data_ptr(), ldh)),
+                                ws.data_ptr(), ws.numel())
+    ok()
+    (ref, _, _), (bound, _, _) = plain.gated(x, wg, wu, "silu")
+    plain.check(y[:t, :i], ref, bound)
+    refs, bounds = plain.gated_gradients(dy, x, wg, wu, "silu")
+    for o, r, b in zip(outs, refs, bounds):
+        plain.check(o[:-1, :h], r, b)
+        assert (o[-1] == mark).all() and (o[:, h:] == mark).all()
+    assert (y[-1] == mark).all() and (y[:, i:] == mark).all()
+
+
 def test_a_given_workspace_streams_threads_and_graphs():
     x, wg, wu, dy = operands(200, 136, 264, "fp16", 10)
     y, g, u = mpg.gated_gemm(x, wg, wu, keep=True)

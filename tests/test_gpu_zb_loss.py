@@ -242,6 +242,37 @@ def test_nothing_is_written_beyond_the_results(t):
     assert torch.equal(dx[:t, :h], ref[0]) and torch.equal(dw[:v, :h], ref[1])
 
 
+@pytest.mark.parametrize("t", [1, 5, 16, 30, 60, 64, 65])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_lines_of_odd_length_on_aligned_places(t, dtype):
+    """100 columns in lines of 104 elements, all on 16 bytes, the last line's end at the end of its memory."""
+    h, v, ld = 100, 203, 104
+
+    def lined(m):
+        flat = torch.full(((m.shape[0] - 1) * ld + h,), float("nan"), dtype=m.dtype, device="cuda")
+        r = flat.as_strided(m.shape, (ld, 1))
+        r.copy_(m)
+        return r
+    x, w, target = operands(t, h, v, dtype, 14, ignored=0.2)
+    x, w = lined(x), lined(w)
+    value, lse = mpg.linear_cross_entropy(x, w, target)
+    (rv, rl), (ev, el) = plain.loss(x, w, target)
+    plain.check(value, rv, ev)
+    plain.check(lse, rl, el)
+    d = mpg.VocabLoss(t, h, v, mpg.BF16 if dtype == "bf16" else mpg.F16, x.data_ptr(), w.data_ptr(), ld, ld, target.data_ptr(), 8, 1, -100)
+    dloss = torch.rand(t, generator=torch.Generator().manual_seed(2)).cuda() + 0.1
+    mark = 12345.0 if dtype == "fp16" else 12352.0
+    outs = [torch.full((r + 1, ld), mark, dtype=x.dtype, device="cuda") for r in (t, v)]
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    mpg.linear_cross_entropy_backward_raw(d, lse.data_ptr(), dloss.data_ptr(), 1, outs[0].data_ptr(), ld, outs[1].data_ptr(), ld,
+                                          ws.data_ptr(), ws.numel())
+    ok()
+    refs, bounds = plain.loss_gradients(x, w, target, lse, dloss)
+    for o, r, b in zip(outs, refs, bounds):
+        plain.check(o[:-1, :h], r, b)
+        assert (o[-1] == mark).all() and (o[:, h:] == mark).all()
+
+
 def test_graph_stream_and_python_form():
     x, w, target = operands(100, 136, 1003, "fp16", 13)
     d = torch.full((), 0.01, device="cuda").expand(100)

@@ -38,7 +38,7 @@ def exact_gradients(x, target, weights, ignore):
     (12, 128, 256, 4099, torch.float16), (2048, 256, 704, 5000, torch.bfloat16)])
 def test_gradients_are_the_formulas(example, tokens, hidden, inner, vocab, dtype):
     """On no way from the inputs to a gradient are there more than twelve roundings to 16 bits
-    (y, h, D, dh, dy, the kept projections, dgate or dup, the result; dy's and D's own operands
+    (y, h, D, dh, dy, what is kept, dgate or dup, the result; dy's and D's own operands
     again).  Each is half a step of the value at most, and a product of independent matrices
     carries such a part of its operand's norm into the same part of its result's."""
     x, target, weights, _ = example.draw(tokens, hidden, inner, vocab, dtype=dtype)
