@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kGradThreads) few_grad_kernel(const __grid_con
   const int which = (int)blockIdx.z;
   const int row0 = (int)blockIdx.y * kGradTile, col0 = (int)blockIdx.x * kGradTile;
   const uint16_t* d = p.d[which];
-  const Scale sc = warp_scale(p.scale, p.scale_exp, p.scale_largest != 0);
+  const Scale sc = warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
   const bool bf16 = p.bf16 != 0;
   for (int i = threadIdx.x; i < kTokens * (kGradTile / 8); i += kGradThreads) {
     const int t = i / (kGradTile / 8), c = i % (kGradTile / 8) * 8;

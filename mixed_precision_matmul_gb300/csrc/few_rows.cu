@@ -3,7 +3,7 @@
 //
 // Weight lines are the M side of mma.sync m16n8k16 and the rows of X its N
 // side, eight at a time, so that nothing but X is padded.  A strip is 16 lines:
-// 8 of Wg and the same 8 of Wu (gated; c0, c1 of a thread are gates and c2, c3
+// 8 of Wg and the same 8 of Wu (gated, and dgate and dup; c0, c1 of a thread are gates and c2, c3
 // the same elements' ups), or 16 classes of a vocabulary.  The order of k inside
 // a sum is free, so a thread takes 16 contiguous bytes of a line as its values
 // of two instructions, and the same bytes of X's rows: fragments come straight
@@ -44,15 +44,21 @@ __device__ __forceinline__ uint4 load8(const uint16_t* line, int k, int end) {
   if (!line || k >= end) return make_uint4(0, 0, 0, 0);
   return ld_global(reinterpret_cast<const uint4*>(line + k));
 }
+
+constexpr bool two_of(FusedEpi e) { return e == FusedEpi::kGated || e == FusedEpi::kGatedGrad; }
+
 // The warps' sums of a strip (one a CTA) and what becomes of them; by the
 // kWarps * 32 threads of them, `sync` between.
-template <bool kGated, int kNt, class Red, class Sync>
-__device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, int thread, int strip, Sync&& sync) {
+template <FusedEpi E, int kNt, class Red, class Sync>
+__device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, const Scale& sc, int thread, int strip, Sync&& sync) {
   constexpr int kTokens = 8 * kNt;
-  constexpr int kLines = (kGated ? 8 : 16);
+  constexpr int kLines = two_of(E) ? 8 : 16;
   const int first = strip * kLines;
   const bool bf16 = p.bf16 != 0;
-  if constexpr (kGated) {
+  auto store = [&](void* base, int64_t ld, int t, int j, uint32_t w) {
+    static_cast<uint16_t*>(base)[(int64_t)t * ld + first + j] = (uint16_t)w;
+  };
+  if constexpr (two_of(E)) {
     for (int e = thread; e < kLines * kTokens; e += kWarps * 32) {
       const int j = e % kLines, t = e / kLines;
       float gt = 0.0f, up = 0.0f;
@@ -62,13 +68,19 @@ __device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, int thr
         up += red[w][j + 8][t];
       }
       if (t < p.rows && first + j < p.n) {
-        auto store = [&](void* base, int64_t ld, uint32_t w) { static_cast<uint16_t*>(base)[(int64_t)t * ld + first + j] = (uint16_t)w; };
-        store(p.y, p.ldy, pack16(act_value(gt, p.act) * up, 0.0f, bf16));
-        if (p.ka) {
-          float a, d;
+        float a, d;
+        if constexpr (E == FusedEpi::kGatedGrad) {
+          const float y = sc.mul * load16(p.dy, (int64_t)t * p.lddy + first + j, bf16);
           act_both(gt, p.act, a, d);
-          store(p.ka, p.lda, pack_kept(a, 0.0f, bf16));
-          store(p.kb, p.ldb, pack_kept(up * d, 0.0f, bf16));
+          store(p.y, p.ldy, t, j, pack16(y * (up * d), 0.0f, bf16));
+          store(p.ka, p.lda, t, j, pack16(y * a, 0.0f, bf16));
+        } else {
+          store(p.y, p.ldy, t, j, pack16(act_value(gt, p.act) * up, 0.0f, bf16));
+          if (p.ka) {
+            act_both(gt, p.act, a, d);
+            store(p.ka, p.lda, t, j, pack_kept(a, 0.0f, bf16));
+            store(p.kb, p.ldb, t, j, pack_kept(up * d, 0.0f, bf16));
+          }
         }
       }
     }
@@ -78,12 +90,22 @@ __device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, int thr
       float l = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) l += red[w][j][t];
-      red[0][j][t] = l;
+      if constexpr (E == FusedEpi::kProb) {
+        if (t < p.rows && first + j < p.n) {
+          const int64_t target = target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, t);
+          const float weight = target < 0 ? (target == -1 ? 0.0f : NAN) : sc.mul * (ld_global(p.dloss + t * p.dloss_stride) / sc.div);
+          const float x = ex2(fmaf(kLog2e, l, -kLog2e * ld_global(p.lse + t)));
+          store(p.y, p.ldy, t, j, weight == 0.0f ? 0u : pack16(weight * (target == p.col0 + first + j ? x - 1.0f : x), 0.0f, bf16));
+        }
+      } else {
+        red[0][j][t] = l;
+      }
     }
+    if constexpr (E == FusedEpi::kProb) return;
     sync();
     const int t = thread;
     if (t < p.rows) {
-      const int64_t target = target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.n, t);
+      const int64_t target = target_of(p.target, p.target_bytes, p.target_stride, p.ignore_index, p.vocab, t);
       if (target >= first && target < first + kLines) p.target_logit[t] = red[0][(int)(target - first)][t];
       float top = -INFINITY, sum = 0.0f;
       bool nan = false;
@@ -131,7 +153,7 @@ __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
   return v;
 }
 
-template <bool kGated, int kNt>
+template <FusedEpi E, int kNt>
 __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(const __grid_constant__ FewRowsParams p) {
   using T = RingTraits<kNt>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -164,9 +186,9 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
     for (int strip = blockIdx.x; strip < strips && ok; strip += gridDim.x) {
       const uint16_t* line = nullptr;
       if (lane < T::kLines) {
-        const int row = kGated ? strip * 8 + (lane & 7) : strip * 16 + lane;
+        const int row = two_of(E) ? strip * 8 + (lane & 7) : strip * 16 + lane;
         if (row < p.n)
-          line = kGated && lane >= 8 ? static_cast<const uint16_t*>(p.wu) + (int64_t)row * p.ldwu
+          line = two_of(E) && lane >= 8 ? static_cast<const uint16_t*>(p.wu) + (int64_t)row * p.ldwu
                                   : static_cast<const uint16_t*>(p.w) + (int64_t)row * p.ldw;
       }
       const uint32_t lines = __popc(__ballot_sync(0xffffffffu, line != nullptr));
@@ -194,6 +216,7 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
   // -------------------------------------------------------------- sums
   const int g = lane >> 2, tig = lane & 3;
   const bool bf16 = p.bf16 != 0;
+  const Scale sc = warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
   const uint16_t* xr[kNt];
 #pragma unroll
   for (int i = 0; i < kNt; ++i)
@@ -244,13 +267,13 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[warp][g + 8 * (j >> 1)][8 * i + 2 * tig + (j & 1)] = c[i][j];
     sync();
-    finish<kGated, kNt>(p, r, threadIdx.x, strip, sync);
+    finish<E, kNt>(p, r, sc, threadIdx.x, strip, sync);
   }
 }
 
-template <bool kGated, int kNt>
+template <FusedEpi E, int kNt>
 mpg_status launch(DeviceInfo* dev, FewRowsParams& p, cudaStream_t stream) {
-  constexpr int kLines = (kGated ? 8 : 16);
+  constexpr int kLines = two_of(E) ? 8 : 16;
   using T = RingTraits<kNt>;
   p.strips = (p.n + kLines - 1) / kLines;
   p.status = dev->status;
@@ -260,12 +283,12 @@ mpg_status launch(DeviceInfo* dev, FewRowsParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   cfg.numAttrs = (unsigned)launch_attributes(attr, 1);
   cfg.attrs = attr;
-  const mpg_status s = allow_smem(dev, reinterpret_cast<const void*>(&few_rows_kernel<kGated, kNt>), T::kSmemBytes);
+  const mpg_status s = allow_smem(dev, reinterpret_cast<const void*>(&few_rows_kernel<E, kNt>), T::kSmemBytes);
   if (s != MPG_OK) return s;
   cfg.gridDim = dim3((unsigned)std::min(p.strips, 2 * dev->sm_count));
   cfg.blockDim = dim3(T::kThreads);
   cfg.dynamicSmemBytes = T::kSmemBytes;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, few_rows_kernel<kGated, kNt>, static_cast<const FewRowsParams&>(p));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, few_rows_kernel<E, kNt>, static_cast<const FewRowsParams&>(p));
   return e == cudaSuccess ? MPG_OK : fail(MPG_ERR_CUDA, "few rows launch: %s", cudaGetErrorString(e));
 }
 
@@ -275,9 +298,20 @@ int few_rows_parts(int64_t n) {
   return (int)((n + 15) / 16);
 }
 
-mpg_status launch_few_rows(DeviceInfo* dev, FewRowsParams& p, bool gated, cudaStream_t stream) {
-  if (p.rows <= 8) return gated ? launch<true, 1>(dev, p, stream) : launch<false, 1>(dev, p, stream);
-  return gated ? launch<true, 2>(dev, p, stream) : launch<false, 2>(dev, p, stream);
+namespace {
+template <FusedEpi E>
+mpg_status launch_rows(DeviceInfo* dev, FewRowsParams& p, cudaStream_t stream) {
+  return p.rows <= 8 ? launch<E, 1>(dev, p, stream) : launch<E, 2>(dev, p, stream);
+}
+}  // namespace
+
+mpg_status launch_few_rows(DeviceInfo* dev, FewRowsParams& p, FusedEpi epi, cudaStream_t stream) {
+  switch (epi) {
+    case FusedEpi::kGated: return launch_rows<FusedEpi::kGated>(dev, p, stream);
+    case FusedEpi::kGatedGrad: return launch_rows<FusedEpi::kGatedGrad>(dev, p, stream);
+    case FusedEpi::kStats: return launch_rows<FusedEpi::kStats>(dev, p, stream);
+    default: return launch_rows<FusedEpi::kProb>(dev, p, stream);
+  }
 }
 
 }  // namespace mpg

@@ -148,10 +148,10 @@ __device__ __forceinline__ Scale make_scale(float largest, int exp, bool by_larg
   return Scale{1.0f, pow2(e), pow2(-e)};
 }
 // By a whole warp, after griddep_wait.
-__device__ __forceinline__ Scale warp_scale(const float* partial, int exp, bool by_largest) {
+__device__ __forceinline__ Scale warp_scale(const float* partial, int count, int exp, bool by_largest) {
   if (!partial) return Scale{1.0f, 1.0f, 1.0f};
   float x = 0.0f;
-  for (int i = threadIdx.x & 31; i < kScaleBlocks; i += 32) x = fmaxf(x, ld_global(partial + i));
+  for (int i = threadIdx.x & 31; i < count; i += 32) x = fmaxf(x, fabsf(ld_global(partial + i)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return make_scale(x, exp, by_largest);

@@ -56,8 +56,8 @@ struct FusedGemmParams {
   const void* dy;                   // kGatedGrad
   int64_t lddy;
   int32_t dy_vec;
-  const float* scale;               // partial maxima behind the scale that 16-bit gradients carry, or null
-  int32_t scale_exp, scale_largest; // see Scale
+  const float* scale;               // values whose largest sets the scale that 16-bit gradients carry, or null
+  int32_t scale_count, scale_exp, scale_largest;   // see Scale
 
   // cross entropy
   const void* target;
@@ -87,24 +87,31 @@ void fused_lookup_plain(bool pair, FusedKernel* out);
 void fused_lookup_gated(bool pair, int act, FusedKernel* out);
 void fused_lookup_gated_grad(bool pair, int act, FusedKernel* out);
 void fused_lookup_loss(FusedEpi epi, bool pair, FusedKernel* out);
-// The product of few rows: gated (wu given) or the statistics of logits.
+// The product of few rows, with the epilogues of the tiles (but kPlain).
 struct FewRowsParams {
   const void *x, *w, *wu;           // X: rows x k; weights: n x k; lines of whole 16 bytes, k a multiple of 8
   int64_t ldx, ldw, ldwu;
   int32_t bf16, rows, n, k;
   int32_t strips;
   int32_t act;
-  void *y, *ka, *kb;                // Y; act(gate) and up act'(gate), or null
+  void *y, *ka, *kb;                // Y, act(gate) and up act'(gate) (or null); dgate and dup; D
   int64_t ldy, lda, ldb;
+  const void* dy;
+  int64_t lddy;
+  const float* scale;
+  int32_t scale_count, scale_exp, scale_largest;
   const void* target;
   int32_t target_bytes;
   int64_t target_stride, ignore_index;
+  int32_t col0, vocab;              // class of the first line; of all
   float2* stats;
   float* target_logit;
+  const float *lse, *dloss;
+  int64_t dloss_stride;
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
-mpg_status launch_few_rows(DeviceInfo* dev, FewRowsParams& p, bool gated, cudaStream_t stream);
+mpg_status launch_few_rows(DeviceInfo* dev, FewRowsParams& p, FusedEpi epi, cudaStream_t stream);
 int few_rows_parts(int64_t n);      // of the statistics of n logits
 
 // Weight gradients of few tokens: out[i] = inverse * d[i]^T x (few_grad.cu).  Blocks
@@ -118,7 +125,7 @@ struct FewGradParams {
   void* out[2];                     // lines start on 16 bytes
   int64_t ldo[2];
   const float* scale;
-  int32_t scale_exp, scale_largest;
+  int32_t scale_count, scale_exp, scale_largest;
 };
 cudaError_t launch_few_grad(const FewGradParams& p, cudaStream_t stream);
 
@@ -156,7 +163,7 @@ struct GatedGradParams {
   int64_t rows, cols;
   int32_t vec, bf16;
   const float* scale;
-  int32_t scale_exp;
+  int32_t scale_count, scale_exp;
 };
 cudaError_t launch_gated_grad(const GatedGradParams& p, int sm_count, cudaStream_t stream);
 

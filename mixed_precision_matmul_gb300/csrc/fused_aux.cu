@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const __grid_constant__
   griddep_wait();
   griddep_launch_dependents();
   const bool bf16 = p.bf16 != 0, vec = p.vec != 0;
-  const float s = warp_scale(p.scale, p.scale_exp, false).mul;
+  const float s = warp_scale(p.scale, p.scale_count, p.scale_exp, false).mul;
   const int64_t per_line = (p.cols + 7) / 8, n = p.rows * per_line;
   const bool small = n < INT_MAX;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {

@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
     constexpr int kCc = T::kTileN / 32 / 2;         // 32-column chunks of one warp
     const int cc0 = half * kCc;
     const bool bf16 = p.bf16 != 0;
-    const Scale sc = warp_scale(p.scale, p.scale_exp, p.scale_largest != 0);
+    const Scale sc = warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
     uint32_t g = 0;
     FusedItems items(p, worker, workers);
     constexpr bool kAhead = T::kEpi == FusedEpi::kGatedGrad;
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   const int i = blockIdx.y * kAt + place;
   const int r = i / kPerRow, c = i % kPerRow * 4;
   const int row = (second ? tc.mb - pr.mb_second : tc.mb) * T::kTile + r, col = tc.nb * T::kTileN + c;
-  const Scale sc = warp_scale(p.scale, p.scale_exp, p.scale_largest != 0);
+  const Scale sc = warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
   const bool in = row < pr.m;
   const int left = pr.n - col;                       // columns of the matrix from here on
   constexpr int64_t kSlot = T::kTile * T::kTile;

@@ -186,7 +186,7 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
     p.lda = lda;
     p.kb = B;
     p.ldb = ldb;
-    return launch_few_rows(dev, p, true, st);
+    return launch_few_rows(dev, p, FusedEpi::kGated, st);
   }
 
   FusedGemmParams p;
@@ -289,9 +289,34 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     p.vec = fused_lines_ok(dY, lddy) && fused_lines_ok(A, lda) && fused_lines_ok(B, ldb);
     p.bf16 = l.dtype == MPG_BF16;
     p.scale = half ? partial : nullptr;
+    p.scale_count = kScaleBlocks;
     p.scale_exp = kExp;
     const cudaError_t e = launch_gated_grad(p, dev->sm_count, st);
     if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "gradient launch: %s", cudaGetErrorString(e));
+  } else if (l.tokens <= kFewRows && (l.hidden % 8 == 0 || (o.x.copy && o.wg.copy && o.wu.copy))) {
+    // (lines of whole chunks of eight, or copies with zeros behind them)
+    FewRowsParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = o.x.ptr;
+    p.ldx = o.x.ld;
+    p.w = o.wg.ptr;
+    p.ldw = o.wg.ld;
+    p.wu = o.wu.ptr;
+    p.ldwu = o.wu.ld;
+    p.bf16 = !half;
+    p.rows = (int32_t)l.tokens;
+    p.n = (int32_t)l.inner;
+    p.k = (int32_t)fused_line(l.hidden);
+    p.act = (int32_t)l.act;
+    p.y = dg;
+    p.ka = du;
+    p.ldy = p.lda = o.ldd;
+    p.dy = dY;
+    p.lddy = lddy;
+    p.scale = half ? partial : nullptr;
+    p.scale_count = kScaleBlocks;
+    p.scale_exp = kExp;
+    if ((s = launch_few_rows(dev, p, FusedEpi::kGatedGrad, st)) != MPG_OK) return s;
   } else {
     FusedGemmParams p;
     std::memset(&p, 0, sizeof(p));
@@ -308,6 +333,7 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     p.lddy = lddy;
     p.dy_vec = fused_lines_ok(dY, lddy);
     p.scale = half ? partial : nullptr;
+    p.scale_count = kScaleBlocks;
     p.scale_exp = kExp;
     if ((s = launch_fused(dev, product(FusedEpi::kGatedGrad, l.tokens, l.inner, l.hidden), p, slots, st)) != MPG_OK) return s;
   }
@@ -315,6 +341,7 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
   std::memset(&p, 0, sizeof(p));
   p.bf16 = !half;
   p.scale = half ? partial : nullptr;
+  p.scale_count = kScaleBlocks;
   p.scale_exp = kExp;
   const void* const d[2] = {dg, du};
   int count = 0;
@@ -368,6 +395,7 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     w.ldo[0] = lddwg;
     w.ldo[1] = lddwu;
     w.scale = half ? partial : nullptr;
+    w.scale_count = kScaleBlocks;
     w.scale_exp = kExp;
     const cudaError_t e = launch_few_grad(w, st);
     return e == cudaSuccess ? MPG_OK : fail(MPG_ERR_CUDA, "weight gradient launch: %s", cudaGetErrorString(e));

@@ -170,9 +170,10 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
     p.target_bytes = l.target_bytes;
     p.target_stride = l.target_stride;
     p.ignore_index = l.ignore_index;
+    p.vocab = (int32_t)l.vocab;
     p.stats = stats;
     p.target_logit = target_logit;
-    if ((s = launch_few_rows(dev, p, false, st)) != MPG_OK) return s;
+    if ((s = launch_few_rows(dev, p, FusedEpi::kStats, st)) != MPG_OK) return s;
     j.parts = few_rows_parts(l.vocab);
   } else {
     FusedGemmParams p;
@@ -248,7 +249,10 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
   // number.
   const bool half = l.dtype == MPG_F16;
   const int exp = half ? 14 : 0;
-  {
+  // (one weight for all tokens is the largest: ignored ones have no gradient at all)
+  const bool same = dloss_stride == 0 || l.tokens == 1;
+  const float* scale = same ? dloss : partial;
+  if (!same) {
     MaxParams p;
     std::memset(&p, 0, sizeof(p));
     p.rows = l.tokens;
@@ -267,28 +271,60 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
     const uint16_t* w = static_cast<const uint16_t*>(o.w.ptr) + c0 * o.w.ld;
     FusedGemmParams p;
     std::memset(&p, 0, sizeof(p));
-    if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
-    if ((s = fused_map(&p.prod[0].map_b[0], w, o.w.ld, l.dtype, false, cols, l.hidden)) != MPG_OK) return s;
-    p.bf16 = !half;
-    p.prod[0].out[0] = grad;
-    p.prod[0].ldo[0] = o.piece;
-    p.prod[0].out_vec[0] = 1;
-    p.target = l.target;
-    p.target_bytes = l.target_bytes;
-    p.target_stride = l.target_stride;
-    p.ignore_index = l.ignore_index;
-    p.col0 = (int32_t)c0;
-    p.vocab = (int32_t)l.vocab;
-    p.lse = lse;
-    p.dloss = dloss;
-    p.dloss_stride = dloss_stride;
-    p.scale = partial;
-    p.scale_exp = exp;
-    p.scale_largest = 1;
-    if ((s = launch_fused(dev, product(FusedEpi::kProb, l.tokens, cols, l.hidden), p, slots, st)) != MPG_OK) return s;
+    if (l.tokens <= kFewRows && (l.hidden % 8 == 0 || (o.x.copy && o.w.copy))) {
+      // (lines of whole chunks of eight, or copies with zeros behind them)
+      FewRowsParams r;
+      std::memset(&r, 0, sizeof(r));
+      r.x = o.x.ptr;
+      r.ldx = o.x.ld;
+      r.w = w;
+      r.ldw = o.w.ld;
+      r.bf16 = !half;
+      r.rows = (int32_t)l.tokens;
+      r.n = (int32_t)cols;
+      r.k = (int32_t)fused_line(l.hidden);
+      r.y = grad;
+      r.ldy = o.piece;
+      r.target = l.target;
+      r.target_bytes = l.target_bytes;
+      r.target_stride = l.target_stride;
+      r.ignore_index = l.ignore_index;
+      r.col0 = (int32_t)c0;
+      r.vocab = (int32_t)l.vocab;
+      r.lse = lse;
+      r.dloss = dloss;
+      r.dloss_stride = dloss_stride;
+      r.scale = scale;
+      r.scale_count = same ? 1 : kScaleBlocks;
+      r.scale_exp = exp;
+      r.scale_largest = 1;
+      if ((s = launch_few_rows(dev, r, FusedEpi::kProb, st)) != MPG_OK) return s;
+    } else {
+      if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
+      if ((s = fused_map(&p.prod[0].map_b[0], w, o.w.ld, l.dtype, false, cols, l.hidden)) != MPG_OK) return s;
+      p.bf16 = !half;
+      p.prod[0].out[0] = grad;
+      p.prod[0].ldo[0] = o.piece;
+      p.prod[0].out_vec[0] = 1;
+      p.target = l.target;
+      p.target_bytes = l.target_bytes;
+      p.target_stride = l.target_stride;
+      p.ignore_index = l.ignore_index;
+      p.col0 = (int32_t)c0;
+      p.vocab = (int32_t)l.vocab;
+      p.lse = lse;
+      p.dloss = dloss;
+      p.dloss_stride = dloss_stride;
+      p.scale = scale;
+      p.scale_count = same ? 1 : kScaleBlocks;
+      p.scale_exp = exp;
+      p.scale_largest = 1;
+      if ((s = launch_fused(dev, product(FusedEpi::kProb, l.tokens, cols, l.hidden), p, slots, st)) != MPG_OK) return s;
+    }
     std::memset(&p, 0, sizeof(p));
     p.bf16 = !half;
-    p.scale = partial;
+    p.scale = scale;
+    p.scale_count = same ? 1 : kScaleBlocks;
     p.scale_exp = exp;
     p.scale_largest = 1;
     int count = 0;
@@ -334,7 +370,8 @@ mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const f
       y.bf16 = !half;
       y.out[0] = static_cast<uint16_t*>(dW) + c0 * lddw;
       y.ldo[0] = lddw;
-      y.scale = partial;
+      y.scale = scale;
+      y.scale_count = same ? 1 : kScaleBlocks;
       y.scale_exp = exp;
       y.scale_largest = 1;
       const cudaError_t e = launch_few_grad(y, st);
