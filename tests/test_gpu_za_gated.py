@@ -78,7 +78,8 @@ def test_gradients(t, h, i, act):
 
 
 @pytest.mark.parametrize("t,h,i,dtype", [(2048, 512, 2000, "bf16"), (1500, 1032, 3000, "fp16"), (4200, 256, 1030, "bf16"),
-                                         (200, 4000, 300, "fp16"), (40, 3999, 70, "bf16"), (600, 4096, 515, "fp16")])
+                                         (200, 4000, 300, "fp16"), (40, 3999, 70, "bf16"), (600, 4096, 515, "fp16"),
+                                         (40, 1001, 1100, "bf16"), (300, 1003, 1100, "fp16"), (1100, 1001, 130, "bf16")])
 def test_gradients_on_pairs(t, h, i, dtype):
     x, wg, wu, dy = operands(t, h, i, dtype, 4)
     _, g, u = mpg.gated_gemm(x, wg, wu, keep=True)
@@ -222,6 +223,31 @@ def test_nothing_is_written_beyond_the_results(t):
     ref = mpg.gated_gemm_backward(dy, x, wg, wu, kept=(g[:t, :i], u[:t, :i]))
     for b, r in zip(outs, ref):
         assert torch.equal(b[:r.shape[0], :r.shape[1]], r)
+
+
+@pytest.mark.parametrize("t", [20, 70, 1060])
+def test_large_packed_results_of_odd_lines(t):
+    """Results of a million elements whose lines are off 16 bytes, with marks before and behind them."""
+    import ctypes
+    h, i = 1001, 1060
+    x, wg, wu, dy = operands(t, h, i, "bf16", 13)
+    lay = mpg.GatedLayer(t, h, i, mpg.BF16, 0, x.data_ptr(), wg.data_ptr(), wu.data_ptr(), h, h, h)
+    mark = 12352.0
+    outs = [torch.full((16 + r * h + 16,), mark, dtype=torch.bfloat16, device="cuda") for r in (t, i, i)]
+    need = int(mpg.lib().mpg_gated_gemm_backward_workspace_size(ctypes.byref(lay)))
+    ws = torch.full((need + 256,), 77, dtype=torch.uint8, device="cuda")
+    refs, bounds = plain.gated_gradients(dy, x, wg, wu, "silu")
+    for shift in (16, 8, 9):                          # (9: not on 16 bytes, written as it comes)
+        for b in outs:
+            b.fill_(mark)
+        mpg.gated_gemm_backward_raw(lay, dy.data_ptr(), i, 0, 0, 0, 0, *(v for b in outs for v in (b[shift:].data_ptr(), h)),
+                                    ws.data_ptr(), need)
+        ok()
+        assert (ws[need:] == 77).all()
+        for b, r, e in zip(outs, refs, bounds):
+            n = r.numel()
+            plain.check(b[shift:shift + n].view(r.shape), r, e)
+            assert (b[:shift] == mark).all() and (b[shift + n:] == mark).all()
 
 
 @pytest.mark.parametrize("t", [1, 5, 16, 30, 60, 64, 65])

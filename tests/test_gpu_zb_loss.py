@@ -45,7 +45,8 @@ def test_loss(t, h, v):
             plain.check(b, lse, el)
 
 
-@pytest.mark.parametrize("t,h,v", SHAPES + [(2000, 264, 4099), (40, 64, 30000), (5, 72, 50000), (200, 4000, 300), (40, 3999, 70), (600, 4096, 1003)])
+@pytest.mark.parametrize("t,h,v", SHAPES + [(2000, 264, 4099), (40, 64, 30000), (5, 72, 50000), (200, 4000, 300), (40, 3999, 70), (600, 4096, 1003),
+                                             (9, 1001, 1100), (40, 1003, 1100), (300, 1001, 1100), (1100, 1001, 130)])
 def test_gradients(t, h, v):
     for dtype, pad, shift in (("fp16", 0, 0), ("bf16", 8, 8), ("fp16", 3, 1)):
         x, w, target = operands(t, h, v, dtype, 2, pad, shift)
