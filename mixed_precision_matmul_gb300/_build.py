@@ -59,7 +59,7 @@ SOURCES = [
     "clip.cu",
 ]
 HEADERS = ["ptx.cuh", "cluster.cuh", "internal.h", "tc_gemm.cuh", "outio.cuh", "host.h", "staging.cuh",
-           "fp8.h", "fp8_tc.cuh", "ortho.h", "fused.h", "fused.cuh", "fused_gemm.cuh"]
+           "fp8.h", "fp8_tc.cuh", "ortho.h", "fused.h", "fused.cuh", "fused_deal.h", "fused_gemm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -49,7 +49,8 @@ struct FusedGemmParams {
   int32_t bf16;
   int32_t whole_tiles;              // of the first: taken round by round; the others' blocks of k are dealt out evenly
   int64_t units, units_first;       // blocks of k of those others (and of all of the second's tiles); of the first's
-  float* slots;                     // partial tiles, two for each worker
+  int32_t dealers;                  // workers that they are dealt to (0: none), no more than there are blocks
+  float* slots;                     // partial tiles, two for each of those
   int32_t late, late_workers, late_rounds;   // the second's tiles: see FusedItems
 
   int32_t act;
@@ -81,7 +82,7 @@ struct FusedKernel {
   int tile;                         // rows of a tile, and columns of its accumulators
   int ctas;
   // sums the parts of split tiles and does the epilogue's work
-  cudaError_t (*join)(const FusedGemmParams& p, int workers, cudaStream_t stream);
+  cudaError_t (*join)(const FusedGemmParams& p, cudaStream_t stream);
 };
 void fused_lookup_plain(bool pair, FusedKernel* out);
 void fused_lookup_gated(bool pair, int act, FusedKernel* out);

@@ -55,6 +55,7 @@
 
 #include "cluster.cuh"
 #include "fused.cuh"
+#include "fused_deal.h"
 #include "outio.cuh"
 #include "staging.cuh"
 #include "tc_gemm.cuh"
@@ -222,90 +223,6 @@ __device__ __forceinline__ float row_weight(const FusedGemmParams& p, int row, i
   if (target < 0) return target == -1 ? 0.0f : NAN;
   return sc.mul * (ld_global(p.dloss + (int64_t)row * p.dloss_stride) / sc.div);
 }
-
-struct FusedTile {
-  int mb, nb;
-};
-__device__ __forceinline__ FusedTile fused_tile(const FusedProduct& p, int t) {
-  // groups of tile rows, walked column by column, every other group backwards
-  const int per = p.group_m * p.num_n_blk;
-  const int g = t / per;
-  const int first = g * p.group_m;
-  const int gm = min(p.group_m, p.num_m_blk - first);
-  const int within = t - g * per;
-  FusedTile c;
-  c.mb = first + within % gm;
-  c.nb = within / gm;
-  if (g & 1) c.nb = p.num_n_blk - 1 - c.nb;
-  return c;
-}
-
-// The first of the split tiles' blocks of k that worker w takes.
-__host__ __device__ __forceinline__ int64_t first_unit(int64_t units, int w, int workers) { return units * w / workers; }
-
-// A worker's tiles: the first product's whole ones round by round, then its run of
-// the split tiles' blocks of k (that product's, then the second's where all of
-// its tiles are dealt out: p.units_first of the blocks are the first's), then the
-// second product's whole ones.  Workers p.late .. have one tile of the first product less than those before them; they
-// take p.late_rounds rounds of the second's alone, about as long as that tile,
-// and then go first in the rounds of all.
-struct FusedItem {
-  int which;                         // product
-  int mb, nb, kb0, kb1;
-  int slot;                          // of a part of a tile's k; -1: all of it
-};
-struct FusedItems {
-  int t, round, worker, workers;
-  int64_t u, u0, u1;
-  __device__ __forceinline__ FusedItems(const FusedGemmParams& p, int w, int n) : t(w), round(0), worker(w), workers(n) {
-    u = u0 = u1 = 0;
-    if (p.units) {
-      u = u0 = first_unit(p.units, w, n);
-      u1 = first_unit(p.units, w + 1, n);
-    }
-  }
-  template <bool kMore>                              // whether there may be a second product
-  __device__ __forceinline__ bool next(const FusedGemmParams& p, FusedItem& x) {
-    int tile;
-    x.which = 0;
-    x.kb0 = 0;
-    x.kb1 = p.prod[0].num_k_blk;
-    x.slot = -1;
-    if (t < p.whole_tiles) {
-      tile = t;
-      t += workers;
-    } else if (u < u1) {
-      x.which = kMore && u >= p.units_first ? 1 : 0;
-      const int kb = p.prod[x.which].num_k_blk;
-      const int64_t v = x.which ? u - p.units_first : u;
-      const int64_t j = v / kb;
-      tile = (x.which ? 0 : p.whole_tiles) + (int)j;
-      x.kb0 = (int)(v - j * kb);
-      x.kb1 = (int)min((int64_t)kb, x.kb0 + (u1 - u));
-      x.slot = x.kb1 - x.kb0 == kb ? -1 : 2 * worker + (u == u0 ? 0 : 1);
-      u += x.kb1 - x.kb0;
-    } else if (kMore && p.prod[1].num_tiles && p.units <= p.units_first) {
-      int rank = worker - p.late;
-      if (rank >= 0 && round < p.late_rounds) {
-        tile = round * p.late_workers + rank;
-      } else {
-        if (rank < 0) rank += workers;
-        const int more = worker >= p.late ? round - p.late_rounds : round;
-        tile = p.late_rounds * p.late_workers + more * workers + rank;
-      }
-      ++round;
-      if (tile >= p.prod[1].num_tiles) return false;
-      x.which = 1;
-      x.kb1 = p.prod[1].num_k_blk;
-    } else {
-      return false;
-    }
-    const FusedTile c = fused_tile(p.prod[kMore ? x.which : 0], tile);
-    x.mb = c.mb;
-    x.nb = c.nb;
-    return true;
-  }
-};
 
 template <class T>
 __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid_constant__ FusedGemmParams p) {
@@ -827,13 +744,11 @@ __device__ __forceinline__ void load_four(float (&v)[4], const void* src, int64_
 
 // Adds a tile's parts in the order of k, four columns a thread, and does what the
 // epilogue does with the sums.  Tiles that one worker had whole are done already.
-// Every worker has a block of k at least, so the parts of a tile are those of
-// consecutive workers, and only the first can have begun in an earlier tile (its
-// second slot).  A tile of many parts (few tiles, long k) has kSlices warps that
+// A tile of many parts (few tiles, long k) has kSlices warps that
 // add a run of them each: 150 parts of one tile 27 us with one.
 constexpr int kJoinThreads = 256;
 template <class T, int kSlices>
-__global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_constant__ FusedGemmParams p, int workers) {
+__global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_constant__ FusedGemmParams p) {
   constexpr int kPerRow = T::kTileN / 4;
   constexpr int kAt = kJoinThreads / kSlices;        // places of a block
   __shared__ float4 slices[kSlices > 1 ? kSlices : 1][T::kTwo ? 2 : 1][kSlices > 1 ? kAt : 1];
@@ -845,8 +760,8 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   const int tile = which ? (int)blockIdx.x - tiles0 : p.whole_tiles + (int)blockIdx.x;
   const int64_t u0 = which ? p.units_first + (int64_t)tile * pr.num_k_blk : (int64_t)blockIdx.x * pr.num_k_blk;
   const int64_t u1 = u0 + pr.num_k_blk;
-  const int w0 = (int)(((u0 + 1) * workers - 1) / p.units);                     // the last that begins at u0 or before
-  const int n = (int)((u1 * workers + p.units - 1) / p.units) - w0;             // up to the last that begins before u1
+  const FusedParts parts(p, u0, u1);
+  const int n = parts.count;
   if (n == 1) return;
   const FusedTile tc = fused_tile(pr, tile);
   const bool second = tc.mb >= pr.mb_second;
@@ -858,7 +773,6 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   const bool in = row < pr.m;
   const int left = pr.n - col;                       // columns of the matrix from here on
   constexpr int64_t kSlot = T::kTile * T::kTile;
-  const int first = 2 * w0 + (first_unit(p.units, w0, workers) < u0 ? 1 : 0);
   auto sum = [&](int which, int column, float (&v)[4]) {
     const float* at = p.slots + (int64_t)r * T::kTile + column;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -870,9 +784,9 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
     };
     if (in && left > 0) {
       const int j0 = kSlices > 1 ? n * slice / kSlices : 0, j1 = kSlices > 1 ? n * (slice + 1) / kSlices : n;
-      if (j0 == 0) add(out_load4(at, first * kSlot, kOutF32));
+      if (j0 == 0) add(out_load4(at, parts.slot(0) * kSlot, kOutF32));
 #pragma unroll 4
-      for (int j = max(j0, 1); j < j1; ++j) add(out_load4(at, 2 * (w0 + j) * kSlot, kOutF32));
+      for (int j = max(j0, 1); j < j1; ++j) add(out_load4(at, parts.slot(j) * kSlot, kOutF32));
     }
     if constexpr (kSlices > 1) {
       slices[slice][which][place] = o;
@@ -973,11 +887,11 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
 }
 
 template <class T>
-cudaError_t launch_fused_join(const FusedGemmParams& p, int workers, cudaStream_t stream) {
+cudaError_t launch_fused_join(const FusedGemmParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   const bool both = p.units > p.units_first;
   const int tiles = p.prod[0].num_tiles - p.whole_tiles + (both ? p.prod[1].num_tiles : 0);
-  const bool many = workers >= 8 * tiles;
+  const bool many = p.dealers >= 8 * tiles;
   const int rows = both ? std::max(p.prod[0].m, p.prod[1].m) : p.prod[0].m;
   const int places = std::min(T::kTile, rows) * (T::kTileN / 4), at = many ? kJoinThreads / 8 : kJoinThreads;
   cfg.gridDim = dim3((unsigned)tiles, (unsigned)((places + at - 1) / at));
@@ -986,8 +900,8 @@ cudaError_t launch_fused_join(const FusedGemmParams& p, int workers, cudaStream_
   cudaLaunchAttribute attr[2];
   cfg.numAttrs = (unsigned)launch_attributes(attr, 1);
   cfg.attrs = attr;
-  return many ? cudaLaunchKernelEx(&cfg, fused_join_kernel<T, 8>, p, workers)
-              : cudaLaunchKernelEx(&cfg, fused_join_kernel<T, 1>, p, workers);
+  return many ? cudaLaunchKernelEx(&cfg, fused_join_kernel<T, 8>, p)
+              : cudaLaunchKernelEx(&cfg, fused_join_kernel<T, 1>, p);
 }
 
 template <class T>

@@ -3,71 +3,16 @@
 #include <cstring>
 #include <utility>
 
-#include "fused.h"
+#include "fused_deal.h"
 
 namespace mpg {
-
-namespace {
-
-constexpr int64_t kMinUnits = 4;       // blocks of k of a worker with a part of a tile, at least
-constexpr int64_t kMaxPairs = kMaxCtas / 2;
-
-struct Shape {
-  int64_t mb, nb, kb, tiles, units;    // blocks of one matrix and one part of k; all tiles, all blocks of k
-};
-Shape shape_of(const FusedLaunch& l, int64_t tile) {
-  const bool two = l.epi == FusedEpi::kGated || l.epi == FusedEpi::kGatedGrad;
-  Shape s;
-  s.mb = (l.m + tile - 1) / tile;
-  s.nb = (l.n + (two ? tile / 2 : tile) - 1) / (two ? tile / 2 : tile);
-  s.kb = (l.k + 63) / 64;
-  s.tiles = s.mb * (l.second_m ? 2 : 1) * s.nb;
-  s.units = s.tiles * s.kb * (l.second_k ? 2 : 1);
-  return s;
-}
-
-// What the forms take on a GB300 (us): a way in and out, and a time for each
-// block of 64 k of a round of tiles.  Workers with parts of split tiles are at
-// different places of k: where the operands do not fit into L2 each fetches its
-// own blocks, at about 8300 bytes a ns together (a last round of 52 pairs' tiles
-// over k = 32768, dealt to 76: 210 us where the round takes 173), so that
-// splitting pays where it gives many idle workers something to do.  The parts
-// go through memory twice, and the second launch takes 3 us.
-constexpr double kOneEpi = 1.9, kPairEpi = 3.8;    // a tile's way out, beside the next one's products
-constexpr double kOneEdge = 4.3, kPairEdge = 7.5, kOneBlock = 0.29, kPairBlock = 0.31;
-constexpr double kJoin = 3.0, kApartBytes = 8.3e6, kPartBytes = 5.0e6;     // bytes a us
-constexpr double kL2Bytes = 100e6;
-
-struct Deal {
-  int64_t workers, whole;              // whole: tiles taken round by round
-  double time;
-};
-Deal deal(const FusedLaunch& l, const Shape& s, int64_t tile, int64_t most, double edge, double block, bool may_split) {
-  const int64_t kb = s.units / s.tiles;
-  const int64_t rounds = (s.tiles + most - 1) / most;
-  const double round = std::max((double)kb * block, tile == 256 ? kPairEpi : kOneEpi);
-  Deal d{std::min(s.tiles, most), s.tiles, edge + (double)rounds * round};
-  const int64_t rest = s.tiles % most;
-  if (!may_split || !rest || kb < 2) return d;
-  const int64_t whole = s.tiles - rest;
-  const int64_t workers = whole ? most : std::min(most, std::max(rest, rest * kb / kMinUnits));
-  const double operands = 128.0 * (double)kb * (double)((l.second_m ? 2 : 1) * l.m + l.n);
-  const double apart = operands < kL2Bytes ? block : std::max(block, 256.0 * (double)tile * (double)workers / kApartBytes);
-  const double parts = (double)(rest + workers) * (double)(tile * tile) * 4.0;
-  const double time = edge + kJoin + 2.0 * parts / kPartBytes + (double)(whole / most) * round +
-                      (double)((rest * kb + workers - 1) / workers) * apart;
-  if (time < d.time) d = Deal{workers, whole, time};
-  return d;
-}
-
-}  // namespace
 
 size_t fused_slot_bytes(const FusedLaunch& l, const FusedLaunch* second) {
   size_t most = 0;
   for (int64_t tile : {(int64_t)128, (int64_t)256}) {
-    Shape s = shape_of(l, tile);
+    FusedShape s = shape_of(l, tile);
     if (second) {
-      const Shape t = shape_of(*second, tile);
+      const FusedShape t = shape_of(*second, tile);
       s.tiles += t.tiles;
       s.units += t.units;
     }
@@ -107,13 +52,12 @@ mpg_status forms_of(DeviceInfo* dev, FusedEpi epi, int act, Forms* f) {
   f->workers[1] = std::min<int64_t>(pairs, kMaxPairs);
   return allow_smem(dev, f->kernel[0].fn, f->kernel[0].smem_bytes);
 }
-Deal deal_form(const FusedLaunch& l, const Forms& f, int pair, bool split) {
-  const int64_t tile = f.kernel[pair].tile;
-  return deal(l, shape_of(l, tile), tile, f.workers[pair], pair ? kPairEdge : kOneEdge, pair ? kPairBlock : kOneBlock, split);
+FusedDeal deal_form(const FusedLaunch& l, const Forms& f, int pair, bool split) {
+  return deal(l, f.kernel[pair].tile, f.workers[pair], split);
 }
 
 mpg_status fill_product(FusedProduct& p, const FusedLaunch& l, int64_t tile, bool pair) {
-  const Shape s = shape_of(l, tile);
+  const FusedShape s = shape_of(l, tile);
   if (s.tiles > kFusedMaxExtent || s.units / s.tiles > kFusedMaxExtent) return fail(MPG_ERR_INVALID_ARG, "too many tiles");
   p.m = (int32_t)l.m;
   p.n = (int32_t)l.n;
@@ -127,11 +71,16 @@ mpg_status fill_product(FusedProduct& p, const FusedLaunch& l, int64_t tile, boo
   return MPG_OK;
 }
 
-// dealt: the blocks of k of both products' tiles are dealt out.
-mpg_status launch(DeviceInfo* dev, const FusedKernel& k, FusedGemmParams& p, int64_t workers, bool dealt, float* slots,
-                  cudaStream_t stream) {
+// dealers: of the workers, those with a run of the split tiles' blocks of k;
+// dealt: both products' tiles are split.
+mpg_status launch(DeviceInfo* dev, const FusedKernel& k, FusedGemmParams& p, int64_t workers, int64_t dealers, bool dealt,
+                  float* slots, cudaStream_t stream) {
   p.units_first = (int64_t)(p.prod[0].num_tiles - p.whole_tiles) * p.prod[0].num_k_blk;
   p.units = p.units_first + (dealt ? (int64_t)p.prod[1].num_tiles * p.prod[1].num_k_blk : 0);
+  p.dealers = (int32_t)dealers;
+  // (a dealer without a block would leave its slots as they are, and the join adds them)
+  if (dealers > workers || p.units < dealers || (p.units > 0) != (dealers > 0))
+    return fail(MPG_ERR_INVALID_ARG, "%lld blocks for %lld of %lld workers", (long long)p.units, (long long)dealers, (long long)workers);
   p.slots = slots;
   p.status = dev->status;
   p.wait_limit_ns = kDefaultWaitNs;
@@ -147,7 +96,7 @@ mpg_status launch(DeviceInfo* dev, const FusedKernel& k, FusedGemmParams& p, int
   cudaError_t e = cudaLaunchKernelExC(&cfg, k.fn, args);
   if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "product launch: %s", cudaGetErrorString(e));
   if (p.units) {
-    e = k.join(p, (int)workers, stream);
+    e = k.join(p, stream);
     if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "join launch: %s", cudaGetErrorString(e));
   }
   return MPG_OK;
@@ -160,13 +109,13 @@ mpg_status launch_fused(DeviceInfo* dev, const FusedLaunch& l, FusedGemmParams& 
   mpg_status s = forms_of(dev, l.epi, p.act, &f);
   if (s != MPG_OK) return s;
   const bool split = slots != nullptr;
-  const Deal d1 = deal_form(l, f, 0, split), d2 = deal_form(l, f, 1, split);
+  const FusedDeal d1 = deal_form(l, f, 0, split), d2 = deal_form(l, f, 1, split);
   const int pair = d2.time < d1.time;
-  const Deal& d = pair ? d2 : d1;
+  const FusedDeal& d = pair ? d2 : d1;
   if ((s = fill_product(p.prod[0], l, f.kernel[pair].tile, pair)) != MPG_OK) return s;
   p.prod[1].num_tiles = 0;
   p.whole_tiles = (int32_t)d.whole;
-  return launch(dev, f.kernel[pair], p, d.workers, false, slots, stream);
+  return launch(dev, f.kernel[pair], p, d.workers, d.dealers, false, slots, stream);
 }
 
 // In one launch the second product's tiles fill what the first's last round
@@ -181,7 +130,7 @@ mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedL
   mpg_status s = forms_of(dev, FusedEpi::kPlain, 0, &f);
   if (s != MPG_OK) return s;
   const FusedLaunch* l[2] = {&l0, &l1};
-  const Shape first = shape_of(l0, 256), second = shape_of(l1, 256);
+  const FusedShape first = shape_of(l0, 256), second = shape_of(l1, 256);
   const bool swap = second.units / second.tiles > first.units / first.tiles;     // the longer k goes first
   if (swap) {
     std::swap(l[0], l[1]);
@@ -195,7 +144,7 @@ mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedL
   bool dealt = false;
   for (int pair = 0; pair < 2; ++pair) {
     const int64_t tile = f.kernel[pair].tile, w = f.workers[pair];
-    const Shape a = shape_of(*l[0], tile), b = shape_of(*l[1], tile);
+    const FusedShape a = shape_of(*l[0], tile), b = shape_of(*l[1], tile);
     const int64_t ka = a.units / a.tiles, kb = b.units / b.tiles;
     const int64_t busy = a.tiles % w;                                             // workers with one tile more than the others
     const int64_t idle = busy ? w - busy : 0;
@@ -238,14 +187,14 @@ mpg_status launch_fused_two(DeviceInfo* dev, const FusedLaunch& l0, const FusedL
     if ((s = fill_product(p.prod[i], *l[i], k.tile, form)) != MPG_OK) return s;
   if (dealt) {
     p.whole_tiles = 0;
-    return launch(dev, k, p, workers, true, slots, stream);
+    return launch(dev, k, p, workers, workers, true, slots, stream);
   }
   p.whole_tiles = p.prod[0].num_tiles;
   p.late = (int32_t)late;
   p.late_workers = (int32_t)late_workers;
   p.late_rounds = (int32_t)late_rounds;
   const int64_t tiles = (int64_t)p.prod[0].num_tiles + p.prod[1].num_tiles;
-  return launch(dev, k, p, std::min(f.workers[form], tiles), false, slots, stream);
+  return launch(dev, k, p, std::min(f.workers[form], tiles), 0, false, slots, stream);
 }
 
 }  // namespace mpg
