@@ -539,8 +539,11 @@ mpg_status mpg_gated_gemm(const mpg_gated_layer* layer, void* Y, int64_t ldy, vo
  * many operations more).
  * dG and dU are rounded once to the 16-bit type, as operands of the products;
  * in fp16 they carry a power of two meanwhile, which brings the largest of dY
- * to [16, 32), so that small gradients keep their precision; products up * act'
- * above 2^11 then overflow.  tokens or inner 0: gradients of 0. */
+ * to [16, 32), or, where the largest finite dG or dU then leaves fp16 or is below
+ * 2^-4, that one to [2^14, 2^15): no finite gradient overflows on the way, and
+ * what is 2^18 times smaller than the largest still has fp16's precision.  What was
+ * kept has its own range (see above): beyond it gradients are infinite or NaN
+ * that are finite when computed again.  tokens or inner 0: gradients of 0. */
 size_t mpg_gated_gemm_backward_workspace_size(const mpg_gated_layer* layer);
 mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY, int64_t lddy, const void* A, int64_t lda,
                                    const void* B, int64_t ldb, void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,

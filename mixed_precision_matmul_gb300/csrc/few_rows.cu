@@ -50,7 +50,7 @@ constexpr bool two_of(FusedEpi e) { return e == FusedEpi::kGated || e == FusedEp
 // The warps' sums of a strip (one a CTA) and what becomes of them; by the
 // kWarps * 32 threads of them, `sync` between.
 template <FusedEpi E, int kNt, class Red, class Sync>
-__device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, const Scale& sc, int thread, int strip, Sync&& sync) {
+__device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, const Scale& sc, float& top, int thread, int strip, Sync&& sync) {
   constexpr int kTokens = 8 * kNt;
   constexpr int kLines = two_of(E) ? 8 : 16;
   const int first = strip * kLines;
@@ -72,8 +72,10 @@ __device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, const S
         if constexpr (E == FusedEpi::kGatedGrad) {
           const float y = sc.mul * load16(p.dy, (int64_t)t * p.lddy + first + j, bf16);
           act_both(gt, p.act, a, d);
-          store(p.y, p.ldy, t, j, pack16(y * (up * d), 0.0f, bf16));
-          store(p.ka, p.lda, t, j, pack16(y * a, 0.0f, bf16));
+          const float dg = y * (up * d), du = y * a;
+          top = largest_finite(largest_finite(top, dg), du);
+          store(p.y, p.ldy, t, j, pack16(dg, 0.0f, bf16));
+          store(p.ka, p.lda, t, j, pack16(du, 0.0f, bf16));
         } else {
           store(p.y, p.ldy, t, j, pack16(act_value(gt, p.act) * up, 0.0f, bf16));
           if (p.ka) {
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
+  if (E == FusedEpi::kGatedGrad && !GradTop::needed(p, blockIdx.x == 0 && warp == 0)) return;
   WaitCtl ctl;
   ctl.abort = abort_flag;
   ctl.status = p.status;
@@ -216,7 +219,8 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
   // -------------------------------------------------------------- sums
   const int g = lane >> 2, tig = lane & 3;
   const bool bf16 = p.bf16 != 0;
-  const Scale sc = warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
+  const Scale sc = E == FusedEpi::kGatedGrad ? GradTop::scale(p) : warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
+  float top = 0.0f;
   const uint16_t* xr[kNt];
 #pragma unroll
   for (int i = 0; i < kNt; ++i)
@@ -267,7 +271,11 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[warp][g + 8 * (j >> 1)][8 * i + 2 * tig + (j & 1)] = c[i][j];
     sync();
-    finish<E, kNt>(p, r, sc, threadIdx.x, strip, sync);
+    finish<E, kNt>(p, r, sc, top, threadIdx.x, strip, sync);
+  }
+  if (E == FusedEpi::kGatedGrad && p.record) {
+    __syncwarp();
+    GradTop::record(p.record, (int)blockIdx.x * kWarps + warp, top);
   }
 }
 

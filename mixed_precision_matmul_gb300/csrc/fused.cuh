@@ -136,25 +136,71 @@ __device__ __forceinline__ int64_t target_of(const void* target, int bytes, int6
 //                      weight is then exact, and not off by one rounding in all of
 //                      them at once (half a step of bf16 in the whole gradient).
 // 1 where the largest is 0 or not finite.
+//
+// The gradients of gate and up are dY times what may be far above 1 (channels in
+// which gate and up are large together) or below.  They are made with the scale of dY
+// alone first, and the largest of them is kept in `record` (kTopParts parts, of
+// finite values): where it does not fit into fp16, or all of them are small, the
+// scale brings it to [2^14, 2^15) instead, and the launch that made them is done `again`.
+// As a rule that launch finds that they fit, and ends.  It leaves what the products
+// are multiplied by behind the parts, for those that come after it.
 struct Scale {
   float div, mul, inv;
 };
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-__device__ __forceinline__ Scale make_scale(float largest, int exp, bool by_largest) {
-  if (!(largest > 0.0f) || largest > 3.0e38f) return Scale{1.0f, 1.0f, 1.0f};
-  if (by_largest) return Scale{largest, pow2(exp), largest * pow2(-exp)};
-  int e = exp - ilogbf(largest);
-  e = e > 126 ? 126 : e < -126 ? -126 : e;
+__device__ __forceinline__ int scale_exponent(int e) { return e > 126 ? 126 : e < -126 ? -126 : e; }
+__device__ __forceinline__ Scale make_scale(float largest, int exp, bool by_largest, int more) {
+  const bool none = !(largest > 0.0f) || largest > 3.0e38f;
+  if (by_largest) return none ? Scale{1.0f, 1.0f, 1.0f} : Scale{largest, pow2(exp), largest * pow2(-exp)};
+  const int e = scale_exponent((none ? 0 : scale_exponent(exp - ilogbf(largest))) + more);
   return Scale{1.0f, pow2(e), pow2(-e)};
 }
-// By a whole warp, after griddep_wait.
-__device__ __forceinline__ Scale warp_scale(const float* partial, int count, int exp, bool by_largest) {
-  if (!partial) return Scale{1.0f, 1.0f, 1.0f};
+__device__ __forceinline__ float warp_largest(const float* partial, int count) {
   float x = 0.0f;
   for (int i = threadIdx.x & 31; i < count; i += 32) x = fmaxf(x, fabsf(ld_global(partial + i)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return make_scale(x, exp, by_largest);
+  return x;
+}
+// By a whole warp, after griddep_wait, as what follows.
+__device__ __forceinline__ Scale warp_scale(const float* partial, int count, int exp, bool by_largest, int more = 0) {
+  if (!partial) return Scale{1.0f, 1.0f, 1.0f};
+  return make_scale(warp_largest(partial, count), exp, by_largest, more);
+}
+// The gradients' largest.  `more`: what it adds to the exponent of the scale that they were
+// made with: nothing from 2^-4 (the smallest normal number is 2^-10 of that) to fp16's largest.
+struct GradTop {
+  static __device__ __forceinline__ int more(const float* top) {
+    const float x = warp_largest(top, kTopParts);
+    return x == 0.0f || (x >= 0.0625f && x <= 65504.0f) ? 0 : 14 - ilogbf(x);
+  }
+  // A launch that may be the second: whether its work is to be done (the same in all of its threads).
+  // `first`: one of its warps, which leaves the products' factor.
+  template <class P>
+  static __device__ __forceinline__ bool needed(const P& p, bool first) {
+    if (!p.again) return true;
+    const int m = more(p.again);
+    if (first) {
+      const float inv = warp_scale(p.scale, p.scale_count, p.scale_exp, false, m).inv;
+      if ((threadIdx.x & 31) == 0) p.again[kTopParts] = inv;
+    }
+    return m != 0;
+  }
+  template <class P>
+  static __device__ __forceinline__ Scale scale(const P& p) {
+    return warp_scale(p.scale, p.scale_count, p.scale_exp, false, p.again ? more(p.again) : 0);
+  }
+  // The largest of a warp's gradients (none below 0, so that their bits are in the same
+  // order), into one of the parts.
+  static __device__ __forceinline__ void record(float* top, int part, float x) {
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(x));
+    uint32_t* to = reinterpret_cast<uint32_t*>(top) + part % kTopParts;
+    if ((threadIdx.x & 31) == 0 && bits > ld_global(to)) atomicMax(to, bits);
+  }
+};
+__device__ __forceinline__ float largest_finite(float top, float x) {
+  x = fabsf(x);
+  return x < INFINITY ? fmaxf(top, x) : top;
 }
 
 }  // namespace mpg

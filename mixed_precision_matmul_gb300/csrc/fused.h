@@ -23,6 +23,7 @@ enum class FusedEpi {
 
 constexpr int kMaxCtas = 160;          // workers of a launch, at most: the slots of split tiles are laid out for them
 constexpr int kScaleBlocks = 304;      // partial maxima behind a scale
+constexpr int kTopParts = 128;         // of the largest gradients made with it
 
 // Rows that a product of few rows takes (few_rows.cu).
 constexpr int kFewRows = 16;
@@ -59,6 +60,7 @@ struct FusedGemmParams {
   int32_t dy_vec;
   const float* scale;               // values whose largest sets the scale that 16-bit gradients carry, or null
   int32_t scale_count, scale_exp, scale_largest;   // see Scale
+  float *record, *again;            // kGatedGrad: see GradTop (one of them, or neither)
 
   // cross entropy
   const void* target;
@@ -101,6 +103,7 @@ struct FewRowsParams {
   int64_t lddy;
   const float* scale;
   int32_t scale_count, scale_exp, scale_largest;
+  float *record, *again;            // kGatedGrad: see GradTop
   const void* target;
   int32_t target_bytes;
   int64_t target_stride, ignore_index;
@@ -152,6 +155,7 @@ struct MaxParams {
   int32_t target_bytes;
   int64_t target_stride, ignore_index;
   float* partial;                   // [kScaleBlocks]
+  float* top;                       // [kTopParts], set to 0; or null
 };
 cudaError_t launch_max(const MaxParams& p, cudaStream_t stream);
 
@@ -165,6 +169,7 @@ struct GatedGradParams {
   int32_t vec, bf16;
   const float* scale;
   int32_t scale_count, scale_exp;
+  float *record, *again;            // see GradTop
 };
 cudaError_t launch_gated_grad(const GatedGradParams& p, int sm_count, cudaStream_t stream);
 

@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(512) max_kernel(const __grid_constant__ MaxPar
 #pragma unroll
     for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     if (threadIdx.x == 0) p.partial[blockIdx.x] = x;
+    if (threadIdx.x == 0 && p.top && blockIdx.x < kTopParts) p.top[blockIdx.x] = 0.0f;
   }
 }
 
@@ -131,8 +132,10 @@ __global__ void __launch_bounds__(512) max_kernel(const __grid_constant__ MaxPar
 __global__ void __launch_bounds__(256) gated_grad_kernel(const __grid_constant__ GatedGradParams p) {
   griddep_wait();
   griddep_launch_dependents();
+  if (!GradTop::needed(p, blockIdx.x == 0 && threadIdx.x < 32)) return;
   const bool bf16 = p.bf16 != 0, vec = p.vec != 0;
-  const float s = warp_scale(p.scale, p.scale_count, p.scale_exp, false).mul;
+  const float s = GradTop::scale(p).mul;
+  float top = 0.0f;
   const int64_t per_line = (p.cols + 7) / 8, n = p.rows * per_line;
   const bool small = n < INT_MAX;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
@@ -147,12 +150,23 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const __grid_constant__
     for (int j = 0; j < 4; ++j) {
       const float2 yy = unpack16(y[j], bf16), aa = unpack_kept(a[j], bf16), bb = unpack_kept(b[j], bf16);
       const float y0 = s * yy.x, y1 = s * yy.y;
-      dg[j] = pack16(y0 * bb.x, y1 * bb.y, bf16);
-      du[j] = pack16(y0 * aa.x, y1 * aa.y, bf16);
+      const float g0 = y0 * bb.x, g1 = y1 * bb.y, u0 = y0 * aa.x, u1 = y1 * aa.y;
+      if (p.record) top = largest_finite(largest_finite(largest_finite(largest_finite(top, g0), g1), u0), u1);
+      dg[j] = pack16(g0, g1, bf16);
+      du[j] = pack16(u0, u1, bf16);
     }
     // (the lines of dg and du are padded to whole chunks; what lies beyond the columns is not read)
     *reinterpret_cast<uint4*>(p.dg + c.row * p.ldd + c.col) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
     *reinterpret_cast<uint4*>(p.du + c.row * p.ldd + c.col) = make_uint4(du[0], du[1], du[2], du[3]);
+  }
+  if (p.record) {
+    // (a warp of each block: from all of them at once the atomics took longer than the reads)
+    __shared__ float warps[8];
+    __syncwarp();
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x < 32) GradTop::record(p.record, (int)blockIdx.x, threadIdx.x < 8 ? warps[threadIdx.x] : 0.0f);
   }
 }
 
@@ -241,7 +255,8 @@ cudaError_t launch_pad(const PadParams& p, int sm_count, cudaStream_t stream) {
 }
 cudaError_t launch_max(const MaxParams& p, cudaStream_t stream) { return launch(max_kernel, dim3(kScaleBlocks), 512, p, stream); }
 cudaError_t launch_gated_grad(const GatedGradParams& p, int sm_count, cudaStream_t stream) {
-  return launch(gated_grad_kernel, dim3(blocks_for(p.rows * ((p.cols + 7) / 8), 32 * (int64_t)sm_count)), 256, p, stream);
+  // (done again, as a rule it does nothing: fewer blocks begin and end sooner)
+  return launch(gated_grad_kernel, dim3(blocks_for(p.rows * ((p.cols + 7) / 8), (p.again ? 8 : 32) * (int64_t)sm_count)), 256, p, stream);
 }
 cudaError_t launch_loss_join(const LossJoinParams& p, cudaStream_t stream) {
   if (p.rows <= 2 * kFewRows) return launch(loss_join_kernel<1>, dim3((unsigned)p.rows), kJoinThreads, p, stream);

@@ -226,6 +226,14 @@ __device__ __forceinline__ float row_weight(const FusedGemmParams& p, int row, i
 
 template <class T>
 __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid_constant__ FusedGemmParams p) {
+  if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
+    if (p.again) {
+      // (every thread of both CTAs finds the same)
+      griddep_launch_dependents();
+      griddep_wait();
+      if (!GradTop::needed(p, blockIdx.x == 0 && threadIdx.x < 32)) return;
+    }
+  }
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* epi_base = smem + T::kStages * T::kStage;
@@ -394,8 +402,9 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
     constexpr int kCc = T::kTileN / 32 / 2;         // 32-column chunks of one warp
     const int cc0 = half * kCc;
     const bool bf16 = p.bf16 != 0;
-    const Scale sc = warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
+    const Scale sc = T::kEpi == FusedEpi::kGatedGrad ? GradTop::scale(p) : warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
     uint32_t g = 0;
+    float top = 0.0f;                                // kGatedGrad: the largest gradient of a thread
     FusedItems items(p, worker, workers);
     constexpr bool kAhead = T::kEpi == FusedEpi::kGatedGrad;
     FusedItem x, ahead;
@@ -592,8 +601,10 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
                 float a0, d0, a1, d1;
                 act_both(gt[j], T::kAct, a0, d0);
                 act_both(gt[j + 1], T::kAct, a1, d1);
-                w[j >> 1] = pack16(y0 * (up[j] * d0), y1 * (up[j + 1] * d1), bf16);
-                wu[j >> 1] = pack16(y0 * a0, y1 * a1, bf16);
+                const float g0 = y0 * (up[j] * d0), g1 = y1 * (up[j + 1] * d1), u0 = y0 * a0, u1 = y1 * a1;
+                top = largest_finite(largest_finite(largest_finite(largest_finite(top, g0), g1), u0), u1);
+                w[j >> 1] = pack16(g0, g1, bf16);
+                wu[j >> 1] = pack16(u0, u1, bf16);
               }
               store(0, w);
               store(1, wu);
@@ -692,6 +703,10 @@ __global__ void __launch_bounds__(T::kThreads, 1) fused_gemm_kernel(const __grid
         }
       }
     }
+    if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
+      __syncwarp();
+      if (p.record) GradTop::record(p.record, (int)blockIdx.x * T::kEpiWarps + warp - 2, top);
+    }
   }
 
   // neither CTA of a pair leaves while the other may address its shared memory
@@ -754,6 +769,7 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   __shared__ float4 slices[kSlices > 1 ? kSlices : 1][T::kTwo ? 2 : 1][kSlices > 1 ? kAt : 1];
   griddep_wait();
   griddep_launch_dependents();
+  if (T::kEpi == FusedEpi::kGatedGrad && !GradTop::needed(p, false)) return;
   const int tiles0 = p.prod[0].num_tiles - p.whole_tiles;                       // the second product's come after them
   const int which = T::kEpi == FusedEpi::kPlain && (int)blockIdx.x >= tiles0 ? 1 : 0;
   const FusedProduct& pr = p.prod[which];
@@ -769,7 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
   const int i = blockIdx.y * kAt + place;
   const int r = i / kPerRow, c = i % kPerRow * 4;
   const int row = (second ? tc.mb - pr.mb_second : tc.mb) * T::kTile + r, col = tc.nb * T::kTileN + c;
-  const Scale sc = warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
+  const Scale sc = T::kEpi == FusedEpi::kGatedGrad ? GradTop::scale(p) : warp_scale(p.scale, p.scale_count, p.scale_exp, p.scale_largest != 0);
   const bool in = row < pr.m;
   const int left = pr.n - col;                       // columns of the matrix from here on
   constexpr int64_t kSlot = T::kTile * T::kTile;
@@ -805,36 +821,45 @@ __global__ void __launch_bounds__(kJoinThreads) fused_join_kernel(const __grid_c
     float gt[4], up[4];
     sum(0, c, gt);
     sum(1, T::kTile / 2 + c, up);
-    if (slice > 0 || !in || left <= 0) return;
-    auto at = [&](int k) { return (int64_t)row * pr.ldo[k] + col; };
-    if constexpr (T::kEpi == FusedEpi::kGated) {
-      if (pr.out[1]) {
-        float ka[4], kb[4];
+    const bool none = slice > 0 || !in || left <= 0;
+    if (T::kEpi != FusedEpi::kGatedGrad && none) return;
+    float top = 0.0f;
+    if (!none) {
+      auto at = [&](int k) { return (int64_t)row * pr.ldo[k] + col; };
+      if constexpr (T::kEpi == FusedEpi::kGated) {
+        if (pr.out[1]) {
+          float ka[4], kb[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float d;
+            act_both(gt[j], T::kAct, ka[j], d);
+            kb[j] = up[j] * d;
+          }
+          store_kept(pr.out[1], at(1), ka, left, pr.out_vec[1], p.bf16 != 0);
+          store_kept(pr.out[2], at(2), kb, left, pr.out_vec[2], p.bf16 != 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) gt[j] = act_value(gt[j], T::kAct) * up[j];
+      } else {
+        float dy[4];
+        load_four(dy, p.dy, (int64_t)row * p.lddy + col, left, p.dy_vec, type);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float d;
-          act_both(gt[j], T::kAct, ka[j], d);
-          kb[j] = up[j] * d;
+          float a, d;
+          act_both(gt[j], T::kAct, a, d);
+          const float y = sc.mul * dy[j];
+          gt[j] = y * (up[j] * d);
+          up[j] = y * a;
+          if (j < left) top = largest_finite(largest_finite(top, gt[j]), up[j]);
         }
-        store_kept(pr.out[1], at(1), ka, left, pr.out_vec[1], p.bf16 != 0);
-        store_kept(pr.out[2], at(2), kb, left, pr.out_vec[2], p.bf16 != 0);
+        store_four(pr.out[1], at(1), up, left, pr.out_vec[1], type);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) gt[j] = act_value(gt[j], T::kAct) * up[j];
-    } else {
-      float dy[4];
-      load_four(dy, p.dy, (int64_t)row * p.lddy + col, left, p.dy_vec, type);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float a, d;
-        act_both(gt[j], T::kAct, a, d);
-        const float y = sc.mul * dy[j];
-        gt[j] = y * (up[j] * d);
-        up[j] = y * a;
-      }
-      store_four(pr.out[1], at(1), up, left, pr.out_vec[1], type);
+      store_four(pr.out[0], at(0), gt, left, pr.out_vec[0], type);
     }
-    store_four(pr.out[0], at(0), gt, left, pr.out_vec[0], type);
+    if constexpr (T::kEpi == FusedEpi::kGatedGrad) {
+      __syncwarp();
+      if (p.record) GradTop::record(p.record, (int)(blockIdx.x * gridDim.y + blockIdx.y) * (kJoinThreads / 32) + (int)(threadIdx.x >> 5), top);
+    }
   } else {
     float v[4];
     sum(0, c, v);

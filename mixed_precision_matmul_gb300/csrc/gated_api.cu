@@ -48,7 +48,7 @@ Source source(const void* ptr, int64_t ld, int64_t rows, int64_t cols) {
 
 struct Layout {
   Source x, wg, wu;
-  size_t dg, du, partial, slots, bytes;
+  size_t dg, du, partial, top, slots, bytes;
   int64_t ldd;
 };
 FusedLaunch product(FusedEpi epi, int64_t m, int64_t n, int64_t k) {
@@ -80,7 +80,7 @@ Layout layout(const mpg_gated_layer* l, bool backward) {
   o.x = source(l->x, l->ldx, l->tokens, l->hidden);
   o.wg = source(l->wg, l->ldwg, l->inner, l->hidden);
   o.wu = source(l->wu, l->ldwu, l->inner, l->hidden);
-  o.dg = o.du = o.partial = o.slots = 0;
+  o.dg = o.du = o.partial = o.top = o.slots = 0;
   o.ldd = fused_wide_line(l->inner);
   // (few rows are multiplied in whole chunks of eight: zeros behind all of them, or none needed)
   const bool all = !backward && l->tokens <= kFewRows && l->hidden % 8 != 0;
@@ -92,6 +92,7 @@ Layout layout(const mpg_gated_layer* l, bool backward) {
     o.dg = take((size_t)l->tokens * (size_t)o.ldd * 2);
     o.du = take((size_t)l->tokens * (size_t)o.ldd * 2);
     o.partial = take(kScaleBlocks * sizeof(float));
+    o.top = take((kTopParts + 1) * sizeof(float));
   }
   if (backward) {
     const FusedLaunch to_x = input_gradient(l), to_w = weight_gradient(l);
@@ -249,14 +250,19 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
   if ((s = get_device(&dev)) != MPG_OK) return s;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* partial = reinterpret_cast<float*>(ws + o.partial);
+  float* top = reinterpret_cast<float*>(ws + o.top);
   float* slots = reinterpret_cast<float*>(ws + o.slots);
   uint16_t* dg = reinterpret_cast<uint16_t*>(ws + o.dg);
   uint16_t* du = reinterpret_cast<uint16_t*>(ws + o.du);
   if ((s = make_copies(dev, {&o.x, &o.wg, &o.wu}, ws, st)) != MPG_OK) return s;
 
   // fp16: dgate and dup carry a power of two that brings the largest of dY to
-  // [2^4, 2^5).  2^11 is left above for up times act', and 18 bits below before
-  // values lose precision.
+  // [2^4, 2^5), which leaves 2^11 above for what they are multiplied by, and 18 bits
+  // below before values lose precision.  Where the largest of them leaves fp16
+  // (or all are small) they are made again with a scale from themselves (see GradTop):
+  // a second launch, which ends at once where nothing is to be done: 1 to 5 us
+  // (17 x 2048 x 5632 recomputed 47 -> 50, 2048 x 2048 x 5504 186 -> 188).  A bound
+  // beforehand costs two more reads of what was kept, or a read of the operands.
   const bool half = l.dtype == MPG_F16;
   constexpr int kExp = 4;
   if (half) {
@@ -269,80 +275,92 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     p.vec = fused_lines_ok(dY, l.tokens > 1 ? lddy : 0);
     p.flat = p.vec && l.inner % 8 == 0 && (lddy == l.inner || l.tokens == 1);
     p.partial = partial;
+    p.top = top;
     const cudaError_t e = launch_max(p, st);
     if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "maximum launch: %s", cudaGetErrorString(e));
   }
-  if (A) {
-    GatedGradParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.dy = dY;
-    p.lddy = lddy;
-    p.a = A;
-    p.lda = lda;
-    p.b = B;
-    p.ldb = ldb;
-    p.dg = dg;
-    p.du = du;
-    p.ldd = o.ldd;
-    p.rows = l.tokens;
-    p.cols = l.inner;
-    p.vec = fused_lines_ok(dY, lddy) && fused_lines_ok(A, lda) && fused_lines_ok(B, ldb);
-    p.bf16 = l.dtype == MPG_BF16;
-    p.scale = half ? partial : nullptr;
-    p.scale_count = kScaleBlocks;
-    p.scale_exp = kExp;
-    const cudaError_t e = launch_gated_grad(p, dev->sm_count, st);
-    if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "gradient launch: %s", cudaGetErrorString(e));
-  } else if (l.tokens <= kFewRows && (l.hidden % 8 == 0 || (o.x.copy && o.wg.copy && o.wu.copy))) {
-    // (lines of whole chunks of eight, or copies with zeros behind them)
-    FewRowsParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.x = o.x.ptr;
-    p.ldx = o.x.ld;
-    p.w = o.wg.ptr;
-    p.ldw = o.wg.ld;
-    p.wu = o.wu.ptr;
-    p.ldwu = o.wu.ld;
-    p.bf16 = !half;
-    p.rows = (int32_t)l.tokens;
-    p.n = (int32_t)l.inner;
-    p.k = (int32_t)fused_line(l.hidden);
-    p.act = (int32_t)l.act;
-    p.y = dg;
-    p.ka = du;
-    p.ldy = p.lda = o.ldd;
-    p.dy = dY;
-    p.lddy = lddy;
-    p.scale = half ? partial : nullptr;
-    p.scale_count = kScaleBlocks;
-    p.scale_exp = kExp;
-    if ((s = launch_few_rows(dev, p, FusedEpi::kGatedGrad, st)) != MPG_OK) return s;
-  } else {
-    FusedGemmParams p;
-    std::memset(&p, 0, sizeof(p));
-    if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
-    if ((s = fused_map(&p.prod[0].map_b[0], o.wg.ptr, o.wg.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
-    if ((s = fused_map(&p.prod[0].map_b[1], o.wu.ptr, o.wu.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
-    p.bf16 = l.dtype == MPG_BF16;
-    p.act = (int32_t)l.act;
-    p.prod[0].out[0] = dg;
-    p.prod[0].out[1] = du;
-    p.prod[0].ldo[0] = p.prod[0].ldo[1] = o.ldd;
-    p.prod[0].out_vec[0] = p.prod[0].out_vec[1] = 1;
-    p.dy = dY;
-    p.lddy = lddy;
-    p.dy_vec = fused_lines_ok(dY, lddy);
-    p.scale = half ? partial : nullptr;
-    p.scale_count = kScaleBlocks;
-    p.scale_exp = kExp;
-    if ((s = launch_fused(dev, product(FusedEpi::kGatedGrad, l.tokens, l.inner, l.hidden), p, slots, st)) != MPG_OK) return s;
+  for (int pass = 0; pass < (half ? 2 : 1); ++pass) {
+    float* record = half && !pass ? top : nullptr;
+    float* again = pass ? top : nullptr;
+    if (A) {
+      GatedGradParams p;
+      std::memset(&p, 0, sizeof(p));
+      p.dy = dY;
+      p.lddy = lddy;
+      p.a = A;
+      p.lda = lda;
+      p.b = B;
+      p.ldb = ldb;
+      p.dg = dg;
+      p.du = du;
+      p.ldd = o.ldd;
+      p.rows = l.tokens;
+      p.cols = l.inner;
+      p.vec = fused_lines_ok(dY, lddy) && fused_lines_ok(A, lda) && fused_lines_ok(B, ldb);
+      p.bf16 = l.dtype == MPG_BF16;
+      p.scale = half ? partial : nullptr;
+      p.scale_count = kScaleBlocks;
+      p.scale_exp = kExp;
+      p.record = record;
+      p.again = again;
+      const cudaError_t e = launch_gated_grad(p, dev->sm_count, st);
+      if (e != cudaSuccess) return fail(MPG_ERR_CUDA, "gradient launch: %s", cudaGetErrorString(e));
+    } else if (l.tokens <= kFewRows && (l.hidden % 8 == 0 || (o.x.copy && o.wg.copy && o.wu.copy))) {
+      // (lines of whole chunks of eight, or copies with zeros behind them)
+      FewRowsParams p;
+      std::memset(&p, 0, sizeof(p));
+      p.x = o.x.ptr;
+      p.ldx = o.x.ld;
+      p.w = o.wg.ptr;
+      p.ldw = o.wg.ld;
+      p.wu = o.wu.ptr;
+      p.ldwu = o.wu.ld;
+      p.bf16 = !half;
+      p.rows = (int32_t)l.tokens;
+      p.n = (int32_t)l.inner;
+      p.k = (int32_t)fused_line(l.hidden);
+      p.act = (int32_t)l.act;
+      p.y = dg;
+      p.ka = du;
+      p.ldy = p.lda = o.ldd;
+      p.dy = dY;
+      p.lddy = lddy;
+      p.scale = half ? partial : nullptr;
+      p.scale_count = kScaleBlocks;
+      p.scale_exp = kExp;
+      p.record = record;
+      p.again = again;
+      if ((s = launch_few_rows(dev, p, FusedEpi::kGatedGrad, st)) != MPG_OK) return s;
+    } else {
+      FusedGemmParams p;
+      std::memset(&p, 0, sizeof(p));
+      if ((s = fused_map(&p.prod[0].map_a[0], o.x.ptr, o.x.ld, l.dtype, false, l.tokens, l.hidden)) != MPG_OK) return s;
+      if ((s = fused_map(&p.prod[0].map_b[0], o.wg.ptr, o.wg.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
+      if ((s = fused_map(&p.prod[0].map_b[1], o.wu.ptr, o.wu.ld, l.dtype, false, l.inner, l.hidden)) != MPG_OK) return s;
+      p.bf16 = l.dtype == MPG_BF16;
+      p.act = (int32_t)l.act;
+      p.prod[0].out[0] = dg;
+      p.prod[0].out[1] = du;
+      p.prod[0].ldo[0] = p.prod[0].ldo[1] = o.ldd;
+      p.prod[0].out_vec[0] = p.prod[0].out_vec[1] = 1;
+      p.dy = dY;
+      p.lddy = lddy;
+      p.dy_vec = fused_lines_ok(dY, lddy);
+      p.scale = half ? partial : nullptr;
+      p.scale_count = kScaleBlocks;
+      p.scale_exp = kExp;
+      p.record = record;
+      p.again = again;
+      if ((s = launch_fused(dev, product(FusedEpi::kGatedGrad, l.tokens, l.inner, l.hidden), p, slots, st)) != MPG_OK) return s;
+    }
   }
   FusedGemmParams p;
   std::memset(&p, 0, sizeof(p));
   p.bf16 = !half;
-  p.scale = half ? partial : nullptr;
-  p.scale_count = kScaleBlocks;
-  p.scale_exp = kExp;
+  // (the factor that dgate and dup carry, as it was left)
+  const float* factor = half ? top + kTopParts : nullptr;
+  p.scale = factor;
+  p.scale_count = p.scale_largest = 1;
   const void* const d[2] = {dg, du};
   int count = 0;
   if (dX) {
@@ -394,9 +412,8 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
     w.out[1] = dWu;
     w.ldo[0] = lddwg;
     w.ldo[1] = lddwu;
-    w.scale = half ? partial : nullptr;
-    w.scale_count = kScaleBlocks;
-    w.scale_exp = kExp;
+    w.scale = factor;
+    w.scale_count = w.scale_largest = 1;
     const cudaError_t e = launch_few_grad(w, st);
     return e == cudaSuccess ? MPG_OK : fail(MPG_ERR_CUDA, "weight gradient launch: %s", cudaGetErrorString(e));
   }
