@@ -1,4 +1,4 @@
-// Products of few rows (a token or a few dozen being decoded or scored): the
+// Products of few rows (up to 16 tokens being decoded or scored): the
 // weights are read once, and their bytes are all that counts (sm_103a).
 //
 // Weight lines are the M side of mma.sync m16n8k16 and the rows of X its N
@@ -129,7 +129,11 @@ __device__ __forceinline__ void finish(const FewRowsParams& p, Red& red, const S
 template <int kNt>
 struct RingTraits {
   static constexpr int kLines = 16;                       // of weights in a stage
-  static constexpr int kWidth = 512;                      // k of a stage
+  static constexpr int kWidth = 512;                      // k of a stage, 64 of each warp
+  // Stages that are summed by the tensor cores at a time where the sums become a loss
+  // (1024 of k in a warp): their sums are cut off towards zero, and those of 65536
+  // positive products in one were off by 1.5e-5.
+  static constexpr int kFold = 16;
   static constexpr int kPitch = kWidth * 2 + 64;
   static constexpr int kStage = kLines * kPitch;
   static constexpr int kTokens = 8 * kNt;
@@ -236,11 +240,11 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
   uint32_t it = 0, n = 0;
   bool ok = true;                                    // (a CTA that gives up still meets at its barriers)
   for (int strip = blockIdx.x; strip < strips; strip += gridDim.x, ++n) {
-    float c[kNt][4];
+    float c[kNt][4], folded[kNt][4];
 #pragma unroll
     for (int i = 0; i < kNt; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) c[i][j] = folded[i][j] = 0.0f;
     for (int k = 0; k < chunks; ++k, ++it) {
       const uint32_t st = it % T::kStages;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (it / T::kStages) & 1u, ctl));
@@ -262,6 +266,23 @@ __global__ void __launch_bounds__(RingTraits<kNt>::kThreads, 2) few_rows_kernel(
         }
         fetch(k + 1 < chunks ? k + 1 : 0, h);
       }
+      if constexpr (E == FusedEpi::kStats) {
+        if (k % T::kFold == T::kFold - 1 || k + 1 == chunks) {
+#pragma unroll
+          for (int i = 0; i < kNt; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              folded[i][j] += c[i][j];
+              c[i][j] = 0.0f;
+            }
+        }
+      }
+    }
+    if constexpr (E == FusedEpi::kStats) {
+#pragma unroll
+      for (int i = 0; i < kNt; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[i][j] = folded[i][j];
     }
     // (two sets of sums in turn: one barrier a strip keeps them apart)
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
