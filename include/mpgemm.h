@@ -557,7 +557,7 @@ mpg_status mpg_gated_gemm_backward(const mpg_gated_layer* layer, const void* dY,
  * A target that is neither ignore_index nor a class makes loss and lse NaN, and
  * in the backward pass its row of dX and all of dW.  loss and lse: tokens fp32.
  * Maxima, sums and logits are fp32, logits summed by the tensor cores over at
- * most 1024 of hidden at a time: loss and lse are off by about 5e-7 of lse (1e-6
+ * most 1024 of hidden at a time: loss and lse are off by about 5e-7 of lse (1.3e-6
  * where all products have one sign).  A NaN in a row makes its loss NaN. */
 typedef struct {
   int64_t tokens, hidden, vocab;
@@ -580,7 +580,9 @@ mpg_status mpg_linear_cross_entropy(const mpg_vocab_loss* desc, float* loss, flo
  * D is made for a piece of the vocabulary at a time (512 MB at most, or 256
  * classes), from logits that are computed again; divided by the largest dloss (and
  * in fp16 times 2^14) it is rounded once to the 16-bit type.  dX is summed over the
- * pieces in fp32.  tokens 0: dW = 0. */
+ * pieces in fp32.  D is 0 for ignored tokens, and multiplied all the same: rows of X
+ * that are infinite or NaN there make dW NaN, as they do in a plain product.
+ * tokens 0: dW = 0. */
 size_t mpg_linear_cross_entropy_backward_workspace_size(const mpg_vocab_loss* desc);
 mpg_status mpg_linear_cross_entropy_backward(const mpg_vocab_loss* desc, const float* lse, const float* dloss,
                                              int64_t dloss_stride, void* dX, int64_t lddx, void* dW, int64_t lddw,

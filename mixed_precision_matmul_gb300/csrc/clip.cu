@@ -10,8 +10,10 @@
 // tensors.  A thread has four loads of eight elements on their way.  1.0e9 bf16
 // gradients take 278 us for the norm (7.3 TB/s) and 622 for the scaling (6.5).
 //
-// Squares: a thread sums 32 in fp32 and carries the sums in 64 bits (a sum of
-// eight at a time was bound by the 64-bit adder: 1.0e9 bf16 gradients 483 us).
+// Squares: a thread sums 32 in fp32 (four sums of eight, then two additions: off by
+// 10 * 2^-24 at most, so the norm by 5 * 2^-24, and 6 with its own rounding) and
+// carries the sums in 64 bits (a sum of eight at a time was bound by the 64-bit
+// adder: 1.0e9 bf16 gradients 483 us).
 // fp32 cannot hold the square of what is below 2^-63 or above 2^64; elements
 // whose sum leaves [2^-90, 2^120] are squared in 64 bits instead (all zeros
 // apart, which need no sum).

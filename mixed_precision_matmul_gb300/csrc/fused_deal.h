@@ -142,6 +142,18 @@ inline FusedShape shape_of(const FusedLaunch& l, int64_t tile) {
 // over k = 32768, dealt to 76: 210 us where the round takes 173), so that
 // splitting pays where it gives many idle workers something to do.  The parts
 // go through memory twice, and the second launch takes 3 us.
+// Split behind whole rounds, against one more round (us, gated tokens x hidden x inner
+// and losses tokens x hidden over classes):
+//   gated  64 x 4096 x  9856     2 tiles behind 152    36.9 |  45.8
+//   gated  64 x 4096 x 10300     9 behind 152          40.4 |  49.2
+//   gated 256 x 4096 x  9856     1 behind 76           43.1 |  49.0
+//   gated 2183 x 4096 x 2131     1 behind 152          55.8 |  63.5
+//   gated 256 x 4096 x 10500     7 behind 76           52.8 |  51.7
+//   gated 4096 x 4096 x 4920    16 behind 608           182 |   181
+//   loss   64 x 4096, 19500      1 behind 152          39.0 |  50.5
+//   loss  120 x 2304, 58752      3 behind 456          57.8 |  61.6
+//   loss 1092 x 2752, 93248      1 behind 1824          369 |   378
+//   loss 1024 x 2048,  9800      4 behind 152          47.2 |  46.2
 constexpr double kOneEpi = 1.9, kPairEpi = 3.8;    // a tile's way out, beside the next one's products
 constexpr double kOneEdge = 4.3, kPairEdge = 7.5, kOneBlock = 0.29, kPairBlock = 0.31;
 constexpr double kJoin = 3.0, kApartBytes = 8.3e6, kPartBytes = 5.0e6;     // bytes a us

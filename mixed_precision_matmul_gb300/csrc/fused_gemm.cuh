@@ -28,8 +28,8 @@
 // next tile's products.
 //
 // Tiles go round by round to the workers.  What does not fill a round may be split:
-// its blocks of k are dealt out evenly, each worker getting one run of them, and a
-// worker whose run holds only a part of a tile's k leaves its sums in a slot.  A
+// its blocks of k are dealt out evenly, in runs of a few at least, and a worker
+// whose run holds only a part of a tile's k leaves its sums in a slot (fused_deal.h).  A
 // second launch adds the slots of a tile in the order of k and does the epilogue's
 // work: the result does not depend on timing.  Or (kPlain) a second product's
 // tiles, shorter ones, fill the first's last round: the gradients of an input and

@@ -119,7 +119,10 @@ def gated_gemm(x, wg, wu, act: str = "silu", keep: bool = False, workspace=None,
     where a and b are what :func:`gated_gemm_backward` makes gradients from, act(g)
     and u act'(g) of the projections g and u: fp16 in an fp16 layer, and in a bf16
     layer int16 codes of a 16-bit type with more precision than bf16 (mpgemm.h says
-    which).
+    which) and less range: what is kept is infinite from 65504 on in fp16 and from 2^32
+    on in a bf16 layer, and loses bits below 2^-14 and 2^-30.  Gradients are then
+    infinite or NaN that are finite when the projections are computed again
+    (``kept=None``).
     """
     torch = _types()[0]
     if stream is not None:
@@ -149,8 +152,9 @@ def gated_gemm_backward(dy, x, wg, wu, act: str = "silu", kept=None, need_dx: bo
                         workspace=None, stream=None):
     """Gradients ``(dx, dwg, dwu)`` of :func:`gated_gemm` for dy (tokens, inner).
 
-    ``kept`` is the ``(a, b)`` of ``gated_gemm(..., keep=True)``; without it the
-    projections are computed again.  What is not needed is None.
+    ``kept`` is the ``(a, b)`` of ``gated_gemm(..., keep=True)``, whose range is
+    smaller than the layer's; without it the projections are computed again, over the
+    whole range.  What is not needed is None.
     """
     torch = _types()[0]
     a, b = kept if kept is not None else (None, None)

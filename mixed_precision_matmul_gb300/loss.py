@@ -105,7 +105,8 @@ def linear_cross_entropy_backward(x, w, target, lse, dloss, ignore_index: int = 
                                   need_dw: bool = True, workspace=None, stream=None):
     """Gradients ``(dx, dw)`` of :func:`linear_cross_entropy`'s loss for ``dloss``
     (tokens,), fp32 (an expanded one too: ``(1 / count).expand(tokens)`` for the
-    mean).  ``lse`` is the forward call's.  What is not needed is None.
+    mean).  ``lse`` is the forward call's.  What is not needed is None.  Rows of x
+    whose token is ignored are multiplied by 0: infinities and NaN there make dw NaN.
     """
     torch = _types()[0]
     if stream is not None:
